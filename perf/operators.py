@@ -339,7 +339,7 @@ def plain_map_step(s, lens, new, slots):
     gives = (have - need).clamp(min=0)
     wants = (need - have).clamp(min=0)
     stack_size = count + gives.sum()
-    served = torch.cumsum(wants, 0) <= stack_size
+    served = (wants == 0) | (torch.cumsum(wants, 0) <= stack_size)
     gets = torch.where(served, wants, 0)
     col = torch.arange(cols, device="cuda")[None, :]
     going = (col >= need[:, None]) & (col < have[:, None])
