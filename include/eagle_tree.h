@@ -18,6 +18,11 @@
  *   et_verify_accept                                (lossless acceptance)
  *   et_kv_commit                                    (accepted rows -> KV cache)
  *
+ * With a paged 8-bit KV cache (requests that come and go, half the bytes of a
+ * bf16 cache) the step is the same but for three calls: et_block_map before
+ * it, et_tree_attention_paged and et_kv_commit_paged in place of the last two
+ * that touch the cache.
+ *
  * Conventions shared by every call
  * --------------------------------
  * - Every pointer argument that names a tensor is a DEVICE pointer unless the
@@ -72,6 +77,7 @@ typedef enum {
 #define ET_DEV_DISCONNECTED 4 /* rerank found a kept node whose parent is not kept (cannot happen
                                  for keys produced by et_tree_expand) */
 #define ET_DEV_TIMEOUT     8  /* a bounded wait inside a kernel gave up */
+#define ET_DEV_NO_PAGES   16  /* et_block_map: the free pages did not cover every request */
 
 /* Tree shape.  Limits: 1 <= topk <= 32, 1 <= m <= 32, 1 <= depth <= 16,
  * topk <= V, 1 <= n <= C, n + 1 <= 128, C <= 4096, temperature > 0. */
@@ -169,6 +175,55 @@ typedef struct {
     int64_t kv_rows;          /* d-element rows in each of k_cache / v_cache (bounds check) */
     int32_t feat_dim;         /* F: elements per feature row (0 = no features); F * sizeof(dtype) % 16 == 0 */
 } et_commit_shape;
+
+/* 8-bit formats of a paged KV cache: 1-4-3 (largest value 448, no infinity) and 1-5-2 (57344). */
+typedef enum { ET_KV_E4M3 = 0, ET_KV_E5M2 = 1 } et_kv_format;
+
+/*
+ * Paged 8-bit KV cache (host struct of caller-owned device pointers).  A page
+ * holds page_size tokens of every KV head; row t of head g of page p is the d
+ * codes at k_pages + p * page_stride + (g * page_size + t) * d, and stands for
+ * code * k_scale[p * Hkv + g] (V the same).  Token j of sequence b lives in
+ * page block_table[b, j / page_size], row j % page_size.  K and V may be the
+ * two halves of one array (page_stride covers both).
+ */
+typedef struct {
+    int32_t Hkv, d;           /* KV heads, head dim (64 or 128) */
+    int32_t page_size;        /* tokens per page: a multiple of 16, 16..256 */
+    int32_t format;           /* et_kv_format */
+    int64_t num_pages;        /* pages in each of k_pages / v_pages, < 2^31 (page ids are checked against it) */
+    int64_t page_stride;      /* bytes from page to page, >= Hkv * page_size * d, a multiple of 16, < 2^40 */
+    void *k_pages, *v_pages;  /* 16-byte aligned */
+    float *k_scale, *v_scale; /* fp32 [num_pages, Hkv] */
+} et_paged_cache;
+
+/* Block map shape (host struct), see et_block_map. */
+typedef struct {
+    int32_t B;                /* requests, 1..4096 */
+    int32_t page_size;        /* tokens per page, >= 1 */
+    int32_t max_blocks;       /* columns of block_table; max_blocks * page_size < 2^31 */
+    int32_t max_new;          /* columns of slot_map (0: no slot map) */
+    int64_t num_pages;        /* pages of the cache = entries of free_list; + B * max_blocks < 2^31 */
+} et_block_map_shape;
+
+/* Paged commit shape (host struct), see et_kv_commit_paged. */
+typedef struct {
+    int32_t B, N;             /* sequences; rows of k_tree / v_tree per sequence */
+    int32_t path_len;         /* columns of path, 1..17; 0 with path = NULL (rows are taken in order) */
+    int32_t max_blocks;       /* columns of block_table */
+    et_dtype dtype;           /* of k/v tree and the features */
+    int32_t feat_dim;         /* F, as in et_commit_shape (0 with path = NULL) */
+} et_paged_commit_shape;
+
+/* Paged attention shape (host struct), see et_tree_attention_paged. */
+typedef struct {
+    int32_t B, N, Hq;         /* N <= 128 tree rows (1: plain decoding), Hq a multiple of the cache's Hkv */
+    int32_t max_blocks;       /* columns of block_table */
+    et_dtype dtype;           /* of q, k/v tree and out */
+    float scale;              /* score scale, usually 1/sqrt(d) */
+    int32_t max_prefix;       /* host upper bound of prefix_len[b] (sizes the grid) */
+    int32_t num_splits;       /* blocks a sequence's keys are split over; 0 = library heuristic */
+} et_paged_attn_shape;
 
 /* ---- geometry helpers (host, no device work) ---- */
 
@@ -572,6 +627,125 @@ et_status et_kv_commit(const et_commit_shape *shape, const void *k_tree, const v
                        const int32_t *accept_len, const int32_t *path, void *k_cache, void *v_cache,
                        const int64_t *kv_row0, const int32_t *prefix_len, int32_t *new_prefix_len,
                        const void *features, void *feat_out, int32_t *dev_status, et_stream_t stream);
+
+/*
+ * et_block_map -- block tables and slot maps of a paged KV cache, on the GPU,
+ * from the requests' lengths.  The pages have no counterpart: in a server the
+ * requests of a batch come, grow and end, and a host that keeps the free list
+ * would have to wait for every accept_len.
+ *
+ * Request b holds n_blocks[b] pages and is to hold
+ * need = ceil((prefix_len[b] + new_len[b]) / page_size):
+ *   - pages past need return to the free stack, in ascending (request, block)
+ *     order (a request of length 0 with no new rows returns all of them; the
+ *     table entries become -1);
+ *   - then missing pages are taken from the top of the stack, in ascending
+ *     (request, block) order.  A request is served if the pages that all
+ *     requests up to it are missing fit in the stack; from the first that does
+ *     not fit on, requests that miss pages keep what they had, get no slots,
+ *     and ET_DEV_NO_PAGES is set.
+ *   slot_map[b, i] = page * page_size + row of token prefix_len[b] + i for
+ *   i < new_len[b] (where a model's own kernels put that token), else -1.
+ * The result depends on the arguments alone (no atomics).
+ *
+ * prefix_len, new_len  int32 [B]; new_len in [0, max_new] (any count >= 0 when
+ *             max_new is 0).  prefix_len < 0: no request in this place, its
+ *             row of block_table and n_blocks stay, its slots are -1.
+ * n_blocks    int32 [B], block_table int32 [B, max_blocks]: in and out.
+ *             Columns from n_blocks[b] on are not read.
+ * free_list   int32 [num_pages], free_count int32 [1]: the stack of free
+ *             pages, in and out (top = free_list[free_count - 1]; entries from
+ *             free_count on are left as they are).
+ * slot_map    int64 [B, max_new], null when max_new is 0.
+ * A length past max_blocks pages or an n_blocks or new_len outside its range
+ * sets ET_DEV_BAD_INDEX and leaves that request as it is, without slots.  A
+ * free_count outside [0, num_pages] is clamped, a page id outside the pool is
+ * moved as it is (its tokens get no slots) and a stack that would pass
+ * num_pages is cut: ET_DEV_BAD_INDEX too.  Pages belong to one request each: shared prefixes are the
+ * caller's to count.  No workspace; one launch of one thread-block cluster.
+ */
+et_status et_block_map(const et_block_map_shape *shape, const int32_t *prefix_len, const int32_t *new_len,
+                       int32_t *n_blocks, int32_t *block_table, int32_t *free_list, int32_t *free_count,
+                       int64_t *slot_map, int32_t *dev_status, et_stream_t stream);
+
+/*
+ * et_kv_commit_paged -- et_kv_commit into a paged 8-bit cache: the accepted
+ * rows (or the rows of a prompt) are quantised and appended.
+ *
+ * Sequence b appends rows r_0..r_A, A = accept_len[b], r_i = path[b, i] (or i
+ * when path is NULL), at token positions prefix_len[b] + i.  For each page
+ * that receives rows, each head, K and V apart, with MAX the largest value of
+ * the format (448 or 57344) and amax the largest finite magnitude among the
+ * rows the page receives:
+ *   need = the smallest 2^e >= amax / MAX, -48 <= e <= 48 (amax = 0: 2^-48);
+ *   scale = need if the first row received is the page's row 0, else
+ *           max(old scale, need);
+ *   code  = x / scale, rounded to nearest even, past MAX to +-MAX, NaN to NaN;
+ *   where the scale grew, the codes of the rows before are rounded anew:
+ *           code * (old scale / scale).
+ * Powers of two divide exactly, so the codes do not depend on the order of
+ * any sum, and a grown scale loses nothing above the format's subnormals.
+ *
+ * k_tree, v_tree  [B, N, Hkv, d], 16-byte aligned.
+ * accept_len      int32 [B]: -1 appends nothing (rows of a padded batch).
+ * path            int32 [B, path_len] from et_verify_accept, or NULL.
+ * block_table     int32 [B, max_blocks]: must hold the pages of the new rows
+ *                 (et_block_map).  A page that receives rows belongs to one
+ *                 sequence: two that append to the same page race.
+ * prefix_len      int32 [B], read only; new_prefix_len int32 [B], must not
+ *                 alias it: prefix_len + A + 1.  prefix_len < 0: no sequence
+ *                 here, nothing appended, new_prefix_len = prefix_len.
+ * features, feat_out  [B, N, F] and [B, path_len, F] as in et_kv_commit.
+ * A NaN or infinity among the rows, or an old scale that is not positive and
+ * finite (taken as need, codes kept), sets ET_DEV_NONFINITE.  An accept_len
+ * outside [-1, path_len - 1] ([-1, N - 1]), a path row outside [0, N), a
+ * position past the table or a page id outside the cache sets
+ * ET_DEV_BAD_INDEX and that row, page or sequence is skipped (with such an
+ * accept_len new_prefix_len[b] is not written).  No workspace.
+ */
+et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_cache *cache,
+                             const int32_t *block_table, const void *k_tree, const void *v_tree,
+                             const int32_t *accept_len, const int32_t *path, const int32_t *prefix_len,
+                             int32_t *new_prefix_len, const void *features, void *feat_out, int32_t *dev_status,
+                             et_stream_t stream);
+
+/*
+ * et_tree_attention_paged -- et_tree_attention over a paged 8-bit cache.
+ *
+ *   out[b,i,h] = sum_j softmax_j(scale * q[b,i,h] . k_j) v_j,
+ *   j over cached tokens 0..prefix_len[b]-1 of KV head g = h / (Hq/Hkv), the
+ *   values their codes and scales stand for, and tree rows t with mask bit
+ *   (b,i,t) (in the input type, not quantised).
+ *
+ * block_table   int32 [B, max_blocks].
+ * prefix_len    int32 [B], each <= max_prefix; 0 is an empty prefix; < 0: no
+ *               sequence here, its rows of out and lse are left as they are.
+ * q, out        [B, N, Hq, d]; k/v_tree [B, N, Hkv, d]; 16-byte aligned.
+ * mask          uint64 [B, N, W] from et_tree_mask_posids, or NULL: row i
+ *               attends tree rows 0..i (a chain; with N = 1 one decoded token).
+ *               A row that neither prefix nor mask leaves a key has out = 0
+ *               and lse = -inf.
+ * lse           nullable fp32 [B, Hq, N], as in et_tree_attention.
+ * ws            et_tree_attention_paged_workspace_size() bytes, zero-filled
+ *               once (see conventions); 0/null when that size is 0.
+ * v_scale counts as at least 2^-48 and at most 2^48 (what et_kv_commit_paged
+ * writes); k_scale may be any finite value.  Rows of a page past the prefix
+ * are not used, whatever they hold.  A prefix past max_prefix or past
+ * max_blocks pages is cut there, a page id outside the cache drops its
+ * tokens; both set ET_DEV_BAD_INDEX.
+ * Scores, softmax statistics and outputs accumulate in fp32.  bf16 inputs:
+ * the codes and a scaled copy of q go through fp16 tensor-core products (an
+ * 8-bit code is exact in fp16; q loses only what lies 2^-24 below the largest
+ * of its row), weights are rounded to fp16 (cached tokens) or bf16 (tree
+ * rows) before they meet V.  fp32 inputs: fp32 throughout.
+ */
+et_status et_tree_attention_paged(const et_paged_attn_shape *shape, const et_paged_cache *cache,
+                                  const int32_t *block_table, const int32_t *prefix_len, const void *q,
+                                  const void *k_tree, const void *v_tree, const uint64_t *mask, void *out, float *lse,
+                                  int32_t *dev_status, void *ws, size_t ws_bytes, et_stream_t stream);
+/* Workspace bytes of that call (0 if no split merge is needed), and the blocks its keys are split over (-1 if the shape breaks a limit). */
+size_t et_tree_attention_paged_workspace_size(const et_paged_attn_shape *shape, const et_paged_cache *cache);
+int32_t et_tree_attention_paged_splits(const et_paged_attn_shape *shape, const et_paged_cache *cache);
 
 #ifdef __cplusplus
 }

@@ -11,3 +11,5 @@ from .eagle_tree_oracle import (TreeCfg, Tree, AcceptResult, GREEDY, STOCH_POINT
 from .kv_commit_oracle import kv_commit  # noqa: F401
 from .static_tree_oracle import static_tree, static_tree_sampled, static_depths  # noqa: F401
 from .lm_head_oracle import lm_head_logits, lm_head_error_bound  # noqa: F401
+from .paged_oracle import (code_value, decode, encode, page_scale, block_map, kv_commit_paged,  # noqa: F401
+                           dequantised, paged_attention)

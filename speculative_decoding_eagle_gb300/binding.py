@@ -20,8 +20,9 @@ from .build_lib import LIB
 c_i32, c_i64, c_f32, c_vp, c_sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
 ET_OK, ET_ERR_INVALID_ARG, ET_ERR_UNSUPPORTED, ET_ERR_WORKSPACE, ET_ERR_CUDA, ET_ERR_TIMEOUT = range(6)
-ET_DEV_NONFINITE, ET_DEV_BAD_INDEX, ET_DEV_DISCONNECTED, ET_DEV_TIMEOUT = 1, 2, 4, 8
+ET_DEV_NONFINITE, ET_DEV_BAD_INDEX, ET_DEV_DISCONNECTED, ET_DEV_TIMEOUT, ET_DEV_NO_PAGES = 1, 2, 4, 8, 16
 ET_BF16, ET_F32 = 0, 1
+ET_KV_E4M3, ET_KV_E5M2 = 0, 1
 ET_ACCEPT_GREEDY, ET_ACCEPT_STOCH_POINT, ET_ACCEPT_STOCH_DRAFTQ = 0, 1, 2
 ATTN_AUTO, ATTN_MMA_SYNC, ATTN_TCGEN05 = 0, 1, 2
 ET_ATTN_INPUTS_READY = 1
@@ -32,7 +33,8 @@ EXPORTED = ("et_num_candidates", "et_layer_expanded", "et_layer_base", "et_tree_
             "et_status_string", "et_abi_version", "et_tree_expand", "et_tree_expand_noalloc", "et_tree_rerank", "et_tree_rerank_mask",
             "et_tree_build", "et_tree_build_launches", "et_set_wait_limit", "et_set_expand_kernel",
             "et_tree_mask_posids", "et_tree_attention", "et_verify_accept", "et_kv_commit", "et_static_tree", "et_lm_head", "et_static_tree_sampled",
-            "et_static_tree_workspace_size")
+            "et_static_tree_workspace_size", "et_block_map", "et_kv_commit_paged", "et_tree_attention_paged",
+            "et_tree_attention_paged_workspace_size", "et_tree_attention_paged_splits")
 
 
 class TreeCfgC(ctypes.Structure):
@@ -62,6 +64,25 @@ class StaticCfgC(ctypes.Structure):
 class CommitShapeC(ctypes.Structure):
     _fields_ = [("B", c_i32), ("N", c_i32), ("Hkv", c_i32), ("d", c_i32), ("path_len", c_i32), ("dtype", c_i32),
                 ("kv_head_stride", c_i64), ("kv_rows", c_i64), ("feat_dim", c_i32)]
+
+
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [("Hkv", c_i32), ("d", c_i32), ("page_size", c_i32), ("format", c_i32), ("num_pages", c_i64),
+                ("page_stride", c_i64), ("k_pages", c_vp), ("v_pages", c_vp), ("k_scale", c_vp), ("v_scale", c_vp)]
+
+
+class BlockMapShapeC(ctypes.Structure):
+    _fields_ = [("B", c_i32), ("page_size", c_i32), ("max_blocks", c_i32), ("max_new", c_i32), ("num_pages", c_i64)]
+
+
+class PagedCommitShapeC(ctypes.Structure):
+    _fields_ = [("B", c_i32), ("N", c_i32), ("path_len", c_i32), ("max_blocks", c_i32), ("dtype", c_i32),
+                ("feat_dim", c_i32)]
+
+
+class PagedAttnShapeC(ctypes.Structure):
+    _fields_ = [("B", c_i32), ("N", c_i32), ("Hq", c_i32), ("max_blocks", c_i32), ("dtype", c_i32), ("scale", c_f32),
+                ("max_prefix", c_i32), ("num_splits", c_i32)]
 
 
 class EtError(RuntimeError):
@@ -114,6 +135,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                  c_vp, c_vp]),
         "et_verify_accept": (c_i32, [P(TreeCfgC), c_i32, P(TreeC), c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_vp,
                                      c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+        "et_block_map": (c_i32, [P(BlockMapShapeC), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+        "et_kv_commit_paged": (c_i32, [P(PagedCommitShapeC), P(PagedCacheC), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                       c_vp, c_vp, c_vp, c_vp]),
+        "et_tree_attention_paged": (c_i32, [P(PagedAttnShapeC), P(PagedCacheC), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                            c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+        "et_tree_attention_paged_workspace_size": (c_sz, [P(PagedAttnShapeC), P(PagedCacheC)]),
+        "et_tree_attention_paged_splits": (c_i32, [P(PagedAttnShapeC), P(PagedCacheC)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -477,3 +505,199 @@ def et_static_tree_sampled(B: int, V: int, temperature: float, parent: torch.Ten
                                        _ptr(dev_status, torch.int32, "dev_status"), _ptr(ws, None, "ws"),
                                        ws.numel() * ws.element_size(), _stream(stream))
     _check("et_static_tree_sampled", st)
+
+
+# ---------------------------------------------------------------------------
+# the paged 8-bit KV cache
+# ---------------------------------------------------------------------------
+_TORCH_DTYPE = {ET_BF16: torch.bfloat16, ET_F32: torch.float32}
+_KV_FORMAT = {torch.float8_e4m3fn: ET_KV_E4M3, torch.float8_e5m2: ET_KV_E5M2}
+_i32, _i64, _f32 = torch.int32, torch.int64, torch.float32
+
+
+def _arg(t: Optional[torch.Tensor], dtype, shape, device: int, what: str) -> Optional[int]:
+    """The address of an argument that must be a contiguous tensor of this type, shape and device."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _status(t: Optional[torch.Tensor], device: int) -> Optional[int]:
+    return None if t is None else _arg(t, _i32, (1,), device, "dev_status")
+
+
+def _call(fn: str, device: int, stream: Optional[torch.cuda.Stream], *args) -> None:
+    """Run a call on the device of its tensors, on `stream` or that device's current stream."""
+    if device < 0:
+        raise ValueError(f"{fn} takes CUDA tensors")
+    f = getattr(load(), fn)
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch.cuda.current_device():
+        st = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, s)
+    if st != ET_OK:
+        raise EtError(fn, st)
+
+
+class _Shape:
+    """A frozen shape whose C struct is built once."""
+
+    def ref(self):
+        r = self.__dict__.get("_ref")
+        if r is None:
+            c = self.c()
+            r = ctypes.byref(c)  # keeps c alive
+            self.__dict__["_ref"] = r
+        return r
+
+
+class PagedCache:
+    """Device tensors behind one ``et_paged_cache``.
+
+    k_pages, v_pages: float8_e4m3fn or float8_e5m2 ``[num_pages, Hkv, page_size, d]``, each page contiguous (the
+    stride from page to page is free, so both may be views of one ``[num_pages, 2, Hkv, page_size, d]`` tensor);
+    k_scale, v_scale: fp32 ``[num_pages, Hkv]``.
+    """
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k_pages.dim() != 4 or k_pages.dtype not in _KV_FORMAT or not k_pages.is_cuda:
+            raise ValueError("k_pages must be a CUDA float8 [num_pages, Hkv, page_size, d] tensor")
+        self.num_pages, self.Hkv, self.page_size, self.d = k_pages.shape
+        if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or v_pages.stride() != k_pages.stride() or \
+                v_pages.device != k_pages.device:
+            raise ValueError("v_pages must match k_pages in shape, type, strides and device")
+        if k_pages.stride()[1:] != (self.page_size * self.d, self.d, 1):
+            raise ValueError("each page must be contiguous")
+        self.device = k_pages.get_device()
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _arg(t, _f32, (self.num_pages, self.Hkv), self.device, what)
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.format = _KV_FORMAT[k_pages.dtype]
+        # one page: its stride may be anything
+        stride = k_pages.stride(0) if self.num_pages > 1 else self.Hkv * self.page_size * self.d
+        self._c = PagedCacheC(self.Hkv, self.d, self.page_size, self.format, self.num_pages, stride,
+                              k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+    @staticmethod
+    def allocate(num_pages: int, Hkv: int, page_size: int, d: int, dtype=torch.float8_e4m3fn,
+                 device="cuda") -> "PagedCache":
+        """Zeroed pages, K and V of a page side by side."""
+        kv = torch.zeros((num_pages, 2, Hkv, page_size, d), dtype=torch.uint8, device=device).view(dtype)
+        scale = torch.ones((2, num_pages, Hkv), dtype=torch.float32, device=device)
+        return PagedCache(kv[:, 0], kv[:, 1], scale[0], scale[1])
+
+
+@dataclasses.dataclass(frozen=True)
+class BlockMapShape(_Shape):
+    B: int
+    page_size: int
+    max_blocks: int
+    num_pages: int
+    max_new: int = 0
+
+    def c(self) -> BlockMapShapeC:
+        return BlockMapShapeC(self.B, self.page_size, self.max_blocks, self.max_new, self.num_pages)
+
+
+def et_block_map(shape: BlockMapShape, prefix_len: torch.Tensor, new_len: torch.Tensor, n_blocks: torch.Tensor,
+                 block_table: torch.Tensor, free_list: torch.Tensor, free_count: torch.Tensor,
+                 slot_map: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """Return and take pages so that each request holds its length, and map its new tokens to slots."""
+    B, dev = (shape.B,), n_blocks.get_device()
+    _call("et_block_map", dev, stream, shape.ref(), _arg(prefix_len, _i32, B, dev, "prefix_len"),
+          _arg(new_len, _i32, B, dev, "new_len"), _arg(n_blocks, _i32, B, dev, "n_blocks"),
+          _arg(block_table, _i32, (shape.B, shape.max_blocks), dev, "block_table"),
+          _arg(free_list, _i32, (shape.num_pages,), dev, "free_list"),
+          _arg(free_count, _i32, (1,), dev, "free_count"),
+          _arg(slot_map, _i64, (shape.B, shape.max_new), dev, "slot_map"), _status(dev_status, dev))
+
+
+@dataclasses.dataclass(frozen=True)
+class PagedCommitShape(_Shape):
+    B: int
+    N: int
+    path_len: int
+    max_blocks: int
+    dtype: int = ET_BF16
+    feat_dim: int = 0
+
+    def c(self) -> PagedCommitShapeC:
+        return PagedCommitShapeC(self.B, self.N, self.path_len, self.max_blocks, self.dtype, self.feat_dim)
+
+
+def et_kv_commit_paged(shape: PagedCommitShape, cache: PagedCache, block_table: torch.Tensor, k_tree: torch.Tensor,
+                       v_tree: torch.Tensor, accept_len: torch.Tensor, path: Optional[torch.Tensor],
+                       prefix_len: torch.Tensor, new_prefix_len: torch.Tensor,
+                       features: Optional[torch.Tensor] = None, feat_out: Optional[torch.Tensor] = None,
+                       dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise each sequence's accepted path (``path`` None: its first accept_len + 1 rows) into its pages."""
+    dt, dev, B, N = _TORCH_DTYPE[shape.dtype], cache.device, shape.B, shape.N
+    tree = (B, N, cache.Hkv, cache.d)
+    _call("et_kv_commit_paged", dev, stream, shape.ref(), cache._ref,
+          _arg(block_table, _i32, (B, shape.max_blocks), dev, "block_table"), _arg(k_tree, dt, tree, dev, "k_tree"),
+          _arg(v_tree, dt, tree, dev, "v_tree"), _arg(accept_len, _i32, (B,), dev, "accept_len"),
+          _arg(path, _i32, (B, shape.path_len), dev, "path"), _arg(prefix_len, _i32, (B,), dev, "prefix_len"),
+          _arg(new_prefix_len, _i32, (B,), dev, "new_prefix_len"),
+          _arg(features, dt, (B, N, shape.feat_dim), dev, "features"),
+          _arg(feat_out, dt, (B, shape.path_len, shape.feat_dim), dev, "feat_out"), _status(dev_status, dev))
+
+
+@dataclasses.dataclass(frozen=True)
+class PagedAttnShape(_Shape):
+    B: int
+    N: int
+    Hq: int
+    max_blocks: int
+    dtype: int = ET_BF16
+    scale: float = 0.0  # 0: 1 / sqrt(d) of the cache
+    max_prefix: int = 0
+    num_splits: int = 0
+
+    def c(self) -> PagedAttnShapeC:
+        return PagedAttnShapeC(self.B, self.N, self.Hq, self.max_blocks, self.dtype, self.scale, self.max_prefix,
+                               self.num_splits)
+
+    def for_cache(self, cache: PagedCache):
+        """The C struct with the default scale filled in, kept per head dim."""
+        refs = self.__dict__.setdefault("_refs", {})
+        r = refs.get(cache.d)
+        if r is None:
+            c = self.c()
+            if not c.scale > 0:
+                c.scale = cache.d ** -0.5
+            r = refs[cache.d] = ctypes.byref(c)
+        return r
+
+
+def et_tree_attention_paged_workspace_size(shape: PagedAttnShape, cache: PagedCache) -> int:
+    with torch.cuda.device(cache.device):
+        return load().et_tree_attention_paged_workspace_size(shape.for_cache(cache), cache._ref)
+
+
+def et_tree_attention_paged_splits(shape: PagedAttnShape, cache: PagedCache) -> int:
+    with torch.cuda.device(cache.device):
+        return load().et_tree_attention_paged_splits(shape.for_cache(cache), cache._ref)
+
+
+def et_tree_attention_paged(shape: PagedAttnShape, cache: PagedCache, block_table: torch.Tensor,
+                            prefix_len: torch.Tensor, q: torch.Tensor, k_tree: torch.Tensor, v_tree: torch.Tensor,
+                            mask: Optional[torch.Tensor], out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                            ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """Attention of the tree rows (or, with N = 1, one token) over a paged 8-bit prefix and their ancestors."""
+    dt, dev, B, N = _TORCH_DTYPE[shape.dtype], cache.device, shape.B, shape.N
+    rows, tree = (B, N, shape.Hq, cache.d), (B, N, cache.Hkv, cache.d)
+    _call("et_tree_attention_paged", dev, stream, shape.for_cache(cache), cache._ref,
+          _arg(block_table, _i32, (B, shape.max_blocks), dev, "block_table"),
+          _arg(prefix_len, _i32, (B,), dev, "prefix_len"), _arg(q, dt, rows, dev, "q"),
+          _arg(k_tree, dt, tree, dev, "k_tree"), _arg(v_tree, dt, tree, dev, "v_tree"),
+          _arg(mask, _i64, (B, N, (N + 63) // 64), dev, "mask"), _arg(out, dt, rows, dev, "out"),
+          _arg(lse, _f32, (B, shape.Hq, N), dev, "lse"), _status(dev_status, dev),
+          None if ws is None else _arg(ws, torch.uint8, ws.shape, dev, "ws"), 0 if ws is None else ws.numel())

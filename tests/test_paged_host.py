@@ -1,0 +1,204 @@
+"""The paged 8-bit KV cache without a GPU: the oracle against closed forms and
+hand-worked examples, and every argument that the calls refuse."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from speculative_decoding_eagle_gb300 import binding as E
+from speculative_decoding_eagle_gb300 import build_lib
+
+FAKE = 0x100000  # a non-null, 256-byte aligned address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_lib.build()
+    return E.load()
+
+
+# ---------------------------------------------------------------------------
+# the oracle
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt,dt", [("e4m3", torch.float8_e4m3fn), ("e5m2", torch.float8_e5m2)])
+def test_formats_match_torch(fmt, dt):
+    codes = np.arange(256, dtype=np.uint8)
+    want = torch.from_numpy(codes.copy()).view(dt).float().numpy().astype(np.float64)
+    np.testing.assert_array_equal(O.decode(codes, fmt), want)
+    rng = np.random.default_rng(5)
+    finite = np.unique(want[np.isfinite(want)])
+    mid = (finite[1:] + finite[:-1]) / 2  # every tie, and points beside them
+    x = np.concatenate([finite, mid, np.nextafter(mid, -np.inf), np.nextafter(mid, np.inf),
+                        rng.standard_normal(2000) * finite.max() / 3]).astype(np.float32)
+    x = x[np.abs(x) <= finite.max()]
+    got = O.decode(O.encode(x, fmt), fmt)
+    np.testing.assert_array_equal(got, torch.from_numpy(x).to(dt).float().numpy())
+    assert O.decode(O.encode(np.array([1e9, -1e9, np.inf]), fmt), fmt).tolist() == [finite.max(), -finite.max(), finite.max()]
+    assert np.isnan(O.decode(O.encode(np.array([np.nan]), fmt), fmt))[0]
+
+
+def test_page_scale_is_the_smallest_power_of_two():
+    for fmt in ("e4m3", "e5m2"):
+        top = O.paged_oracle.MAX_VALUE[fmt]
+        assert O.page_scale(top, fmt) == 1.0
+        assert O.page_scale(np.nextafter(top, 1e9), fmt) == 2.0
+        assert O.page_scale(top / 2, fmt) == 0.5
+        assert O.page_scale(0.0, fmt) == 2.0 ** -48 and O.page_scale(1e-30, fmt) == 2.0 ** -48
+        assert O.page_scale(1e30, fmt) == 2.0 ** 48
+
+
+def test_block_map_by_hand():
+    # page size 4: request 0 (two pages) ends, request 1 grows from one page to three, request 2 is absent
+    table = np.array([[7, 2, -1], [5, -1, -1], [9, -1, -1]], np.int32)
+    n, t, free, slots, short, bad = O.block_map([0, 4, -1], [0, 5, 1], [2, 1, 1], table, [1, 3], 4, 5)
+    assert n.tolist() == [0, 3, 1] and not short and not bad
+    assert t.tolist() == [[-1, -1, -1], [5, 2, 7], [9, -1, -1]]  # 7 and 2 went on the stack; 2 was on top
+    assert free == [1, 3]
+    assert slots.tolist() == [[-1] * 5, [8, 9, 10, 11, 28], [-1] * 5]
+    # three pages wanted, one there: request 0 waits, and so does request 1 behind it
+    n, t, free, slots, short, bad = O.block_map([9, 0], [0, 2], [0, 0], np.full((2, 3), -1, np.int32), [6], 4, 2)
+    assert short and n.tolist() == [0, 0] and free == [6] and (slots == -1).all()
+
+
+def test_commit_by_hand():
+    # e4m3, page of 16: one cached token 448 at scale 1; a row of 1000 needs scale 4 (448 * 2 < 1000)
+    codes = np.zeros((1, 1, 16, 64), np.uint8)
+    codes[0, 0, 0] = O.encode(np.full(64, 448.0), "e4m3")
+    codes[0, 0, 0, 1] = 1                          # the smallest value, 2^-9: falls below at scale 4
+    tree = np.full((1, 2, 1, 64), 1000.0)
+    tree[0, 1, 0, 0] = 3.0
+    c, s = O.kv_commit_paged(codes, np.ones((1, 1), np.float32), "e4m3", np.zeros((1, 1), np.int32), tree,
+                             np.array([1]), np.array([[0, 1]]), np.array([1]))
+    assert s[0, 0] == 4.0
+    v = O.decode(c, "e4m3")[0, 0] * 4.0
+    assert v[0, 0] == 448.0 and v[0, 1] == 0.0     # 2^-9 / 4 rounds to the even neighbour, zero
+    assert v[1, 0] == 1024.0 and v[2, 0] == 3.0    # 1000 / 4 = 250: between 240 and 256, nearer 256
+    assert (c[0, 0, 3:] == 0).all()
+
+
+def test_paged_attention_matches_the_dense_oracle():
+    rng = np.random.default_rng(3)
+    N, Hq, Hkv, d, L, P = 5, 4, 2, 64, 21, 16
+    codes = rng.integers(0, 256, (3, Hkv, P, d)).astype(np.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0
+    scale = (2.0 ** rng.integers(-8, -4, (3, Hkv))).astype(np.float32)
+    kc = O.dequantised(codes, scale, "e4m3", np.array([2, 0]), L)
+    q, kt, vt = rng.standard_normal((N, Hq, d)), rng.standard_normal((N, Hkv, d)), rng.standard_normal((N, Hkv, d))
+    keep = np.tril(np.ones((N, N), bool))
+    out, lse, abs_c, abs_t, _ = O.paged_attention(q, kc, kc, kt, vt, np.ones(L, bool), keep, d ** -0.5)
+    mask = np.array([[[sum(1 << j for j in range(i + 1))] for i in range(N)]], np.uint64)
+    ref, rlse = O.tree_attention(q[None], [kc], [kc], kt[None], vt[None], mask, d ** -0.5)
+    np.testing.assert_allclose(out, ref[0], rtol=1e-12, atol=1e-12)
+    np.testing.assert_allclose(lse, rlse[0], rtol=1e-12)
+    assert (abs_c + abs_t >= np.abs(out) - 1e-12).all()
+
+
+# ---------------------------------------------------------------------------
+# refusals
+# ---------------------------------------------------------------------------
+def cache(**kw):
+    c = dict(Hkv=8, d=128, page_size=64, format=0, num_pages=100, page_stride=8 * 64 * 128, k_pages=FAKE,
+             v_pages=FAKE, k_scale=FAKE, v_scale=FAKE)
+    c.update(kw)
+    return E.PagedCacheC(*c.values())
+
+
+BAD_CACHES = [(dict(Hkv=0), 1), (dict(d=0), 1), (dict(d=96), 2), (dict(d=256), 2), (dict(page_size=0), 1),
+              (dict(page_size=24), 2), (dict(page_size=272, page_stride=1 << 20), 2), (dict(format=2), 1),
+              (dict(format=-1), 1), (dict(num_pages=0), 1), (dict(num_pages=1 << 31), 1),
+              (dict(page_stride=8 * 64 * 128 - 16), 1), (dict(page_stride=8 * 64 * 128 + 8), 1),
+              (dict(page_stride=1 << 40), 1), (dict(k_pages=None), 1), (dict(v_pages=None), 1),
+              (dict(k_scale=None), 1), (dict(v_scale=None), 1), (dict(k_pages=FAKE + 8), 1),
+              (dict(v_scale=FAKE + 2), 1)]
+
+
+def attn(lib, c=None, ws=FAKE, wsb=1 << 40, **kw):
+    s = dict(B=2, N=61, Hq=64, max_blocks=16, dtype=0, scale=0.088, max_prefix=1024, num_splits=0)
+    p = dict(table=FAKE, prefix=FAKE, q=FAKE, kt=FAKE, vt=FAKE, mask=FAKE, out=FAKE, lse=None)
+    p.update({k: kw.pop(k) for k in list(kw) if k in p})
+    s.update(kw)
+    return lib.et_tree_attention_paged(ctypes.byref(E.PagedAttnShapeC(*s.values())), ctypes.byref(c or cache()),
+                                       p["table"], p["prefix"], p["q"], p["kt"], p["vt"], p["mask"], p["out"],
+                                       p["lse"], None, ws, wsb, None)
+
+
+def commit(lib, c=None, **kw):
+    s = dict(B=2, N=61, path_len=7, max_blocks=16, dtype=0, feat_dim=64)
+    p = dict(table=FAKE, kt=FAKE, vt=FAKE, alen=FAKE, path=FAKE, prefix=FAKE, newp=FAKE + 256, feat=FAKE, fout=FAKE)
+    p.update({k: kw.pop(k) for k in list(kw) if k in p})
+    s.update(kw)
+    return lib.et_kv_commit_paged(ctypes.byref(E.PagedCommitShapeC(*s.values())), ctypes.byref(c or cache()),
+                                  p["table"], p["kt"], p["vt"], p["alen"], p["path"], p["prefix"], p["newp"],
+                                  p["feat"], p["fout"], None, None)
+
+
+def bmap(lib, **kw):
+    s = dict(B=4, page_size=64, max_blocks=16, max_new=8, num_pages=100)
+    p = dict(prefix=FAKE, new=FAKE, n=FAKE, table=FAKE, free=FAKE, count=FAKE, slots=FAKE)
+    p.update({k: kw.pop(k) for k in list(kw) if k in p})
+    s.update(kw)
+    return lib.et_block_map(ctypes.byref(E.BlockMapShapeC(*s.values())), p["prefix"], p["new"], p["n"], p["table"],
+                            p["free"], p["count"], p["slots"], None, None)
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_bad_caches_are_refused(lib, bad, status):
+    assert attn(lib, c=cache(**bad)) == status
+    assert commit(lib, c=cache(**bad)) == status
+    shape = E.PagedAttnShapeC(2, 61, 64, 16, 0, 0.088, 1024, 0)
+    assert lib.et_tree_attention_paged_splits(ctypes.byref(shape), ctypes.byref(cache(**bad))) == -1
+    assert lib.et_tree_attention_paged_workspace_size(ctypes.byref(shape), ctypes.byref(cache(**bad))) == 0
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(B=0), 1), (dict(N=0), 1), (dict(N=129), 1), (dict(Hq=0), 1), (dict(Hq=60), 1), (dict(max_blocks=0), 1),
+    (dict(dtype=2), 1), (dict(scale=0.0), 1), (dict(scale=math.nan), 1), (dict(max_prefix=-1), 1),
+    (dict(num_splits=-1), 1), (dict(B=65536), 2), (dict(max_blocks=1 << 26), 2), (dict(table=None), 1),
+    (dict(prefix=None), 1), (dict(q=None), 1), (dict(kt=None), 1), (dict(vt=None), 1), (dict(out=None), 1),
+    (dict(q=FAKE + 8), 1), (dict(out=FAKE + 2), 1), (dict(mask=FAKE + 4), 1)])
+def test_attention_refusals(lib, bad, status):
+    assert attn(lib, **bad) == status
+
+
+def test_attention_null_structs(lib):
+    assert lib.et_tree_attention_paged(None, ctypes.byref(cache()), *[FAKE] * 7, None, None, None, 0, None) == 1
+    shape = E.PagedAttnShapeC(2, 61, 64, 16, 0, 0.088, 1024, 0)
+    assert lib.et_tree_attention_paged(ctypes.byref(shape), None, *[FAKE] * 7, None, None, None, 0, None) == 1
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(B=0), 1), (dict(B=65536), 1), (dict(N=0), 1), (dict(path_len=-1), 1), (dict(path_len=18), 1),
+    (dict(max_blocks=0), 1), (dict(dtype=2), 1), (dict(feat_dim=-8), 1), (dict(feat_dim=4), 2),
+    (dict(path=None), 1), (dict(path=None, path_len=0), 1), (dict(path_len=0), 1), (dict(max_blocks=1 << 26), 2),
+    (dict(table=None), 1), (dict(kt=None), 1), (dict(vt=None), 1), (dict(alen=None), 1), (dict(prefix=None), 1),
+    (dict(newp=None), 1), (dict(newp=FAKE), 1), (dict(feat=None), 1), (dict(fout=None), 1), (dict(kt=FAKE + 8), 1),
+    (dict(fout=FAKE + 8), 1)])
+def test_commit_refusals(lib, bad, status):
+    assert commit(lib, **bad) == status
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(B=0), 1), (dict(B=4097), 2), (dict(page_size=0), 1), (dict(max_blocks=0), 1), (dict(max_new=-1), 1),
+    (dict(num_pages=0), 1), (dict(num_pages=1 << 31), 1), (dict(max_blocks=1 << 29), 2),
+    (dict(num_pages=(1 << 31) - 1), 2), (dict(max_blocks=1 << 26), 2), (dict(max_new=0), 1), (dict(slots=None), 1),
+    (dict(prefix=None), 1), (dict(new=None), 1), (dict(n=None), 1), (dict(table=None), 1), (dict(free=None), 1),
+    (dict(count=None), 1)])
+def test_block_map_refusals(lib, bad, status):
+    assert bmap(lib, **bad) == status
+
+
+def test_binding_refuses_host_and_misshapen_tensors():
+    with pytest.raises(ValueError):
+        E.PagedCache(*[torch.zeros(4, 2, 16, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)] * 2,
+                     *[torch.ones(4, 2)] * 2)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    shape = E.BlockMapShape(B=2, page_size=16, max_blocks=3, num_pages=5)
+    with pytest.raises(ValueError, match="prefix_len"):
+        E.et_block_map(shape, torch.zeros(2), i32(2), i32(2), i32(2, 3), i32(5), i32(1))
+    with pytest.raises(ValueError, match="block_table"):
+        E.et_block_map(shape, i32(2), i32(2), i32(2), i32(2, 4), i32(5), i32(1))
+    with pytest.raises(ValueError, match="CUDA"):
+        E.et_block_map(shape, i32(2), i32(2), i32(2), i32(2, 3), i32(5), i32(1))
