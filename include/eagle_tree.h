@@ -734,10 +734,13 @@ et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_
  * max_blocks pages is cut there, a page id outside the cache drops its
  * tokens; both set ET_DEV_BAD_INDEX.
  * Scores, softmax statistics and outputs accumulate in fp32.  bf16 inputs:
- * the codes and a scaled copy of q go through fp16 tensor-core products (an
- * 8-bit code is exact in fp16; q loses only what lies 2^-24 below the largest
- * of its row), weights are rounded to fp16 (cached tokens) or bf16 (tree
- * rows) before they meet V.  fp32 inputs: fp32 throughout.
+ * cached codes meet q as it is (two 8-bit terms per element; only what lies
+ * 2^-18 below the largest of its row is lost), weights are rounded to fp16
+ * (cached tokens) or bf16 (tree rows) before they meet V.  A q row that holds
+ * a NaN or an infinity gives NaN.  fp32 inputs: fp32 throughout.
+ * bf16 inputs: a bounded wait that expires sets ET_DEV_TIMEOUT and leaves that
+ * block's rows undefined.  Calls that can run at the same time need separate
+ * workspaces.
  */
 et_status et_tree_attention_paged(const et_paged_attn_shape *shape, const et_paged_cache *cache,
                                   const int32_t *block_table, const int32_t *prefix_len, const void *q,

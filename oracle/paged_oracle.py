@@ -164,13 +164,14 @@ def paged_attention(q, kc, vc, k_tree, v_tree, keep_prefix, keep_tree, scale):
     """One sequence: q [N, Hq, d], kc/vc [Hkv, L, d], k/v_tree [N, Hkv, d], keep_prefix [L] and keep_tree [N, N] bool.
 
     Returns out [N, Hq, d], lse [Hq, N], and what bounds a kernel's error: the weighted magnitudes sum p |v| over the
-    cached tokens and over the tree rows, [N, Hq, d] each, and the largest sum |q||k| * scale of a row, [Hq, N]."""
+    cached tokens and over the tree rows, [N, Hq, d] each, the largest sum |q||k| * scale of a row, [Hq, N], and the
+    same for cached tokens with every |q| at its row's largest."""
     q = np.asarray(q, np.float64)
     N, Hq, d = q.shape
     G = Hq // k_tree.shape[1]
     L = kc.shape[1]
     out, lse = np.zeros((N, Hq, d)), np.full((Hq, N), -np.inf)
-    abs_c, abs_t, reach = np.zeros((N, Hq, d)), np.zeros((N, Hq, d)), np.zeros((Hq, N))
+    abs_c, abs_t, reach, flat = np.zeros((N, Hq, d)), np.zeros((N, Hq, d)), np.zeros((Hq, N)), np.zeros((Hq, N))
     for h in range(Hq):
         g = h // G
         for i in range(N):
@@ -188,4 +189,6 @@ def paged_attention(q, kc, vc, k_tree, v_tree, keep_prefix, keep_tree, scale):
             abs_c[i, h] = p[:len(jc)] @ np.abs(V[:len(jc)])
             abs_t[i, h] = p[len(jc):] @ np.abs(V[len(jc):])
             reach[h, i] = scale * (np.abs(K) @ np.abs(q[i, h])).max()
-    return out, lse, abs_c, abs_t, reach
+            if len(jc):
+                flat[h, i] = scale * np.abs(q[i, h]).max() * np.abs(kc[g][jc]).sum(1).max()
+    return out, lse, abs_c, abs_t, reach, flat

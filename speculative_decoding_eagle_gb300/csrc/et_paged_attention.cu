@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 
 #include "et_paged.cuh"
+#include "et_tc.cuh"
 
 namespace et {
 namespace {
@@ -30,13 +31,6 @@ struct PagedAttnArgs {
   float *lse;
   int32_t *dev_status;
 };
-
-template <typename T> __device__ __forceinline__ float to_f32(T v);
-template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 // prefix length of sequence b as the kernels use it: -1 = no sequence here
 __device__ __forceinline__ int paged_prefix(const PagedAttnArgs &a, int b, int &bad) {
@@ -57,13 +51,13 @@ __device__ __forceinline__ bool tree_keeps(const PagedAttnArgs &a, int b, int i,
 }
 
 // ---------------------------------------------------------------------------
-// CUDA cores: one block per (row, head, sequence), fp32 throughout
+// fp32: CUDA cores, one block per (row, head, sequence)
 // ---------------------------------------------------------------------------
 // Each warp takes every fourth group of 32 keys: a lane scores one key (its
 // whole row, 16 bytes a load), the group's maximum and sum are warp
 // reductions, then the lanes turn to the head's dims and add the 32 weighted
 // V rows, whose loads do not depend on one another.
-template <typename T, int FMT, int D>
+template <int FMT, int D>
 __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
   constexpr int PL = D / 32;  // dims per lane
   __shared__ float qs[D];
@@ -77,9 +71,9 @@ __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
   const int L = paged_prefix(a, b, bad);
   if (L < 0) return;
   const long long orow = ((long long)b * a.N + i) * a.Hq + h;
-  for (int c = t; c < D; c += 128) qs[c] = to_f32(static_cast<const T *>(a.q)[orow * D + c]);
+  for (int c = t; c < D; c += 128) qs[c] = static_cast<const float *>(a.q)[orow * D + c];
   __syncthreads();
-  const T *KT = static_cast<const T *>(a.kt), *VT = static_cast<const T *>(a.vt);
+  const float *KT = static_cast<const float *>(a.kt), *VT = static_cast<const float *>(a.vt);
   float m = -INFINITY, l = 0.f, acc[PL];
 #pragma unroll
   for (int c = 0; c < PL; ++c) acc[c] = 0.f;
@@ -121,7 +115,7 @@ __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
       s *= ks;
     } else if (ok) {
 #pragma unroll 8
-      for (int c = 0; c < D; ++c) s = fmaf(qs[c], to_f32(KT[at + c]), s);
+      for (int c = 0; c < D; ++c) s = fmaf(qs[c], KT[at + c], s);
     }
     s = ok ? s * a.scale_log2 : -INFINITY;
     const unsigned int keep = __ballot_sync(0xffffffffu, ok);
@@ -154,7 +148,7 @@ __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < PL; ++c) x[c] = to_f32(VT[row + PL * lane + c]);
+        for (int c = 0; c < PL; ++c) x[c] = VT[row + PL * lane + c];
       }
 #pragma unroll
       for (int c = 0; c < PL; ++c) acc[c] = fmaf(w, x[c], acc[c]);
@@ -180,24 +174,742 @@ __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) v += wacc[w][c] * wts[w];
-    static_cast<T *>(a.out)[orow * D + c] = from_f32<T>(Ls == 0.f ? 0.f : v / Ls);
+    static_cast<float *>(a.out)[orow * D + c] = Ls == 0.f ? 0.f : v / Ls;
   }
   if (t == 0 && a.lse)
     a.lse[((long long)b * a.Hq + h) * a.N + i] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * 0.69314718055994531f;
   if (bad) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
 }
 
-template <typename T, int FMT>
+template <int FMT>
 et_status launch_row(const PagedAttnArgs &a, int d, cudaStream_t st) {
   const dim3 grid(a.N, a.Hq, a.B);
-  if (d == 64) return et_launch(k_paged_attn_row<T, FMT, 64>, grid, dim3(128), 0, st, 0, a);
-  return et_launch(k_paged_attn_row<T, FMT, 128>, grid, dim3(128), 0, st, 0, a);
+  if (d == 64) return et_launch(k_paged_attn_row<FMT, 64>, grid, dim3(128), 0, st, 0, a);
+  return et_launch(k_paged_attn_row<FMT, 128>, grid, dim3(128), 0, st, 0, a);
+}
+
+// ---------------------------------------------------------------------------
+// bf16: tensor cores (mma.sync), cached codes as operands
+// ---------------------------------------------------------------------------
+// The scores of cached keys are 8-bit products: K's codes are the B operand
+// as they lie in the page (no conversion), q scaled by a power of two per row
+// and split into two e4m3 terms, q = hi + lo, each four significant bits of a
+// bf16 value's eight, is the A operand of two m16n8k32 products into one fp32
+// sum.  (Exact for elements above 2^-11 of their row's largest, within 2^-18
+// of it below; the sums keep fp32 precision, checked against exact sums.)
+// P.V runs as fp16 m16n8k16 products: codes become fp16 exactly, weights are
+// kept at most 2^15 and lose only what lies 2^-31 below the largest.
+// Measured on this part: 8-bit m16n8k32 2241 TFLOP/s, fp16 m16n8k16 600, so
+// two 8-bit products cost half of one fp16 product and save K's conversion.
+//
+// A block of four warps owns R = 16 * WR * MT query rows (token, head in
+// group) of one KV head and a chunk of the prefix.  WR warps share the rows,
+// KG = 4 / WR groups of them take alternate tiles of 32 keys.  Each group has
+// its own ring of tiles, brought by TMA (one box of 32 rows, two of 16 where
+// a page is not a multiple of 32) into the 128- or 64-byte swizzle, in which
+// every operand load is conflict-free.  Page ids and scales are fetched 32
+// units of 16 keys at a time, one per lane, a batch ahead.
+constexpr int kPaThreads = 128;
+constexpr int kPaWarps = 4;
+constexpr int kPaTile = 32;  // keys per tile
+constexpr float kPaTop = 7.f, kPaSlack = 8.f;  // weights lie below 2^kPaTop when the maximum moves, below 2^15 always
+
+struct PagedMmaArgs {
+  PagedAttnArgs a;
+  int S, tiles_y;       // chunks, Hkv * row tiles
+  int row_tiles;        // row tiles per KV head
+  int box;              // rows per TMA box: 32 or 16
+  int min_tiles;        // smallest chunk, in tiles
+  unsigned int *cnt;    // [B * tiles_y] arrival counters
+  float2 *part_ml;      // [B * tiles_y][S][R] (maximum, sum)
+  float4 *part_o;       // [B * tiles_y][S][R][D] fp32
+  long long wait_cycles;
+};
+
+template <int D, int WR, int MT>
+struct PaShape {
+  static constexpr int KG = kPaWarps / WR;
+  static constexpr int R = 16 * WR * MT;
+  // two blocks fit an SM's shared memory with these (64 or 96 KB of tiles each)
+  static constexpr int kStages = WR == 2 ? 4 : MT == 1 ? 3 : 2;
+  static constexpr int kTileBytes = kPaTile * D;            // K or V
+  static constexpr int kRing = KG * kStages * 2 * kTileBytes;
+  static constexpr int kOffQ8 = kRing;                      // hi and lo terms, fragment order
+  static constexpr int kOffQ16 = kOffQ8 + R * D * 2;        // bf16, fragment order
+  static constexpr int kOffRow = kOffQ16 + R * D * 2;       // row factors
+  static constexpr int kOffBar = kOffRow + R * 4;
+  static constexpr int kBytes = kOffBar + KG * kStages * 8 + 1024;  // + slack for 1024-byte alignment
+  static_assert(KG * R * D * 4 + KG * R * 8 <= kOffRow, "the groups' rows are merged in the space of the ring and q");
+  static_assert(2 * (kBytes + 1024 + 64) <= 228 * 1024, "two blocks per SM");
+};
+
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int FMT>
+__device__ __forceinline__ void mma_f8(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+  if (FMT == ET_KV_E4M3)
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e5m2.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+template <bool BF16>
+__device__ __forceinline__ void mma_16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  if (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+// 16-byte chunk c of row r of a merged fp32 row set: rotated so that the four
+// lanes of a quad and two neighbouring rows hit different banks
+template <int D>
+__device__ __forceinline__ int merge_chunk(int r, int c) {
+  return (c & ~7) | ((c + (c >> 3) + (D == 128 ? 4 : 2) * r) & 7);
+}
+
+// Weights of NT n-tiles of scores (16 keys = two n-tiles share a scale): x =
+// score * f + lv relative to the row's reference mr, which moves only when a
+// weight would pass 2^15 (then it becomes the row maximum - 7 and what was
+// summed is rescaled).  keep: bit (8 * n-tile + key) per row, all ones when
+// `masked` is false.  On return p holds the weights as packed pairs.
+template <int NT, int MT, int NTO, bool BF16>
+__device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const float (&rf)[2 * MT],
+                                              const float (&ks)[NT / 2], const float (&lv)[NT / 2],
+                                              const float (&iv)[NT / 2], bool masked, const uint32_t (&keep)[2 * MT],
+                                              float (&mr)[2 * MT], float (&l)[2 * MT], float (&o)[MT][NTO][4],
+                                              uint32_t (&p)[MT][NT][2]) {
+  const int t2 = 2 * (threadIdx.x & 3);
+  float x[MT][NT][4];
+  auto weigh = [&]() {
+    float top = -INFINITY;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int u = 0; u < NT / 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float f = rf[2 * mt + h] * ks[u], c = lv[u] - mr[2 * mt + h];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int nt = 2 * u + (e >> 1), i = 2 * h + (e & 1);
+            float v = fmaf(s[mt][nt][i], f, c);
+            if (masked && !((keep[2 * mt + h] >> (8 * nt + t2 + (e & 1))) & 1u)) v = -INFINITY;
+            x[mt][nt][i] = v;
+            top = fmaxf(top, v);
+          }
+        }
+    return top;
+  };
+  if (__any_sync(0xffffffffu, weigh() > kPaTop + kPaSlack)) {
+    // a weight too large (or the first key of a row): the maxima of the rows, from the scores themselves
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) {
+      const int mt = r >> 1, h = r & 1;
+      float top = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!masked || ((keep[r] >> (8 * nt + t2 + e)) & 1u))
+            top = fmaxf(top, fmaf(s[mt][nt][2 * h + e], rf[r] * ks[nt / 2], lv[nt / 2]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float now = fmaxf(mr[r], top - kPaTop), corr = ex2_fast(mr[r] - now);
+      mr[r] = now;
+      l[r] *= corr;
+#pragma unroll
+      for (int nt = 0; nt < NTO; ++nt) {
+        o[mt][nt][2 * h] *= corr;
+        o[mt][nt][2 * h + 1] *= corr;
+      }
+    }
+    weigh();
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int u = 0; u < NT / 2; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float w0 = ex2_fast(x[mt][2 * u][2 * h]), w1 = ex2_fast(x[mt][2 * u][2 * h + 1]);
+        const float w2 = ex2_fast(x[mt][2 * u + 1][2 * h]), w3 = ex2_fast(x[mt][2 * u + 1][2 * h + 1]);
+        l[2 * mt + h] = fmaf((w0 + w1) + (w2 + w3), iv[u], l[2 * mt + h]);
+        p[mt][2 * u][h] = BF16 ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1);
+        p[mt][2 * u + 1][h] = BF16 ? pack_bf16x2(w2, w3) : pack_f16x2(w2, w3);
+      }
+}
+
+template <int D, int FMT, int WR, int MT>
+__global__ void __launch_bounds__(kPaThreads, 2)
+    k_paged_attn_mma(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ PagedMmaArgs ma) {
+  using Sh = PaShape<D, WR, MT>;
+  constexpr int KG = Sh::KG, R = Sh::R, ST = Sh::kStages, TB = Sh::kTileBytes;
+  constexpr int K8 = D / 32, K16 = D / 16, NTO = D / 8;
+  const PagedAttnArgs &a = ma.a;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ int s_abort, s_last;
+  __shared__ int s_red[kPaWarps];
+  unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t sb = saddr(sm);
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g8 = lane >> 2, tq = lane & 3;
+  const int wr = warp % WR, kg = warp / WR;
+  auto bar = [&](int stage) -> uint32_t { return sb + Sh::kOffBar + 8u * (uint32_t)(kg * ST + stage); };
+
+  // ---- set-up that touches no global memory ----
+  if (t == 0) {
+    s_abort = 0;
+    for (int i = 0; i < KG * ST; ++i) mbar_init(sb + Sh::kOffBar + 8u * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  pdl_wait();     // the previous kernel in the stream has completed
+  pdl_trigger();  // only now may the next kernel launch
+  const int b = blockIdx.z, g = blockIdx.y / ma.row_tiles, rt = blockIdx.y - g * ma.row_tiles, chunk = blockIdx.x;
+  int bad = 0;
+  const int L = paged_prefix(a, b, bad);
+  // chunks are as long in every sequence: the longest sequence's share
+  int longest = L;
+  if (a.B > 1) {
+    int other = 0;
+    if (a.B <= kPaThreads) {
+      int ignore = 0;
+      if (t < a.B) other = paged_prefix(a, t, ignore);
+    } else {
+      other = min((long long)a.max_prefix, (long long)a.max_blocks * a.P);
+    }
+    other = __reduce_max_sync(0xffffffffu, other);
+    if (lane == 0) s_red[warp] = other;
+    __syncthreads();  // (also: the barriers are initialised)
+    longest = max(max(s_red[0], s_red[1]), max(s_red[2], s_red[3]));
+  } else {
+    __syncthreads();
+  }
+  if (L < 0) return;
+  const int T = (L + kPaTile - 1) / kPaTile, Tl = (longest + kPaTile - 1) / kPaTile;
+  const int per = max((Tl + ma.S - 1) / ma.S, ma.min_tiles);
+  const int chunks = max(1, (T + per - 1) / per);
+  if (chunk >= chunks) return;
+  const int t0 = chunk * per, t1 = min(T, t0 + per);
+  const int first = t0 + kg;  // this group's i-th tile: first + KG * i
+  const int n = t1 > first ? (t1 - first + KG - 1) / KG : 0;
+
+  // ---- units of 16 keys, two per tile: lane l holds unit l of a batch of 16 tiles ----
+  int page = -1, slot = 0, page_n = -1, slot_n = 0;
+  float ksc = 0.f, vsc = 1.f, ksc_n = 0.f, vsc_n = 1.f;
+  auto fetch_page = [&](int batch, int &pg, int &sl) {
+    const int i = 16 * batch + (lane >> 1);
+    const long long key = (long long)(first + (long long)KG * i) * kPaTile + 16 * (lane & 1);
+    pg = -1;
+    if (i < n && key < L) {
+      const int blk = (int)key / a.P;
+      sl = (int)key - blk * a.P;
+      pg = a.block_table[(long long)b * a.max_blocks + blk];
+      if (pg < 0 || pg >= a.num_pages) {
+        pg = -1;
+        bad = 1;
+      }
+    }
+  };
+  auto fetch_scale = [&](int pg, float &ks, float &vs) {
+    ks = 0.f;
+    vs = 1.f;
+    if (pg >= 0) {
+      ks = a.k_scale[(long long)pg * a.Hkv + g];
+      vs = clamp_v_scale(a.v_scale[(long long)pg * a.Hkv + g]);
+    }
+  };
+  // the group's i-th tile into its stage (the whole warp wr == 0 calls it); pg, sl: the batch that holds it
+  auto issue = [&](int i, int pg, int sl) {
+    const int u = 2 * (i & 15);
+    const int p0 = __shfl_sync(0xffffffffu, pg, u), p1 = __shfl_sync(0xffffffffu, pg, u + 1);
+    const int s0 = __shfl_sync(0xffffffffu, sl, u), s1 = __shfl_sync(0xffffffffu, sl, u + 1);
+    if (lane != 0) return;
+    const int stage = i % ST;
+    const uint32_t kd = sb + (uint32_t)((kg * ST + stage) * 2 * TB), vd = kd + TB, fb = bar(stage);
+    if (ma.box == kPaTile) {  // both units in one page
+      if (p0 >= 0) {
+        mbar_expect_tx(fb, 2 * TB);
+        tma_4d(kd, &tm_k, 0, s0, g, p0, fb);
+        tma_4d(vd, &tm_v, 0, s0, g, p0, fb);
+      } else {
+        mbar_arrive(fb);
+      }
+    } else {
+      const int boxes = (p0 >= 0 ? 1 : 0) + (p1 >= 0 ? 1 : 0);
+      if (boxes == 0) {
+        mbar_arrive(fb);
+      } else {
+        mbar_expect_tx(fb, (uint32_t)(boxes * TB));
+        if (p0 >= 0) {
+          tma_4d(kd, &tm_k, 0, s0, g, p0, fb);
+          tma_4d(vd, &tm_v, 0, s0, g, p0, fb);
+        }
+        if (p1 >= 0) {
+          tma_4d(kd + TB / 2, &tm_k, 0, s1, g, p1, fb);
+          tma_4d(vd + TB / 2, &tm_v, 0, s1, g, p1, fb);
+        }
+      }
+    }
+  };
+  fetch_page(0, page, slot);
+  if (wr == 0)
+    for (int i = 0; i < n && i < ST; ++i) issue(i, page, slot);
+
+  // ---- q into fragment order: a warp per row, four dims a lane ----
+  float *row_f = reinterpret_cast<float *>(sm + Sh::kOffRow);
+  {
+    constexpr int QR = R / kPaWarps;  // rows per warp
+    uint2 raw[QR];
+#pragma unroll
+    for (int k = 0; k < QR; ++k) {
+      const int r = warp + kPaWarps * k, Rg = rt * R + r, i = Rg / a.G;
+      raw[k] = make_uint2(0u, 0u);
+      if (i < a.N && lane < D / 4)
+        raw[k] = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                  (((long long)b * a.N + i) * a.Hq + g * a.G + (Rg - i * a.G)) * D +
+                                                  4 * lane);
+    }
+    fetch_scale(page, ksc, vsc);  // in flight while q is staged
+#pragma unroll
+    for (int k = 0; k < QR; ++k) {
+      const int r = warp + kPaWarps * k, mt = r >> 4, up = (r >> 3) & 1, lr = r & 7;
+      float x[4] = {__uint_as_float(raw[k].x << 16), __uint_as_float(raw[k].x & 0xffff0000u),
+                    __uint_as_float(raw[k].y << 16), __uint_as_float(raw[k].y & 0xffff0000u)};
+      float amax = 0.f;
+      bool odd = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        amax = fmaxf(amax, fabsf(x[e]));
+        odd |= !(fabsf(x[e]) <= FLT_MAX);
+      }
+      amax = warp_max(amax);
+      odd = __any_sync(0xffffffffu, odd);
+      // up = 2^e with amax * up in (224, 448]: the exponent field of amax decides, 448 = 0.875 * 2^9
+      int ex = 0;
+      const float m = frexpf(odd || amax == 0.f ? 1.f : amax, &ex);
+      const int e2 = 9 - ex - (m > 0.875f ? 1 : 0);
+      const float lift_a = ldexpf(1.f, e2 / 2), lift_b = ldexpf(1.f, e2 - e2 / 2);  // 2^e2 may leave fp32's range
+      uint32_t hi = 0u, lo = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const float y0 = x[e] * lift_a * lift_b, y1 = x[e + 1] * lift_a * lift_b;
+        const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1);
+        const uint32_t hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
+        const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
+        hi |= h2 << (8 * e);
+        lo |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (8 * e);
+      }
+      if (lane < D / 4) {
+        const int d = 4 * lane;
+        // 8-bit fragments: thread (g, t) of a k-step holds dims 32 t + 4 ks (D = 128; register h: + 16), or
+        // 16 t + 8 ks (D = 64; register h: + 4) of rows g and g + 8
+        const int tt = D == 128 ? d / 32 : d / 16, hh = D == 128 ? (d % 32) / 16 : (d % 8) / 4,
+                  ks = D == 128 ? (d % 16) / 4 : (d % 16) / 8;
+        unsigned char *q8 = sm + Sh::kOffQ8 + ((((mt * K8 + ks) * 2) * 32) + 4 * lr + tt) * 16 + (2 * hh + up) * 4;
+        *reinterpret_cast<uint32_t *>(q8) = hi;
+        *reinterpret_cast<uint32_t *>(q8 + 32 * 16) = lo;
+        // bf16 fragments: thread (g, t) of a k-step holds dims (D / 4) t + 4 ks + {0, 1} and + {2, 3}
+        const int t16 = d / (D / 4), k16 = (d % (D / 4)) / 4;
+        unsigned char *q16 = sm + Sh::kOffQ16 + (((mt * K16 + k16) * 32) + 4 * lr + t16) * 16 + up * 4;
+        *reinterpret_cast<uint32_t *>(q16) = raw[k].x;
+        *reinterpret_cast<uint32_t *>(q16 + 8) = raw[k].y;
+      }
+      // what a score of scaled q and codes stands for, in log2 units; a row that is not finite scores NaN
+      if (lane == 0) row_f[r] = odd ? __uint_as_float(0x7fc00000u) : a.scale_log2 / lift_a / lift_b;
+    }
+  }
+  __syncthreads();
+
+  float rf[2 * MT], mr[2 * MT], l[2 * MT];
+  int tok[2 * MT];
+#pragma unroll
+  for (int r = 0; r < 2 * MT; ++r) {
+    const int row = wr * 16 * MT + 16 * (r >> 1) + 8 * (r & 1) + g8;
+    rf[r] = row_f[row];
+    tok[r] = (rt * R + row) / a.G;  // >= N: no such row
+    mr[r] = -3e38f;
+    l[r] = 0.f;
+  }
+  float o[MT][NTO][4];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NTO; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
+
+  // ---- the tree's own rows, 16 keys at a time, while the first tiles arrive ----
+  if (chunk == 0) {
+    const __nv_bfloat16 *KT = static_cast<const __nv_bfloat16 *>(a.kt), *VT = static_cast<const __nv_bfloat16 *>(a.vt);
+    for (int tc = kg; 16 * tc < a.N; tc += KG) {
+      uint32_t keep[2 * MT];
+#pragma unroll
+      for (int r = 0; r < 2 * MT; ++r) {
+        const int i = tok[r];
+        uint32_t w = 0u;
+        if (i < a.N) {
+          if (a.mask) w = (uint32_t)(a.mask[((long long)b * a.N + i) * a.W + (tc >> 2)] >> (16 * (tc & 3))) & 0xffffu;
+          else w = i >= 16 * tc + 15 ? 0xffffu : (i < 16 * tc ? 0u : (2u << (i - 16 * tc)) - 1u);
+        }
+        if (16 * tc + 16 > a.N) w &= (1u << (a.N - 16 * tc)) - 1u;
+        keep[r] = w;
+      }
+      uint32_t kw[2][D / 8];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const int key = 16 * tc + 8 * nt + g8;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (key < a.N)
+            v = *reinterpret_cast<const uint4 *>(KT + (((long long)b * a.N + key) * a.Hkv + g) * D + (D / 4) * tq + 8 * c);
+          kw[nt][4 * c] = v.x; kw[nt][4 * c + 1] = v.y; kw[nt][4 * c + 2] = v.z; kw[nt][4 * c + 3] = v.w;
+        }
+      }
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < K16; ++ks)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint4 q = lds128(sb + Sh::kOffQ16 + (uint32_t)((((wr * MT + mt) * K16 + ks) * 32 + lane) * 16));
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+            mma_16<true>(s[mt][nt], q.x, q.y, q.z, q.w, kw[nt][2 * ks], kw[nt][2 * ks + 1]);
+        }
+      float fs[2 * MT];
+#pragma unroll
+      for (int r = 0; r < 2 * MT; ++r) fs[r] = a.scale_log2;
+      const float one[1] = {1.f}, zero[1] = {0.f};
+      uint32_t p[MT][2][2];
+      paged_softmax<2, MT, NTO, true>(s, fs, one, zero, one, true, keep, mr, l, o, p);
+      bool odd = false;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {  // 8 of the thread's dims at a time
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = 16 * tc + 2 * tq + (k & 1) + 8 * (k >> 1);
+          v[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (key < a.N)
+            v[k] = *reinterpret_cast<const uint4 *>(VT + (((long long)b * a.N + key) * a.Hkv + g) * D + (D / 8) * g8 + 8 * c);
+        }
+        uint32_t w[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
+                            {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
+        // NaN and infinities would reach rows that do not attend their key (0 * inf): they are added by hand below
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((w[k][e] & 0x7f80u) == 0x7f80u) { w[k][e] &= 0xffff0000u; odd = true; }
+            if ((w[k][e] & 0x7f800000u) == 0x7f800000u) { w[k][e] &= 0xffffu; odd = true; }
+          }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+          const uint32_t b0 = __byte_perm(w[0][e >> 1], w[1][e >> 1], sel), b1 = __byte_perm(w[2][e >> 1], w[3][e >> 1], sel);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            mma_16<true>(o[mt][8 * c + e], p[mt][0][0], p[mt][0][1], p[mt][1][0], p[mt][1][1], b0, b1);
+        }
+      }
+      if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+        for (int k = 0; k < 16 && 16 * tc + k < a.N; ++k) {
+          const __nv_bfloat16 *vr = VT + (((long long)b * a.N + 16 * tc + k) * a.Hkv + g) * D + (D / 4) * tq;
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int nt = 0; nt < NTO; ++nt) {
+              const float x = __bfloat162float(vr[(D / 8) * half + nt]);
+              if (fabsf(x) <= FLT_MAX) continue;
+#pragma unroll
+              for (int r = 0; r < 2 * MT; ++r)
+                if ((keep[r] >> k) & 1u) o[r >> 1][nt][2 * (r & 1) + half] += x;
+            }
+        }
+      }
+    }
+  }
+
+  // ---- the cached keys ----
+  bool dead = false;  // a wait gave up: go on without waiting, computing or fetching, in step with the partner warp
+  int issued = n < ST ? n : ST;
+  for (int i = 0; i < n; ++i) {
+    if ((i & 15) == 0) {
+      if (i > 0) {
+        page = page_n; slot = slot_n; ksc = ksc_n; vsc = vsc_n;
+      }
+      fetch_page((i >> 4) + 1, page_n, slot_n);
+    } else if ((i & 15) == 1) {
+      fetch_scale(page_n, ksc_n, vsc_n);
+    }
+    const int stage = i % ST;
+    if (!dead && !mbar_try(bar(stage), (uint32_t)(i / ST) & 1u))
+      dead = !mbar_wait(bar(stage), (uint32_t)(i / ST) & 1u, &s_abort, ma.wait_cycles);
+    dead = __any_sync(0xffffffffu, dead);
+    if (!dead) {
+      const int u = 2 * (i & 15), key0 = (first + KG * i) * kPaTile;
+      float ks[2], vs[2], lv[2], iv[2];
+      bool there[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ks[h] = __shfl_sync(0xffffffffu, ksc, u + h);
+        vs[h] = __shfl_sync(0xffffffffu, vsc, u + h);
+        there[h] = __shfl_sync(0xffffffffu, page, u + h) >= 0;
+        lv[h] = __log2f(vs[h]);
+        iv[h] = __frcp_rn(vs[h]);
+      }
+      const bool whole = there[0] && there[1] && L - key0 >= kPaTile;
+      uint32_t valid = 0xffffffffu;  // bit k: key key0 + k is there
+      if (!whole) {
+        valid = L - key0 >= kPaTile ? 0xffffffffu : (1u << (L - key0)) - 1u;
+        if (!there[0]) valid &= 0xffff0000u;
+        if (!there[1]) valid &= 0x0000ffffu;
+      }
+      const uint32_t kb = sb + (uint32_t)((kg * ST + stage) * 2 * TB), vb = kb + TB;
+      // S = q K^T: a thread's 32 (16) bytes of a key row are two words a k-step
+      float s[MT][4][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+      uint4 kw[4][D / 64];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const uint32_t row = kb + (uint32_t)((8 * nt + g8) * D);
+        if (D == 128) {
+          kw[nt][0] = lds128(row + (uint32_t)(((2 * tq) ^ g8) << 4));
+          kw[nt][D / 64 - 1] = lds128(row + (uint32_t)(((2 * tq + 1) ^ g8) << 4));
+        } else {
+          kw[nt][0] = lds128(row + (uint32_t)((tq ^ ((g8 >> 1) & 3)) << 4));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < K8; ++k) {
+        uint32_t b0[4], b1[4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          const uint4 x = kw[nt][0], y = kw[nt][D / 64 - 1];
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+          b0[nt] = D == 128 ? xw[k & 3] : xw[(2 * k) & 3];
+          b1[nt] = D == 128 ? yw[k & 3] : xw[(2 * k + 1) & 3];
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+            const uint4 q = lds128(sb + Sh::kOffQ8 + (uint32_t)(((((wr * MT + mt) * K8 + k) * 2 + term) * 32 + lane) * 16));
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) mma_f8<FMT>(s[mt][nt], q, b0[nt], b1[nt]);
+          }
+      }
+      uint32_t keep[2 * MT];
+#pragma unroll
+      for (int r = 0; r < 2 * MT; ++r) keep[r] = valid;
+      uint32_t p[MT][4][2];
+      if (whole) paged_softmax<4, MT, NTO, false>(s, rf, ks, lv, iv, false, keep, mr, l, o, p);
+      else paged_softmax<4, MT, NTO, false>(s, rf, ks, lv, iv, true, keep, mr, l, o, p);
+      // O += P V: the bytes of two keys at one dim become a pair of fp16
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t w[4][D / 32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = 16 * j + 2 * tq + (k & 1) + 8 * (k >> 1);
+          const uint32_t row = vb + (uint32_t)(key * D);
+          if (D == 128) {
+            const uint4 v = lds128(row + (uint32_t)((g8 ^ (key & 7)) << 4));
+            w[k][0] = v.x; w[k][1] = v.y; w[k][D / 32 - 2] = v.z; w[k][D / 32 - 1] = v.w;
+          } else {
+            const uint2 v = lds64(row + (uint32_t)((((g8 >> 1) ^ ((key >> 1) & 3)) << 4) + 8 * (g8 & 1)));
+            w[k][0] = v.x; w[k][1] = v.y;
+          }
+          if (!whole && !((valid >> key) & 1u)) {  // whatever the page holds there must not meet a zero weight
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) w[k][c] = 0u;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t b0[4], b1[4];
+          f8x4_to_f16<FMT>(__byte_perm(w[0][c], w[1][c], 0x5140), b0[0], b0[1]);
+          f8x4_to_f16<FMT>(__byte_perm(w[0][c], w[1][c], 0x7362), b0[2], b0[3]);
+          f8x4_to_f16<FMT>(__byte_perm(w[2][c], w[3][c], 0x5140), b1[0], b1[1]);
+          f8x4_to_f16<FMT>(__byte_perm(w[2][c], w[3][c], 0x7362), b1[2], b1[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              mma_16<false>(o[mt][4 * c + e], p[mt][2 * j][0], p[mt][2 * j][1], p[mt][2 * j + 1][0],
+                            p[mt][2 * j + 1][1], b0[e], b1[e]);
+        }
+      }
+    }
+    // the stage is free once both warps of the group have read it
+    if (WR == 2) asm volatile("bar.sync %0, 64;" ::"r"(1 + kg) : "memory");
+    else __syncwarp();
+    if (wr == 0 && !dead && i + ST < n) {
+      const bool later = ((i + ST) >> 4) != (i >> 4);
+      issue(i + ST, later ? page_n : page, later ? slot_n : slot);
+      issued = i + ST + 1;
+    }
+  }
+  if (dead && wr == 0 && lane == 0)  // copies still in flight land before the block reuses or leaves its memory
+    for (int i = issued > ST ? issued - ST : 0; i < issued; ++i) mbar_drain(bar(i % ST), (uint32_t)(i / ST) & 1u);
+  if (bad) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
+  __syncthreads();
+  const bool aborted = *(volatile int *)&s_abort != 0;
+  if (aborted && t == 0) flag_status(a.dev_status, ET_DEV_TIMEOUT);
+
+  // ---- the groups' rows, merged through shared memory ----
+  float4 *rows = reinterpret_cast<float4 *>(sm);                       // [KG][R][D / 4]
+  float2 *ml = reinterpret_cast<float2 *>(sm + KG * R * D * 4);        // [KG][R]
+#pragma unroll
+  for (int r = 0; r < 2 * MT; ++r) {
+    const int mt = r >> 1, h = r & 1, row = wr * 16 * MT + 16 * mt + 8 * h + g8;
+    float sum = l[r];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (tq == 0) ml[kg * R + row] = make_float2(mr[r], sum);
+#pragma unroll
+    for (int half = 0; half < 2; ++half)  // column 2 tq + half of n-tile nt is dim (D / 8) (2 tq + half) + nt
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+        rows[(kg * R + row) * (D / 4) + merge_chunk<D>(row, (D / 16) * tq + (D / 32) * half + c)] =
+            make_float4(o[mt][4 * c][2 * h + half], o[mt][4 * c + 1][2 * h + half], o[mt][4 * c + 2][2 * h + half],
+                        o[mt][4 * c + 3][2 * h + half]);
+  }
+  __syncthreads();
+  const int real = min(R, a.N * a.G - rt * R);  // rows that exist are a prefix of the tile
+  const long long tile_id = (long long)b * ma.tiles_y + blockIdx.y;
+  auto write_row = [&](int r, int c, const float4 &v, float M, float sum) {
+    const int Rg = rt * R + r, i = Rg / a.G, h = g * a.G + (Rg - i * a.G);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint2 w;
+    w.x = pack_bf16x2(v.x * inv, v.y * inv);
+    w.y = pack_bf16x2(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + (((long long)b * a.N + i) * a.Hq + h) * D + 4 * c) = w;
+    if (c == 0 && a.lse)
+      a.lse[((long long)b * a.Hq + h) * a.N + i] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+  };
+  for (int x = t; x < real * (D / 4); x += kPaThreads) {
+    const int r = x / (D / 4), c = x - r * (D / 4);
+    float M = ml[r].x;
+#pragma unroll
+    for (int k = 1; k < KG; ++k) M = fmaxf(M, ml[k * R + r].x);
+    float sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < KG; ++k) {
+      const float2 e = ml[k * R + r];
+      const float w = ex2_fast(e.x - M);
+      const float4 y = rows[(k * R + r) * (D / 4) + merge_chunk<D>(r, c)];
+      sum = fmaf(e.y, w, sum);
+      v.x = fmaf(y.x, w, v.x); v.y = fmaf(y.y, w, v.y); v.z = fmaf(y.z, w, v.z); v.w = fmaf(y.w, w, v.w);
+    }
+    if (chunks == 1) {
+      write_row(r, c, v, M, sum);
+    } else {
+      const long long at = (tile_id * ma.S + chunk) * R + r;
+      ma.part_o[at * (D / 4) + c] = v;
+      if (c == 0) ma.part_ml[at] = make_float2(M, sum);
+    }
+  }
+  if (chunks == 1) return;
+  // ---- the chunks' rows, merged by the last block to arrive ----
+  if (!arrive_last(ma.cnt + tile_id, (unsigned)chunks, &s_last)) return;
+  for (int x = t; x < real * (D / 4); x += kPaThreads) {
+    const int r = x / (D / 4), c = x - r * (D / 4);
+    const long long at = tile_id * ma.S * R + r;
+    float M = -INFINITY;
+    for (int k = 0; k < chunks; ++k) M = fmaxf(M, __ldcg(&ma.part_ml[at + (long long)k * R].x));
+    float sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < chunks; ++k) {
+      const float2 e = __ldcg(&ma.part_ml[at + (long long)k * R]);
+      const float4 y = __ldcg(&ma.part_o[(at + (long long)k * R) * (D / 4) + c]);
+      const float w = ex2_fast(e.x - M);
+      sum = fmaf(e.y, w, sum);
+      v.x = fmaf(y.x, w, v.x); v.y = fmaf(y.y, w, v.y); v.z = fmaf(y.z, w, v.z); v.w = fmaf(y.w, w, v.w);
+    }
+    write_row(r, c, v, M, sum);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+// pages as [num_pages][Hkv][P][d] bytes; a box is `box` rows of one head of one page
+bool make_page_map(CUtensorMap *m, const void *base, const et_paged_cache *c, int box) {
+  const cuuint64_t dims[4] = {(cuuint64_t)c->d, (cuuint64_t)c->page_size, (cuuint64_t)c->Hkv, (cuuint64_t)c->num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c->d, (cuuint64_t)c->d * c->page_size, (cuuint64_t)c->page_stride};
+  const cuuint32_t boxes[4] = {(cuuint32_t)c->d, (cuuint32_t)box, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, boxes, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int FMT, int WR, int MT>
+et_status launch_mma(const CUtensorMap &mk, const CUtensorMap &mv, const PagedMmaArgs &ma, cudaStream_t st) {
+  using Sh = PaShape<D, WR, MT>;
+  if (et_smem_attr((const void *)k_paged_attn_mma<D, FMT, WR, MT>, Sh::kBytes) != cudaSuccess) return ET_ERR_CUDA;
+  return et_launch(k_paged_attn_mma<D, FMT, WR, MT>, dim3(ma.S, ma.tiles_y, ma.a.B), dim3(kPaThreads), Sh::kBytes, st,
+                   0, mk, mv, ma);
+}
+template <int D, int FMT>
+et_status launch_mma_rows(int R, const CUtensorMap &mk, const CUtensorMap &mv, const PagedMmaArgs &ma, cudaStream_t st) {
+  if (R == 16) return launch_mma<D, FMT, 1, 1>(mk, mv, ma, st);
+  if (R == 32) return launch_mma<D, FMT, 1, 2>(mk, mv, ma, st);
+  return launch_mma<D, FMT, 2, 2>(mk, mv, ma, st);
 }
 
 struct PagedPlan {
   int S;      // blocks a sequence's keys are split over
-  size_t ws;  // workspace bytes
+  int R;      // query rows per block
+  int row_tiles;
+  size_t ws;  // workspace bytes: counters, (maximum, sum) pairs, partial rows
+  size_t ml_off, o_off;
 };
+
+constexpr int kPaMinTiles = 2;  // tiles of a chunk at least
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    n = 152;
+  cudaGetLastError();
+  return n;
+}
 
 et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, PagedPlan *p) {
   if (!s) return ET_ERR_INVALID_ARG;
@@ -208,7 +920,36 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
     return ET_ERR_INVALID_ARG;
   if (s->B > 65535 || s->Hq > 65535 || (long long)s->max_blocks * c->page_size >= (1ll << 31)) return ET_ERR_UNSUPPORTED;
   p->S = 1;
-  p->ws = 0;
+  p->ws = p->ml_off = p->o_off = 0;
+  p->R = p->row_tiles = 1;
+  if (s->dtype == ET_F32) return ET_OK;
+  const long long rows = (long long)s->N * (s->Hq / c->Hkv);
+  p->R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  p->row_tiles = (int)((rows + p->R - 1) / p->R);
+  const long long tiles = (long long)s->B * c->Hkv * p->row_tiles;
+  if ((long long)c->Hkv * p->row_tiles > 65535) return ET_ERR_UNSUPPORTED;
+  const long long room = (long long)s->max_blocks * c->page_size;
+  const int T = (int)(((s->max_prefix < room ? s->max_prefix : room) + kPaTile - 1) / kPaTile);
+  int S = s->num_splits;
+  if (S <= 0) {
+    // two blocks fit an SM: one wave for one sequence, four when the lengths may differ
+    const long long want = (s->B > 1 ? 4ll : 1ll) * 2 * sm_count();
+    S = (int)(want / tiles);
+    const int by_tiles = T / (2 * kPaMinTiles);
+    if (S > by_tiles) S = by_tiles;
+    if (S > 64) S = 64;
+  }
+  if (S > T) S = T;
+  if (S > 256) S = 256;
+  if (S < 1) S = 1;
+  p->S = S;
+  if (S > 1) {
+    const size_t cnt = ((size_t)tiles * sizeof(unsigned int) + 255) & ~(size_t)255;
+    const size_t ml = ((size_t)tiles * S * p->R * sizeof(float2) + 255) & ~(size_t)255;
+    p->ml_off = cnt;
+    p->o_off = cnt + ml;
+    p->ws = cnt + ml + (size_t)tiles * S * p->R * c->d * sizeof(float);
+  }
   return ET_OK;
 }
 
@@ -256,7 +997,26 @@ extern "C" et_status et_tree_attention_paged(const et_paged_attn_shape *shape, c
   cudaStream_t st = (cudaStream_t)stream;
   const bool e4m3 = cache->format == ET_KV_E4M3;
   if (shape->dtype == ET_F32)
-    return e4m3 ? launch_row<float, ET_KV_E4M3>(a, cache->d, st) : launch_row<float, ET_KV_E5M2>(a, cache->d, st);
-  return e4m3 ? launch_row<__nv_bfloat16, ET_KV_E4M3>(a, cache->d, st)
-              : launch_row<__nv_bfloat16, ET_KV_E5M2>(a, cache->d, st);
+    return e4m3 ? launch_row<ET_KV_E4M3>(a, cache->d, st) : launch_row<ET_KV_E5M2>(a, cache->d, st);
+  if (!encode_fn()) return ET_ERR_CUDA;
+  PagedMmaArgs ma;
+  ma.a = a;
+  ma.S = plan.S;
+  ma.row_tiles = plan.row_tiles;
+  ma.tiles_y = cache->Hkv * plan.row_tiles;
+  ma.box = cache->page_size % kPaTile == 0 ? kPaTile : 16;
+  ma.min_tiles = shape->num_splits > 0 ? 1 : kPaMinTiles;
+  unsigned char *wsb = static_cast<unsigned char *>(ws);
+  ma.cnt = plan.S > 1 ? reinterpret_cast<unsigned int *>(wsb) : nullptr;
+  ma.part_ml = plan.S > 1 ? reinterpret_cast<float2 *>(wsb + plan.ml_off) : nullptr;
+  ma.part_o = plan.S > 1 ? reinterpret_cast<float4 *>(wsb + plan.o_off) : nullptr;
+  ma.wait_cycles = et_wait_limit_cycles();
+  CUtensorMap mk, mv;
+  if (!make_page_map(&mk, cache->k_pages, cache, ma.box) || !make_page_map(&mv, cache->v_pages, cache, ma.box))
+    return ET_ERR_INVALID_ARG;
+  if (cache->d == 64)
+    return e4m3 ? launch_mma_rows<64, ET_KV_E4M3>(plan.R, mk, mv, ma, st)
+                : launch_mma_rows<64, ET_KV_E5M2>(plan.R, mk, mv, ma, st);
+  return e4m3 ? launch_mma_rows<128, ET_KV_E4M3>(plan.R, mk, mv, ma, st)
+              : launch_mma_rows<128, ET_KV_E5M2>(plan.R, mk, mv, ma, st);
 }

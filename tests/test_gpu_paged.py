@@ -96,10 +96,12 @@ def check_attention(got, glse, ref, d, dtype, L):
 
     A score is a sum of d products in fp32 and a few more roundings: (d + 8) 2^-24 of sum |q||k| * scale, and its
     image in 2^x of a few 2^-22 (the hardware base-2 exponential); both sums of weights run in fp32 over L + N terms
-    of one sign each (2^-24 a term at the worst; the partial sums of a block tree lose less).  bf16: weights that
-    meet cached values are rounded to fp16 (2^-11), those that meet tree rows to bf16 (2^-8), out to bf16 (2^-8)."""
-    out, lse, abs_c, abs_t, reach = ref
-    eps = (d + 8) * 2.0 ** -24 * reach + 2.0 ** -19
+    of one sign each (2^-24 a term at the worst; the partial sums of a block tree lose less).  bf16: q meets cached codes
+    as two e4m3 terms of at most 448, the second with steps of 2^-9 (half a step off) where the first is below 2^-2:
+    2^-10 / 224 of the row's largest element; weights that meet cached values are rounded to fp16 (2^-11), those that
+    meet tree rows to bf16 (2^-8), out to bf16 (2^-8)."""
+    out, lse, abs_c, abs_t, reach, flat = ref
+    eps = (d + 8) * 2.0 ** -24 * reach + 2.0 ** -19 + (2.0 ** -10 / 224 * flat if dtype == "bf16" else 0)
     weight = (2 * eps).T[:, :, None] + min((L + 128) * 2.0 ** -24, 2.0 ** -16)
     if dtype == "bf16":
         tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -11 + weight) * abs_c + (2.0 ** -8 + weight) * abs_t
@@ -262,6 +264,28 @@ def test_nan_in_a_cached_value_reaches_its_rows_alone():
     want = torch.zeros_like(nan)
     want[0, :, 2:4, 5] = True
     assert torch.equal(nan, want) and not torch.isnan(r["lse"]).any()
+
+
+def test_nan_in_a_tree_row_reaches_its_descendants_alone():
+    rng = np.random.default_rng(16)
+    N = 40
+    pool = Pool(rng, [40], 16, 2, 64, "e4m3")
+    keep = random_tree(rng, 1, N)
+    r = run_attention(pool, 1, N, 4, "bf16", rng, keep)
+    clean = r["out"].clone()
+    kt, vt = r["args"][5], r["args"][6]
+    kt[0, 33, 0, 7] = float("nan")            # head 0 of the group pair: scores of row 33 and below it
+    vt[0, 21, 1, 3] = float("inf")            # head 1, dim 3
+    vt[0, 5, 1, 60] = float("nan")
+    E.et_tree_attention_paged(*r["args"], lse=r["lse"], ws=r["ws"], dev_status=r["status"])
+    torch.cuda.synchronize()
+    want = clean.clone()
+    sees = torch.from_numpy(keep[0]).cuda()
+    want[0, sees[:, 33], 0:2] = float("nan")
+    want[0, sees[:, 21], 2:4, 3] = float("inf")
+    want[0, sees[:, 5], 2:4, 60] = float("nan")
+    assert torch.equal(torch.isnan(want), torch.isnan(r["out"]))
+    assert torch.equal(torch.nan_to_num(want, nan=0.0), torch.nan_to_num(r["out"], nan=0.0))
 
 
 @pytest.mark.parametrize("N", [1, 61])

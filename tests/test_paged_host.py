@@ -88,7 +88,7 @@ def test_paged_attention_matches_the_dense_oracle():
     kc = O.dequantised(codes, scale, "e4m3", np.array([2, 0]), L)
     q, kt, vt = rng.standard_normal((N, Hq, d)), rng.standard_normal((N, Hkv, d)), rng.standard_normal((N, Hkv, d))
     keep = np.tril(np.ones((N, N), bool))
-    out, lse, abs_c, abs_t, _ = O.paged_attention(q, kc, kc, kt, vt, np.ones(L, bool), keep, d ** -0.5)
+    out, lse, abs_c, abs_t, _, _ = O.paged_attention(q, kc, kc, kt, vt, np.ones(L, bool), keep, d ** -0.5)
     mask = np.array([[[sum(1 << j for j in range(i + 1))] for i in range(N)]], np.uint64)
     ref, rlse = O.tree_attention(q[None], [kc], [kc], kt[None], vt[None], mask, d ** -0.5)
     np.testing.assert_allclose(out, ref[0], rtol=1e-12, atol=1e-12)
