@@ -479,67 +479,70 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   if (wr == 0)
     for (int i = 0; i < n && i < ST; ++i) issue(i, page, slot);
 
-  // ---- q into fragment order: a warp per row, four dims a lane ----
+  // ---- q into fragment order: D / 8 lanes per row, eight dims a lane ----
   float *row_f = reinterpret_cast<float *>(sm + Sh::kOffRow);
   {
-    constexpr int QR = R / kPaWarps;  // rows per warp
-    uint2 raw[QR];
+    constexpr int LR = D / 8, RW = 32 / LR;       // lanes per row, rows a warp takes at once
+    constexpr int QR = R / (kPaWarps * RW);       // rounds
+    const int lr = lane % LR, sub = lane / LR;
+    uint4 raw[QR];
 #pragma unroll
     for (int k = 0; k < QR; ++k) {
-      const int r = warp + kPaWarps * k, Rg = rt * R + r, i = Rg / a.G;
-      raw[k] = make_uint2(0u, 0u);
-      if (i < a.N && lane < D / 4)
-        raw[k] = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+      const int r = (warp + kPaWarps * k) * RW + sub, Rg = rt * R + r, i = Rg / a.G;
+      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < a.N)
+        raw[k] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
                                                   (((long long)b * a.N + i) * a.Hq + g * a.G + (Rg - i * a.G)) * D +
-                                                  4 * lane);
+                                                  8 * lr);
     }
     fetch_scale(page, ksc, vsc);  // in flight while q is staged
 #pragma unroll
     for (int k = 0; k < QR; ++k) {
-      const int r = warp + kPaWarps * k, mt = r >> 4, up = (r >> 3) & 1, lr = r & 7;
-      float x[4] = {__uint_as_float(raw[k].x << 16), __uint_as_float(raw[k].x & 0xffff0000u),
-                    __uint_as_float(raw[k].y << 16), __uint_as_float(raw[k].y & 0xffff0000u)};
-      float amax = 0.f;
-      bool odd = false;
+      const int r = (warp + kPaWarps * k) * RW + sub, mt = r >> 4, up = (r >> 3) & 1, r8 = r & 7;
+      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+      uint32_t top = 0u;  // the row's largest magnitude, as the bits of a bf16 value: they order like the values
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        amax = fmaxf(amax, fabsf(x[e]));
-        odd |= !(fabsf(x[e]) <= FLT_MAX);
-      }
-      amax = warp_max(amax);
-      odd = __any_sync(0xffffffffu, odd);
-      // up = 2^e with amax * up in (224, 448]: the exponent field of amax decides, 448 = 0.875 * 2^9
-      int ex = 0;
-      const float m = frexpf(odd || amax == 0.f ? 1.f : amax, &ex);
-      const int e2 = 9 - ex - (m > 0.875f ? 1 : 0);
-      const float lift_a = ldexpf(1.f, e2 / 2), lift_b = ldexpf(1.f, e2 - e2 / 2);  // 2^e2 may leave fp32's range
-      uint32_t hi = 0u, lo = 0u;
+      for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const float y0 = x[e] * lift_a * lift_b, y1 = x[e + 1] * lift_a * lift_b;
-        const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1);
-        const uint32_t hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
-        const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
-        hi |= h2 << (8 * e);
-        lo |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (8 * e);
-      }
-      if (lane < D / 4) {
-        const int d = 4 * lane;
+      for (int x = 1; x < LR; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const bool odd = top >= 0x7f80u;  // NaN or infinity
+      // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8; e2 may leave fp32's exponents, half of it cannot
+      const int ex = max((int)(top >> 7), 1), e2 = top == 0u || odd ? 0 : 135 - ex - ((top & 0x7fu) > 0x60u ? 1 : 0);
+      const int ea = e2 >> 1, eb = e2 - ea;
+      const float lift_a = __uint_as_float((uint32_t)(127 + ea) << 23), lift_b = __uint_as_float((uint32_t)(127 + eb) << 23);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t hi = 0u, lo = 0u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t v = w[2 * half + e];
+          const float y0 = __uint_as_float(v << 16) * lift_a * lift_b, y1 = __uint_as_float(v & 0xffff0000u) * lift_a * lift_b;
+          const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1);
+          const uint32_t hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
+          const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
+          hi |= h2 << (16 * e);
+          lo |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (16 * e);
+        }
+        const int d = 8 * lr + 4 * half;
         // 8-bit fragments: thread (g, t) of a k-step holds dims 32 t + 4 ks (D = 128; register h: + 16), or
         // 16 t + 8 ks (D = 64; register h: + 4) of rows g and g + 8
         const int tt = D == 128 ? d / 32 : d / 16, hh = D == 128 ? (d % 32) / 16 : (d % 8) / 4,
                   ks = D == 128 ? (d % 16) / 4 : (d % 16) / 8;
-        unsigned char *q8 = sm + Sh::kOffQ8 + ((((mt * K8 + ks) * 2) * 32) + 4 * lr + tt) * 16 + (2 * hh + up) * 4;
+        unsigned char *q8 = sm + Sh::kOffQ8 + ((((mt * K8 + ks) * 2) * 32) + 4 * r8 + tt) * 16 + (2 * hh + up) * 4;
         *reinterpret_cast<uint32_t *>(q8) = hi;
         *reinterpret_cast<uint32_t *>(q8 + 32 * 16) = lo;
-        // bf16 fragments: thread (g, t) of a k-step holds dims (D / 4) t + 4 ks + {0, 1} and + {2, 3}
-        const int t16 = d / (D / 4), k16 = (d % (D / 4)) / 4;
-        unsigned char *q16 = sm + Sh::kOffQ16 + (((mt * K16 + k16) * 32) + 4 * lr + t16) * 16 + up * 4;
-        *reinterpret_cast<uint32_t *>(q16) = raw[k].x;
-        *reinterpret_cast<uint32_t *>(q16 + 8) = raw[k].y;
+        if (chunk == 0) {  // the block that attends the tree
+          // bf16 fragments: thread (g, t) of a k-step holds dims (D / 4) t + 4 ks + {0, 1} and + {2, 3}
+          const int t16 = d / (D / 4), k16 = (d % (D / 4)) / 4;
+          unsigned char *q16 = sm + Sh::kOffQ16 + (((mt * K16 + k16) * 32) + 4 * r8 + t16) * 16 + up * 4;
+          *reinterpret_cast<uint32_t *>(q16) = w[2 * half];
+          *reinterpret_cast<uint32_t *>(q16 + 8) = w[2 * half + 1];
+        }
       }
-      // what a score of scaled q and codes stands for, in log2 units; a row that is not finite scores NaN
-      if (lane == 0) row_f[r] = odd ? __uint_as_float(0x7fc00000u) : a.scale_log2 / lift_a / lift_b;
+      // what a score of lifted q and codes stands for, in log2 units; a row that is not finite scores NaN
+      if (lr == 0)
+        row_f[r] = odd ? __uint_as_float(0x7fc00000u)
+                       : a.scale_log2 * __uint_as_float((uint32_t)(127 - ea) << 23) * __uint_as_float((uint32_t)(127 - eb) << 23);
     }
   }
   __syncthreads();
