@@ -734,9 +734,9 @@ et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_
  * max_blocks pages is cut there, a page id outside the cache drops its
  * tokens; both set ET_DEV_BAD_INDEX.
  * Scores, softmax statistics and outputs accumulate in fp32.  bf16 inputs:
- * cached codes meet q as it is (two 8-bit terms per element; only what lies
- * 2^-18 below the largest of its row is lost), weights are rounded to fp16
- * (cached tokens) or bf16 (tree rows) before they meet V.  A q row that holds
+ * cached codes meet q as it is (only what lies 2^-38 below the largest of its
+ * row is lost), weights are rounded to fp16 (cached tokens) or bf16 (tree
+ * rows) before they meet V.  A q row that holds
  * a NaN or an infinity gives NaN.  fp32 inputs: fp32 throughout.
  * bf16 inputs: a bounded wait that expires sets ET_DEV_TIMEOUT and leaves that
  * block's rows undefined.  Calls that can run at the same time need separate

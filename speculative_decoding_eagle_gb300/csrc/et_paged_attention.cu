@@ -191,16 +191,13 @@ et_status launch_row(const PagedAttnArgs &a, int d, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // bf16: tensor cores (mma.sync), cached codes as operands
 // ---------------------------------------------------------------------------
-// The scores of cached keys are 8-bit products: K's codes are the B operand
-// as they lie in the page (no conversion), q scaled by a power of two per row
-// and split into two e4m3 terms, q = hi + lo, each four significant bits of a
-// bf16 value's eight, is the A operand of two m16n8k32 products into one fp32
-// sum.  (Exact for elements above 2^-11 of their row's largest, within 2^-18
-// of it below; the sums keep fp32 precision, checked against exact sums.)
-// P.V runs as fp16 m16n8k16 products: codes become fp16 exactly, weights are
-// kept at most 2^15 and lose only what lies 2^-31 below the largest.
-// Measured on this part: 8-bit m16n8k32 2241 TFLOP/s, fp16 m16n8k16 600, so
-// two 8-bit products cost half of one fp16 product and save K's conversion.
+// Codes become fp16 exactly, so both products are fp16 m16n8k16 into fp32
+// sums.  q is lifted by a power of two per row to [2^14, 2^15) before it is
+// rounded to fp16: nothing above 2^-38 of its row's largest element is lost.
+// Weights stay below 2^15 and lose only what lies 2^-31 below the largest.
+// (8-bit mma.sync is no way out here: on this part it runs as two fp16
+// products and conversions; 479 TFLOP/s against 573 for fp16 in a loop with
+// changing operands.)
 //
 // A block of four warps owns R = 16 * WR * MT query rows (token, head in
 // group) of one KV head and a chunk of the prefix.  WR warps share the rows,
@@ -212,6 +209,7 @@ et_status launch_row(const PagedAttnArgs &a, int d, cudaStream_t st) {
 constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
 constexpr int kPaTile = 32;  // keys per tile
+constexpr int kPaMaxSplits = 64;
 constexpr float kPaTop = 7.f, kPaSlack = 8.f;  // weights lie below 2^kPaTop when the maximum moves, below 2^15 always
 
 struct PagedMmaArgs {
@@ -234,12 +232,13 @@ struct PaShape {
   static constexpr int kStages = WR == 2 ? 4 : MT == 1 ? 3 : 2;
   static constexpr int kTileBytes = kPaTile * D;            // K or V
   static constexpr int kRing = KG * kStages * 2 * kTileBytes;
-  static constexpr int kOffQ8 = kRing;                      // hi and lo terms, fragment order
-  static constexpr int kOffQ16 = kOffQ8 + R * D * 2;        // bf16, fragment order
+  static constexpr int kOffQ = kRing;                       // lifted fp16, fragment order
+  static constexpr int kOffQ16 = kOffQ + R * D * 2;         // bf16, fragment order
   static constexpr int kOffRow = kOffQ16 + R * D * 2;       // row factors
   static constexpr int kOffBar = kOffRow + R * 4;
   static constexpr int kBytes = kOffBar + KG * kStages * 8 + 1024;  // + slack for 1024-byte alignment
   static_assert(KG * R * D * 4 + KG * R * 8 <= kOffRow, "the groups' rows are merged in the space of the ring and q");
+  static_assert((kPaMaxSplits + 1) * R * 8 <= kOffRow, "the chunks' pairs, too");
   static_assert(2 * (kBytes + 1024 + 64) <= 228 * 1024, "two blocks per SM");
 };
 
@@ -247,17 +246,6 @@ __device__ __forceinline__ float ex2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-template <int FMT>
-__device__ __forceinline__ void mma_f8(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
-  if (FMT == ET_KV_E4M3)
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e5m2.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 template <bool BF16>
 __device__ __forceinline__ void mma_16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -367,7 +355,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
                      const __grid_constant__ PagedMmaArgs ma) {
   using Sh = PaShape<D, WR, MT>;
   constexpr int KG = Sh::KG, R = Sh::R, ST = Sh::kStages, TB = Sh::kTileBytes;
-  constexpr int K8 = D / 32, K16 = D / 16, NTO = D / 8;
+  constexpr int K16 = D / 16, NTO = D / 8;
   const PagedAttnArgs &a = ma.a;
   extern __shared__ unsigned char smem_raw[];
   __shared__ int s_abort, s_last;
@@ -506,37 +494,21 @@ __global__ void __launch_bounds__(kPaThreads, 2)
 #pragma unroll
       for (int x = 1; x < LR; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
       const bool odd = top >= 0x7f80u;  // NaN or infinity
-      // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8; e2 may leave fp32's exponents, half of it cannot
-      const int ex = max((int)(top >> 7), 1), e2 = top == 0u || odd ? 0 : 135 - ex - ((top & 0x7fu) > 0x60u ? 1 : 0);
+      // 2^e2 lifts the largest magnitude into [2^14, 2^15); e2 may leave fp32's exponents, half of it cannot
+      const int e2 = top == 0u || odd ? 0 : 141 - max((int)(top >> 7), 1);
       const int ea = e2 >> 1, eb = e2 - ea;
       const float lift_a = __uint_as_float((uint32_t)(127 + ea) << 23), lift_b = __uint_as_float((uint32_t)(127 + eb) << 23);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        uint32_t hi = 0u, lo = 0u;
+        // thread (g, t) of a k-step holds dims (D / 4) t + 4 ks + {0, 1} and + {2, 3} of rows g and g + 8
+        const int d = 8 * lr + 4 * half, tt = d / (D / 4), ks = (d % (D / 4)) / 4;
+        const uint32_t at = (uint32_t)((((mt * K16 + ks) * 32) + 4 * r8 + tt) * 16 + up * 4);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t v = w[2 * half + e];
-          const float y0 = __uint_as_float(v << 16) * lift_a * lift_b, y1 = __uint_as_float(v & 0xffff0000u) * lift_a * lift_b;
-          const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1);
-          const uint32_t hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
-          const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
-          hi |= h2 << (16 * e);
-          lo |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (16 * e);
-        }
-        const int d = 8 * lr + 4 * half;
-        // 8-bit fragments: thread (g, t) of a k-step holds dims 32 t + 4 ks (D = 128; register h: + 16), or
-        // 16 t + 8 ks (D = 64; register h: + 4) of rows g and g + 8
-        const int tt = D == 128 ? d / 32 : d / 16, hh = D == 128 ? (d % 32) / 16 : (d % 8) / 4,
-                  ks = D == 128 ? (d % 16) / 4 : (d % 16) / 8;
-        unsigned char *q8 = sm + Sh::kOffQ8 + ((((mt * K8 + ks) * 2) * 32) + 4 * r8 + tt) * 16 + (2 * hh + up) * 4;
-        *reinterpret_cast<uint32_t *>(q8) = hi;
-        *reinterpret_cast<uint32_t *>(q8 + 32 * 16) = lo;
-        if (chunk == 0) {  // the block that attends the tree
-          // bf16 fragments: thread (g, t) of a k-step holds dims (D / 4) t + 4 ks + {0, 1} and + {2, 3}
-          const int t16 = d / (D / 4), k16 = (d % (D / 4)) / 4;
-          unsigned char *q16 = sm + Sh::kOffQ16 + (((mt * K16 + k16) * 32) + 4 * r8 + t16) * 16 + up * 4;
-          *reinterpret_cast<uint32_t *>(q16) = w[2 * half];
-          *reinterpret_cast<uint32_t *>(q16 + 8) = w[2 * half + 1];
+          *reinterpret_cast<uint32_t *>(sm + Sh::kOffQ + at + 8 * e) =
+              pack_f16x2(__uint_as_float(v << 16) * lift_a * lift_b, __uint_as_float(v & 0xffff0000u) * lift_a * lift_b);
+          if (chunk == 0) *reinterpret_cast<uint32_t *>(sm + Sh::kOffQ16 + at + 8 * e) = v;  // for the tree's rows
         }
       }
       // what a score of lifted q and codes stands for, in log2 units; a row that is not finite scores NaN
@@ -696,7 +668,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
         if (!there[1]) valid &= 0x0000ffffu;
       }
       const uint32_t kb = sb + (uint32_t)((kg * ST + stage) * 2 * TB), vb = kb + TB;
-      // S = q K^T: a thread's 32 (16) bytes of a key row are two words a k-step
+      // S = q K^T: a thread's 32 (16) bytes of a key row are one word a k-step
       float s[MT][4][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -714,23 +686,19 @@ __global__ void __launch_bounds__(kPaThreads, 2)
         }
       }
 #pragma unroll
-      for (int k = 0; k < K8; ++k) {
+      for (int k = 0; k < K16; ++k) {
         uint32_t b0[4], b1[4];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-          const uint4 x = kw[nt][0], y = kw[nt][D / 64 - 1];
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-          b0[nt] = D == 128 ? xw[k & 3] : xw[(2 * k) & 3];
-          b1[nt] = D == 128 ? yw[k & 3] : xw[(2 * k + 1) & 3];
+          const uint4 x = kw[nt][k >> 2];
+          f8x4_to_f16<FMT>((k & 3) == 0 ? x.x : (k & 3) == 1 ? x.y : (k & 3) == 2 ? x.z : x.w, b0[nt], b1[nt]);
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint4 q = lds128(sb + Sh::kOffQ + (uint32_t)((((wr * MT + mt) * K16 + k) * 32 + lane) * 16));
 #pragma unroll
-          for (int term = 0; term < 2; ++term) {
-            const uint4 q = lds128(sb + Sh::kOffQ8 + (uint32_t)(((((wr * MT + mt) * K8 + k) * 2 + term) * 32 + lane) * 16));
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) mma_f8<FMT>(s[mt][nt], q, b0[nt], b1[nt]);
-          }
+          for (int nt = 0; nt < 4; ++nt) mma_16<false>(s[mt][nt], q.x, q.y, q.z, q.w, b0[nt], b1[nt]);
+        }
       }
       uint32_t keep[2 * MT];
 #pragma unroll
@@ -847,22 +815,41 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   if (chunks == 1) return;
   // ---- the chunks' rows, merged by the last block to arrive ----
   if (!arrive_last(ma.cnt + tile_id, (unsigned)chunks, &s_last)) return;
+  const long long base = tile_id * ma.S * R;
+  float2 *pair = reinterpret_cast<float2 *>(sm);           // [chunks][real]: (maximum, sum), then (weight, -)
+  float2 *stat = pair + kPaMaxSplits * R;                  // [real]: the row's maximum and sum
+  for (int x = t; x < chunks * real; x += kPaThreads) {
+    const int k = x / real, r = x - k * real;
+    pair[x] = __ldcg(&ma.part_ml[base + (long long)k * R + r]);
+  }
+  __syncthreads();
+  for (int r = t; r < real; r += kPaThreads) {
+    float M = pair[r].x, sum = 0.f;
+    for (int k = 1; k < chunks; ++k) M = fmaxf(M, pair[k * real + r].x);
+    for (int k = 0; k < chunks; ++k) {
+      const float w = ex2_fast(pair[k * real + r].x - M);
+      sum = fmaf(pair[k * real + r].y, w, sum);
+      pair[k * real + r].x = w;
+    }
+    stat[r] = make_float2(M, sum);
+  }
+  __syncthreads();
   for (int x = t; x < real * (D / 4); x += kPaThreads) {
     const int r = x / (D / 4), c = x - r * (D / 4);
-    const long long at = tile_id * ma.S * R + r;
-    float M = -INFINITY;
-    for (int k = 0; k < chunks; ++k) M = fmaxf(M, __ldcg(&ma.part_ml[at + (long long)k * R].x));
-    float sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < chunks; ++k) {
-      const float2 e = __ldcg(&ma.part_ml[at + (long long)k * R]);
-      const float4 y = __ldcg(&ma.part_o[(at + (long long)k * R) * (D / 4) + c]);
-      const float w = ex2_fast(e.x - M);
-      sum = fmaf(e.y, w, sum);
-      v.x = fmaf(y.x, w, v.x); v.y = fmaf(y.y, w, v.y); v.z = fmaf(y.z, w, v.z); v.w = fmaf(y.w, w, v.w);
+    for (int k0 = 0; k0 < chunks; k0 += 8) {
+      float4 y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // every load in flight before any arithmetic
+        y[j] = k0 + j < chunks ? __ldcg(&ma.part_o[(base + (long long)(k0 + j) * R + r) * (D / 4) + c])
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w = k0 + j < chunks ? pair[(k0 + j) * real + r].x : 0.f;
+        v.x = fmaf(y[j].x, w, v.x); v.y = fmaf(y[j].y, w, v.y); v.z = fmaf(y[j].z, w, v.z); v.w = fmaf(y[j].w, w, v.w);
+      }
     }
-    write_row(r, c, v, M, sum);
+    write_row(r, c, v, stat[r].x, stat[r].y);
   }
 }
 
@@ -940,10 +927,9 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
     S = (int)(want / tiles);
     const int by_tiles = T / (2 * kPaMinTiles);
     if (S > by_tiles) S = by_tiles;
-    if (S > 64) S = 64;
   }
   if (S > T) S = T;
-  if (S > 256) S = 256;
+  if (S > kPaMaxSplits) S = kPaMaxSplits;
   if (S < 1) S = 1;
   p->S = S;
   if (S > 1) {

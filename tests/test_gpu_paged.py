@@ -97,11 +97,11 @@ def check_attention(got, glse, ref, d, dtype, L):
     A score is a sum of d products in fp32 and a few more roundings: (d + 8) 2^-24 of sum |q||k| * scale, and its
     image in 2^x of a few 2^-22 (the hardware base-2 exponential); both sums of weights run in fp32 over L + N terms
     of one sign each (2^-24 a term at the worst; the partial sums of a block tree lose less).  bf16: q meets cached codes
-    as two e4m3 terms of at most 448, the second with steps of 2^-9 (half a step off) where the first is below 2^-2:
-    2^-10 / 224 of the row's largest element; weights that meet cached values are rounded to fp16 (2^-11), those that
-    meet tree rows to bf16 (2^-8), out to bf16 (2^-8)."""
+    in fp16, its row's largest element at 2^14 or above, so a bf16 value loses at most half of fp16's last step there:
+    2^-25 / 2^14; weights that meet cached values are rounded to fp16 (2^-11), those that meet tree rows to bf16
+    (2^-8), out to bf16 (2^-8)."""
     out, lse, abs_c, abs_t, reach, flat = ref
-    eps = (d + 8) * 2.0 ** -24 * reach + 2.0 ** -19 + (2.0 ** -10 / 224 * flat if dtype == "bf16" else 0)
+    eps = (d + 8) * 2.0 ** -24 * reach + 2.0 ** -19 + (2.0 ** -39 * flat if dtype == "bf16" else 0)
     weight = (2 * eps).T[:, :, None] + min((L + 128) * 2.0 ** -24, 2.0 ** -16)
     if dtype == "bf16":
         tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -11 + weight) * abs_c + (2.0 ** -8 + weight) * abs_t
