@@ -735,7 +735,8 @@ et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_
  * tokens; both set ET_DEV_BAD_INDEX.
  * Scores, softmax statistics and outputs accumulate in fp32.  bf16 inputs:
  * cached codes meet q as it is (only what lies 2^-38 below the largest of its
- * row is lost), weights are rounded to fp16 (cached tokens) or bf16 (tree
+ * row is lost; 2^-18 with d = 128 and more than 16 rows, N * Hq / Hkv, per KV
+ * head, where q goes to the 8-bit tensor cores in two terms), weights are rounded to fp16 (cached tokens) or bf16 (tree
  * rows) before they meet V.  A q row that holds
  * a NaN or an infinity gives NaN.  fp32 inputs: fp32 throughout.
  * bf16 inputs: a bounded wait that expires sets ET_DEV_TIMEOUT and leaves that

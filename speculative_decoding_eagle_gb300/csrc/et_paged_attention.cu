@@ -12,43 +12,10 @@
 // softmax's numerator and denominator.
 #include <cuda_bf16.h>
 
-#include "et_paged.cuh"
-#include "et_tc.cuh"
+#include "et_paged_attn.cuh"
 
 namespace et {
 namespace {
-
-struct PagedAttnArgs {
-  int B, N, Hq, Hkv, G, P, max_blocks, W, max_prefix;
-  float scale_log2;  // scale * log2(e)
-  long long num_pages, page_stride;
-  const uint8_t *k_pages, *v_pages;
-  const float *k_scale, *v_scale;
-  const int32_t *block_table, *prefix_len;
-  const void *q, *kt, *vt;
-  const unsigned long long *mask;
-  void *out;
-  float *lse;
-  int32_t *dev_status;
-};
-
-// prefix length of sequence b as the kernels use it: -1 = no sequence here
-__device__ __forceinline__ int paged_prefix(const PagedAttnArgs &a, int b, int &bad) {
-  int L = a.prefix_len[b];
-  const long long room = min((long long)a.max_prefix, (long long)a.max_blocks * a.P);
-  if (L > room) {
-    bad = 1;
-    L = (int)room;
-  }
-  return L < 0 ? -1 : L;
-}
-__device__ __forceinline__ float clamp_v_scale(float s) {
-  return fminf(fmaxf(s, 1.f / (1ll << kScaleExp)), (float)(1ll << kScaleExp));  // NaN -> the smallest
-}
-__device__ __forceinline__ bool tree_keeps(const PagedAttnArgs &a, int b, int i, int tt) {
-  if (!a.mask) return tt <= i;
-  return (a.mask[((long long)b * a.N + i) * a.W + (tt >> 6)] >> (tt & 63)) & 1ull;
-}
 
 // ---------------------------------------------------------------------------
 // fp32: CUDA cores, one block per (row, head, sequence)
@@ -209,20 +176,6 @@ et_status launch_row(const PagedAttnArgs &a, int d, cudaStream_t st) {
 constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
 constexpr int kPaTile = 32;  // keys per tile
-constexpr int kPaMaxSplits = 64;
-constexpr float kPaTop = 7.f, kPaSlack = 8.f;  // weights lie below 2^kPaTop when the maximum moves, below 2^15 always
-
-struct PagedMmaArgs {
-  PagedAttnArgs a;
-  int S, tiles_y;       // chunks, Hkv * row tiles
-  int row_tiles;        // row tiles per KV head
-  int box;              // rows per TMA box: 32 or 16
-  int min_tiles;        // smallest chunk, in tiles
-  unsigned int *cnt;    // [B * tiles_y] arrival counters
-  float2 *part_ml;      // [B * tiles_y][S][R] (maximum, sum)
-  float4 *part_o;       // [B * tiles_y][S][R][D] fp32
-  long long wait_cycles;
-};
 
 template <int D, int WR, int MT>
 struct PaShape {
@@ -242,11 +195,6 @@ struct PaShape {
   static_assert(2 * (kBytes + 1024 + 64) <= 228 * 1024, "two blocks per SM");
 };
 
-__device__ __forceinline__ float ex2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 template <bool BF16>
 __device__ __forceinline__ void mma_16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
@@ -352,7 +300,7 @@ __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const
 template <int D, int FMT, int WR, int MT>
 __global__ void __launch_bounds__(kPaThreads, 2)
     k_paged_attn_mma(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const __grid_constant__ PagedMmaArgs ma) {
+                     const __grid_constant__ PagedSplitArgs ma) {
   using Sh = PaShape<D, WR, MT>;
   constexpr int KG = Sh::KG, R = Sh::R, ST = Sh::kStages, TB = Sh::kTileBytes;
   constexpr int K16 = D / 16, NTO = D / 8;
@@ -815,77 +763,33 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   if (chunks == 1) return;
   // ---- the chunks' rows, merged by the last block to arrive ----
   if (!arrive_last(ma.cnt + tile_id, (unsigned)chunks, &s_last)) return;
-  const long long base = tile_id * ma.S * R;
-  float2 *pair = reinterpret_cast<float2 *>(sm);           // [chunks][real]: (maximum, sum), then (weight, -)
-  float2 *stat = pair + kPaMaxSplits * R;                  // [real]: the row's maximum and sum
-  for (int x = t; x < chunks * real; x += kPaThreads) {
-    const int k = x / real, r = x - k * real;
-    pair[x] = __ldcg(&ma.part_ml[base + (long long)k * R + r]);
-  }
-  __syncthreads();
-  for (int r = t; r < real; r += kPaThreads) {
-    float M = pair[r].x, sum = 0.f;
-    for (int k = 1; k < chunks; ++k) M = fmaxf(M, pair[k * real + r].x);
-    for (int k = 0; k < chunks; ++k) {
-      const float w = ex2_fast(pair[k * real + r].x - M);
-      sum = fmaf(pair[k * real + r].y, w, sum);
-      pair[k * real + r].x = w;
-    }
-    stat[r] = make_float2(M, sum);
-  }
-  __syncthreads();
-  for (int x = t; x < real * (D / 4); x += kPaThreads) {
-    const int r = x / (D / 4), c = x - r * (D / 4);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < chunks; k0 += 8) {
-      float4 y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)  // every load in flight before any arithmetic
-        y[j] = k0 + j < chunks ? __ldcg(&ma.part_o[(base + (long long)(k0 + j) * R + r) * (D / 4) + c])
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float w = k0 + j < chunks ? pair[(k0 + j) * real + r].x : 0.f;
-        v.x = fmaf(y[j].x, w, v.x); v.y = fmaf(y[j].y, w, v.y); v.z = fmaf(y[j].z, w, v.z); v.w = fmaf(y[j].w, w, v.w);
-      }
-    }
-    write_row(r, c, v, stat[r].x, stat[r].y);
-  }
+  merge_chunks<D, R, kPaThreads>(ma, tile_id, chunks, real, sm, write_row);
 }
 
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-// pages as [num_pages][Hkv][P][d] bytes; a box is `box` rows of one head of one page
-bool make_page_map(CUtensorMap *m, const void *base, const et_paged_cache *c, int box) {
-  const cuuint64_t dims[4] = {(cuuint64_t)c->d, (cuuint64_t)c->page_size, (cuuint64_t)c->Hkv, (cuuint64_t)c->num_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)c->d, (cuuint64_t)c->d * c->page_size, (cuuint64_t)c->page_stride};
-  const cuuint32_t boxes[4] = {(cuuint32_t)c->d, (cuuint32_t)box, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, boxes, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, int FMT, int WR, int MT>
-et_status launch_mma(const CUtensorMap &mk, const CUtensorMap &mv, const PagedMmaArgs &ma, cudaStream_t st) {
+et_status launch_mma(const CUtensorMap &mk, const CUtensorMap &mv, const PagedSplitArgs &ma, cudaStream_t st) {
   using Sh = PaShape<D, WR, MT>;
   if (et_smem_attr((const void *)k_paged_attn_mma<D, FMT, WR, MT>, Sh::kBytes) != cudaSuccess) return ET_ERR_CUDA;
   return et_launch(k_paged_attn_mma<D, FMT, WR, MT>, dim3(ma.S, ma.tiles_y, ma.a.B), dim3(kPaThreads), Sh::kBytes, st,
                    0, mk, mv, ma);
 }
 template <int D, int FMT>
-et_status launch_mma_rows(int R, const CUtensorMap &mk, const CUtensorMap &mv, const PagedMmaArgs &ma, cudaStream_t st) {
-  if (R == 16) return launch_mma<D, FMT, 1, 1>(mk, mv, ma, st);
-  if (R == 32) return launch_mma<D, FMT, 1, 2>(mk, mv, ma, st);
-  return launch_mma<D, FMT, 2, 2>(mk, mv, ma, st);
+et_status launch_mma_rows(int R, const CUtensorMap &mk, const CUtensorMap &mv, const PagedSplitArgs &ma, cudaStream_t st) {
+  if constexpr (D == 64) {  // with d = 128 more rows go to the tcgen05 kernel
+    if (R == 32) return launch_mma<D, FMT, 1, 2>(mk, mv, ma, st);
+    if (R == 64) return launch_mma<D, FMT, 2, 2>(mk, mv, ma, st);
+  }
+  return launch_mma<D, FMT, 1, 1>(mk, mv, ma, st);
 }
 
 struct PagedPlan {
   int S;      // blocks a sequence's keys are split over
   int R;      // query rows per block
   int row_tiles;
+  bool tc;    // tcgen05 kernel (bf16, d = 128, more than 16 rows per KV head), else mma.sync
   size_t ws;  // workspace bytes: counters, (maximum, sum) pairs, partial rows
   size_t ml_off, o_off;
 };
@@ -912,20 +816,24 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   p->S = 1;
   p->ws = p->ml_off = p->o_off = 0;
   p->R = p->row_tiles = 1;
+  p->tc = false;
   if (s->dtype == ET_F32) return ET_OK;
   const long long rows = (long long)s->N * (s->Hq / c->Hkv);
-  p->R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  p->tc = c->d == 128 && rows > 16;
+  p->R = rows <= 16 ? 16 : rows <= 32 && !p->tc ? 32 : 64;
   p->row_tiles = (int)((rows + p->R - 1) / p->R);
   const long long tiles = (long long)s->B * c->Hkv * p->row_tiles;
   if ((long long)c->Hkv * p->row_tiles > 65535) return ET_ERR_UNSUPPORTED;
   const long long room = (long long)s->max_blocks * c->page_size;
-  const int T = (int)(((s->max_prefix < room ? s->max_prefix : room) + kPaTile - 1) / kPaTile);
+  const int tile = p->tc ? kPtKeys : kPaTile;
+  const int T = (int)(((s->max_prefix < room ? s->max_prefix : room) + tile - 1) / tile);
   int S = s->num_splits;
   if (S <= 0) {
-    // two blocks fit an SM: one wave for one sequence, four when the lengths may differ
-    const long long want = (s->B > 1 ? 4ll : 1ll) * 2 * sm_count();
+    // one wave of blocks for one sequence (two mma.sync blocks fit an SM, one tcgen05 block), four when the lengths
+    // may differ
+    const long long want = (s->B > 1 ? 4ll : 1ll) * (p->tc ? 1 : 2) * sm_count();
     S = (int)(want / tiles);
-    const int by_tiles = T / (2 * kPaMinTiles);
+    const int by_tiles = p->tc ? T : T / (2 * kPaMinTiles);
     if (S > by_tiles) S = by_tiles;
   }
   if (S > T) S = T;
@@ -988,7 +896,7 @@ extern "C" et_status et_tree_attention_paged(const et_paged_attn_shape *shape, c
   if (shape->dtype == ET_F32)
     return e4m3 ? launch_row<ET_KV_E4M3>(a, cache->d, st) : launch_row<ET_KV_E5M2>(a, cache->d, st);
   if (!encode_fn()) return ET_ERR_CUDA;
-  PagedMmaArgs ma;
+  PagedSplitArgs ma;
   ma.a = a;
   ma.S = plan.S;
   ma.row_tiles = plan.row_tiles;
@@ -1000,6 +908,7 @@ extern "C" et_status et_tree_attention_paged(const et_paged_attn_shape *shape, c
   ma.part_ml = plan.S > 1 ? reinterpret_cast<float2 *>(wsb + plan.ml_off) : nullptr;
   ma.part_o = plan.S > 1 ? reinterpret_cast<float4 *>(wsb + plan.o_off) : nullptr;
   ma.wait_cycles = et_wait_limit_cycles();
+  if (plan.tc) return paged_tc_launch(cache, ma, st);
   CUtensorMap mk, mv;
   if (!make_page_map(&mk, cache->k_pages, cache, ma.box) || !make_page_map(&mv, cache->v_pages, cache, ma.box))
     return ET_ERR_INVALID_ARG;

@@ -1,0 +1,745 @@
+// Paged 8-bit attention on the 5th-generation tensor cores (tcgen05): the many
+// rows of a draft tree (EAGLE-2 article, attention-mask paragraph) against a
+// cache whose codes go to the tensor cores as they lie in the page.  D = 128.
+//
+// Everything is transposed: keys are the rows of the products, query rows
+// their columns.
+//   S^T [128 keys x 64 rows] = K8 . Q8^T   (kind::f8f6f4; K's codes by TMA, q
+//        lifted by a power of two per row and split into two e4m3 terms that
+//        are 128 columns of one product, so K is read once)
+//   O^T [128 dims x 64 rows] += V16^T . P^T (kind::f16; V's codes as fp16)
+// A tree of up to 64 rows per KV head (every MHA tree) then fills the 128
+// lanes of tensor memory with keys instead of padding them with rows that do
+// not exist; the softmax runs one key per thread, and a tile of a page's
+// codes needs no conversion before the scores.
+//
+// One block per SM, twelve warps:
+//   warp 0      TMA: a 128-key tile of K and of V, into rings of 3
+//   warp 1      owns 512 columns of TMEM, issues every product
+//   warps 2, 3  V's codes -> fp16 (two buffers)
+//   warps 4-7, 8-11  two softmax groups on alternate tiles, each with its own
+//               scores, weights, running maximum and O in TMEM: independent
+//               online softmaxes, joined at the end.
+// A weight's reference moves only when some weight would pass 2^15 (one vote
+// per 32 rows in place of a maximum over the lanes); the slow path finds the
+// maxima, and rescales the group's sums and O.  The tree's own rows are one
+// more tile in bf16, staged by all warps before the roles part.
+// Bounds: K8 and V8 through shared memory and V16 written and read again make
+// shared-memory traffic (about 1400 cycles a tile at 128 bytes a cycle) the
+// next limit after HBM (1365 cycles a tile).  Every mbarrier wait is bounded:
+// a block that gives up sets ET_DEV_TIMEOUT, drains what it issued and leaves.
+#include "et_paged_attn.cuh"
+
+namespace et {
+namespace {
+
+constexpr int kPtThreads = 384;
+constexpr int kPtD = 128;
+constexpr int kPtStages = 3;
+constexpr int kPtConvWarps = 2;
+constexpr uint32_t kPtTile8 = kPtKeys * kPtD;            // 16 KB: K8 or V8
+constexpr uint32_t kPtTile16 = 2 * kPtTile8;             // 32 KB: V16, two halves of 64 dims
+constexpr uint32_t kPtHalf16 = kPtKeys * 128;            // 16 KB
+constexpr uint32_t kPtP = kPtKeys * kPtRows * 2;         // 16 KB
+constexpr uint32_t kPtOffQ = 0;                          // Q8: 64 rows hi, 64 rows lo, 128 bytes each
+constexpr uint32_t kPtOffK = kPtOffQ + 2 * kPtRows * kPtD;
+constexpr uint32_t kPtOffV = kPtOffK + kPtStages * kPtTile8;
+constexpr uint32_t kPtOffVH = kPtOffV + kPtStages * kPtTile8;
+constexpr uint32_t kPtOffP = kPtOffVH + 2 * kPtTile16;
+constexpr uint32_t kPtOffBar = kPtOffP + 2 * kPtP;
+constexpr uint32_t kPtOffFC = kPtOffBar + 256;           // [2 groups][64] (row factor, -reference)
+constexpr uint32_t kPtOffRed = kPtOffFC + 2 * kPtRows * 8;     // [2][4 warps][64]
+constexpr uint32_t kPtOffAdj = kPtOffRed + 2 * 4 * kPtRows * 4;  // [2][64] (reference change, factor)
+constexpr uint32_t kPtOffMask = kPtOffAdj + 2 * kPtRows * 8;   // [64] two mask words
+constexpr uint32_t kPtOffML = kPtOffMask + kPtRows * 16;       // [2][64] (reference, sum)
+constexpr uint32_t kPtBytes = kPtOffML + 2 * kPtRows * 8 + 1024;  // + slack for 1024-byte alignment
+static_assert(kPtBytes <= 227 * 1024 - 256, "one block per SM");
+// before the first products the tree's rows use the weights' and V16's space
+constexpr uint32_t kPtOffTreeK = kPtOffP;                    // K tree, bf16, two halves of 128 rows
+constexpr uint32_t kPtOffTreeV = kPtOffVH;                   // V tree, bf16, as V16 buffer 0
+constexpr uint32_t kPtOffTreeQ = kPtOffVH + kPtTile16;       // q, bf16, two halves of 64 rows
+// TMEM columns
+constexpr uint32_t kPtColS = 0, kPtColO = 256, kPtTmemCols = 512;
+
+enum { T_KFULL = 0, T_KEMPTY = 3, T_VFULL = 6, T_VEMPTY = 9, T_SFULL = 12, T_SFREE = 14, T_PFULL = 16, T_VHFULL = 18,
+       T_PVDONE = 20, T_TREE = 22, T_DRAIN = 23, T_COUNT = 24 };
+
+// instruction descriptors: fp32 sums (bits 4-5 = 1), A type in bits 7-9, B
+// type in 10-12, A / B stored MN-major in bits 15 / 16, N >> 3, M >> 4
+constexpr uint32_t pt_idesc(int a_type, int b_type, bool a_mn, bool b_mn, int M, int N) {
+  return (1u << 4) | ((uint32_t)a_type << 7) | ((uint32_t)b_type << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void pt_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void pt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+// OR of a condition over a softmax group's 128 threads, and a barrier
+__device__ __forceinline__ bool group_any(int group, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(1 + group), "r"(p ? 1u : 0u)
+      : "memory");
+  return r != 0u;
+}
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
+// chunk c (16 bytes) of row r in a tile of 128-byte rows, 128-byte swizzle
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+// an fp32 value as an integer that orders like it
+__device__ __forceinline__ int order_int(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kPtThreads, 1)
+    k_paged_attn_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ PagedSplitArgs ma) {
+  const PagedAttnArgs &a = ma.a;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ int s_abort, s_last, s_odd;
+  __shared__ int s_red[kPtThreads / 32];
+  __shared__ uint32_t s_tmem, s_units[kPtStages];
+  unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t sb = saddr(sm);
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  auto bar = [&](int i) -> uint32_t { return sb + kPtOffBar + 8u * (uint32_t)i; };
+
+  // ---- set-up that touches no global memory ----
+  if (t == 0) {
+    s_abort = 0;
+    s_odd = 0;
+    for (int i = 0; i < T_COUNT; ++i) {
+      int count = 1;
+      if (i >= T_VEMPTY && i < T_SFULL) count = kPtConvWarps;
+      if (i >= T_SFREE && i < T_VHFULL) count = 4;
+      if (i >= T_VHFULL && i < T_PVDONE) count = kPtConvWarps;
+      mbar_init(bar(i), (uint32_t)count);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  pdl_wait();  // the previous kernel in the stream has completed
+  const int b = blockIdx.z, g = blockIdx.y / ma.row_tiles, rt = blockIdx.y - g * ma.row_tiles, chunk = blockIdx.x;
+  int bad = 0;
+  const int L = paged_prefix(a, b, bad);
+  int longest = L;  // chunks are as long in every sequence: the longest sequence's share
+  if (a.B > 1) {
+    int other = 0;
+    if (a.B <= kPtThreads) {
+      int ignore = 0;
+      if (t < a.B) other = paged_prefix(a, t, ignore);
+    } else {
+      other = (int)min((long long)a.max_prefix, (long long)a.max_blocks * a.P);
+    }
+    other = __reduce_max_sync(0xffffffffu, other);
+    if (lane == 0) s_red[warp] = other;
+    __syncthreads();
+    longest = s_red[0];
+    for (int w = 1; w < kPtThreads / 32; ++w) longest = max(longest, s_red[w]);
+  }
+  if (L < 0) return;
+  const int T = (L + kPtKeys - 1) / kPtKeys, Tl = (longest + kPtKeys - 1) / kPtKeys;
+  const int per = max((Tl + ma.S - 1) / ma.S, 1);
+  const int chunks = max(1, (T + per - 1) / per);
+  if (chunk >= chunks) return;
+  const int t0 = chunk * per, n = min(T, t0 + per) - t0;  // prefix tiles t0 .. t0 + n - 1
+  const int tree = chunk == 0 ? 1 : 0;                    // item 0 is the tree's tile
+  const int items = n + tree;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&s_tmem)), "r"(kPtTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  __syncthreads();  // barriers initialised (and the longest prefix read by all)
+  pdl_trigger();    // after the TMEM allocation: a waiting dependent block must not hold what this block needs
+
+  // ---- TMA (warp 0): tile j of this block into ring stage j % stages ----
+  int page = -1, slot = 0;  // lane: unit (lane & 7) of tile 4 * (j / 4) + (lane >> 3), 16 keys a unit
+  auto fetch_pages = [&](int j0) {
+    const int j = j0 + (lane >> 3);
+    const long long key = (long long)(t0 + j) * kPtKeys + 16 * (lane & 7);
+    page = -1;
+    if (j < n && key < L) {
+      const int blk = (int)key / a.P;
+      slot = (int)key - blk * a.P;
+      page = a.block_table[(long long)b * a.max_blocks + blk];
+      if (page < 0 || page >= a.num_pages) {
+        page = -1;
+        bad = 1;
+      }
+    }
+  };
+  auto issue = [&](int j) {
+    const int stage = j % kPtStages, src = 8 * (j & 3), per_box = ma.box / 16;
+    const int pg = __shfl_sync(0xffffffffu, page, src + (lane & 7)), sl = __shfl_sync(0xffffffffu, slot, src + (lane & 7));
+    const uint32_t there = __ballot_sync(0xffffffffu, lane < 8 && pg >= 0);
+    const uint32_t mine = __ballot_sync(0xffffffffu, lane < 8 && lane % per_box == 0 && pg >= 0);
+    const uint32_t bytes = (uint32_t)__popc(mine) * (uint32_t)ma.box * kPtD;
+    if (lane == 0) {
+      s_units[stage] = there;
+      if (bytes) {
+        mbar_expect_tx(bar(T_KFULL + stage), bytes);
+        mbar_expect_tx(bar(T_VFULL + stage), bytes);
+      } else {
+        mbar_arrive(bar(T_KFULL + stage));
+        mbar_arrive(bar(T_VFULL + stage));
+      }
+    }
+    __syncwarp();
+    if ((mine >> lane) & 1u) {
+      const uint32_t off = (uint32_t)(stage * kPtTile8 + lane * 16 * kPtD);
+      tma_4d(sb + kPtOffK + off, &tm_k, 0, sl, g, pg, bar(T_KFULL + stage));
+      tma_4d(sb + kPtOffV + off, &tm_v, 0, sl, g, pg, bar(T_VFULL + stage));
+    }
+  };
+  if (warp == 0) {
+    fetch_pages(0);
+    for (int j = 0; j < n && j < kPtStages; ++j) issue(j);
+  }
+
+  // ---- q: two e4m3 terms, K-major; 16 lanes a row, eight dims a lane ----
+  float2 *fc = reinterpret_cast<float2 *>(sm + kPtOffFC);
+  {
+    const int lr = t & 15;
+    for (int r = t >> 4; r < kPtRows; r += kPtThreads / 16) {
+      const int Rg = rt * kPtRows + r, i = Rg / a.G;
+      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+      if (i < a.N)
+        raw = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                               (((long long)b * a.N + i) * a.Hq + g * a.G + (Rg - i * a.G)) * kPtD + 8 * lr);
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      uint32_t top = 0u;  // the row's largest magnitude, as the bits of a bf16 value: they order like the values
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x, 16));
+      const bool odd = top >= 0x7f80u;  // NaN or infinity
+      // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8; half of e2 stays within fp32's exponents
+      const int e2 = top == 0u || odd ? 0 : 135 - max((int)(top >> 7), 1) - ((top & 0x7fu) > 0x60u ? 1 : 0);
+      const int ea = e2 >> 1, eb = e2 - ea;
+      const float lift_a = __uint_as_float((uint32_t)(127 + ea) << 23), lift_b = __uint_as_float((uint32_t)(127 + eb) << 23);
+      uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float y0 = __uint_as_float(w[e] << 16) * lift_a * lift_b, y1 = __uint_as_float(w[e] & 0xffff0000u) * lift_a * lift_b;
+        const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1);
+        const uint32_t hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
+        const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
+        hi[e >> 1] |= h2 << (16 * (e & 1));
+        lo[e >> 1] |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (16 * (e & 1));
+      }
+      unsigned char *dst = sm + kPtOffQ + sw128(r, lr >> 1) + 8 * (lr & 1);
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2 *>(dst + kPtRows * kPtD) = make_uint2(lo[0], lo[1]);
+      if (tree) sts128(sb + kPtOffTreeQ + (uint32_t)((lr >> 3) * kPtRows * 128) + sw128(r, lr & 7), w[0], w[1], w[2], w[3]);
+      if (lr == 0) {
+        // what a score of lifted q and codes stands for, in log2 units; a row that is not finite scores NaN
+        const float f = odd ? __uint_as_float(0x7fc00000u)
+                            : a.scale_log2 * __uint_as_float((uint32_t)(127 - ea) << 23) * __uint_as_float((uint32_t)(127 - eb) << 23);
+        fc[kPtRows + r] = make_float2(f, 0.f);
+        fc[r] = make_float2(tree ? a.scale_log2 : f, 0.f);  // group 0 takes the tree's tile first: q as it is
+      }
+    }
+  }
+  if (tree) {  // ---- the tree's rows: K as keys x dims, V as keys x dims, 16 bytes a thread at a time ----
+    const __nv_bfloat16 *KT = static_cast<const __nv_bfloat16 *>(a.kt), *VT = static_cast<const __nv_bfloat16 *>(a.vt);
+    const int rows = (a.N + 15) & ~15;
+    bool odd = false;
+    for (int x = t; x < rows * 16; x += kPtThreads) {
+      const int r = x >> 4, c = x & 15;
+      uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
+      if (r < a.N) {
+        const long long at = (((long long)b * a.N + r) * a.Hkv + g) * kPtD + 8 * c;
+        k = *reinterpret_cast<const uint4 *>(KT + at);
+        v = *reinterpret_cast<const uint4 *>(VT + at);
+      }
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      // NaN and infinities would reach rows that do not attend their key (0 * inf): they are added at the end
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; odd = true; }
+        if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; odd = true; }
+      }
+      const uint32_t at = (uint32_t)((c >> 3) * kPtHalf16) + sw128(r, c & 7);
+      sts128(sb + kPtOffTreeK + at, k.x, k.y, k.z, k.w);
+      sts128(sb + kPtOffTreeV + at, w[0], w[1], w[2], w[3]);
+    }
+    if (odd) s_odd = 1;
+    if (t < kPtRows) {
+      const int i = (rt * kPtRows + t) / a.G;
+      unsigned long long m0 = 0ull, m1 = 0ull;
+      if (i < a.N) {
+        if (a.mask) {
+          m0 = a.mask[((long long)b * a.N + i) * a.W];
+          if (a.W > 1) m1 = a.mask[((long long)b * a.N + i) * a.W + 1];
+        } else {
+          m0 = i >= 63 ? ~0ull : (2ull << i) - 1ull;
+          m1 = i < 64 ? 0ull : (i >= 127 ? ~0ull : (2ull << (i - 64)) - 1ull);
+        }
+      }
+      unsigned long long *m = reinterpret_cast<unsigned long long *>(sm + kPtOffMask) + 2 * t;
+      m[0] = m0;
+      m[1] = m1;
+    }
+  }
+  fence_async_smem();  // q and the tree's rows are read by the tensor cores
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const long long limit = ma.wait_cycles;
+
+  if (warp == 0) {
+    // ---------------- TMA ----------------
+    bool ok = true;
+    int issued = n < kPtStages ? n : kPtStages;
+    for (int j = kPtStages; j < n; ++j) {
+      if ((j & 3) == 0) fetch_pages(j);
+      const int stage = j % kPtStages;
+      const uint32_t phase = (uint32_t)(j / kPtStages - 1) & 1u;
+      ok = mbar_wait(bar(T_KEMPTY + stage), phase, &s_abort, limit) && mbar_wait(bar(T_VEMPTY + stage), phase, &s_abort, limit);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      issue(j);
+      issued = j + 1;
+    }
+    if (lane == 0)  // no copy may be in flight when the block leaves
+      for (int j = issued > kPtStages ? issued - kPtStages : 0; j < issued; ++j) {
+        mbar_drain(bar(T_KFULL + j % kPtStages), (uint32_t)(j / kPtStages) & 1u);
+        mbar_drain(bar(T_VFULL + j % kPtStages), (uint32_t)(j / kPtStages) & 1u);
+      }
+    if (bad) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
+  } else if (warp == 1) {
+    // ---------------- products ----------------
+    if (lane == 0 && items > 0) {
+      constexpr uint32_t iS = pt_idesc(FMT == ET_KV_E4M3 ? 0 : 1, 0, false, false, 128, 128);
+      constexpr uint32_t iSt = pt_idesc(1, 1, false, false, 128, 64);
+      constexpr uint32_t iO = pt_idesc(0, 0, true, true, 128, 64), iOt = pt_idesc(1, 1, true, true, 128, 64);
+      auto scores = [&](int i) -> bool {  // item i into S buffer i & 1
+        const uint32_t d = tmem + kPtColS + 128u * (uint32_t)(i & 1);
+        if (i >= 2 && !mbar_wait(bar(T_SFREE + (i & 1)), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit)) return false;
+        if (tree && i == 0) {
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma(d, sw128_desc(sb + kPtOffTreeK + (kk >> 2) * kPtHalf16 + (kk & 3) * 32, 16, 1024),
+                   sw128_desc(sb + kPtOffTreeQ + (kk >> 2) * (kPtRows * 128) + (kk & 3) * 32, 16, 1024), iSt, kk > 0);
+          tc_commit(bar(T_TREE));
+        } else {
+          const int j = i - tree, stage = j % kPtStages;
+          if (!mbar_wait(bar(T_KFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            pt_mma_f8(d, sw128_desc(sb + kPtOffK + stage * kPtTile8 + kk * 32, 16, 1024),
+                      sw128_desc(sb + kPtOffQ + kk * 32, 16, 1024), iS, kk > 0);
+          if (j + kPtStages < n) tc_commit(bar(T_KEMPTY + stage));
+        }
+        tc_commit(bar(T_SFULL + (i & 1)));
+        return true;
+      };
+      bool ok = scores(0);
+      for (int i = 0; ok && i < items; ++i) {
+        if (i + 1 < items && !scores(i + 1)) break;
+        const int w = i & 1;
+        const uint32_t phase = (uint32_t)(i >> 1) & 1u;
+        if (!mbar_wait(bar(T_VHFULL + w), phase, &s_abort, limit) || !mbar_wait(bar(T_PFULL + w), phase, &s_abort, limit)) break;
+        tc_fence_after();
+        const bool is_tree = tree && i == 0;
+        const int steps = is_tree ? (a.N + 15) >> 4 : kPtKeys / 16;
+        for (int kk = 0; kk < steps; ++kk)
+          tc_mma(tmem + kPtColO + 64u * (uint32_t)w,
+                 sw128_desc(sb + kPtOffVH + w * kPtTile16 + kk * 2048, kPtHalf16, 1024),
+                 sw128_desc(sb + kPtOffP + w * kPtP + kk * 2048, kPtHalf16, 1024), is_tree ? iOt : iO, (i >= 2 || kk > 0) ? 1u : 0u);
+        tc_commit(bar(T_PVDONE + w));
+      }
+      // every product this thread issued has finished before TMEM is freed
+      tc_commit(bar(T_DRAIN));
+      mbar_drain(bar(T_DRAIN), 0);
+    }
+  } else if (warp < 4) {
+    // ---------------- V's codes -> fp16: 16 codes of a row a thread, halves of 64 dims, 128-byte swizzle ----------------
+    const int ct = t - 64;
+    bool ok = true;
+    for (int i = 0; i < items; ++i) {
+      const int w = i & 1;
+      if (!(tree && i == 0)) {
+        const int j = i - tree, stage = j % kPtStages;
+        if (i >= 2) ok = mbar_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
+        else if (tree) ok = mbar_wait(bar(T_TREE), 0, &s_abort, limit);  // q of the tree's scores lies in this buffer
+        ok = ok && mbar_wait(bar(T_VFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t units = *(volatile uint32_t *)&s_units[stage];
+        const int lim = L - (t0 + j) * kPtKeys;  // rows past it hold no key of this sequence
+        const uint32_t src = sb + kPtOffV + stage * kPtTile8, dst = sb + kPtOffVH + w * kPtTile16;
+        const int c = ct & 7, swap = c >> 2;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = (ct >> 3) + 8 * (4 * h + k);
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(src + sw128(r, c)));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = (ct >> 3) + 8 * (4 * h + k);
+            uint32_t x[8];
+            f8x4_to_f16<FMT>(v[k].x, x[0], x[1]);
+            f8x4_to_f16<FMT>(v[k].y, x[2], x[3]);
+            f8x4_to_f16<FMT>(v[k].z, x[4], x[5]);
+            f8x4_to_f16<FMT>(v[k].w, x[6], x[7]);
+            if (r >= lim || !((units >> (r >> 4)) & 1u)) {  // whatever lies there must not meet a zero weight
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = 0u;
+            }
+            // dims 16 c .. + 15: two 16-byte chunks of half c / 4; the upper half's lanes store them in the other order
+            const uint32_t base = dst + (uint32_t)((c >> 2) * kPtHalf16);
+            const int c0 = 2 * (c & 3);
+            if (swap) {
+              sts128(base + sw128(r, c0 + 1), x[4], x[5], x[6], x[7]);
+              sts128(base + sw128(r, c0), x[0], x[1], x[2], x[3]);
+            } else {
+              sts128(base + sw128(r, c0), x[0], x[1], x[2], x[3]);
+              sts128(base + sw128(r, c0 + 1), x[4], x[5], x[6], x[7]);
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(T_VEMPTY + stage));
+          mbar_arrive(bar(T_VHFULL + w));
+        }
+      } else if (lane == 0) {
+        mbar_arrive(bar(T_VHFULL + w));  // the tree's V was staged above
+      }
+    }
+  } else {
+    // ---------------- softmax: group w, one key per thread ----------------
+    const int w = (warp - 4) >> 2, quarter = warp & 3, tid = t & 127;  // warps 4-7 and 8-11: threads 128.. and 256..
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t fcb = sb + kPtOffFC + (uint32_t)(w * kPtRows * 8), prow = sb + kPtOffP + (uint32_t)(w * kPtP);
+    float *red = reinterpret_cast<float *>(sm + kPtOffRed) + w * 4 * kPtRows;
+    float2 *adj = reinterpret_cast<float2 *>(sm + kPtOffAdj) + w * kPtRows;
+    float l[kPtRows];
+#pragma unroll
+    for (int q = 0; q < kPtRows; ++q) l[q] = 0.f;
+    bool dead = false;
+    bool fresh[2] = {true, true};  // some row of the half has no reference yet (the same in the whole group)
+    bool mine_fresh = true;        // threads 0..63: row tid has none
+    // a key's page and scales, fetched an item ahead
+    auto my_page = [&](int i) -> int {
+      const int j = i - tree;
+      const long long key = (long long)(t0 + j) * kPtKeys + tid;
+      if (i >= items || j < 0 || key >= L) return -1;
+      const int p = a.block_table[(long long)b * a.max_blocks + (int)key / a.P];
+      return p < 0 || p >= a.num_pages ? -1 : p;
+    };
+    auto my_scale = [&](int p, float &ks, float &vs) {
+      ks = 0.f;
+      vs = 1.f;
+      if (p >= 0) {
+        ks = a.k_scale[(long long)p * a.Hkv + g];
+        vs = clamp_v_scale(a.v_scale[(long long)p * a.Hkv + g]);
+      }
+    };
+    int page_n = my_page(w);
+    float ks_n, vs_n;
+    my_scale(page_n, ks_n, vs_n);
+    for (int i = w; i < items; i += 2) {
+      const bool is_tree = tree && i == 0;
+      const bool there = is_tree ? tid < a.N : page_n >= 0;
+      const float ks = is_tree ? 1.f : ks_n, vs = is_tree ? 1.f : vs_n;
+      const float lv = __log2f(vs), iv = __frcp_rn(vs);
+      page_n = my_page(i + 2);
+      // bit q: row q attends this thread's key
+      uint32_t keep[2] = {there ? 0xffffffffu : 0u, there ? 0xffffffffu : 0u};
+      if (is_tree && there) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t bits = 0u;
+#pragma unroll 4
+          for (int q = 0; q < 32; ++q) {
+            const unsigned long long m =
+                *(reinterpret_cast<const unsigned long long *>(sm + kPtOffMask) + 2 * (32 * h + q) + (tid >> 6));
+            bits |= (uint32_t)((m >> (tid & 63)) & 1ull) << q;
+          }
+          if (h == 0) keep[0] = bits; else keep[1] = bits;
+        }
+      }
+      const bool masked = __any_sync(0xffffffffu, (keep[0] & keep[1]) != 0xffffffffu);
+      const uint32_t phase = (uint32_t)(i >> 1) & 1u;
+      if (!dead) dead = !mbar_wait(bar(T_SFULL + w), phase, &s_abort, limit);
+      dead = __any_sync(0xffffffffu, dead);
+      tc_fence_after();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x[32];
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t hi[16], lo[16];
+          const uint32_t col = lanes + kPtColS + 128u * (uint32_t)w + (uint32_t)(32 * half + 16 * part);
+          pt_ld16(col, hi);
+          pt_ld16(col + 64, lo);
+          tmem_wait_ld();
+          if (is_tree) {  // one term: the other columns hold nothing yet
+#pragma unroll
+            for (int e = 0; e < 16; ++e) lo[e] = 0u;
+          }
+          if (half == 1 && part == 1) {  // S is free once it sits in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(T_SFREE + w));
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float4 f = lds_f4(fcb + 8u * (uint32_t)(32 * half + 16 * part + e));  // two rows' (factor, -reference)
+            const float y0 = fmaf(__uint_as_float(lo[e]), ks, __uint_as_float(hi[e]) * ks);
+            const float y1 = fmaf(__uint_as_float(lo[e + 1]), ks, __uint_as_float(hi[e + 1]) * ks);
+            x[16 * part + e] = fmaf(y0, f.x, lv + f.y);
+            x[16 * part + e + 1] = fmaf(y1, f.z, lv + f.w);
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) x[q] = (keep[half] >> q) & 1u ? x[q] : -INFINITY;
+        }
+        float top = x[0];
+#pragma unroll
+        for (int q = 1; q < 32; ++q) top = fmaxf(top, x[q]);
+        if (group_any(w, fresh[half] || top > kPaTop + kPaSlack)) {
+          // the rows' maxima over the tile: a warp's 32 keys, then the four warps
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            const int m = __reduce_max_sync(0xffffffffu, order_int(x[q] == x[q] ? x[q] : -INFINITY));
+            if (lane == q) red[quarter * kPtRows + 32 * half + q] = __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+          }
+          group_sync(w);
+          bool still = false;
+          if (tid >= 32 * half && tid < 32 * half + 32) {
+            float m = fmaxf(fmaxf(red[tid], red[kPtRows + tid]), fmaxf(red[2 * kPtRows + tid], red[3 * kPtRows + tid]));
+            float2 *at = reinterpret_cast<float2 *>(sm + kPtOffFC) + w * kPtRows + tid;
+            const float was = -at->y;  // the reference; 0 while the row is fresh
+            float now = was;
+            if (m > -INFINITY) now = mine_fresh ? m - kPaTop : fmaxf(was, m + was - kPaTop);
+            const float corr = mine_fresh ? 0.f : ex2_fast(was - now);
+            mine_fresh = mine_fresh && !(m > -INFINITY);
+            still = mine_fresh;
+            at->y = -now;
+            adj[tid] = make_float2(was - now, corr);
+          }
+          fresh[half] = group_any(w, still);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            const float2 d = adj[32 * half + q];
+            x[q] += d.x;
+            l[32 * half + q] *= d.y;
+          }
+          if (i >= 2) {  // O holds the sums of this group's earlier tiles
+            if (!dead) dead = !mbar_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
+            dead = __any_sync(0xffffffffu, dead);
+            tc_fence_after();
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              uint32_t o[16];
+              const uint32_t col = lanes + kPtColO + 64u * (uint32_t)w + (uint32_t)(32 * half + 16 * part);
+              pt_ld16(col, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * adj[32 * half + 16 * part + e].y);
+              tmem_st16(col, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          group_sync(w);  // the changes are read before they may change again
+        }
+        // this group's weights buffer is free once its last product has run
+        if (half == 0 && i >= 2) {
+          if (!dead) dead = !mbar_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
+          dead = __any_sync(0xffffffffu, dead);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int q = 8 * c + 2 * e;
+            const float w0 = ex2_fast(x[q]), w1 = ex2_fast(x[q + 1]);
+            l[32 * half + q] = fmaf(w0, iv, l[32 * half + q]);
+            l[32 * half + q + 1] = fmaf(w1, iv, l[32 * half + q + 1]);
+            x[q] = w0;
+            x[q + 1] = w1;
+          }
+          if (is_tree) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = pack_bf16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = pack_f16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
+          }
+          sts128(prow + sw128(tid, 4 * half + c), p[0], p[1], p[2], p[3]);
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(T_PFULL + w));
+      my_scale(page_n, ks_n, vs_n);
+      if (is_tree) {  // cached tiles from here on: the rows' own factors
+        group_sync(w);
+        if (tid < kPtRows) fc[tid].x = fc[kPtRows + tid].x;
+        group_sync(w);
+      }
+    }
+    // the group's sums: 64 rows over 128 threads.  After the step of offset o a lane holds the rows whose index
+    // agrees with it in the bits done: 64 values become two
+#pragma unroll
+    for (int o = 16, m = 32; o > 0; o >>= 1, m >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int q = 0; q < m; ++q) {
+        const float keep = up ? l[q + m] : l[q], send = up ? l[q] : l[q + m];
+        l[q] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+    }
+    // lane bits 4..0 chose row bits 5..1
+    red[quarter * kPtRows + 2 * lane] = l[0];
+    red[quarter * kPtRows + 2 * lane + 1] = l[1];
+    group_sync(w);
+    const int mine = items > w ? (items - w + 1) / 2 : 0;  // this group's items
+    if (tid < kPtRows)
+      reinterpret_cast<float2 *>(sm + kPtOffML)[w * kPtRows + tid] =
+          make_float2(mine && !mine_fresh ? -fc[w * kPtRows + tid].y : -3e38f,
+                      (red[tid] + red[kPtRows + tid]) + (red[2 * kPtRows + tid] + red[3 * kPtRows + tid]));
+    if (mine && !dead) dead = !mbar_wait(bar(T_PVDONE + w), (uint32_t)(mine - 1) & 1u, &s_abort, limit);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const bool aborted = *(volatile int *)&s_abort != 0;
+  if (aborted && t == 0) flag_status(a.dev_status, ET_DEV_TIMEOUT);
+
+  // ---- the two groups' O, joined; thread = dim, each group takes half of the rows ----
+  const int real = min(kPtRows, a.N * a.G - rt * kPtRows);  // rows that exist are a prefix of the tile
+  const long long tile_id = (long long)b * ma.tiles_y + blockIdx.y;
+  auto place = [&](int r) -> long long {  // element index of row r in out
+    const int Rg = rt * kPtRows + r, i = Rg / a.G;
+    return (((long long)b * a.N + i) * a.Hq + g * a.G + (Rg - i * a.G)) * kPtD;
+  };
+  auto write_lse = [&](int r, float M, float sum) {
+    const int Rg = rt * kPtRows + r, i = Rg / a.G, h = g * a.G + (Rg - i * a.G);
+    if (a.lse) a.lse[((long long)b * a.Hq + h) * a.N + i] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+  };
+  if (warp >= 4) {
+    const int w = (warp - 4) >> 2, quarter = warp & 3, d = 32 * quarter + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    const float2 *ml = reinterpret_cast<const float2 *>(sm + kPtOffML);
+    const bool odd = tree && s_odd;
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const int q0 = 32 * w + 16 * part;
+      uint32_t o0[16], o1[16];
+      pt_ld16(lanes + kPtColO + (uint32_t)q0, o0);
+      pt_ld16(lanes + kPtColO + 64u + (uint32_t)q0, o1);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int q = q0 + e;
+        if (q >= real) continue;
+        const float2 x = ml[q], y = ml[kPtRows + q];
+        const float M = fmaxf(x.x, y.x), wx = ex2_fast(x.x - M), wy = ex2_fast(y.x - M);
+        const float sum = fmaf(x.y, wx, y.y * wy);
+        // a group without items left its columns unwritten
+        float v = (items > 0 ? __uint_as_float(o0[e]) * wx : 0.f) + (items > 1 ? __uint_as_float(o1[e]) * wy : 0.f);
+        if (odd) {
+          const unsigned long long *m = reinterpret_cast<const unsigned long long *>(sm + kPtOffMask) + 2 * q;
+          for (int k = 0; k < a.N; ++k) {
+            const float z = __bfloat162float(
+                static_cast<const __nv_bfloat16 *>(a.vt)[(((long long)b * a.N + k) * a.Hkv + g) * kPtD + d]);
+            if (!(fabsf(z) <= FLT_MAX) && ((m[k >> 6] >> (k & 63)) & 1ull)) v += z;
+          }
+        }
+        if (chunks == 1) {
+          static_cast<__nv_bfloat16 *>(a.out)[place(q) + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
+          if (d == 0) write_lse(q, M, sum);
+        } else {
+          const long long at = (tile_id * ma.S + chunk) * kPtRows + q;
+          reinterpret_cast<float *>(ma.part_o)[at * kPtD + d] = v;
+          if (d == 0) ma.part_ml[at] = make_float2(M, sum);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  __syncwarp();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPtTmemCols) : "memory");
+  if (chunks == 1) return;
+  // ---- the chunks' rows, merged by the last block to arrive ----
+  if (!arrive_last(ma.cnt + tile_id, (unsigned)chunks, &s_last)) return;
+  merge_chunks<kPtD, kPtRows, kPtThreads>(ma, tile_id, chunks, real, sm, [&](int r, int c, const float4 &v, float M, float sum) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint2 u;
+    u.x = pack_bf16x2(v.x * inv, v.y * inv);
+    u.y = pack_bf16x2(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + place(r) + 4 * c) = u;
+    if (c == 0) write_lse(r, M, sum);
+  });
+}
+
+}  // namespace
+
+bool make_page_map(CUtensorMap *m, const void *base, const et_paged_cache *c, int box) {
+  const cuuint64_t dims[4] = {(cuuint64_t)c->d, (cuuint64_t)c->page_size, (cuuint64_t)c->Hkv, (cuuint64_t)c->num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c->d, (cuuint64_t)c->d * c->page_size, (cuuint64_t)c->page_stride};
+  const cuuint32_t boxes[4] = {(cuuint32_t)c->d, (cuuint32_t)box, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, boxes, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+et_status paged_tc_launch(const et_paged_cache *cache, const PagedSplitArgs &args, cudaStream_t stream) {
+  PagedSplitArgs ma = args;
+  ma.box = cache->page_size % 128 == 0 ? 128 : cache->page_size % 64 == 0 ? 64 : cache->page_size % 32 == 0 ? 32 : 16;
+  CUtensorMap mk, mv;
+  if (!make_page_map(&mk, cache->k_pages, cache, ma.box) || !make_page_map(&mv, cache->v_pages, cache, ma.box))
+    return ET_ERR_INVALID_ARG;
+  const dim3 grid(ma.S, ma.tiles_y, ma.a.B);
+  if (cache->format == ET_KV_E4M3) {
+    if (et_smem_attr((const void *)k_paged_attn_tc<ET_KV_E4M3>, (int)kPtBytes) != cudaSuccess) return ET_ERR_CUDA;
+    return et_launch(k_paged_attn_tc<ET_KV_E4M3>, grid, dim3(kPtThreads), kPtBytes, stream, 0, mk, mv, ma);
+  }
+  if (et_smem_attr((const void *)k_paged_attn_tc<ET_KV_E5M2>, (int)kPtBytes) != cudaSuccess) return ET_ERR_CUDA;
+  return et_launch(k_paged_attn_tc<ET_KV_E5M2>, grid, dim3(kPtThreads), kPtBytes, stream, 0, mk, mv, ma);
+}
+
+}  // namespace et

@@ -1,0 +1,122 @@
+// Shared by the paged attention's kernels: their arguments, the merge of the
+// chunks a prefix is split into, and small helpers.  Not part of the C ABI.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "et_attn_internal.h"
+#include "et_paged.cuh"
+#include "et_tc.cuh"
+
+namespace et {
+
+struct PagedAttnArgs {
+  int B, N, Hq, Hkv, G, P, max_blocks, W, max_prefix;
+  float scale_log2;  // scale * log2(e)
+  long long num_pages, page_stride;
+  const uint8_t *k_pages, *v_pages;
+  const float *k_scale, *v_scale;
+  const int32_t *block_table, *prefix_len;
+  const void *q, *kt, *vt;
+  const unsigned long long *mask;
+  void *out;
+  float *lse;
+  int32_t *dev_status;
+};
+
+// A call whose prefixes are split into chunks.
+struct PagedSplitArgs {
+  PagedAttnArgs a;
+  int S, tiles_y;       // chunks, Hkv * row tiles
+  int row_tiles;        // row tiles per KV head
+  int box;              // rows per TMA box
+  int min_tiles;        // smallest chunk, in tiles
+  unsigned int *cnt;    // [B * tiles_y] arrival counters
+  float2 *part_ml;      // [B * tiles_y][S][R] (maximum, sum)
+  float4 *part_o;       // [B * tiles_y][S][R][D] fp32
+  long long wait_cycles;
+};
+
+// D = 128, many rows per KV head (et_paged_attention_tc.cu)
+constexpr int kPtKeys = 128;  // keys per tile
+constexpr int kPtRows = 64;   // query rows per block
+// pages as [num_pages][Hkv][P][d] bytes; a box is `box` rows of one head of one page
+ET_HIDDEN bool make_page_map(CUtensorMap *m, const void *base, const et_paged_cache *c, int box);
+ET_HIDDEN et_status paged_tc_launch(const et_paged_cache *cache, const PagedSplitArgs &a, cudaStream_t stream);
+
+namespace {
+
+constexpr int kPaMaxSplits = 64;
+constexpr float kPaTop = 7.f, kPaSlack = 8.f;  // weights lie below 2^kPaTop when the maximum moves, below 2^15 always
+
+// prefix length of sequence b as the kernels use it: -1 = no sequence here
+__device__ __forceinline__ int paged_prefix(const PagedAttnArgs &a, int b, int &bad) {
+  int L = a.prefix_len[b];
+  const long long room = min((long long)a.max_prefix, (long long)a.max_blocks * a.P);
+  if (L > room) {
+    bad = 1;
+    L = (int)room;
+  }
+  return L < 0 ? -1 : L;
+}
+__device__ __forceinline__ float clamp_v_scale(float s) {
+  return fminf(fmaxf(s, 1.f / (1ll << kScaleExp)), (float)(1ll << kScaleExp));  // NaN -> the smallest
+}
+__device__ __forceinline__ bool tree_keeps(const PagedAttnArgs &a, int b, int i, int tt) {
+  if (!a.mask) return tt <= i;
+  return (a.mask[((long long)b * a.N + i) * a.W + (tt >> 6)] >> (tt & 63)) & 1ull;
+}
+
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The rows of a tile's chunks, from the workspace, weighted by their maxima:
+// run by the last block of the tile to arrive (NT threads, `sm` free shared
+// memory).  Every load of a row's parts is in flight before any arithmetic.
+template <int D, int R, int NT, typename Write>
+__device__ __forceinline__ void merge_chunks(const PagedSplitArgs &ma, long long tile_id, int chunks, int real,
+                                             unsigned char *sm, Write write_row) {
+  const int t = threadIdx.x;
+  const long long base = tile_id * ma.S * R;
+  float2 *pair = reinterpret_cast<float2 *>(sm);  // [chunks][real]: (maximum, sum), then (weight, -)
+  float2 *stat = pair + kPaMaxSplits * R;         // [real]: the row's maximum and sum
+  for (int x = t; x < chunks * real; x += NT) {
+    const int k = x / real, r = x - k * real;
+    pair[x] = __ldcg(&ma.part_ml[base + (long long)k * R + r]);
+  }
+  __syncthreads();
+  for (int r = t; r < real; r += NT) {
+    float M = pair[r].x, sum = 0.f;
+    for (int k = 1; k < chunks; ++k) M = fmaxf(M, pair[k * real + r].x);
+    for (int k = 0; k < chunks; ++k) {
+      const float w = ex2_fast(pair[k * real + r].x - M);
+      sum = fmaf(pair[k * real + r].y, w, sum);
+      pair[k * real + r].x = w;
+    }
+    stat[r] = make_float2(M, sum);
+  }
+  __syncthreads();
+  for (int x = t; x < real * (D / 4); x += NT) {
+    const int r = x / (D / 4), c = x - r * (D / 4);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < chunks; k0 += 8) {
+      float4 y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        y[j] = k0 + j < chunks ? __ldcg(&ma.part_o[(base + (long long)(k0 + j) * R + r) * (D / 4) + c])
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w = k0 + j < chunks ? pair[(k0 + j) * real + r].x : 0.f;
+        v.x = fmaf(y[j].x, w, v.x); v.y = fmaf(y[j].y, w, v.y); v.z = fmaf(y[j].z, w, v.z); v.w = fmaf(y[j].w, w, v.w);
+      }
+    }
+    write_row(r, c, v, stat[r].x, stat[r].y);
+  }
+}
+
+}  // namespace
+}  // namespace et
