@@ -59,10 +59,10 @@ constexpr uint32_t kPtOffTreeK = kPtOffP;                    // K tree, bf16, tw
 constexpr uint32_t kPtOffTreeV = kPtOffVH;                   // V tree, bf16, as V16 buffer 0
 constexpr uint32_t kPtOffTreeQ = kPtOffVH + kPtTile16;       // q, bf16, two halves of 64 rows
 // TMEM columns
-constexpr uint32_t kPtColS = 0, kPtColO = 256, kPtTmemCols = 512;
+constexpr uint32_t kPtColS = 0, kPtColO = 384, kPtTmemCols = 512;  // three score buffers, two O
 
-enum { T_KFULL = 0, T_KEMPTY = 3, T_VFULL = 6, T_VEMPTY = 9, T_SFULL = 12, T_SFREE = 14, T_PFULL = 16, T_VHFULL = 18,
-       T_PVDONE = 20, T_TREE = 22, T_DRAIN = 23, T_COUNT = 24 };
+enum { T_KFULL = 0, T_KEMPTY = 3, T_VFULL = 6, T_VEMPTY = 9, T_SFULL = 12, T_SFREE = 15, T_PFULL = 18, T_VHFULL = 20,
+       T_PVDONE = 22, T_TREE = 24, T_DRAIN = 25, T_COUNT = 26 };
 
 // instruction descriptors: fp32 sums (bits 4-5 = 1), A type in bits 7-9, B
 // type in 10-12, A / B stored MN-major in bits 15 / 16, N >> 3, M >> 4
@@ -336,9 +336,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       constexpr uint32_t iS = pt_idesc(FMT == ET_KV_E4M3 ? 0 : 1, 0, false, false, 128, 128);
       constexpr uint32_t iSt = pt_idesc(1, 1, false, false, 128, 64);
       constexpr uint32_t iO = pt_idesc(0, 0, true, true, 128, 64), iOt = pt_idesc(1, 1, true, true, 128, 64);
-      auto scores = [&](int i) -> bool {  // item i into S buffer i & 1
-        const uint32_t d = tmem + kPtColS + 128u * (uint32_t)(i & 1);
-        if (i >= 2 && !mbar_wait(bar(T_SFREE + (i & 1)), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit)) return false;
+      auto scores = [&](int i) -> bool {  // item i into S buffer i % 3
+        const int buf = i % 3;
+        const uint32_t d = tmem + kPtColS + 128u * (uint32_t)buf;
+        if (i >= 3 && !mbar_wait(bar(T_SFREE + buf), (uint32_t)(i / 3 - 1) & 1u, &s_abort, limit)) return false;
         if (tree && i == 0) {
           tc_fence_after();
 #pragma unroll
@@ -356,12 +357,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                       sw128_desc(sb + kPtOffQ + kk * 32, 16, 1024), iS, kk > 0);
           if (j + kPtStages < n) tc_commit(bar(T_KEMPTY + stage));
         }
-        tc_commit(bar(T_SFULL + (i & 1)));
+        tc_commit(bar(T_SFULL + buf));
         return true;
       };
-      bool ok = scores(0);
+      bool ok = scores(0) && (items < 2 || scores(1));
       for (int i = 0; ok && i < items; ++i) {
-        if (i + 1 < items && !scores(i + 1)) break;
+        if (i + 2 < items && !scores(i + 2)) break;  // two ahead: a group finds its next scores when it has stored its weights
         const int w = i & 1;
         const uint32_t phase = (uint32_t)(i >> 1) & 1u;
         if (!mbar_wait(bar(T_VHFULL + w), phase, &s_abort, limit) || !mbar_wait(bar(T_PFULL + w), phase, &s_abort, limit)) break;
@@ -393,38 +394,37 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const uint32_t units = *(volatile uint32_t *)&s_units[stage];
         const int lim = L - (t0 + j) * kPtKeys;  // rows past it hold no key of this sequence
         const uint32_t src = sb + kPtOffV + stage * kPtTile8, dst = sb + kPtOffVH + w * kPtTile16;
-        const int c = ct & 7, swap = c >> 2;
+        // 16 codes of a row a thread; the row's place in its group of eight is the thread's own, so addresses advance
+        // by whole groups.  Dims 16 c .. + 15 are two 16-byte chunks of half c / 4; the lanes of the upper half store
+        // them in the other order, which keeps the stores free of bank conflicts
+        const int c = ct & 7, r7 = ct >> 3, c0 = 2 * (c & 3);
+        const bool swap = c >= 4;
+        const uint32_t from = src + sw128(r7, c), half = dst + (uint32_t)((c >> 2) * kPtHalf16);
+        const uint32_t to0 = half + sw128(r7, swap ? c0 + 1 : c0), to1 = half + sw128(r7, swap ? c0 : c0 + 1);
+        const bool whole = lim >= kPtKeys && units == 0xffu;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint4 v[8];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint4 v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = (ct >> 3) + 8 * (4 * h + k);
+          for (int k = 0; k < 8; ++k)
             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(src + sw128(r, c)));
+                         : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(from + 8192u * h + 1024u * k));
+          if (!whole) {  // whatever lies in rows without a key must not meet a zero weight
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = r7 + 8 * (8 * h + k);
+              if (r >= lim || !((units >> (r >> 4)) & 1u)) v[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = (ct >> 3) + 8 * (4 * h + k);
+          for (int k = 0; k < 8; ++k) {
             uint32_t x[8];
-            f8x4_to_f16<FMT>(v[k].x, x[0], x[1]);
-            f8x4_to_f16<FMT>(v[k].y, x[2], x[3]);
-            f8x4_to_f16<FMT>(v[k].z, x[4], x[5]);
-            f8x4_to_f16<FMT>(v[k].w, x[6], x[7]);
-            if (r >= lim || !((units >> (r >> 4)) & 1u)) {  // whatever lies there must not meet a zero weight
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = 0u;
-            }
-            // dims 16 c .. + 15: two 16-byte chunks of half c / 4; the upper half's lanes store them in the other order
-            const uint32_t base = dst + (uint32_t)((c >> 2) * kPtHalf16);
-            const int c0 = 2 * (c & 3);
-            if (swap) {
-              sts128(base + sw128(r, c0 + 1), x[4], x[5], x[6], x[7]);
-              sts128(base + sw128(r, c0), x[0], x[1], x[2], x[3]);
-            } else {
-              sts128(base + sw128(r, c0), x[0], x[1], x[2], x[3]);
-              sts128(base + sw128(r, c0 + 1), x[4], x[5], x[6], x[7]);
-            }
+            f8x4_to_f16<FMT>(swap ? v[k].z : v[k].x, x[0], x[1]);
+            f8x4_to_f16<FMT>(swap ? v[k].w : v[k].y, x[2], x[3]);
+            f8x4_to_f16<FMT>(swap ? v[k].x : v[k].z, x[4], x[5]);
+            f8x4_to_f16<FMT>(swap ? v[k].y : v[k].w, x[6], x[7]);
+            sts128(to0 + 8192u * h + 1024u * k, x[0], x[1], x[2], x[3]);
+            sts128(to1 + 8192u * h + 1024u * k, x[4], x[5], x[6], x[7]);
           }
         }
         fence_async_smem();
@@ -491,8 +491,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
       }
       const bool masked = __any_sync(0xffffffffu, (keep[0] & keep[1]) != 0xffffffffu);
-      const uint32_t phase = (uint32_t)(i >> 1) & 1u;
-      if (!dead) dead = !mbar_wait(bar(T_SFULL + w), phase, &s_abort, limit);
+      const int buf = i % 3;
+      if (!dead) dead = !mbar_wait(bar(T_SFULL + buf), (uint32_t)(i / 3) & 1u, &s_abort, limit);
       dead = __any_sync(0xffffffffu, dead);
       tc_fence_after();
 #pragma unroll
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           uint32_t hi[16], lo[16];
-          const uint32_t col = lanes + kPtColS + 128u * (uint32_t)w + (uint32_t)(32 * half + 16 * part);
+          const uint32_t col = lanes + kPtColS + 128u * (uint32_t)buf + (uint32_t)(32 * half + 16 * part);
           pt_ld16(col, hi);
           pt_ld16(col + 64, lo);
           tmem_wait_ld();
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           if (half == 1 && part == 1) {  // S is free once it sits in registers
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(T_SFREE + w));
+            if (lane == 0) mbar_arrive(bar(T_SFREE + buf));
           }
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
@@ -655,43 +655,62 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int Rg = rt * kPtRows + r, i = Rg / a.G, h = g * a.G + (Rg - i * a.G);
     if (a.lse) a.lse[((long long)b * a.Hq + h) * a.N + i] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
   };
+  // factors of the two groups' sums and the row's place, per row (short loops: cold code runs at the speed of its fetch)
+  float2 *mix = reinterpret_cast<float2 *>(sm + kPtOffAdj);
+  long long *to = reinterpret_cast<long long *>(sm + kPtOffRed);
+  if (t < real) {
+    const float2 *ml = reinterpret_cast<const float2 *>(sm + kPtOffML);
+    const float2 x = ml[t], y = ml[kPtRows + t];
+    const float M = fmaxf(x.x, y.x), wx = ex2_fast(x.x - M), wy = ex2_fast(y.x - M), sum = fmaf(x.y, wx, y.y * wy);
+    if (chunks == 1) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      mix[t] = make_float2(wx * inv, wy * inv);
+      to[t] = place(t);
+      write_lse(t, M, sum);
+    } else {
+      const long long at = (tile_id * ma.S + chunk) * kPtRows + t;
+      mix[t] = make_float2(wx, wy);
+      to[t] = at * kPtD;
+      ma.part_ml[at] = make_float2(M, sum);
+    }
+  }
+  __syncthreads();
   if (warp >= 4) {
     const int w = (warp - 4) >> 2, quarter = warp & 3, d = 32 * quarter + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-    const float2 *ml = reinterpret_cast<const float2 *>(sm + kPtOffML);
-    const bool odd = tree && s_odd;
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const int q0 = 32 * w + 16 * part;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + kPtColO;
+    const bool odd = tree && s_odd, two = items > 1;  // a group without items left its columns unwritten
+#pragma unroll 1
+    for (int q0 = 32 * w; q0 < min(real, 32 * w + 32); q0 += 16) {
       uint32_t o0[16], o1[16];
-      pt_ld16(lanes + kPtColO + (uint32_t)q0, o0);
-      pt_ld16(lanes + kPtColO + 64u + (uint32_t)q0, o1);
+      pt_ld16(lanes + (uint32_t)q0, o0);
+      pt_ld16(lanes + 64u + (uint32_t)q0, o1);
       tmem_wait_ld();
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int q = q0 + e;
-        if (q >= real) continue;
-        const float2 x = ml[q], y = ml[kPtRows + q];
-        const float M = fmaxf(x.x, y.x), wx = ex2_fast(x.x - M), wy = ex2_fast(y.x - M);
-        const float sum = fmaf(x.y, wx, y.y * wy);
-        // a group without items left its columns unwritten
-        float v = (items > 0 ? __uint_as_float(o0[e]) * wx : 0.f) + (items > 1 ? __uint_as_float(o1[e]) * wy : 0.f);
-        if (odd) {
-          const unsigned long long *m = reinterpret_cast<const unsigned long long *>(sm + kPtOffMask) + 2 * q;
-          for (int k = 0; k < a.N; ++k) {
-            const float z = __bfloat162float(
-                static_cast<const __nv_bfloat16 *>(a.vt)[(((long long)b * a.N + k) * a.Hkv + g) * kPtD + d]);
-            if (!(fabsf(z) <= FLT_MAX) && ((m[k >> 6] >> (k & 63)) & 1ull)) v += z;
-          }
+        const float2 f = mix[q0 + e];
+        o0[e] = __float_as_uint(__uint_as_float(o0[e]) * f.x + (two ? __uint_as_float(o1[e]) * f.y : 0.f));
+      }
+      if (odd) {
+#pragma unroll 1
+        for (int k = 0; k < a.N; ++k) {
+          const float z = __bfloat162float(
+              static_cast<const __nv_bfloat16 *>(a.vt)[(((long long)b * a.N + k) * a.Hkv + g) * kPtD + d]);
+          if (fabsf(z) <= FLT_MAX) continue;
+          const unsigned long long *m = reinterpret_cast<const unsigned long long *>(sm + kPtOffMask) + (k >> 6);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if ((m[2 * (q0 + e)] >> (k & 63)) & 1ull) o0[e] = __float_as_uint(__uint_as_float(o0[e]) + z);
         }
-        if (chunks == 1) {
-          static_cast<__nv_bfloat16 *>(a.out)[place(q) + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
-          if (d == 0) write_lse(q, M, sum);
-        } else {
-          const long long at = (tile_id * ma.S + chunk) * kPtRows + q;
-          reinterpret_cast<float *>(ma.part_o)[at * kPtD + d] = v;
-          if (d == 0) ma.part_ml[at] = make_float2(M, sum);
-        }
+      }
+      if (chunks == 1) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (q0 + e < real)
+            static_cast<__nv_bfloat16 *>(a.out)[to[q0 + e] + d] = __float2bfloat16_rn(__uint_as_float(o0[e]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (q0 + e < real) reinterpret_cast<float *>(ma.part_o)[to[q0 + e] + d] = __uint_as_float(o0[e]);
       }
     }
   }
