@@ -13,27 +13,32 @@
 // not exist; the softmax runs one key per thread, and a tile of a page's
 // codes needs no conversion before the scores.
 //
-// One block per SM, twelve warps:
+// One block per SM, twenty warps:
 //   warp 0      TMA: a 128-key tile of K and of V, into rings of 3
 //   warp 1      owns 512 columns of TMEM, issues every product
 //   warps 2, 3  V's codes -> fp16 (two buffers)
-//   warps 4-7, 8-11  two softmax groups on alternate tiles, each with its own
-//               scores, weights, running maximum and O in TMEM: independent
-//               online softmaxes, joined at the end.
+//   warps 4-11, 12-19  two softmax groups on alternate tiles, each with its
+//               own weights, running maximum and O in TMEM: independent
+//               online softmaxes, joined at the end.  A thread has one key
+//               and half of the rows.
 // A weight's reference moves only when some weight would pass 2^15 (one vote
-// per 32 rows in place of a maximum over the lanes); the slow path finds the
+// of the group in place of a maximum over the lanes); the slow path finds the
 // maxima, and rescales the group's sums and O.  The tree's own rows are one
 // more tile in bf16, staged by all warps before the roles part.
 // Bounds: K8 and V8 through shared memory and V16 written and read again make
 // shared-memory traffic (about 1400 cycles a tile at 128 bytes a cycle) the
 // next limit after HBM (1365 cycles a tile).  Every mbarrier wait is bounded:
 // a block that gives up sets ET_DEV_TIMEOUT, drains what it issued and leaves.
+#include <type_traits>
+
 #include "et_paged_attn.cuh"
 
 namespace et {
 namespace {
 
-constexpr int kPtThreads = 384;
+constexpr int kPtThreads = 640;
+constexpr int kPtGroup = 256;   // threads of a softmax group
+constexpr int kPtQ = kPtRows / 2;  // rows per softmax thread
 constexpr int kPtD = 128;
 constexpr int kPtStages = 3;
 constexpr int kPtConvWarps = 2;
@@ -76,6 +81,11 @@ __device__ __forceinline__ void pt_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
       : "memory");
 }
+__device__ __forceinline__ void pt_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void pt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
@@ -90,18 +100,41 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
-// OR of a condition over a softmax group's 128 threads, and a barrier
+// OR of a condition over a softmax group's threads, and a barrier
 __device__ __forceinline__ bool group_any(int group, bool p) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"(1 + group), "r"(p ? 1u : 0u)
       : "memory");
   return r != 0u;
 }
 __device__ __forceinline__ void group_sync(int group) {
-  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
+  asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + group) : "memory");
+}
+// mbar_wait without a call: the warps that wait hold most of their registers live
+__device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile int *abort, long long limit) {
+  if (mbar_try(bar, parity)) return true;
+  const long long start = clock64();
+  auto parked = [&]() -> bool {  // parked by the hardware up to 2 us at a time: a spinning warp takes issue slots
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0u;
+  };
+#pragma unroll 1
+  while (!parked()) {
+    if (*abort) return false;
+    if (clock64() - start > limit) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
 }
 // chunk c (16 bytes) of row r in a tile of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
@@ -132,7 +165,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     for (int i = 0; i < T_COUNT; ++i) {
       int count = 1;
       if (i >= T_VEMPTY && i < T_SFULL) count = kPtConvWarps;
-      if (i >= T_SFREE && i < T_VHFULL) count = 4;
+      if (i >= T_SFREE && i < T_VHFULL) count = kPtGroup / 32;
       if (i >= T_VHFULL && i < T_PVDONE) count = kPtConvWarps;
       mbar_init(bar(i), (uint32_t)count);
     }
@@ -219,17 +252,54 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     for (int j = 0; j < n && j < kPtStages; ++j) issue(j);
   }
 
-  // ---- q: two e4m3 terms, K-major; 16 lanes a row, eight dims a lane ----
+  // ---- q and, in the block that takes it, the tree's rows: every load in flight first ----
+  constexpr int kQRounds = (kPtRows * 16 + kPtThreads - 1) / kPtThreads, kTreeRounds = 2;
+  const __nv_bfloat16 *KT = static_cast<const __nv_bfloat16 *>(a.kt), *VT = static_cast<const __nv_bfloat16 *>(a.vt);
+  const int tree_cells = tree ? ((a.N + 15) & ~15) * 16 : 0;  // 16-byte cells, rows in whole k-steps of 16 keys
+  auto tree_cell = [&](int x, uint4 &k, uint4 &v) {
+    const int r = x >> 4;
+    k = v = make_uint4(0u, 0u, 0u, 0u);
+    if (x < tree_cells && r < a.N) {
+      const long long at = (((long long)b * a.N + r) * a.Hkv + g) * kPtD + 8 * (x & 15);
+      k = *reinterpret_cast<const uint4 *>(KT + at);
+      v = *reinterpret_cast<const uint4 *>(VT + at);
+    }
+  };
   float2 *fc = reinterpret_cast<float2 *>(sm + kPtOffFC);
+  bool odd_v = false;
+  auto store_cell = [&](int x, const uint4 &k, const uint4 &v) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // NaN and infinities would reach rows that do not attend their key (0 * inf): they are added at the end
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; odd_v = true; }
+      if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; odd_v = true; }
+    }
+    const uint32_t at = (uint32_t)(((x & 15) >> 3) * kPtHalf16) + sw128(x >> 4, x & 7);
+    sts128(sb + kPtOffTreeK + at, k.x, k.y, k.z, k.w);
+    sts128(sb + kPtOffTreeV + at, w[0], w[1], w[2], w[3]);
+  };
   {
     const int lr = t & 15;
-    for (int r = t >> 4; r < kPtRows; r += kPtThreads / 16) {
-      const int Rg = rt * kPtRows + r, i = Rg / a.G;
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (i < a.N)
-        raw = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                               (((long long)b * a.N + i) * a.Hq + g * a.G + (Rg - i * a.G)) * kPtD + 8 * lr);
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint4 raw[kQRounds], tk[kTreeRounds], tv[kTreeRounds];
+#pragma unroll
+    for (int k = 0; k < kQRounds; ++k) {
+      const int r = (t >> 4) + k * (kPtThreads / 16), Rg = rt * kPtRows + r, i = Rg / a.G;
+      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < kPtRows && i < a.N)
+        raw[k] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                  (((long long)b * a.N + i) * a.Hq + g * a.G + (Rg - i * a.G)) * kPtD + 8 * lr);
+    }
+    if (tree) {
+#pragma unroll
+      for (int k = 0; k < kTreeRounds; ++k) tree_cell(t + k * kPtThreads, tk[k], tv[k]);
+    }
+    // two e4m3 terms, K-major; 16 lanes a row, eight dims a lane
+#pragma unroll
+    for (int k = 0; k < kQRounds; ++k) {
+      const int r = (t >> 4) + k * (kPtThreads / 16);
+      if (r >= kPtRows) break;  // whole warps
+      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
       uint32_t top = 0u;  // the row's largest magnitude, as the bits of a bf16 value: they order like the values
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
@@ -262,31 +332,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         fc[r] = make_float2(tree ? a.scale_log2 : f, 0.f);  // group 0 takes the tree's tile first: q as it is
       }
     }
-  }
-  if (tree) {  // ---- the tree's rows: K as keys x dims, V as keys x dims, 16 bytes a thread at a time ----
-    const __nv_bfloat16 *KT = static_cast<const __nv_bfloat16 *>(a.kt), *VT = static_cast<const __nv_bfloat16 *>(a.vt);
-    const int rows = (a.N + 15) & ~15;
-    bool odd = false;
-    for (int x = t; x < rows * 16; x += kPtThreads) {
-      const int r = x >> 4, c = x & 15;
-      uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
-      if (r < a.N) {
-        const long long at = (((long long)b * a.N + r) * a.Hkv + g) * kPtD + 8 * c;
-        k = *reinterpret_cast<const uint4 *>(KT + at);
-        v = *reinterpret_cast<const uint4 *>(VT + at);
-      }
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      // NaN and infinities would reach rows that do not attend their key (0 * inf): they are added at the end
+    if (tree) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; odd = true; }
-        if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; odd = true; }
-      }
-      const uint32_t at = (uint32_t)((c >> 3) * kPtHalf16) + sw128(r, c & 7);
-      sts128(sb + kPtOffTreeK + at, k.x, k.y, k.z, k.w);
-      sts128(sb + kPtOffTreeV + at, w[0], w[1], w[2], w[3]);
+      for (int k = 0; k < kTreeRounds; ++k)
+        if (t + k * kPtThreads < tree_cells) store_cell(t + k * kPtThreads, tk[k], tv[k]);
     }
-    if (odd) s_odd = 1;
+  }
+  if (tree) {
+#pragma unroll 1
+    for (int x = t + kTreeRounds * kPtThreads; x < tree_cells; x += kPtThreads) {
+      uint4 k, v;
+      tree_cell(x, k, v);
+      store_cell(x, k, v);
+    }
+    if (odd_v) s_odd = 1;
     if (t < kPtRows) {
       const int i = (rt * kPtRows + t) / a.G;
       unsigned long long m0 = 0ull, m1 = 0ull;
@@ -319,7 +378,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       if ((j & 3) == 0) fetch_pages(j);
       const int stage = j % kPtStages;
       const uint32_t phase = (uint32_t)(j / kPtStages - 1) & 1u;
-      ok = mbar_wait(bar(T_KEMPTY + stage), phase, &s_abort, limit) && mbar_wait(bar(T_VEMPTY + stage), phase, &s_abort, limit);
+      ok = pt_wait(bar(T_KEMPTY + stage), phase, &s_abort, limit) && pt_wait(bar(T_VEMPTY + stage), phase, &s_abort, limit);
       if (!__all_sync(0xffffffffu, ok)) break;
       issue(j);
       issued = j + 1;
@@ -339,7 +398,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       auto scores = [&](int i) -> bool {  // item i into S buffer i % 3
         const int buf = i % 3;
         const uint32_t d = tmem + kPtColS + 128u * (uint32_t)buf;
-        if (i >= 3 && !mbar_wait(bar(T_SFREE + buf), (uint32_t)(i / 3 - 1) & 1u, &s_abort, limit)) return false;
+        if (i >= 3 && !pt_wait(bar(T_SFREE + buf), (uint32_t)(i / 3 - 1) & 1u, &s_abort, limit)) return false;
         if (tree && i == 0) {
           tc_fence_after();
 #pragma unroll
@@ -349,7 +408,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           tc_commit(bar(T_TREE));
         } else {
           const int j = i - tree, stage = j % kPtStages;
-          if (!mbar_wait(bar(T_KFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit)) return false;
+          if (!pt_wait(bar(T_KFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit)) return false;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -365,7 +424,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (i + 2 < items && !scores(i + 2)) break;  // two ahead: a group finds its next scores when it has stored its weights
         const int w = i & 1;
         const uint32_t phase = (uint32_t)(i >> 1) & 1u;
-        if (!mbar_wait(bar(T_VHFULL + w), phase, &s_abort, limit) || !mbar_wait(bar(T_PFULL + w), phase, &s_abort, limit)) break;
+        if (!pt_wait(bar(T_VHFULL + w), phase, &s_abort, limit) || !pt_wait(bar(T_PFULL + w), phase, &s_abort, limit)) break;
         tc_fence_after();
         const bool is_tree = tree && i == 0;
         const int steps = is_tree ? (a.N + 15) >> 4 : kPtKeys / 16;
@@ -387,9 +446,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const int w = i & 1;
       if (!(tree && i == 0)) {
         const int j = i - tree, stage = j % kPtStages;
-        if (i >= 2) ok = mbar_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
-        else if (tree) ok = mbar_wait(bar(T_TREE), 0, &s_abort, limit);  // q of the tree's scores lies in this buffer
-        ok = ok && mbar_wait(bar(T_VFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit);
+        if (i >= 2) ok = pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
+        else if (tree) ok = pt_wait(bar(T_TREE), 0, &s_abort, limit);  // q of the tree's scores lies in this buffer
+        ok = ok && pt_wait(bar(T_VFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t units = *(volatile uint32_t *)&s_units[stage];
         const int lim = L - (t0 + j) * kPtKeys;  // rows past it hold no key of this sequence
@@ -438,205 +497,193 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
     }
   } else {
-    // ---------------- softmax: group w, one key per thread ----------------
-    const int w = (warp - 4) >> 2, quarter = warp & 3, tid = t & 127;  // warps 4-7 and 8-11: threads 128.. and 256..
-    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-    const uint32_t fcb = sb + kPtOffFC + (uint32_t)(w * kPtRows * 8), prow = sb + kPtOffP + (uint32_t)(w * kPtP);
+    // ---------------- softmax: group w, one key and half of the rows per thread ----------------
+    const int w = (warp - 4) >> 3, quarter = warp & 3, col = ((warp - 4) >> 2) & 1, tid = 32 * quarter + lane;
+    const int gt = t - 128 - kPtGroup * w, r0 = kPtQ * col;  // thread of the group; first of its rows
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)r0;
+    const uint32_t fcb = sb + kPtOffFC + (uint32_t)((w * kPtRows + r0) * 8), prow = sb + kPtOffP + (uint32_t)(w * kPtP);
     float *red = reinterpret_cast<float *>(sm + kPtOffRed) + w * 4 * kPtRows;
     float2 *adj = reinterpret_cast<float2 *>(sm + kPtOffAdj) + w * kPtRows;
-    float l[kPtRows];
+    float l[kPtQ];
 #pragma unroll
-    for (int q = 0; q < kPtRows; ++q) l[q] = 0.f;
+    for (int q = 0; q < kPtQ; ++q) l[q] = 0.f;
     bool dead = false;
-    bool fresh[2] = {true, true};  // some row of the half has no reference yet (the same in the whole group)
-    bool mine_fresh = true;        // threads 0..63: row tid has none
+    bool fresh = true;       // some row has no reference yet (the same in the whole group)
+    bool mine_fresh = true;  // threads 0..63 of the group: row gt has none
     // a key's page and scales, fetched an item ahead
     auto my_page = [&](int i) -> int {
       const int j = i - tree;
       const long long key = (long long)(t0 + j) * kPtKeys + tid;
       if (i >= items || j < 0 || key >= L) return -1;
-      const int p = a.block_table[(long long)b * a.max_blocks + (int)key / a.P];
-      return p < 0 || p >= a.num_pages ? -1 : p;
+      return a.block_table[(long long)b * a.max_blocks + (int)key / a.P];  // checked where it is used: no wait here
     };
+    auto real_page = [&](int p) -> bool { return p >= 0 && p < a.num_pages; };
     auto my_scale = [&](int p, float &ks, float &vs) {
       ks = 0.f;
       vs = 1.f;
-      if (p >= 0) {
+      if (real_page(p)) {
         ks = a.k_scale[(long long)p * a.Hkv + g];
-        vs = clamp_v_scale(a.v_scale[(long long)p * a.Hkv + g]);
+        vs = a.v_scale[(long long)p * a.Hkv + g];
       }
     };
     int page_n = my_page(w);
     float ks_n, vs_n;
     my_scale(page_n, ks_n, vs_n);
-    for (int i = w; i < items; i += 2) {
-      const bool is_tree = tree && i == 0;
-      const bool there = is_tree ? tid < a.N : page_n >= 0;
-      const float ks = is_tree ? 1.f : ks_n, vs = is_tree ? 1.f : vs_n;
-      const float lv = __log2f(vs), iv = __frcp_rn(vs);
+    // one item; the tree's tile (group 0's first) is compiled apart, which keeps its choices out of the others
+    auto item = [&](int i, auto is_tree_) {
+      constexpr bool is_tree = decltype(is_tree_)::value;
+      const bool there = is_tree ? tid < a.N : real_page(page_n);
+      const float ks = is_tree ? 1.f : ks_n, vs = is_tree ? 1.f : clamp_v_scale(vs_n);
+      const float lv = is_tree ? 0.f : __log2f(vs), iv = is_tree ? 1.f : __frcp_rn(vs);
       page_n = my_page(i + 2);
-      // bit q: row q attends this thread's key
-      uint32_t keep[2] = {there ? 0xffffffffu : 0u, there ? 0xffffffffu : 0u};
+      uint32_t keep = 0u;  // the tree's tile, bit q: row r0 + q attends this thread's key
       if (is_tree && there) {
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t bits = 0u;
 #pragma unroll 4
-          for (int q = 0; q < 32; ++q) {
-            const unsigned long long m =
-                *(reinterpret_cast<const unsigned long long *>(sm + kPtOffMask) + 2 * (32 * h + q) + (tid >> 6));
-            bits |= (uint32_t)((m >> (tid & 63)) & 1ull) << q;
-          }
-          if (h == 0) keep[0] = bits; else keep[1] = bits;
+        for (int q = 0; q < kPtQ; ++q) {
+          const unsigned long long m =
+              *(reinterpret_cast<const unsigned long long *>(sm + kPtOffMask) + 2 * (r0 + q) + (tid >> 6));
+          keep |= (uint32_t)((m >> (tid & 63)) & 1ull) << q;
         }
       }
-      const bool masked = __any_sync(0xffffffffu, (keep[0] & keep[1]) != 0xffffffffu);
+      const float cap = there ? INFINITY : -INFINITY;
       const int buf = i % 3;
-      if (!dead) dead = !mbar_wait(bar(T_SFULL + buf), (uint32_t)(i / 3) & 1u, &s_abort, limit);
+      if (!dead) dead = !pt_wait(bar(T_SFULL + buf), (uint32_t)(i / 3) & 1u, &s_abort, limit);
       dead = __any_sync(0xffffffffu, dead);
       tc_fence_after();
+      float x[kPtQ];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x[32];
+      for (int part = 0; part < kPtQ / 8; ++part) {
+        uint32_t hi[8], lo[8];
+        pt_ld8(lanes + kPtColS + 128u * (uint32_t)buf + 8u * part, hi);
+        if (!is_tree) pt_ld8(lanes + kPtColS + 128u * (uint32_t)buf + 64u + 8u * part, lo);
+        tmem_wait_ld();
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint32_t hi[16], lo[16];
-          const uint32_t col = lanes + kPtColS + 128u * (uint32_t)buf + (uint32_t)(32 * half + 16 * part);
-          pt_ld16(col, hi);
-          pt_ld16(col + 64, lo);
-          tmem_wait_ld();
-          if (is_tree) {  // one term: the other columns hold nothing yet
-#pragma unroll
-            for (int e = 0; e < 16; ++e) lo[e] = 0u;
-          }
-          if (half == 1 && part == 1) {  // S is free once it sits in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(T_SFREE + buf));
-          }
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float4 f = lds_f4(fcb + 8u * (uint32_t)(32 * half + 16 * part + e));  // two rows' (factor, -reference)
+        for (int e = 0; e < 8; e += 2) {
+          const float4 f = lds_f4(fcb + 8u * (uint32_t)(8 * part + e));  // two rows' (factor, -reference)
+          if (is_tree) {
+            const float y0 = fmaf(__uint_as_float(hi[e]), f.x, f.y), y1 = fmaf(__uint_as_float(hi[e + 1]), f.z, f.w);
+            x[8 * part + e] = (keep >> (8 * part + e)) & 1u ? y0 : -INFINITY;
+            x[8 * part + e + 1] = (keep >> (8 * part + e + 1)) & 1u ? y1 : -INFINITY;
+          } else {
             const float y0 = fmaf(__uint_as_float(lo[e]), ks, __uint_as_float(hi[e]) * ks);
             const float y1 = fmaf(__uint_as_float(lo[e + 1]), ks, __uint_as_float(hi[e + 1]) * ks);
-            x[16 * part + e] = fmaf(y0, f.x, lv + f.y);
-            x[16 * part + e + 1] = fmaf(y1, f.z, lv + f.w);
+            // a key that is not there: -inf, whatever was scored (a NaN score of one that is becomes +inf, whose
+            // weight the slow path below turns into NaN again)
+            x[8 * part + e] = fminf(fmaf(y0, f.x, lv + f.y), cap);
+            x[8 * part + e + 1] = fminf(fmaf(y1, f.z, lv + f.w), cap);
           }
         }
-        if (masked) {
+      }
+      tc_fence_before();  // the scores sit in registers: their buffer is free
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(T_SFREE + buf));
+      my_scale(page_n, ks_n, vs_n);  // in flight until the next item
+      float top = x[0];
 #pragma unroll
-          for (int q = 0; q < 32; ++q) x[q] = (keep[half] >> q) & 1u ? x[q] : -INFINITY;
+      for (int q = 1; q < kPtQ; ++q) top = fmaxf(top, x[q]);
+      if (group_any(w, fresh || top > kPaTop + kPaSlack)) {
+        // the rows' maxima over the tile: a warp's 32 keys, then the four quarters
+#pragma unroll
+        for (int q = 0; q < kPtQ; ++q) {
+          const int m = __reduce_max_sync(0xffffffffu, order_int(x[q] == x[q] ? x[q] : -INFINITY));
+          if (lane == q) red[quarter * kPtRows + r0 + q] = __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
         }
-        float top = x[0];
-#pragma unroll
-        for (int q = 1; q < 32; ++q) top = fmaxf(top, x[q]);
-        if (group_any(w, fresh[half] || top > kPaTop + kPaSlack)) {
-          // the rows' maxima over the tile: a warp's 32 keys, then the four warps
-#pragma unroll
-          for (int q = 0; q < 32; ++q) {
-            const int m = __reduce_max_sync(0xffffffffu, order_int(x[q] == x[q] ? x[q] : -INFINITY));
-            if (lane == q) red[quarter * kPtRows + 32 * half + q] = __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
-          }
-          group_sync(w);
-          bool still = false;
-          if (tid >= 32 * half && tid < 32 * half + 32) {
-            float m = fmaxf(fmaxf(red[tid], red[kPtRows + tid]), fmaxf(red[2 * kPtRows + tid], red[3 * kPtRows + tid]));
-            float2 *at = reinterpret_cast<float2 *>(sm + kPtOffFC) + w * kPtRows + tid;
-            const float was = -at->y;  // the reference; 0 while the row is fresh
-            float now = was;
-            if (m > -INFINITY) now = mine_fresh ? m - kPaTop : fmaxf(was, m + was - kPaTop);
-            const float corr = mine_fresh ? 0.f : ex2_fast(was - now);
-            mine_fresh = mine_fresh && !(m > -INFINITY);
-            still = mine_fresh;
-            at->y = -now;
-            adj[tid] = make_float2(was - now, corr);
-          }
-          fresh[half] = group_any(w, still);
-#pragma unroll
-          for (int q = 0; q < 32; ++q) {
-            const float2 d = adj[32 * half + q];
-            x[q] += d.x;
-            l[32 * half + q] *= d.y;
-          }
-          if (i >= 2) {  // O holds the sums of this group's earlier tiles
-            if (!dead) dead = !mbar_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
-            dead = __any_sync(0xffffffffu, dead);
-            tc_fence_after();
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              uint32_t o[16];
-              const uint32_t col = lanes + kPtColO + 64u * (uint32_t)w + (uint32_t)(32 * half + 16 * part);
-              pt_ld16(col, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                o[e] = __float_as_uint(__uint_as_float(o[e]) * adj[32 * half + 16 * part + e].y);
-              tmem_st16(col, o);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-          }
-          group_sync(w);  // the changes are read before they may change again
+        group_sync(w);
+        bool still = false;
+        if (gt < kPtRows) {
+          const float m = fmaxf(fmaxf(red[gt], red[kPtRows + gt]), fmaxf(red[2 * kPtRows + gt], red[3 * kPtRows + gt]));
+          float2 *at = fc + w * kPtRows + gt;
+          const float was = -at->y;  // the reference; 0 while the row is fresh
+          float now = was;
+          if (m > -INFINITY) now = mine_fresh ? m - kPaTop : fmaxf(was, m + was - kPaTop);
+          const float corr = mine_fresh ? 0.f : ex2_fast(was - now);
+          mine_fresh = mine_fresh && !(m > -INFINITY);
+          still = mine_fresh;
+          at->y = -now;
+          adj[gt] = make_float2(was - now, corr);
         }
-        // this group's weights buffer is free once its last product has run
-        if (half == 0 && i >= 2) {
-          if (!dead) dead = !mbar_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
+        fresh = group_any(w, still);
+#pragma unroll
+        for (int q = 0; q < kPtQ; ++q) {
+          const float2 d = adj[r0 + q];
+          x[q] += d.x;
+          l[q] *= d.y;
+        }
+        if (i >= 2) {  // O holds the sums of this group's earlier tiles
+          if (!dead) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
           dead = __any_sync(0xffffffffu, dead);
+          tc_fence_after();
+#pragma unroll
+          for (int part = 0; part < kPtQ / 16; ++part) {
+            uint32_t o[16];
+            const uint32_t at = lanes + kPtColO + 64u * (uint32_t)w + 16u * part;
+            pt_ld16(at, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * adj[r0 + 16 * part + e].y);
+            tmem_st16(at, o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        group_sync(w);  // the changes are read before they may change again
+      }
+      // this group's weights buffer is free once its last product has run
+      if (i >= 2) {
+        if (!dead) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
+        dead = __any_sync(0xffffffffu, dead);
+      }
+#pragma unroll
+      for (int c = 0; c < kPtQ / 8; ++c) {
+        uint32_t p[4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int q = 8 * c + e;
+          x[q] = ex2_fast(x[q]);
+          l[q] = fmaf(x[q], iv, l[q]);
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int q = 8 * c + 2 * e;
-            const float w0 = ex2_fast(x[q]), w1 = ex2_fast(x[q + 1]);
-            l[32 * half + q] = fmaf(w0, iv, l[32 * half + q]);
-            l[32 * half + q + 1] = fmaf(w1, iv, l[32 * half + q + 1]);
-            x[q] = w0;
-            x[q + 1] = w1;
-          }
-          if (is_tree) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = pack_bf16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = pack_f16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
-          }
-          sts128(prow + sw128(tid, 4 * half + c), p[0], p[1], p[2], p[3]);
-        }
+        for (int e = 0; e < 4; ++e)
+          p[e] = is_tree ? pack_bf16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1])
+                         : pack_f16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
+        sts128(prow + sw128(tid, 4 * col + c), p[0], p[1], p[2], p[3]);
       }
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(T_PFULL + w));
-      my_scale(page_n, ks_n, vs_n);
       if (is_tree) {  // cached tiles from here on: the rows' own factors
         group_sync(w);
-        if (tid < kPtRows) fc[tid].x = fc[kPtRows + tid].x;
+        if (gt < kPtRows) fc[gt].x = fc[kPtRows + gt].x;
         group_sync(w);
       }
+    };
+    int i0 = w;
+    if (tree && w == 0) {
+      item(0, std::true_type{});
+      i0 = 2;
     }
-    // the group's sums: 64 rows over 128 threads.  After the step of offset o a lane holds the rows whose index
-    // agrees with it in the bits done: 64 values become two
+#pragma unroll 1
+    for (int i = i0; i < items; i += 2) item(i, std::false_type{});
+    // the group's sums: a warp's 32 rows over its 32 keys; after the step of offset o a lane holds the rows whose
+    // index agrees with it in the bits done, in the end row r0 + lane
 #pragma unroll
-    for (int o = 16, m = 32; o > 0; o >>= 1, m >>= 1) {
+    for (int o = 16; o > 0; o >>= 1) {
       const bool up = lane & o;
 #pragma unroll
-      for (int q = 0; q < m; ++q) {
-        const float keep = up ? l[q + m] : l[q], send = up ? l[q] : l[q + m];
-        l[q] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      for (int q = 0; q < o; ++q) {
+        const float kept = up ? l[q + o] : l[q], send = up ? l[q] : l[q + o];
+        l[q] = kept + __shfl_xor_sync(0xffffffffu, send, o);
       }
     }
-    // lane bits 4..0 chose row bits 5..1
-    red[quarter * kPtRows + 2 * lane] = l[0];
-    red[quarter * kPtRows + 2 * lane + 1] = l[1];
+    red[quarter * kPtRows + r0 + lane] = l[0];
     group_sync(w);
     const int mine = items > w ? (items - w + 1) / 2 : 0;  // this group's items
-    if (tid < kPtRows)
-      reinterpret_cast<float2 *>(sm + kPtOffML)[w * kPtRows + tid] =
-          make_float2(mine && !mine_fresh ? -fc[w * kPtRows + tid].y : -3e38f,
-                      (red[tid] + red[kPtRows + tid]) + (red[2 * kPtRows + tid] + red[3 * kPtRows + tid]));
-    if (mine && !dead) dead = !mbar_wait(bar(T_PVDONE + w), (uint32_t)(mine - 1) & 1u, &s_abort, limit);
+    if (gt < kPtRows)
+      reinterpret_cast<float2 *>(sm + kPtOffML)[w * kPtRows + gt] =
+          make_float2(mine && !mine_fresh ? -fc[w * kPtRows + gt].y : -3e38f,
+                      (red[gt] + red[kPtRows + gt]) + (red[2 * kPtRows + gt] + red[3 * kPtRows + gt]));
+    if (mine && !dead) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)(mine - 1) & 1u, &s_abort, limit);
   }
   tc_fence_before();
   __syncthreads();
@@ -644,7 +691,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const bool aborted = *(volatile int *)&s_abort != 0;
   if (aborted && t == 0) flag_status(a.dev_status, ET_DEV_TIMEOUT);
 
-  // ---- the two groups' O, joined; thread = dim, each group takes half of the rows ----
+  // ---- the two groups' O, joined; thread = dim ----
   const int real = min(kPtRows, a.N * a.G - rt * kPtRows);  // rows that exist are a prefix of the tile
   const long long tile_id = (long long)b * ma.tiles_y + blockIdx.y;
   auto place = [&](int r) -> long long {  // element index of row r in out
@@ -676,11 +723,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   }
   __syncthreads();
   if (warp >= 4) {
-    const int w = (warp - 4) >> 2, quarter = warp & 3, d = 32 * quarter + lane;
+    const int quarter = warp & 3, d = 32 * quarter + lane, q0 = 16 * ((warp - 4) >> 2);  // 16 rows a warp
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + kPtColO;
     const bool odd = tree && s_odd, two = items > 1;  // a group without items left its columns unwritten
-#pragma unroll 1
-    for (int q0 = 32 * w; q0 < min(real, 32 * w + 32); q0 += 16) {
+    if (q0 < real) {
       uint32_t o0[16], o1[16];
       pt_ld16(lanes + (uint32_t)q0, o0);
       pt_ld16(lanes + 64u + (uint32_t)q0, o1);
