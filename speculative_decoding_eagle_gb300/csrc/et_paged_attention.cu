@@ -161,7 +161,7 @@ et_status launch_row(const PagedAttnArgs &a, int d, cudaStream_t st) {
 // Codes become fp16 exactly, so both products are fp16 m16n8k16 into fp32
 // sums.  q is lifted by a power of two per row to [2^14, 2^15) before it is
 // rounded to fp16: nothing above 2^-38 of its row's largest element is lost.
-// Weights stay below 2^15 and lose only what lies 2^-31 below the largest.
+// Weights stay below 2^15 and lose only what lies 2^-28 below the largest.
 // (8-bit mma.sync is no way out here: on this part it runs as two fp16
 // products and conversions; 479 TFLOP/s against 573 for fp16 in a loop with
 // changing operands.)
@@ -227,7 +227,7 @@ __device__ __forceinline__ int merge_chunk(int r, int c) {
 
 // Weights of NT n-tiles of scores (16 keys = two n-tiles share a scale): x =
 // score * f + lv relative to the row's reference mr, which moves only when a
-// weight would pass 2^15 (then it becomes the row maximum - 7 and what was
+// weight would pass 2^15 (then it becomes the row maximum - 3 and what was
 // summed is rescaled).  keep: bit (8 * n-tile + key) per row, all ones when
 // `masked` is false.  On return p holds the weights as packed pairs.
 template <int NT, int MT, int NTO, bool BF16>

@@ -138,10 +138,11 @@ __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile 
 }
 // chunk c (16 bytes) of row r in a tile of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-// an fp32 value as an integer that orders like it
-__device__ __forceinline__ int order_int(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
+// maximum over the warp's lanes; NaN is passed over
+__device__ __forceinline__ float warp_max_f32(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
 
 template <int FMT>
@@ -583,11 +584,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       for (int q = 1; q < kPtQ; ++q) top = fmaxf(top, x[q]);
       if (group_any(w, fresh || top > kPaTop + kPaSlack)) {
         // the rows' maxima over the tile: a warp's 32 keys, then the four quarters
+        float highest = -INFINITY;
 #pragma unroll
         for (int q = 0; q < kPtQ; ++q) {
-          const int m = __reduce_max_sync(0xffffffffu, order_int(x[q] == x[q] ? x[q] : -INFINITY));
-          if (lane == q) red[quarter * kPtRows + r0 + q] = __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+          const float m = warp_max_f32(x[q]);
+          if (lane == q) highest = m;
         }
+        red[quarter * kPtRows + r0 + lane] = highest;
         group_sync(w);
         bool still = false;
         if (gt < kPtRows) {
@@ -604,10 +607,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         fresh = group_any(w, still);
 #pragma unroll
-        for (int q = 0; q < kPtQ; ++q) {
-          const float2 d = adj[r0 + q];
+        for (int q = 0; q < kPtQ; q += 2) {
+          const float4 d = *reinterpret_cast<const float4 *>(adj + r0 + q);
           x[q] += d.x;
           l[q] *= d.y;
+          x[q + 1] += d.z;
+          l[q + 1] *= d.w;
         }
         if (i >= 2) {  // O holds the sums of this group's earlier tiles
           if (!dead) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);

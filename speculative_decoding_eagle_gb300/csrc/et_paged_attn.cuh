@@ -47,7 +47,9 @@ ET_HIDDEN et_status paged_tc_launch(const et_paged_cache *cache, const PagedSpli
 namespace {
 
 constexpr int kPaMaxSplits = 64;
-constexpr float kPaTop = 7.f, kPaSlack = 8.f;  // weights lie below 2^kPaTop when the maximum moves, below 2^15 always
+// Weights lie at or below 2^kPaTop when a row's reference moves to its maximum, and the reference stays until one would
+// pass 2^15, short of fp16's largest.  What lies 2^28 below the maximum is lost then (fp16's smallest value is 2^-24).
+constexpr float kPaTop = 3.f, kPaSlack = 12.f;
 
 // prefix length of sequence b as the kernels use it: -1 = no sequence here
 __device__ __forceinline__ int paged_prefix(const PagedAttnArgs &a, int b, int &bad) {
