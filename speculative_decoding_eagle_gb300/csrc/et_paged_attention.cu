@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     const long long key = (long long)(first + (long long)KG * i) * kPaTile + 16 * (lane & 1);
     pg = -1;
     if (i < n && key < L) {
-      const int blk = (int)key / a.P;
+      const int blk = page_index(ma, (int)key);
       sl = (int)key - blk * a.P;
       pg = a.block_table[(long long)b * a.max_blocks + blk];
       if (pg < 0 || pg >= a.num_pages) {
@@ -907,6 +907,8 @@ extern "C" et_status et_tree_attention_paged(const et_paged_attn_shape *shape, c
   ma.cnt = plan.S > 1 ? reinterpret_cast<unsigned int *>(wsb) : nullptr;
   ma.part_ml = plan.S > 1 ? reinterpret_cast<float2 *>(wsb + plan.ml_off) : nullptr;
   ma.part_o = plan.S > 1 ? reinterpret_cast<float4 *>(wsb + plan.o_off) : nullptr;
+  const uint32_t units = (uint32_t)cache->page_size / 16;
+  ma.page_magic = units == 1 ? 0u : (uint32_t)(((1ull << 32) + units - 1) / units);
   ma.wait_cycles = et_wait_limit_cycles();
   if (plan.tc) return paged_tc_launch(cache, ma, st);
   CUtensorMap mk, mv;

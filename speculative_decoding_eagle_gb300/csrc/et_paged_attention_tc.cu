@@ -5,22 +5,24 @@
 // Everything is transposed: keys are the rows of the products, query rows
 // their columns.
 //   S^T [128 keys x 64 rows] = K8 . Q8^T   (kind::f8f6f4; K's codes by TMA, q
-//        lifted by a power of two per row and split into two e4m3 terms that
-//        are 128 columns of one product, so K is read once)
+//        lifted by a power of two per row and split into two e4m3 terms, two
+//        products into one sum)
 //   O^T [128 dims x 64 rows] += V16^T . P^T (kind::f16; V's codes as fp16)
 // A tree of up to 64 rows per KV head (every MHA tree) then fills the 128
 // lanes of tensor memory with keys instead of padding them with rows that do
 // not exist; the softmax runs one key per thread, and a tile of a page's
 // codes needs no conversion before the scores.
 //
-// One block per SM, twenty warps:
-//   warp 0      TMA: a 128-key tile of K and of V, into rings of 3
-//   warp 1      owns 512 columns of TMEM, issues every product
-//   warps 2, 3  V's codes -> fp16 (two buffers)
-//   warps 4-11, 12-19  two softmax groups on alternate tiles, each with its
-//               own weights, running maximum and O in TMEM: independent
-//               online softmaxes, joined at the end.  A thread has one key
-//               and half of the rows.
+// One block per SM, eighteen warps:
+//   warps 0-7, 8-15  two softmax groups on alternate tiles, each with its own
+//               weights, running maximum and O in TMEM: independent online
+//               softmaxes, joined at the end.  A thread has one key and half
+//               of the rows.  The group also turns its tile's V codes into
+//               fp16, before its scores arrive
+//   warp 16     TMA: a 128-key tile of K and of V, into rings of 3
+//   warp 17     owns 512 columns of TMEM, issues every product
+// (Twenty warps with two that only converted left 96 registers a thread, and
+// the softmax's spills cost more than the conversion: 227 against ... us.)
 // A weight's reference moves only when some weight would pass 2^15 (one vote
 // of the group in place of a maximum over the lanes); the slow path finds the
 // maxima, and rescales the group's sums and O.  The tree's own rows are one
@@ -36,12 +38,12 @@
 namespace et {
 namespace {
 
-constexpr int kPtThreads = 640;
+constexpr int kPtThreads = 576;
 constexpr int kPtGroup = 256;   // threads of a softmax group
 constexpr int kPtQ = kPtRows / 2;  // rows per softmax thread
 constexpr int kPtD = 128;
 constexpr int kPtStages = 3;
-constexpr int kPtConvWarps = 2;
+constexpr int kPtTmaWarp = 16, kPtMmaWarp = 17;
 constexpr uint32_t kPtTile8 = kPtKeys * kPtD;            // 16 KB: K8 or V8
 constexpr uint32_t kPtTile16 = 2 * kPtTile8;             // 32 KB: V16, two halves of 64 dims
 constexpr uint32_t kPtHalf16 = kPtKeys * 128;            // 16 KB
@@ -52,9 +54,9 @@ constexpr uint32_t kPtOffV = kPtOffK + kPtStages * kPtTile8;
 constexpr uint32_t kPtOffVH = kPtOffV + kPtStages * kPtTile8;
 constexpr uint32_t kPtOffP = kPtOffVH + 2 * kPtTile16;
 constexpr uint32_t kPtOffBar = kPtOffP + 2 * kPtP;
-constexpr uint32_t kPtOffFC = kPtOffBar + 256;           // [2 groups][64] (row factor, -reference)
+constexpr uint32_t kPtOffFC = kPtOffBar + 256;           // [2 groups][32 pairs of rows] factors, -references
 constexpr uint32_t kPtOffRed = kPtOffFC + 2 * kPtRows * 8;     // [2][4 warps][64]
-constexpr uint32_t kPtOffAdj = kPtOffRed + 2 * 4 * kPtRows * 4;  // [2][64] (reference change, factor)
+constexpr uint32_t kPtOffAdj = kPtOffRed + 2 * 4 * kPtRows * 4;  // [2][32 pairs] reference changes, factors
 constexpr uint32_t kPtOffMask = kPtOffAdj + 2 * kPtRows * 8;   // [64] two mask words
 constexpr uint32_t kPtOffML = kPtOffMask + kPtRows * 16;       // [2][64] (reference, sum)
 constexpr uint32_t kPtBytes = kPtOffML + 2 * kPtRows * 8 + 1024;  // + slack for 1024-byte alignment
@@ -64,10 +66,10 @@ constexpr uint32_t kPtOffTreeK = kPtOffP;                    // K tree, bf16, tw
 constexpr uint32_t kPtOffTreeV = kPtOffVH;                   // V tree, bf16, as V16 buffer 0
 constexpr uint32_t kPtOffTreeQ = kPtOffVH + kPtTile16;       // q, bf16, two halves of 64 rows
 // TMEM columns
-constexpr uint32_t kPtColS = 0, kPtColO = 384, kPtTmemCols = 512;  // three score buffers, two O
+constexpr uint32_t kPtColS = 0, kPtColO = 192, kPtTmemCols = 512;  // three score buffers, two O
 
-enum { T_KFULL = 0, T_KEMPTY = 3, T_VFULL = 6, T_VEMPTY = 9, T_SFULL = 12, T_SFREE = 15, T_PFULL = 18, T_VHFULL = 20,
-       T_PVDONE = 22, T_TREE = 24, T_DRAIN = 25, T_COUNT = 26 };
+enum { T_KFULL = 0, T_KEMPTY = 3, T_VFULL = 6, T_VEMPTY = 9, T_SFULL = 12, T_SFREE = 15, T_PFULL = 18, T_PVDONE = 20,
+       T_TREE = 22, T_DRAIN = 23, T_COUNT = 24 };
 
 // instruction descriptors: fp32 sums (bits 4-5 = 1), A type in bits 7-9, B
 // type in 10-12, A / B stored MN-major in bits 15 / 16, N >> 3, M >> 4
@@ -81,10 +83,30 @@ __device__ __forceinline__ void pt_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void pt_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
+// pairs of fp32 values: one instruction for two
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t &a, uint64_t &b) {
+  asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
 __device__ __forceinline__ void pt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -94,11 +116,6 @@ __device__ __forceinline__ void pt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-  return v;
 }
 // OR of a condition over a softmax group's threads, and a barrier
 __device__ __forceinline__ bool group_any(int group, bool p) {
@@ -136,6 +153,9 @@ __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile 
   }
   return true;
 }
+// tables of two values per row, by pairs of rows: x of both, then y of both
+__device__ __forceinline__ int px(int row) { return 4 * (row >> 1) + (row & 1); }
+__device__ __forceinline__ int py(int row) { return px(row) + 2; }
 // chunk c (16 bytes) of row r in a tile of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 // maximum over the warp's lanes; NaN is passed over
@@ -165,9 +185,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     s_odd = 0;
     for (int i = 0; i < T_COUNT; ++i) {
       int count = 1;
-      if (i >= T_VEMPTY && i < T_SFULL) count = kPtConvWarps;
-      if (i >= T_SFREE && i < T_VHFULL) count = kPtGroup / 32;
-      if (i >= T_VHFULL && i < T_PVDONE) count = kPtConvWarps;
+      if ((i >= T_VEMPTY && i < T_SFULL) || (i >= T_SFREE && i < T_PVDONE)) count = kPtGroup / 32;  // a group's warps
       mbar_init(bar(i), (uint32_t)count);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -201,7 +219,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const int t0 = chunk * per, n = min(T, t0 + per) - t0;  // prefix tiles t0 .. t0 + n - 1
   const int tree = chunk == 0 ? 1 : 0;                    // item 0 is the tree's tile
   const int items = n + tree;
-  if (warp == 1) {
+  if (warp == kPtMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&s_tmem)), "r"(kPtTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -209,14 +227,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   __syncthreads();  // barriers initialised (and the longest prefix read by all)
   pdl_trigger();    // after the TMEM allocation: a waiting dependent block must not hold what this block needs
 
-  // ---- TMA (warp 0): tile j of this block into ring stage j % stages ----
+  // ---- TMA: tile j of this block into ring stage j % stages ----
   int page = -1, slot = 0;  // lane: unit (lane & 7) of tile 4 * (j / 4) + (lane >> 3), 16 keys a unit
   auto fetch_pages = [&](int j0) {
     const int j = j0 + (lane >> 3);
     const long long key = (long long)(t0 + j) * kPtKeys + 16 * (lane & 7);
     page = -1;
     if (j < n && key < L) {
-      const int blk = (int)key / a.P;
+      const int blk = page_index(ma, (int)key);
       slot = (int)key - blk * a.P;
       page = a.block_table[(long long)b * a.max_blocks + blk];
       if (page < 0 || page >= a.num_pages) {
@@ -248,7 +266,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       tma_4d(sb + kPtOffV + off, &tm_v, 0, sl, g, pg, bar(T_VFULL + stage));
     }
   };
-  if (warp == 0) {
+  if (warp == kPtTmaWarp) {
     fetch_pages(0);
     for (int j = 0; j < n && j < kPtStages; ++j) issue(j);
   }
@@ -266,7 +284,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       v = *reinterpret_cast<const uint4 *>(VT + at);
     }
   };
-  float2 *fc = reinterpret_cast<float2 *>(sm + kPtOffFC);
+  float *fc = reinterpret_cast<float *>(sm + kPtOffFC);  // group w at 2 * kPtRows * w
   bool odd_v = false;
   auto store_cell = [&](int x, const uint4 &k, const uint4 &v) {
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -329,8 +347,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         // what a score of lifted q and codes stands for, in log2 units; a row that is not finite scores NaN
         const float f = odd ? __uint_as_float(0x7fc00000u)
                             : a.scale_log2 * __uint_as_float((uint32_t)(127 - ea) << 23) * __uint_as_float((uint32_t)(127 - eb) << 23);
-        fc[kPtRows + r] = make_float2(f, 0.f);
-        fc[r] = make_float2(tree ? a.scale_log2 : f, 0.f);  // group 0 takes the tree's tile first: q as it is
+        fc[2 * kPtRows + px(r)] = f;
+        fc[px(r)] = tree ? a.scale_log2 : f;  // group 0 takes the tree's tile first: q as it is
+        fc[py(r)] = fc[2 * kPtRows + py(r)] = 0.f;
       }
     }
     if (tree) {
@@ -371,7 +390,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const uint32_t tmem = s_tmem;
   const long long limit = ma.wait_cycles;
 
-  if (warp == 0) {
+  if (warp == kPtTmaWarp) {
     // ---------------- TMA ----------------
     bool ok = true;
     int issued = n < kPtStages ? n : kPtStages;
@@ -390,15 +409,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         mbar_drain(bar(T_VFULL + j % kPtStages), (uint32_t)(j / kPtStages) & 1u);
       }
     if (bad) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
-  } else if (warp == 1) {
+  } else if (warp == kPtMmaWarp) {
     // ---------------- products ----------------
     if (lane == 0 && items > 0) {
-      constexpr uint32_t iS = pt_idesc(FMT == ET_KV_E4M3 ? 0 : 1, 0, false, false, 128, 128);
+      constexpr uint32_t iS = pt_idesc(FMT == ET_KV_E4M3 ? 0 : 1, 0, false, false, 128, 64);
       constexpr uint32_t iSt = pt_idesc(1, 1, false, false, 128, 64);
       constexpr uint32_t iO = pt_idesc(0, 0, true, true, 128, 64), iOt = pt_idesc(1, 1, true, true, 128, 64);
       auto scores = [&](int i) -> bool {  // item i into S buffer i % 3
         const int buf = i % 3;
-        const uint32_t d = tmem + kPtColS + 128u * (uint32_t)buf;
+        const uint32_t d = tmem + kPtColS + 64u * (uint32_t)buf;
         if (i >= 3 && !pt_wait(bar(T_SFREE + buf), (uint32_t)(i / 3 - 1) & 1u, &s_abort, limit)) return false;
         if (tree && i == 0) {
           tc_fence_after();
@@ -412,9 +431,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           if (!pt_wait(bar(T_KFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit)) return false;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            pt_mma_f8(d, sw128_desc(sb + kPtOffK + stage * kPtTile8 + kk * 32, 16, 1024),
-                      sw128_desc(sb + kPtOffQ + kk * 32, 16, 1024), iS, kk > 0);
+          for (int kk = 0; kk < 8; ++kk)  // the two terms of q one after the other
+            pt_mma_f8(d, sw128_desc(sb + kPtOffK + stage * kPtTile8 + (kk & 3) * 32, 16, 1024),
+                      sw128_desc(sb + kPtOffQ + (kk >> 2) * (kPtRows * kPtD) + (kk & 3) * 32, 16, 1024), iS, kk > 0);
           if (j + kPtStages < n) tc_commit(bar(T_KEMPTY + stage));
         }
         tc_commit(bar(T_SFULL + buf));
@@ -425,7 +444,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (i + 2 < items && !scores(i + 2)) break;  // two ahead: a group finds its next scores when it has stored its weights
         const int w = i & 1;
         const uint32_t phase = (uint32_t)(i >> 1) & 1u;
-        if (!pt_wait(bar(T_VHFULL + w), phase, &s_abort, limit) || !pt_wait(bar(T_PFULL + w), phase, &s_abort, limit)) break;
+        if (!pt_wait(bar(T_PFULL + w), phase, &s_abort, limit)) break;
         tc_fence_after();
         const bool is_tree = tree && i == 0;
         const int steps = is_tree ? (a.N + 15) >> 4 : kPtKeys / 16;
@@ -439,75 +458,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       tc_commit(bar(T_DRAIN));
       mbar_drain(bar(T_DRAIN), 0);
     }
-  } else if (warp < 4) {
-    // ---------------- V's codes -> fp16: 16 codes of a row a thread, halves of 64 dims, 128-byte swizzle ----------------
-    const int ct = t - 64;
-    bool ok = true;
-    for (int i = 0; i < items; ++i) {
-      const int w = i & 1;
-      if (!(tree && i == 0)) {
-        const int j = i - tree, stage = j % kPtStages;
-        if (i >= 2) ok = pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
-        else if (tree) ok = pt_wait(bar(T_TREE), 0, &s_abort, limit);  // q of the tree's scores lies in this buffer
-        ok = ok && pt_wait(bar(T_VFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const uint32_t units = *(volatile uint32_t *)&s_units[stage];
-        const int lim = L - (t0 + j) * kPtKeys;  // rows past it hold no key of this sequence
-        const uint32_t src = sb + kPtOffV + stage * kPtTile8, dst = sb + kPtOffVH + w * kPtTile16;
-        // 16 codes of a row a thread; the row's place in its group of eight is the thread's own, so addresses advance
-        // by whole groups.  Dims 16 c .. + 15 are two 16-byte chunks of half c / 4; the lanes of the upper half store
-        // them in the other order, which keeps the stores free of bank conflicts
-        const int c = ct & 7, r7 = ct >> 3, c0 = 2 * (c & 3);
-        const bool swap = c >= 4;
-        const uint32_t from = src + sw128(r7, c), half = dst + (uint32_t)((c >> 2) * kPtHalf16);
-        const uint32_t to0 = half + sw128(r7, swap ? c0 + 1 : c0), to1 = half + sw128(r7, swap ? c0 : c0 + 1);
-        const bool whole = lim >= kPtKeys && units == 0xffu;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint4 v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(from + 8192u * h + 1024u * k));
-          if (!whole) {  // whatever lies in rows without a key must not meet a zero weight
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int r = r7 + 8 * (8 * h + k);
-              if (r >= lim || !((units >> (r >> 4)) & 1u)) v[k] = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t x[8];
-            f8x4_to_f16<FMT>(swap ? v[k].z : v[k].x, x[0], x[1]);
-            f8x4_to_f16<FMT>(swap ? v[k].w : v[k].y, x[2], x[3]);
-            f8x4_to_f16<FMT>(swap ? v[k].x : v[k].z, x[4], x[5]);
-            f8x4_to_f16<FMT>(swap ? v[k].y : v[k].w, x[6], x[7]);
-            sts128(to0 + 8192u * h + 1024u * k, x[0], x[1], x[2], x[3]);
-            sts128(to1 + 8192u * h + 1024u * k, x[4], x[5], x[6], x[7]);
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(T_VEMPTY + stage));
-          mbar_arrive(bar(T_VHFULL + w));
-        }
-      } else if (lane == 0) {
-        mbar_arrive(bar(T_VHFULL + w));  // the tree's V was staged above
-      }
-    }
   } else {
     // ---------------- softmax: group w, one key and half of the rows per thread ----------------
-    const int w = (warp - 4) >> 3, quarter = warp & 3, col = ((warp - 4) >> 2) & 1, tid = 32 * quarter + lane;
-    const int gt = t - 128 - kPtGroup * w, r0 = kPtQ * col;  // thread of the group; first of its rows
+    const int w = warp >> 3, quarter = warp & 3, col = (warp >> 2) & 1, tid = 32 * quarter + lane;
+    const int gt = t & (kPtGroup - 1), r0 = kPtQ * col;  // thread of the group; first of its rows
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)r0;
-    const uint32_t fcb = sb + kPtOffFC + (uint32_t)((w * kPtRows + r0) * 8), prow = sb + kPtOffP + (uint32_t)(w * kPtP);
+    const uint32_t fcb = sb + kPtOffFC + (uint32_t)((2 * kPtRows * w + 2 * r0) * 4), prow = sb + kPtOffP + (uint32_t)(w * kPtP);
     float *red = reinterpret_cast<float *>(sm + kPtOffRed) + w * 4 * kPtRows;
-    float2 *adj = reinterpret_cast<float2 *>(sm + kPtOffAdj) + w * kPtRows;
-    float l[kPtQ];
+    float *adj = reinterpret_cast<float *>(sm + kPtOffAdj) + 2 * kPtRows * w, *ref = fc + 2 * kPtRows * w;
+    const uint32_t adjb = sb + kPtOffAdj + (uint32_t)((2 * kPtRows * w + 2 * r0) * 4);
+    uint64_t l2[kPtQ / 2];
 #pragma unroll
-    for (int q = 0; q < kPtQ; ++q) l[q] = 0.f;
+    for (int q = 0; q < kPtQ / 2; ++q) l2[q] = 0ull;
     bool dead = false;
     bool fresh = true;       // some row has no reference yet (the same in the whole group)
     bool mine_fresh = true;  // threads 0..63 of the group: row gt has none
@@ -516,7 +478,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const int j = i - tree;
       const long long key = (long long)(t0 + j) * kPtKeys + tid;
       if (i >= items || j < 0 || key >= L) return -1;
-      return a.block_table[(long long)b * a.max_blocks + (int)key / a.P];  // checked where it is used: no wait here
+      return a.block_table[(long long)b * a.max_blocks + page_index(ma, (int)key)];  // checked where it is used: no wait here
     };
     auto real_page = [&](int p) -> bool { return p >= 0 && p < a.num_pages; };
     auto my_scale = [&](int p, float &ks, float &vs) {
@@ -535,10 +497,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       constexpr bool is_tree = decltype(is_tree_)::value;
       const bool there = is_tree ? tid < a.N : real_page(page_n);
       const float ks = is_tree ? 1.f : ks_n, vs = is_tree ? 1.f : clamp_v_scale(vs_n);
-      const float lv = is_tree ? 0.f : __log2f(vs), iv = is_tree ? 1.f : __frcp_rn(vs);
+      const float lv = is_tree ? 0.f : __log2f(vs), iv = is_tree ? 1.f : __fdividef(1.f, vs);
       page_n = my_page(i + 2);
-      uint32_t keep = 0u;  // the tree's tile, bit q: row r0 + q attends this thread's key
+      uint32_t keep = there ? 0xffffffffu : 0u;  // bit q: row r0 + q attends this thread's key
       if (is_tree && there) {
+        keep = 0u;
 #pragma unroll 4
         for (int q = 0; q < kPtQ; ++q) {
           const unsigned long long m =
@@ -546,42 +509,84 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           keep |= (uint32_t)((m >> (tid & 63)) & 1ull) << q;
         }
       }
-      const float cap = there ? INFINITY : -INFINITY;
+      const bool masked = __any_sync(0xffffffffu, keep != 0xffffffffu);
+      // this group's weights and V16 are free once its last product has run; q of the tree's scores lay in V16 buffer 1
+      if (!dead) {
+        if (i >= 2) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
+        else if (tree && i == 1) dead = !pt_wait(bar(T_TREE), 0, &s_abort, limit);
+      }
+      if (!is_tree) {
+        // V's codes -> fp16: 16 codes of a row a thread.  The row's place in its group of eight is the thread's own, so
+        // addresses advance by whole groups.  Dims 16 c .. + 15 are two 16-byte chunks of half c / 4; the lanes of the
+        // upper half store them in the other order, which keeps the stores free of bank conflicts
+        const int j = i - tree, stage = j % kPtStages;
+        if (!dead) dead = !pt_wait(bar(T_VFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit);
+        const uint32_t units = *(volatile uint32_t *)&s_units[stage];
+        const int lim = L - (t0 + j) * kPtKeys;  // rows past it hold no key of this sequence
+        const int c = gt & 7, r7 = (gt >> 3) & 7, r64 = gt >> 6, c0 = 2 * (c & 3);
+        const bool swap = c >= 4;
+        const uint32_t from = sb + kPtOffV + stage * kPtTile8 + 1024u * (uint32_t)r64 + sw128(r7, c);
+        const uint32_t half = sb + kPtOffVH + w * kPtTile16 + (uint32_t)((c >> 2) * kPtHalf16) + 1024u * (uint32_t)r64;
+        const uint32_t to0 = half + sw128(r7, swap ? c0 + 1 : c0), to1 = half + sw128(r7, swap ? c0 : c0 + 1);
+        const bool whole = lim >= kPtKeys && units == 0xffu;
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(from + 4096u * k));
+        if (!whole) {  // whatever lies in rows without a key must not meet a zero weight
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = r7 + 8 * (r64 + 4 * k);
+            if (r >= lim || !((units >> (r >> 4)) & 1u)) v[k] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h[8];
+          f8x4_to_f16<FMT>(swap ? v[k].z : v[k].x, h[0], h[1]);
+          f8x4_to_f16<FMT>(swap ? v[k].w : v[k].y, h[2], h[3]);
+          f8x4_to_f16<FMT>(swap ? v[k].x : v[k].z, h[4], h[5]);
+          f8x4_to_f16<FMT>(swap ? v[k].y : v[k].w, h[6], h[7]);
+          sts128(to0 + 4096u * k, h[0], h[1], h[2], h[3]);
+          sts128(to1 + 4096u * k, h[4], h[5], h[6], h[7]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(T_VEMPTY + stage));
+      }
       const int buf = i % 3;
       if (!dead) dead = !pt_wait(bar(T_SFULL + buf), (uint32_t)(i / 3) & 1u, &s_abort, limit);
       dead = __any_sync(0xffffffffu, dead);
       tc_fence_after();
       float x[kPtQ];
+      const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv), iv2 = pair(iv, iv);
 #pragma unroll
-      for (int part = 0; part < kPtQ / 8; ++part) {
-        uint32_t hi[8], lo[8];
-        pt_ld8(lanes + kPtColS + 128u * (uint32_t)buf + 8u * part, hi);
-        if (!is_tree) pt_ld8(lanes + kPtColS + 128u * (uint32_t)buf + 64u + 8u * part, lo);
+      for (int part = 0; part < kPtQ / 16; ++part) {
+        uint32_t sc[16];
+        pt_ld16(lanes + kPtColS + 64u * (uint32_t)buf + 16u * part, sc);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float4 f = lds_f4(fcb + 8u * (uint32_t)(8 * part + e));  // two rows' (factor, -reference)
-          if (is_tree) {
-            const float y0 = fmaf(__uint_as_float(hi[e]), f.x, f.y), y1 = fmaf(__uint_as_float(hi[e + 1]), f.z, f.w);
-            x[8 * part + e] = (keep >> (8 * part + e)) & 1u ? y0 : -INFINITY;
-            x[8 * part + e + 1] = (keep >> (8 * part + e + 1)) & 1u ? y1 : -INFINITY;
-          } else {
-            const float y0 = fmaf(__uint_as_float(lo[e]), ks, __uint_as_float(hi[e]) * ks);
-            const float y1 = fmaf(__uint_as_float(lo[e + 1]), ks, __uint_as_float(hi[e + 1]) * ks);
-            // a key that is not there: -inf, whatever was scored (a NaN score of one that is becomes +inf, whose
-            // weight the slow path below turns into NaN again)
-            x[8 * part + e] = fminf(fmaf(y0, f.x, lv + f.y), cap);
-            x[8 * part + e + 1] = fminf(fmaf(y1, f.z, lv + f.w), cap);
-          }
+        for (int e = 0; e < 16; e += 2) {
+          uint64_t f, c;  // two rows' factors and -references
+          lds_pairs(fcb + 8u * (uint32_t)(16 * part + e), f, c);
+          uint64_t y = pair(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1]));
+          y = is_tree ? fma2(y, f, c) : fma2(mul2(y, ks2), f, add2(lv2, c));
+          unpair(y, x[16 * part + e], x[16 * part + e + 1]);
         }
       }
       tc_fence_before();  // the scores sit in registers: their buffer is free
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(T_SFREE + buf));
       my_scale(page_n, ks_n, vs_n);  // in flight until the next item
+      if (masked) {  // whatever was scored there
+#pragma unroll
+        for (int q = 0; q < kPtQ; ++q) x[q] = (keep >> q) & 1u ? x[q] : -INFINITY;
+        __syncwarp();
+      }
       float top = x[0];
 #pragma unroll
-      for (int q = 1; q < kPtQ; ++q) top = fmaxf(top, x[q]);
+      for (int q = 1; q + 1 < kPtQ; q += 2) top = fmaxf(top, fmaxf(x[q], x[q + 1]));
+      top = fmaxf(top, x[kPtQ - 1]);
       if (group_any(w, fresh || top > kPaTop + kPaSlack)) {
         // the rows' maxima over the tile: a warp's 32 keys, then the four quarters
         float highest = -INFINITY;
@@ -595,29 +600,25 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         bool still = false;
         if (gt < kPtRows) {
           const float m = fmaxf(fmaxf(red[gt], red[kPtRows + gt]), fmaxf(red[2 * kPtRows + gt], red[3 * kPtRows + gt]));
-          float2 *at = fc + w * kPtRows + gt;
-          const float was = -at->y;  // the reference; 0 while the row is fresh
+          const float was = -ref[py(gt)];  // the reference; 0 while the row is fresh
           float now = was;
           if (m > -INFINITY) now = mine_fresh ? m - kPaTop : fmaxf(was, m + was - kPaTop);
           const float corr = mine_fresh ? 0.f : ex2_fast(was - now);
           mine_fresh = mine_fresh && !(m > -INFINITY);
           still = mine_fresh;
-          at->y = -now;
-          adj[gt] = make_float2(was - now, corr);
+          ref[py(gt)] = -now;
+          adj[px(gt)] = was - now;
+          adj[py(gt)] = corr;
         }
         fresh = group_any(w, still);
 #pragma unroll
         for (int q = 0; q < kPtQ; q += 2) {
-          const float4 d = *reinterpret_cast<const float4 *>(adj + r0 + q);
-          x[q] += d.x;
-          l[q] *= d.y;
-          x[q + 1] += d.z;
-          l[q + 1] *= d.w;
+          uint64_t d, f;
+          lds_pairs(adjb + 8u * (uint32_t)q, d, f);
+          unpair(add2(pair(x[q], x[q + 1]), d), x[q], x[q + 1]);
+          l2[q / 2] = mul2(l2[q / 2], f);
         }
         if (i >= 2) {  // O holds the sums of this group's earlier tiles
-          if (!dead) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
-          dead = __any_sync(0xffffffffu, dead);
-          tc_fence_after();
 #pragma unroll
           for (int part = 0; part < kPtQ / 16; ++part) {
             uint32_t o[16];
@@ -625,7 +626,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             pt_ld16(at, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * adj[r0 + 16 * part + e].y);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * adj[py(r0 + 16 * part + e)]);
             tmem_st16(at, o);
           }
           tmem_wait_st();
@@ -633,24 +634,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         group_sync(w);  // the changes are read before they may change again
       }
-      // this group's weights buffer is free once its last product has run
-      if (i >= 2) {
-        if (!dead) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
-        dead = __any_sync(0xffffffffu, dead);
-      }
 #pragma unroll
       for (int c = 0; c < kPtQ / 8; ++c) {
         uint32_t p[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int q = 8 * c + e;
-          x[q] = ex2_fast(x[q]);
-          l[q] = fmaf(x[q], iv, l[q]);
+        for (int e = 0; e < 4; ++e) {
+          const int q = 8 * c + 2 * e;
+          const float w0 = ex2_fast(x[q]), w1 = ex2_fast(x[q + 1]);
+          l2[q / 2] = fma2(pair(w0, w1), iv2, l2[q / 2]);
+          p[e] = is_tree ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          p[e] = is_tree ? pack_bf16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1])
-                         : pack_f16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
         sts128(prow + sw128(tid, 4 * col + c), p[0], p[1], p[2], p[3]);
       }
       fence_async_smem();
@@ -659,7 +652,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       if (lane == 0) mbar_arrive(bar(T_PFULL + w));
       if (is_tree) {  // cached tiles from here on: the rows' own factors
         group_sync(w);
-        if (gt < kPtRows) fc[gt].x = fc[kPtRows + gt].x;
+        if (gt < kPtRows) fc[px(gt)] = fc[2 * kPtRows + px(gt)];
         group_sync(w);
       }
     };
@@ -672,6 +665,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     for (int i = i0; i < items; i += 2) item(i, std::false_type{});
     // the group's sums: a warp's 32 rows over its 32 keys; after the step of offset o a lane holds the rows whose
     // index agrees with it in the bits done, in the end row r0 + lane
+    float l[kPtQ];
+#pragma unroll
+    for (int q = 0; q < kPtQ; q += 2) unpair(l2[q / 2], l[q], l[q + 1]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const bool up = lane & o;
@@ -686,7 +682,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int mine = items > w ? (items - w + 1) / 2 : 0;  // this group's items
     if (gt < kPtRows)
       reinterpret_cast<float2 *>(sm + kPtOffML)[w * kPtRows + gt] =
-          make_float2(mine && !mine_fresh ? -fc[w * kPtRows + gt].y : -3e38f,
+          make_float2(mine && !mine_fresh ? -ref[py(gt)] : -3e38f,
                       (red[gt] + red[kPtRows + gt]) + (red[2 * kPtRows + gt] + red[3 * kPtRows + gt]));
     if (mine && !dead) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)(mine - 1) & 1u, &s_abort, limit);
   }
@@ -727,8 +723,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
   }
   __syncthreads();
-  if (warp >= 4) {
-    const int quarter = warp & 3, d = 32 * quarter + lane, q0 = 16 * ((warp - 4) >> 2);  // 16 rows a warp
+  if (warp < kPtTmaWarp) {
+    const int quarter = warp & 3, d = 32 * quarter + lane, q0 = 16 * (warp >> 2);  // 16 rows a warp
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + kPtColO;
     const bool odd = tree && s_odd, two = items > 1;  // a group without items left its columns unwritten
     if (q0 < real) {
@@ -769,7 +765,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   __syncthreads();
   tc_fence_after();
   __syncwarp();
-  if (warp == 1)
+  if (warp == kPtMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPtTmemCols) : "memory");
   if (chunks == 1) return;
   // ---- the chunks' rows, merged by the last block to arrive ----

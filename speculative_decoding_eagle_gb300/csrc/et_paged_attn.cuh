@@ -34,6 +34,7 @@ struct PagedSplitArgs {
   unsigned int *cnt;    // [B * tiles_y] arrival counters
   float2 *part_ml;      // [B * tiles_y][S][R] (maximum, sum)
   float4 *part_o;       // [B * tiles_y][S][R][D] fp32
+  uint32_t page_magic;  // page_index
   long long wait_cycles;
 };
 
@@ -51,6 +52,11 @@ constexpr int kPaMaxSplits = 64;
 // pass 2^15, short of fp16's largest.  What lies 2^28 below the maximum is lost then (fp16's smallest value is 2^-24).
 constexpr float kPaTop = 3.f, kPaSlack = 12.f;
 
+// token -> page of its sequence, pages of 16 * p tokens, p <= 16: umulhi by ceil(2^32 / p) is exact below 2^28 units of 16
+__device__ __forceinline__ int page_index(const PagedSplitArgs &a, int token) {
+  const uint32_t u = (uint32_t)token >> 4;
+  return (int)(a.page_magic ? __umulhi(u, a.page_magic) : u);
+}
 // prefix length of sequence b as the kernels use it: -1 = no sequence here
 __device__ __forceinline__ int paged_prefix(const PagedAttnArgs &a, int b, int &bad) {
   int L = a.prefix_len[b];
