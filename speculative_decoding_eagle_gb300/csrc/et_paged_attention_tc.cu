@@ -13,16 +13,18 @@
 // not exist; the softmax runs one key per thread, and a tile of a page's
 // codes needs no conversion before the scores.
 //
-// One block per SM, eighteen warps:
+// One block per SM, nineteen warps:
 //   warps 0-7, 8-15  two softmax groups on alternate tiles, each with its own
 //               weights, running maximum and O in TMEM: independent online
 //               softmaxes, joined at the end.  A thread has one key and half
 //               of the rows.  The group also turns its tile's V codes into
 //               fp16, before its scores arrive
 //   warp 16     TMA: a 128-key tile of K and of V, into rings of 3
-//   warp 17     owns 512 columns of TMEM, issues every product
-// (Twenty warps with two that only converted left 96 registers a thread, and
-// the softmax's spills cost more than the conversion: 227 against ... us.)
+//   warp 17     owns 512 columns of TMEM, issues the score products
+//   warp 18     issues the P.V products.  A thread that issues waits for its
+//               products to be taken (measured: 71 cycles an fp16 product of
+//               up to 128 columns, 47 an 8-bit one of 64), so one warp for
+//               both spent more time polling between them than computing
 // A weight's reference moves only when some weight would pass 2^15 (one vote
 // of the group in place of a maximum over the lanes); the slow path finds the
 // maxima, and rescales the group's sums and O.  The tree's own rows are one
@@ -38,12 +40,12 @@
 namespace et {
 namespace {
 
-constexpr int kPtThreads = 576;
+constexpr int kPtThreads = 608;
 constexpr int kPtGroup = 256;   // threads of a softmax group
 constexpr int kPtQ = kPtRows / 2;  // rows per softmax thread
 constexpr int kPtD = 128;
 constexpr int kPtStages = 3;
-constexpr int kPtTmaWarp = 16, kPtMmaWarp = 17;
+constexpr int kPtTmaWarp = 16, kPtScoreWarp = 17, kPtPvWarp = 18;
 constexpr uint32_t kPtTile8 = kPtKeys * kPtD;            // 16 KB: K8 or V8
 constexpr uint32_t kPtTile16 = 2 * kPtTile8;             // 32 KB: V16, two halves of 64 dims
 constexpr uint32_t kPtHalf16 = kPtKeys * 128;            // 16 KB
@@ -69,7 +71,7 @@ constexpr uint32_t kPtOffTreeQ = kPtOffVH + kPtTile16;       // q, bf16, two hal
 constexpr uint32_t kPtColS = 0, kPtColO = 192, kPtTmemCols = 512;  // three score buffers, two O
 
 enum { T_KFULL = 0, T_KEMPTY = 3, T_VFULL = 6, T_VEMPTY = 9, T_SFULL = 12, T_SFREE = 15, T_PFULL = 18, T_PVDONE = 20,
-       T_TREE = 22, T_DRAIN = 23, T_COUNT = 24 };
+       T_TREE = 22, T_DRAIN = 23 /* two */, T_COUNT = 25 };
 
 // instruction descriptors: fp32 sums (bits 4-5 = 1), A type in bits 7-9, B
 // type in 10-12, A / B stored MN-major in bits 15 / 16, N >> 3, M >> 4
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const int t0 = chunk * per, n = min(T, t0 + per) - t0;  // prefix tiles t0 .. t0 + n - 1
   const int tree = chunk == 0 ? 1 : 0;                    // item 0 is the tree's tile
   const int items = n + tree;
-  if (warp == kPtMmaWarp) {
+  if (warp == kPtScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&s_tmem)), "r"(kPtTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -409,16 +411,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         mbar_drain(bar(T_VFULL + j % kPtStages), (uint32_t)(j / kPtStages) & 1u);
       }
     if (bad) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
-  } else if (warp == kPtMmaWarp) {
-    // ---------------- products ----------------
-    if (lane == 0 && items > 0) {
+  } else if (warp == kPtScoreWarp) {
+    // ---------------- score products, three items ahead of the weights at most ----------------
+    if (lane == 0) {
       constexpr uint32_t iS = pt_idesc(FMT == ET_KV_E4M3 ? 0 : 1, 0, false, false, 128, 64);
       constexpr uint32_t iSt = pt_idesc(1, 1, false, false, 128, 64);
-      constexpr uint32_t iO = pt_idesc(0, 0, true, true, 128, 64), iOt = pt_idesc(1, 1, true, true, 128, 64);
-      auto scores = [&](int i) -> bool {  // item i into S buffer i % 3
+      for (int i = 0; i < items; ++i) {
         const int buf = i % 3;
         const uint32_t d = tmem + kPtColS + 64u * (uint32_t)buf;
-        if (i >= 3 && !pt_wait(bar(T_SFREE + buf), (uint32_t)(i / 3 - 1) & 1u, &s_abort, limit)) return false;
+        if (i >= 3 && !pt_wait(bar(T_SFREE + buf), (uint32_t)(i / 3 - 1) & 1u, &s_abort, limit)) break;
         if (tree && i == 0) {
           tc_fence_after();
 #pragma unroll
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           tc_commit(bar(T_TREE));
         } else {
           const int j = i - tree, stage = j % kPtStages;
-          if (!pt_wait(bar(T_KFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit)) return false;
+          if (!pt_wait(bar(T_KFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit)) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // the two terms of q one after the other
@@ -437,14 +438,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           if (j + kPtStages < n) tc_commit(bar(T_KEMPTY + stage));
         }
         tc_commit(bar(T_SFULL + buf));
-        return true;
-      };
-      bool ok = scores(0) && (items < 2 || scores(1));
-      for (int i = 0; ok && i < items; ++i) {
-        if (i + 2 < items && !scores(i + 2)) break;  // two ahead: a group finds its next scores when it has stored its weights
+      }
+      // every product this thread issued has finished before TMEM is freed
+      tc_commit(bar(T_DRAIN));
+      mbar_drain(bar(T_DRAIN), 0);
+    }
+  } else if (warp == kPtPvWarp) {
+    // ---------------- P.V products ----------------
+    if (lane == 0) {
+      constexpr uint32_t iO = pt_idesc(0, 0, true, true, 128, 64), iOt = pt_idesc(1, 1, true, true, 128, 64);
+      for (int i = 0; i < items; ++i) {
         const int w = i & 1;
-        const uint32_t phase = (uint32_t)(i >> 1) & 1u;
-        if (!pt_wait(bar(T_PFULL + w), phase, &s_abort, limit)) break;
+        if (!pt_wait(bar(T_PFULL + w), (uint32_t)(i >> 1) & 1u, &s_abort, limit)) break;
         tc_fence_after();
         const bool is_tree = tree && i == 0;
         const int steps = is_tree ? (a.N + 15) >> 4 : kPtKeys / 16;
@@ -454,9 +459,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                  sw128_desc(sb + kPtOffP + w * kPtP + kk * 2048, kPtHalf16, 1024), is_tree ? iOt : iO, (i >= 2 || kk > 0) ? 1u : 0u);
         tc_commit(bar(T_PVDONE + w));
       }
-      // every product this thread issued has finished before TMEM is freed
-      tc_commit(bar(T_DRAIN));
-      mbar_drain(bar(T_DRAIN), 0);
+      tc_commit(bar(T_DRAIN + 1));
+      mbar_drain(bar(T_DRAIN + 1), 0);
     }
   } else {
     // ---------------- softmax: group w, one key and half of the rows per thread ----------------
@@ -765,7 +769,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   __syncthreads();
   tc_fence_after();
   __syncwarp();
-  if (warp == kPtMmaWarp)
+  if (warp == kPtScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPtTmemCols) : "memory");
   if (chunks == 1) return;
   // ---- the chunks' rows, merged by the last block to arrive ----
