@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     uint4 raw[kQRounds], tk[kTreeRounds], tv[kTreeRounds];
 #pragma unroll
     for (int k = 0; k < kQRounds; ++k) {
-      const int r = (t >> 4) + k * (kPtThreads / 16), Rg = rt * kPtRows + r, i = Rg / a.G;
+      const int r = (t >> 4) + k * (kPtThreads / 16), Rg = rt * kPtRows + r, i = row_token(ma, Rg);
       raw[k] = make_uint4(0u, 0u, 0u, 0u);
       if (r < kPtRows && i < a.N)
         raw[k] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
     if (odd_v) s_odd = 1;
     if (t < kPtRows) {
-      const int i = (rt * kPtRows + t) / a.G;
+      const int i = row_token(ma, rt * kPtRows + t);
       unsigned long long m0 = 0ull, m1 = 0ull;
       if (i < a.N) {
         if (a.mask) {
@@ -700,11 +700,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const int real = min(kPtRows, a.N * a.G - rt * kPtRows);  // rows that exist are a prefix of the tile
   const long long tile_id = (long long)b * ma.tiles_y + blockIdx.y;
   auto place = [&](int r) -> long long {  // element index of row r in out
-    const int Rg = rt * kPtRows + r, i = Rg / a.G;
+    const int Rg = rt * kPtRows + r, i = row_token(ma, Rg);
     return (((long long)b * a.N + i) * a.Hq + g * a.G + (Rg - i * a.G)) * kPtD;
   };
   auto write_lse = [&](int r, float M, float sum) {
-    const int Rg = rt * kPtRows + r, i = Rg / a.G, h = g * a.G + (Rg - i * a.G);
+    const int Rg = rt * kPtRows + r, i = row_token(ma, Rg), h = g * a.G + (Rg - i * a.G);
     if (a.lse) a.lse[((long long)b * a.Hq + h) * a.N + i] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
   };
   // factors of the two groups' sums and the row's place, per row (short loops: cold code runs at the speed of its fetch)

@@ -34,7 +34,7 @@ struct PagedSplitArgs {
   unsigned int *cnt;    // [B * tiles_y] arrival counters
   float2 *part_ml;      // [B * tiles_y][S][R] (maximum, sum)
   float4 *part_o;       // [B * tiles_y][S][R][D] fp32
-  uint32_t page_magic;  // page_index
+  uint32_t page_magic, group_magic;  // page_index, row_token
   long long wait_cycles;
 };
 
@@ -56,6 +56,10 @@ constexpr float kPaTop = 3.f, kPaSlack = 12.f;
 __device__ __forceinline__ int page_index(const PagedSplitArgs &a, int token) {
   const uint32_t u = (uint32_t)token >> 4;
   return (int)(a.page_magic ? __umulhi(u, a.page_magic) : u);
+}
+// row of a KV head's (token, head in group) rows -> token: umulhi by ceil(2^32 / G) is exact below 2^32 / G rows
+__device__ __forceinline__ int row_token(const PagedSplitArgs &a, int row) {
+  return (int)(a.group_magic ? __umulhi((uint32_t)row, a.group_magic) : (uint32_t)row);
 }
 // prefix length of sequence b as the kernels use it: -1 = no sequence here
 __device__ __forceinline__ int paged_prefix(const PagedAttnArgs &a, int b, int &bad) {
