@@ -513,6 +513,9 @@ def et_static_tree_sampled(B: int, V: int, temperature: float, parent: torch.Ten
 _TORCH_DTYPE = {ET_BF16: torch.bfloat16, ET_F32: torch.float32}
 _KV_FORMAT = {torch.float8_e4m3fn: ET_KV_E4M3, torch.float8_e5m2: ET_KV_E5M2}
 _i32, _i64, _f32 = torch.int32, torch.int64, torch.float32
+# the device and stream without a Python frame each: a call's cost on the host is what a small one takes
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
 def _arg(t: Optional[torch.Tensor], dtype, shape, device: int, what: str) -> Optional[int]:
@@ -533,9 +536,9 @@ def _call(fn: str, device: int, stream: Optional[torch.cuda.Stream], *args) -> N
     """Run a call on the device of its tensors, on `stream` or that device's current stream."""
     if device < 0:
         raise ValueError(f"{fn} takes CUDA tensors")
-    f = getattr(load(), fn)
-    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if device == torch.cuda.current_device():
+    f = getattr(_lib or load(), fn)
+    s = _raw_stream(device) if stream is None else stream.cuda_stream
+    if device == _current_device():
         st = f(*args, s)
     else:
         with torch.cuda.device(device):

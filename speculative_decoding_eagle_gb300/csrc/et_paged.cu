@@ -173,29 +173,36 @@ __global__ void __launch_bounds__(kMapThreads) k_block_map(MapArgs a) {
   if (bad & ET_DEV_BAD_INDEX) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
   if (a.max_new == 0) return;  // uniform over the cluster
   cl_sync();  // the tables are written
-  // ---- slots ----
-  const long long cells = (long long)a.B * a.max_new;
-  for (long long x = first; x < cells; x += step) {
-    const int b = (int)(x / a.max_new), i = (int)(x - (long long)b * a.max_new);
-    long long slot = -1;
-    if (i < s_new[b]) {
-      const int pos = a.prefix_len[b] + i, blk = pos / a.P;  // need pages cover it: no overflow past max_blocks * P
-      const int page = __ldcg(a.block_table + (long long)b * a.max_blocks + blk);
-      if ((unsigned)page < (unsigned)a.num_pages) slot = (long long)page * a.P + (pos - blk * a.P);
-      else flag_status(a.dev_status, ET_DEV_BAD_INDEX);
+  // ---- slots: a warp per request ----
+  const int lane = t & 31, warps = blocks * (kMapThreads / 32);
+  for (int b = rank * (kMapThreads / 32) + (t >> 5); b < a.B; b += warps) {
+    const int count = s_new[b], len = count > 0 ? a.prefix_len[b] : 0;
+    const int32_t *row = a.block_table + (long long)b * a.max_blocks;
+    for (int i = lane; i < a.max_new; i += 32) {
+      long long slot = -1;
+      if (i < count) {
+        const int pos = len + i, blk = pos / a.P;  // need pages cover it: no overflow past max_blocks * P
+        const int page = __ldcg(row + blk);
+        if ((unsigned)page < (unsigned)a.num_pages) slot = (long long)page * a.P + (pos - blk * a.P);
+        else flag_status(a.dev_status, ET_DEV_BAD_INDEX);
+      }
+      a.slot_map[(long long)b * a.max_new + i] = slot;
     }
-    a.slot_map[x] = slot;
   }
 }
 
 // ---------------------------------------------------------------------------
 // commit
 // ---------------------------------------------------------------------------
-// One block per (page that receives rows, head, K or V, sequence): it alone
-// reads and writes that page's codes and scale, so nothing is shared and no
-// order matters.  Rows are read twice, once for the largest magnitude and
-// once to be coded; the second read hits L1 (a 64-token page of one head is
-// 16 KB of bf16).  Extra blocks copy the feature rows.
+// A unit of threads has one (page that receives rows, head, K or V, sequence):
+// it alone reads and writes that page's codes and scale, so nothing is shared
+// and no order matters.  An accepted path brings at most 17 rows to a page:
+// a warp is the unit, four to a block (32 sequences, 32 heads: 6.4 us with a
+// block per unit).  A prompt fills whole pages: a block is the unit.
+// Either way the rows stay in registers between the search for the largest
+// magnitude and the rounding, every load in flight at once; only a prompt's
+// pages of more rows than that (64 of 128 dims) are read twice.  Bound by
+// latency, a prompt by HBM.  Extra blocks copy the feature rows.
 constexpr int kCpThreads = 128;
 
 struct CommitPagedArgs {
@@ -213,24 +220,6 @@ struct CommitPagedArgs {
   int32_t *dev_status;
 };
 
-template <bool BF16>
-__device__ __forceinline__ void load8(const void *base, long long elem, float (&x)[8]) {
-  if (BF16) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + elem);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(w[e] << 16);
-      x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-  } else {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + elem);
-    const float4 u = p[0], v = p[1];
-    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-  }
-}
-
 // smallest 2^e >= amax / MAX, MAX = 0.875 * 2^TOP: amax = m 2^x with m in
 // [0.5, 1) needs x - TOP when m <= 0.875, one more otherwise
 template <int FMT>
@@ -243,50 +232,77 @@ __device__ __forceinline__ float page_scale(float amax) {
   return ldexpf(1.f, e);
 }
 
-template <bool BF16, int FMT, int D>
+// eight elements as they lie in memory, and as fp32
+template <bool BF16> struct Raw8 { uint4 v; };
+template <> struct Raw8<false> { float4 u, v; };
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> raw8(const void *base, long long elem) {
+  Raw8<BF16> r;
+  if constexpr (BF16) {
+    r.v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + elem);
+  } else {
+    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + elem);
+    r.u = p[0];
+    r.v = p[1];
+  }
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const Raw8<BF16> &r, float (&x)[8]) {
+  if constexpr (BF16) {
+    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+  } else {
+    x[0] = r.u.x; x[1] = r.u.y; x[2] = r.u.z; x[3] = r.u.w;
+    x[4] = r.v.x; x[5] = r.v.y; x[6] = r.v.z; x[7] = r.v.w;
+  }
+}
+
+// U threads per unit: 32 (a path's rows) or kCpThreads (a prompt's)
+template <bool BF16, int FMT, int D, int U>
 __global__ void __launch_bounds__(kCpThreads) k_commit_paged(CommitPagedArgs a) {
   constexpr int CH = D / 8;               // 8-element chunks per row
-  constexpr int RP = kCpThreads / CH;     // rows per pass
+  constexpr int RP = U / CH;              // rows per pass
+  constexpr int UN = kCpThreads / U;      // units per block
+  constexpr int KEEP = U == 32 ? (kMaxDepth + 1 + RP - 1) / RP : 8;  // passes whose rows stay in registers
   __shared__ float red[32];
   pdl_wait();     // the previous kernel in the stream has completed
   pdl_trigger();  // only now may the next kernel launch
-  const int tp = blockIdx.x, y = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
+  const int tp = blockIdx.x, b = blockIdx.z, t = threadIdx.x % U;
+  const int unit = blockIdx.y * UN + threadIdx.x / U, unit_blocks = (2 * a.Hkv + UN - 1) / UN;
   const int alen = a.accept_len[b], base = a.prefix_len[b];
   const bool alen_ok = alen >= -1 && alen < a.max_rows;
   const int rows = (alen_ok && base >= 0) ? alen + 1 : 0;  // rows appended
-  if (tp == 0 && y == 0 && t == 0) {
+  if (tp == 0 && unit == 0 && t == 0) {
     if (alen_ok) a.new_prefix_len[b] = base < 0 ? base : (int)min((long long)base + rows, 0x7fffffffll);
     else flag_status(a.dev_status, ET_DEV_BAD_INDEX);
   }
-  if (y >= 2 * a.Hkv) {  // ---- a feature row ----
+  if ((int)blockIdx.y >= unit_blocks) {  // ---- a feature row, by the whole block ----
     if (tp > 0) return;
-    const int i = y - 2 * a.Hkv;
+    const int i = blockIdx.y - unit_blocks;
     const int row = i < rows ? a.path[(long long)b * a.path_len + i] : -1;
     const bool ok = row >= 0 && row < a.N;
-    if (i < rows && !ok) return;  // flagged by the page's blocks; the row is skipped
+    if (i < rows && !ok) return;  // flagged by the page's units; the row is skipped
     uint4 *dst = a.feat_out + ((long long)b * a.path_len + i) * a.chunks_f;
     const uint4 *src = a.features + ((long long)b * a.N + (ok ? row : 0)) * a.chunks_f;
-    for (int c = t; c < a.chunks_f; c += kCpThreads) dst[c] = ok ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 4
+    for (int c = threadIdx.x; c < a.chunks_f; c += kCpThreads) dst[c] = ok ? src[c] : make_uint4(0u, 0u, 0u, 0u);
     return;
   }
   // ---- one page of one head ----
-  const int g = y >> 1;
-  const bool isV = y & 1;
+  const int g = unit >> 1;
+  const bool isV = unit & 1;
   const long long blk = base / a.P + tp;  // meaningless unless rows > 0
   const long long start = blk * a.P;      // first token of the page
   const long long end = (long long)base + rows;
-  if (rows == 0 || start >= end) return;
-  const int lo = start < base ? base - (int)start : 0;              // first row received
-  const int hi = end - start < a.P ? (int)(end - start) : a.P;      // one past the last
+  if (unit >= 2 * a.Hkv || rows == 0 || start >= end) return;  // the same in the whole unit
+  const int lo = start < base ? base - (int)start : 0;          // first row received
+  const int hi = end - start < a.P ? (int)(end - start) : a.P;  // one past the last
   const long long page = blk < a.max_blocks ? a.block_table[(long long)b * a.max_blocks + blk] : -1;
-  if (page < 0 || page >= a.num_pages) {
-    if (t == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
-    return;
-  }
-  uint8_t *codes = (isV ? a.v_pages : a.k_pages) + page * a.page_stride + (long long)g * a.P * D;
-  float *scale_at = (isV ? a.v_scale : a.k_scale) + page * a.Hkv + g;
-  const void *tree = isV ? a.v_tree : a.k_tree;
-  const float was = lo > 0 ? *scale_at : 0.f;
   const int c = t % CH, r0 = t / CH;
   const int skip = (int)(start - base);  // path index of the page's row 0 (may be negative)
   auto source = [&](int r) -> long long {  // element index of the row that page row r receives, -1: none
@@ -294,25 +310,51 @@ __global__ void __launch_bounds__(kCpThreads) k_commit_paged(CommitPagedArgs a) 
     const int row = a.path ? a.path[(long long)b * a.path_len + i] : i;
     return row >= 0 && row < a.N ? (((long long)b * a.N + row) * a.Hkv + g) * D + c * 8 : -1;
   };
-  float amax = 0.f;
+  const void *tree = isV ? a.v_tree : a.k_tree;
+  Raw8<BF16> held[KEEP];
+  bool have[KEEP];
   int bad = 0;
-#pragma unroll 4
-  for (int r = lo + r0; r < hi; r += RP) {
-    const long long src = source(r);
-    if (src < 0) {
-      bad |= ET_DEV_BAD_INDEX;
-      continue;
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    const int r = lo + r0 + k * RP;
+    have[k] = false;
+    if (r < hi) {
+      const long long src = source(r);
+      if (src < 0) bad |= ET_DEV_BAD_INDEX;
+      else {
+        have[k] = true;
+        held[k] = raw8<BF16>(tree, src);
+      }
     }
+  }
+  if (page < 0 || page >= a.num_pages) {
+    if (t == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
+    return;
+  }
+  uint8_t *codes = (isV ? a.v_pages : a.k_pages) + page * a.page_stride + (long long)g * a.P * D;
+  float *scale_at = (isV ? a.v_scale : a.k_scale) + page * a.Hkv + g;
+  const float was = lo > 0 ? *scale_at : 0.f;
+  float amax = 0.f;
+  auto see = [&](const Raw8<BF16> &r) {
     float x[8];
-    load8<BF16>(tree, src, x);
+    unpack8<BF16>(r, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float m = fabsf(x[e]);
       if (m <= FLT_MAX) amax = fmaxf(amax, m);
       else bad |= ET_DEV_NONFINITE;
     }
+  };
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k)
+    if (have[k]) see(held[k]);
+  for (int r = lo + r0 + KEEP * RP; r < hi; r += RP) {  // (a prompt's large pages)
+    const long long src = source(r);
+    if (src < 0) bad |= ET_DEV_BAD_INDEX;
+    else see(raw8<BF16>(tree, src));
   }
-  amax = block_max<kCpThreads>(amax, red);
+  if (U == 32) amax = warp_max(amax);
+  else amax = block_max<kCpThreads>(amax, red);
   const float need = page_scale<FMT>(amax);
   const bool was_ok = was > 0.f && was <= FLT_MAX;
   if (lo > 0 && !was_ok) bad |= ET_DEV_NONFINITE;
@@ -320,18 +362,22 @@ __global__ void __launch_bounds__(kCpThreads) k_commit_paged(CommitPagedArgs a) 
   // 1 / 2^e is exact; a scale of another origin divides
   const bool pow2 = (__float_as_uint(now) & 0x007fffffu) == 0u;
   const float inv = 1.f / now;
-#pragma unroll 4
-  for (int r = lo + r0; r < hi; r += RP) {
-    const long long src = source(r);
-    if (src < 0) continue;
+  auto put = [&](int r, const Raw8<BF16> &v) {
     float x[8];
-    load8<BF16>(tree, src, x);
+    unpack8<BF16>(v, x);
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       w[e] = pow2 ? f32x2_to_f8x2<FMT>(x[2 * e] * inv, x[2 * e + 1] * inv)
                   : f32x2_to_f8x2<FMT>(__fdiv_rn(x[2 * e], now), __fdiv_rn(x[2 * e + 1], now));
     *reinterpret_cast<uint2 *>(codes + (long long)r * D + c * 8) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  };
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k)
+    if (have[k]) put(lo + r0 + k * RP, held[k]);
+  for (int r = lo + r0 + KEEP * RP; r < hi; r += RP) {
+    const long long src = source(r);
+    if (src >= 0) put(r, raw8<BF16>(tree, src));
   }
   if (lo > 0 && was_ok && now > was) {  // the rows before, on the grown scale
     const float ratio = __fdiv_rn(was, now);
@@ -351,9 +397,15 @@ __global__ void __launch_bounds__(kCpThreads) k_commit_paged(CommitPagedArgs a) 
 }
 
 template <bool BF16, int FMT>
-et_status launch_commit(const CommitPagedArgs &a, int d, dim3 grid, cudaStream_t st) {
-  if (d == 64) return et_launch(k_commit_paged<BF16, FMT, 64>, grid, dim3(kCpThreads), 0, st, 0, a);
-  return et_launch(k_commit_paged<BF16, FMT, 128>, grid, dim3(kCpThreads), 0, st, 0, a);
+et_status launch_commit(const CommitPagedArgs &a, int d, int touch, int feature_rows, int B, cudaStream_t st) {
+  if (a.path) {  // a warp per unit
+    const dim3 grid(touch, (2 * a.Hkv + kCpThreads / 32 - 1) / (kCpThreads / 32) + feature_rows, B);
+    if (d == 64) return et_launch(k_commit_paged<BF16, FMT, 64, 32>, grid, dim3(kCpThreads), 0, st, 0, a);
+    return et_launch(k_commit_paged<BF16, FMT, 128, 32>, grid, dim3(kCpThreads), 0, st, 0, a);
+  }
+  const dim3 grid(touch, 2 * a.Hkv, B);
+  if (d == 64) return et_launch(k_commit_paged<BF16, FMT, 64, kCpThreads>, grid, dim3(kCpThreads), 0, st, 0, a);
+  return et_launch(k_commit_paged<BF16, FMT, 128, kCpThreads>, grid, dim3(kCpThreads), 0, st, 0, a);
 }
 
 }  // namespace
@@ -424,11 +476,11 @@ extern "C" et_status et_kv_commit_paged(const et_paged_commit_shape *s, const et
   a.feat_out = s->feat_dim > 0 ? static_cast<uint4 *>(feat_out) : nullptr;
   a.dev_status = dev_status;
   const int touch = (int)(((long long)a.max_rows + 2ll * a.P - 2) / a.P);  // pages max_rows rows can lie in
-  const dim3 grid(touch, 2 * a.Hkv + (s->feat_dim > 0 ? s->path_len : 0), s->B);
+  const int feature_rows = s->feat_dim > 0 ? s->path_len : 0;
   cudaStream_t st = (cudaStream_t)stream;
   if (s->dtype == ET_BF16)
-    return cache->format == ET_KV_E4M3 ? launch_commit<true, ET_KV_E4M3>(a, cache->d, grid, st)
-                                       : launch_commit<true, ET_KV_E5M2>(a, cache->d, grid, st);
-  return cache->format == ET_KV_E4M3 ? launch_commit<false, ET_KV_E4M3>(a, cache->d, grid, st)
-                                     : launch_commit<false, ET_KV_E5M2>(a, cache->d, grid, st);
+    return cache->format == ET_KV_E4M3 ? launch_commit<true, ET_KV_E4M3>(a, cache->d, touch, feature_rows, s->B, st)
+                                       : launch_commit<true, ET_KV_E5M2>(a, cache->d, touch, feature_rows, s->B, st);
+  return cache->format == ET_KV_E4M3 ? launch_commit<false, ET_KV_E4M3>(a, cache->d, touch, feature_rows, s->B, st)
+                                     : launch_commit<false, ET_KV_E5M2>(a, cache->d, touch, feature_rows, s->B, st);
 }

@@ -20,16 +20,17 @@ namespace {
 // ---------------------------------------------------------------------------
 // fp32: CUDA cores, one block per (row, head, sequence)
 // ---------------------------------------------------------------------------
-// Each warp takes every fourth group of 32 keys: a lane scores one key (its
+// Each warp takes every eighth group of 32 keys: a lane scores one key (its
 // whole row, 16 bytes a load), the group's maximum and sum are warp
 // reductions, then the lanes turn to the head's dims and add the 32 weighted
 // V rows, whose loads do not depend on one another.
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 template <int FMT, int D>
-__global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
+__global__ void __launch_bounds__(kRowThreads) k_paged_attn_row(PagedAttnArgs a) {
   constexpr int PL = D / 32;  // dims per lane
   __shared__ float qs[D];
-  __shared__ float wm[4], wl[4];
-  __shared__ float wacc[4][D];
+  __shared__ float wm[kRowWarps], wl[kRowWarps];
+  __shared__ float wacc[kRowWarps][D];
   pdl_wait();     // the previous kernel in the stream has completed
   pdl_trigger();  // only now may the next kernel launch
   const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
@@ -38,14 +39,14 @@ __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
   const int L = paged_prefix(a, b, bad);
   if (L < 0) return;
   const long long orow = ((long long)b * a.N + i) * a.Hq + h;
-  for (int c = t; c < D; c += 128) qs[c] = static_cast<const float *>(a.q)[orow * D + c];
+  for (int c = t; c < D; c += kRowThreads) qs[c] = static_cast<const float *>(a.q)[orow * D + c];
   __syncthreads();
   const float *KT = static_cast<const float *>(a.kt), *VT = static_cast<const float *>(a.vt);
   float m = -INFINITY, l = 0.f, acc[PL];
 #pragma unroll
   for (int c = 0; c < PL; ++c) acc[c] = 0.f;
   const int nP = (L + 31) / 32, nT = (a.N + 31) / 32;
-  for (int grp = warp; grp < nP + nT; grp += 4) {
+  for (int grp = warp; grp < nP + nT; grp += kRowWarps) {
     const bool cached = grp < nP;
     const int j = cached ? grp * 32 + lane : (grp - nP) * 32 + lane;
     bool ok = cached ? j < L : (j < a.N && tree_keeps(a, b, i, j));
@@ -81,8 +82,14 @@ __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
       }
       s *= ks;
     } else if (ok) {
-#pragma unroll 8
-      for (int c = 0; c < D; ++c) s = fmaf(qs[c], KT[at + c], s);
+#pragma unroll
+      for (int c = 0; c < D / 4; ++c) {
+        const float4 v = *reinterpret_cast<const float4 *>(KT + at + 4 * c);
+        s = fmaf(qs[4 * c], v.x, s);
+        s = fmaf(qs[4 * c + 1], v.y, s);
+        s = fmaf(qs[4 * c + 2], v.z, s);
+        s = fmaf(qs[4 * c + 3], v.w, s);
+      }
     }
     s = ok ? s * a.scale_log2 : -INFINITY;
     const unsigned int keep = __ballot_sync(0xffffffffu, ok);
@@ -95,30 +102,42 @@ __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
     for (int c = 0; c < PL; ++c) acc[c] *= corr;
     m = mn;
     const float pv = p * vs;
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-      const float w = __shfl_sync(0xffffffffu, pv, k);
-      const long long row = __shfl_sync(0xffffffffu, at, k);
-      if (!((keep >> k) & 1u)) continue;
-      float x[PL];
-      if (cached) {
-        if (PL == 4) {
-          float y[4];
-          f8x4_to_f32<FMT>(*reinterpret_cast<const uint32_t *>(a.v_pages + row + 4 * lane), y);
+#pragma unroll 1
+    for (int k0 = 0; k0 < 32; k0 += 16) {
+      uint32_t code[16];
+      float xt[16][PL];
 #pragma unroll
-          for (int c = 0; c < PL; ++c) x[c] = y[c];
-        } else {
-          const uint32_t hv = f8x2_to_f16x2<FMT>(*reinterpret_cast<const uint16_t *>(a.v_pages + row + 2 * lane));
-          const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&hv));
-          x[0] = y.x;
-          x[1] = y.y;
+      for (int k = 0; k < 16; ++k) {  // sixteen rows' loads in flight
+        const long long row = __shfl_sync(0xffffffffu, at, k0 + k);
+        const bool on = (keep >> (k0 + k)) & 1u;
+        code[k] = 0u;
+#pragma unroll
+        for (int c = 0; c < PL; ++c) xt[k][c] = 0.f;
+        if (on && cached) {
+          if (PL == 4) code[k] = *reinterpret_cast<const uint32_t *>(a.v_pages + row + 4 * lane);
+          else code[k] = *reinterpret_cast<const uint16_t *>(a.v_pages + row + 2 * lane);
+        } else if (on) {
+#pragma unroll
+          for (int c = 0; c < PL; c += 2) {
+            const float2 y = *reinterpret_cast<const float2 *>(VT + row + PL * lane + c);
+            xt[k][c] = y.x;
+            xt[k][c + 1] = y.y;
+          }
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < PL; ++c) x[c] = VT[row + PL * lane + c];
       }
 #pragma unroll
-      for (int c = 0; c < PL; ++c) acc[c] = fmaf(w, x[c], acc[c]);
+      for (int k = 0; k < 16; ++k) {
+        const float w = __shfl_sync(0xffffffffu, pv, k0 + k);
+        if (!((keep >> (k0 + k)) & 1u)) continue;
+        if (cached) {
+          float y[4];
+          f8x4_to_f32<FMT>(code[k], y);
+#pragma unroll
+          for (int c = 0; c < PL; ++c) xt[k][c] = y[c];
+        }
+#pragma unroll
+        for (int c = 0; c < PL; ++c) acc[c] = fmaf(w, xt[k][c], acc[c]);
+      }
     }
   }
   if (lane == 0) {
@@ -130,17 +149,17 @@ __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
   __syncthreads();
   float M = wm[0];
 #pragma unroll
-  for (int w = 1; w < 4; ++w) M = fmaxf(M, wm[w]);
-  float Ls = 0.f, wts[4];
+  for (int w = 1; w < kRowWarps; ++w) M = fmaxf(M, wm[w]);
+  float Ls = 0.f, wts[kRowWarps];
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < kRowWarps; ++w) {
     wts[w] = wm[w] == -INFINITY ? 0.f : exp2f(wm[w] - M);
     Ls += wl[w] * wts[w];
   }
-  for (int c = t; c < D; c += 128) {
+  for (int c = t; c < D; c += kRowThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) v += wacc[w][c] * wts[w];
+    for (int w = 0; w < kRowWarps; ++w) v += wacc[w][c] * wts[w];
     static_cast<float *>(a.out)[orow * D + c] = Ls == 0.f ? 0.f : v / Ls;
   }
   if (t == 0 && a.lse)
@@ -151,8 +170,8 @@ __global__ void __launch_bounds__(128) k_paged_attn_row(PagedAttnArgs a) {
 template <int FMT>
 et_status launch_row(const PagedAttnArgs &a, int d, cudaStream_t st) {
   const dim3 grid(a.N, a.Hq, a.B);
-  if (d == 64) return et_launch(k_paged_attn_row<FMT, 64>, grid, dim3(128), 0, st, 0, a);
-  return et_launch(k_paged_attn_row<FMT, 128>, grid, dim3(128), 0, st, 0, a);
+  if (d == 64) return et_launch(k_paged_attn_row<FMT, 64>, grid, dim3(kRowThreads), 0, st, 0, a);
+  return et_launch(k_paged_attn_row<FMT, 128>, grid, dim3(kRowThreads), 0, st, 0, a);
 }
 
 // ---------------------------------------------------------------------------
