@@ -28,6 +28,7 @@ namespace {
 constexpr int kMapThreads = 1024;
 constexpr int kMapMaxB = 4096;
 constexpr int kMapCluster = 8;  // portable cluster size
+constexpr int kMapBatch = 4;    // items a thread has in flight
 
 struct MapArgs {
   int B, P, max_blocks, max_new, num_pages;
@@ -76,6 +77,7 @@ __global__ void __launch_bounds__(kMapThreads) k_block_map(MapArgs a) {
   int *s_need = cum_take + a.B + 1;       // [B] pages after this call
   int *s_have = s_need + a.B;             // [B] pages before, -1: the request is left alone
   int *s_new = s_have + a.B;              // [B] slots to write
+  int *s_len = s_new + a.B;               // [B] tokens before them
   pdl_wait();     // the previous kernel in the stream has completed
   pdl_trigger();  // only now may the next kernel launch
   const int t = threadIdx.x, rank = blockIdx.x, blocks = gridDim.x;
@@ -104,6 +106,7 @@ __global__ void __launch_bounds__(kMapThreads) k_block_map(MapArgs a) {
       s_need[b] = need;
       s_have[b] = ok ? have : -1;
       s_new[b] = ok ? add : 0;
+      s_len[b] = len;
       if (ok) {
         back = have > need ? have - need : 0;
         miss = need > have ? need - have : 0;
@@ -148,21 +151,41 @@ __global__ void __launch_bounds__(kMapThreads) k_block_map(MapArgs a) {
     const int b = find_request(cum_take, a.B, turn);
     a.block_table[(long long)b * a.max_blocks + s_have[b] + (turn - cum_take[b])] = page;
   };
-  for (int r = first; r < R; r += step) {
-    const int b = find_request(cum_back, a.B, r);
-    int32_t *cell = a.block_table + (long long)b * a.max_blocks + s_need[b] + (r - cum_back[b]);
-    const int page = *cell, place = F + r;
-    if ((unsigned)page >= (unsigned)a.num_pages) bad = ET_DEV_BAD_INDEX;
-    if (place >= left) give(top - 1 - place, page);
-    else if (place < a.num_pages) a.free_list[place] = page;
-    *cell = -1;
+  for (int r0 = first; r0 < R; r0 += kMapBatch * step) {  // loads of a batch first: each is a trip to L2
+    int32_t *cell[kMapBatch];
+    int page[kMapBatch];
+#pragma unroll
+    for (int k = 0; k < kMapBatch; ++k) {
+      const int r = r0 + k * step;
+      if (r >= R) continue;
+      const int b = find_request(cum_back, a.B, r);
+      cell[k] = a.block_table + (long long)b * a.max_blocks + s_need[b] + (r - cum_back[b]);
+      page[k] = *cell[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kMapBatch; ++k) {
+      const int place = F + r0 + k * step;
+      if (r0 + k * step >= R) continue;
+      if ((unsigned)page[k] >= (unsigned)a.num_pages) bad = ET_DEV_BAD_INDEX;
+      if (place >= left) give(top - 1 - place, page[k]);
+      else if (place < a.num_pages) a.free_list[place] = page[k];
+      *cell[k] = -1;
+    }
   }
-  for (int k = first; k < A; k += step) {
-    const int place = top - 1 - k;
-    if (place >= F) continue;  // a returned page: its own thread moves it
-    const int page = a.free_list[place];
-    if ((unsigned)page >= (unsigned)a.num_pages) bad = ET_DEV_BAD_INDEX;
-    give(k, page);
+  for (int k0 = first; k0 < A; k0 += kMapBatch * step) {
+    int page[kMapBatch];
+#pragma unroll
+    for (int k = 0; k < kMapBatch; ++k) {
+      const int turn = k0 + k * step, place = top - 1 - turn;
+      page[k] = turn < A && place < F ? a.free_list[place] : 0;  // (a returned page: its own thread moves it)
+    }
+#pragma unroll
+    for (int k = 0; k < kMapBatch; ++k) {
+      const int turn = k0 + k * step;
+      if (turn >= A || top - 1 - turn >= F) continue;
+      if ((unsigned)page[k] >= (unsigned)a.num_pages) bad = ET_DEV_BAD_INDEX;
+      give(turn, page[k]);
+    }
   }
   for (int b = first; b < a.B; b += step)
     if (s_have[b] >= 0) a.n_blocks[b] = s_need[b];
@@ -176,8 +199,9 @@ __global__ void __launch_bounds__(kMapThreads) k_block_map(MapArgs a) {
   // ---- slots: a warp per request ----
   const int lane = t & 31, warps = blocks * (kMapThreads / 32);
   for (int b = rank * (kMapThreads / 32) + (t >> 5); b < a.B; b += warps) {
-    const int count = s_new[b], len = count > 0 ? a.prefix_len[b] : 0;
+    const int count = s_new[b], len = s_len[b];
     const int32_t *row = a.block_table + (long long)b * a.max_blocks;
+#pragma unroll 4
     for (int i = lane; i < a.max_new; i += 32) {
       long long slot = -1;
       if (i < count) {
@@ -433,8 +457,8 @@ extern "C" et_status et_block_map(const et_block_map_shape *s, const int32_t *pr
   a.n_blocks = n_blocks; a.block_table = block_table; a.free_list = free_list; a.free_count = free_count;
   a.slot_map = reinterpret_cast<long long *>(slot_map);
   a.dev_status = dev_status;
-  const int smem = (5 * s->B + 2) * (int)sizeof(int);
-  const int largest = (5 * kMapMaxB + 2) * (int)sizeof(int);  // the attribute is set once, for every B
+  const int smem = (6 * s->B + 2) * (int)sizeof(int);
+  const int largest = (6 * kMapMaxB + 2) * (int)sizeof(int);  // the attribute is set once, for every B
   ET_RETURN_IF(et_smem_attr((const void *)k_block_map, largest) != cudaSuccess, ET_ERR_CUDA);
   return et_launch(k_block_map, dim3(kMapCluster), dim3(kMapThreads), smem, (cudaStream_t)stream, kMapCluster, a);
 }
