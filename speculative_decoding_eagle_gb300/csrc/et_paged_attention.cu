@@ -200,8 +200,8 @@ template <int D, int WR, int MT>
 struct PaShape {
   static constexpr int KG = kPaWarps / WR;
   static constexpr int R = 16 * WR * MT;
-  // two blocks fit an SM's shared memory with these (64 or 96 KB of tiles each)
-  static constexpr int kStages = WR == 2 ? 4 : MT == 1 ? 3 : 2;
+  static constexpr int kBlocks = MT == 1 ? 3 : 2;           // resident blocks per SM
+  static constexpr int kStages = WR == 2 ? 4 : 2;           // 64 KB of tiles a block
   static constexpr int kTileBytes = kPaTile * D;            // K or V
   static constexpr int kRing = KG * kStages * 2 * kTileBytes;
   static constexpr int kOffQ = kRing;                       // lifted fp16, fragment order
@@ -211,7 +211,7 @@ struct PaShape {
   static constexpr int kBytes = kOffBar + KG * kStages * 8 + 1024;  // + slack for 1024-byte alignment
   static_assert(KG * R * D * 4 + KG * R * 8 <= kOffRow, "the groups' rows are merged in the space of the ring and q");
   static_assert((kPaMaxSplits + 1) * R * 8 <= kOffRow, "the chunks' pairs, too");
-  static_assert(2 * (kBytes + 1024 + 64) <= 228 * 1024, "two blocks per SM");
+  static_assert(kBlocks * (kBytes + 1024 + 64) <= 228 * 1024, "the blocks of an SM");
 };
 
 template <bool BF16>
@@ -317,7 +317,7 @@ __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const
 }
 
 template <int D, int FMT, int WR, int MT>
-__global__ void __launch_bounds__(kPaThreads, 2)
+__global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
     k_paged_attn_mma(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ PagedSplitArgs ma) {
   using Sh = PaShape<D, WR, MT>;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   }
   if (L < 0) return;
   const int T = (L + kPaTile - 1) / kPaTile, Tl = (longest + kPaTile - 1) / kPaTile;
-  const int per = max((Tl + ma.S - 1) / ma.S, ma.min_tiles);
+  const int per = max((Tl + ma.S - 1) / ma.S, 1);
   const int chunks = max(1, (T + per - 1) / per);
   if (chunk >= chunks) return;
   const int t0 = chunk * per, t1 = min(T, t0 + per);
@@ -813,8 +813,6 @@ struct PagedPlan {
   size_t ml_off, o_off;
 };
 
-constexpr int kPaMinTiles = 2;  // tiles of a chunk at least
-
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -823,6 +821,8 @@ int sm_count() {
   cudaGetLastError();
   return n;
 }
+
+long long least(long long a, long long b) { return a < b ? a : b; }
 
 // Chunks of the tcgen05 kernel, one block per SM.  A block costs about twelve of its 128-key tiles before its first and
 // after its last (measured: 15.6 against 1.3 us), a merge about five.  One sequence: whole waves of equal blocks.
@@ -869,9 +869,18 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   const int T = (int)(((s->max_prefix < room ? s->max_prefix : room) + tile - 1) / tile);
   int S = s->num_splits;
   if (S <= 0) {
-    S = p->tc ? tc_splits(tiles, T, s->B) : (int)((s->B > 1 ? 4ll : 1ll) * 2 * sm_count() / tiles);
-    const int by_tiles = p->tc ? T : T / (2 * kPaMinTiles);
-    if (S > by_tiles) S = by_tiles;
+    if (p->tc) {
+      S = tc_splits(tiles, T, s->B);
+    } else if (s->B == 1) {
+      // one block per SM, of eight 32-key tiles at least (8 KV heads, prefix 16384: 20.7 us in 19 chunks, 21.9 in 38)
+      S = (int)least(sm_count() / tiles, T / 8);
+    } else {
+      // sequences of any length: a wave of three blocks per SM of eight tiles at least; many waves only of long chunks
+      // (8 KV heads, 512..16384 tokens: 16 sequences 66.9 us in 4 chunks, 64.9 in 16; 4
+      // sequences 57 us in 64, 43 in 16)
+      const long long wave = least(3ll * sm_count() / tiles, T / 8), waves = least(14ll * sm_count() / tiles, T / 32);
+      S = (int)(waves >= 2 * wave ? waves : wave);
+    }
   }
   if (S > T) S = T;
   if (S > kPaMaxSplits) S = kPaMaxSplits;
@@ -939,7 +948,6 @@ extern "C" et_status et_tree_attention_paged(const et_paged_attn_shape *shape, c
   ma.row_tiles = plan.row_tiles;
   ma.tiles_y = cache->Hkv * plan.row_tiles;
   ma.box = cache->page_size % kPaTile == 0 ? kPaTile : 16;
-  ma.min_tiles = shape->num_splits > 0 ? 1 : kPaMinTiles;
   unsigned char *wsb = static_cast<unsigned char *>(ws);
   ma.cnt = plan.S > 1 ? reinterpret_cast<unsigned int *>(wsb) : nullptr;
   ma.part_ml = plan.S > 1 ? reinterpret_cast<float2 *>(wsb + plan.ml_off) : nullptr;

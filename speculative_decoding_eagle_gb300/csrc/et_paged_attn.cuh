@@ -30,7 +30,6 @@ struct PagedSplitArgs {
   int S, tiles_y;       // chunks, Hkv * row tiles
   int row_tiles;        // row tiles per KV head
   int box;              // rows per TMA box
-  int min_tiles;        // smallest chunk, in tiles
   unsigned int *cnt;    // [B * tiles_y] arrival counters
   float2 *part_ml;      // [B * tiles_y][S][R] (maximum, sum)
   float4 *part_o;       // [B * tiles_y][S][R][D] fp32

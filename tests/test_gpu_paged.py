@@ -638,3 +638,145 @@ def test_a_served_batch_over_several_steps():
         lens = lens + halen + 1
         np.testing.assert_array_equal(dlens.cpu().numpy(), lens)
     assert int(status.item()) == 0
+
+
+# ---------------------------------------------------------------------------
+# many sequences, many chunks, shared workspaces, waits that run out
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("B,N,Hq,Hkv,d", [(150, 1, 2, 1, 128), (150, 9, 4, 2, 64), (650, 17, 1, 1, 128)])
+def test_batches_past_one_block_of_lengths(B, N, Hq, Hkv, d):
+    # the kernels read a batch's lengths with one thread each up to their block's size, else take the bound
+    rng = np.random.default_rng(B + N)
+    lens = rng.integers(-1, 60, B)
+    lens[B // 2], lens[-1] = 300, 200
+    pool = Pool(rng, list(lens), 16, Hkv, d, "e4m3")
+    keep = random_tree(rng, B, N)
+    r = run_attention(pool, B, N, Hq, "bf16", rng, keep, splits=3)
+    picked = [0, 1, B // 2, B // 2 + 1, B - 2, B - 1]
+    got, glse = r["out"].double().cpu().numpy(), r["lse"].double().cpu().numpy()
+    for b in picked:
+        if lens[b] < 0:
+            assert (got[b] == 7).all()
+            continue
+        kc, vc = pool.sequence(b)
+        ref = O.paged_attention(r["q"][b], kc, vc, r["kt"][b], r["vt"][b], np.ones(lens[b], bool), keep[b], d ** -0.5)
+        check_attention(got[b], glse[b], ref, d, "bf16", int(lens[b]), N * Hq // Hkv)
+    assert int(r["status"].item()) == 0
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,d", [(1, 4, 2, 128), (30, 2, 1, 128), (30, 2, 1, 64), (70, 1, 1, 64)])
+@pytest.mark.parametrize("splits", [1, 2, 7, 64, 1000])
+def test_every_number_of_chunks_gives_the_same_sums(N, Hq, Hkv, d, splits):
+    rng = np.random.default_rng(3)
+    pool = Pool(rng, [900, 1, 130], 48, Hkv, d, "e5m2")
+    keep = random_tree(rng, 3, N)
+    r = run_attention(pool, 3, N, Hq, "bf16", rng, keep, splits)
+    assert E.et_tree_attention_paged_splits(r["shape"], pool.cache) <= 64
+    check_all(pool, r, keep, "bf16")
+
+
+@pytest.mark.parametrize("N", [1, 61])
+def test_a_loose_prefix_bound_changes_nothing_but_the_plan(N):
+    rng = np.random.default_rng(5)
+    pool = Pool(rng, [100, 40], 16, 2, 128, "e4m3", cols=400)
+    keep = random_tree(rng, 2, N)
+    r = run_attention(pool, 2, N, 4, "bf16", rng, keep, max_prefix=6000)
+    check_all(pool, r, keep, "bf16")
+    assert int(r["status"].item()) == 0
+
+
+@pytest.mark.parametrize("N", [1, 61])
+def test_graphs_and_streams(N):
+    """Two captured graphs that use one workspace one after the other, and two streams with one each."""
+    rng = np.random.default_rng(23)
+    pool = Pool(rng, [500, 90], 32, 2, 128, "e4m3")
+    keep = random_tree(rng, 2, N)
+    runs = [run_attention(pool, 2, N, 4, "bf16", rng, keep, splits=3) for _ in range(2)]
+    want = [r["out"].clone() for r in runs]
+    graphs = []
+    for r in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            E.et_tree_attention_paged(*r["args"], lse=r["lse"], ws=runs[0]["ws"], dev_status=r["status"])
+        graphs.append(g)
+    for _ in range(5):
+        for r, g in zip(runs, graphs):
+            r["out"].zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    for r, w in zip(runs, want):
+        assert torch.equal(r["out"], w)
+        r["out"].zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for r, s in zip(runs, streams):
+            E.et_tree_attention_paged(*r["args"], lse=r["lse"], ws=r["ws"], dev_status=r["status"], stream=s)
+    torch.cuda.synchronize()
+    for r, w in zip(runs, want):
+        assert torch.equal(r["out"], w) and int(r["status"].item()) == 0
+
+
+@pytest.mark.parametrize("N,d,splits", [(1, 128, 1), (1, 128, 3), (61, 128, 1), (61, 128, 3), (61, 64, 2)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(N, d, splits):
+    rng = np.random.default_rng(17)
+    pool = Pool(rng, [900, 300], 64, 2, d, "e4m3")
+    keep = random_tree(rng, 2, N)
+    r = run_attention(pool, 2, N, 4, "bf16", rng, keep, splits)
+    want = r["out"].clone()
+    before = E.et_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            E.et_tree_attention_paged(*r["args"], lse=r["lse"], ws=r["ws"], dev_status=r["status"])
+        torch.cuda.synchronize()
+    finally:
+        E.et_set_wait_limit(before if before < 1 << 32 else 0)
+    # one wait may last some microseconds by itself: the mma.sync kernel's copies may land within its first
+    status = int(r["status"].item())
+    assert status == E.ET_DEV_TIMEOUT or (status == 0 and (N == 1 or d == 64) and torch.equal(r["out"], want))
+    r["status"].zero_()
+    E.et_tree_attention_paged(*r["args"], lse=r["lse"], ws=r["ws"], dev_status=r["status"])
+    torch.cuda.synchronize()
+    assert torch.equal(r["out"], want) and int(r["status"].item()) == 0
+
+
+def test_commit_and_map_in_a_graph():
+    """A captured step that maps a block, commits a path and maps again replays like eager calls."""
+    rng = np.random.default_rng(31)
+    B, N, Hkv, d, P, D, cols = 3, 9, 2, 64, 16, 3, 4
+    m = Map(B, cols, B * cols, D + 1, P)
+    cache = E.PagedCache.allocate(B * cols, Hkv, P, d, torch.float8_e5m2)
+    lens = torch.tensor([14, 0, 15], dtype=torch.int32, device="cuda")
+    new, more = torch.full_like(lens, D + 1), torch.zeros_like(lens)
+    kt, vt = (dev(rounded(rng, "bf16", B, N, Hkv, d)).bfloat16() for _ in range(2))
+    path = torch.tensor([[0, 2, 5, 7]] * B, dtype=torch.int32, device="cuda")
+    alen = torch.tensor([3, 1, 2], dtype=torch.int32, device="cuda")
+    shape = E.PagedCommitShape(B=B, N=N, path_len=D + 1, max_blocks=cols)
+
+    def step():
+        E.et_block_map(m.shape, lens, new, m.n, m.table, m.free, m.count, m.slots, dev_status=m.status)
+        E.et_kv_commit_paged(shape, cache, m.table, kt, vt, alen, path, lens, more, dev_status=m.status)
+        lens.copy_(more)
+    first = [t.clone() for t in (lens, m.n, m.table, m.free, m.count)]
+    for _ in range(3):
+        step()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (lens, m.n, m.table, m.free, m.count, m.slots, cache.k_pages.view(torch.uint8),
+                                cache.v_pages.view(torch.uint8), cache.k_scale, cache.v_scale)]
+    for t, f in zip((lens, m.n, m.table, m.free, m.count), first):
+        t.copy_(f)
+    cache.k_pages.view(torch.uint8).zero_()
+    cache.v_pages.view(torch.uint8).zero_()
+    cache.k_scale.fill_(1)
+    cache.v_scale.fill_(1)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    got = (lens, m.n, m.table, m.free, m.count, m.slots, cache.k_pages.view(torch.uint8),
+           cache.v_pages.view(torch.uint8), cache.k_scale, cache.v_scale)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert int(m.status.item()) == 0
