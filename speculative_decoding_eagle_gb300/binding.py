@@ -532,6 +532,14 @@ def _status(t: Optional[torch.Tensor], device: int) -> Optional[int]:
     return None if t is None else _arg(t, _i32, (1,), device, "dev_status")
 
 
+def _refuse(device: int, *args) -> None:
+    """Name the argument that the caller's one-expression check found wrong (the checks are written out in the calls:
+    a Python frame per argument would take longer than a small kernel)."""
+    for a in args:
+        _arg(a[0], a[1], a[2], device, a[3])
+    raise ValueError("arguments must be contiguous tensors on one CUDA device")
+
+
 def _call(fn: str, device: int, stream: Optional[torch.cuda.Stream], *args) -> None:
     """Run a call on the device of its tensors, on `stream` or that device's current stream."""
     if device < 0:
@@ -547,16 +555,15 @@ def _call(fn: str, device: int, stream: Optional[torch.cuda.Stream], *args) -> N
         raise EtError(fn, st)
 
 
-class _Shape:
-    """A frozen shape whose C struct is built once."""
-
-    def ref(self):
-        r = self.__dict__.get("_ref")
-        if r is None:
-            c = self.c()
-            r = ctypes.byref(c)  # keeps c alive
-            self.__dict__["_ref"] = r
-        return r
+def _kept(shape, key, make):
+    """What follows from a frozen shape (and a cache's geometry), made once: its C struct and its tensors' shapes."""
+    made = shape.__dict__.get("_made")
+    if made is None:
+        made = shape.__dict__["_made"] = {}
+    v = made.get(key)
+    if v is None:
+        v = made[key] = make()
+    return v
 
 
 class PagedCache:
@@ -597,7 +604,7 @@ class PagedCache:
 
 
 @dataclasses.dataclass(frozen=True)
-class BlockMapShape(_Shape):
+class BlockMapShape:
     B: int
     page_size: int
     max_blocks: int
@@ -613,17 +620,25 @@ def et_block_map(shape: BlockMapShape, prefix_len: torch.Tensor, new_len: torch.
                  slot_map: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
                  stream=None) -> None:
     """Return and take pages so that each request holds its length, and map its new tokens to slots."""
-    B, dev = (shape.B,), n_blocks.get_device()
-    _call("et_block_map", dev, stream, shape.ref(), _arg(prefix_len, _i32, B, dev, "prefix_len"),
-          _arg(new_len, _i32, B, dev, "new_len"), _arg(n_blocks, _i32, B, dev, "n_blocks"),
-          _arg(block_table, _i32, (shape.B, shape.max_blocks), dev, "block_table"),
-          _arg(free_list, _i32, (shape.num_pages,), dev, "free_list"),
-          _arg(free_count, _i32, (1,), dev, "free_count"),
-          _arg(slot_map, _i64, (shape.B, shape.max_new), dev, "slot_map"), _status(dev_status, dev))
+    ref, B, table, pool, slots = _kept(shape, None, lambda: (
+        ctypes.byref(shape.c()), (shape.B,), (shape.B, shape.max_blocks), (shape.num_pages,), (shape.B, shape.max_new)))
+    dev = n_blocks.get_device()
+    if not (prefix_len.dtype is new_len.dtype is n_blocks.dtype is block_table.dtype is free_list.dtype
+            is free_count.dtype is _i32 and prefix_len.shape == B and new_len.shape == B and n_blocks.shape == B
+            and block_table.shape == table and free_list.shape == pool and free_count.shape == (1,)
+            and prefix_len.get_device() == new_len.get_device() == block_table.get_device() == free_list.get_device()
+            == free_count.get_device() == dev and prefix_len.is_contiguous() and new_len.is_contiguous()
+            and n_blocks.is_contiguous() and block_table.is_contiguous() and free_list.is_contiguous()):
+        _refuse(dev, (prefix_len, _i32, B, "prefix_len"), (new_len, _i32, B, "new_len"),
+                (n_blocks, _i32, B, "n_blocks"), (block_table, _i32, table, "block_table"),
+                (free_list, _i32, pool, "free_list"), (free_count, _i32, (1,), "free_count"))
+    _call("et_block_map", dev, stream, ref, prefix_len.data_ptr(), new_len.data_ptr(), n_blocks.data_ptr(),
+          block_table.data_ptr(), free_list.data_ptr(), free_count.data_ptr(),
+          _arg(slot_map, _i64, slots, dev, "slot_map"), None if dev_status is None else _status(dev_status, dev))
 
 
 @dataclasses.dataclass(frozen=True)
-class PagedCommitShape(_Shape):
+class PagedCommitShape:
     B: int
     N: int
     path_len: int
@@ -641,19 +656,30 @@ def et_kv_commit_paged(shape: PagedCommitShape, cache: PagedCache, block_table: 
                        features: Optional[torch.Tensor] = None, feat_out: Optional[torch.Tensor] = None,
                        dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantise each sequence's accepted path (``path`` None: its first accept_len + 1 rows) into its pages."""
-    dt, dev, B, N = _TORCH_DTYPE[shape.dtype], cache.device, shape.B, shape.N
-    tree = (B, N, cache.Hkv, cache.d)
-    _call("et_kv_commit_paged", dev, stream, shape.ref(), cache._ref,
-          _arg(block_table, _i32, (B, shape.max_blocks), dev, "block_table"), _arg(k_tree, dt, tree, dev, "k_tree"),
-          _arg(v_tree, dt, tree, dev, "v_tree"), _arg(accept_len, _i32, (B,), dev, "accept_len"),
-          _arg(path, _i32, (B, shape.path_len), dev, "path"), _arg(prefix_len, _i32, (B,), dev, "prefix_len"),
-          _arg(new_prefix_len, _i32, (B,), dev, "new_prefix_len"),
-          _arg(features, dt, (B, N, shape.feat_dim), dev, "features"),
-          _arg(feat_out, dt, (B, shape.path_len, shape.feat_dim), dev, "feat_out"), _status(dev_status, dev))
+    ref, dt, B, table, tree, steps, feat, fout = _kept(shape, (cache.Hkv, cache.d), lambda: (
+        ctypes.byref(shape.c()), _TORCH_DTYPE[shape.dtype], (shape.B,), (shape.B, shape.max_blocks),
+        (shape.B, shape.N, cache.Hkv, cache.d), (shape.B, shape.path_len), (shape.B, shape.N, shape.feat_dim),
+        (shape.B, shape.path_len, shape.feat_dim)))
+    dev = cache.device
+    if not (block_table.dtype is accept_len.dtype is prefix_len.dtype is new_prefix_len.dtype is _i32
+            and k_tree.dtype is v_tree.dtype is dt and block_table.shape == table and k_tree.shape == tree
+            and v_tree.shape == tree and accept_len.shape == B and prefix_len.shape == B
+            and new_prefix_len.shape == B and block_table.get_device() == k_tree.get_device() == v_tree.get_device()
+            == accept_len.get_device() == prefix_len.get_device() == new_prefix_len.get_device() == dev
+            and block_table.is_contiguous() and k_tree.is_contiguous() and v_tree.is_contiguous()
+            and accept_len.is_contiguous() and prefix_len.is_contiguous() and new_prefix_len.is_contiguous()):
+        _refuse(dev, (block_table, _i32, table, "block_table"), (k_tree, dt, tree, "k_tree"),
+                (v_tree, dt, tree, "v_tree"), (accept_len, _i32, B, "accept_len"), (prefix_len, _i32, B, "prefix_len"),
+                (new_prefix_len, _i32, B, "new_prefix_len"))
+    _call("et_kv_commit_paged", dev, stream, ref, cache._ref, block_table.data_ptr(), k_tree.data_ptr(),
+          v_tree.data_ptr(), accept_len.data_ptr(), _arg(path, _i32, steps, dev, "path"), prefix_len.data_ptr(),
+          new_prefix_len.data_ptr(), None if features is None else _arg(features, dt, feat, dev, "features"),
+          None if feat_out is None else _arg(feat_out, dt, fout, dev, "feat_out"),
+          None if dev_status is None else _status(dev_status, dev))
 
 
 @dataclasses.dataclass(frozen=True)
-class PagedAttnShape(_Shape):
+class PagedAttnShape:
     B: int
     N: int
     Hq: int
@@ -668,25 +694,25 @@ class PagedAttnShape(_Shape):
                                self.num_splits)
 
     def for_cache(self, cache: PagedCache):
-        """The C struct with the default scale filled in, kept per head dim."""
-        refs = self.__dict__.setdefault("_refs", {})
-        r = refs.get(cache.d)
-        if r is None:
+        """The C struct with the default scale filled in, and the tensors' shapes."""
+        def make():
             c = self.c()
             if not c.scale > 0:
                 c.scale = cache.d ** -0.5
-            r = refs[cache.d] = ctypes.byref(c)
-        return r
+            B, N, Hq = self.B, self.N, self.Hq
+            return (ctypes.byref(c), _TORCH_DTYPE[self.dtype], (B,), (B, self.max_blocks), (B, N, Hq, cache.d),
+                    (B, N, cache.Hkv, cache.d), (B, N, (N + 63) // 64), (B, Hq, N))
+        return _kept(self, (cache.Hkv, cache.d), make)
 
 
 def et_tree_attention_paged_workspace_size(shape: PagedAttnShape, cache: PagedCache) -> int:
     with torch.cuda.device(cache.device):
-        return load().et_tree_attention_paged_workspace_size(shape.for_cache(cache), cache._ref)
+        return load().et_tree_attention_paged_workspace_size(shape.for_cache(cache)[0], cache._ref)
 
 
 def et_tree_attention_paged_splits(shape: PagedAttnShape, cache: PagedCache) -> int:
     with torch.cuda.device(cache.device):
-        return load().et_tree_attention_paged_splits(shape.for_cache(cache), cache._ref)
+        return load().et_tree_attention_paged_splits(shape.for_cache(cache)[0], cache._ref)
 
 
 def et_tree_attention_paged(shape: PagedAttnShape, cache: PagedCache, block_table: torch.Tensor,
@@ -695,12 +721,18 @@ def et_tree_attention_paged(shape: PagedAttnShape, cache: PagedCache, block_tabl
                             ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
                             stream=None) -> None:
     """Attention of the tree rows (or, with N = 1, one token) over a paged 8-bit prefix and their ancestors."""
-    dt, dev, B, N = _TORCH_DTYPE[shape.dtype], cache.device, shape.B, shape.N
-    rows, tree = (B, N, shape.Hq, cache.d), (B, N, cache.Hkv, cache.d)
-    _call("et_tree_attention_paged", dev, stream, shape.for_cache(cache), cache._ref,
-          _arg(block_table, _i32, (B, shape.max_blocks), dev, "block_table"),
-          _arg(prefix_len, _i32, (B,), dev, "prefix_len"), _arg(q, dt, rows, dev, "q"),
-          _arg(k_tree, dt, tree, dev, "k_tree"), _arg(v_tree, dt, tree, dev, "v_tree"),
-          _arg(mask, _i64, (B, N, (N + 63) // 64), dev, "mask"), _arg(out, dt, rows, dev, "out"),
-          _arg(lse, _f32, (B, shape.Hq, N), dev, "lse"), _status(dev_status, dev),
-          None if ws is None else _arg(ws, torch.uint8, ws.shape, dev, "ws"), 0 if ws is None else ws.numel())
+    ref, dt, B, table, rows, tree, words, sums = shape.for_cache(cache)
+    dev = cache.device
+    if not (block_table.dtype is prefix_len.dtype is _i32 and q.dtype is k_tree.dtype is v_tree.dtype is out.dtype is dt
+            and block_table.shape == table and prefix_len.shape == B and q.shape == rows and k_tree.shape == tree
+            and v_tree.shape == tree and out.shape == rows and block_table.get_device() == prefix_len.get_device()
+            == q.get_device() == k_tree.get_device() == v_tree.get_device() == out.get_device() == dev
+            and block_table.is_contiguous() and prefix_len.is_contiguous() and q.is_contiguous()
+            and k_tree.is_contiguous() and v_tree.is_contiguous() and out.is_contiguous()):
+        _refuse(dev, (block_table, _i32, table, "block_table"), (prefix_len, _i32, B, "prefix_len"),
+                (q, dt, rows, "q"), (k_tree, dt, tree, "k_tree"), (v_tree, dt, tree, "v_tree"), (out, dt, rows, "out"))
+    _call("et_tree_attention_paged", dev, stream, ref, cache._ref, block_table.data_ptr(), prefix_len.data_ptr(),
+          q.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), _arg(mask, _i64, words, dev, "mask"), out.data_ptr(),
+          None if lse is None else _arg(lse, _f32, sums, dev, "lse"),
+          None if dev_status is None else _status(dev_status, dev),
+          None if ws is None else _arg(ws, torch.uint8, (ws.numel(),), dev, "ws"), 0 if ws is None else ws.numel())

@@ -202,3 +202,26 @@ def test_binding_refuses_host_and_misshapen_tensors():
         E.et_block_map(shape, i32(2), i32(2), i32(2), i32(2, 4), i32(5), i32(1))
     with pytest.raises(ValueError, match="CUDA"):
         E.et_block_map(shape, i32(2), i32(2), i32(2), i32(2, 3), i32(5), i32(1))
+
+
+def test_every_misfit_is_named_before_a_call(monkeypatch):
+    # the checks of the paged calls, on host tensors: a cache that says it lies where they do
+    class Host:
+        device, Hkv, d, _ref = -1, 2, 64, None
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    commit = dict(block_table=i32(3, 4), k_tree=bf(3, 5, 2, 64), v_tree=bf(3, 5, 2, 64), accept_len=i32(3),
+                  path=i32(3, 2), prefix_len=i32(3), new_prefix_len=i32(3), features=bf(3, 5, 8), feat_out=bf(3, 2, 8),
+                  dev_status=i32(1))
+    shape = E.PagedCommitShape(B=3, N=5, path_len=2, max_blocks=4, feat_dim=8)
+    attn = dict(block_table=i32(3, 4), prefix_len=i32(3), q=bf(3, 5, 6, 64), k_tree=bf(3, 5, 2, 64),
+                v_tree=bf(3, 5, 2, 64), mask=torch.zeros(3, 5, 1, dtype=torch.int64), out=bf(3, 5, 6, 64),
+                lse=torch.zeros(3, 6, 5), ws=torch.zeros(256, dtype=torch.uint8), dev_status=i32(1))
+    ashape = E.PagedAttnShape(B=3, N=5, Hq=6, max_blocks=4)
+    for fn, sh, args in ((E.et_kv_commit_paged, shape, commit), (E.et_tree_attention_paged, ashape, attn)):
+        with pytest.raises(ValueError, match="takes CUDA tensors"):
+            fn(sh, Host, **args)  # all fit: refused for where they lie
+        for name, t in args.items():
+            for wrong in (t[..., :-1] if name != "ws" else t[::2], t.double()):  # another shape or stride, another type
+                with pytest.raises(ValueError, match=name):
+                    fn(sh, Host, **dict(args, **{name: wrong}))
