@@ -110,6 +110,16 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t &a, uint64_t &b) {
   asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
+__device__ __forceinline__ void pt_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void pt_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void pt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
@@ -118,6 +128,18 @@ __device__ __forceinline__ void pt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float lds32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory"); }
+// read anew each time: what is needed rarely is not kept in registers
+__device__ __forceinline__ int thread_now() {
+  int t;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+  return t;
 }
 // OR of a condition over a softmax group's threads, and a barrier
 __device__ __forceinline__ bool group_any(int group, bool p) {
@@ -468,9 +490,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int gt = t & (kPtGroup - 1), r0 = kPtQ * col;  // thread of the group; first of its rows
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)r0;
     const uint32_t fcb = sb + kPtOffFC + (uint32_t)((2 * kPtRows * w + 2 * r0) * 4), prow = sb + kPtOffP + (uint32_t)(w * kPtP);
-    float *red = reinterpret_cast<float *>(sm + kPtOffRed) + w * 4 * kPtRows;
-    float *adj = reinterpret_cast<float *>(sm + kPtOffAdj) + 2 * kPtRows * w, *ref = fc + 2 * kPtRows * w;
-    const uint32_t adjb = sb + kPtOffAdj + (uint32_t)((2 * kPtRows * w + 2 * r0) * 4);
     uint64_t l2[kPtQ / 2];
 #pragma unroll
     for (int q = 0; q < kPtQ / 2; ++q) l2[q] = 0ull;
@@ -565,17 +584,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       float x[kPtQ];
       const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv), iv2 = pair(iv, iv);
 #pragma unroll
-      for (int part = 0; part < kPtQ / 16; ++part) {
-        uint32_t sc[16];
-        pt_ld16(lanes + kPtColS + 64u * (uint32_t)buf + 16u * part, sc);
+      for (int part = 0; part < kPtQ / 8; ++part) {
+        uint32_t sc[8];
+        pt_ld8(lanes + kPtColS + 64u * (uint32_t)buf + 8u * part, sc);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
+        for (int e = 0; e < 8; e += 2) {
           uint64_t f, c;  // two rows' factors and -references
-          lds_pairs(fcb + 8u * (uint32_t)(16 * part + e), f, c);
+          lds_pairs(fcb + 8u * (uint32_t)(8 * part + e), f, c);
           uint64_t y = pair(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1]));
           y = is_tree ? fma2(y, f, c) : fma2(mul2(y, ks2), f, add2(lv2, c));
-          unpair(y, x[16 * part + e], x[16 * part + e + 1]);
+          unpair(y, x[8 * part + e], x[8 * part + e + 1]);
         }
       }
       tc_fence_before();  // the scores sit in registers: their buffer is free
@@ -593,50 +612,57 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       top = fmaxf(top, x[kPtQ - 1]);
       if (group_any(w, fresh || top > kPaTop + kPaSlack)) {
         // the rows' maxima over the tile: a warp's 32 keys, then the four quarters
+        const int now_t = thread_now(), sw = now_t / kPtGroup, sgt = now_t % kPtGroup, sl = now_t & 31;
+        const int sr0 = kPtQ * ((now_t >> 7) & 1);
+        const uint32_t redb = sb + kPtOffRed + (uint32_t)(sw * 4 * kPtRows * 4);
+        const uint32_t adjb = sb + kPtOffAdj + (uint32_t)(sw * 2 * kPtRows * 4);
         float highest = -INFINITY;
 #pragma unroll
         for (int q = 0; q < kPtQ; ++q) {
           const float m = warp_max_f32(x[q]);
-          if (lane == q) highest = m;
+          if (sl == q) highest = m;
         }
-        red[quarter * kPtRows + r0 + lane] = highest;
-        group_sync(w);
+        sts32(redb + (uint32_t)((((now_t >> 5) & 3) * kPtRows + sr0 + sl) * 4), highest);
+        group_sync(sw);
         bool still = false;
-        if (gt < kPtRows) {
-          const float m = fmaxf(fmaxf(red[gt], red[kPtRows + gt]), fmaxf(red[2 * kPtRows + gt], red[3 * kPtRows + gt]));
-          const float was = -ref[py(gt)];  // the reference; 0 while the row is fresh
+        if (sgt < kPtRows) {
+          const uint32_t at = redb + 4u * (uint32_t)sgt, refb = sb + kPtOffFC + (uint32_t)((2 * kPtRows * sw + py(sgt)) * 4);
+          const float m = fmaxf(fmaxf(lds32(at), lds32(at + 4 * kPtRows)), fmaxf(lds32(at + 8 * kPtRows), lds32(at + 12 * kPtRows)));
+          const float was = -lds32(refb);  // the reference; 0 while the row is fresh
           float now = was;
           if (m > -INFINITY) now = mine_fresh ? m - kPaTop : fmaxf(was, m + was - kPaTop);
           const float corr = mine_fresh ? 0.f : ex2_fast(was - now);
           mine_fresh = mine_fresh && !(m > -INFINITY);
           still = mine_fresh;
-          ref[py(gt)] = -now;
-          adj[px(gt)] = was - now;
-          adj[py(gt)] = corr;
+          sts32(refb, -now);
+          sts32(adjb + 4u * (uint32_t)px(sgt), was - now);
+          sts32(adjb + 4u * (uint32_t)py(sgt), corr);
         }
-        fresh = group_any(w, still);
+        fresh = group_any(sw, still);
 #pragma unroll
         for (int q = 0; q < kPtQ; q += 2) {
           uint64_t d, f;
-          lds_pairs(adjb + 8u * (uint32_t)q, d, f);
+          lds_pairs(adjb + 8u * (uint32_t)(sr0 + q), d, f);
           unpair(add2(pair(x[q], x[q + 1]), d), x[q], x[q + 1]);
           l2[q / 2] = mul2(l2[q / 2], f);
         }
         if (i >= 2) {  // O holds the sums of this group's earlier tiles
-#pragma unroll
-          for (int part = 0; part < kPtQ / 16; ++part) {
-            uint32_t o[16];
-            const uint32_t at = lanes + kPtColO + 64u * (uint32_t)w + 16u * part;
-            pt_ld16(at, o);
+          tc_fence_after();
+#pragma unroll 1
+          for (int part = 0; part < kPtQ / 8; ++part) {
+            uint32_t o[8];
+            const uint32_t at = lanes + kPtColO + 64u * (uint32_t)sw + 8u * part;
+            pt_ld8(at, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * adj[py(r0 + 16 * part + e)]);
-            tmem_st16(at, o);
+            for (int e = 0; e < 8; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * lds32(adjb + 4u * (uint32_t)py(sr0 + 8 * part + e)));
+            pt_st8(at, o);
           }
           tmem_wait_st();
           tc_fence_before();
         }
-        group_sync(w);  // the changes are read before they may change again
+        group_sync(sw);  // the changes are read before they may change again
       }
 #pragma unroll
       for (int c = 0; c < kPtQ / 8; ++c) {
@@ -681,6 +707,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         l[q] = kept + __shfl_xor_sync(0xffffffffu, send, o);
       }
     }
+    float *red = reinterpret_cast<float *>(sm + kPtOffRed) + w * 4 * kPtRows;
+    const float *ref = fc + 2 * kPtRows * w;
     red[quarter * kPtRows + r0 + lane] = l[0];
     group_sync(w);
     const int mine = items > w ? (items - w + 1) / 2 : 0;  // this group's items

@@ -110,22 +110,37 @@ __device__ __forceinline__ void merge_chunks(const PagedSplitArgs &ma, long long
     stat[r] = make_float2(M, sum);
   }
   __syncthreads();
-  for (int x = t; x < real * (D / 4); x += NT) {
-    const int r = x / (D / 4), c = x - r * (D / 4);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < chunks; k0 += 8) {
-      float4 y[8];
+  constexpr int X = 4, K = 4;  // four cells' loads of four chunks
+  for (int x0 = t; x0 < real * (D / 4); x0 += X * NT) {
+    float4 v[X];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        y[j] = k0 + j < chunks ? __ldcg(&ma.part_o[(base + (long long)(k0 + j) * R + r) * (D / 4) + c])
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < X; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < chunks; k0 += K) {
+      float4 y[X][K];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float w = k0 + j < chunks ? pair[(k0 + j) * real + r].x : 0.f;
-        v.x = fmaf(y[j].x, w, v.x); v.y = fmaf(y[j].y, w, v.y); v.z = fmaf(y[j].z, w, v.z); v.w = fmaf(y[j].w, w, v.w);
-      }
+      for (int i = 0; i < X; ++i)
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          const int x = x0 + i * NT, r = x / (D / 4), c = x - r * (D / 4);
+          y[i][j] = x < real * (D / 4) && k0 + j < chunks
+                        ? __ldcg(&ma.part_o[(base + (long long)(k0 + j) * R + r) * (D / 4) + c])
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int i = 0; i < X; ++i)
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          const int x = x0 + i * NT, r = x / (D / 4);
+          const float w = x < real * (D / 4) && k0 + j < chunks ? pair[(k0 + j) * real + r].x : 0.f;
+          v[i].x = fmaf(y[i][j].x, w, v[i].x); v[i].y = fmaf(y[i][j].y, w, v[i].y);
+          v[i].z = fmaf(y[i][j].z, w, v[i].z); v[i].w = fmaf(y[i][j].w, w, v[i].w);
+        }
     }
-    write_row(r, c, v, stat[r].x, stat[r].y);
+#pragma unroll
+    for (int i = 0; i < X; ++i) {
+      const int x = x0 + i * NT, r = x / (D / 4), c = x - r * (D / 4);
+      if (x < real * (D / 4)) write_row(r, c, v[i], stat[r].x, stat[r].y);
+    }
   }
 }
 
