@@ -44,7 +44,8 @@ constexpr int kPtThreads = 608;
 constexpr int kPtGroup = 256;   // threads of a softmax group
 constexpr int kPtQ = kPtRows / 2;  // rows per softmax thread
 constexpr int kPtD = 128;
-constexpr int kPtStages = 3;
+constexpr int kPtStages = 2;
+constexpr int kPtVBuf = 3;  // V16 buffers: one more than groups, so that a conversion waits for no product of its group
 constexpr int kPtTmaWarp = 16, kPtScoreWarp = 17, kPtPvWarp = 18;
 constexpr uint32_t kPtTile8 = kPtKeys * kPtD;            // 16 KB: K8 or V8
 constexpr uint32_t kPtTile16 = 2 * kPtTile8;             // 32 KB: V16, two halves of 64 dims
@@ -54,7 +55,7 @@ constexpr uint32_t kPtOffQ = 0;                          // Q8: 64 rows hi, 64 r
 constexpr uint32_t kPtOffK = kPtOffQ + 2 * kPtRows * kPtD;
 constexpr uint32_t kPtOffV = kPtOffK + kPtStages * kPtTile8;
 constexpr uint32_t kPtOffVH = kPtOffV + kPtStages * kPtTile8;
-constexpr uint32_t kPtOffP = kPtOffVH + 2 * kPtTile16;
+constexpr uint32_t kPtOffP = kPtOffVH + kPtVBuf * kPtTile16;
 constexpr uint32_t kPtOffBar = kPtOffP + 2 * kPtP;
 constexpr uint32_t kPtOffFC = kPtOffBar + 256;           // [2 groups][32 pairs of rows] factors, -references
 constexpr uint32_t kPtOffRed = kPtOffFC + 2 * kPtRows * 8;     // [2][4 warps][64]
@@ -70,8 +71,8 @@ constexpr uint32_t kPtOffTreeQ = kPtOffVH + kPtTile16;       // q, bf16, two hal
 // TMEM columns
 constexpr uint32_t kPtColS = 0, kPtColO = 192, kPtTmemCols = 512;  // three score buffers, two O
 
-enum { T_KFULL = 0, T_KEMPTY = 3, T_VFULL = 6, T_VEMPTY = 9, T_SFULL = 12, T_SFREE = 15, T_PFULL = 18, T_PVDONE = 20,
-       T_TREE = 22, T_DRAIN = 23 /* two */, T_COUNT = 25 };
+enum { T_KFULL = 0, T_KEMPTY = 2, T_VFULL = 4, T_VEMPTY = 6, T_SFULL = 8, T_SFREE = 11, T_PFULL = 14, T_PVDONE = 16,
+       T_VHFREE = 18, T_TREE = 21, T_DRAIN = 22 /* two */, T_COUNT = 24 };
 
 // instruction descriptors: fp32 sums (bits 4-5 = 1), A type in bits 7-9, B
 // type in 10-12, A / B stored MN-major in bits 15 / 16, N >> 3, M >> 4
@@ -477,8 +478,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int steps = is_tree ? (a.N + 15) >> 4 : kPtKeys / 16;
         for (int kk = 0; kk < steps; ++kk)
           tc_mma(tmem + kPtColO + 64u * (uint32_t)w,
-                 sw128_desc(sb + kPtOffVH + w * kPtTile16 + kk * 2048, kPtHalf16, 1024),
+                 sw128_desc(sb + kPtOffVH + (i % kPtVBuf) * kPtTile16 + kk * 2048, kPtHalf16, 1024),
                  sw128_desc(sb + kPtOffP + w * kPtP + kk * 2048, kPtHalf16, 1024), is_tree ? iOt : iO, (i >= 2 || kk > 0) ? 1u : 0u);
+        tc_commit(bar(T_VHFREE + i % kPtVBuf));
         tc_commit(bar(T_PVDONE + w));
       }
       tc_commit(bar(T_DRAIN + 1));
@@ -518,6 +520,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // one item; the tree's tile (group 0's first) is compiled apart, which keeps its choices out of the others
     auto item = [&](int i, auto is_tree_) {
       constexpr bool is_tree = decltype(is_tree_)::value;
+      const int buf = i % 3;  // of the scores and of V16
+      static_assert(kPtVBuf == 3, "as many as score buffers");
       const bool there = is_tree ? tid < a.N : real_page(page_n);
       const float ks = is_tree ? 1.f : ks_n, vs = is_tree ? 1.f : clamp_v_scale(vs_n);
       const float lv = is_tree ? 0.f : __log2f(vs), iv = is_tree ? 1.f : __fdividef(1.f, vs);
@@ -533,30 +537,33 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
       }
       const bool masked = __any_sync(0xffffffffu, keep != 0xffffffffu);
-      // this group's weights and V16 are free once its last product has run; q of the tree's scores lay in V16 buffer 1
-      if (!dead) {
-        if (i >= 2) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
+      // V16 buffer 1 held q of the tree's scores; else the buffer is free once the other group's product has run
+      if (!is_tree && !dead) {
+        if (i >= kPtVBuf) dead = !pt_wait(bar(T_VHFREE + buf), (uint32_t)(i / 3 - 1) & 1u, &s_abort, limit);
         else if (tree && i == 1) dead = !pt_wait(bar(T_TREE), 0, &s_abort, limit);
       }
       if (!is_tree) {
-        // V's codes -> fp16: 16 codes of a row a thread.  The row's place in its group of eight is the thread's own, so
-        // addresses advance by whole groups.  Dims 16 c .. + 15 are two 16-byte chunks of half c / 4; the lanes of the
-        // upper half store them in the other order, which keeps the stores free of bank conflicts
+        // V's codes -> fp16: 16 codes of a row a thread, read as two chunks of eight.  The row's place in its group of
+        // eight is the thread's own, so addresses advance by whole groups.  Dims 16 c .. + 15 become two 16-byte chunks
+        // of half c / 4; which one a lane takes first alternates between the halves, which keeps the stores free of
+        // bank conflicts, and between rows, which keeps the reads free of them
         const int j = i - tree, stage = j % kPtStages;
         if (!dead) dead = !pt_wait(bar(T_VFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit);
         const uint32_t units = *(volatile uint32_t *)&s_units[stage];
         const int lim = L - (t0 + j) * kPtKeys;  // rows past it hold no key of this sequence
         const int c = gt & 7, r7 = (gt >> 3) & 7, r64 = gt >> 6, c0 = 2 * (c & 3);
-        const bool swap = c >= 4;
+        const int swap = (c >> 2) ^ (r7 & 1);
         const uint32_t from = sb + kPtOffV + stage * kPtTile8 + 1024u * (uint32_t)r64 + sw128(r7, c);
-        const uint32_t half = sb + kPtOffVH + w * kPtTile16 + (uint32_t)((c >> 2) * kPtHalf16) + 1024u * (uint32_t)r64;
-        const uint32_t to0 = half + sw128(r7, swap ? c0 + 1 : c0), to1 = half + sw128(r7, swap ? c0 : c0 + 1);
+        const uint32_t half = sb + kPtOffVH + (uint32_t)buf * kPtTile16 + (uint32_t)((c >> 2) * kPtHalf16) + 1024u * (uint32_t)r64;
+        const uint32_t from0 = from + 8u * (uint32_t)swap, from1 = from + 8u - 8u * (uint32_t)swap;
+        const uint32_t to0 = half + sw128(r7, c0 + swap), to1 = half + sw128(r7, c0 + 1 - swap);
         const bool whole = lim >= kPtKeys && units == 0xffu;
         uint4 v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(from + 4096u * k));
+        for (int k = 0; k < 4; ++k) {
+          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v[k].x), "=r"(v[k].y) : "r"(from0 + 4096u * k));
+          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v[k].z), "=r"(v[k].w) : "r"(from1 + 4096u * k));
+        }
         if (!whole) {  // whatever lies in rows without a key must not meet a zero weight
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -567,18 +574,19 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t h[8];
-          f8x4_to_f16<FMT>(swap ? v[k].z : v[k].x, h[0], h[1]);
-          f8x4_to_f16<FMT>(swap ? v[k].w : v[k].y, h[2], h[3]);
-          f8x4_to_f16<FMT>(swap ? v[k].x : v[k].z, h[4], h[5]);
-          f8x4_to_f16<FMT>(swap ? v[k].y : v[k].w, h[6], h[7]);
+          f8x4_to_f16<FMT>(v[k].x, h[0], h[1]);
+          f8x4_to_f16<FMT>(v[k].y, h[2], h[3]);
+          f8x4_to_f16<FMT>(v[k].z, h[4], h[5]);
+          f8x4_to_f16<FMT>(v[k].w, h[6], h[7]);
           sts128(to0 + 4096u * k, h[0], h[1], h[2], h[3]);
           sts128(to1 + 4096u * k, h[4], h[5], h[6], h[7]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(T_VEMPTY + stage));
       }
-      const int buf = i % 3;
       if (!dead) dead = !pt_wait(bar(T_SFULL + buf), (uint32_t)(i / 3) & 1u, &s_abort, limit);
+      // this group's weights (and O) are free once its last product has run, long before now
+      if (!dead && i >= 2) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
       dead = __any_sync(0xffffffffu, dead);
       tc_fence_after();
       float x[kPtQ];
