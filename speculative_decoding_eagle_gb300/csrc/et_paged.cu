@@ -245,15 +245,14 @@ struct CommitPagedArgs {
 };
 
 // smallest 2^e >= amax / MAX, MAX = 0.875 * 2^TOP: amax = m 2^x with m in
-// [0.5, 1) needs x - TOP when m <= 0.875, one more otherwise
+// [0.5, 1) needs x - TOP when m <= 0.875, one more otherwise; x and m from the
+// bits of amax (a subnormal one is below the smallest scale whatever its x)
 template <int FMT>
 __device__ __forceinline__ float page_scale(float amax) {
-  if (!(amax > 0.f)) return ldexpf(1.f, -kScaleExp);
-  int x;
-  const float m = frexpf(amax, &x);
-  int e = x - (FMT == ET_KV_E4M3 ? 9 : 16) + (m > 0.875f ? 1 : 0);
-  e = max(-kScaleExp, min(kScaleExp, e));
-  return ldexpf(1.f, e);
+  const uint32_t bits = __float_as_uint(amax);
+  const int x = (int)(bits >> 23) - 126;
+  const int e = x - (FMT == ET_KV_E4M3 ? 9 : 16) + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float((uint32_t)(127 + max(-kScaleExp, min(kScaleExp, e))) << 23);
 }
 
 // eight elements as they lie in memory, and as fp32
@@ -286,6 +285,22 @@ __device__ __forceinline__ void unpack8(const Raw8<BF16> &r, float (&x)[8]) {
   }
 }
 
+// magnitudes order like their bits, NaN and infinities above all: the running
+// maximum of eight, one instruction for two bf16 values
+template <bool BF16>
+__device__ __forceinline__ void see8(const Raw8<BF16> &r, uint32_t &top) {
+  if constexpr (BF16) {
+    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(w[e] & 0x7fff7fffu));
+  } else {
+    float x[8];
+    unpack8<BF16>(r, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+  }
+}
+
 // U threads per unit: 32 (a path's rows) or kCpThreads (a prompt's)
 template <bool BF16, int FMT, int D, int U>
 __global__ void __launch_bounds__(kCpThreads) k_commit_paged(CommitPagedArgs a) {
@@ -296,8 +311,10 @@ __global__ void __launch_bounds__(kCpThreads) k_commit_paged(CommitPagedArgs a) 
   __shared__ float red[32];
   pdl_wait();     // the previous kernel in the stream has completed
   pdl_trigger();  // only now may the next kernel launch
-  const int tp = blockIdx.x, b = blockIdx.z, t = threadIdx.x % U;
-  const int unit = blockIdx.y * UN + threadIdx.x / U, unit_blocks = (2 * a.Hkv + UN - 1) / UN;
+  // a prompt's neighbouring blocks take the heads of one page, whose rows lie side by side
+  const int tp = a.path ? blockIdx.x : blockIdx.x / (2 * a.Hkv), bu = a.path ? blockIdx.y : blockIdx.x - tp * (2 * a.Hkv);
+  const int b = blockIdx.z, t = threadIdx.x % U;
+  const int unit = bu * UN + threadIdx.x / U, unit_blocks = (2 * a.Hkv + UN - 1) / UN;
   const int alen = a.accept_len[b], base = a.prefix_len[b];
   const bool alen_ok = alen >= -1 && alen < a.max_rows;
   const int rows = (alen_ok && base >= 0) ? alen + 1 : 0;  // rows appended
@@ -329,10 +346,12 @@ __global__ void __launch_bounds__(kCpThreads) k_commit_paged(CommitPagedArgs a) 
   const long long page = blk < a.max_blocks ? a.block_table[(long long)b * a.max_blocks + blk] : -1;
   const int c = t % CH, r0 = t / CH;
   const int skip = (int)(start - base);  // path index of the page's row 0 (may be negative)
+  const long long first = ((long long)b * a.N * a.Hkv + g) * D + c * 8;
+  const int pitch = a.Hkv * D;
   auto source = [&](int r) -> long long {  // element index of the row that page row r receives, -1: none
     const int i = skip + r;
-    const int row = a.path ? a.path[(long long)b * a.path_len + i] : i;
-    return row >= 0 && row < a.N ? (((long long)b * a.N + row) * a.Hkv + g) * D + c * 8 : -1;
+    const int row = U == 32 ? a.path[(long long)b * a.path_len + i] : i;
+    return (unsigned)row < (unsigned)a.N ? first + (long long)row * pitch : -1;
   };
   const void *tree = isV ? a.v_tree : a.k_tree;
   Raw8<BF16> held[KEEP];
@@ -358,50 +377,62 @@ __global__ void __launch_bounds__(kCpThreads) k_commit_paged(CommitPagedArgs a) 
   uint8_t *codes = (isV ? a.v_pages : a.k_pages) + page * a.page_stride + (long long)g * a.P * D;
   float *scale_at = (isV ? a.v_scale : a.k_scale) + page * a.Hkv + g;
   const float was = lo > 0 ? *scale_at : 0.f;
-  float amax = 0.f;
-  auto see = [&](const Raw8<BF16> &r) {
-    float x[8];
-    unpack8<BF16>(r, x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float m = fabsf(x[e]);
-      if (m <= FLT_MAX) amax = fmaxf(amax, m);
-      else bad |= ET_DEV_NONFINITE;
-    }
-  };
+  uint32_t top = 0u;
 #pragma unroll
   for (int k = 0; k < KEEP; ++k)
-    if (have[k]) see(held[k]);
+    if (have[k]) see8<BF16>(held[k], top);
+#pragma unroll 1
   for (int r = lo + r0 + KEEP * RP; r < hi; r += RP) {  // (a prompt's large pages)
     const long long src = source(r);
     if (src < 0) bad |= ET_DEV_BAD_INDEX;
-    else see(raw8<BF16>(tree, src));
+    else see8<BF16>(raw8<BF16>(tree, src), top);
   }
+  if (BF16) top = max(top & 0xffff0000u, top << 16);
+  if (top >= 0x7f800000u) {  // once more, without what is not finite
+    bad |= ET_DEV_NONFINITE;
+    top = 0u;
+#pragma unroll 1
+    for (int r = lo + r0; r < hi; r += RP) {
+      const long long src = source(r);
+      if (src < 0) continue;
+      float x[8];
+      unpack8<BF16>(raw8<BF16>(tree, src), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (fabsf(x[e]) <= FLT_MAX) top = max(top, __float_as_uint(fabsf(x[e])));
+    }
+  }
+  float amax = __uint_as_float(top);
   if (U == 32) amax = warp_max(amax);
   else amax = block_max<kCpThreads>(amax, red);
   const float need = page_scale<FMT>(amax);
   const bool was_ok = was > 0.f && was <= FLT_MAX;
   if (lo > 0 && !was_ok) bad |= ET_DEV_NONFINITE;
   const float now = lo > 0 && was_ok ? fmaxf(was, need) : need;
-  // 1 / 2^e is exact; a scale of another origin divides
-  const bool pow2 = (__float_as_uint(now) & 0x007fffffu) == 0u;
-  const float inv = 1.f / now;
-  auto put = [&](int r, const Raw8<BF16> &v) {
+  auto put = [&](int r, const Raw8<BF16> &v, auto scaled) {
     float x[8];
     unpack8<BF16>(v, x);
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = pow2 ? f32x2_to_f8x2<FMT>(x[2 * e] * inv, x[2 * e + 1] * inv)
-                  : f32x2_to_f8x2<FMT>(__fdiv_rn(x[2 * e], now), __fdiv_rn(x[2 * e + 1], now));
-    *reinterpret_cast<uint2 *>(codes + (long long)r * D + c * 8) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    *reinterpret_cast<uint2 *>(codes + (long long)r * D + c * 8) =
+        make_uint2(f32x4_to_f8x4<FMT>(scaled(x[0]), scaled(x[1]), scaled(x[2]), scaled(x[3])),
+                   f32x4_to_f8x4<FMT>(scaled(x[4]), scaled(x[5]), scaled(x[6]), scaled(x[7])));
   };
+  if ((__float_as_uint(now) & 0x007fffffu) == 0u) {
+    const float inv = 1.f / now;  // exact
+    auto scaled = [&](float x) { return x * inv; };
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k)
-    if (have[k]) put(lo + r0 + k * RP, held[k]);
-  for (int r = lo + r0 + KEEP * RP; r < hi; r += RP) {
-    const long long src = source(r);
-    if (src >= 0) put(r, raw8<BF16>(tree, src));
+    for (int k = 0; k < KEEP; ++k)
+      if (have[k]) put(lo + r0 + k * RP, held[k], scaled);
+#pragma unroll 1
+    for (int r = lo + r0 + KEEP * RP; r < hi; r += RP) {
+      const long long src = source(r);
+      if (src >= 0) put(r, raw8<BF16>(tree, src), scaled);
+    }
+  } else {  // a page whose scale is of another origin
+#pragma unroll 1
+    for (int r = lo + r0; r < hi; r += RP) {
+      const long long src = source(r);
+      if (src >= 0) put(r, raw8<BF16>(tree, src), [&](float x) { return __fdiv_rn(x, now); });
+    }
   }
   if (lo > 0 && was_ok && now > was) {  // the rows before, on the grown scale
     const float ratio = __fdiv_rn(was, now);
@@ -410,9 +441,9 @@ __global__ void __launch_bounds__(kCpThreads) k_commit_paged(CommitPagedArgs a) 
       uint2 v = *at;
       float x[4];
       f8x4_to_f32<FMT>(v.x, x);
-      v.x = f32x2_to_f8x2<FMT>(x[0] * ratio, x[1] * ratio) | f32x2_to_f8x2<FMT>(x[2] * ratio, x[3] * ratio) << 16;
+      v.x = f32x4_to_f8x4<FMT>(x[0] * ratio, x[1] * ratio, x[2] * ratio, x[3] * ratio);
       f8x4_to_f32<FMT>(v.y, x);
-      v.y = f32x2_to_f8x2<FMT>(x[0] * ratio, x[1] * ratio) | f32x2_to_f8x2<FMT>(x[2] * ratio, x[3] * ratio) << 16;
+      v.y = f32x4_to_f8x4<FMT>(x[0] * ratio, x[1] * ratio, x[2] * ratio, x[3] * ratio);
       *at = v;
     }
   }
@@ -427,7 +458,7 @@ et_status launch_commit(const CommitPagedArgs &a, int d, int touch, int feature_
     if (d == 64) return et_launch(k_commit_paged<BF16, FMT, 64, 32>, grid, dim3(kCpThreads), 0, st, 0, a);
     return et_launch(k_commit_paged<BF16, FMT, 128, 32>, grid, dim3(kCpThreads), 0, st, 0, a);
   }
-  const dim3 grid(touch, 2 * a.Hkv, B);
+  const dim3 grid(touch * 2 * a.Hkv, 1, B);
   if (d == 64) return et_launch(k_commit_paged<BF16, FMT, 64, kCpThreads>, grid, dim3(kCpThreads), 0, st, 0, a);
   return et_launch(k_commit_paged<BF16, FMT, 128, kCpThreads>, grid, dim3(kCpThreads), 0, st, 0, a);
 }
@@ -500,6 +531,7 @@ extern "C" et_status et_kv_commit_paged(const et_paged_commit_shape *s, const et
   a.feat_out = s->feat_dim > 0 ? static_cast<uint4 *>(feat_out) : nullptr;
   a.dev_status = dev_status;
   const int touch = (int)(((long long)a.max_rows + 2ll * a.P - 2) / a.P);  // pages max_rows rows can lie in
+  ET_RETURN_IF((long long)touch * 2 * cache->Hkv >= (1ll << 31), ET_ERR_UNSUPPORTED);
   const int feature_rows = s->feat_dim > 0 ? s->path_len : 0;
   cudaStream_t st = (cudaStream_t)stream;
   if (s->dtype == ET_BF16)

@@ -44,6 +44,19 @@ __device__ __forceinline__ uint32_t f32x2_to_f8x2(float lo, float hi) {
   return r;
 }
 
+// four, packed in order
+template <int FMT>
+__device__ __forceinline__ uint32_t f32x4_to_f8x4(float x0, float x1, float x2, float x3) {
+  uint32_t r;
+  if (FMT == ET_KV_E4M3)
+    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}"
+        : "=r"(r) : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+  else
+    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e5m2x2.f32 l, %2, %1;\n cvt.rn.satfinite.e5m2x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}"
+        : "=r"(r) : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+  return r;
+}
+
 inline et_status paged_cache_status(const et_paged_cache *c) {
   if (!c) return ET_ERR_INVALID_ARG;
   if (c->Hkv < 1 || c->d < 1 || c->page_size < 1 || c->num_pages < 1 || c->num_pages >= (1ll << 31))
