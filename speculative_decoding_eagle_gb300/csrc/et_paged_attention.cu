@@ -824,19 +824,21 @@ int sm_count() {
 
 long long least(long long a, long long b) { return a < b ? a : b; }
 
-// Chunks of the tcgen05 kernel, one block per SM.  A block costs about twelve of its 128-key tiles before its first and
-// after its last (measured: 15.6 against 1.3 us), a merge about five.  One sequence: whole waves of equal blocks.
-// Several, of any length up to T: the work of half the bound over all SMs, and half of the longest block at the end
-// (7B heads, 16 sequences of 512..16384 tokens: 369 us in one chunk each, 404 in two).
+// Chunks of the tcgen05 kernel, one block per SM.  A block costs about ten of its 128-key tiles before its first and
+// after its last (measured: 11 against 1.0 us), a merge about three in a cluster and eight through the workspace.  One
+// sequence: whole waves of equal blocks.  Several, of any length up to T: the work of half the bound over all SMs, and
+// half of the longest block at the end.
 int tc_splits(long long tiles, int T, int B) {
-  constexpr double kBlock = 12, kMerge = 5;
+  constexpr double kBlock = 10;
   const int sms = sm_count();
   int best = 1;
   double least = 1e30;
   for (int S = 1; S <= kPaMaxSplits && S <= T; ++S) {
-    const double chunk = (T + S - 1) / S, merge = S > 1 ? kMerge : 0;
-    const double cost = B == 1 ? (double)((tiles * S + sms - 1) / sms) * (kBlock + chunk) + merge
-                               : (double)tiles * (S * kBlock + 0.5 * T) / sms + 0.5 * (kBlock + chunk) + merge;
+    const bool cluster = S > 1 && S <= kPtMaxCluster;
+    const long long together = cluster ? paged_tc_clusters(S, sms) : sms, units = cluster ? tiles : tiles * S;
+    const double chunk = (T + S - 1) / S, merge = cluster ? 3 : S > 1 ? 8 : 0;
+    const double cost = B == 1 ? (double)((units + together - 1) / together) * (kBlock + chunk + merge)
+                               : (double)tiles * (S * (kBlock + merge) + 0.5 * T) / sms + 0.5 * (kBlock + chunk + merge);
     if (cost < least) {
       least = cost;
       best = S;
@@ -886,7 +888,7 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   if (S > kPaMaxSplits) S = kPaMaxSplits;
   if (S < 1) S = 1;
   p->S = S;
-  if (S > 1) {
+  if (S > 1 && !(p->tc && S <= kPtMaxCluster)) {
     const size_t cnt = ((size_t)tiles * sizeof(unsigned int) + 255) & ~(size_t)255;
     const size_t ml = ((size_t)tiles * S * p->R * sizeof(float2) + 255) & ~(size_t)255;
     p->ml_off = cnt;
@@ -949,9 +951,9 @@ extern "C" et_status et_tree_attention_paged(const et_paged_attn_shape *shape, c
   ma.tiles_y = cache->Hkv * plan.row_tiles;
   ma.box = cache->page_size % kPaTile == 0 ? kPaTile : 16;
   unsigned char *wsb = static_cast<unsigned char *>(ws);
-  ma.cnt = plan.S > 1 ? reinterpret_cast<unsigned int *>(wsb) : nullptr;
-  ma.part_ml = plan.S > 1 ? reinterpret_cast<float2 *>(wsb + plan.ml_off) : nullptr;
-  ma.part_o = plan.S > 1 ? reinterpret_cast<float4 *>(wsb + plan.o_off) : nullptr;
+  ma.cnt = plan.ws > 0 ? reinterpret_cast<unsigned int *>(wsb) : nullptr;
+  ma.part_ml = plan.ws > 0 ? reinterpret_cast<float2 *>(wsb + plan.ml_off) : nullptr;
+  ma.part_o = plan.ws > 0 ? reinterpret_cast<float4 *>(wsb + plan.o_off) : nullptr;
   const uint32_t units = (uint32_t)cache->page_size / 16;
   ma.page_magic = units == 1 ? 0u : (uint32_t)(((1ull << 32) + units - 1) / units);
   ma.group_magic = a.G == 1 ? 0u : (uint32_t)(((1ull << 32) + a.G - 1) / a.G);

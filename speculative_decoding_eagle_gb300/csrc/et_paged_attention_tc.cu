@@ -33,6 +33,7 @@
 // shared-memory traffic (about 1400 cycles a tile at 128 bytes a cycle) the
 // next limit after HBM (1365 cycles a tile).  Every mbarrier wait is bounded:
 // a block that gives up sets ET_DEV_TIMEOUT, drains what it issued and leaves.
+#include <atomic>
 #include <type_traits>
 
 #include "et_paged_attn.cuh"
@@ -183,6 +184,11 @@ __device__ __forceinline__ int px(int row) { return 4 * (row >> 1) + (row & 1); 
 __device__ __forceinline__ int py(int row) { return px(row) + 2; }
 // chunk c (16 bytes) of row r in a tile of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+__device__ __forceinline__ float4 cl_ld_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 // maximum over the warp's lanes; NaN is passed over
 __device__ __forceinline__ float warp_max_f32(float x) {
   float m;
@@ -743,6 +749,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int Rg = rt * kPtRows + r, i = row_token(ma, Rg), h = g * a.G + (Rg - i * a.G);
     if (a.lse) a.lse[((long long)b * a.Hq + h) * a.N + i] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
   };
+  // a chunk's rows go to the workspace or, for its cluster to read, to shared memory where the rings and the tables of
+  // factors were
+  const bool cluster = ma.cnt == nullptr;
+  const long long part = cluster ? 0 : (tile_id * ma.S + chunk) * kPtRows;
+  float2 *part_ml = cluster ? reinterpret_cast<float2 *>(sm + kPtOffFC) : ma.part_ml;
+  float *part_o = cluster ? reinterpret_cast<float *>(sm + kPtOffK) : reinterpret_cast<float *>(ma.part_o);
   // factors of the two groups' sums and the row's place, per row (short loops: cold code runs at the speed of its fetch)
   float2 *mix = reinterpret_cast<float2 *>(sm + kPtOffAdj);
   long long *to = reinterpret_cast<long long *>(sm + kPtOffRed);
@@ -756,10 +768,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       to[t] = place(t);
       write_lse(t, M, sum);
     } else {
-      const long long at = (tile_id * ma.S + chunk) * kPtRows + t;
       mix[t] = make_float2(wx, wy);
-      to[t] = at * kPtD;
-      ma.part_ml[at] = make_float2(M, sum);
+      to[t] = (part + t) * kPtD;
+      part_ml[part + t] = make_float2(M, sum);
     }
   }
   __syncthreads();
@@ -797,7 +808,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (q0 + e < real) reinterpret_cast<float *>(ma.part_o)[to[q0 + e] + d] = __uint_as_float(o0[e]);
+          if (q0 + e < real) part_o[to[q0 + e] + d] = __uint_as_float(o0[e]);
       }
     }
   }
@@ -808,16 +819,56 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   if (warp == kPtScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPtTmemCols) : "memory");
   if (chunks == 1) return;
-  // ---- the chunks' rows, merged by the last block to arrive ----
-  if (!arrive_last(ma.cnt + tile_id, (unsigned)chunks, &s_last)) return;
-  merge_chunks<kPtD, kPtRows, kPtThreads>(ma, tile_id, chunks, real, sm, [&](int r, int c, const float4 &v, float M, float sum) {
+  auto write4 = [&](int r, int c, const float4 &v, float M, float sum) {
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint2 u;
     u.x = pack_bf16x2(v.x * inv, v.y * inv);
     u.y = pack_bf16x2(v.z * inv, v.w * inv);
     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + place(r) + 4 * c) = u;
     if (c == 0) write_lse(r, M, sum);
-  });
+  };
+  if (cluster) {
+    // ---- the chunks' rows, each merged by a warp of one of the cluster's blocks ----
+    // (blocks without keys have left: the barrier counts the others)
+    __syncwarp();
+    cl_sync();
+#pragma unroll 1
+    for (int r = chunk + warp * chunks; r < real; r += kPtThreads / 32 * chunks) {
+      float4 v[kPtMaxCluster];
+#pragma unroll
+      for (int k = 0; k < kPtMaxCluster; ++k) {
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < chunks) v[k] = cl_ld_f32x4(cl_map(part_o, (uint32_t)k) + (uint32_t)((r * kPtD + 4 * lane) * 4));
+      }
+      float m = -3e38f, l = 0.f;
+      if (lane < chunks) {
+        const uint32_t at = cl_map(part_ml, (uint32_t)lane) + 8u * (uint32_t)r;
+        m = cl_ld_f32(at);
+        l = cl_ld_f32(at + 4u);
+      }
+      const float M = warp_max_f32(m), f = ex2_fast(m - M);
+      float sum = l * f;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum = __shfl_sync(0xffffffffu, sum, 0);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kPtMaxCluster; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        if (k < chunks) {
+          y.x = fmaf(v[k].x, fk, y.x); y.y = fmaf(v[k].y, fk, y.y);
+          y.z = fmaf(v[k].z, fk, y.z); y.w = fmaf(v[k].w, fk, y.w);
+        }
+      }
+      write4(r, lane, y, M, sum);
+    }
+    __syncwarp();
+    cl_sync();  // no block leaves while another reads its rows
+    return;
+  }
+  // ---- more chunks than a cluster has blocks: merged by the last block to arrive ----
+  if (!arrive_last(ma.cnt + tile_id, (unsigned)chunks, &s_last)) return;
+  merge_chunks<kPtD, kPtRows, kPtThreads>(ma, tile_id, chunks, real, sm, write4);
 }
 
 }  // namespace
@@ -840,12 +891,36 @@ et_status paged_tc_launch(const et_paged_cache *cache, const PagedSplitArgs &arg
   if (!make_page_map(&mk, cache->k_pages, cache, ma.box) || !make_page_map(&mv, cache->v_pages, cache, ma.box))
     return ET_ERR_INVALID_ARG;
   const dim3 grid(ma.S, ma.tiles_y, ma.a.B);
-  if (cache->format == ET_KV_E4M3) {
-    if (et_smem_attr((const void *)k_paged_attn_tc<ET_KV_E4M3>, (int)kPtBytes) != cudaSuccess) return ET_ERR_CUDA;
-    return et_launch(k_paged_attn_tc<ET_KV_E4M3>, grid, dim3(kPtThreads), kPtBytes, stream, 0, mk, mv, ma);
+  const int cluster = ma.cnt || ma.S == 1 ? 0 : ma.S;
+  auto *kernel = cache->format == ET_KV_E4M3 ? k_paged_attn_tc<ET_KV_E4M3> : k_paged_attn_tc<ET_KV_E5M2>;
+  if (et_smem_attr((const void *)kernel, (int)kPtBytes) != cudaSuccess) return ET_ERR_CUDA;
+  return et_launch(kernel, grid, dim3(kPtThreads), kPtBytes, stream, cluster, mk, mv, ma);
+}
+
+int paged_tc_clusters(int S, int sms) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kPtMaxCluster + 1];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+  if (dev >= 0 && dev < kDevices && (n = known[dev][S].load(std::memory_order_relaxed)) > 0) return n;
+  auto *kernel = k_paged_attn_tc<ET_KV_E4M3>;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)S;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)S);
+  cfg.blockDim = dim3(kPtThreads);
+  cfg.dynamicSmemBytes = kPtBytes;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (dev < 0 || et_smem_attr((const void *)kernel, (int)kPtBytes) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return sms / S > 0 ? sms / S : 1;
   }
-  if (et_smem_attr((const void *)k_paged_attn_tc<ET_KV_E5M2>, (int)kPtBytes) != cudaSuccess) return ET_ERR_CUDA;
-  return et_launch(k_paged_attn_tc<ET_KV_E5M2>, grid, dim3(kPtThreads), kPtBytes, stream, 0, mk, mv, ma);
+  if (dev < kDevices) known[dev][S].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 }  // namespace et

@@ -30,7 +30,7 @@ struct PagedSplitArgs {
   int S, tiles_y;       // chunks, Hkv * row tiles
   int row_tiles;        // row tiles per KV head
   int box;              // rows per TMA box
-  unsigned int *cnt;    // [B * tiles_y] arrival counters
+  unsigned int *cnt;    // [B * tiles_y] arrival counters; null when the chunks need none (one, or a cluster)
   float2 *part_ml;      // [B * tiles_y][S][R] (maximum, sum)
   float4 *part_o;       // [B * tiles_y][S][R][D] fp32
   uint32_t page_magic, group_magic;  // page_index, row_token
@@ -40,6 +40,9 @@ struct PagedSplitArgs {
 // D = 128, many rows per KV head (et_paged_attention_tc.cu)
 constexpr int kPtKeys = 128;  // keys per tile
 constexpr int kPtRows = 64;   // query rows per block
+constexpr int kPtMaxCluster = 8;  // chunks up to which a sequence's blocks form a cluster (the portable size)
+// clusters of S blocks that the device runs at once (a property of the device, asked once)
+ET_HIDDEN int paged_tc_clusters(int S, int sms);
 // pages as [num_pages][Hkv][P][d] bytes; a box is `box` rows of one head of one page
 ET_HIDDEN bool make_page_map(CUtensorMap *m, const void *base, const et_paged_cache *c, int box);
 ET_HIDDEN et_status paged_tc_launch(const et_paged_cache *cache, const PagedSplitArgs &a, cudaStream_t stream);
