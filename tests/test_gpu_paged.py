@@ -664,6 +664,32 @@ def test_batches_past_one_block_of_lengths(B, N, Hq, Hkv, d):
     assert int(r["status"].item()) == 0
 
 
+@pytest.mark.parametrize("splits,chunks", [(3, 3), (8, 8), (9, 9), (13, 13), (40, 14)])
+def test_chunks_that_form_a_cluster_and_more_that_use_the_workspace(splits, chunks):
+    """Up to eight chunks merge through shared memory, more through the workspace; some have no keys, some half a tile."""
+    rng = np.random.default_rng(29)
+    lens = [1700, 0, 1, 300, 1664]
+    pool = Pool(rng, lens, 48, 2, 128, "e4m3")
+    keep = random_tree(rng, 5, 37)
+    runs = [run_attention(pool, 5, 37, 4, "bf16", rng, keep, splits) for _ in range(2)]
+    assert E.et_tree_attention_paged_splits(runs[0]["shape"], pool.cache) == chunks
+    graphs = []
+    for r in runs:
+        check_all(pool, r, keep, "bf16")
+        r["want"] = r["out"].clone()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):  # both on one workspace
+            E.et_tree_attention_paged(*r["args"], lse=r["lse"], ws=runs[0]["ws"], dev_status=r["status"])
+    for r in runs:
+        r["out"].zero_()
+    for _ in range(4):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for r in runs:
+        assert torch.equal(r["out"], r["want"]) and int(r["status"].item()) == 0
+
+
 @pytest.mark.parametrize("N,Hq,Hkv,d", [(1, 4, 2, 128), (30, 2, 1, 128), (30, 2, 1, 64), (70, 1, 1, 64)])
 @pytest.mark.parametrize("splits", [1, 2, 7, 64, 1000])
 def test_every_number_of_chunks_gives_the_same_sums(N, Hq, Hkv, d, splits):
