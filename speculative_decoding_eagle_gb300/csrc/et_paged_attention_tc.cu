@@ -137,6 +137,9 @@ __device__ __forceinline__ float lds32(uint32_t addr) {
   return v;
 }
 __device__ __forceinline__ void sts32(uint32_t addr, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory"); }
+__device__ __forceinline__ void lds_f4(uint32_t addr, float &x, float &y, float &z) {
+  asm volatile("{\n .reg .f32 w;\n ld.shared.v4.f32 {%0, %1, %2, w}, [%3];\n}\n" : "=f"(x), "=f"(y), "=f"(z) : "r"(addr) : "memory");
+}
 // read anew each time: what is needed rarely is not kept in registers
 __device__ __forceinline__ int thread_now() {
   int t;
@@ -205,6 +208,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   __shared__ int s_abort, s_last, s_odd;
   __shared__ int s_red[kPtThreads / 32];
   __shared__ uint32_t s_tmem, s_units[kPtStages];
+  __shared__ float4 s_scale[kPtStages][kPtKeys / 16];  // a unit's K scale, log2 of its V scale, the inverse of that
   unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = saddr(sm);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -216,6 +220,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     s_odd = 0;
     for (int i = 0; i < T_COUNT; ++i) {
       int count = 1;
+      if (i >= T_VFULL && i < T_VEMPTY) count = 2;  // the copies, the scales
       if ((i >= T_VEMPTY && i < T_SFULL) || (i >= T_SFREE && i < T_PVDONE)) count = kPtGroup / 32;  // a group's warps
       mbar_init(bar(i), (uint32_t)count);
     }
@@ -259,19 +264,33 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   pdl_trigger();    // after the TMEM allocation: a waiting dependent block must not hold what this block needs
 
   // ---- TMA: tile j of this block into ring stage j % stages ----
-  int page = -1, slot = 0;  // lane: unit (lane & 7) of tile 4 * (j / 4) + (lane >> 3), 16 keys a unit
-  auto fetch_pages = [&](int j0) {
+  // lane: unit (lane & 7) of tile 4 * (j / 4) + (lane >> 3), 16 keys a unit; the next four tiles' (_n) in flight ahead
+  int page = -1, slot = 0, page_n = -1, slot_n = 0;
+  float ks = 0.f, vs = 1.f, ks_n = 0.f, vs_n = 1.f;
+  auto unit_key = [&](int j0) -> long long {
     const int j = j0 + (lane >> 3);
     const long long key = (long long)(t0 + j) * kPtKeys + 16 * (lane & 7);
-    page = -1;
-    if (j < n && key < L) {
-      const int blk = page_index(ma, (int)key);
-      slot = (int)key - blk * a.P;
-      page = a.block_table[(long long)b * a.max_blocks + blk];
-      if (page < 0 || page >= a.num_pages) {
-        page = -1;
-        bad = 1;
-      }
+    return j < n && key < L ? key : -1;
+  };
+  auto fetch_pages = [&](int j0, int &pg, int &sl) {
+    const int key = (int)unit_key(j0);
+    pg = -1;
+    if (key >= 0) {
+      const int blk = page_index(ma, key);
+      sl = key - blk * a.P;
+      pg = a.block_table[(long long)b * a.max_blocks + blk];
+    }
+  };
+  auto fetch_scales = [&](int j0, int &pg, float &k, float &v) {
+    if (pg < 0 || pg >= a.num_pages) {
+      if (unit_key(j0) >= 0) bad = 1;
+      pg = -1;
+    }
+    k = 0.f;
+    v = 1.f;
+    if (pg >= 0) {
+      k = a.k_scale[(long long)pg * a.Hkv + g];
+      v = a.v_scale[(long long)pg * a.Hkv + g];
     }
   };
   auto issue = [&](int j) {
@@ -297,8 +316,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       tma_4d(sb + kPtOffV + off, &tm_v, 0, sl, g, pg, bar(T_VFULL + stage));
     }
   };
+  auto publish = [&](int j) {  // the tile's scales, and the arrival that goes with them
+    const int stage = j % kPtStages, src = 8 * (j & 3) + (lane & 7);
+    const float k = __shfl_sync(0xffffffffu, ks, src), v = clamp_v_scale(__shfl_sync(0xffffffffu, vs, src));
+    if (lane < 8) s_scale[stage][lane] = make_float4(k, __log2f(v), __fdividef(1.f, v), 0.f);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(T_VFULL + stage));
+  };
   if (warp == kPtTmaWarp) {
-    fetch_pages(0);
+    fetch_pages(0, page, slot);
+    fetch_scales(0, page, ks, vs);
     for (int j = 0; j < n && j < kPtStages; ++j) issue(j);
   }
 
@@ -425,13 +452,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // ---------------- TMA ----------------
     bool ok = true;
     int issued = n < kPtStages ? n : kPtStages;
+    fetch_pages(4, page_n, slot_n);
+    for (int j = 0; j < issued; ++j) publish(j);
     for (int j = kPtStages; j < n; ++j) {
-      if ((j & 3) == 0) fetch_pages(j);
+      if ((j & 3) == 2) fetch_scales(j + 2, page_n, ks_n, vs_n);
+      if ((j & 3) == 0) {
+        page = page_n; slot = slot_n; ks = ks_n; vs = vs_n;
+        fetch_pages(j + 4, page_n, slot_n);
+      }
       const int stage = j % kPtStages;
       const uint32_t phase = (uint32_t)(j / kPtStages - 1) & 1u;
       ok = pt_wait(bar(T_KEMPTY + stage), phase, &s_abort, limit) && pt_wait(bar(T_VEMPTY + stage), phase, &s_abort, limit);
       if (!__all_sync(0xffffffffu, ok)) break;
       issue(j);
+      publish(j);
       issued = j + 1;
     }
     if (lane == 0)  // no copy may be in flight when the block leaves
@@ -504,45 +538,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     bool dead = false;
     bool fresh = true;       // some row has no reference yet (the same in the whole group)
     bool mine_fresh = true;  // threads 0..63 of the group: row gt has none
-    // a key's page and scales, fetched an item ahead
-    auto my_page = [&](int i) -> int {
-      const int j = i - tree;
-      const long long key = (long long)(t0 + j) * kPtKeys + tid;
-      if (i >= items || j < 0 || key >= L) return -1;
-      return a.block_table[(long long)b * a.max_blocks + page_index(ma, (int)key)];  // checked where it is used: no wait here
-    };
-    auto real_page = [&](int p) -> bool { return p >= 0 && p < a.num_pages; };
-    auto my_scale = [&](int p, float &ks, float &vs) {
-      ks = 0.f;
-      vs = 1.f;
-      if (real_page(p)) {
-        ks = a.k_scale[(long long)p * a.Hkv + g];
-        vs = a.v_scale[(long long)p * a.Hkv + g];
-      }
-    };
-    int page_n = my_page(w);
-    float ks_n, vs_n;
-    my_scale(page_n, ks_n, vs_n);
     // one item; the tree's tile (group 0's first) is compiled apart, which keeps its choices out of the others
     auto item = [&](int i, auto is_tree_) {
       constexpr bool is_tree = decltype(is_tree_)::value;
       const int buf = i % 3;  // of the scores and of V16
       static_assert(kPtVBuf == 3, "as many as score buffers");
-      const bool there = is_tree ? tid < a.N : real_page(page_n);
-      const float ks = is_tree ? 1.f : ks_n, vs = is_tree ? 1.f : clamp_v_scale(vs_n);
-      const float lv = is_tree ? 0.f : __log2f(vs), iv = is_tree ? 1.f : __fdividef(1.f, vs);
-      page_n = my_page(i + 2);
-      uint32_t keep = there ? 0xffffffffu : 0u;  // bit q: row r0 + q attends this thread's key
-      if (is_tree && there) {
-        keep = 0u;
-#pragma unroll 4
-        for (int q = 0; q < kPtQ; ++q) {
-          const unsigned long long m =
-              *(reinterpret_cast<const unsigned long long *>(sm + kPtOffMask) + 2 * (r0 + q) + (tid >> 6));
-          keep |= (uint32_t)((m >> (tid & 63)) & 1ull) << q;
-        }
-      }
-      const bool masked = __any_sync(0xffffffffu, keep != 0xffffffffu);
+      bool there = is_tree && tid < a.N;
+      float ks = 1.f, lv = 0.f, iv = 1.f;
       // V16 buffer 1 held q of the tree's scores; else the buffer is free once the other group's product has run
       if (!is_tree && !dead) {
         if (i >= kPtVBuf) dead = !pt_wait(bar(T_VHFREE + buf), (uint32_t)(i / 3 - 1) & 1u, &s_abort, limit);
@@ -557,6 +559,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (!dead) dead = !pt_wait(bar(T_VFULL + stage), (uint32_t)(j / kPtStages) & 1u, &s_abort, limit);
         const uint32_t units = *(volatile uint32_t *)&s_units[stage];
         const int lim = L - (t0 + j) * kPtKeys;  // rows past it hold no key of this sequence
+        lds_f4(saddr(&s_scale[stage][tid >> 4]), ks, lv, iv);
+        there = tid < lim && ((units >> (tid >> 4)) & 1u);
         const int c = gt & 7, r7 = (gt >> 3) & 7, r64 = gt >> 6, c0 = 2 * (c & 3);
         const int swap = (c >> 2) ^ (r7 & 1);
         const uint32_t from = sb + kPtOffV + stage * kPtTile8 + 1024u * (uint32_t)r64 + sw128(r7, c);
@@ -590,6 +594,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(T_VEMPTY + stage));
       }
+      uint32_t keep = there ? 0xffffffffu : 0u;  // bit q: row r0 + q attends this thread's key
+      if (is_tree && there) {
+        keep = 0u;
+#pragma unroll 4
+        for (int q = 0; q < kPtQ; ++q) {
+          const unsigned long long m =
+              *(reinterpret_cast<const unsigned long long *>(sm + kPtOffMask) + 2 * (r0 + q) + (tid >> 6));
+          keep |= (uint32_t)((m >> (tid & 63)) & 1ull) << q;
+        }
+      }
+      const bool masked = __any_sync(0xffffffffu, keep != 0xffffffffu);
       if (!dead) dead = !pt_wait(bar(T_SFULL + buf), (uint32_t)(i / 3) & 1u, &s_abort, limit);
       // this group's weights (and O) are free once its last product has run, long before now
       if (!dead && i >= 2) dead = !pt_wait(bar(T_PVDONE + w), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
@@ -614,7 +629,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       tc_fence_before();  // the scores sit in registers: their buffer is free
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(T_SFREE + buf));
-      my_scale(page_n, ks_n, vs_n);  // in flight until the next item
       if (masked) {  // whatever was scored there
 #pragma unroll
         for (int q = 0; q < kPtQ; ++q) x[q] = (keep >> q) & 1u ? x[q] : -INFINITY;
