@@ -195,6 +195,7 @@ et_status launch_row(const PagedAttnArgs &a, int d, cudaStream_t st) {
 constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
 constexpr int kPaTile = 32;  // keys per tile
+constexpr int kPaLeast = 8;  // tiles in a chunk, at least
 
 template <int D, int WR, int MT>
 struct PaShape {
@@ -316,6 +317,51 @@ __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const
       }
 }
 
+// A batch of up to 32 sequences shared among `blocks` blocks per tile of rows, all chunks of one length: the shortest,
+// to a 31st of its range, that needs no more blocks.  Every warp works it out for itself, a sequence a lane.
+struct Share { int b, chunk, chunks, per; };  // b < 0: nothing for block c
+__device__ __forceinline__ Share share_batch(const PagedAttnArgs &a, int lane, int blocks, int c) {
+  int ignore = 0;
+  const int L = lane < a.B ? paged_prefix(a, lane, ignore) : -1, T = L < 0 ? 0 : (L + kPaTile - 1) / kPaTile;
+  const int present = __popc(__ballot_sync(0xffffffffu, L >= 0));
+  const int longest = __reduce_max_sync(0xffffffffu, T);
+  const float total = (float)__reduce_add_sync(0xffffffffu, (unsigned)T);  // < 2^31: 32 sequences of 2^26 tiles at most
+  // sum of ceil(T / per) <= total / per + present, so the upper end needs no more than `blocks`
+  const int lo = max(max(kPaLeast, (longest + kPaMaxSplits - 1) / kPaMaxSplits), (int)(total / (float)blocks));
+  const int hi = max(lo, (int)(total * 1.000001f / (float)(blocks - present)) + 1), step = (hi - lo + 30) / 31;
+  const int mine = lo + lane * step;
+  // ceil(T / per): at most kPaMaxSplits, so the quotient in fp32 is off by one at most
+  auto pieces = [&](int tiles, int per) -> int {
+    const int x = tiles + per - 1;
+    int q = (int)((float)x * (1.f / (float)per));
+    const int r = x - q * per;
+    q += (r >= per ? 1 : 0) - (r < 0 ? 1 : 0);
+    return max(q, 1);
+  };
+  int need = 0;
+#pragma unroll 4
+  for (int k = 0; k < a.B; ++k) {
+    const int Lk = __shfl_sync(0xffffffffu, L, k), Tk = __shfl_sync(0xffffffffu, T, k);
+    need += Lk < 0 ? 0 : pieces(Tk, mine);
+  }
+  const uint32_t fits = __ballot_sync(0xffffffffu, need <= blocks);
+  Share s;
+  s.per = __shfl_sync(0xffffffffu, mine, fits ? __ffs(fits) - 1 : 31);
+  const int own = L < 0 ? 0 : pieces(T, s.per);
+  int upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int before = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += before;
+  }
+  const uint32_t past = __ballot_sync(0xffffffffu, upto > c);
+  s.b = past ? __ffs(past) - 1 : -1;
+  const int at = max(s.b, 0);
+  s.chunks = __shfl_sync(0xffffffffu, own, at);
+  s.chunk = c - __shfl_sync(0xffffffffu, upto - own, at);
+  return s;
+}
+
 template <int D, int FMT, int WR, int MT>
 __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
     k_paged_attn_mma(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -343,31 +389,43 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   }
   pdl_wait();     // the previous kernel in the stream has completed
   pdl_trigger();  // only now may the next kernel launch
-  const int b = blockIdx.z, g = blockIdx.y / ma.row_tiles, rt = blockIdx.y - g * ma.row_tiles, chunk = blockIdx.x;
-  int bad = 0;
-  const int L = paged_prefix(a, b, bad);
-  // chunks are as long in every sequence: the longest sequence's share
-  int longest = L;
-  if (a.B > 1) {
-    int other = 0;
-    if (a.B <= kPaThreads) {
-      int ignore = 0;
-      if (t < a.B) other = paged_prefix(a, t, ignore);
-    } else {
-      other = min((long long)a.max_prefix, (long long)a.max_blocks * a.P);
-    }
-    other = __reduce_max_sync(0xffffffffu, other);
-    if (lane == 0) s_red[warp] = other;
-    __syncthreads();  // (also: the barriers are initialised)
-    longest = max(max(s_red[0], s_red[1]), max(s_red[2], s_red[3]));
-  } else {
-    __syncthreads();
+  const int g = blockIdx.y / ma.row_tiles, rt = blockIdx.y - g * ma.row_tiles;
+  // chunks are as long in every sequence: the length that shares the batch among the grid's blocks, or the longest
+  // sequence's share
+  int b = blockIdx.z, chunk = blockIdx.x, per, chunks, bad = 0;
+  long long slot0 = ((long long)b * ma.tiles_y + blockIdx.y) * ma.S;  // of the sequence's first chunk, in the workspace
+  if (ma.flat) {
+    const Share share = share_batch(a, lane, gridDim.x, blockIdx.x);
+    if (share.b < 0) return;
+    b = share.b;
+    chunk = share.chunk;
+    per = share.per;
+    chunks = share.chunks;
+    slot0 = (long long)blockIdx.y * gridDim.x + blockIdx.x - chunk;
   }
-  if (L < 0) return;
-  const int T = (L + kPaTile - 1) / kPaTile, Tl = (longest + kPaTile - 1) / kPaTile;
-  const int per = max((Tl + ma.S - 1) / ma.S, 1);
-  const int chunks = max(1, (T + per - 1) / per);
-  if (chunk >= chunks) return;
+  const int L = paged_prefix(a, b, bad);
+  if (!ma.flat) {
+    int longest = L;
+    if (a.B > 1) {
+      int other = 0;
+      if (a.B <= kPaThreads) {
+        int ignore = 0;
+        if (t < a.B) other = paged_prefix(a, t, ignore);
+      } else {
+        other = min((long long)a.max_prefix, (long long)a.max_blocks * a.P);
+      }
+      other = __reduce_max_sync(0xffffffffu, other);
+      if (lane == 0) s_red[warp] = other;
+      __syncthreads();
+      longest = max(max(s_red[0], s_red[1]), max(s_red[2], s_red[3]));
+    }
+    if (L < 0) return;
+    per = max(((longest + kPaTile - 1) / kPaTile + ma.S - 1) / ma.S, 1);
+    chunks = max(1, ((L + kPaTile - 1) / kPaTile + per - 1) / per);
+    if (chunk >= chunks) return;
+  }
+  __syncthreads();  // the barriers are initialised
+  const int T = (L + kPaTile - 1) / kPaTile;
   const int t0 = chunk * per, t1 = min(T, t0 + per);
   const int first = t0 + kg;  // this group's i-th tile: first + KG * i
   const int n = t1 > first ? (t1 - first + KG - 1) / KG : 0;
@@ -774,7 +832,7 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
     if (chunks == 1) {
       write_row(r, c, v, M, sum);
     } else {
-      const long long at = (tile_id * ma.S + chunk) * R + r;
+      const long long at = (slot0 + chunk) * R + r;
       ma.part_o[at * (D / 4) + c] = v;
       if (c == 0) ma.part_ml[at] = make_float2(M, sum);
     }
@@ -782,7 +840,7 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   if (chunks == 1) return;
   // ---- the chunks' rows, merged by the last block to arrive ----
   if (!arrive_last(ma.cnt + tile_id, (unsigned)chunks, &s_last)) return;
-  merge_chunks<D, R, kPaThreads>(ma, tile_id, chunks, real, sm, write_row);
+  merge_chunks<D, R, kPaThreads>(ma, slot0, chunks, real, sm, write_row);
 }
 
 // ---------------------------------------------------------------------------
@@ -792,7 +850,8 @@ template <int D, int FMT, int WR, int MT>
 et_status launch_mma(const CUtensorMap &mk, const CUtensorMap &mv, const PagedSplitArgs &ma, cudaStream_t st) {
   using Sh = PaShape<D, WR, MT>;
   if (et_smem_attr((const void *)k_paged_attn_mma<D, FMT, WR, MT>, Sh::kBytes) != cudaSuccess) return ET_ERR_CUDA;
-  return et_launch(k_paged_attn_mma<D, FMT, WR, MT>, dim3(ma.S, ma.tiles_y, ma.a.B), dim3(kPaThreads), Sh::kBytes, st,
+  const dim3 grid = ma.flat ? dim3(ma.flat, ma.tiles_y) : dim3(ma.S, ma.tiles_y, ma.a.B);
+  return et_launch(k_paged_attn_mma<D, FMT, WR, MT>, grid, dim3(kPaThreads), Sh::kBytes, st,
                    0, mk, mv, ma);
 }
 template <int D, int FMT>
@@ -805,7 +864,8 @@ et_status launch_mma_rows(int R, const CUtensorMap &mk, const CUtensorMap &mv, c
 }
 
 struct PagedPlan {
-  int S;      // blocks a sequence's keys are split over
+  int S;      // blocks a sequence's keys are split over (flat: at most)
+  int flat;   // blocks per tile of rows that share the batch, 0: S of each sequence
   int R;      // query rows per block
   int row_tiles;
   bool tc;    // tcgen05 kernel (bf16, d = 128, more than 16 rows per KV head), else mma.sync
@@ -859,6 +919,7 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   p->ws = p->ml_off = p->o_off = 0;
   p->R = p->row_tiles = 1;
   p->tc = false;
+  p->flat = 0;
   if (s->dtype == ET_F32) return ET_OK;
   const long long rows = (long long)s->N * (s->Hq / c->Hkv);
   p->tc = c->d == 128 && rows > 16;
@@ -877,11 +938,18 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
       // one block per SM, of eight 32-key tiles at least (8 KV heads, prefix 16384: 20.7 us in 19 chunks, 21.9 in 38)
       S = (int)least(sm_count() / tiles, T / 8);
     } else {
-      // sequences of any length: a wave of three blocks per SM of eight tiles at least; many waves only of long chunks
-      // (8 KV heads, 512..16384 tokens: 16 sequences 66.9 us in 4 chunks, 64.9 in 16; 4
-      // sequences 57 us in 64, 43 in 16)
-      const long long wave = least(3ll * sm_count() / tiles, T / 8), waves = least(14ll * sm_count() / tiles, T / 32);
+      // Where one wave of blocks gives every sequence three chunks, the lengths themselves share it out (8 KV heads,
+      // 16 sequences: of 512..16384 tokens 59.4 us, 65.1 in 16 chunks each; of 8880 each 59.4, 58.2 in 3 chunks each,
+      // 73.2 in 16).  Short ones (4 of 1024: 16.0 us against 14.4) and larger batches take chunks of the longest's
+      // share: a wave of eight tiles at least, or many waves of long chunks (32 KV heads: 16 sequences of up to 8192
+      // 110.7 us in 4 chunks, 113.3 in one; 32 of up to 2048 61 in one, 71 in two, 107 shared out by length).
+      const long long slots = (p->R <= 16 ? 3ll : 2ll) * sm_count() / (tiles / s->B);  // blocks per tile of rows at once
+      const long long wave = least(3ll * sm_count() / tiles, T / 8), waves = least(14ll * sm_count() / tiles, T / 64);
       S = (int)(waves >= 2 * wave ? waves : wave);
+      if (s->B <= 32 && slots >= 3 * s->B && T >= 8 * kPaLeast) {
+        p->flat = (int)slots;
+        S = (int)least(slots - s->B + 1, T / kPaLeast);
+      }
     }
   }
   if (S > T) S = T;
@@ -889,11 +957,12 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   if (S < 1) S = 1;
   p->S = S;
   if (S > 1 && !(p->tc && S <= kPtMaxCluster)) {
+    const size_t parts = p->flat ? (size_t)(tiles / s->B) * p->flat : (size_t)tiles * S;
     const size_t cnt = ((size_t)tiles * sizeof(unsigned int) + 255) & ~(size_t)255;
-    const size_t ml = ((size_t)tiles * S * p->R * sizeof(float2) + 255) & ~(size_t)255;
+    const size_t ml = (parts * p->R * sizeof(float2) + 255) & ~(size_t)255;
     p->ml_off = cnt;
     p->o_off = cnt + ml;
-    p->ws = cnt + ml + (size_t)tiles * S * p->R * c->d * sizeof(float);
+    p->ws = cnt + ml + parts * p->R * c->d * sizeof(float);
   }
   return ET_OK;
 }
@@ -947,6 +1016,7 @@ extern "C" et_status et_tree_attention_paged(const et_paged_attn_shape *shape, c
   PagedSplitArgs ma;
   ma.a = a;
   ma.S = plan.S;
+  ma.flat = plan.flat;
   ma.row_tiles = plan.row_tiles;
   ma.tiles_y = cache->Hkv * plan.row_tiles;
   ma.box = cache->page_size % kPaTile == 0 ? kPaTile : 16;

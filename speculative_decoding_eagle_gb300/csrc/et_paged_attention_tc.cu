@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   }
   // ---- more chunks than a cluster has blocks: merged by the last block to arrive ----
   if (!arrive_last(ma.cnt + tile_id, (unsigned)chunks, &s_last)) return;
-  merge_chunks<kPtD, kPtRows, kPtThreads>(ma, tile_id, chunks, real, sm, write4);
+  merge_chunks<kPtD, kPtRows, kPtThreads>(ma, tile_id * ma.S, chunks, real, sm, write4);
 }
 
 }  // namespace

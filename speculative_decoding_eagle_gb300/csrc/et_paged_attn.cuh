@@ -28,6 +28,7 @@ struct PagedAttnArgs {
 struct PagedSplitArgs {
   PagedAttnArgs a;
   int S, tiles_y;       // chunks, Hkv * row tiles
+  int flat;             // blocks per row tile that share the whole batch; 0: S of each sequence
   int row_tiles;        // row tiles per KV head
   int box;              // rows per TMA box
   unsigned int *cnt;    // [B * tiles_y] arrival counters; null when the chunks need none (one, or a cluster)
@@ -91,10 +92,10 @@ __device__ __forceinline__ float ex2_fast(float x) {
 // run by the last block of the tile to arrive (NT threads, `sm` free shared
 // memory).  Every load of a row's parts is in flight before any arithmetic.
 template <int D, int R, int NT, typename Write>
-__device__ __forceinline__ void merge_chunks(const PagedSplitArgs &ma, long long tile_id, int chunks, int real,
+__device__ __forceinline__ void merge_chunks(const PagedSplitArgs &ma, long long slot0, int chunks, int real,
                                              unsigned char *sm, Write write_row) {
   const int t = threadIdx.x;
-  const long long base = tile_id * ma.S * R;
+  const long long base = slot0 * R;  // slot0: the first chunk's place in the workspace
   float2 *pair = reinterpret_cast<float2 *>(sm);  // [chunks][real]: (maximum, sum), then (weight, -)
   float2 *stat = pair + kPaMaxSplits * R;         // [real]: the row's maximum and sum
   for (int x = t; x < chunks * real; x += NT) {

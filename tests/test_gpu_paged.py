@@ -690,6 +690,43 @@ def test_chunks_that_form_a_cluster_and_more_that_use_the_workspace(splits, chun
         assert torch.equal(r["out"], r["want"]) and int(r["status"].item()) == 0
 
 
+SHARED = [  # lens: sequences whose lengths decide how many blocks each has
+    [2100, -1, 0, 1, 700, 64, 2048],
+    [2048, 2048],
+    [-1, 2500, -1],
+    [5000, 33, 32, 31],
+    [int(n) for n in np.random.default_rng(1).integers(0, 900, 31)] + [2049],
+]
+
+
+@pytest.mark.parametrize("lens", SHARED, ids=lambda v: f"{len(v)}x{max(v)}")
+@pytest.mark.parametrize("N,Hq,Hkv,d,fmt", [(1, 4, 2, 128, "e4m3"), (1, 2, 1, 64, "e5m2"), (20, 1, 1, 64, "e4m3"),
+                                            (60, 1, 1, 64, "e4m3")])
+def test_a_batch_shared_out_by_its_lengths(lens, N, Hq, Hkv, d, fmt):
+    """One graph serves the lengths it was captured with and others; the share is worked out on the device."""
+    rng = np.random.default_rng(41)
+    B = len(lens)
+    pool = Pool(rng, lens, 48, Hkv, d, fmt)
+    keep = random_tree(rng, B, N)
+    r = run_attention(pool, B, N, Hq, "bf16", rng, keep)
+    assert E.et_tree_attention_paged_splits(r["shape"], pool.cache) > 1
+    check_all(pool, r, keep, "bf16")
+    want = r["out"].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        E.et_tree_attention_paged(*r["args"], lse=r["lse"], ws=r["ws"], dev_status=r["status"])
+    prefix, first = r["args"][3], list(lens)
+    for other in ([n // 3 if n > 0 else n for n in lens], [min(n, 0) for n in lens], [-1] * B, first):
+        prefix.copy_(torch.tensor(other, dtype=torch.int32))
+        r["out"].fill_(7.0)
+        r["lse"].fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        pool.lens = other
+        check_all(pool, r, keep, "bf16")
+    assert torch.equal(r["out"], want) and int(r["status"].item()) == 0
+
+
 @pytest.mark.parametrize("N,Hq,Hkv,d", [(1, 4, 2, 128), (30, 2, 1, 128), (30, 2, 1, 64), (70, 1, 1, 64)])
 @pytest.mark.parametrize("splits", [1, 2, 7, 64, 1000])
 def test_every_number_of_chunks_gives_the_same_sums(N, Hq, Hkv, d, splits):
