@@ -402,8 +402,9 @@ int32_t et_tree_build_launches(const et_tree_cfg *cfg);
 /*
  * et_set_wait_limit -- a diagnostic, not part of the method.  Sets the bound,
  * in SM clock cycles, of every device-side wait of the kernels launched
- * after the call (the mbarrier waits of et_tree_attention's tcgen05 path and
- * of et_lm_head, the frontier waits of et_tree_build); 0 or a negative value
+ * after the call (the mbarrier waits of et_tree_attention's tcgen05 path, of
+ * bf16 et_tree_attention_paged and of et_lm_head, the frontier waits of
+ * et_tree_build); 0 or a negative value
  * restores the default of 2^32 cycles (about 2 s).  A wait that runs out
  * sets ET_DEV_TIMEOUT in dev_status; the kernel lets its copies and MMAs in
  * flight finish (with the default bound), frees its tensor memory and
@@ -661,8 +662,9 @@ et_status et_kv_commit(const et_commit_shape *shape, const void *k_tree, const v
  * sets ET_DEV_BAD_INDEX and leaves that request as it is, without slots.  A
  * free_count outside [0, num_pages] is clamped, a page id outside the pool is
  * moved as it is (its tokens get no slots) and a stack that would pass
- * num_pages is cut: ET_DEV_BAD_INDEX too.  Pages belong to one request each: shared prefixes are the
- * caller's to count.  No workspace; one launch of one thread-block cluster.
+ * num_pages is cut: ET_DEV_BAD_INDEX too.  Pages belong to one request each:
+ * shared prefixes are the caller's to count.  No workspace; one launch of one
+ * thread-block cluster.
  */
 et_status et_block_map(const et_block_map_shape *shape, const int32_t *prefix_len, const int32_t *new_len,
                        int32_t *n_blocks, int32_t *block_table, int32_t *free_list, int32_t *free_count,
@@ -735,10 +737,11 @@ et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_
  * tokens; both set ET_DEV_BAD_INDEX.
  * Scores, softmax statistics and outputs accumulate in fp32.  bf16 inputs:
  * cached codes meet q as it is (only what lies 2^-38 below the largest of its
- * row is lost; 2^-18 with d = 128 and more than 16 rows, N * Hq / Hkv, per KV
- * head, where q goes to the 8-bit tensor cores in two terms), weights are rounded to fp16 (cached tokens) or bf16 (tree
- * rows) before they meet V.  A q row that holds
- * a NaN or an infinity gives NaN.  fp32 inputs: fp32 throughout.
+ * row is lost; 2^-17.8 of it at most with d = 128 and more than 16 rows,
+ * N * Hq / Hkv, per KV head, where q goes to the 8-bit tensor cores in two
+ * terms), weights are rounded to fp16 (cached tokens) or bf16 (tree rows)
+ * before they meet V.  A q row that holds a NaN or an infinity gives NaN.
+ * fp32 inputs: fp32 throughout.
  * bf16 inputs: a bounded wait that expires sets ET_DEV_TIMEOUT and leaves that
  * block's rows undefined.  Calls that can run at the same time need separate
  * workspaces.
@@ -747,7 +750,13 @@ et_status et_tree_attention_paged(const et_paged_attn_shape *shape, const et_pag
                                   const int32_t *block_table, const int32_t *prefix_len, const void *q,
                                   const void *k_tree, const void *v_tree, const uint64_t *mask, void *out, float *lse,
                                   int32_t *dev_status, void *ws, size_t ws_bytes, et_stream_t stream);
-/* Workspace bytes of that call (0 if no split merge is needed), and the blocks its keys are split over (-1 if the shape breaks a limit). */
+/*
+ * Workspace bytes of that call (0 if no merge through memory is needed), and
+ * the blocks a sequence's keys are split over at most (-1 if the shape breaks
+ * a limit).  With num_splits = 0 a batch of up to 32 sequences of up to 16
+ * rows per KV head (d = 64: any) may be shared out by its lengths, on the
+ * device: a longer sequence then has more blocks.
+ */
 size_t et_tree_attention_paged_workspace_size(const et_paged_attn_shape *shape, const et_paged_cache *cache);
 int32_t et_tree_attention_paged_splits(const et_paged_attn_shape *shape, const et_paged_cache *cache);
 
