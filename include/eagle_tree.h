@@ -729,7 +729,9 @@ et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_
  *               and lse = -inf.
  * lse           nullable fp32 [B, Hq, N], as in et_tree_attention.
  * ws            et_tree_attention_paged_workspace_size() bytes, zero-filled
- *               once (see conventions); 0/null when that size is 0.
+ *               once (see conventions); 0/null when that size is 0.  Calls of
+ *               this function with other shapes may use it before and after,
+ *               other functions may not.
  * v_scale counts as at least 2^-48 and at most 2^48 (what et_kv_commit_paged
  * writes); k_scale may be any finite value.  Rows of a page past the prefix
  * are not used, whatever they hold.  A prefix past max_prefix or past

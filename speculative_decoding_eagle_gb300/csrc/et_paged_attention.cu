@@ -207,6 +207,9 @@ constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
 constexpr int kPaTile = 32;  // keys per tile
 constexpr int kPaLeast = 8;  // tiles in a chunk, at least
+// arrival counters in every workspace, at its start: the same place whatever the shape, so that calls of different
+// shapes can use one workspace one after the other
+constexpr int kPaCounters = 1 << 16;
 
 template <int D, int WR, int MT>
 struct PaShape {
@@ -966,10 +969,12 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   if (S > T) S = T;
   if (S > kPaMaxSplits) S = kPaMaxSplits;
   if (S < 1) S = 1;
+  if (tiles > kPaCounters && !(p->tc && S <= kPtMaxCluster)) S = 1;  // far more blocks than SMs as it is
+  if (S == 1) p->flat = 0;
   p->S = S;
   if (S > 1 && !(p->tc && S <= kPtMaxCluster)) {
     const size_t parts = p->flat ? (size_t)(tiles / s->B) * p->flat : (size_t)tiles * S;
-    const size_t cnt = ((size_t)tiles * sizeof(unsigned int) + 255) & ~(size_t)255;
+    const size_t cnt = kPaCounters * sizeof(unsigned int);
     const size_t ml = (parts * p->R * sizeof(float2) + 255) & ~(size_t)255;
     p->ml_off = cnt;
     p->o_off = cnt + ml;

@@ -690,6 +690,25 @@ def test_chunks_that_form_a_cluster_and_more_that_use_the_workspace(splits, chun
         assert torch.equal(r["out"], r["want"]) and int(r["status"].item()) == 0
 
 
+def test_one_workspace_serves_calls_of_different_shapes():
+    """What one call leaves in a workspace of the largest size is no other call's counter."""
+    rng = np.random.default_rng(43)
+    pool = Pool(rng, [2100, 700], 48, 4, 128, "e4m3")
+    small = Pool(rng, [900] + [40] * 30, 16, 4, 128, "e4m3")
+    runs = []
+    for p, N, splits in ((pool, 1, 5), (small, 1, 2), (pool, 61, 12), (pool, 2, 0), (small, 4, 7)):
+        keep = random_tree(rng, len(p.lens), N)
+        r = run_attention(p, len(p.lens), N, 4, "bf16", rng, keep, splits)
+        check_all(p, r, keep, "bf16")
+        runs.append(dict(r, want=r["out"].clone()))
+    ws = E.new_workspace(max(r["ws"].numel() for r in runs))
+    for r in runs + runs[::-1]:
+        r["out"].zero_()
+        E.et_tree_attention_paged(*r["args"], lse=r["lse"], ws=ws, dev_status=r["status"])
+        torch.cuda.synchronize()
+        assert torch.equal(r["out"], r["want"]) and int(r["status"].item()) == 0
+
+
 SHARED = [  # lens: sequences whose lengths decide how many blocks each has
     [2100, -1, 0, 1, 700, 64, 2048],
     [2048, 2048],
