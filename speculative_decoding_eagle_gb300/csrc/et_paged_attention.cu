@@ -201,8 +201,8 @@ et_status launch_row(const PagedAttnArgs &a, int d, cudaStream_t st) {
 // one row each: 320 us, 6.7 TB/s.  A block takes about 10 us beside its stream (its
 // lengths, page table and first tiles one after the other; its groups' rows
 // and the sequence's chunks merged): 16 sequences of 512..16384 tokens, 8 KV
-// heads of 8 query heads: 57 us in a graph, 5.1 TB/s; one of 1023, 32 heads: 10.2 us in a
-// graph, 0.8 TB/s.
+// heads of 8 query heads: 57 us in a graph, 5.1 TB/s; one of 1023, 32 heads: 8.4 us in a
+// graph, 1.0 TB/s.
 constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
 constexpr int kPaTile = 32;  // keys per tile
@@ -224,7 +224,7 @@ struct PaShape {
   static constexpr int kOffRow = kOffQ16 + R * D * 2;       // row factors
   static constexpr int kOffBar = kOffRow + R * 4;
   static constexpr int kBytes = kOffBar + KG * kStages * 8 + 1024;  // + slack for 1024-byte alignment
-  static_assert(KG * R * D * 4 + KG * R * 8 <= kOffRow, "the groups' rows are merged in the space of the ring and q");
+  static_assert(KG * R * D * 4 + (KG + 1) * R * 8 <= kOffRow, "the groups' rows are merged in the space of the ring and q");
   static_assert((kPaMaxSplits + 1) * R * 8 <= kOffRow, "the chunks' pairs, too");
   static_assert(kBlocks * (kBytes + 1024 + 64) <= 228 * 1024, "the blocks of an SM");
 };
@@ -450,16 +450,17 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   auto fetch_page = [&](int batch, int &pg, int &sl) {
     const int i = 16 * batch + (lane >> 1);
     const long long key = (long long)(first + (long long)KG * i) * kPaTile + 16 * (lane & 1);
-    pg = -1;
+    pg = sl = -1;
     if (i < n && key < L) {
       const int blk = page_index(ma, (int)key);
       sl = (int)key - blk * a.P;
       pg = a.block_table[(long long)b * a.max_blocks + blk];
-      if (pg < 0 || pg >= a.num_pages) {
-        pg = -1;
-        bad = 1;
-      }
     }
+  };
+  auto check_page = [&](int &pg, int sl) {  // apart from the load, which it would wait for
+    if (pg >= 0 && pg < a.num_pages) return;
+    if (sl >= 0) bad = 1;
+    pg = -1;
   };
   auto fetch_scale = [&](int pg, float &ks, float &vs) {
     ks = 0.f;
@@ -503,6 +504,7 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
     }
   };
   fetch_page(0, page, slot);
+  check_page(page, slot);
   if (wr == 0)
     for (int i = 0; i < n && i < ST; ++i) issue(i, page, slot);
 
@@ -681,6 +683,7 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
       }
       fetch_page((i >> 4) + 1, page_n, slot_n);
     } else if ((i & 15) == 1) {
+      check_page(page_n, slot_n);
       fetch_scale(page_n, ksc_n, vsc_n);
     }
     const int stage = i % ST;
@@ -818,6 +821,7 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   __syncthreads();
   const int real = min(R, a.N * a.G - rt * R);  // rows that exist are a prefix of the tile
   const long long tile_id = (long long)b * ma.tiles_y + blockIdx.y;
+  const bool cluster = ma.cnt == nullptr;
   auto write_row = [&](int r, int c, const float4 &v, float M, float sum) {
     const int Rg = rt * R + r, i = row_token(ma, Rg), h = g * a.G + (Rg - i * a.G);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -845,6 +849,9 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
     }
     if (chunks == 1) {
       write_row(r, c, v, M, sum);
+    } else if (cluster) {  // for the cluster to read: a cell where only this thread read one
+      rows[r * (D / 4) + merge_chunk<D>(r, c)] = v;
+      if (c == 0) ml[KG * R + r] = make_float2(M, sum);
     } else {
       const long long at = (slot0 + chunk) * R + r;
       ma.part_o[at * (D / 4) + c] = v;
@@ -852,6 +859,41 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
     }
   }
   if (chunks == 1) return;
+  if (cluster) {
+    // ---- the chunks' rows, each merged by one of the cluster's blocks ----
+    // (blocks without keys have left: the barrier counts the others)
+    __syncwarp();
+    cl_sync();
+    for (int x = t; x < (real - chunk + chunks - 1) / chunks * (D / 4); x += kPaThreads) {
+      const int r = chunk + x / (D / 4) * chunks, c = x % (D / 4);
+      float4 y[kPaMaxCluster];
+      float2 e[kPaMaxCluster];
+#pragma unroll
+      for (int k = 0; k < kPaMaxCluster; ++k) {  // every load in flight before any arithmetic
+        y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        e[k] = make_float2(-3e38f, 0.f);
+        if (k < chunks) {
+          y[k] = cl_ld_f32x4(cl_map(&rows[r * (D / 4) + merge_chunk<D>(r, c)], (uint32_t)k));
+          const uint32_t at = cl_map(&ml[KG * R + r], (uint32_t)k);
+          e[k] = make_float2(cl_ld_f32(at), cl_ld_f32(at + 4u));
+        }
+      }
+      float M = e[0].x, sum = 0.f;
+#pragma unroll
+      for (int k = 1; k < kPaMaxCluster; ++k) M = fmaxf(M, e[k].x);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kPaMaxCluster; ++k) {
+        const float w = ex2_fast(e[k].x - M);
+        sum = fmaf(e[k].y, w, sum);
+        v.x = fmaf(y[k].x, w, v.x); v.y = fmaf(y[k].y, w, v.y); v.z = fmaf(y[k].z, w, v.z); v.w = fmaf(y[k].w, w, v.w);
+      }
+      write_row(r, c, v, M, sum);
+    }
+    __syncwarp();
+    cl_sync();  // no block leaves while another reads its rows
+    return;
+  }
   // ---- the chunks' rows, merged by the last block to arrive ----
   if (!arrive_last(ma.cnt + tile_id, (unsigned)chunks, &s_last)) return;
   merge_chunks<D, R, kPaThreads>(ma, slot0, chunks, real, sm, write_row);
@@ -866,7 +908,7 @@ et_status launch_mma(const CUtensorMap &mk, const CUtensorMap &mv, const PagedSp
   if (et_smem_attr((const void *)k_paged_attn_mma<D, FMT, WR, MT>, Sh::kBytes) != cudaSuccess) return ET_ERR_CUDA;
   const dim3 grid = ma.flat ? dim3(ma.flat, ma.tiles_y) : dim3(ma.S, ma.tiles_y, ma.a.B);
   return et_launch(k_paged_attn_mma<D, FMT, WR, MT>, grid, dim3(kPaThreads), Sh::kBytes, st,
-                   0, mk, mv, ma);
+                   ma.cnt || ma.S == 1 ? 0 : ma.S, mk, mv, ma);
 }
 template <int D, int FMT>
 et_status launch_mma_rows(int R, const CUtensorMap &mk, const CUtensorMap &mv, const PagedSplitArgs &ma, cudaStream_t st) {
@@ -908,7 +950,7 @@ int tc_splits(long long tiles, int T, int B) {
   int best = 1;
   double least = 1e30;
   for (int S = 1; S <= kPaMaxSplits && S <= T; ++S) {
-    const bool cluster = S > 1 && S <= kPtMaxCluster;
+    const bool cluster = S > 1 && S <= kPaMaxCluster;
     const long long together = cluster ? paged_tc_clusters(S, sms) : sms, units = cluster ? tiles : tiles * S;
     const double chunk = (T + S - 1) / S, merge = cluster ? 3 : S > 1 ? 8 : 0;
     const double cost = B == 1 ? (double)((units + together - 1) / together) * (kBlock + chunk + merge)
@@ -969,10 +1011,15 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   if (S > T) S = T;
   if (S > kPaMaxSplits) S = kPaMaxSplits;
   if (S < 1) S = 1;
-  if (tiles > kPaCounters && !(p->tc && S <= kPtMaxCluster)) S = 1;  // far more blocks than SMs as it is
+  // one sequence's blocks merge as a cluster where they can (32 KV heads, prefix 1023: 8.4 us in a graph, 10.0 through
+  // the workspace); a batch's blocks of few rows do not, its short sequences leave clusters half empty (32 KV heads, 16
+  // sequences of up to 8192: 131 us, 110 through the workspace).  Of the tcgen05 kernel's blocks an SM holds one, so few
+  // wait (32 KV heads, 2 sequences of up to 16384: 68.3 us, 71.2 through the workspace)
+  const bool cluster = S > 1 && S <= kPaMaxCluster && (p->tc || s->B == 1);
+  if (tiles > kPaCounters && !cluster) S = 1;  // far more blocks than SMs as it is
   if (S == 1) p->flat = 0;
   p->S = S;
-  if (S > 1 && !(p->tc && S <= kPtMaxCluster)) {
+  if (S > 1 && !cluster) {
     const size_t parts = p->flat ? (size_t)(tiles / s->B) * p->flat : (size_t)tiles * S;
     const size_t cnt = kPaCounters * sizeof(unsigned int);
     const size_t ml = (parts * p->R * sizeof(float2) + 255) & ~(size_t)255;

@@ -198,11 +198,6 @@ __device__ __forceinline__ int px(int row) { return 4 * (row >> 1) + (row & 1); 
 __device__ __forceinline__ int py(int row) { return px(row) + 2; }
 // chunk c (16 bytes) of row r in a tile of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-__device__ __forceinline__ float4 cl_ld_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 // maximum over the warp's lanes; NaN is passed over
 __device__ __forceinline__ float warp_max_f32(float x) {
   float m;
@@ -859,9 +854,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     cl_sync();
 #pragma unroll 1
     for (int r = chunk + warp * chunks; r < real; r += kPtThreads / 32 * chunks) {
-      float4 v[kPtMaxCluster];
+      float4 v[kPaMaxCluster];
 #pragma unroll
-      for (int k = 0; k < kPtMaxCluster; ++k) {
+      for (int k = 0; k < kPaMaxCluster; ++k) {
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k < chunks) v[k] = cl_ld_f32x4(cl_map(part_o, (uint32_t)k) + (uint32_t)((r * kPtD + 4 * lane) * 4));
       }
@@ -878,7 +873,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       sum = __shfl_sync(0xffffffffu, sum, 0);
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < kPtMaxCluster; ++k) {
+      for (int k = 0; k < kPaMaxCluster; ++k) {
         const float fk = __shfl_sync(0xffffffffu, f, k);
         if (k < chunks) {
           y.x = fmaf(v[k].x, fk, y.x); y.y = fmaf(v[k].y, fk, y.y);
@@ -924,7 +919,7 @@ et_status paged_tc_launch(const et_paged_cache *cache, const PagedSplitArgs &arg
 
 int paged_tc_clusters(int S, int sms) {
   constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices][kPtMaxCluster + 1];
+  static std::atomic<int> known[kDevices][kPaMaxCluster + 1];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
   if (dev >= 0 && dev < kDevices && (n = known[dev][S].load(std::memory_order_relaxed)) > 0) return n;

@@ -41,7 +41,7 @@ struct PagedSplitArgs {
 // D = 128, many rows per KV head (et_paged_attention_tc.cu)
 constexpr int kPtKeys = 128;  // keys per tile
 constexpr int kPtRows = 64;   // query rows per block
-constexpr int kPtMaxCluster = 8;  // chunks up to which a sequence's blocks form a cluster (the portable size)
+constexpr int kPaMaxCluster = 8;  // chunks up to which a sequence's blocks form a cluster (the portable size)
 // clusters of S blocks that the device runs at once (a property of the device, asked once)
 ET_HIDDEN int paged_tc_clusters(int S, int sms);
 // pages as [num_pages][Hkv][P][d] bytes; a box is `box` rows of one head of one page
@@ -86,6 +86,12 @@ __device__ __forceinline__ float ex2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float4 cl_ld_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
 // The rows of a tile's chunks, from the workspace, weighted by their maxima:
