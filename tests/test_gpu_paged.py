@@ -690,6 +690,33 @@ def test_chunks_that_form_a_cluster_and_more_that_use_the_workspace(splits, chun
         assert torch.equal(r["out"], r["want"]) and int(r["status"].item()) == 0
 
 
+@pytest.mark.parametrize("N,Hq,Hkv,d", [(1, 4, 2, 128), (5, 6, 2, 128), (30, 2, 1, 128), (1, 2, 2, 64), (30, 2, 1, 64),
+                                        (70, 1, 1, 64)])
+@pytest.mark.parametrize("splits", [2, 3, 5, 8])
+def test_one_sequence_whose_chunks_merge_as_a_cluster(N, Hq, Hkv, d, splits):
+    """One graph, the prefix it was captured with and shorter ones, which leave blocks of the cluster without keys."""
+    rng = np.random.default_rng(47)
+    pool = Pool(rng, [1100], 48, Hkv, d, "e4m3")
+    keep = random_tree(rng, 1, N)
+    r = run_attention(pool, 1, N, Hq, "bf16", rng, keep, splits)
+    assert E.et_tree_attention_paged_splits(r["shape"], pool.cache) == splits
+    assert E.et_tree_attention_paged_workspace_size(r["shape"], pool.cache) == 0
+    check_all(pool, r, keep, "bf16")
+    want = r["out"].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        E.et_tree_attention_paged(*r["args"], lse=r["lse"], ws=r["ws"], dev_status=r["status"])
+    for L in (0, 1, 31, 128, 140, 700, -1, 1100):
+        r["args"][3].fill_(L)
+        r["out"].fill_(7.0)
+        r["lse"].fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        pool.lens = [L]
+        check_all(pool, r, keep, "bf16")
+    assert torch.equal(r["out"], want) and int(r["status"].item()) == 0
+
+
 def test_one_workspace_serves_calls_of_different_shapes():
     """What one call leaves in a workspace of the largest size is no other call's counter."""
     rng = np.random.default_rng(43)
