@@ -978,6 +978,8 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   p->flat = 0;
   if (s->dtype == ET_F32) return ET_OK;
   const long long rows = (long long)s->N * (s->Hq / c->Hkv);
+  // 16 sequences of 8880 tokens, 8 KV heads: 16 rows each 60.7 us with mma.sync, 90.2 with tcgen05; 24 rows 101.3 (two
+  // row tiles) and 90.8; one sequence of 8192: 18.5 and 19.2, 21.6 and 19.5
   p->tc = c->d == 128 && rows > 16;
   p->R = rows <= 16 ? 16 : rows <= 32 && !p->tc ? 32 : 64;
   p->row_tiles = (int)((rows + p->R - 1) / p->R);
