@@ -741,8 +741,11 @@ et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_
  * cached codes meet q as it is (only what lies 2^-38 below the largest of its
  * row is lost; 2^-17.8 of it at most with d = 128 and more than 16 rows,
  * N * Hq / Hkv, per KV head, where q goes to the 8-bit tensor cores in two
- * terms), weights are rounded to fp16 (cached tokens) or bf16 (tree rows)
- * before they meet V.  A q row that holds a NaN or an infinity gives NaN.
+ * terms).  A key's weight is its softmax numerator times the V scale of its
+ * page (for tree rows: the scale that a page with their V of that head would
+ * have), and is rounded to bf16 (tree rows) or fp16 (cached tokens: to 11 bits
+ * if it is at least 2^-17 of its row's largest, to fewer below, to zero 2^-28
+ * below) before it meets V; the sum of weights is not rounded.  A q row that holds a NaN or an infinity gives NaN.
  * fp32 inputs: fp32 throughout.
  * bf16 inputs: a bounded wait that expires sets ET_DEV_TIMEOUT and leaves that
  * block's rows undefined.  Calls that can run at the same time need separate

@@ -249,17 +249,6 @@ struct CommitPagedArgs {
   int32_t *dev_status;
 };
 
-// smallest 2^e >= amax / MAX, MAX = 0.875 * 2^TOP: amax = m 2^x with m in
-// [0.5, 1) needs x - TOP when m <= 0.875, one more otherwise; x and m from the
-// bits of amax (a subnormal one is below the smallest scale whatever its x)
-template <int FMT>
-__device__ __forceinline__ float page_scale(float amax) {
-  const uint32_t bits = __float_as_uint(amax);
-  const int x = (int)(bits >> 23) - 126;
-  const int e = x - (FMT == ET_KV_E4M3 ? 9 : 16) + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return __uint_as_float((uint32_t)(127 + max(-kScaleExp, min(kScaleExp, e))) << 23);
-}
-
 // eight elements as they lie in memory, and as fp32
 template <bool BF16> struct Raw8 { uint4 v; };
 template <> struct Raw8<false> { float4 u, v; };

@@ -57,6 +57,23 @@ __device__ __forceinline__ uint32_t f32x4_to_f8x4(float x0, float x1, float x2, 
   return r;
 }
 
+// smallest 2^e >= amax / MAX, MAX = 0.875 * 2^TOP: amax = m 2^x with m in
+// [0.5, 1) needs x - TOP when m <= 0.875, one more otherwise; x and m from the
+// bits of amax (a subnormal one is below the smallest scale whatever its x)
+template <int FMT>
+__device__ __forceinline__ int page_exponent(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int x = (int)(bits >> 23) - 126;
+  const int e = x - (FMT == ET_KV_E4M3 ? 9 : 16) + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(-kScaleExp, min(kScaleExp, e));
+}
+// 2^e, e a normal number's exponent
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+template <int FMT>
+__device__ __forceinline__ float page_scale(float amax) {
+  return power_of_two(page_exponent<FMT>(amax));
+}
+
 inline et_status paged_cache_status(const et_paged_cache *c) {
   if (!c) return ET_ERR_INVALID_ARG;
   if (c->Hkv < 1 || c->d < 1 || c->page_size < 1 || c->num_pages < 1 || c->num_pages >= (1ll << 31))

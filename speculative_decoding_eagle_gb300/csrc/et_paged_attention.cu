@@ -10,6 +10,13 @@
 // so the weights meet the raw codes, no weight overflows whatever the scales
 // (the running maximum is taken over t), and the two sums hold the plain
 // softmax's numerator and denominator.
+//
+// The tree's rows, whose V is not quantised, get a scale of the same kind: vt,
+// the power of two that a page with their largest |V| would have.  t then
+// bounds p |v| for both kinds of key, whatever the size of V, and no key's
+// weight falls out of fp16's range because the other kind's V is held in
+// another unit.  Their weight is 2^(t - m) / vt (bf16, whose range has room for
+// it), so that V meets it as it is.
 #include <cuda_bf16.h>
 
 #include "et_paged_attn.cuh"
@@ -263,7 +270,8 @@ __device__ __forceinline__ int merge_chunk(int r, int c) {
 // score * f + lv relative to the row's reference mr, which moves only when a
 // weight would pass 2^15 (then it becomes the row maximum - 3 and what was
 // summed is rescaled).  keep: bit (8 * n-tile + key) per row, all ones when
-// `masked` is false.  On return p holds the weights as packed pairs.
+// `masked` is false.  On return p holds the weights as packed pairs, for the
+// tree's rows (BF16) over their V scale.
 template <int NT, int MT, int NTO, bool BF16>
 __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const float (&rf)[2 * MT],
                                               const float (&ks)[NT / 2], const float (&lv)[NT / 2],
@@ -326,8 +334,8 @@ __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const
         const float w0 = ex2_fast(x[mt][2 * u][2 * h]), w1 = ex2_fast(x[mt][2 * u][2 * h + 1]);
         const float w2 = ex2_fast(x[mt][2 * u + 1][2 * h]), w3 = ex2_fast(x[mt][2 * u + 1][2 * h + 1]);
         l[2 * mt + h] = fmaf((w0 + w1) + (w2 + w3), iv[u], l[2 * mt + h]);
-        p[mt][2 * u][h] = BF16 ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1);
-        p[mt][2 * u + 1][h] = BF16 ? pack_bf16x2(w2, w3) : pack_f16x2(w2, w3);
+        p[mt][2 * u][h] = BF16 ? pack_bf16x2(w0 * iv[u], w1 * iv[u]) : pack_f16x2(w0, w1);
+        p[mt][2 * u + 1][h] = BF16 ? pack_bf16x2(w2 * iv[u], w3 * iv[u]) : pack_f16x2(w2, w3);
       }
 }
 
@@ -387,6 +395,7 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   extern __shared__ unsigned char smem_raw[];
   __shared__ int s_abort, s_last;
   __shared__ int s_red[kPaWarps];
+  __shared__ uint32_t s_vtop;  // the tree's largest finite |V| of this head, as the bits of an fp32 value
   unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = saddr(sm);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g8 = lane >> 2, tq = lane & 3;
@@ -396,6 +405,7 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   // ---- set-up that touches no global memory ----
   if (t == 0) {
     s_abort = 0;
+    s_vtop = 0u;
     for (int i = 0; i < KG * ST; ++i) mbar_init(sb + Sh::kOffBar + 8u * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_tmap(&tm_k);
@@ -508,6 +518,27 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   if (wr == 0)
     for (int i = 0; i < n && i < ST; ++i) issue(i, page, slot);
 
+  // ---- the tree's V once over, for its scale (its products read it again, out of L1) ----
+  const int tree_cells = chunk == 0 ? a.N * (D / 8) : 0;  // 16 bytes each
+  uint32_t vtop = 0u;  // largest finite magnitudes of the low and of the high halves
+  constexpr int kTreeCells = 2;  // in flight beside q
+  uint4 cell[kTreeCells];
+  auto tree_cell = [&](int x) {
+    return x < tree_cells ? *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.vt) +
+                                                             (((long long)b * a.N + x / (D / 8)) * a.Hkv + g) * D + x % (D / 8) * 8)
+                          : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto see_cell = [&](const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = w[e] & 0x7fffu, hi = w[e] & 0x7fff0000u;
+      vtop = __vmaxu2(vtop, (lo < 0x7f80u ? lo : 0u) | (hi < 0x7f800000u ? hi : 0u));
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kTreeCells; ++k) cell[k] = tree_cell(t + k * kPaThreads);
+
   // ---- q into fragment order: D / 8 lanes per row, eight dims a lane ----
   float *row_f = reinterpret_cast<float *>(sm + Sh::kOffRow);
   {
@@ -557,6 +588,14 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
         row_f[r] = odd ? __uint_as_float(0x7fc00000u)
                        : a.scale_log2 * __uint_as_float((uint32_t)(127 - ea) << 23) * __uint_as_float((uint32_t)(127 - eb) << 23);
     }
+  }
+  if (chunk == 0) {
+#pragma unroll
+    for (int k = 0; k < kTreeCells; ++k) see_cell(cell[k]);
+#pragma unroll 1
+    for (int x = t + kTreeCells * kPaThreads; x < tree_cells; x += kPaThreads) see_cell(tree_cell(x));
+    vtop = __reduce_max_sync(0xffffffffu, max(vtop << 16, vtop & 0xffff0000u));
+    if (lane == 0) atomicMax(&s_vtop, vtop);
   }
   __syncthreads();
 
@@ -621,9 +660,10 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
       float fs[2 * MT];
 #pragma unroll
       for (int r = 0; r < 2 * MT; ++r) fs[r] = a.scale_log2;
-      const float one[1] = {1.f}, zero[1] = {0.f};
+      const int ve = page_exponent<FMT>(__uint_as_float(s_vtop));
+      const float one[1] = {1.f}, lvt[1] = {(float)ve}, ivt[1] = {power_of_two(-ve)};
       uint32_t p[MT][2][2];
-      paged_softmax<2, MT, NTO, true>(s, fs, one, zero, one, true, keep, mr, l, o, p);
+      paged_softmax<2, MT, NTO, true>(s, fs, one, lvt, ivt, true, keep, mr, l, o, p);
       bool odd = false;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {  // 8 of the thread's dims at a time

@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   __shared__ int s_abort, s_last, s_odd;
   __shared__ int s_red[kPtThreads / 32];
   __shared__ uint32_t s_tmem, s_units[kPtStages];
+  __shared__ uint32_t s_vtop;  // the tree's largest finite |V| of this head, as the bits of an fp32 value
   __shared__ float4 s_scale[kPtStages][kPtKeys / 16];  // a unit's K scale, log2 of its V scale, the inverse of that
   unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = saddr(sm);
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   if (t == 0) {
     s_abort = 0;
     s_odd = 0;
+    s_vtop = 0u;
     for (int i = 0; i < T_COUNT; ++i) {
       int count = 1;
       if (i >= T_VFULL && i < T_VEMPTY) count = 2;  // the copies, the scales
@@ -350,6 +352,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   };
   float *fc = reinterpret_cast<float *>(sm + kPtOffFC);  // group w at 2 * kPtRows * w
   bool odd_v = false;
+  uint32_t vtop = 0u;  // largest magnitudes of the low and of the high halves
   auto store_cell = [&](int x, const uint4 &k, const uint4 &v) {
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
     // NaN and infinities would reach rows that do not attend their key (0 * inf): they are added at the end
@@ -357,6 +360,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     for (int e = 0; e < 4; ++e) {
       if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; odd_v = true; }
       if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; odd_v = true; }
+      vtop = __vmaxu2(vtop, w[e] & 0x7fff7fffu);
     }
     const uint32_t at = (uint32_t)(((x & 15) >> 3) * kPtHalf16) + sw128(x >> 4, x & 7);
     sts128(sb + kPtOffTreeK + at, k.x, k.y, k.z, k.w);
@@ -430,6 +434,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       store_cell(x, k, v);
     }
     if (odd_v) s_odd = 1;
+    vtop = __reduce_max_sync(0xffffffffu, max(vtop << 16, vtop & 0xffff0000u));
+    if (lane == 0) atomicMax(&s_vtop, vtop);
     if (t < kPtRows) {
       const int i = row_token(ma, rt * kPtRows + t);
       unsigned long long m0 = 0ull, m1 = 0ull;
@@ -551,6 +557,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       static_assert(kPtVBuf == 3, "as many as score buffers");
       bool there = is_tree && tid < a.N;
       float ks = 1.f, lv = 0.f, iv = 1.f;
+      if (is_tree) {  // the scale a page with this V would have
+        const int ve = page_exponent<FMT>(__uint_as_float(*(volatile uint32_t *)&s_vtop));
+        lv = (float)ve;
+        iv = power_of_two(-ve);
+      }
       // V16 buffer 1 held q of the tree's scores; else the buffer is free once the other group's product has run
       if (!is_tree && !dead) {
         if (i >= kPtVBuf) dead = !pt_wait(bar(T_VHFREE + buf), (uint32_t)(i / 3 - 1) & 1u, &s_abort, limit);
@@ -628,7 +639,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           uint64_t f, c;  // two rows' factors and -references
           lds_pairs(fcb + 8u * (uint32_t)(8 * part + e), f, c);
           uint64_t y = pair(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1]));
-          y = is_tree ? fma2(y, f, c) : fma2(mul2(y, ks2), f, add2(lv2, c));
+          y = fma2(is_tree ? y : mul2(y, ks2), f, add2(lv2, c));
           unpair(y, x[8 * part + e], x[8 * part + e + 1]);
         }
       }
@@ -706,7 +717,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           const int q = 8 * c + 2 * e;
           const float w0 = ex2_fast(x[q]), w1 = ex2_fast(x[q + 1]);
           l2[q / 2] = fma2(pair(w0, w1), iv2, l2[q / 2]);
-          p[e] = is_tree ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1);
+          p[e] = is_tree ? pack_bf16x2(w0 * iv, w1 * iv) : pack_f16x2(w0, w1);
         }
         sts128(prow + sw128(tid, 4 * col + c), p[0], p[1], p[2], p[3]);
       }
