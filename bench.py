@@ -17,6 +17,7 @@ region are the only communication.
 from __future__ import annotations
 
 import argparse
+import contextlib
 import json
 import os
 import statistics
@@ -342,6 +343,23 @@ def whole_job_rate(step_ms: float, world: int) -> float:
     return world * 1000.0 / step_ms
 
 
+def after_current(*streams):
+    """Let side streams start after everything the current stream was given: inputs are drawn, and outputs and
+    workspaces cleared, on the current stream, which a side stream does not wait for by itself."""
+    import torch
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+
+
+@contextlib.contextmanager
+def on(stream):
+    """Work on a side stream, in order after the current one (loops that are timed order their streams once, before)."""
+    import torch
+    after_current(stream)
+    with torch.cuda.stream(stream):
+        yield
+
+
 def run_gpu(args):
     import numpy as np
     import torch
@@ -384,7 +402,7 @@ def run_gpu(args):
 
     stream = torch.cuda.Stream()
     # eager warm-up on a side stream, then one graph per input set
-    with torch.cuda.stream(stream):
+    with on(stream):
         for r in range(R):
             st.run(sets[r], stream=stream)
     stream.synchronize()
@@ -431,6 +449,7 @@ def run_gpu(args):
     eager_ms = None
     if graphs:
         ke = max(3, min(50, args.steps))
+        after_current(stream)
         e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         with torch.cuda.stream(stream):
             e0.record(stream)
@@ -446,7 +465,7 @@ def run_gpu(args):
                       attn_impl={"auto": E.ATTN_AUTO, "mma": E.ATTN_MMA_SYNC, "tcgen05": E.ATTN_TCGEN05}[args.attn])
     sa.prepare(sets[0])
     ga = torch.cuda.CUDAGraph()
-    with torch.cuda.stream(stream):
+    with on(stream):
         for r in range(R):
             sa.run(sets[r], stream=stream)  # its own trees and masks
     stream.synchronize()
@@ -467,7 +486,7 @@ def run_gpu(args):
 
     # ---- each call of the step alone, graph-timed the same way: which kernel dominates ----
     def graph_us(call):
-        with torch.cuda.stream(stream):
+        with on(stream):
             for r in range(R):
                 call(sets[r])
         stream.synchronize()
@@ -493,7 +512,8 @@ def run_gpu(args):
     # the acceptance's algorithmic minimum: the rows on the accepted paths and each stop row
     path_rows = []
     for r in range(R):
-        st.accept(sets[r], stream=stream)
+        with on(stream):
+            st.accept(sets[r], stream=stream)
         stream.synchronize()
         path_rows.append(int((st.accept_len.cpu() + 1).clamp(max=wl.depth + 1).sum()))
     accept_path_b = int(round(4 * wl.V * sum(path_rows) / len(path_rows)))
@@ -608,7 +628,8 @@ def time_attention_shape(name, prefix, stream, K, hbm_peak, bf16_peak):
     wl = W.WORKLOADS[name].with_(B=1, prefix=prefix, ragged=False)
     st = S.VerifyStep(wl, overlap=False)  # the standalone split plan
     base = S.to_device(wl, S.host_inputs(wl, st.C))
-    st.run(base, stream=stream)  # the mask of a real tree
+    with on(stream):
+        st.run(base, stream=stream)  # the mask of a real tree
     stream.synchronize()
     nb = attention_bytes(wl, [prefix])
     R = max(2, int(np.ceil(2 * L2_BYTES / nb)) + 1)
@@ -625,7 +646,7 @@ def time_attention_shape(name, prefix, stream, K, hbm_peak, bf16_peak):
         sets.append(dataclasses.replace(base, q=up(x["q"])[None], k_prefix=up(x["k_prefix"].reshape(-1, wl.d)),
                                         v_prefix=up(x["v_prefix"].reshape(-1, wl.d)), k_tree=up(x["k_tree"])[None],
                                         v_tree=up(x["v_tree"])[None]))
-    with torch.cuda.stream(stream):
+    with on(stream):
         for r in range(R):
             st.attention(sets[r], stream=stream)
     stream.synchronize()
@@ -703,7 +724,7 @@ def time_attention_batch(B, stream, K, hbm_peak, seed=11, splits=0):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     call = lambda: E.et_tree_attention(shape, q, kp, vp, row0, plen, kt, vt, mask, out, lse=lse, ws=ws,
                                        dev_status=status, stream=stream)
-    with torch.cuda.stream(stream):
+    with on(stream):
         for _ in range(3):
             call()
     stream.synchronize()
@@ -779,7 +800,7 @@ def time_tree_batch(B, stream, K, hbm_peak, seed=23, per_layer=False):
                        prefix_len=prefix, kv_row0=None, q=None, k_prefix=None, v_prefix=None, k_tree=None,
                        v_tree=None, uniforms=None, host={})
     call = lambda: st.build_tree(inp, stream=stream)
-    with torch.cuda.stream(stream):
+    with on(stream):
         for _ in range(3):
             call()
     stream.synchronize()
@@ -829,9 +850,10 @@ def time_accept_batch(B, stream, K, hbm_peak, seed=23):
                        root_tok=torch.from_numpy(W.root_tokens(wl, B)).cuda(), prefix_len=prefix, kv_row0=None,
                        q=None, k_prefix=None, v_prefix=None, k_tree=None, v_tree=None,
                        uniforms=torch.rand((B, N), device="cuda", generator=gen), host={})
-    st.build_tree(inp, stream=stream)
+    with on(stream):
+        st.build_tree(inp, stream=stream)
     call = lambda: st.accept(inp, stream=stream)
-    with torch.cuda.stream(stream):
+    with on(stream):
         for _ in range(3):
             call()
     stream.synchronize()
@@ -901,7 +923,7 @@ def time_sweep_step(B, stream, K, hbm_peak, seed=23, n=None):
     cur = torch.cuda.current_stream()
 
     def graph_us(call):
-        with torch.cuda.stream(stream):
+        with on(stream):
             for _ in range(2):
                 call()
         stream.synchronize()
@@ -957,14 +979,14 @@ def time_kv_commit(st, inp, wl, cfg, prefix, stream, K):
     shape = E.CommitShape(B=B, N=cfg.N, Hkv=Hkv, d=d, path_len=wl.depth + 1,
                           dtype=E.ET_BF16 if wl.dtype == "bf16" else E.ET_F32, kv_head_stride=cap,
                           kv_rows=B * Hkv * cap)
-    with torch.cuda.stream(stream):
+    with on(stream):
         st.run(inp, stream=stream)
     stream.synchronize()
 
     def one():
         E.et_kv_commit(shape, inp.k_tree, inp.v_tree, st.accept_len, st.path, kc, vc, kv_row0, inp.prefix_len,
                        new_len, dev_status=st.dev_status, stream=stream)
-    with torch.cuda.stream(stream):
+    with on(stream):
         one()
     stream.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -1004,7 +1026,7 @@ def time_lm_head(wl, cfg, stream, K, hbm_peak):
     x = torch.randn((M, H), device="cuda", generator=g).to(torch.bfloat16)
     out = torch.empty((M, wl.V), device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    with torch.cuda.stream(stream):
+    with on(stream):
         for w in ws:
             E.et_lm_head(x, w, out, dev_status=status, stream=stream)
     stream.synchronize()
@@ -1052,7 +1074,7 @@ def time_static_tree(wl, cfg, inp, stream, K):
 
     def one():
         E.et_static_tree(B, wl.V, k, par_d, rank_d, inp.draft, rmap, tb, stream=stream)
-    with torch.cuda.stream(stream):
+    with on(stream):
         one()
     stream.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -1076,7 +1098,7 @@ def time_static_tree(wl, cfg, inp, stream, K):
 
     def drawn():
         E.et_static_tree_sampled(B, wl.V, 1.0, par_d, inp.draft, rmap, u, tb, ws=ws, stream=stream)
-    with torch.cuda.stream(stream):
+    with on(stream):
         drawn()
     stream.synchronize()
     g2 = torch.cuda.CUDAGraph()
@@ -1131,6 +1153,7 @@ def run_e2e(args, st, sets, wl, stream, host_tables=True):
     d2h = sum(t.numel() * t.element_size() for t in host_out[0])
     K = max(3, min(20, args.steps))
     copy_stream = torch.cuda.Stream()
+    after_current(copy_stream, stream)
     copied = [torch.cuda.Event() for _ in range(2)]
     done = [torch.cuda.Event() for _ in range(2)]
     issued = [False, False]
@@ -1242,7 +1265,7 @@ def run_split_sweep(args):
     for splits in [int(x) for x in args.splits_sweep.split(",")]:
         st = S.VerifyStep(wl, num_splits=splits, attn_impl=E.ATTN_TCGEN05, overlap=False)
         st.prepare(sets[0])
-        with torch.cuda.stream(stream):
+        with on(stream):
             for r in range(R):
                 st.run(sets[r], stream=stream)  # trees and masks of every set
         stream.synchronize()

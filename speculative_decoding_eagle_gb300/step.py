@@ -110,7 +110,11 @@ def overlap_splits(tiles: int, depth: int, auto_splits: int, blocks_per_split: i
 
 
 class VerifyStep:
-    """Buffers and call chain of one verification step for a fixed shape."""
+    """Buffers and call chain of one verification step for a fixed shape.
+
+    The buffers are cleared on the stream that is current when they are made (here, and in ``prepare``).  A step on
+    another stream has to come after that and after the kernels that write its inputs
+    (``stream.wait_stream(torch.cuda.current_stream())``)."""
 
     def __init__(self, wl: W.Workload, B: Optional[int] = None, mode: Optional[int] = None, device="cuda",
                  num_splits: int = 0, max_prefix: Optional[int] = None, attn_impl: int = E.ATTN_AUTO,

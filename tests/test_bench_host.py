@@ -1,5 +1,7 @@
 """Host-side pieces of bench.py (no GPU): the clocks summary that vets a
 timed run, and the algorithmic byte counts the roofline divides by."""
+import ast
+import contextlib
 import os
 import sys
 
@@ -92,3 +94,80 @@ def test_extras_child_result_is_merged(monkeypatch):
     monkeypatch.setattr(bench.subprocess, "run", fake_run)
     ex = bench.run_extras_child(types.SimpleNamespace(steps=10))
     assert ex["tree_attention_shapes"] == [{"us_per_launch": 1.0}] and ex["sweep_step"] == [{"batch": 32}]
+
+
+# ---------------------------------------------------------------------------
+# side streams
+# ---------------------------------------------------------------------------
+def _stream_uses(fn):
+    """(line, stream's name, what) of everything a function sends to a side stream, nested functions and lambdas aside."""
+    ordered, uses = [], []
+
+    def visit(node, held):
+        if isinstance(node, (ast.FunctionDef, ast.Lambda)) and node is not fn:
+            return  # runs where it is called
+        if isinstance(node, ast.With):
+            for item in node.items:
+                call = item.context_expr
+                name = ast.unparse(call.func) if isinstance(call, ast.Call) else ""
+                if name == "on":
+                    ordered.append((node.lineno, ast.unparse(call.args[0])))
+                    held = held | {ast.unparse(call.args[0])}
+                elif name == "torch.cuda.graph":  # synchronises the device on entry
+                    held = held | {ast.unparse(k.value) for k in call.keywords if k.arg == "stream"}
+                elif name == "torch.cuda.stream":
+                    uses.append((node.lineno, ast.unparse(call.args[0]), "enters"))
+                    held = held | {ast.unparse(call.args[0])}
+            for child in node.body:
+                visit(child, held)
+            return
+        if isinstance(node, ast.Call):
+            if ast.unparse(node.func) == "after_current":
+                ordered.extend((node.lineno, ast.unparse(a)) for a in node.args)
+            for k in node.keywords:
+                if k.arg == "stream" and ast.unparse(k.value) not in held and ast.unparse(k.value) != "None":
+                    uses.append((node.lineno, ast.unparse(k.value), "calls on"))
+        for child in ast.iter_child_nodes(node):
+            visit(child, held)
+    visit(fn, frozenset())
+    return ordered, uses
+
+
+def test_side_streams_are_ordered_after_the_inputs():
+    """Inputs are drawn and workspaces cleared on the current stream; a side stream that starts on them without waiting
+    reads them half written (blocks of one cluster then see different values)."""
+    with open(bench.__file__) as f:
+        tree = ast.parse(f.read())
+    seen = 0
+    for fn in [n for n in tree.body if isinstance(n, ast.FunctionDef) and n.name not in ("on", "after_current")]:
+        outer = _stream_uses(fn)[0]
+        for part in [n for n in ast.walk(fn) if isinstance(n, ast.FunctionDef)]:
+            ordered, uses = _stream_uses(part)
+            for line, stream, what in uses:
+                seen += 1
+                # a nested function runs where the outer one calls it
+                assert any(s == stream and at < line for at, s in ordered) or \
+                    (part is not fn and any(s == stream for _, s in outer)), \
+                    f"{fn.name} line {line}: {what} {stream} before it is ordered after the current stream"
+    assert seen >= 4
+
+
+def test_on_waits_before_it_enters(monkeypatch):
+    import torch
+    log = []
+
+    class Side:
+        def wait_stream(self, other):
+            log.append(("wait", other))
+
+    @contextlib.contextmanager
+    def enter(s):
+        log.append(("enter", s))
+        yield
+        log.append(("leave", s))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: "current")
+    monkeypatch.setattr(torch.cuda, "stream", enter)
+    side = Side()
+    with bench.on(side):
+        log.append("work")
+    assert log == [("wait", "current"), ("enter", side), "work", ("leave", side)]
