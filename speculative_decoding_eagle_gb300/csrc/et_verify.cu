@@ -811,7 +811,11 @@ __global__ void __launch_bounds__(kVClThreads) k_verify_cl(VerifyArgs a) {
 // stores it into every CTA of the cluster (by step parity), and after one
 // cluster barrier every CTA merges the slices in CTA order and decides the
 // row the same way (greedy: the first child carrying the argmax token;
-// point-mass: pm_decide on the same inputs), so the CTAs walk in step.  At
+// point-mass: pm_decide).  What a decision needs beside the slices (the row's
+// children, their logits and uniforms) the leader CTA alone reads and stores
+// into every CTA ahead of the same barrier: the CTAs walk in step whatever
+// they would read themselves, also while another stream still writes the
+// inputs, and none stores into a CTA that has left.  At
 // the stop row the leader CTA draws the bonus token (greedy: the argmax;
 // point-mass: the chunk inverse CDF of the residual, the slices' statistics
 // being its chunks).
@@ -833,6 +837,9 @@ struct SeqWalkSmem {
   float wmax[kVClThreads / 32], wsum[kVClThreads / 32];
   unsigned long long gkey[2][kVClMaxCtas];  // every CTA's best key, by step parity
   float2 gms[2][kVClMaxCtas];               // every CTA's (max, sum), by step parity
+  // the leader's view of the row's children, by step parity: row, token (greedy), logit and uniform (point-mass)
+  int skid[2][kMaxN], stok[2][kMaxN], scount[2];
+  float sz[2][kMaxN], su[2][kMaxN];
   int opath[kMaxDepth + 2], otok[kMaxDepth + 2];
   int rej[kMaxN];
   float redz[32];
@@ -904,7 +911,7 @@ __global__ void __launch_bounds__(kVClThreads) k_verify_seq(VerifyArgs a) {
           const int off = (e >> 2) * (kVClThreads * 4) + t * 4 + (e & 3);
           if ((w.rejbits[off >> 5] >> (off & 31)) & 1u) v[e] = -INFINITY;
         }
-        pm_child_inputs(a, fo, w.kid, nkid, zrow, w.ktok, w.zk, w.uk);  // every CTA: the same inputs
+        if (q == 0) pm_child_inputs(a, fo, w.kid, nkid, zrow, w.ktok, w.zk, w.uk);
       }
       float lm = -INFINITY;
 #pragma unroll
@@ -930,15 +937,28 @@ __global__ void __launch_bounds__(kVClThreads) k_verify_seq(VerifyArgs a) {
         cl_st_f32x2(cl_map(&w.gms[par][q], (uint32_t)t), Mq, Sq);
       }
     }
+    if (q == 0 && warp < R) {  // the children, a warp for each block of the cluster
+      if (lane == 0) cl_st_f32(cl_map(&w.scount[par], (uint32_t)warp), __int_as_float(nkid));
+      for (int k = lane; k < nkid; k += 32) {
+        cl_st_f32(cl_map(&w.skid[par][k], (uint32_t)warp), __int_as_float(w.kid[k]));
+        if (greedy) {
+          cl_st_f32(cl_map(&w.stok[par][k], (uint32_t)warp), __int_as_float(w.tok[w.kid[k]]));
+        } else {
+          cl_st_f32(cl_map(&w.sz[par][k], (uint32_t)warp), w.zk[k]);
+          cl_st_f32(cl_map(&w.su[par][k], (uint32_t)warp), w.uk[k]);
+        }
+      }
+    }
     cl_arrive();  // release this block's stores
     cl_wait();    // every block's statistic is in every block
+    const int count = w.scount[par];
     int nxt = -1;
     if (greedy) {
       unsigned long long kk = w.gkey[par][0];
       for (int x = 1; x < R; ++x) kk = w.gkey[par][x] < kk ? w.gkey[par][x] : kk;
       am = (int)zid_id(kk);
-      for (int k = 0; k < nkid && nxt < 0; ++k)
-        if (w.tok[w.kid[k]] == am) nxt = w.kid[k];  // the first child (row order) with the argmax token
+      for (int k = 0; k < count && nxt < 0; ++k)
+        if (w.stok[par][k] == am) nxt = w.skid[par][k];  // the first child (row order) with the argmax token
     } else {
       M = -INFINITY;
       for (int x = 0; x < R; ++x) M = fmaxf(M, w.gms[par][x].x);
@@ -946,7 +966,7 @@ __global__ void __launch_bounds__(kVClThreads) k_verify_seq(VerifyArgs a) {
       for (int x = 0; x < R; ++x)  // the same order in every block: the same M and S
         S += w.gms[par][x].x > -INFINITY ? w.gms[par][x].y * expf((w.gms[par][x].x - M) * invT) : 0.f;
       if (warp == 0) {
-        const int d = nkid > 0 ? pm_decide(nkid, w.kid, w.zk, w.uk, M, S, invT) : -1;
+        const int d = count > 0 ? pm_decide(count, w.skid[par], w.sz[par], w.su[par], M, S, invT) : -1;
         if (lane == 0) w.s_acc = d;
       }
       __syncthreads();
