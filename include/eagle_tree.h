@@ -31,6 +31,9 @@
  * - Calls are asynchronous and stream-ordered on `stream` (a cudaStream_t; 0
  *   is the legacy default stream).  They do no host<->device copies, so they
  *   can be captured in a CUDA graph.
+ * - A call reads its inputs at its place in `stream`: what writes them on
+ *   another stream must be ordered before it, and nothing may write them until
+ *   it has finished.
  * - Shapes and limits are checked on the host before any launch; a bad
  *   argument returns ET_ERR_INVALID_ARG / ET_ERR_UNSUPPORTED and launches
  *   nothing.  A failed launch returns ET_ERR_CUDA (cudaGetLastError is

@@ -598,9 +598,10 @@ __global__ void __launch_bounds__(kVClThreads) k_verify_cl(VerifyArgs a) {
   if (kDraftQ && nkid > 0) {
     const float invT = 1.f / a.T;
     const float *drow = table_row(a.dlog, a.dstride, a.dmap, a.C, b, node, row, bad);
-    // every block loads each child's token logits and uniform: the tests below
-    // are evaluated alike in all blocks of the cluster
-    for (int k = t; k < nkid; k += kVClThreads) {
+    // the leader loads each child's token logits and uniform and stores them
+    // into every block: the tests below come out alike in all of them, also
+    // while another stream still writes the inputs
+    for (int k = t; q == 0 && k < nkid; k += kVClThreads) {
       const long long j = fo + w.kid[k];
       const int x = a.flat_tok[j];
       const bool ok = x >= 0 && x < a.V;
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kVClThreads) k_verify_cl(VerifyArgs a) {
       w.dc[k] = (ok && drow) ? sanitize_logit(__ldg(drow + x), f2) : -INFINITY;
       w.uni[k] = a.uniforms[j];
       w.tokf[k] = ok;
-      if (!ok && q == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
+      if (!ok) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
     }
     float d[4 * kVClVec];
     cl_load_span(drow, base, a.vec4d, a.V, d, flag);
@@ -628,6 +629,13 @@ __global__ void __launch_bounds__(kVClThreads) k_verify_cl(VerifyArgs a) {
     if (bad && q == 0 && t == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
     __syncthreads();
     cl_wait();  // phase 0 done: every block of the cluster runs
+    if (q == 0 && warp > 0 && warp < R)  // (the leader has its own)
+      for (int k = lane; k < nkid; k += 32) {
+        cl_st_f32(cl_map(&w.zc[k], (uint32_t)warp), w.zc[k]);
+        cl_st_f32(cl_map(&w.dc[k], (uint32_t)warp), w.dc[k]);
+        cl_st_f32(cl_map(&w.uni[k], (uint32_t)warp), w.uni[k]);
+        cl_st_f32(cl_map(&w.tokf[k], (uint32_t)warp), __int_as_float(w.tokf[k]));
+      }
     float Mc = -INFINITY, Mqc = -INFINITY;
 #pragma unroll
     for (int x = 0; x < NW; ++x) { Mc = fmaxf(Mc, wmax[x]); Mqc = fmaxf(Mqc, wmaxq[x]); }

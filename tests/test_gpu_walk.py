@@ -59,3 +59,28 @@ def test_uniforms_written_while_the_walk_reads_them(B):
         torch.cuda.synchronize()
         check_walks(cfg, tb, out, parent)
         assert (out["accept_len"] == deepest).all() and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("B", [1, 4])
+def test_uniforms_written_while_draftq_rows_are_decided(B):
+    """Rows of a draft-q tree are decided by a cluster each; its blocks test the children one after the other."""
+    cfg, tb, draft, out, ws, parent = accepting(B, 32000, (4, 2, 2, 1, 1))
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    target = draft + torch.randn(draft.shape, generator=gen, device="cuda")
+    uniforms = torch.zeros(B, cfg.n + 1, device="cuda")
+    call = lambda stream=None: E.et_verify_accept(  # noqa: E731
+        cfg, E.ET_ACCEPT_STOCH_DRAFTQ, tb, target, out["accept_len"], out["path"], out["tokens"], ws, draft_logits=draft,
+        uniforms=uniforms, stream=stream)
+    torch.cuda.synchronize()
+    writer, reader = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(150):
+        with torch.cuda.stream(writer):
+            for u in (0.0, 0.9999999, 0.0, 0.9999999):
+                uniforms.fill_(u)
+        call(reader)
+    torch.cuda.synchronize()
+    check_walks(cfg, tb, out, parent)
+    uniforms.fill_(0.5)
+    call()
+    torch.cuda.synchronize()
+    check_walks(cfg, tb, out, parent)
