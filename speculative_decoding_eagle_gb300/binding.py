@@ -685,13 +685,13 @@ class PagedAttnShape:
     Hq: int
     max_blocks: int
     dtype: int = ET_BF16
-    scale: float = 0.0  # 0: 1 / sqrt(d) of the cache
-    max_prefix: int = 0
+    scale: float = 0.0                # 0: 1 / sqrt(d) of the cache
+    max_prefix: Optional[int] = None  # longest prefix of the batch; None: whatever the table's pages hold
     num_splits: int = 0
 
     def c(self) -> PagedAttnShapeC:
-        return PagedAttnShapeC(self.B, self.N, self.Hq, self.max_blocks, self.dtype, self.scale, self.max_prefix,
-                               self.num_splits)
+        bound = 0x7fffffff if self.max_prefix is None else self.max_prefix  # the library cuts it at the table's size
+        return PagedAttnShapeC(self.B, self.N, self.Hq, self.max_blocks, self.dtype, self.scale, bound, self.num_splits)
 
     def for_cache(self, cache: PagedCache):
         """The C struct with the default scale filled in, and the tensors' shapes."""

@@ -225,3 +225,20 @@ def test_every_misfit_is_named_before_a_call(monkeypatch):
             for wrong in (t[..., :-1] if name != "ws" else t[::2], t.double()):  # another shape or stride, another type
                 with pytest.raises(ValueError, match=name):
                     fn(sh, Host, **dict(args, **{name: wrong}))
+
+
+def _cache_of(page_size=64, Hkv=8, d=128, num_pages=100):
+    class Host:  # the geometry that a shape and the library look at
+        device = -1
+    c = Host()
+    c.Hkv, c.d, c.page_size = Hkv, d, page_size
+    c._ref = ctypes.byref(cache(Hkv=Hkv, d=d, page_size=page_size, num_pages=num_pages, page_stride=Hkv * page_size * d))
+    return c
+
+
+def test_a_shape_without_a_prefix_bound_takes_all_that_its_table_holds(lib):
+    c = _cache_of()
+    splits = lambda **kw: lib.et_tree_attention_paged_splits(  # noqa: E731
+        E.PagedAttnShape(B=1, N=61, Hq=64, max_blocks=256, **kw).for_cache(c)[0], c._ref)
+    assert E.PagedAttnShape(B=1, N=61, Hq=64, max_blocks=256).for_cache(c)[0]._obj.max_prefix >= 256 * 64
+    assert splits() == splits(max_prefix=256 * 64) > splits(max_prefix=0) == 1
