@@ -697,7 +697,7 @@ class PagedAttnShape:
         """The C struct with the default scale filled in, and the tensors' shapes."""
         def make():
             c = self.c()
-            if not c.scale > 0:
+            if self.scale == 0:
                 c.scale = cache.d ** -0.5
             B, N, Hq = self.B, self.N, self.Hq
             return (ctypes.byref(c), _TORCH_DTYPE[self.dtype], (B,), (B, self.max_blocks), (B, N, Hq, cache.d),

@@ -242,3 +242,12 @@ def test_a_shape_without_a_prefix_bound_takes_all_that_its_table_holds(lib):
         E.PagedAttnShape(B=1, N=61, Hq=64, max_blocks=256, **kw).for_cache(c)[0], c._ref)
     assert E.PagedAttnShape(B=1, N=61, Hq=64, max_blocks=256).for_cache(c)[0]._obj.max_prefix >= 256 * 64
     assert splits() == splits(max_prefix=256 * 64) > splits(max_prefix=0) == 1
+
+
+@pytest.mark.parametrize("scale", [-0.5, math.nan, -math.inf])
+def test_a_scale_that_is_no_scale_is_refused_not_replaced(lib, scale):
+    c = _cache_of()
+    shape = E.PagedAttnShape(B=1, N=61, Hq=64, max_blocks=256, scale=scale)
+    assert lib.et_tree_attention_paged_splits(shape.for_cache(c)[0], c._ref) == -1
+    assert lib.et_tree_attention_paged(shape.for_cache(c)[0], c._ref, *[FAKE] * 7, None, None, FAKE, 1 << 40, None) == 1
+    assert E.PagedAttnShape(B=1, N=61, Hq=64, max_blocks=256).for_cache(c)[0]._obj.scale == np.float32(128 ** -0.5)
