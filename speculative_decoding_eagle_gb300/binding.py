@@ -555,6 +555,13 @@ def _call(fn: str, device: int, stream: Optional[torch.cuda.Stream], *args) -> N
         raise EtError(fn, st)
 
 
+class _Kept:
+    """A frozen shape that keeps what follows from it (C structs, which cannot be copied) out of its copies."""
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_made"}
+
+
 def _kept(shape, key, make):
     """What follows from a frozen shape (and a cache's geometry), made once: its C struct and its tensors' shapes."""
     made = shape.__dict__.get("_made")
@@ -594,6 +601,9 @@ class PagedCache:
                               k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
         self._ref = ctypes.byref(self._c)
 
+    def __reduce__(self):  # copies and pickles are handles of the tensors' copies
+        return PagedCache, (self.k_pages, self.v_pages, self.k_scale, self.v_scale)
+
     @staticmethod
     def allocate(num_pages: int, Hkv: int, page_size: int, d: int, dtype=torch.float8_e4m3fn,
                  device="cuda") -> "PagedCache":
@@ -604,7 +614,7 @@ class PagedCache:
 
 
 @dataclasses.dataclass(frozen=True)
-class BlockMapShape:
+class BlockMapShape(_Kept):
     B: int
     page_size: int
     max_blocks: int
@@ -638,7 +648,7 @@ def et_block_map(shape: BlockMapShape, prefix_len: torch.Tensor, new_len: torch.
 
 
 @dataclasses.dataclass(frozen=True)
-class PagedCommitShape:
+class PagedCommitShape(_Kept):
     B: int
     N: int
     path_len: int
@@ -679,7 +689,7 @@ def et_kv_commit_paged(shape: PagedCommitShape, cache: PagedCache, block_table: 
 
 
 @dataclasses.dataclass(frozen=True)
-class PagedAttnShape:
+class PagedAttnShape(_Kept):
     B: int
     N: int
     Hq: int

@@ -1,7 +1,9 @@
 """The paged 8-bit KV cache without a GPU: the oracle against closed forms and
 hand-worked examples, and every argument that the calls refuse."""
+import copy
 import ctypes
 import math
+import pickle
 
 import numpy as np
 import pytest
@@ -251,3 +253,27 @@ def test_a_scale_that_is_no_scale_is_refused_not_replaced(lib, scale):
     assert lib.et_tree_attention_paged_splits(shape.for_cache(c)[0], c._ref) == -1
     assert lib.et_tree_attention_paged(shape.for_cache(c)[0], c._ref, *[FAKE] * 7, None, None, FAKE, 1 << 40, None) == 1
     assert E.PagedAttnShape(B=1, N=61, Hq=64, max_blocks=256).for_cache(c)[0]._obj.scale == np.float32(128 ** -0.5)
+
+
+@pytest.mark.parametrize("shape,use", [
+    (E.PagedAttnShape(B=1, N=61, Hq=64, max_blocks=256), lambda s, c: s.for_cache(c)),
+    (E.PagedCommitShape(B=3, N=5, path_len=2, max_blocks=4), lambda s, c: E.et_kv_commit_paged(s, c, *[_i32(1)] * 8)),
+    (E.BlockMapShape(B=2, page_size=16, max_blocks=3, num_pages=5), lambda s, c: E.et_block_map(s, *[_i32(1)] * 6)),
+], ids=lambda v: type(v).__name__)
+def test_a_shape_that_was_used_can_be_copied_and_pickled(shape, use):
+    c = _cache_of()
+    try:
+        use(shape, c)
+    except ValueError:  # host tensors that do not fit; the shape has been looked at
+        pass
+    assert "_made" in shape.__dict__
+    for again in (copy.copy(shape), copy.deepcopy(shape), pickle.loads(pickle.dumps(shape))):
+        assert again == shape and hash(again) == hash(shape) and "_made" not in again.__dict__
+        try:
+            use(again, c)
+        except ValueError:
+            pass
+
+
+def _i32(*s):
+    return torch.zeros(*s, dtype=torch.int32)
