@@ -1131,7 +1131,9 @@ extern "C" et_status et_tree_attention_paged(const et_paged_attn_shape *shape, c
   ma.part_o = plan.ws > 0 ? reinterpret_cast<float4 *>(wsb + plan.o_off) : nullptr;
   const uint32_t units = (uint32_t)cache->page_size / 16;
   ma.page_magic = units == 1 ? 0u : (uint32_t)(((1ull << 32) + units - 1) / units);
-  ma.group_magic = a.G == 1 ? 0u : (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
+  ma.group_shift = 0;
+  while ((2ll << ma.group_shift) < a.G) ++ma.group_shift;
+  ma.group_magic = a.G == 1 ? 0u : (uint32_t)(((1ull << (32 + ma.group_shift)) + a.G - 1) / a.G);
   ma.wait_cycles = et_wait_limit_cycles();
   if (plan.tc) return paged_tc_launch(cache, ma, st);
   CUtensorMap mk, mv;

@@ -34,7 +34,7 @@ struct PagedSplitArgs {
   unsigned int *cnt;    // [B * tiles_y] arrival counters; null when the chunks need none (one, or a cluster)
   float2 *part_ml;      // [B * tiles_y][S][R] (maximum, sum)
   float4 *part_o;       // [B * tiles_y][S][R][D] fp32
-  uint32_t page_magic, group_magic;  // page_index, row_token
+  uint32_t page_magic, group_magic, group_shift;  // page_index, row_token
   long long wait_cycles;
 };
 
@@ -60,9 +60,10 @@ __device__ __forceinline__ int page_index(const PagedSplitArgs &a, int token) {
   const uint32_t u = (uint32_t)token >> 4;
   return (int)(a.page_magic ? __umulhi(u, a.page_magic) : u);
 }
-// row of a KV head's (token, head in group) rows -> token: umulhi by ceil(2^32 / G) is exact below 2^32 / G rows
+// row of a KV head's (token, head in group) rows -> token: with 2^k < G <= 2^(k + 1), umulhi by ceil(2^(32 + k) / G) and a
+// shift by k are exact below 2^31 rows
 __device__ __forceinline__ int row_token(const PagedSplitArgs &a, int row) {
-  return (int)(a.group_magic ? __umulhi((uint32_t)row, a.group_magic) : (uint32_t)row);
+  return (int)(a.group_magic ? __umulhi((uint32_t)row, a.group_magic) >> a.group_shift : (uint32_t)row);
 }
 // prefix length of sequence b as the kernels use it: -1 = no sequence here
 __device__ __forceinline__ int paged_prefix(const PagedAttnArgs &a, int b, int &bad) {

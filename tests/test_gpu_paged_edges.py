@@ -23,3 +23,38 @@ def test_a_copied_cache_is_a_handle_of_its_own_tensors():
         t.view(torch.uint8).fill_(0x7F)
     r = run_attention(pool, 2, 5, 4, "bf16", rng, keep)
     check_all(pool, r, keep, "bf16")
+
+
+@pytest.mark.parametrize("Hkv,G,d", [(1, 8191, 128), (2, 8191, 64), (2, 16383, 128)])
+def test_thousands_of_query_heads_per_kv_head(Hkv, G, d):
+    """128 * G rows of a KV head pass 2^32 / G: the row's token is a division that has to stay exact there.
+
+    No prefix and no mask: row i attends tree rows 0..i.  Weights and out round to bf16 (2^-8 each); scores are fp32 sums
+    of d products, (d + 8) 2^-24 sum |q||k| scale < 2^-12 for these values, and weigh twice that."""
+    N, Hq = 128, Hkv * G
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, kt, vt = rnd(1, N, Hq, d), rnd(1, N, Hkv, d), rnd(1, N, Hkv, d)
+    cache = E.PagedCache.allocate(1, Hkv, 16, d)
+    shape = E.PagedAttnShape(B=1, N=N, Hq=Hq, max_blocks=1, max_prefix=0)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    # a margin around what the call may write, which has to stay as it is
+    room = torch.full((3, N, Hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lroom = torch.full((3, Hq, N), 7.0, device="cuda")
+    E.et_tree_attention_paged(shape, cache, i32(0)[None], i32(0), q, kt, vt, None, room[1:2], lse=lroom[1:2],
+                              ws=E.new_workspace(E.et_tree_attention_paged_workspace_size(shape, cache)))
+    assert all(bool((x[i] == 7).all()) for x in (room, lroom) for i in (0, 2))
+    sees = torch.ones(N, N, dtype=torch.bool, device="cuda").tril()
+    for g in range(Hkv):
+        k, v = kt[0, :, g].float(), vt[0, :, g].float()
+        for h0 in range(g * G, (g + 1) * G, 2048):
+            hs = slice(h0, min(h0 + 2048, (g + 1) * G))
+            z = torch.einsum("nhd,td->hnt", q[0, :, hs].float(), k) * d ** -0.5
+            z = z.masked_fill(~sees, -math.inf)
+            total = torch.logsumexp(z, -1)
+            p = torch.exp(z - total[..., None])
+            want, size = p @ v, p @ v.abs()
+            got = room[1, :, hs].float().transpose(0, 1)
+            err = (got - want).abs() - (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -11) * size)
+            assert float(err.max()) <= 0
+            assert float((lroom[1, hs] - total).abs().max()) <= 2.0 ** -11
