@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kRowThreads) k_paged_attn_row(PagedAttnArgs a)
   float m = -INFINITY, l = 0.f, acc[PL];
 #pragma unroll
   for (int c = 0; c < PL; ++c) acc[c] = 0.f;
-  const int nP = (L + 31) / 32, nT = (a.N + 31) / 32;
+  const int nP = tiles_of(L, 32), nT = (a.N + 31) / 32;
   for (int grp = warp; grp < nP + nT; grp += kRowWarps) {
     const bool cached = grp < nP;
     const int j = cached ? grp * 32 + lane : (grp - nP) * 32 + lane;
@@ -344,7 +344,7 @@ __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const
 struct Share { int b, chunk, chunks, per; };  // b < 0: nothing for block c
 __device__ __forceinline__ Share share_batch(const PagedAttnArgs &a, int lane, int blocks, int c) {
   int ignore = 0;
-  const int L = lane < a.B ? paged_prefix(a, lane, ignore) : -1, T = L < 0 ? 0 : (L + kPaTile - 1) / kPaTile;
+  const int L = lane < a.B ? paged_prefix(a, lane, ignore) : -1, T = L < 0 ? 0 : tiles_of(L, kPaTile);
   const int present = __popc(__ballot_sync(0xffffffffu, L >= 0));
   const int longest = __reduce_max_sync(0xffffffffu, T);
   const float total = (float)__reduce_add_sync(0xffffffffu, (unsigned)T);  // < 2^31: 32 sequences of 2^26 tiles at most
@@ -444,12 +444,12 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
       longest = max(max(s_red[0], s_red[1]), max(s_red[2], s_red[3]));
     }
     if (L < 0) return;
-    per = max(((longest + kPaTile - 1) / kPaTile + ma.S - 1) / ma.S, 1);
-    chunks = max(1, ((L + kPaTile - 1) / kPaTile + per - 1) / per);
+    per = max((tiles_of(longest, kPaTile) + ma.S - 1) / ma.S, 1);
+    chunks = max(1, (tiles_of(L, kPaTile) + per - 1) / per);
     if (chunk >= chunks) return;
   }
   __syncthreads();  // the barriers are initialised
-  const int T = (L + kPaTile - 1) / kPaTile;
+  const int T = tiles_of(L, kPaTile);
   const int t0 = chunk * per, t1 = min(T, t0 + per);
   const int first = t0 + kg;  // this group's i-th tile: first + KG * i
   const int n = t1 > first ? (t1 - first + KG - 1) / KG : 0;

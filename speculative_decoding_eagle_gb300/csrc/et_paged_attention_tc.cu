@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     for (int w = 1; w < kPtThreads / 32; ++w) longest = max(longest, s_red[w]);
   }
   if (L < 0) return;
-  const int T = (L + kPtKeys - 1) / kPtKeys, Tl = (longest + kPtKeys - 1) / kPtKeys;
+  const int T = tiles_of(L, kPtKeys), Tl = tiles_of(longest, kPtKeys);
   const int per = max((Tl + ma.S - 1) / ma.S, 1);
   const int chunks = max(1, (T + per - 1) / per);
   if (chunk >= chunks) return;

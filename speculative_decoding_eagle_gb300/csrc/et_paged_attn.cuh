@@ -75,6 +75,8 @@ __device__ __forceinline__ int paged_prefix(const PagedAttnArgs &a, int b, int &
   }
   return L < 0 ? -1 : L;
 }
+// tiles that n tokens take, n < 2^31
+__device__ __forceinline__ int tiles_of(int n, uint32_t tile) { return (int)(((uint32_t)n + tile - 1u) / tile); }
 __device__ __forceinline__ float clamp_v_scale(float s) {
   return fminf(fmaxf(s, 1.f / (1ll << kScaleExp)), (float)(1ll << kScaleExp));  // NaN -> the smallest
 }

@@ -58,3 +58,32 @@ def test_thousands_of_query_heads_per_kv_head(Hkv, G, d):
             err = (got - want).abs() - (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -11) * size)
             assert float(err.max()) <= 0
             assert float((lroom[1, hs] - total).abs().max()) <= 2.0 ** -11
+
+
+@pytest.mark.parametrize("N", [1, 17])
+def test_the_longest_prefix_a_table_can_hold(N):
+    """2^31 - 16 tokens, all of them in one page of 16: its softmax, and a log-sum-exp larger by ln(2^27 - 1).
+
+    A thread's or an accumulator's sum takes up to 2^20 terms of one sign, each rounded (or cut) by 2^-23 at most: 2^-3 of
+    the numerator and of the sum at the very worst.  Without the tokens the result is the tree's rows alone."""
+    rng = np.random.default_rng(2)
+    L = (1 << 31) - 16
+    pool = Pool(rng, [16], 16, 1, 128, "e4m3")
+    cols = L // 16
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.full((1, cols), int(pool.table[0, 0]), **i32)
+    shape = E.PagedAttnShape(B=1, N=N, Hq=1, max_blocks=cols)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, kt, vt = (torch.randn(1, N, 1, 128, generator=gen, device="cuda").bfloat16() for _ in range(3))
+    out, lse = torch.zeros_like(q), torch.zeros(1, 1, N, device="cuda")
+    status = torch.zeros(1, **i32)
+    E.et_tree_attention_paged(shape, pool.cache, table, torch.tensor([L], **i32), q, kt, vt, None, out, lse=lse,
+                              ws=E.new_workspace(E.et_tree_attention_paged_workspace_size(shape, pool.cache)),
+                              dev_status=status)
+    assert int(status.item()) == 0
+    k, v = pool.sequence(0)
+    want, wlse, size, *_ = O.paged_attention(q[0].double().cpu().numpy(), k, v, kt[0].double().cpu().numpy(),
+                                             vt[0].double().cpu().numpy(), np.ones(16, bool), np.zeros((N, N), bool),
+                                             128 ** -0.5)
+    assert (np.abs(out[0].double().cpu().numpy() - want) <= 2.0 ** -2 * size).all()
+    assert (np.abs(lse[0].double().cpu().numpy() - wlse - math.log(cols)) <= 2.0 ** -2).all()
