@@ -147,48 +147,50 @@ __global__ void __launch_bounds__(kMapThreads) k_block_map(MapArgs a) {
   cl_sync();  // every block has read the lengths, block counts and the free count
   if (bad && rank == 0) flag_status(a.dev_status, bad);
   // ---- pages ----
-  const int step = blocks * kMapThreads, first = rank * kMapThreads + t;
+  // (unsigned: R, A and the slots of a request lie below 2^31, one round past them does not)
+  const uint32_t step = (uint32_t)blocks * kMapThreads, first = (uint32_t)(rank * kMapThreads + t);
   auto give = [&](int turn, int page) {  // the turn-th taken page
     const int b = find_request(cum_take, a.B, turn);
     a.block_table[(long long)b * a.max_blocks + s_have[b] + (turn - cum_take[b])] = page;
   };
-  for (int r0 = first; r0 < R; r0 += kMapBatch * step) {  // loads of a batch first: each is a trip to L2
+  for (uint32_t r0 = first; r0 < (uint32_t)R; r0 += kMapBatch * step) {  // loads of a batch first: each is a trip to L2
     int32_t *cell[kMapBatch];
     int page[kMapBatch];
 #pragma unroll
     for (int k = 0; k < kMapBatch; ++k) {
-      const int r = r0 + k * step;
-      if (r >= R) continue;
-      const int b = find_request(cum_back, a.B, r);
-      cell[k] = a.block_table + (long long)b * a.max_blocks + s_need[b] + (r - cum_back[b]);
+      const uint32_t r = r0 + k * step;
+      if (r >= (uint32_t)R) continue;
+      const int b = find_request(cum_back, a.B, (int)r);
+      cell[k] = a.block_table + (long long)b * a.max_blocks + s_need[b] + ((int)r - cum_back[b]);
       page[k] = *cell[k];
     }
 #pragma unroll
     for (int k = 0; k < kMapBatch; ++k) {
-      const int place = F + r0 + k * step;
-      if (r0 + k * step >= R) continue;
+      if (r0 + k * step >= (uint32_t)R) continue;
+      const int place = F + (int)(r0 + k * step);
       if ((unsigned)page[k] >= (unsigned)a.num_pages) bad = ET_DEV_BAD_INDEX;
       if (place >= left) give(top - 1 - place, page[k]);
       else if (place < a.num_pages) a.free_list[place] = page[k];
       *cell[k] = -1;
     }
   }
-  for (int k0 = first; k0 < A; k0 += kMapBatch * step) {
+  for (uint32_t k0 = first; k0 < (uint32_t)A; k0 += kMapBatch * step) {
     int page[kMapBatch];
 #pragma unroll
     for (int k = 0; k < kMapBatch; ++k) {
-      const int turn = k0 + k * step, place = top - 1 - turn;
-      page[k] = turn < A && place < F ? a.free_list[place] : 0;  // (a returned page: its own thread moves it)
+      const uint32_t turn = k0 + k * step;
+      const int place = top - 1 - (int)turn;
+      page[k] = turn < (uint32_t)A && place < F ? a.free_list[place] : 0;  // (a returned page: its own thread moves it)
     }
 #pragma unroll
     for (int k = 0; k < kMapBatch; ++k) {
-      const int turn = k0 + k * step;
-      if (turn >= A || top - 1 - turn >= F) continue;
+      const uint32_t turn = k0 + k * step;
+      if (turn >= (uint32_t)A || top - 1 - (int)turn >= F) continue;
       if ((unsigned)page[k] >= (unsigned)a.num_pages) bad = ET_DEV_BAD_INDEX;
-      give(turn, page[k]);
+      give((int)turn, page[k]);
     }
   }
-  for (int b = first; b < a.B; b += step)
+  for (int b = (int)first; b < a.B; b += (int)step)
     if (s_have[b] >= 0) a.n_blocks[b] = s_need[b];
   if (first == 0) {
     a.free_count[0] = min(left, a.num_pages);
@@ -203,10 +205,10 @@ __global__ void __launch_bounds__(kMapThreads) k_block_map(MapArgs a) {
     const int count = s_new[b], len = s_len[b];
     const int32_t *row = a.block_table + (long long)b * a.max_blocks;
 #pragma unroll 4
-    for (int i = lane; i < a.max_new; i += 32) {
+    for (uint32_t i = lane; i < (uint32_t)a.max_new; i += 32) {
       long long slot = -1;
-      if (i < count) {
-        const int pos = len + i, blk = pos / a.P;  // need pages cover it: no overflow past max_blocks * P
+      if (i < (uint32_t)count) {
+        const int pos = len + (int)i, blk = pos / a.P;  // need pages cover it: no overflow past max_blocks * P
         const int page = __ldcg(row + blk);
         if ((unsigned)page < (unsigned)a.num_pages) slot = (long long)page * a.P + (pos - blk * a.P);
         else flag_status(a.dev_status, ET_DEV_BAD_INDEX);

@@ -87,3 +87,21 @@ def test_the_longest_prefix_a_table_can_hold(N):
                                              128 ** -0.5)
     assert (np.abs(out[0].double().cpu().numpy() - want) <= 2.0 ** -2 * size).all()
     assert (np.abs(lse[0].double().cpu().numpy() - wlse - math.log(cols)) <= 2.0 ** -2).all()
+
+
+def test_a_block_map_that_returns_almost_two_to_the_31_pages():
+    """Rounds of the page loops pass 2^31 there.  The pool holds eight pages, so that the stack is cut and flagged."""
+    cols, pool = (1 << 30) - 8, 8
+    i32 = dict(dtype=torch.int32, device="cuda")
+    room = torch.full((2 * cols + 2048,), 5, **i32)  # with a margin on both sides
+    table = room[1024:-1024].view(2, cols)
+    table[0, 0], table[0, 1] = 7, 6
+    n, free, count = torch.full((2,), cols, **i32), torch.full((pool,), -9, **i32), torch.zeros(1, **i32)
+    status = torch.zeros(1, **i32)
+    shape = E.BlockMapShape(B=2, page_size=1, max_blocks=cols, num_pages=pool)
+    zero = torch.zeros(2, **i32)
+    E.et_block_map(shape, zero, zero, n, table, free, count, dev_status=status)
+    assert int(status.item()) == E.ET_DEV_BAD_INDEX and n.tolist() == [0, 0] and count.tolist() == [pool]
+    assert free.tolist() == [7, 6] + [5] * 6  # the first eight returned
+    assert bool((room[:1024] == 5).all()) and bool((room[-1024:] == 5).all())
+    assert int(table.min()) == int(table.max()) == -1
