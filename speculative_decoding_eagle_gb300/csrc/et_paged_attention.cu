@@ -103,13 +103,13 @@ __global__ void __launch_bounds__(kRowThreads) k_paged_attn_row(PagedAttnArgs a)
     s = ok ? s * a.scale_log2 : -INFINITY;
     const unsigned int keep = __ballot_sync(0xffffffffu, ok);
     if (keep == 0u) continue;  // no key for this row in this group
-    float mn = fmaxf(m, warp_max(s));
-    if (mn == -INFINITY) mn = 0.f;  // only NaN or -inf scores so far: the weights below become NaN or 0
-    const float corr = exp2f(m - mn), p = ok ? exp2f(s - mn) : 0.f;
+    const float was = m;
+    m = fmaxf(m, warp_max(s));
+    const float ref = m == -INFINITY ? 0.f : m;  // only NaN or -inf scores so far: the weights below become NaN or 0
+    const float corr = exp2f(was - ref), p = ok ? exp2f(s - ref) : 0.f;
     l = l * corr + warp_sum(p);
 #pragma unroll
     for (int c = 0; c < PL; ++c) acc[c] *= corr;
-    m = mn;
     const float pv = p * vs;
 #pragma unroll 1
     for (int k0 = 0; k0 < 32; k0 += 16) {

@@ -105,3 +105,27 @@ def test_a_block_map_that_returns_almost_two_to_the_31_pages():
     assert free.tolist() == [7, 6] + [5] * 6  # the first eight returned
     assert bool((room[:1024] == 5).all()) and bool((room[-1024:] == 5).all())
     assert int(table.min()) == int(table.max()) == -1
+
+
+def test_fp32_keys_that_score_minus_infinity_leave_the_others_their_weight():
+    """A warp whose first keys all score -inf (an infinite K) and whose later ones lie far below 0."""
+    d, L, P = 64, 288, 32
+    codes = torch.zeros(L // P, 1, P, d, dtype=torch.uint8, device="cuda")
+    codes[..., 0] = 0xE0                     # e5m2: -512
+    codes[0, ..., 0] = 0xFC                  # -infinity
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    v = torch.randn(L // P, 1, P, d, generator=gen, device="cuda").to(torch.float8_e5m2)
+    ones = torch.ones(L // P, 1, device="cuda")
+    cache = E.PagedCache(codes.view(torch.float8_e5m2), v, ones, ones)
+    q, kt, vt = (torch.zeros(1, 1, 1, d, device="cuda") for _ in range(3))
+    q[..., 0], kt[..., 0] = 1.0, -512.0
+    out, lse = torch.zeros_like(q), torch.zeros(1, 1, 1, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    shape = E.PagedAttnShape(B=1, N=1, Hq=1, max_blocks=L // P, dtype=E.ET_F32, scale=1.0)
+    E.et_tree_attention_paged(shape, cache, i32(*range(L // P))[None], i32(L), q, kt, vt, None, out, lse=lse)
+    want = v.double().view(L, d)[P:].sum(0) / (L - P + 1)  # 256 tokens and the row itself, all alike
+    # equal weights: sums of 257 terms in fp32, 2^-24 a term
+    assert (out.view(d).double() - want).abs().max() <= 257 * 2.0 ** -24 * v.double().abs().max()
+    assert abs(float(lse) - (-512 + math.log(L - P + 1))) <= 2.0 ** -13
+    # half steps of 738 (base 2: score, sum; 2^-15 each, times ln 2), of 506 (2^-16) and of the two constants (2^-25 of
+    # 738 times ln 2, of 506): 1.4 * 2^-15 + 2^-16 + 1.02 * 2^-15 * 0.7 + 2^-16 < 2^-13
