@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
         }
       float fs[2 * MT];
 #pragma unroll
-      for (int r = 0; r < 2 * MT; ++r) fs[r] = a.scale_log2;
+      for (int r = 0; r < 2 * MT; ++r) fs[r] = rf[r] == rf[r] ? a.scale_log2 : rf[r];  // NaN: q is not finite
       const int ve = page_exponent<FMT>(__uint_as_float(s_vtop));
       const float one[1] = {1.f}, lvt[1] = {(float)ve}, ivt[1] = {power_of_two(-ve)};
       uint32_t p[MT][2][2];

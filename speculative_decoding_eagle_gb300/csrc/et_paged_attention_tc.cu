@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const float f = odd ? __uint_as_float(0x7fc00000u)
                             : a.scale_log2 * __uint_as_float((uint32_t)(127 - ea) << 23) * __uint_as_float((uint32_t)(127 - eb) << 23);
         fc[2 * kPtRows + px(r)] = f;
-        fc[px(r)] = tree ? a.scale_log2 : f;  // group 0 takes the tree's tile first: q as it is
+        fc[px(r)] = tree && !odd ? a.scale_log2 : f;  // group 0 takes the tree's tile first: q as it is
         fc[py(r)] = fc[2 * kPtRows + py(r)] = 0.f;
       }
     }

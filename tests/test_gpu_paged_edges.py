@@ -129,3 +129,30 @@ def test_fp32_keys_that_score_minus_infinity_leave_the_others_their_weight():
     assert abs(float(lse) - (-512 + math.log(L - P + 1))) <= 2.0 ** -13
     # half steps of 738 (base 2: score, sum; 2^-15 each, times ln 2), of 506 (2^-16) and of the two constants (2^-25 of
     # 738 times ln 2, of 506): 1.4 * 2^-15 + 2^-16 + 1.02 * 2^-15 * 0.7 + 2^-16 < 2^-13
+
+
+@pytest.mark.parametrize("L", [0, 40])
+@pytest.mark.parametrize("N,d", [(1, 128), (20, 64), (20, 128)])
+def test_a_query_with_an_infinity_gives_nan_and_nothing_else_does(N, d, L):
+    """Also where every score of the row is -inf: the tree's keys oppose it and there is no prefix."""
+    rng = np.random.default_rng(4)
+    pool = Pool(rng, [L], 16, 2, d, "e4m3", cols=3)
+    keep = random_tree(rng, 1, N)
+    keep[0, N - 1] = N == 1  # the last of several rows attends no key of the tree
+    q = torch.randn(1, N, 2, d, generator=torch.Generator().manual_seed(1)).bfloat16().float().numpy()
+    clean = run_attention(pool, 1, N, 2, "bf16", np.random.default_rng(8), keep, q=q)
+    hit = sorted({0, N // 2, N - 1})
+    r = dict(clean, out=torch.full_like(clean["out"], 7.0), lse=torch.full_like(clean["lse"], 7.0))
+    args = list(clean["args"])
+    args[4], args[5], args[8] = args[4].clone(), args[5].clone(), r["out"]
+    for i in hit:
+        args[4][0, i, 1, 3] = math.inf
+    args[5][..., 3] = -args[5][..., 3].abs() - 1  # scores of -inf
+    E.et_tree_attention_paged(*args, lse=r["lse"], ws=clean["ws"], dev_status=clean["status"])
+    for i in range(N):
+        has_key = L > 0 or keep[0, i].any()
+        for x in (r["out"][0, i, 1], r["lse"][0, 1, i]):
+            assert bool(torch.isnan(x).all()) == (i in hit and has_key)
+        assert not torch.isnan(r["out"][0, i, 0]).any()
+        if not has_key:
+            assert (r["out"][0, i] == 0).all() and torch.isneginf(r["lse"][0, :, i]).all()
