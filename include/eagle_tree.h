@@ -736,7 +736,10 @@ et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_
  *               this function with other shapes may use it before and after,
  *               other functions may not.
  * v_scale counts as at least 2^-48 and at most 2^48 (what et_kv_commit_paged
- * writes); k_scale may be any finite value.  Rows of a page past the prefix
+ * writes); k_scale may be any value up to 2^100 in magnitude, as long as
+ * scale * |q| * |k_scale| stays below 2^100 (the scores of larger ones leave
+ * fp32's range on the way); an infinite code (e5m2) in a K row that is attended
+ * may make its rows NaN.  Rows of a page past the prefix
  * are not used, whatever they hold.  A prefix past max_prefix or past
  * max_blocks pages is cut there, a page id outside the cache drops its
  * tokens; both set ET_DEV_BAD_INDEX.

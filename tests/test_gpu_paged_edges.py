@@ -156,3 +156,18 @@ def test_a_query_with_an_infinity_gives_nan_and_nothing_else_does(N, d, L):
         assert not torch.isnan(r["out"][0, i, 0]).any()
         if not has_key:
             assert (r["out"][0, i] == 0).all() and torch.isneginf(r["lse"][0, :, i]).all()
+
+
+@pytest.mark.parametrize("N,d", [(1, 128), (30, 64), (30, 128)])
+@pytest.mark.parametrize("exp", [-104, 100])
+def test_k_scales_and_queries_at_the_ends_of_their_range(N, d, exp):
+    """K scales up to 2^99 on queries of 2^-104, and the other way round: plain scores."""
+    rng = np.random.default_rng(9)
+    pool = Pool(rng, [100], 32, 2, d, "e4m3")
+    mag = np.float32(2.0) ** exp
+    pool.scale[0] = (pool.scale[0] / mag).astype(np.float32)
+    pool.upload()
+    keep = np.zeros((1, N, N), bool)  # cached tokens only: the tree's keys have no scale
+    q = torch.randn(1, N, 4, d, generator=torch.Generator().manual_seed(2)).bfloat16().float().numpy() * mag
+    r = run_attention(pool, 1, N, 4, "bf16", rng, keep, q=q)
+    check_all(pool, r, keep, "bf16")
