@@ -748,8 +748,8 @@ et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_
  * row is lost; 2^-17.8 of it at most with d = 128 and more than 16 rows,
  * N * Hq / Hkv, per KV head, where q goes to the 8-bit tensor cores in two
  * terms).  A key's weight is its softmax numerator times the V scale of its
- * page (for tree rows: the scale that a page with their V of that head would
- * have), and is rounded to bf16 (tree rows) or fp16 (cached tokens: to 11 bits
+ * page (for a tree row: the scale that a page of its V alone would have), and is
+ * rounded to bf16 (tree rows) or fp16 (cached tokens: to 11 bits
  * if it is at least 2^-17 of its row's largest, to fewer below, to zero 2^-28
  * below) before it meets V; the sum of weights is not rounded.  A q row that holds a NaN or an infinity gives NaN.
  * fp32 inputs: fp32 throughout.

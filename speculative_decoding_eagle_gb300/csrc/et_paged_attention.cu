@@ -11,12 +11,13 @@
 // (the running maximum is taken over t), and the two sums hold the plain
 // softmax's numerator and denominator.
 //
-// The tree's rows, whose V is not quantised, get a scale of the same kind: vt,
-// the power of two that a page with their largest |V| would have.  t then
-// bounds p |v| for both kinds of key, whatever the size of V, and no key's
-// weight falls out of fp16's range because the other kind's V is held in
-// another unit.  Their weight is 2^(t - m) / vt (bf16, whose range has room for
-// it), so that V meets it as it is.
+// A tree row, whose V is not quantised, gets a scale of the same kind: vt, the
+// power of two that a page of this V alone would have.  t then bounds p |v|
+// for both kinds of key, whatever the size of V, and no key's weight falls out
+// of fp16's range because another kind's V is held in another unit.  (One
+// scale for the whole tree would let a row that others do not attend, padding
+// for one, decide about them.)  Its weight is 2^(t - m) / vt (bf16, whose range
+// has room for it), so that V meets it as it is.
 #include <cuda_bf16.h>
 
 #include "et_paged_attn.cuh"
@@ -233,7 +234,7 @@ struct PaShape {
   static constexpr int kBytes = kOffBar + KG * kStages * 8 + 1024;  // + slack for 1024-byte alignment
   static_assert(KG * R * D * 4 + (KG + 1) * R * 8 <= kOffRow, "the groups' rows are merged in the space of the ring and q");
   static_assert((kPaMaxSplits + 1) * R * 8 <= kOffRow, "the chunks' pairs, too");
-  static_assert(kBlocks * (kBytes + 1024 + 64) <= 228 * 1024, "the blocks of an SM");
+  static_assert(kBlocks * (kBytes + 1024 + 64 + kMaxN * 4) <= 228 * 1024, "the blocks of an SM");
 };
 
 template <bool BF16>
@@ -270,12 +271,13 @@ __device__ __forceinline__ int merge_chunk(int r, int c) {
 // score * f + lv relative to the row's reference mr, which moves only when a
 // weight would pass 2^15 (then it becomes the row maximum - 3 and what was
 // summed is rescaled).  keep: bit (8 * n-tile + key) per row, all ones when
-// `masked` is false.  On return p holds the weights as packed pairs, for the
-// tree's rows (BF16) over their V scale.
+// `masked` is false.  On return p holds the weights as packed pairs.  The
+// tree's rows (BF16) have a V scale each, 2 * n-tile + (column & 1), and their
+// weights are divided by it.
 template <int NT, int MT, int NTO, bool BF16>
 __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const float (&rf)[2 * MT],
-                                              const float (&ks)[NT / 2], const float (&lv)[NT / 2],
-                                              const float (&iv)[NT / 2], bool masked, const uint32_t (&keep)[2 * MT],
+                                              const float (&ks)[NT / 2], const float (&lv)[BF16 ? 2 * NT : NT / 2],
+                                              const float (&iv)[BF16 ? 2 * NT : NT / 2], bool masked, const uint32_t (&keep)[2 * MT],
                                               float (&mr)[2 * MT], float (&l)[2 * MT], float (&o)[MT][NTO][4],
                                               uint32_t (&p)[MT][NT][2]) {
   const int t2 = 2 * (threadIdx.x & 3);
@@ -288,10 +290,11 @@ __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const
       for (int u = 0; u < NT / 2; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float f = rf[2 * mt + h] * ks[u], c = lv[u] - mr[2 * mt + h];
+          const float f = rf[2 * mt + h] * ks[u];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int nt = 2 * u + (e >> 1), i = 2 * h + (e & 1);
+            const float c = lv[BF16 ? 2 * nt + (e & 1) : u] - mr[2 * mt + h];
             float v = fmaf(s[mt][nt][i], f, c);
             if (masked && !((keep[2 * mt + h] >> (8 * nt + t2 + (e & 1))) & 1u)) v = -INFINITY;
             x[mt][nt][i] = v;
@@ -311,7 +314,7 @@ __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           if (!masked || ((keep[r] >> (8 * nt + t2 + e)) & 1u))
-            top = fmaxf(top, fmaf(s[mt][nt][2 * h + e], rf[r] * ks[nt / 2], lv[nt / 2]));
+            top = fmaxf(top, fmaf(s[mt][nt][2 * h + e], rf[r] * ks[nt / 2], lv[BF16 ? 2 * nt + e : nt / 2]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const float now = fmaxf(mr[r], top - kPaTop), corr = ex2_fast(mr[r] - now);
@@ -331,11 +334,16 @@ __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const
     for (int u = 0; u < NT / 2; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float w0 = ex2_fast(x[mt][2 * u][2 * h]), w1 = ex2_fast(x[mt][2 * u][2 * h + 1]);
-        const float w2 = ex2_fast(x[mt][2 * u + 1][2 * h]), w3 = ex2_fast(x[mt][2 * u + 1][2 * h + 1]);
-        l[2 * mt + h] = fmaf((w0 + w1) + (w2 + w3), iv[u], l[2 * mt + h]);
-        p[mt][2 * u][h] = BF16 ? pack_bf16x2(w0 * iv[u], w1 * iv[u]) : pack_f16x2(w0, w1);
-        p[mt][2 * u + 1][h] = BF16 ? pack_bf16x2(w2 * iv[u], w3 * iv[u]) : pack_f16x2(w2, w3);
+        float w0 = ex2_fast(x[mt][2 * u][2 * h]), w1 = ex2_fast(x[mt][2 * u][2 * h + 1]);
+        float w2 = ex2_fast(x[mt][2 * u + 1][2 * h]), w3 = ex2_fast(x[mt][2 * u + 1][2 * h + 1]);
+        if (BF16) {
+          w0 *= iv[4 * u]; w1 *= iv[4 * u + 1]; w2 *= iv[4 * u + 2]; w3 *= iv[4 * u + 3];
+          l[2 * mt + h] += (w0 + w1) + (w2 + w3);
+        } else {
+          l[2 * mt + h] = fmaf((w0 + w1) + (w2 + w3), iv[u], l[2 * mt + h]);
+        }
+        p[mt][2 * u][h] = BF16 ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1);
+        p[mt][2 * u + 1][h] = BF16 ? pack_bf16x2(w2, w3) : pack_f16x2(w2, w3);
       }
 }
 
@@ -395,7 +403,7 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   extern __shared__ unsigned char smem_raw[];
   __shared__ int s_abort, s_last;
   __shared__ int s_red[kPaWarps];
-  __shared__ uint32_t s_vtop;  // the tree's largest finite |V| of this head, as the bits of an fp32 value
+  __shared__ float s_tree_lv[kMaxN];  // log2 of the tree rows' V scales
   unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = saddr(sm);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g8 = lane >> 2, tq = lane & 3;
@@ -403,9 +411,10 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   auto bar = [&](int stage) -> uint32_t { return sb + Sh::kOffBar + 8u * (uint32_t)(kg * ST + stage); };
 
   // ---- set-up that touches no global memory ----
+  static_assert(kPaThreads >= kMaxN, "an entry a thread");
+  if (t < kMaxN) s_tree_lv[t] = 0.f;  // (entries past the tree's rows are read, for keys that are masked)
   if (t == 0) {
     s_abort = 0;
-    s_vtop = 0u;
     for (int i = 0; i < KG * ST; ++i) mbar_init(sb + Sh::kOffBar + 8u * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_tmap(&tm_k);
@@ -518,33 +527,20 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
   if (wr == 0)
     for (int i = 0; i < n && i < ST; ++i) issue(i, page, slot);
 
-  // ---- the tree's V once over, for its scale (its products read it again, out of L1) ----
-  const int tree_cells = chunk == 0 ? a.N * (D / 8) : 0;  // 16 bytes each
-  uint32_t vtop = 0u;  // largest finite magnitudes of the low and of the high halves
-  constexpr int kTreeCells = 2;  // in flight beside q
-  uint4 cell[kTreeCells];
-  auto tree_cell = [&](int x) {
-    return x < tree_cells ? *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.vt) +
-                                                             (((long long)b * a.N + x / (D / 8)) * a.Hkv + g) * D + x % (D / 8) * 8)
-                          : make_uint4(0u, 0u, 0u, 0u);
-  };
-  auto see_cell = [&](const uint4 &v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = w[e] & 0x7fffu, hi = w[e] & 0x7fff0000u;
-      vtop = __vmaxu2(vtop, (lo < 0x7f80u ? lo : 0u) | (hi < 0x7f800000u ? hi : 0u));
-    }
-  };
-#pragma unroll
-  for (int k = 0; k < kTreeCells; ++k) cell[k] = tree_cell(t + k * kPaThreads);
-
   // ---- q into fragment order: D / 8 lanes per row, eight dims a lane ----
   float *row_f = reinterpret_cast<float *>(sm + Sh::kOffRow);
   {
     constexpr int LR = D / 8, RW = 32 / LR;       // lanes per row, rows a warp takes at once
     constexpr int QR = R / (kPaWarps * RW);       // rounds
     const int lr = lane % LR, sub = lane / LR;
+    // the tree's V once over, for its rows' scales (its products read it again, out of L1)
+    const int r_tree = warp * RW + sub;
+    auto tree_cell = [&](int r) {
+      return r < a.N && chunk == 0 ? *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.vt) +
+                                                                      (((long long)b * a.N + r) * a.Hkv + g) * D + 8 * lr)
+                                   : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 tree_v = tree_cell(r_tree);
     uint4 raw[QR];
 #pragma unroll
     for (int k = 0; k < QR; ++k) {
@@ -556,6 +552,20 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
                                                   8 * lr);
     }
     fetch_scale(page, ksc, vsc);  // in flight while q is staged
+    for (int r = r_tree; r - sub < a.N && chunk == 0; r += kPaWarps * RW) {  // whole warps
+      const uint32_t w[4] = {tree_v.x, tree_v.y, tree_v.z, tree_v.w};
+      tree_v = tree_cell(r + kPaWarps * RW);
+      uint32_t top = 0u;  // largest finite magnitudes of the low and of the high halves
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = w[e] & 0x7fffu, hi = w[e] & 0x7fff0000u;
+        top = __vmaxu2(top, (lo < 0x7f80u ? lo : 0u) | (hi < 0x7f800000u ? hi : 0u));
+      }
+      top = max(top << 16, top & 0xffff0000u);
+#pragma unroll
+      for (int x = 1; x < LR; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+      if (lr == 0) s_tree_lv[r] = (float)page_exponent<FMT>(__uint_as_float(top));
+    }
 #pragma unroll
     for (int k = 0; k < QR; ++k) {
       const int r = (warp + kPaWarps * k) * RW + sub, mt = r >> 4, up = (r >> 3) & 1, r8 = r & 7;
@@ -588,14 +598,6 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
         row_f[r] = odd ? __uint_as_float(0x7fc00000u)
                        : a.scale_log2 * __uint_as_float((uint32_t)(127 - ea) << 23) * __uint_as_float((uint32_t)(127 - eb) << 23);
     }
-  }
-  if (chunk == 0) {
-#pragma unroll
-    for (int k = 0; k < kTreeCells; ++k) see_cell(cell[k]);
-#pragma unroll 1
-    for (int x = t + kTreeCells * kPaThreads; x < tree_cells; x += kPaThreads) see_cell(tree_cell(x));
-    vtop = __reduce_max_sync(0xffffffffu, max(vtop << 16, vtop & 0xffff0000u));
-    if (lane == 0) atomicMax(&s_vtop, vtop);
   }
   __syncthreads();
 
@@ -660,8 +662,13 @@ __global__ void __launch_bounds__(kPaThreads, (PaShape<D, WR, MT>::kBlocks))
       float fs[2 * MT];
 #pragma unroll
       for (int r = 0; r < 2 * MT; ++r) fs[r] = rf[r] == rf[r] ? a.scale_log2 : rf[r];  // NaN: q is not finite
-      const int ve = page_exponent<FMT>(__uint_as_float(s_vtop));
-      const float one[1] = {1.f}, lvt[1] = {(float)ve}, ivt[1] = {power_of_two(-ve)};
+      const float one[1] = {1.f};
+      float lvt[4], ivt[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        lvt[k] = s_tree_lv[16 * tc + 2 * tq + 8 * (k >> 1) + (k & 1)];
+        ivt[k] = power_of_two(-(int)lvt[k]);
+      }
       uint32_t p[MT][2][2];
       paged_softmax<2, MT, NTO, true>(s, fs, one, lvt, ivt, true, keep, mr, l, o, p);
       bool odd = false;

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   __shared__ int s_abort, s_last, s_odd;
   __shared__ int s_red[kPtThreads / 32];
   __shared__ uint32_t s_tmem, s_units[kPtStages];
-  __shared__ uint32_t s_vtop;  // the tree's largest finite |V| of this head, as the bits of an fp32 value
+  __shared__ float s_tree_lv[kPtKeys];  // log2 of the tree rows' V scales
   __shared__ float4 s_scale[kPtStages][kPtKeys / 16];  // a unit's K scale, log2 of its V scale, the inverse of that
   unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = saddr(sm);
@@ -225,7 +225,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   if (t == 0) {
     s_abort = 0;
     s_odd = 0;
-    s_vtop = 0u;
     for (int i = 0; i < T_COUNT; ++i) {
       int count = 1;
       if (i >= T_VFULL && i < T_VEMPTY) count = 2;  // the copies, the scales
@@ -352,16 +351,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   };
   float *fc = reinterpret_cast<float *>(sm + kPtOffFC);  // group w at 2 * kPtRows * w
   bool odd_v = false;
-  uint32_t vtop = 0u;  // largest magnitudes of the low and of the high halves
-  auto store_cell = [&](int x, const uint4 &k, const uint4 &v) {
+  auto store_cell = [&](int x, const uint4 &k, const uint4 &v) {  // whole warps: 16 lanes have a row
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t top = 0u;  // largest finite magnitudes of the low and of the high halves
     // NaN and infinities would reach rows that do not attend their key (0 * inf): they are added at the end
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; odd_v = true; }
       if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; odd_v = true; }
-      vtop = __vmaxu2(vtop, w[e] & 0x7fff7fffu);
+      top = __vmaxu2(top, w[e] & 0x7fff7fffu);
     }
+    top = max(top << 16, top & 0xffff0000u);
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o, 16));
+    if ((x & 15) == 0) s_tree_lv[x >> 4] = (float)page_exponent<FMT>(__uint_as_float(top));
     const uint32_t at = (uint32_t)(((x & 15) >> 3) * kPtHalf16) + sw128(x >> 4, x & 7);
     sts128(sb + kPtOffTreeK + at, k.x, k.y, k.z, k.w);
     sts128(sb + kPtOffTreeV + at, w[0], w[1], w[2], w[3]);
@@ -434,8 +437,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       store_cell(x, k, v);
     }
     if (odd_v) s_odd = 1;
-    vtop = __reduce_max_sync(0xffffffffu, max(vtop << 16, vtop & 0xffff0000u));
-    if (lane == 0) atomicMax(&s_vtop, vtop);
     if (t < kPtRows) {
       const int i = row_token(ma, rt * kPtRows + t);
       unsigned long long m0 = 0ull, m1 = 0ull;
@@ -557,10 +558,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       static_assert(kPtVBuf == 3, "as many as score buffers");
       bool there = is_tree && tid < a.N;
       float ks = 1.f, lv = 0.f, iv = 1.f;
-      if (is_tree) {  // the scale a page with this V would have
-        const int ve = page_exponent<FMT>(__uint_as_float(*(volatile uint32_t *)&s_vtop));
-        lv = (float)ve;
-        iv = power_of_two(-ve);
+      if (is_tree) {
+        lv = there ? s_tree_lv[tid] : 0.f;
+        iv = power_of_two(-(int)lv);
       }
       // V16 buffer 1 held q of the tree's scores; else the buffer is free once the other group's product has run
       if (!is_tree && !dead) {

@@ -30,8 +30,10 @@ def quantised(x, fmt, P):
     return codes, scale
 
 
-def peaked(fmt, d, N, v_size, splits, lens=(1500, 333), Hkv=2, P=48, nats=7.0, dtype=torch.bfloat16, tree_v=1.0):
-    """Rows whose own key scores `nats` above the cached ones, V of mean half its deviation, sizes v_size * N(0, 1)."""
+def peaked(fmt, d, N, v_size, splits, lens=(1500, 333), Hkv=2, P=48, nats=7.0, dtype=torch.bfloat16, tree_v=1.0,
+           lone=()):
+    """Rows whose own key scores `nats` above the cached ones, V of mean half its deviation, sizes v_size * N(0, 1).
+    Rows `lone` are attended by themselves alone, and their V is 2^60 times as large."""
     rng = np.random.default_rng(int(d + N + splits))
     B, scale = len(lens), d ** -0.5
     bf = lambda x: torch.from_numpy(x.astype(np.float32)).bfloat16().float().numpy()  # noqa: E731
@@ -53,6 +55,10 @@ def peaked(fmt, d, N, v_size, splits, lens=(1500, 333), Hkv=2, P=48, nats=7.0, d
     pages = [dev(np.concatenate(c)).view(F8[fmt]) for c in codes]
     cache = E.PagedCache(pages[0], pages[1], *[dev(np.concatenate(s)) for s in scales])
     keep = random_tree(rng, B, N)
+    for j in lone:
+        keep[:, :, j] = False
+        keep[:, j, j] = True
+        vt[:, j] *= np.float32(2.0 ** 60)
     shape = E.PagedAttnShape(B=B, N=N, Hq=Hkv, max_blocks=cols, max_prefix=max(lens), num_splits=splits,
                              dtype=E.ET_BF16 if dtype == torch.bfloat16 else E.ET_F32)
     ws = E.new_workspace(E.et_tree_attention_paged_workspace_size(shape, cache))
@@ -93,3 +99,10 @@ def test_fp32_takes_v_of_any_size():
     for v_size in (2.0 ** -20, 1.0, 2.0 ** 10):
         for got, glse, ref, n in peaked("e5m2", 64, 5, v_size, 0, lens=(200, 33), dtype=torch.float32):
             check_attention(got, glse, ref, 64, "f32", n, 5)
+
+
+@pytest.mark.parametrize("d,N,splits", [(64, 40, 1), (128, 2, 1), (128, 16, 3), (128, 61, 1), (128, 128, 2)])
+def test_a_row_of_the_tree_does_not_decide_about_rows_that_do_not_attend_it(d, N, splits):
+    """Padding of a tree may hold anything finite: rows beside it get what they get without it."""
+    for got, glse, ref, n in peaked("e4m3", d, N, 0.05, splits, nats=5.0, lone=(N // 2, N - 1)):
+        check_attention(got, glse, ref, d, "bf16", n, N)
