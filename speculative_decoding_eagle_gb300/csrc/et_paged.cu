@@ -25,7 +25,7 @@ namespace {
 // barrier lets the first write happen only after the last read, the pages and
 // then (after a second barrier) the slots are dealt out over all threads.
 // Latency-bound: three dependent rounds of loads between two barriers (32
-// requests 5.7 us in a graph, 1024 with 128 new tokens each 13.6 us).
+// requests 5.5 us in a graph, 1024 with 128 new tokens each 13.3 us).
 constexpr int kMapThreads = 1024;
 constexpr int kMapMaxB = 4096;
 constexpr int kMapCluster = 8;  // portable cluster size
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kMapThreads) k_block_map(MapArgs a) {
 // magnitude and the rounding, every load in flight at once; only a prompt's
 // pages of more rows than that (64 of 128 dims) are read twice.  Bound by
 // latency (one sequence 2.7 us in a graph).  A prompt is bound by HBM and the
-// instructions of the conversion: 2 x 2047 rows of 32 heads 19.0 us in a
+// instructions of the conversion: 2 x 2047 rows of 32 heads 18.9 us in a
 // graph, 5.3 TB/s; 26.4 us with magnitudes compared as fp32 and codes packed by shifts (20
 // instructions an element, 11 now).  Extra blocks copy the feature rows.
 constexpr int kCpThreads = 128;

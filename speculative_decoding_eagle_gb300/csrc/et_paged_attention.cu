@@ -209,7 +209,7 @@ et_status launch_row(const PagedAttnArgs &a, int d, cudaStream_t st) {
 // one row each: 320 us, 6.7 TB/s.  A block takes about 10 us beside its stream (its
 // lengths, page table and first tiles one after the other; its groups' rows
 // and the sequence's chunks merged): 16 sequences of 512..16384 tokens, 8 KV
-// heads of 8 query heads: 57 us in a graph, 5.1 TB/s; one of 1023, 32 heads: 8.4 us in a
+// heads of 8 query heads: 57.4 us in a graph, 5.1 TB/s; one of 1023, 32 heads: 8.7 us in a
 // graph, 1.0 TB/s.
 constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
@@ -1025,8 +1025,9 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   p->flat = 0;
   if (s->dtype == ET_F32) return ET_OK;
   const long long rows = (long long)s->N * (s->Hq / c->Hkv);
-  // 16 sequences of 8880 tokens, 8 KV heads: 16 rows each 60.7 us with mma.sync, 90.2 with tcgen05; 24 rows 101.3 (two
-  // row tiles) and 90.8; one sequence of 8192: 18.5 and 19.2, 21.6 and 19.5
+  // mma.sync and tcgen05 from a graph, 16 rows and 24 (two of mma.sync's row tiles): 16 sequences of 8880 tokens, 8 KV
+  // heads: 57.3 and 87.4 us, 99.6 and 88.3; one of 8192: 16.9 and 17.8, 20.0 and 18.1; 8 of 4096, 32 KV heads: 24 rows
+  // 96.4 and 80.5.  One of 1024, 32 KV heads, is the exception: 24 rows 11.6 and 12.9, 32 rows 11.8 and 13.1
   p->tc = c->d == 128 && rows > 16;
   p->R = rows <= 16 ? 16 : rows <= 32 && !p->tc ? 32 : 64;
   p->row_tiles = (int)((rows + p->R - 1) / p->R);
@@ -1060,7 +1061,7 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   if (S > T) S = T;
   if (S > kPaMaxSplits) S = kPaMaxSplits;
   if (S < 1) S = 1;
-  // one sequence's blocks merge as a cluster where they can (32 KV heads, prefix 1023: 8.4 us in a graph, 10.0 through
+  // one sequence's blocks merge as a cluster where they can (32 KV heads, prefix 1023, side by side: 8.4 us in a graph, 10.0 through
   // the workspace); a batch's blocks of few rows do not, its short sequences leave clusters half empty (32 KV heads, 16
   // sequences of up to 8192: 131 us, 110 through the workspace).  Of the tcgen05 kernel's blocks an SM holds one, so few
   // wait (32 KV heads, 2 sequences of up to 16384: 68.3 us, 71.2 through the workspace)

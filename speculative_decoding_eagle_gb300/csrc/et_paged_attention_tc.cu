@@ -33,15 +33,16 @@
 // maxima, and rescales the group's sums and O.  The tree's own rows are one
 // more tile in bf16, staged by all warps before the roles part.
 // Up to eight chunks of a sequence form a cluster and merge through its shared
-// memory (7B heads, prefix 1024: 16.0 us, 18.9 through the workspace); more go
-// through the workspace, and the last block merges them.
+// memory (7B heads, prefix 1024, side by side when it was chosen: 16.0 us, 18.9
+// through the workspace; 14.3 now); more go through the workspace, and the last
+// block merges them.
 //
-// Measured: 32 heads, N = 61, 16 sequences of 512..16384 tokens: 303 us, 3.9
+// Measured: 32 heads, N = 61, 16 sequences of 512..16384 tokens: 304 us, 3.9
 // TB/s of codes and 466 TFLOP/s, 1.7 times what the bytes take.  A tile costs
 // 1.1 us with every SM at work (0.73 for its bytes).  What bounds it is the
-// softmax warps' chain of instructions (issue slots 66% taken in the busiest
-// SM, half of its ALU's cycles, tensor pipe 24%, shared memory 0.5 wavefronts
-// a cycle); a block spends about 10 us before its first and after its last
+// softmax warps' chain of instructions and of waits (issue slots 66% taken in
+// the busiest SM, half of its ALU's cycles, tensor pipe 24%, shared memory 0.5
+// wavefronts a cycle); a block spends about 10 us before its first and after its last
 // tile, which is most of the time of one short sequence.  Every mbarrier wait is bounded: a block that gives up
 // sets ET_DEV_TIMEOUT, drains what it issued and leaves.
 #include <atomic>
