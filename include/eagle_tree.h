@@ -737,21 +737,21 @@ et_status et_kv_commit_paged(const et_paged_commit_shape *shape, const et_paged_
  *               other functions may not.
  * v_scale counts as at least 2^-48 and at most 2^48 (what et_kv_commit_paged
  * writes); k_scale may be any value up to 2^100 in magnitude, as long as
- * scale * |q| * |k_scale| stays below 2^100 (the scores of larger ones leave
- * fp32's range on the way); an infinite code (e5m2) in a K row that is attended
- * may make its rows NaN.  Rows of a page past the prefix
- * are not used, whatever they hold.  A prefix past max_prefix or past
- * max_blocks pages is cut there, a page id outside the cache drops its
- * tokens; both set ET_DEV_BAD_INDEX.
+ * scale * |q| * |k_scale| stays below 2^100 (larger ones leave fp32's range on
+ * the way); an infinite code (e5m2) in a K row that is attended may make its
+ * rows NaN.  Rows of a page past the prefix are not used, whatever they hold.
+ * A prefix past max_prefix or past max_blocks pages is cut there, a page id
+ * outside the cache drops its tokens; both set ET_DEV_BAD_INDEX.
  * Scores, softmax statistics and outputs accumulate in fp32.  bf16 inputs:
  * cached codes meet q as it is (only what lies 2^-38 below the largest of its
  * row is lost; 2^-17.8 of it at most with d = 128 and more than 16 rows,
  * N * Hq / Hkv, per KV head, where q goes to the 8-bit tensor cores in two
  * terms).  A key's weight is its softmax numerator times the V scale of its
- * page (for a tree row: the scale that a page of its V alone would have), and is
- * rounded to bf16 (tree rows) or fp16 (cached tokens: to 11 bits
- * if it is at least 2^-17 of its row's largest, to fewer below, to zero 2^-28
- * below) before it meets V; the sum of weights is not rounded.  A q row that holds a NaN or an infinity gives NaN.
+ * page (for a tree row: the scale that a page of its V alone would have).  It
+ * is rounded before it meets V: of a tree row to bf16; of a cached token to
+ * fp16, that is to 11 bits if it is at least 2^-17 of its row's largest, to
+ * fewer below, to zero 2^-28 below.  The sum of weights is not rounded.  A q
+ * row that holds a NaN or an infinity gives NaN.
  * fp32 inputs: fp32 throughout.
  * bf16 inputs: a bounded wait that expires sets ET_DEV_TIMEOUT and leaves that
  * block's rows undefined.  Calls that can run at the same time need separate

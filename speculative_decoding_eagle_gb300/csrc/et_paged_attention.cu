@@ -277,8 +277,8 @@ __device__ __forceinline__ int merge_chunk(int r, int c) {
 template <int NT, int MT, int NTO, bool BF16>
 __device__ __forceinline__ void paged_softmax(const float (&s)[MT][NT][4], const float (&rf)[2 * MT],
                                               const float (&ks)[NT / 2], const float (&lv)[BF16 ? 2 * NT : NT / 2],
-                                              const float (&iv)[BF16 ? 2 * NT : NT / 2], bool masked, const uint32_t (&keep)[2 * MT],
-                                              float (&mr)[2 * MT], float (&l)[2 * MT], float (&o)[MT][NTO][4],
+                                              const float (&iv)[BF16 ? 2 * NT : NT / 2], bool masked,
+                                              const uint32_t (&keep)[2 * MT], float (&mr)[2 * MT], float (&l)[2 * MT], float (&o)[MT][NTO][4],
                                               uint32_t (&p)[MT][NT][2]) {
   const int t2 = 2 * (threadIdx.x & 3);
   float x[MT][NT][4];
@@ -1061,10 +1061,10 @@ et_status make_plan(const et_paged_attn_shape *s, const et_paged_cache *c, Paged
   if (S > T) S = T;
   if (S > kPaMaxSplits) S = kPaMaxSplits;
   if (S < 1) S = 1;
-  // one sequence's blocks merge as a cluster where they can (32 KV heads, prefix 1023, side by side: 8.4 us in a graph, 10.0 through
-  // the workspace); a batch's blocks of few rows do not, its short sequences leave clusters half empty (32 KV heads, 16
-  // sequences of up to 8192: 131 us, 110 through the workspace).  Of the tcgen05 kernel's blocks an SM holds one, so few
-  // wait (32 KV heads, 2 sequences of up to 16384: 68.3 us, 71.2 through the workspace)
+  // one sequence's blocks merge as a cluster where they can (32 KV heads, prefix 1023, side by side: 8.4 us in a graph,
+  // 10.0 through the workspace); a batch's blocks of few rows do not, its short sequences leave clusters half empty (32
+  // KV heads, 16 sequences of up to 8192: 131 us, 110 through the workspace).  Of the tcgen05 kernel's blocks an SM holds
+  // one, so few wait (32 KV heads, 2 sequences of up to 16384: 68.3 us, 71.2 through the workspace)
   const bool cluster = S > 1 && S <= kPaMaxCluster && (p->tc || s->B == 1);
   if (tiles > kPaCounters && !cluster) S = 1;  // far more blocks than SMs as it is
   if (S == 1) p->flat = 0;
