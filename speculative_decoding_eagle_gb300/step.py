@@ -112,9 +112,8 @@ def overlap_splits(tiles: int, depth: int, auto_splits: int, blocks_per_split: i
 class VerifyStep:
     """Buffers and call chain of one verification step for a fixed shape.
 
-    The buffers are cleared on the stream that is current when they are made (here, and in ``prepare``).  A step on
-    another stream has to come after that and after the kernels that write its inputs
-    (``stream.wait_stream(torch.cuda.current_stream())``)."""
+    The buffers are cleared on the stream that is current when they are made.  A step on another stream has to come after
+    that and after the kernels that write its inputs (``stream.wait_stream(torch.cuda.current_stream())``)."""
 
     def __init__(self, wl: W.Workload, B: Optional[int] = None, mode: Optional[int] = None, device="cuda",
                  num_splits: int = 0, max_prefix: Optional[int] = None, attn_impl: int = E.ATTN_AUTO,
@@ -179,11 +178,13 @@ class VerifyStep:
         sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
         return overlap_splits(tiles, self.cfg.depth, auto, self.B * shape.Hkv * MT, 2 * max(0, sms - tree_blocks))
 
-    def prepare(self, inp: StepInputs) -> None:
+    def prepare(self, inp: StepInputs, stream=None) -> None:
+        """What a step on these inputs needs; a new workspace is cleared on `stream` (default: the current one)."""
         shape = self.attn_shape(inp)
         if self.shape != shape:
             self.shape = shape
-            self.attn_ws = E.new_workspace(E.et_tree_attention_workspace_size(shape), self.device)
+            with torch.cuda.stream(stream):
+                self.attn_ws = E.new_workspace(E.et_tree_attention_workspace_size(shape), self.device)
         self.tree.root_tok = inp.root_tok
 
     # the five calls -------------------------------------------------------
@@ -217,7 +218,7 @@ class VerifyStep:
 
     def run(self, inp: StepInputs, stream=None) -> None:
         """The whole step: D expands, rerank with mask/posids (one launch), attention, acceptance."""
-        self.prepare(inp)
+        self.prepare(inp, stream)
         self.build_tree(inp, stream)
         self.attention(inp, stream)
         self.accept(inp, stream)
