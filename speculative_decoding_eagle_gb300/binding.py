@@ -497,8 +497,9 @@ def et_static_tree_sampled(B: int, V: int, temperature: float, parent: torch.Ten
         raise ValueError("logits must be a CUDA fp32 [rows, >=V] table with unit inner stride")
     N = parent.numel()
     cfg = StaticCfgC(B, V, N, 1, temperature)
-    if ws is None:
-        ws = new_workspace(load().et_static_tree_workspace_size(ctypes.byref(cfg)), logits.device)
+    if ws is None:  # of the call's own stream: written, and given back, in its order
+        with torch.cuda.stream(stream):
+            ws = new_workspace(load().et_static_tree_workspace_size(ctypes.byref(cfg)), logits.device)
     st = load().et_static_tree_sampled(ctypes.byref(cfg), _ptr(parent, torch.int32, "parent"), logits.data_ptr(),
                                        logits.stride(0), _ptr(row_of_flat, torch.int32, "row_of_flat"),
                                        _ptr(uniforms, torch.float32, "uniforms"), ctypes.byref(tree.c()),
