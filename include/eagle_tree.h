@@ -23,6 +23,12 @@
  * it, et_tree_attention_paged and et_kv_commit_paged in place of the last two
  * that touch the cache.
  *
+ * Around the step: et_rotary turns queries and keys at their positions (the
+ * tree's rows at et_tree_mask_posids' posids), et_chunk_attention_paged runs a
+ * prompt (or a batch of prompts' pieces and single tokens) over the paged
+ * cache before et_kv_commit_paged appends it, and et_sample draws a token from
+ * truncated logits, or writes those logits for et_verify_accept.
+ *
  * Conventions shared by every call
  * --------------------------------
  * - Every pointer argument that names a tensor is a DEVICE pointer unless the
@@ -227,6 +233,62 @@ typedef struct {
     int32_t max_prefix;       /* host upper bound of prefix_len[b] (sizes the grid) */
     int32_t num_splits;       /* blocks a sequence's keys are split over; 0 = library heuristic */
 } et_paged_attn_shape;
+
+/* Chunk attention shape (host struct), see et_chunk_attention_paged. */
+typedef struct {
+    int32_t B, Hq;            /* sequences; query heads, a multiple of the cache's Hkv */
+    int32_t rows;             /* rows in each of q, k_new, v_new and out, >= 1 */
+    int32_t max_rows;         /* host upper bound of one sequence's new rows (sizes the grid), 1..rows */
+    int32_t max_blocks;       /* columns of block_table */
+    et_dtype dtype;           /* of q, k/v new and out */
+    float scale;              /* score scale, usually 1/sqrt(d) */
+    int32_t max_prefix;       /* host upper bound of prefix_len[b] (sizes the grid) */
+    int32_t num_splits;       /* parts a sequence's keys are split into; 0 = library heuristic */
+    int64_t q_stride, k_stride, v_stride; /* elements from row to row, >= Hq * d (Hkv * d); multiples of 16 bytes */
+} et_chunk_attn_shape;
+
+/* Which dims of a head turn together (et_rotary): i with i + rot / 2, or 2 i with 2 i + 1. */
+typedef enum { ET_ROTARY_HALF = 0, ET_ROTARY_PAIRS = 1 } et_rotary_layout;
+
+/* Rotary shape (host struct), see et_rotary. */
+typedef struct {
+    int32_t rows;             /* tokens (B * N for a tree batch) */
+    int32_t Hq, Hkv;          /* heads of q and of k (Hkv 0 with k = NULL) */
+    int32_t d;                /* head dim, a multiple of 8 up to 512 */
+    int32_t rot;              /* dims of each head that turn: a multiple of 16, <= d; the others are copied */
+    et_rotary_layout layout;
+    et_dtype dtype;           /* of q, k and the outputs */
+    float factor;             /* factor on the turned values, usually 1 */
+    int64_t q_stride, k_stride;         /* elements from row to row of q and k, >= H * d; multiples of 16 bytes */
+    int64_t q_out_stride, k_out_stride; /* the same of the outputs */
+} et_rotary_shape;
+
+/* How the angles of long contexts are scaled (et_rotary_frequencies). */
+typedef enum {
+    ET_ROPE_PLAIN = 0,   /* f_i = theta^(-2 i / rot) */
+    ET_ROPE_LINEAR = 1,  /* f_i / scale */
+    ET_ROPE_BASE = 2,    /* theta replaced by theta * scale^(rot / (rot - 2)) */
+    ET_ROPE_RAMP = 3,    /* by dims: a linear ramp from f_i to f_i / scale between the dims that turn `fast` and `slow`
+                            times over `trained` tokens, and the factor 0.1 ln(scale) + 1 */
+    ET_ROPE_BANDS = 4    /* by wavelengths: f_i where it turns `fast` times or more over `trained` tokens, f_i / scale
+                            where it turns `slow` times or fewer, in between mixed linearly in the number of turns */
+} et_rope_scaling;
+
+typedef struct {
+    int32_t rot;          /* dims that turn */
+    double theta;         /* base, > 1 */
+    et_rope_scaling scaling;
+    double scale;         /* >= 1; not read by ET_ROPE_PLAIN */
+    double trained;       /* tokens the model was trained on (RAMP, BANDS) */
+    double fast, slow;    /* turns, fast > slow > 0 (RAMP: usually 32 and 1; BANDS: 4 and 1) */
+} et_rope_cfg;
+
+/* Sampling shape (host struct), see et_sample. */
+typedef struct {
+    int32_t B, V;             /* rows, vocabulary (<= 262144) */
+    int64_t row_stride;       /* elements from row to row of logits, >= V */
+    int64_t out_stride;       /* of truncated, >= V (0 with truncated = NULL) */
+} et_sample_shape;
 
 /* ---- geometry helpers (host, no device work) ---- */
 
@@ -770,6 +832,117 @@ et_status et_tree_attention_paged(const et_paged_attn_shape *shape, const et_pag
  */
 size_t et_tree_attention_paged_workspace_size(const et_paged_attn_shape *shape, const et_paged_cache *cache);
 int32_t et_tree_attention_paged_splits(const et_paged_attn_shape *shape, const et_paged_cache *cache);
+
+/*
+ * et_chunk_attention_paged -- attention of new rows over a paged 8-bit prefix
+ * and over themselves: a prompt's piece of any length, or a batch of such
+ * pieces and of single decoded tokens, packed one sequence behind the other.
+ *
+ *   out[r,h] = sum_j softmax_j(scale * q[r,h] . k_j) v_j,
+ *   r = row_start[b] + i, j over cached tokens 0..prefix_len[b]-1 of KV head
+ *   g = h / (Hq/Hkv), the values their codes and scales stand for, and new
+ *   rows row_start[b]..r of the same sequence (in the input type).
+ *
+ * block_table   int32 [B, max_blocks].
+ * prefix_len    int32 [B], each <= max_prefix; 0 is an empty prefix; < 0: no
+ *               sequence here, its rows of out and lse are left as they are.
+ * row_start     int32 [B + 1], ascending: sequence b has rows
+ *               row_start[b]..row_start[b+1]-1, at most max_rows, none allowed.
+ *               Rows of no sequence are left as they are.
+ * q             [rows, Hq, d]; k_new, v_new [rows, Hkv, d]: heads contiguous,
+ *               rows their stride apart (parts of one projection's output);
+ *               out [rows, Hq, d] contiguous; all 16-byte aligned, already
+ *               rotated (et_rotary).
+ * lse           nullable fp32 [rows, Hq]: natural-log log-sum-exp of the
+ *               scaled scores.  A row whose scores are all -inf has out = 0
+ *               and lse = -inf.
+ * ws            et_chunk_attention_paged_workspace_size() bytes, zero-filled
+ *               once (see conventions); 0/null when that size is 0.  Calls of
+ *               this function with other shapes may use it before and after,
+ *               other functions may not.
+ * The new rows are not written to the cache (et_kv_commit_paged with path =
+ * NULL does that, after this call has read the prefix).  Scales, codes that
+ * are NaN or infinite, prefixes past their bounds and page ids outside the
+ * cache: as in et_tree_attention_paged.  A row_start that descends, lies
+ * outside [0, rows] or gives a sequence more than max_rows rows sets
+ * ET_DEV_BAD_INDEX; the sequence is skipped, or in the last case cut after
+ * max_rows.
+ * Scores, softmax statistics and outputs accumulate in fp32.  bf16 inputs:
+ * q meets the cached codes in two 8-bit terms (as there, for any number of
+ * rows) and the new keys as it is; a cached key's weight times its V scale is
+ * rounded to fp16, a new key's weight to bf16; the sum of weights is not
+ * rounded.  A q row that holds a NaN or an infinity gives NaN.  fp32 inputs:
+ * fp32 throughout.
+ * bf16 inputs: a bounded wait that expires sets ET_DEV_TIMEOUT and leaves that
+ * block's rows undefined.
+ */
+et_status et_chunk_attention_paged(const et_chunk_attn_shape *shape, const et_paged_cache *cache,
+                                   const int32_t *block_table, const int32_t *prefix_len, const int32_t *row_start,
+                                   const void *q, const void *k_new, const void *v_new, void *out, float *lse,
+                                   int32_t *dev_status, void *ws, size_t ws_bytes, et_stream_t stream);
+/* Workspace bytes of that call, and the parts a sequence's keys are split into at most (-1: the shape breaks a limit). */
+size_t et_chunk_attention_paged_workspace_size(const et_chunk_attn_shape *shape, const et_paged_cache *cache);
+int32_t et_chunk_attention_paged_splits(const et_chunk_attn_shape *shape, const et_paged_cache *cache);
+
+/*
+ * et_rotary -- rotary positions of queries and keys: with the pairs (x, y) of
+ * dims that the layout names, pair i of a head at position t becomes
+ *   (x cos a - y sin a, y cos a + x sin a) * factor,   a = t * freq[i].
+ *
+ * positions     int32 [rows] (posids of et_tree_mask_posids, or the positions
+ *               of a prompt's rows); a negative one marks a row without a
+ *               token, whose outputs are left as they are.
+ * freq          fp64 [rot / 2] (device): angle per position, finite.
+ * q, k          [rows, H, d], heads contiguous, rows their stride apart.
+ * q_out, k_out  the same shape; each may be its input (same stride), or lie
+ *               apart from every input.  k and k_out NULL: q alone.
+ * All 16-byte aligned.  The angle is taken modulo a turn in 64-bit fixed
+ * point, freq / 2 pi rounded to 2^-64 of a turn: exact to t * 2^-65 turns at any
+ * position.  Sine and cosine are fp32, the products fp32, one rounding to
+ * the output's type.  No workspace.
+ */
+et_status et_rotary(const et_rotary_shape *shape, const int32_t *positions, const double *freq, const void *q,
+                    const void *k, void *q_out, void *k_out, et_stream_t stream);
+/* Host: freq[0 .. rot / 2 - 1] and the factor of a configuration (host pointers; copy freq to the device). */
+et_status et_rotary_frequencies(const et_rope_cfg *cfg, double *freq, float *factor);
+
+/*
+ * et_sample -- the next token of each row from its logits, truncated: with
+ * z the row (NaN counts as -inf, +inf as FLT_MAX; both set ET_DEV_NONFINITE)
+ * and w(v) = exp((z(v) - max z) / temperature),
+ *   top_k   keeps the k largest logits (ties: lower id first),
+ *   top_p   of these, in the same order, every token before which less than
+ *           top_p of their mass lies,
+ *   min_p   of these, every token with w(v) >= min_p;
+ *   the largest token (lowest id on ties) always stays;
+ *   token = the smallest kept id whose cumulative kept mass, in ascending id,
+ *           exceeds uniform * total kept mass.
+ *
+ * logits        fp32 [B], rows row_stride apart (device memory).
+ * temperature   nullable fp32 [B] (null: 1); not positive: the largest token
+ *               alone is kept (greedy).
+ * top_k         nullable int32 [B]; < 1: off.
+ * top_p, min_p  nullable fp32 [B]; top_p >= 1, min_p <= 0: off; top_p <= 0
+ *               keeps the largest token.
+ * uniforms      fp32 [B] in [0, 1) (others are clamped).
+ * token         int32 [B]; -1 for a row without a logit above -inf (which
+ *               also sets ET_DEV_NONFINITE).
+ * logprob       nullable fp32 [B]: log of the token's share of the kept mass
+ *               (-inf with token -1).
+ * truncated     nullable fp32 [B], rows out_stride apart: z where kept, -inf
+ *               elsewhere.  As et_verify_accept's target_logits (with the same
+ *               temperature; a greedy row has one logit left) it makes the
+ *               acceptance lossless for the truncated distribution.  May not
+ *               overlap logits.
+ * Masses are sums of w in 64-bit fixed point (2^-44 of the largest weight, w
+ * evaluated to 2^-40), so tokens and kept sets do not depend on the order of
+ * any sum and agree with 64-bit floating point but where a border lies within
+ * about 2^-36 of the total.  No workspace; one launch, a thread-block cluster
+ * per row.
+ */
+et_status et_sample(const et_sample_shape *shape, const float *logits, const float *temperature, const int32_t *top_k,
+                    const float *top_p, const float *min_p, const float *uniforms, int32_t *token, float *logprob,
+                    float *truncated, int32_t *dev_status, et_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,8 @@ ET_ACCEPT_GREEDY, ET_ACCEPT_STOCH_POINT, ET_ACCEPT_STOCH_DRAFTQ = 0, 1, 2
 ATTN_AUTO, ATTN_MMA_SYNC, ATTN_TCGEN05 = 0, 1, 2
 ET_ATTN_INPUTS_READY = 1
 ET_EXPAND_AUTO, ET_EXPAND_CLUSTER, ET_EXPAND_BLOCK = 0, 1, 2
+ET_ROTARY_HALF, ET_ROTARY_PAIRS = 0, 1
+ET_ROPE_PLAIN, ET_ROPE_LINEAR, ET_ROPE_BASE, ET_ROPE_RAMP, ET_ROPE_BANDS = range(5)
 
 EXPORTED = ("et_num_candidates", "et_layer_expanded", "et_layer_base", "et_tree_workspace_size",
             "et_tree_attention_workspace_size", "et_tree_attention_splits", "et_workspace_init",
@@ -34,7 +36,9 @@ EXPORTED = ("et_num_candidates", "et_layer_expanded", "et_layer_base", "et_tree_
             "et_tree_build", "et_tree_build_launches", "et_set_wait_limit", "et_set_expand_kernel",
             "et_tree_mask_posids", "et_tree_attention", "et_verify_accept", "et_kv_commit", "et_static_tree", "et_lm_head", "et_static_tree_sampled",
             "et_static_tree_workspace_size", "et_block_map", "et_kv_commit_paged", "et_tree_attention_paged",
-            "et_tree_attention_paged_workspace_size", "et_tree_attention_paged_splits")
+            "et_tree_attention_paged_workspace_size", "et_tree_attention_paged_splits", "et_chunk_attention_paged",
+            "et_chunk_attention_paged_workspace_size", "et_chunk_attention_paged_splits", "et_rotary",
+            "et_rotary_frequencies", "et_sample")
 
 
 class TreeCfgC(ctypes.Structure):
@@ -83,6 +87,27 @@ class PagedCommitShapeC(ctypes.Structure):
 class PagedAttnShapeC(ctypes.Structure):
     _fields_ = [("B", c_i32), ("N", c_i32), ("Hq", c_i32), ("max_blocks", c_i32), ("dtype", c_i32), ("scale", c_f32),
                 ("max_prefix", c_i32), ("num_splits", c_i32)]
+
+
+class ChunkAttnShapeC(ctypes.Structure):
+    _fields_ = [("B", c_i32), ("Hq", c_i32), ("rows", c_i32), ("max_rows", c_i32), ("max_blocks", c_i32),
+                ("dtype", c_i32), ("scale", c_f32), ("max_prefix", c_i32), ("num_splits", c_i32), ("q_stride", c_i64),
+                ("k_stride", c_i64), ("v_stride", c_i64)]
+
+
+class RotaryShapeC(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("Hq", c_i32), ("Hkv", c_i32), ("d", c_i32), ("rot", c_i32), ("layout", c_i32),
+                ("dtype", c_i32), ("factor", c_f32), ("q_stride", c_i64), ("k_stride", c_i64),
+                ("q_out_stride", c_i64), ("k_out_stride", c_i64)]
+
+
+class RopeCfgC(ctypes.Structure):
+    _fields_ = [("rot", c_i32), ("theta", ctypes.c_double), ("scaling", c_i32), ("scale", ctypes.c_double),
+                ("trained", ctypes.c_double), ("fast", ctypes.c_double), ("slow", ctypes.c_double)]
+
+
+class SampleShapeC(ctypes.Structure):
+    _fields_ = [("B", c_i32), ("V", c_i32), ("row_stride", c_i64), ("out_stride", c_i64)]
 
 
 class EtError(RuntimeError):
@@ -142,6 +167,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                             c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
         "et_tree_attention_paged_workspace_size": (c_sz, [P(PagedAttnShapeC), P(PagedCacheC)]),
         "et_tree_attention_paged_splits": (c_i32, [P(PagedAttnShapeC), P(PagedCacheC)]),
+        "et_chunk_attention_paged": (c_i32, [P(ChunkAttnShapeC), P(PagedCacheC), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                             c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+        "et_chunk_attention_paged_workspace_size": (c_sz, [P(ChunkAttnShapeC), P(PagedCacheC)]),
+        "et_chunk_attention_paged_splits": (c_i32, [P(ChunkAttnShapeC), P(PagedCacheC)]),
+        "et_rotary": (c_i32, [P(RotaryShapeC), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+        "et_rotary_frequencies": (c_i32, [P(RopeCfgC), P(ctypes.c_double), P(c_f32)]),
+        "et_sample": (c_i32, [P(SampleShapeC), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -747,3 +779,144 @@ def et_tree_attention_paged(shape: PagedAttnShape, cache: PagedCache, block_tabl
           None if lse is None else _arg(lse, _f32, sums, dev, "lse"),
           None if dev_status is None else _status(dev_status, dev),
           None if ws is None else _arg(ws, torch.uint8, (ws.numel(),), dev, "ws"), 0 if ws is None else ws.numel())
+
+
+# ---------------------------------------------------------------------------
+# around the step: a prompt's rows, their positions, the drawn token
+# ---------------------------------------------------------------------------
+def _rows(t: torch.Tensor, dtype, shape, device: int, what: str) -> int:
+    """The stride from row to row of a [rows, H, d] tensor whose heads are contiguous."""
+    rows, H, d = shape
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or t.stride(2) != 1 or \
+            (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} with contiguous heads on CUDA device "
+                         f"{device}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.stride(0) if rows > 1 else H * d  # one row: its stride may be anything
+
+
+@dataclasses.dataclass(frozen=True)
+class ChunkAttnShape(_Kept):
+    B: int
+    rows: int
+    Hq: int
+    max_rows: int                     # most new rows of one sequence
+    max_blocks: int
+    dtype: int = ET_BF16
+    scale: float = 0.0                # 0: 1 / sqrt(d) of the cache
+    max_prefix: Optional[int] = None  # longest prefix of the batch; None: whatever the table's pages hold
+    num_splits: int = 0
+
+    def for_cache(self, cache: PagedCache, strides=None):
+        """The C struct with the default scale and the rows' strides filled in, and the tensors' shapes."""
+        def make():
+            kv = cache.Hkv * cache.d
+            sq, sk, sv = strides or (self.Hq * cache.d, kv, kv)
+            c = ChunkAttnShapeC(self.B, self.Hq, self.rows, self.max_rows, self.max_blocks, self.dtype,
+                                cache.d ** -0.5 if self.scale == 0 else self.scale,
+                                0x7fffffff if self.max_prefix is None else self.max_prefix, self.num_splits, sq, sk, sv)
+            return (ctypes.byref(c), _TORCH_DTYPE[self.dtype], (self.B,), (self.B, self.max_blocks), (self.B + 1,),
+                    (self.rows, self.Hq, cache.d), (self.rows, cache.Hkv, cache.d), (self.rows, self.Hq))
+        return _kept(self, (cache.Hkv, cache.d, strides), make)
+
+
+def et_chunk_attention_paged_workspace_size(shape: ChunkAttnShape, cache: PagedCache) -> int:
+    with torch.cuda.device(cache.device):
+        return load().et_chunk_attention_paged_workspace_size(shape.for_cache(cache)[0], cache._ref)
+
+
+def et_chunk_attention_paged_splits(shape: ChunkAttnShape, cache: PagedCache) -> int:
+    with torch.cuda.device(cache.device):
+        return load().et_chunk_attention_paged_splits(shape.for_cache(cache)[0], cache._ref)
+
+
+def et_chunk_attention_paged(shape: ChunkAttnShape, cache: PagedCache, block_table: torch.Tensor,
+                             prefix_len: torch.Tensor, row_start: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor,
+                             v_new: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                             ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                             stream=None) -> None:
+    """Causal attention of each sequence's new rows (packed, ``row_start``) over its paged 8-bit prefix and themselves."""
+    dev = cache.device
+    _, dt, B, table, starts, rows, new, sums = shape.for_cache(cache)
+    strides = (_rows(q, dt, rows, dev, "q"), _rows(k_new, dt, new, dev, "k_new"), _rows(v_new, dt, new, dev, "v_new"))
+    ref = shape.for_cache(cache, strides)[0]
+    if not (block_table.dtype is prefix_len.dtype is row_start.dtype is _i32 and out.dtype is dt
+            and block_table.shape == table and prefix_len.shape == B and row_start.shape == starts and out.shape == rows
+            and block_table.get_device() == prefix_len.get_device() == row_start.get_device() == out.get_device() == dev
+            and block_table.is_contiguous() and prefix_len.is_contiguous() and row_start.is_contiguous()
+            and out.is_contiguous()):
+        _refuse(dev, (block_table, _i32, table, "block_table"), (prefix_len, _i32, B, "prefix_len"),
+                (row_start, _i32, starts, "row_start"), (out, dt, rows, "out"))
+    _call("et_chunk_attention_paged", dev, stream, ref, cache._ref, block_table.data_ptr(), prefix_len.data_ptr(),
+          row_start.data_ptr(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), out.data_ptr(),
+          None if lse is None else _arg(lse, _f32, sums, dev, "lse"),
+          None if dev_status is None else _status(dev_status, dev),
+          None if ws is None else _arg(ws, torch.uint8, (ws.numel(),), dev, "ws"), 0 if ws is None else ws.numel())
+
+
+def et_rotary_frequencies(rot: int, theta: float = 10000.0, scaling: int = ET_ROPE_PLAIN, scale: float = 1.0,
+                          trained: float = 4096.0, fast: float = 32.0, slow: float = 1.0):
+    """Angles per position of ``rot`` turning dims (fp64, on the host) and the factor on the turned values."""
+    freq = torch.empty(max(int(rot), 0) // 2, dtype=torch.float64)
+    factor = c_f32()
+    st = load().et_rotary_frequencies(ctypes.byref(RopeCfgC(rot, theta, scaling, scale, trained, fast, slow)),
+                                      ctypes.cast(freq.data_ptr(), ctypes.POINTER(ctypes.c_double)),
+                                      ctypes.byref(factor))
+    _check("et_rotary_frequencies", st)
+    return freq, factor.value
+
+
+@dataclasses.dataclass(frozen=True)
+class RotaryShape(_Kept):
+    rows: int
+    Hq: int
+    d: int
+    Hkv: int = 0
+    rot: int = 0                      # 0: the whole head
+    layout: int = ET_ROTARY_HALF
+    dtype: int = ET_BF16
+    factor: float = 1.0
+
+    def with_strides(self, strides):
+        def make():
+            return ctypes.byref(RotaryShapeC(self.rows, self.Hq, self.Hkv, self.d, self.rot or self.d, self.layout,
+                                             self.dtype, self.factor, *strides))
+        return _kept(self, strides, make)
+
+
+def et_rotary(shape: RotaryShape, positions: torch.Tensor, freq: torch.Tensor, q: torch.Tensor, q_out: torch.Tensor,
+              k: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Turn q and k (``[rows, H, d]``, rows any stride apart) at ``positions``; outputs may be the inputs themselves."""
+    dt, dev = _TORCH_DTYPE[shape.dtype], positions.get_device()
+    if (k is None) != (k_out is None) or (k is None) != (shape.Hkv == 0):
+        raise ValueError("k and k_out go with Hkv heads")
+    qs, ks = (shape.rows, shape.Hq, shape.d), (shape.rows, shape.Hkv, shape.d)
+    strides = (_rows(q, dt, qs, dev, "q"), 0 if k is None else _rows(k, dt, ks, dev, "k"),
+               _rows(q_out, dt, qs, dev, "q_out"), 0 if k is None else _rows(k_out, dt, ks, dev, "k_out"))
+    _call("et_rotary", dev, stream, shape.with_strides(strides),
+          _arg(positions, _i32, (shape.rows,), dev, "positions"),
+          _arg(freq, torch.float64, ((shape.rot or shape.d) // 2,), dev, "freq"), q.data_ptr(),
+          None if k is None else k.data_ptr(), q_out.data_ptr(), None if k is None else k_out.data_ptr())
+
+
+def et_sample(logits: torch.Tensor, uniforms: torch.Tensor, token: torch.Tensor,
+              temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+              top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+              logprob: Optional[torch.Tensor] = None, truncated: Optional[torch.Tensor] = None,
+              dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Draw each row's token from its truncated logits; ``truncated`` gets the row with -inf where a token is dropped."""
+    dev = logits.get_device()
+    for t, what in ((logits, "logits"), (truncated, "truncated")):
+        if t is not None and (t.dim() != 2 or t.dtype is not _f32 or t.shape != logits.shape or t.get_device() != dev
+                              or (t.shape[1] > 1 and t.stride(1) != 1)):
+            raise ValueError(f"{what} must be an fp32 CUDA [B, V] tensor with unit inner stride")
+    B, V = logits.shape
+    n = (B,)
+
+    def stride(t):
+        return t.stride(0) if B > 1 else V
+    c = SampleShapeC(B, V, stride(logits), 0 if truncated is None else stride(truncated))
+    _call("et_sample", dev, stream, ctypes.byref(c), logits.data_ptr(), _arg(temperature, _f32, n, dev, "temperature"),
+          _arg(top_k, _i32, n, dev, "top_k"), _arg(top_p, _f32, n, dev, "top_p"), _arg(min_p, _f32, n, dev, "min_p"),
+          _arg(uniforms, _f32, n, dev, "uniforms"), _arg(token, _i32, n, dev, "token"),
+          _arg(logprob, _f32, n, dev, "logprob"), None if truncated is None else truncated.data_ptr(),
+          None if dev_status is None else _status(dev_status, dev))

@@ -1,0 +1,33 @@
+// Shared by the chunk attention's kernels: their arguments and the reading of
+// a sequence's place in the batch.  Not part of the C ABI.
+#pragma once
+
+#include "et_paged_attn.cuh"
+
+namespace et {
+
+struct ChunkArgs {
+  PagedAttnArgs a;   // N: the most new rows of a sequence; kt, vt: the new keys and values; mask unused
+  int rows;          // of q, the new keys and values and out
+  long long qs, ks, vs;  // elements from row to row
+  const int32_t *row_start;
+};
+
+namespace {
+
+// New rows of sequence b: first row and count; count 0 = nothing to do.
+__device__ __forceinline__ void chunk_rows(const ChunkArgs &c, int b, int &first, int &n, int &bad) {
+  const int r0 = c.row_start[b], r1 = c.row_start[b + 1];
+  first = r0;
+  n = r1 - r0;
+  if (r0 < 0 || r1 > c.rows || r1 < r0) {
+    bad = 1;
+    n = 0;
+  } else if (n > c.a.N) {
+    bad = 1;
+    n = c.a.N;
+  }
+}
+
+}  // namespace
+}  // namespace et
