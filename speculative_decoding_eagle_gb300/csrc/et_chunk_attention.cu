@@ -14,18 +14,9 @@ namespace {
 
 constexpr int kCrThreads = 256, kCrRows = 32, kCrKeys = 32;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float4 *>(p);
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-  }
-}
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-template <typename T, int D, int FMT>
+template <int D, int FMT>
 __global__ void __launch_bounds__(kCrThreads) k_chunk_rows(const ChunkArgs c) {
   const PagedAttnArgs &a = c.a;
   constexpr int LD = D + 4;  // rows end four words further each: conflict-free reads of a column of rows
@@ -49,7 +40,7 @@ __global__ void __launch_bounds__(kCrThreads) k_chunk_rows(const ChunkArgs c) {
     if (r < real) {
       const long long i = (R0 + r) / a.G;
       const int h = g * a.G + (int)(R0 + r - i * a.G);
-      v = load4(static_cast<const T *>(a.q) + (first + i) * c.qs + (long long)h * D + e);
+      v = load4(static_cast<const float *>(a.q) + (first + i) * c.qs + (long long)h * D + e);
     }
     *reinterpret_cast<float4 *>(Q + r * LD + e) = v;
   }
@@ -73,8 +64,8 @@ __global__ void __launch_bounds__(kCrThreads) k_chunk_rows(const ChunkArgs c) {
       if (mine) {
         if (key <= last_token) {
           const long long row = first + key;
-          kv = load4(static_cast<const T *>(a.kt) + row * c.ks + (long long)g * D + e);
-          vv = load4(static_cast<const T *>(a.vt) + row * c.vs + (long long)g * D + e);
+          kv = load4(static_cast<const float *>(a.kt) + row * c.ks + (long long)g * D + e);
+          vv = load4(static_cast<const float *>(a.vt) + row * c.vs + (long long)g * D + e);
         }
       } else if (key < L) {
         const int blk = key / a.P, page = a.block_table[(long long)b * a.max_blocks + blk];
@@ -171,33 +162,41 @@ __global__ void __launch_bounds__(kCrThreads) k_chunk_rows(const ChunkArgs c) {
     for (int jj = 0; jj < D / 64; ++jj) {
       float4 v = o[i][jj];
       v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-      T *dst = static_cast<T *>(a.out) + row * D + 4 * tx + 64 * jj;
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(dst) = v;
-      else *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + 4 * tx + 64 * jj) = v;
     }
     if (a.lse && tx == 0) a.lse[row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
   }
 }
 
-template <typename T, int D, int FMT>
+template <int D, int FMT>
 et_status launch_rows(const ChunkArgs &c, cudaStream_t st) {
   constexpr int LD = D + 4;
   constexpr int bytes = (kCrRows * LD + kCrKeys * LD + kCrKeys * D + kCrRows * 33) * 4;
-  if (et_smem_attr((const void *)k_chunk_rows<T, D, FMT>, bytes) != cudaSuccess) return ET_ERR_CUDA;
+  if (et_smem_attr((const void *)k_chunk_rows<D, FMT>, bytes) != cudaSuccess) return ET_ERR_CUDA;
   const long long tiles = ((long long)c.a.N * c.a.G + kCrRows - 1) / kCrRows;
-  return et_launch(k_chunk_rows<T, D, FMT>, dim3((unsigned)tiles, c.a.Hkv, c.a.B), dim3(kCrThreads), bytes, st, 0, c);
+  return et_launch(k_chunk_rows<D, FMT>, dim3((unsigned)tiles, c.a.Hkv, c.a.B), dim3(kCrThreads), bytes, st, 0, c);
 }
-template <typename T>
 et_status launch_rows(const ChunkArgs &c, int d, int format, cudaStream_t st) {
   if (d == 64)
-    return format == ET_KV_E4M3 ? launch_rows<T, 64, ET_KV_E4M3>(c, st) : launch_rows<T, 64, ET_KV_E5M2>(c, st);
-  return format == ET_KV_E4M3 ? launch_rows<T, 128, ET_KV_E4M3>(c, st) : launch_rows<T, 128, ET_KV_E5M2>(c, st);
+    return format == ET_KV_E4M3 ? launch_rows<64, ET_KV_E4M3>(c, st) : launch_rows<64, ET_KV_E5M2>(c, st);
+  return format == ET_KV_E4M3 ? launch_rows<128, ET_KV_E4M3>(c, st) : launch_rows<128, ET_KV_E5M2>(c, st);
 }
 
 struct ChunkPlan {
-  int S;      // parts of a sequence's keys at most
+  ChunkTcPlan tc;
   size_t ws;
 };
+
+constexpr int kChunkCounters = 16384;  // in one place of every workspace, so that calls of other shapes can share it
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    n = 152;
+  cudaGetLastError();
+  return n;
+}
 
 et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, ChunkPlan *p) {
   if (!s) return ET_ERR_INVALID_ARG;
@@ -214,8 +213,30 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
   if (s->B > 65535 || s->Hq > 65535 || (long long)s->max_blocks * c->page_size >= (1ll << 31) ||
       (long long)s->max_rows * (s->Hq / c->Hkv) >= (1ll << 31))
     return ET_ERR_UNSUPPORTED;
-  p->S = 1;
-  p->ws = 0;
+  p->tc.S = 1;
+  p->tc.tiles = 0;
+  p->tc.ml_off = p->tc.o_off = p->ws = 0;
+  if (s->dtype == ET_F32) return ET_OK;
+  // every sequence's rows end in a tile of their own, if they have any
+  const long long rows = (long long)s->rows * (s->Hq / c->Hkv);
+  const long long tiles = rows / 256 + (s->B < s->rows ? s->B : s->rows);
+  const long long units = tiles * c->Hkv;
+  if (units >= (1ll << 24)) return ET_ERR_UNSUPPORTED;
+  const long long room = (long long)s->max_blocks * c->page_size;
+  const long long T = ((s->max_prefix < room ? s->max_prefix : room) + 127) / 128 + (s->max_rows + 127) / 128;
+  long long S = s->num_splits;
+  if (S <= 0) S = sm_count() / units;
+  if (S > T) S = T;
+  if (S > 64) S = 64;
+  if (S < 1 || units > kChunkCounters) S = 1;
+  p->tc.S = (int)S;
+  p->tc.tiles = (int)tiles;
+  if (S > 1) {
+    const size_t slots = (size_t)units * S * 256;
+    p->tc.ml_off = kChunkCounters * sizeof(unsigned int);
+    p->tc.o_off = p->tc.ml_off + slots * sizeof(float2);
+    p->ws = p->tc.o_off + slots * c->d * sizeof(float);
+  }
   return ET_OK;
 }
 
@@ -231,7 +252,7 @@ extern "C" size_t et_chunk_attention_paged_workspace_size(const et_chunk_attn_sh
 
 extern "C" int32_t et_chunk_attention_paged_splits(const et_chunk_attn_shape *shape, const et_paged_cache *cache) {
   ChunkPlan p;
-  return make_plan(shape, cache, &p) == ET_OK ? p.S : -1;
+  return make_plan(shape, cache, &p) == ET_OK ? p.tc.S : -1;
 }
 
 extern "C" et_status et_chunk_attention_paged(const et_chunk_attn_shape *shape, const et_paged_cache *cache,
@@ -261,6 +282,6 @@ extern "C" et_status et_chunk_attention_paged(const et_chunk_attn_shape *shape, 
   c.rows = shape->rows; c.qs = shape->q_stride; c.ks = shape->k_stride; c.vs = shape->v_stride;
   c.row_start = row_start;
   cudaStream_t st = (cudaStream_t)stream;
-  return shape->dtype == ET_F32 ? launch_rows<float>(c, cache->d, cache->format, st)
-                                : launch_rows<__nv_bfloat16>(c, cache->d, cache->format, st);
+  if (shape->dtype == ET_BF16) return chunk_tc_launch(cache, c, plan.tc, ws, st);
+  return launch_rows(c, cache->d, cache->format, st);
 }

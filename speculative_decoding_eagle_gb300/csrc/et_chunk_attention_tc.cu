@@ -1,0 +1,892 @@
+// Chunk attention on the 5th-generation tensor cores (tcgen05): many new rows
+// of a sequence over its paged 8-bit prefix and over themselves, bf16 inputs,
+// D = 64 or 128 (EAGLE blog 1.1: the target's forward over a prompt).
+//
+// One block per SM and 256 (token, head) rows of a KV head, two tiles of 128
+// rows, a row to a TMEM lane; keys in tiles of 128:
+//   S [128 rows x 128 keys] = Q8 . K8^T  (kind::f8f6f4: K's codes by TMA as they
+//        lie in the page; q lifted by a power of two per row and split into
+//        two e4m3 terms, two products into one sum), or Q . K^T in bf16 for
+//        the new rows' own keys;
+//   O [128 rows x D] += P . V  (kind::f16, P from TMEM where S was): V's codes
+//        as fp16, or the new rows' V in bf16.
+// Sixteen warps:
+//   warps 0-3, 4-7  a softmax group each, one row per thread: the row's 128
+//              scores go through registers once, no exchange between threads.
+//              More than 128 rows: each group has its own 128, over the same
+//              tiles.  Fewer (decoded tokens, short pieces): both have the
+//              same rows and alternate tiles, joined at the end, so that one
+//              group's products run under the other's softmax either way
+//   warps 8-11 turn V's codes into fp16, stage q, and clear what no row of
+//              the block may see from the new rows' V
+//   warp 12    TMA;  warp 13 issues the score products, warp 14 those of P.V
+// The prefix comes first.  A weight's reference moves only when some weight
+// would pass 2^15; a row is a thread's own, so nothing but the warp has to
+// agree.  A cached key's weight carries its page's V scale and is rounded to
+// fp16; the new keys' weights are rounded to bf16, whose range does not depend
+// on how large their V is against the cache's.
+// Few rows: a sequence's tiles are split over several blocks, which leave
+// their rows in the workspace; the last one to arrive merges them.
+// Every mbarrier wait is bounded: a block that gives up sets ET_DEV_TIMEOUT,
+// drains what it issued and leaves.
+#include "et_chunk_attn.cuh"
+#include "et_paged_tc.cuh"
+
+#include <type_traits>
+
+namespace et {
+namespace {
+
+constexpr int kCtThreads = 512;
+constexpr int kCtKeys = 128;                          // keys per tile
+constexpr int kCtTmaWarp = 12, kCtScoreWarp = 13, kCtPvWarp = 14;
+constexpr int kCtStages8 = 4, kCtStages16 = 2;        // K ring: stages of codes, or of bf16 rows, in one space
+constexpr int kCtSlots = 8;                           // tiles whose scales are kept
+constexpr uint32_t kCtColS = 0, kCtColO = 256, kCtTmemCols = 512;  // S / P of the two groups, O of the two groups
+
+template <int D>
+struct CtShape {
+  static constexpr uint32_t tile8 = kCtKeys * D;          // codes of a tile of keys, or one term of 128 q rows
+  static constexpr uint32_t tile16 = 2 * tile8;           // bf16 / fp16 rows of a tile
+  static constexpr uint32_t half16 = kCtKeys * 128;       // 64 dims of it
+  static constexpr uint32_t off_q = 0;                    // two groups: two e4m3 terms, later bf16
+  static constexpr uint32_t off_k = 2 * tile16;
+  static constexpr uint32_t off_v8 = off_k + kCtStages16 * tile16;
+  static constexpr uint32_t off_v16 = off_v8 + 2 * tile8;
+  static constexpr uint32_t off_bar = off_v16 + 2 * tile16;
+  static constexpr uint32_t bytes = off_bar + 512 + 1024;  // + slack for 1024-byte alignment
+};
+static_assert(CtShape<128>::bytes <= 227 * 1024 - 1536, "one block per SM, static shared memory besides");
+
+enum {
+  C_KFULL = 0,                        // four stages of codes
+  C_KEMPTY = C_KFULL + kCtStages8,
+  C_K2FULL = C_KEMPTY + kCtStages8,   // two stages of bf16 keys
+  C_K2EMPTY = C_K2FULL + kCtStages16,
+  C_VFULL = C_K2EMPTY + kCtStages16,  // V's codes
+  C_VEMPTY = C_VFULL + 2,
+  C_VTMA = C_VEMPTY + 2,              // bf16 V has landed
+  C_VHFULL = C_VTMA + 2,              // V as the products take it
+  C_VHFREE = C_VHFULL + 2,
+  C_SFULL = C_VHFREE + 2,             // per group from here on
+  C_PFULL = C_SFULL + 2,
+  C_PVDONE = C_PFULL + 2,
+  C_QFREE = C_PVDONE + 2,             // the prefix's score products have run: q and the K ring are free
+  C_QFULL = C_QFREE + 1,              // q in bf16
+  C_SCALES = C_QFULL + 1,             // eight slots: a tile's scales are there
+  C_DRAIN = C_SCALES + kCtSlots,      // two
+  C_COUNT = C_DRAIN + 2
+};
+static_assert(C_COUNT * 8 <= 512, "barriers");
+
+// descriptor of 8-bit rows of D bytes: 128-byte or 64-byte swizzle (mode 2 or 4), eight rows to a group
+template <int D>
+__device__ __forceinline__ uint64_t desc8(uint32_t start) {
+  const uint64_t mode = D == 128 ? 2ull : 4ull;
+  return (uint64_t)((start >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(8 * D >> 4) << 32) | (1ull << 46) | (mode << 61);
+}
+// chunk c (16 bytes) of row r among rows of D bytes
+template <int D>
+__device__ __forceinline__ uint32_t at8(int r, int c) {
+  return D == 128 ? sw128(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+// mbar_drain without a call: registers are split unevenly over the warps, which a call's fixed set does not allow
+__device__ __forceinline__ void ct_drain(uint32_t bar, uint32_t parity) {
+  const long long start = clock64();
+#pragma unroll 1
+  while (!mbar_try(bar, parity) && clock64() - start < kTcWaitCycles) {
+  }
+}
+// all warps at the end of their roles: registers are handed back before any warp asks for its share again (a warp that took
+// them back while a softmax warp still waits for them would leave it waiting)
+__device__ __forceinline__ void roles_end() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kCtThreads) : "memory"); }
+template <int R>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+struct ChunkTcArgs {
+  ChunkArgs c;
+  int S;                 // parts of a block's tiles at most
+  int tiles;             // tiles of 256 rows per KV head in the grid
+  int box;               // rows per TMA box of a page
+  unsigned int *cnt;     // arrival counters (null with S = 1)
+  float2 *part_ml;
+  float4 *part_o;
+  uint32_t page_magic, group_magic, group_shift;
+  long long wait_cycles;
+};
+__device__ __forceinline__ int ct_page_index(const ChunkTcArgs &a, int token) {
+  const uint32_t u = (uint32_t)token >> 4;
+  return (int)(a.page_magic ? __umulhi(u, a.page_magic) : u);
+}
+__device__ __forceinline__ int ct_token(const ChunkTcArgs &a, int row) {
+  return (int)(a.group_magic ? __umulhi((uint32_t)row, a.group_magic) >> a.group_shift : (uint32_t)row);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kCtThreads, 1)
+    k_chunk_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+               const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
+               const __grid_constant__ ChunkTcArgs ca) {
+  using Sh = CtShape<D>;
+  const PagedAttnArgs &a = ca.c.a;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ int s_abort, s_last, s_odd, s_seq, s_tile, s_longest;
+  __shared__ int s_red[kCtThreads / 32], s_len[kCtThreads / 32];
+  __shared__ uint32_t s_tmem, s_units[kCtSlots];
+  __shared__ __align__(16) float4 s_scale[kCtSlots][kCtKeys / 16];  // a unit's K scale, log2 of its V scale, the inverse of that
+  unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t sb = saddr(sm);
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  auto bar = [&](int i) -> uint32_t { return sb + Sh::off_bar + 8u * (uint32_t)i; };
+
+  // ---- set-up that touches no global memory ----
+  if (t == 0) {
+    s_abort = 0;
+    s_odd = 0;
+    s_seq = -1;
+    s_tile = 0;
+    s_longest = 0;
+    for (int i = 0; i < C_COUNT; ++i) {
+      int count = 1;
+      if ((i >= C_VEMPTY && i < C_VTMA) || (i >= C_VHFULL && i < C_VHFREE) || (i >= C_PFULL && i < C_PVDONE) || i == C_QFULL)
+        count = 4;  // the warps of a group
+      mbar_init(bar(i), (uint32_t)count);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    prefetch_tmap(&tm_kn);
+    prefetch_tmap(&tm_vn);
+  }
+  __syncthreads();
+  pdl_wait();  // the previous kernel in the stream has completed
+
+  // ---- which rows: tile `index` of the batch's tiles of 256 rows, in the sequences' order ----
+  const int part = blockIdx.x % ca.S, unit = blockIdx.x / ca.S;
+  const int g = unit / ca.tiles, index = unit - g * ca.tiles;
+  int bad = 0;
+  {
+    int done = 0;  // tiles of the sequences before this round's
+    for (int b0 = 0; b0 < a.B; b0 += kCtThreads) {
+      const int b = b0 + t;
+      int mine = 0, keys = 0;
+      if (b < a.B) {
+        int first, n, ignore = 0;
+        chunk_rows(ca.c, b, first, n, ignore);
+        const int L = paged_prefix(a, b, ignore);
+        if (ignore && blockIdx.x == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
+        if (L >= 0 && n > 0) {
+          mine = (int)(((long long)n * a.G + 255) >> 8);
+          keys = tiles_of(L, kCtKeys) + tiles_of(n, kCtKeys);
+        }
+      }
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      keys = __reduce_max_sync(0xffffffffu, keys);
+      if (lane == 31) s_red[warp] = incl;
+      if (lane == 0) s_len[warp] = keys;
+      __syncthreads();
+      int before = done, all = done, longest = 0;
+      for (int w = 0; w < kCtThreads / 32; ++w) {
+        if (w < warp) before += s_red[w];
+        all += s_red[w];
+        longest = max(longest, s_len[w]);
+      }
+      before += incl - mine;
+      if (before <= index && index < before + mine) {
+        s_seq = b;
+        s_tile = index - before;
+      }
+      if (t == 0) s_longest = max(s_longest, longest);
+      done = all;
+      __syncthreads();
+    }
+  }
+  const int b = s_seq;
+  if (b < 0) return;  // fewer tiles than the grid has places for
+  int first, nrows;
+  chunk_rows(ca.c, b, first, nrows, bad);
+  const int L = paged_prefix(a, b, bad);
+  // the last tiles have the most keys: they go out first
+  const long long all_rows = (long long)nrows * a.G;
+  const int row_tiles = (int)((all_rows + 255) >> 8);
+  const int R0 = (row_tiles - 1 - s_tile) << 8;                    // first row of the KV head's (token, head) rows
+  const int real = (int)min(256ll, all_rows - R0);
+  const bool shared_rows = real <= 128;                            // both groups have the same rows
+  const int tok_first = ct_token(ca, R0), tok_last = ct_token(ca, R0 + real - 1);
+  const int Tp = tiles_of(L, kCtKeys), To = tok_last / kCtKeys + 1, T = Tp + To;
+  const int per = max((s_longest + ca.S - 1) / ca.S, 1);
+  const int parts = (T + per - 1) / per;
+  if (part >= parts) return;
+  const int t0 = part * per, t1 = min(T, t0 + per);
+  const int n8 = max(0, min(t1, Tp) - t0);                         // tiles of the prefix
+  const int o0 = max(t0 - Tp, 0), n16 = max(0, t1 - Tp - o0);      // tiles of the new rows: o0 .. o0 + n16 - 1
+  const int n = n8 + n16;
+  // tiles that group 0 needs: its last row sees fewer of the new rows
+  const int To0 = shared_rows ? To : ct_token(ca, R0 + 127) / kCtKeys + 1;
+  const int n_first = shared_rows ? n : n8 + max(0, min(n16, To0 - o0));
+  if (warp == kCtScoreWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&s_tmem)), "r"(kCtTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // users of tile i: group 0 and 1, or i & 1
+  auto uses = [&](int w, int i) -> bool { return shared_rows ? (i & 1) == w : (w == 1 || i < n_first); };
+
+  // ---- q: a thread per row; two e4m3 terms for the prefix, else bf16 at once ----
+  const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q);
+  auto q_row = [&](int r) -> const __nv_bfloat16 * {  // row r of the block; null past the last
+    if (r >= real) return nullptr;
+    const int R = R0 + r, i = ct_token(ca, R), h = g * a.G + (R - i * a.G);
+    return Q + (long long)(first + i) * ca.c.qs + (long long)h * D;
+  };
+  auto stage_q16 = [&](int w, int r) {  // row r of group w's tile
+    const __nv_bfloat16 *src = q_row(shared_rows ? r : 128 * w + r);
+    const uint32_t dst = sb + Sh::off_q + (uint32_t)w * Sh::tile16;
+#pragma unroll
+    for (int c0 = 0; c0 < D / 8; c0 += 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = src ? reinterpret_cast<const uint4 *>(src)[c0 + c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sts128(dst + (uint32_t)(c0 >> 3) * Sh::half16 + sw128(r, c), v[c].x, v[c].y, v[c].z, v[c].w);
+    }
+  };
+  float f8 = 0.f, f16 = a.scale_log2;  // what a score of lifted q and codes, or of bf16 values, stands for in log2 units
+  if (warp < 8) {
+    const int w = warp >> 2, r = t & 127;
+    const __nv_bfloat16 *src = q_row(shared_rows ? r : 128 * w + r);
+    uint32_t top = 0u;  // the row's largest magnitude, as the bits of a bf16 value: they order like the values
+    if (src) {
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 v = reinterpret_cast<const uint4 *>(src)[c];
+        const uint32_t x = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        top = max(top, max(x & 0xffffu, x >> 16));
+      }
+    }
+    const bool odd = top >= 0x7f80u;  // NaN or infinity: the row scores NaN
+    // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8; half of e2 stays within fp32's exponents
+    const int e2 = top == 0u || odd ? 0 : 135 - max((int)(top >> 7), 1) - ((top & 0x7fu) > 0x60u ? 1 : 0);
+    const int ea = e2 >> 1, eb = e2 - ea;
+    f8 = a.scale_log2 * power_of_two(-ea) * power_of_two(-eb);
+    if (odd) f8 = f16 = __uint_as_float(0x7fc00000u);
+    if (n8 > 0 && (w == 0 || !shared_rows)) {
+      const float lift_a = power_of_two(ea), lift_b = power_of_two(eb);
+      const uint32_t dst = sb + Sh::off_q + (uint32_t)w * Sh::tile16;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t hi[4], lo[4], x[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4 v = src ? reinterpret_cast<const uint4 *>(src)[2 * c + e] : make_uint4(0u, 0u, 0u, 0u);
+          x[4 * e] = v.x; x[4 * e + 1] = v.y; x[4 * e + 2] = v.z; x[4 * e + 3] = v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          hi[e] = lo[e] = 0u;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float y0 = __uint_as_float(x[2 * e + k] << 16) * lift_a * lift_b;
+            const float y1 = __uint_as_float(x[2 * e + k] & 0xffff0000u) * lift_a * lift_b;
+            const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1), hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
+            const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
+            hi[e] |= h2 << (16 * k);
+            lo[e] |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (16 * k);
+          }
+        }
+        sts128(dst + at8<D>(r, c), hi[0], hi[1], hi[2], hi[3]);
+        sts128(dst + Sh::tile8 + at8<D>(r, c), lo[0], lo[1], lo[2], lo[3]);
+      }
+    } else if (n8 == 0 && (w == 0 || !shared_rows)) {
+      stage_q16(w, r);
+    }
+  }
+  fence_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();  // after the TMEM allocation: a waiting dependent block must not hold what this block needs
+  const uint32_t tmem = s_tmem;
+  const long long limit = ca.wait_cycles;
+  float l = 0.f, ref = 0.f;   // a softmax thread's row: sum of weights, reference
+  bool fresh = true;          // no key seen yet
+  int items = 0;              // tiles this group has taken
+
+  // a softmax thread holds a row's 128 scores: it gets registers of the other warps (512 x 128 = 256 x 64 + 256 x 192)
+  if (warp >= kCtTmaWarp) {
+  regs_down<64>();
+  if (warp == kCtTmaWarp) {
+    // ---------------- TMA: tile j of the prefix into stage j & 3 (K) and j & 1 (V) ----------------
+    // lane: unit (lane & 7) of tile 4 * (j / 4) + (lane >> 3), 16 keys a unit; the next four tiles' (_n) in flight ahead
+    int page = -1, slot = 0, page_n = -1, slot_n = 0;
+    float ks = 0.f, vs = 1.f, ks_n = 0.f, vs_n = 1.f;
+    auto unit_key = [&](int j0) -> long long {
+      const int j = j0 + (lane >> 3);
+      const long long key = (long long)(t0 + j) * kCtKeys + 16 * (lane & 7);
+      return j < n8 && key < L ? key : -1;
+    };
+    auto fetch_pages = [&](int j0, int &pg, int &sl) {
+      const int key = (int)unit_key(j0);
+      pg = -1;
+      if (key >= 0) {
+        const int blk = ct_page_index(ca, key);
+        sl = key - blk * a.P;
+        pg = a.block_table[(long long)b * a.max_blocks + blk];
+      }
+    };
+    auto fetch_scales = [&](int j0, int &pg, float &k, float &v) {
+      if (pg < 0 || pg >= a.num_pages) {
+        if (unit_key(j0) >= 0) bad = 1;
+        pg = -1;
+      }
+      k = 0.f;
+      v = 1.f;
+      if (pg >= 0) {
+        k = a.k_scale[(long long)pg * a.Hkv + g];
+        v = a.v_scale[(long long)pg * a.Hkv + g];
+      }
+    };
+    const int per_box = ca.box / 16;
+    bool ok = true;
+    int issued_k = 0, issued_v = 0;
+    fetch_pages(0, page, slot);
+    fetch_scales(0, page, ks, vs);
+    fetch_pages(4, page_n, slot_n);
+    for (int j = 0; j < n8; ++j) {
+      if ((j & 3) == 2) fetch_scales(j + 2, page_n, ks_n, vs_n);
+      if ((j & 3) == 0 && j > 0) {
+        page = page_n; slot = slot_n; ks = ks_n; vs = vs_n;
+        fetch_pages(j + 4, page_n, slot_n);
+      }
+      const int src = 8 * (j & 3) + (lane & 7);
+      const int pg = __shfl_sync(0xffffffffu, page, src), sl = __shfl_sync(0xffffffffu, slot, src);
+      const float k = __shfl_sync(0xffffffffu, ks, src), v = clamp_v_scale(__shfl_sync(0xffffffffu, vs, src));
+      const uint32_t there = __ballot_sync(0xffffffffu, lane < 8 && pg >= 0);
+      const uint32_t mine = __ballot_sync(0xffffffffu, lane < 8 && lane % per_box == 0 && pg >= 0);
+      const uint32_t bytes = (uint32_t)__popc(mine) * (uint32_t)ca.box * D;
+      const int sk = j % kCtStages8, sv = j & 1;
+      if (j >= kCtStages8) ok = pt_wait(bar(C_KEMPTY + sk), (uint32_t)(j / kCtStages8 - 1) & 1u, &s_abort, limit);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      // the scales' slot was last read for tile j - 8, whose softmax is past: tile j - 4's scores have run
+      if (lane < 8) s_scale[j % kCtSlots][lane] = make_float4(k, __log2f(v), __fdividef(1.f, v), 0.f);
+      if (lane == 0) s_units[j % kCtSlots] = there;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(C_SCALES + j % kCtSlots));
+        if (bytes) mbar_expect_tx(bar(C_KFULL + sk), bytes);
+        else mbar_arrive(bar(C_KFULL + sk));
+      }
+      __syncwarp();
+      if ((mine >> lane) & 1u)
+        tma_4d(sb + Sh::off_k + (uint32_t)sk * Sh::tile8 + (uint32_t)(lane * 16 * D), &tm_k, 0, sl, g, pg, bar(C_KFULL + sk));
+      issued_k = j + 1;
+      if (j >= 2) ok = pt_wait(bar(C_VEMPTY + sv), (uint32_t)((j >> 1) - 1) & 1u, &s_abort, limit);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        if (bytes) mbar_expect_tx(bar(C_VFULL + sv), bytes);
+        else mbar_arrive(bar(C_VFULL + sv));
+      }
+      __syncwarp();
+      if ((mine >> lane) & 1u)
+        tma_4d(sb + Sh::off_v8 + (uint32_t)sv * Sh::tile8 + (uint32_t)(lane * 16 * D), &tm_v, 0, sl, g, pg, bar(C_VFULL + sv));
+      issued_v = j + 1;
+    }
+    if (bad) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
+    // ---- the new rows' own keys and values ----
+    int issued16 = 0, issued_v16 = 0;
+    ok = __all_sync(0xffffffffu, ok);
+    if (lane == 0 && ok && n16 > 0) {
+      if (n8 > 0) ok = pt_wait(bar(C_QFREE), 0, &s_abort, limit);
+      for (int j = 0; ok && j < n16; ++j) {
+        const int sk = j & 1, i = n8 + j, sv = i & 1, row = first + (o0 + j) * kCtKeys;
+        if (j >= 2 && !pt_wait(bar(C_K2EMPTY + sk), (uint32_t)((j >> 1) - 1) & 1u, &s_abort, limit)) break;
+        mbar_expect_tx(bar(C_K2FULL + sk), Sh::tile16);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+          tma_3d(sb + Sh::off_k + (uint32_t)sk * Sh::tile16 + (uint32_t)x * Sh::half16, &tm_kn, 64 * x, g, row, bar(C_K2FULL + sk));
+        issued16 = j + 1;
+        if (i >= 2 && !pt_wait(bar(C_VHFREE + sv), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit)) break;
+        mbar_expect_tx(bar(C_VTMA + sv), Sh::tile16);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+          tma_3d(sb + Sh::off_v16 + (uint32_t)sv * Sh::tile16 + (uint32_t)x * Sh::half16, &tm_vn, 64 * x, g, row, bar(C_VTMA + sv));
+        issued_v16 = j + 1;
+      }
+    }
+    if (lane == 0) {  // no copy may be in flight when the block leaves
+      for (int j = max(0, issued_k - kCtStages8); j < issued_k; ++j)
+        ct_drain(bar(C_KFULL + j % kCtStages8), (uint32_t)(j / kCtStages8) & 1u);
+      for (int j = max(0, issued_v - 2); j < issued_v; ++j) ct_drain(bar(C_VFULL + (j & 1)), (uint32_t)(j >> 1) & 1u);
+      for (int j = max(0, issued16 - 2); j < issued16; ++j) ct_drain(bar(C_K2FULL + (j & 1)), (uint32_t)(j >> 1) & 1u);
+      // bf16 tiles of V: the k-th of a buffer is its k-th arrival
+      for (int j = max(0, issued_v16 - 2); j < issued_v16; ++j) {
+        const int sv = (n8 + j) & 1, first_j = (n8 & 1) == sv ? 0 : 1;
+        ct_drain(bar(C_VTMA + sv), (uint32_t)((j - first_j) >> 1) & 1u);
+      }
+    }
+  } else if (warp == kCtScoreWarp) {
+    // ---------------- score products ----------------
+    if (lane == 0) {
+      constexpr uint32_t i8 = pt_idesc(0, FMT == ET_KV_E4M3 ? 0 : 1, false, false, 128, kCtKeys);
+      constexpr uint32_t i16 = pt_idesc(1, 1, false, false, 128, kCtKeys);
+      int k[2] = {0, 0};
+      bool ok = true;
+      for (int i = 0; ok && i < n; ++i) {
+        const int j = i - n8, sk = i < n8 ? i % kCtStages8 : j & 1;
+        if (i < n8) {
+          ok = pt_wait(bar(C_KFULL + sk), (uint32_t)(i / kCtStages8) & 1u, &s_abort, limit);
+        } else {
+          if (j == 0 && n8 > 0) ok = pt_wait(bar(C_QFULL), 0, &s_abort, limit);
+          ok = ok && pt_wait(bar(C_K2FULL + sk), (uint32_t)(j >> 1) & 1u, &s_abort, limit);
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (!ok || !uses(w, i)) continue;
+          // S lies where P of the group's last tile was: that product has run
+          if (k[w] > 0 && !pt_wait(bar(C_PVDONE + w), (uint32_t)(k[w] - 1) & 1u, &s_abort, limit)) { ok = false; continue; }
+          tc_fence_after();
+          const uint32_t q = sb + Sh::off_q + (shared_rows ? 0u : (uint32_t)w * Sh::tile16), d = tmem + kCtColS + 128u * (uint32_t)w;
+          if (i < n8) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)  // the two terms of q one after the other
+              pt_mma_f8(d, desc8<D>(q + (kk / (D / 32)) * Sh::tile8 + (kk % (D / 32)) * 32),
+                        desc8<D>(sb + Sh::off_k + (uint32_t)sk * Sh::tile8 + (kk % (D / 32)) * 32), i8, kk > 0);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma(d, sw128_desc(q + (kk >> 2) * Sh::half16 + (kk & 3) * 32, 16, 1024),
+                     sw128_desc(sb + Sh::off_k + (uint32_t)sk * Sh::tile16 + (kk >> 2) * Sh::half16 + (kk & 3) * 32, 16, 1024),
+                     i16, kk > 0);
+          }
+          tc_commit(bar(C_SFULL + w));
+          ++k[w];
+        }
+        if (!ok) break;
+        if (i < n8 && i + kCtStages8 < n8) tc_commit(bar(C_KEMPTY + sk));
+        if (i >= n8 && j + 2 < n16) tc_commit(bar(C_K2EMPTY + sk));
+        if (i == n8 - 1 && n16 > 0) tc_commit(bar(C_QFREE));
+      }
+      // every product this thread issued has finished before TMEM is freed
+      tc_commit(bar(C_DRAIN));
+      ct_drain(bar(C_DRAIN), 0);
+    }
+  } else if (warp == kCtPvWarp) {
+    // ---------------- P.V products ----------------
+    if (lane == 0) {
+      constexpr uint32_t i8 = pt_idesc(0, 0, false, true, 128, D), i16 = pt_idesc(1, 1, false, true, 128, D);
+      int k[2] = {0, 0};
+      bool ok = true;
+      for (int i = 0; ok && i < n; ++i) {
+        ok = pt_wait(bar(C_VHFULL + (i & 1)), (uint32_t)(i >> 1) & 1u, &s_abort, limit);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (!ok || !uses(w, i)) continue;
+          if (!pt_wait(bar(C_PFULL + w), (uint32_t)k[w] & 1u, &s_abort, limit)) { ok = false; continue; }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kCtKeys / 16; ++kk)
+            tc_mma_ts(tmem + kCtColO + 128u * (uint32_t)w, tmem + kCtColS + 128u * (uint32_t)w + 8u * kk,
+                      sw128_desc(sb + Sh::off_v16 + (uint32_t)(i & 1) * Sh::tile16 + kk * 2048, Sh::half16, 1024),
+                      i < n8 ? i8 : i16, (k[w] > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(bar(C_PVDONE + w));
+          ++k[w];
+        }
+        if (!ok) break;
+        tc_commit(bar(C_VHFREE + (i & 1)));
+      }
+      tc_commit(bar(C_DRAIN + 1));
+      ct_drain(bar(C_DRAIN + 1), 0);
+    }
+  }
+  __syncwarp();
+  roles_end();
+  regs_up<128>();
+  } else if (warp >= 8) {
+    regs_down<64>();
+    // ---------------- V as the products take it ----------------
+    const int gt = t & 127;
+    bool ok = true;
+    for (int i = 0; i < n8; ++i) {
+      const int sv = i & 1;
+      ok = ok && pt_wait(bar(C_VFULL + sv), (uint32_t)(i >> 1) & 1u, &s_abort, limit);
+      if (ok && i >= 2) ok = pt_wait(bar(C_VHFREE + sv), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      const uint32_t units = *(volatile uint32_t *)&s_units[i % kCtSlots];
+      const int lim = L - (t0 + i) * kCtKeys;  // rows past it hold no key of this sequence
+      const bool whole = lim >= kCtKeys && units == 0xffu;
+      constexpr int C = D / 16, RP = 128 / C;  // 16-code chunks of a row; rows the threads take at once
+      const int c = gt % C, r0 = gt / C;
+      const uint32_t from = sb + Sh::off_v8 + (uint32_t)sv * Sh::tile8, to = sb + Sh::off_v16 + (uint32_t)sv * Sh::tile16;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        constexpr int K = kCtKeys / RP / 2;
+        uint4 v[K];
+#pragma unroll
+        for (int x = 0; x < K; ++x) {
+          const int r = r0 + RP * (K * half + x);
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[x].x), "=r"(v[x].y), "=r"(v[x].z), "=r"(v[x].w) : "r"(from + at8<D>(r, c)));
+          if (!whole && (r >= lim || !((units >> (r >> 4)) & 1u))) v[x] = make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int x = 0; x < K; ++x) {
+          const int r = r0 + RP * (K * half + x);
+          uint32_t h[8];
+          f8x4_to_f16<FMT>(v[x].x, h[0], h[1]);
+          f8x4_to_f16<FMT>(v[x].y, h[2], h[3]);
+          f8x4_to_f16<FMT>(v[x].z, h[4], h[5]);
+          f8x4_to_f16<FMT>(v[x].w, h[6], h[7]);
+          const uint32_t dst = to + (uint32_t)(c >> 2) * Sh::half16;
+          const int c0 = 2 * (c & 3), s = (c >> 2) ^ (r & 1);  // which of the two 16-byte chunks goes first
+          sts128(dst + sw128(r, c0 + s), s ? h[4] : h[0], s ? h[5] : h[1], s ? h[6] : h[2], s ? h[7] : h[3]);
+          sts128(dst + sw128(r, c0 + 1 - s), s ? h[0] : h[4], s ? h[1] : h[5], s ? h[2] : h[6], s ? h[3] : h[7]);
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(C_VEMPTY + sv));
+        mbar_arrive(bar(C_VHFULL + sv));
+      }
+    }
+    if (n16 > 0) {
+      if (ok && n8 > 0) {  // q as it is, once the prefix's score products have run
+        ok = __all_sync(0xffffffffu, pt_wait(bar(C_QFREE), 0, &s_abort, limit));
+        if (ok) {
+          stage_q16(0, gt);
+          if (!shared_rows) stage_q16(1, gt);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C_QFULL));
+        }
+      }
+      bool odd = false;
+      for (int j = 0; ok && j < n16; ++j) {
+        const int i = n8 + j, sv = i & 1, first_j = (n8 & 1) == sv ? 0 : 1;
+        ok = __all_sync(0xffffffffu, pt_wait(bar(C_VTMA + sv), (uint32_t)((j - first_j) >> 1) & 1u, &s_abort, limit));
+        if (!ok) break;
+        const int key0 = (o0 + j) * kCtKeys;
+        if (key0 + kCtKeys - 1 > tok_first) {
+          // some row does not see some key here: 0 * NaN must not reach it.  What is not finite is taken out and added
+          // to the rows that see it at the end; rows past the block's last token are nobody's
+          for (int x = gt; x < kCtKeys * (D / 8); x += 128) {
+            const int r = x / (D / 8), c = x % (D / 8);
+            const uint32_t at = sb + Sh::off_v16 + (uint32_t)sv * Sh::tile16 + (uint32_t)(c >> 3) * Sh::half16 + sw128(r, c & 7);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+            bool change = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; change = true; }
+              if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; change = true; }
+            }
+            if (change) sts128(at, w[0], w[1], w[2], w[3]);
+            odd = odd || (change && key0 + r <= tok_last);
+          }
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C_VHFULL + sv));
+      }
+      if (odd) s_odd = 1;
+    }
+    __syncwarp();
+    roles_end();
+    regs_up<128>();
+  } else {
+    regs_up<192>();
+    // ---------------- softmax: group w, a row per thread ----------------
+    const int w = warp >> 2, r = t & 127, Rr = shared_rows ? r : 128 * w + r;
+    const int tok = Rr < real ? ct_token(ca, R0 + Rr) : -1;  // rows that do not exist see nothing
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t sc = lanes + kCtColS + 128u * (uint32_t)w, oc = lanes + kCtColO + 128u * (uint32_t)w;
+    bool dead = false;
+    // the weights of one tile from its scores; `own`: the new rows' keys
+    auto tile = [&](int i, auto own_, auto masked_) {
+      constexpr bool own = decltype(own_)::value, masked = decltype(masked_)::value;
+      const int slot = i % kCtSlots;
+      int lim = 0;
+      uint32_t units = 0xffu;
+      if (masked) {
+        if (own) {
+          lim = tok - (o0 + i - n8) * kCtKeys + 1;
+        } else {
+          units = *(volatile uint32_t *)&s_units[slot];
+          lim = tok < 0 ? 0 : L - (t0 + i) * kCtKeys;
+        }
+      }
+      uint32_t raw[kCtKeys / 32][32];
+#pragma unroll
+      for (int p = 0; p < kCtKeys / 32; ++p) tmem_ld32(sc + 32u * p, raw[p]);
+      tmem_wait_ld();
+      float top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kCtKeys / 16; ++u) {
+        float ks = 1.f, lv = 0.f, iv;
+        if (!own) lds_f4(saddr(&s_scale[slot][u]), ks, lv, iv);
+        const float f = own ? f16 : f8 * ks, c = lv - ref;
+        const uint64_t f2 = pair(f, f), c2 = pair(c, c);
+        int limu = masked ? lim - 16 * u : 16;
+        if (masked && !own && !((units >> u) & 1u)) limu = 0;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          uint32_t *x = &raw[u >> 1][16 * (u & 1) + e];
+          float x0, x1;
+          unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), f2, c2), x0, x1);
+          if (masked) {
+            x0 = e < limu ? x0 : -INFINITY;
+            x1 = e + 1 < limu ? x1 : -INFINITY;
+          }
+          top = fmaxf(top, fmaxf(x0, x1));
+          x[0] = __float_as_uint(x0);
+          x[1] = __float_as_uint(x1);
+        }
+      }
+      const bool move = top > kPaTop + kPaSlack || (fresh && top > -INFINITY);
+      if (__any_sync(0xffffffffu, move)) {
+        const float now = move ? top + ref - kPaTop : ref, by = move ? ref - now : 0.f;
+        const float corr = fresh ? 0.f : ex2_fast(by);
+        if (move) {
+          l *= corr;
+          ref = now;
+        }
+#pragma unroll
+        for (int p = 0; p < kCtKeys / 32; ++p)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) raw[p][e] = __float_as_uint(__uint_as_float(raw[p][e]) + by);
+        if (items > 0) {  // O holds the sums of this group's earlier tiles
+          const float by_o = move ? corr : 1.f;
+#pragma unroll 1
+          for (int p = 0; p < D / 8; ++p) {
+            uint32_t o[8];
+            pt_ld8(oc + 8u * p, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by_o);
+            pt_st8(oc + 8u * p, o);
+          }
+        }
+        if (move) fresh = false;
+      }
+      uint64_t l2[2] = {0ull, 0ull};
+#pragma unroll
+      for (int p = 0; p < kCtKeys / 32; ++p) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float ks, lv, iv = 1.f;
+          if (!own) lds_f4(saddr(&s_scale[slot][2 * p + u]), ks, lv, iv);
+          const uint64_t iv2 = pair(iv, iv);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float w0 = ex2_fast(__uint_as_float(raw[p][16 * u + e])), w1 = ex2_fast(__uint_as_float(raw[p][16 * u + e + 1]));
+            l2[(e >> 1) & 1] = own ? add2(pair(w0, w1), l2[(e >> 1) & 1]) : fma2(pair(w0, w1), iv2, l2[(e >> 1) & 1]);
+            pk[8 * u + (e >> 1)] = own ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1);
+          }
+        }
+        tmem_st16(sc + 16u * p, pk);
+      }
+      float s0, s1;
+      unpair(add2(l2[0], l2[1]), s0, s1);
+      l += s0 + s1;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C_PFULL + w));
+      ++items;
+    };
+    for (int i = 0; i < n; ++i) {
+      if (!uses(w, i)) continue;
+      if (i < n8) dead = dead || !pt_wait(bar(C_SCALES + i % kCtSlots), (uint32_t)(i / kCtSlots) & 1u, &s_abort, limit);
+      dead = dead || !pt_wait(bar(C_SFULL + w), (uint32_t)items & 1u, &s_abort, limit);
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) break;
+      tc_fence_after();
+      if (i < n8) {
+        const bool whole = L - (t0 + i) * kCtKeys >= kCtKeys && *(volatile uint32_t *)&s_units[i % kCtSlots] == 0xffu;
+        if (whole) tile(i, std::false_type{}, std::false_type{});
+        else tile(i, std::false_type{}, std::true_type{});
+      } else {
+        const bool whole = (o0 + i - n8) * kCtKeys + kCtKeys - 1 <= ct_token(ca, R0 + (shared_rows ? 0 : 128 * w));
+        if (whole) tile(i, std::true_type{}, std::false_type{});
+        else tile(i, std::true_type{}, std::true_type{});
+      }
+    }
+    if (items && !dead) pt_wait(bar(C_PVDONE + w), (uint32_t)(items - 1) & 1u, &s_abort, limit);
+    __syncwarp();
+    regs_down<128>();
+    roles_end();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*(volatile int *)&s_abort != 0 && t == 0) flag_status(a.dev_status, ET_DEV_TIMEOUT);
+
+  // ---- the rows: one group's, or the two groups' halves of the keys joined ----
+  float *xo = reinterpret_cast<float *>(sm + Sh::off_q);                       // [D][128] of group 1
+  float2 *xm = reinterpret_cast<float2 *>(sm + Sh::off_v8);                    // [128]
+  const int w = warp >> 2, r = t & 127, Rr = shared_rows ? r : 128 * w + r;
+  const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCtColO + 128u * (uint32_t)w;
+  if (shared_rows && w == 1) {
+    xm[r] = make_float2(fresh ? -3e38f : ref, l);
+    if (items > 0) {
+#pragma unroll 1
+      for (int p = 0; p < D / 8; ++p) {
+        uint32_t o[8];
+        pt_ld8(lanes + 8u * p, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xo[(8 * p + e) * 128 + r] = __uint_as_float(o[e]);
+      }
+    } else {
+      for (int e = 0; e < D; ++e) xo[e * 128 + r] = 0.f;
+    }
+  }
+  __syncthreads();
+  const bool writes = warp < 8 && (w == 0 || !shared_rows);
+  if (writes) {
+    float M = fresh ? -3e38f : ref, mine = 1.f, other = 0.f;
+    if (shared_rows) {
+      const float2 y = xm[r];
+      const float both = fmaxf(M, y.x);
+      mine = ex2_fast(M - both);
+      other = ex2_fast(y.x - both);
+      l = fmaf(l, mine, y.y * other);
+      M = both;
+    }
+    const bool mine_any = items > 0;
+    const int R = R0 + Rr, i = ct_token(ca, R), h = g * a.G + (R - i * a.G);
+    const long long row = (long long)(first + i) * a.Hq + h;
+    const bool odd = s_odd != 0;
+    const long long slot = ((long long)unit * ca.S + part) * 256 + Rr;
+    if (parts == 1) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      mine *= inv;
+      other *= inv;
+      if (Rr < real && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+    } else if (Rr < real) {
+      ca.part_ml[slot] = make_float2(M, l);
+    }
+#pragma unroll 1
+    for (int p = 0; p < D / 16; ++p) {
+      uint32_t o[16];
+      pt_ld16(lanes + 16u * p, o);
+      tmem_wait_ld();
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = mine_any ? __uint_as_float(o[e]) * mine : 0.f;
+        if (shared_rows) x[e] = fmaf(xo[(16 * p + e) * 128 + r], other, x[e]);
+      }
+      if (odd && Rr < real) {
+        // values that are not finite, taken out of the tiles that not every row sees whole
+        const int from = max(tok_first / kCtKeys, o0) * kCtKeys, to = min(i, (o0 + n16) * kCtKeys - 1);
+#pragma unroll 1
+        for (int key = from; key <= to; ++key) {
+          const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.vt) + (long long)(first + key) * ca.c.vs + (long long)g * D + 16 * p;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float z = __bfloat162float(v[e]);
+            if (!(fabsf(z) <= FLT_MAX)) x[e] += z;
+          }
+        }
+      }
+      if (Rr < real) {
+        if (parts == 1) {
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + 16 * p);
+          dst[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+          dst[1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
+        } else {
+          float4 *dst = ca.part_o + slot * (D / 4) + 4 * p;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kCtScoreWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCtTmemCols) : "memory");
+  if (parts == 1) return;
+  // ---- the parts' rows, merged by the last block to arrive ----
+  if (!arrive_last(ca.cnt + unit, (unsigned)parts, &s_last)) return;
+  const long long base = (long long)unit * ca.S * 256;
+#pragma unroll 1
+  for (int x = t; x < real * (D / 4); x += kCtThreads) {
+    const int rr = x / (D / 4), c = x % (D / 4);
+    float M = -3e38f, sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(&ca.part_ml[base + k * 256 + rr]).x);
+    for (int k = 0; k < parts; ++k) {
+      const float2 e = __ldcg(&ca.part_ml[base + k * 256 + rr]);
+      const float4 y = __ldcg(&ca.part_o[(base + k * 256 + rr) * (D / 4) + c]);
+      const float f = ex2_fast(e.x - M);
+      sum = fmaf(e.y, f, sum);
+      v.x = fmaf(y.x, f, v.x); v.y = fmaf(y.y, f, v.y); v.z = fmaf(y.z, f, v.z); v.w = fmaf(y.w, f, v.w);
+    }
+    const int R = R0 + rr, i = ct_token(ca, R), h = g * a.G + (R - i * a.G);
+    const long long row = (long long)(first + i) * a.Hq + h;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + 4 * c) =
+        make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+    if (c == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+  }
+}
+
+// new keys or values: [rows][Hkv][D], rows `stride` elements apart; a box is 128 rows of 64 dims of one head
+bool make_new_map(CUtensorMap *m, const void *base, const ChunkArgs &c, int d, long long stride) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)c.a.Hkv, (cuuint64_t)c.rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t boxes[3] = {64, 1, kCtKeys};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxes, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int FMT>
+et_status launch_tc(const CUtensorMap (&m)[4], const ChunkTcArgs &ca, cudaStream_t st) {
+  if (et_smem_attr((const void *)k_chunk_tc<D, FMT>, (int)CtShape<D>::bytes) != cudaSuccess) return ET_ERR_CUDA;
+  const long long blocks = (long long)ca.tiles * ca.c.a.Hkv * ca.S;
+  return et_launch(k_chunk_tc<D, FMT>, dim3((unsigned)blocks), dim3(kCtThreads), CtShape<D>::bytes, st, 0, m[0], m[1], m[2],
+                   m[3], ca);
+}
+
+}  // namespace
+
+et_status chunk_tc_launch(const et_paged_cache *cache, const ChunkArgs &c, const ChunkTcPlan &p, void *ws, cudaStream_t st) {
+  if (!encode_fn()) return ET_ERR_CUDA;
+  ChunkTcArgs ca;
+  ca.c = c;
+  ca.S = p.S;
+  ca.tiles = p.tiles;
+  const int P = cache->page_size;
+  ca.box = P % 128 == 0 ? 128 : P % 64 == 0 ? 64 : P % 32 == 0 ? 32 : 16;
+  unsigned char *wsb = static_cast<unsigned char *>(ws);
+  ca.cnt = p.S > 1 ? reinterpret_cast<unsigned int *>(wsb) : nullptr;
+  ca.part_ml = p.S > 1 ? reinterpret_cast<float2 *>(wsb + p.ml_off) : nullptr;
+  ca.part_o = p.S > 1 ? reinterpret_cast<float4 *>(wsb + p.o_off) : nullptr;
+  const uint32_t units = (uint32_t)P / 16, G = (uint32_t)c.a.G;
+  ca.page_magic = units == 1 ? 0u : (uint32_t)(((1ull << 32) + units - 1) / units);
+  ca.group_shift = 0;
+  while ((2ull << ca.group_shift) < G) ++ca.group_shift;
+  ca.group_magic = G == 1 ? 0u : (uint32_t)(((1ull << (32 + ca.group_shift)) + G - 1) / G);
+  ca.wait_cycles = et_wait_limit_cycles();
+  CUtensorMap m[4];
+  if (!make_page_map(&m[0], cache->k_pages, cache, ca.box) || !make_page_map(&m[1], cache->v_pages, cache, ca.box) ||
+      !make_new_map(&m[2], c.a.kt, c, cache->d, c.ks) || !make_new_map(&m[3], c.a.vt, c, cache->d, c.vs))
+    return ET_ERR_INVALID_ARG;
+  const bool e4m3 = cache->format == ET_KV_E4M3;
+  if (cache->d == 64) return e4m3 ? launch_tc<64, ET_KV_E4M3>(m, ca, st) : launch_tc<64, ET_KV_E5M2>(m, ca, st);
+  return e4m3 ? launch_tc<128, ET_KV_E4M3>(m, ca, st) : launch_tc<128, ET_KV_E5M2>(m, ca, st);
+}
+
+}  // namespace et

@@ -13,6 +13,15 @@ struct ChunkArgs {
   const int32_t *row_start;
 };
 
+// bf16 (et_chunk_attention_tc.cu): blocks of 256 (token, head) rows of a KV head
+struct ChunkTcPlan {
+  int S;      // parts of a block's keys at most
+  int tiles;  // tiles of 256 rows per KV head at most
+  size_t ml_off, o_off;
+};
+ET_HIDDEN et_status chunk_tc_launch(const et_paged_cache *cache, const ChunkArgs &c, const ChunkTcPlan &p, void *ws,
+                                    cudaStream_t stream);
+
 namespace {
 
 // New rows of sequence b: first row and count; count 0 = nothing to do.
