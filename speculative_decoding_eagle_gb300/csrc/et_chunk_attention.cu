@@ -225,7 +225,19 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
   const long long room = (long long)s->max_blocks * c->page_size;
   const long long T = ((s->max_prefix < room ? s->max_prefix : room) + 127) / 128 + (s->max_rows + 127) / 128;
   long long S = s->num_splits;
-  if (S <= 0) S = sm_count() / units;
+  if (S <= 0) {
+    // A block costs about 14 of its tiles before its first and after its last, and a merge through the workspace six more
+    // (measured: 25000 cycles and 2000 a tile): parts pay where blocks are few and tiles many.  One block per SM
+    const long long sms = sm_count();
+    double best = 1e30;
+    for (long long k = 1; k <= 64 && k <= T; ++k) {
+      const double cost = (double)((units * k + sms - 1) / sms) * (14 + (double)((T + k - 1) / k) + (k > 1 ? 6 : 0));
+      if (cost < best) {
+        best = cost;
+        S = k;
+      }
+    }
+  }
   if (S > T) S = T;
   if (S > 64) S = 64;
   if (S < 1 || units > kChunkCounters) S = 1;

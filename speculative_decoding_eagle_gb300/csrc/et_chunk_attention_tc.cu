@@ -19,7 +19,7 @@
 //              group's products run under the other's softmax either way
 //   warps 8-11 turn V's codes into fp16, stage q, and clear what no row of
 //              the block may see from the new rows' V
-//   warp 12    TMA;  warp 13 issues the score products, warp 14 those of P.V
+//   warps 12, 15  TMA for K (with the scales) and for V;  warp 13 issues the score products, warp 14 those of P.V
 // The prefix comes first.  A weight's reference moves only when some weight
 // would pass 2^15; a row is a thread's own, so nothing but the warp has to
 // agree.  A cached key's weight carries its page's V scale and is rounded to
@@ -39,8 +39,9 @@ namespace {
 
 constexpr int kCtThreads = 512;
 constexpr int kCtKeys = 128;                          // keys per tile
-constexpr int kCtTmaWarp = 12, kCtScoreWarp = 13, kCtPvWarp = 14;
+constexpr int kCtTmaWarp = 12, kCtScoreWarp = 13, kCtPvWarp = 14, kCtTmaVWarp = 15;
 constexpr int kCtStages8 = 4, kCtStages16 = 2;        // K ring: stages of codes, or of bf16 rows, in one space
+constexpr int kCtOrdered = 32;                        // sequences up to which a batch goes out by length
 constexpr int kCtSlots = 8;                           // tiles whose scales are kept
 constexpr uint32_t kCtColS = 0, kCtColO = 256, kCtTmemCols = 512;  // S / P of the two groups, O of the two groups
 
@@ -63,14 +64,15 @@ enum {
   C_KEMPTY = C_KFULL + kCtStages8,
   C_K2FULL = C_KEMPTY + kCtStages8,   // two stages of bf16 keys
   C_K2EMPTY = C_K2FULL + kCtStages16,
-  C_VFULL = C_K2EMPTY + kCtStages16,  // V's codes
-  C_VEMPTY = C_VFULL + 2,
-  C_VTMA = C_VEMPTY + 2,              // bf16 V has landed
+  C_VFULL = C_K2EMPTY + kCtStages16,  // V's codes, two stages or four
+  C_VEMPTY = C_VFULL + 4,
+  C_VTMA = C_VEMPTY + 4,              // bf16 V has landed
   C_VHFULL = C_VTMA + 2,              // V as the products take it
   C_VHFREE = C_VHFULL + 2,
   C_SFULL = C_VHFREE + 2,             // per group from here on
   C_PFULL = C_SFULL + 2,
-  C_PVDONE = C_PFULL + 2,
+  C_PHALF = C_PFULL + 2,
+  C_PVDONE = C_PHALF + 2,
   C_QFREE = C_PVDONE + 2,             // the prefix's score products have run: q and the K ring are free
   C_QFULL = C_QFREE + 1,              // q in bf16
   C_SCALES = C_QFULL + 1,             // eight slots: a tile's scales are there
@@ -105,6 +107,39 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
+// One lane of a converged warp.  Products are issued from control flow that the whole warp shares, under this predicate:
+// their descriptors then stay in uniform registers (a product of 128 x 128 x 16 every 64 cycles; 130 to 160 from a loop that
+// one lane alone runs)
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0u;
+}
+// Products and commits by the one lane whose `lead` is set, without a branch: the operands stay in uniform registers
+__device__ __forceinline__ void ct_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void ct_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void ct_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void ct_commit(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(lead)
+      : "memory");
+}
 struct ChunkTcArgs {
   ChunkArgs c;
   int S;                 // parts of a block's tiles at most
@@ -132,105 +167,115 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   using Sh = CtShape<D>;
   const PagedAttnArgs &a = ca.c.a;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ int s_abort, s_last, s_odd, s_seq, s_tile, s_longest;
+  __shared__ int s_abort, s_last, s_odd, s_seq, s_tile, s_longest, s_first, s_rows, s_prefix;
   __shared__ int s_red[kCtThreads / 32], s_len[kCtThreads / 32];
+  __shared__ int2 s_seqs[kCtOrdered];
   __shared__ uint32_t s_tmem, s_units[kCtSlots];
   __shared__ __align__(16) float4 s_scale[kCtSlots][kCtKeys / 16];  // a unit's K scale, log2 of its V scale, the inverse of that
   unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = saddr(sm);
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
   auto bar = [&](int i) -> uint32_t { return sb + Sh::off_bar + 8u * (uint32_t)i; };
 
   // ---- set-up that touches no global memory ----
-  if (t == 0) {
+  if (t < C_COUNT) {
+    const bool warps = (t >= C_VEMPTY && t < C_VTMA) || (t >= C_VHFULL && t < C_VHFREE) || (t >= C_PFULL && t < C_PVDONE) || t == C_QFULL;
+    mbar_init(bar(t), warps ? 4u : 1u);  // the warps of a group, or one
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (t == C_COUNT) {
     s_abort = 0;
     s_odd = 0;
     s_seq = -1;
-    s_tile = 0;
     s_longest = 0;
-    for (int i = 0; i < C_COUNT; ++i) {
-      int count = 1;
-      if ((i >= C_VEMPTY && i < C_VTMA) || (i >= C_VHFULL && i < C_VHFREE) || (i >= C_PFULL && i < C_PVDONE) || i == C_QFULL)
-        count = 4;  // the warps of a group
-      mbar_init(bar(i), (uint32_t)count);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
-    prefetch_tmap(&tm_kn);
-    prefetch_tmap(&tm_vn);
+  } else if (warp == 3 && lane < 4) {
+    prefetch_tmap(lane == 0 ? &tm_k : lane == 1 ? &tm_v : lane == 2 ? &tm_kn : &tm_vn);
   }
   __syncthreads();
   pdl_wait();  // the previous kernel in the stream has completed
 
   // ---- which rows: tile `index` of the batch's tiles of 256 rows, in the sequences' order ----
   const int part = blockIdx.x % ca.S, unit = blockIdx.x / ca.S;
-  const int g = unit / ca.tiles, index = unit - g * ca.tiles;
+  const int index = unit / a.Hkv, g = unit - index * a.Hkv;
   int bad = 0;
   {
+    // Sequences of the most keys go out first (ties: lower index), as far as one round of threads ranks them: a block that
+    // starts last should not be the longest.  Larger batches keep their order
     int done = 0;  // tiles of the sequences before this round's
     for (int b0 = 0; b0 < a.B; b0 += kCtThreads) {
       const int b = b0 + t;
-      int mine = 0, keys = 0;
+      int mine = 0, keys = 0, first = 0, n = 0, L = -1;
       if (b < a.B) {
-        int first, n, ignore = 0;
+        int ignore = 0;
         chunk_rows(ca.c, b, first, n, ignore);
-        const int L = paged_prefix(a, b, ignore);
+        L = paged_prefix(a, b, ignore);
         if (ignore && blockIdx.x == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
         if (L >= 0 && n > 0) {
           mine = (int)(((long long)n * a.G + 255) >> 8);
           keys = tiles_of(L, kCtKeys) + tiles_of(n, kCtKeys);
         }
       }
-      int incl = mine;
+      const int longest_here = __reduce_max_sync(0xffffffffu, keys);
+      if (lane == 0) s_len[warp] = longest_here;
+      int before = done;
+      if (a.B <= kCtOrdered) {
+        if (t < kCtOrdered) s_seqs[t] = make_int2(keys, mine);
+        __syncthreads();
+        if (b < a.B)
+          for (int c = 0; c < a.B; ++c) {
+            const int2 o = s_seqs[c];
+            if (o.x > keys || (o.x == keys && c < b)) before += o.y;
+          }
+      } else {
+        int incl = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (lane == 31) s_red[warp] = incl;
+        __syncthreads();
+        int all = done;
+        for (int w = 0; w < kCtThreads / 32; ++w) {
+          if (w < warp) before += s_red[w];
+          all += s_red[w];
+        }
+        before += incl - mine;
+        done = all;
       }
-      keys = __reduce_max_sync(0xffffffffu, keys);
-      if (lane == 31) s_red[warp] = incl;
-      if (lane == 0) s_len[warp] = keys;
-      __syncthreads();
-      int before = done, all = done, longest = 0;
-      for (int w = 0; w < kCtThreads / 32; ++w) {
-        if (w < warp) before += s_red[w];
-        all += s_red[w];
-        longest = max(longest, s_len[w]);
-      }
-      before += incl - mine;
       if (before <= index && index < before + mine) {
         s_seq = b;
         s_tile = index - before;
+        s_first = first;
+        s_rows = n;
+        s_prefix = L;
       }
-      if (t == 0) s_longest = max(s_longest, longest);
-      done = all;
+      if (t == 0)
+        for (int w = 0; w < kCtThreads / 32; ++w) s_longest = max(s_longest, s_len[w]);
       __syncthreads();
     }
   }
+  auto uni = [](int x) -> int { return __shfl_sync(0xffffffffu, x, 0); };  // the same in every lane, and known to be so
   const int b = s_seq;
   if (b < 0) return;  // fewer tiles than the grid has places for
-  int first, nrows;
-  chunk_rows(ca.c, b, first, nrows, bad);
-  const int L = paged_prefix(a, b, bad);
+  const int first = s_first, nrows = s_rows, L = s_prefix;
   // the last tiles have the most keys: they go out first
   const long long all_rows = (long long)nrows * a.G;
   const int row_tiles = (int)((all_rows + 255) >> 8);
   const int R0 = (row_tiles - 1 - s_tile) << 8;                    // first row of the KV head's (token, head) rows
   const int real = (int)min(256ll, all_rows - R0);
-  const bool shared_rows = real <= 128;                            // both groups have the same rows
+  const bool shared_rows = uni(real <= 128) != 0;                            // both groups have the same rows
   const int tok_first = ct_token(ca, R0), tok_last = ct_token(ca, R0 + real - 1);
   const int Tp = tiles_of(L, kCtKeys), To = tok_last / kCtKeys + 1, T = Tp + To;
   const int per = max((s_longest + ca.S - 1) / ca.S, 1);
   const int parts = (T + per - 1) / per;
   if (part >= parts) return;
   const int t0 = part * per, t1 = min(T, t0 + per);
-  const int n8 = max(0, min(t1, Tp) - t0);                         // tiles of the prefix
-  const int o0 = max(t0 - Tp, 0), n16 = max(0, t1 - Tp - o0);      // tiles of the new rows: o0 .. o0 + n16 - 1
+  const int n8 = uni(max(0, min(t1, Tp) - t0));                         // tiles of the prefix
+  const int o0 = uni(max(t0 - Tp, 0)), n16 = uni(max(0, t1 - Tp - o0));      // tiles of the new rows: o0 .. o0 + n16 - 1
   const int n = n8 + n16;
   // tiles that group 0 needs: its last row sees fewer of the new rows
   const int To0 = shared_rows ? To : ct_token(ca, R0 + 127) / kCtKeys + 1;
-  const int n_first = shared_rows ? n : n8 + max(0, min(n16, To0 - o0));
+  const int n_first = uni(shared_rows ? n : n8 + max(0, min(n16, To0 - o0)));
   if (warp == kCtScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&s_tmem)), "r"(kCtTmemCols)
                  : "memory");
@@ -239,82 +284,188 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   // users of tile i: group 0 and 1, or i & 1
   auto uses = [&](int w, int i) -> bool { return shared_rows ? (i & 1) == w : (w == 1 || i < n_first); };
 
-  // ---- q: a thread per row; two e4m3 terms for the prefix, else bf16 at once ----
+  // ---- TMA: the prefix's tiles, K four ahead of its products, V two ahead of its conversion; four where the groups share
+  // their rows, in the room of the second group's q (each byte is then used once, and what is in flight bounds the rate) ----
+  const int v_stages = shared_rows ? 4 : 2;
+  auto v8_at = [&](int stage) -> uint32_t {
+    return sb + (stage < 2 ? Sh::off_v8 + (uint32_t)stage * Sh::tile8 : Sh::off_q + Sh::tile16 + (uint32_t)(stage - 2) * Sh::tile8);
+  };
+  // lane: unit (lane & 7) of tile 4 * (j / 4) + (lane >> 3), 16 keys a unit; pages and scales of the four tiles that come
+  // next (n) are in flight ahead
+  int pg = -1, sl = 0, pg_n = -1, sl_n = 0;
+  float ks = 0.f, vs = 1.f, ks_n = 0.f, vs_n = 1.f;
+  auto unit_key = [&](int j0) -> long long {
+    const int j = j0 + (lane >> 3);
+    const long long key = (long long)(t0 + j) * kCtKeys + 16 * (lane & 7);
+    return j < n8 && key < L ? key : -1;
+  };
+  auto fetch_pages = [&](int j0, int &page, int &slot) {
+    const int key = (int)unit_key(j0);
+    page = -1;
+    if (key >= 0) {
+      const int blk = ct_page_index(ca, key);
+      slot = key - blk * a.P;
+      page = a.block_table[(long long)b * a.max_blocks + blk];
+    }
+  };
+  auto fetch_scales = [&](int j0, int &page, float &k, float &v, bool scales) {
+    if (page < 0 || page >= a.num_pages) {
+      if (unit_key(j0) >= 0) bad = 1;
+      page = -1;
+    }
+    k = 0.f;
+    v = 1.f;
+    if (scales && page >= 0) {
+      k = a.k_scale[(long long)page * a.Hkv + g];
+      v = a.v_scale[(long long)page * a.Hkv + g];
+    }
+  };
+  const int per_box = ca.box / 16;
+  // the boxes of tile j into a stage
+  auto load8 = [&](int j, const CUtensorMap *map, uint32_t dst, uint32_t full) {
+    const int src = 8 * (j & 3) + (lane & 7);
+    const int page = __shfl_sync(0xffffffffu, pg, src), slot = __shfl_sync(0xffffffffu, sl, src);
+    const uint32_t mine = __ballot_sync(0xffffffffu, lane < 8 && lane % per_box == 0 && page >= 0);
+    const uint32_t bytes = (uint32_t)__popc(mine) * (uint32_t)ca.box * D;
+    if (lane == 0) {
+      if (bytes) mbar_expect_tx(full, bytes);
+      else mbar_arrive(full);
+    }
+    __syncwarp();
+    if ((mine >> lane) & 1u) tma_4d(dst + (uint32_t)(lane * 16 * D), map, 0, slot, g, page, full);
+  };
+  auto load_k8 = [&](int j) {
+    // the scales' slot was last read for tile j - 8, whose softmax is past: tile j - 4's scores have run
+    const int src = 8 * (j & 3) + (lane & 7), sk = j % kCtStages8;
+    const int page = __shfl_sync(0xffffffffu, pg, src);
+    const float k = __shfl_sync(0xffffffffu, ks, src), v = clamp_v_scale(__shfl_sync(0xffffffffu, vs, src));
+    const uint32_t there = __ballot_sync(0xffffffffu, lane < 8 && page >= 0);
+    if (lane < 8) s_scale[j % kCtSlots][lane] = make_float4(k, __log2f(v), __fdividef(1.f, v), 0.f);
+    if (lane == 0) s_units[j % kCtSlots] = there;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C_SCALES + j % kCtSlots));
+    load8(j, &tm_k, sb + Sh::off_k + (uint32_t)sk * Sh::tile8, bar(C_KFULL + sk));
+  };
+  auto load_v8 = [&](int j) {
+    const int sv = j & (v_stages - 1);
+    load8(j, &tm_v, v8_at(sv), bar(C_VFULL + sv));
+  };
+  // pages of the next tiles, as tile j comes up
+  auto turn_pages = [&](int j, bool scales) {
+    if ((j & 3) == 0) {
+      if (j > 0) {
+        pg = pg_n; sl = sl_n; ks = ks_n; vs = vs_n;
+      }
+      fetch_pages(j + 4, pg_n, sl_n);
+    }
+    if ((j & 3) == 2) fetch_scales(j + 2, pg_n, ks_n, vs_n, scales);
+  };
+  auto load16 = [&](int j, bool is_v) {  // one lane; tile j of the new rows
+    const int sv = is_v ? (n8 + j) & 1 : j & 1, row = first + (o0 + j) * kCtKeys;
+    const uint32_t full = bar((is_v ? C_VTMA : C_K2FULL) + sv), dst = sb + (is_v ? Sh::off_v16 : Sh::off_k) + (uint32_t)sv * Sh::tile16;
+    mbar_expect_tx(full, Sh::tile16);
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) tma_3d(dst + (uint32_t)x * Sh::half16, is_v ? &tm_vn : &tm_kn, 64 * x, g, row, full);
+  };
+
+  // ---- q: D / 8 lanes a row; two e4m3 terms for the prefix, else bf16 at once ----
   const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q);
   auto q_row = [&](int r) -> const __nv_bfloat16 * {  // row r of the block; null past the last
     if (r >= real) return nullptr;
     const int R = R0 + r, i = ct_token(ca, R), h = g * a.G + (R - i * a.G);
     return Q + (long long)(first + i) * ca.c.qs + (long long)h * D;
   };
-  auto stage_q16 = [&](int w, int r) {  // row r of group w's tile
-    const __nv_bfloat16 *src = q_row(shared_rows ? r : 128 * w + r);
-    const uint32_t dst = sb + Sh::off_q + (uint32_t)w * Sh::tile16;
-#pragma unroll
-    for (int c0 = 0; c0 < D / 8; c0 += 8) {
-      uint4 v[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = src ? reinterpret_cast<const uint4 *>(src)[c0 + c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) sts128(dst + (uint32_t)(c0 >> 3) * Sh::half16 + sw128(r, c), v[c].x, v[c].y, v[c].z, v[c].w);
+  constexpr int kLanes = D / 8;  // of a row, eight dims each
+  const int qrows = shared_rows ? 128 : 256;
+  float *row_f = reinterpret_cast<float *>(sm + Sh::off_v8 + Sh::tile8);  // [256], read before V's second stage is loaded
+  if (warp < kCtTmaWarp) {
+    // The rows come by asynchronous copies to where V's fp16 tiles will be (bf16 rows to their place), each thread then takes what it copied
+    constexpr int count = kCtTmaWarp * 32;
+    auto place16 = [&](int x) -> uint32_t {
+      const int r = x / kLanes, c = x % kLanes;
+      return sb + Sh::off_q + (uint32_t)(r >> 7) * Sh::tile16 + (uint32_t)(c >> 3) * Sh::half16 + sw128(r & 127, c & 7);
+    };
+#pragma unroll 4
+    for (int x = t; x < qrows * kLanes; x += count) {
+      const uint32_t dst = n8 > 0 ? sb + Sh::off_v16 + 16u * (uint32_t)x : place16(x);
+      const __nv_bfloat16 *src = q_row(x / kLanes);
+      if (src) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + 8 * (x % kLanes)) : "memory");
+      else sts128(dst, 0u, 0u, 0u, 0u);
     }
-  };
-  float f8 = 0.f, f16 = a.scale_log2;  // what a score of lifted q and codes, or of bf16 values, stands for in log2 units
-  if (warp < 8) {
-    const int w = warp >> 2, r = t & 127;
-    const __nv_bfloat16 *src = q_row(shared_rows ? r : 128 * w + r);
-    uint32_t top = 0u;  // the row's largest magnitude, as the bits of a bf16 value: they order like the values
-    if (src) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    constexpr int U = 4;
+#pragma unroll 1
+    for (int x0 = t; x0 < qrows * kLanes; x0 += U * count) {
+      uint32_t w[U][4], top[U];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = reinterpret_cast<const uint4 *>(src)[c];
-        const uint32_t x = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-        top = max(top, max(x & 0xffffu, x >> 16));
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + u * count < qrows * kLanes ? x0 + u * count : t;  // past the end: its first one again
+        const uint32_t at = n8 > 0 ? sb + Sh::off_v16 + 16u * (uint32_t)x : place16(x);
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3]) : "r"(at) : "memory");
       }
-    }
-    const bool odd = top >= 0x7f80u;  // NaN or infinity: the row scores NaN
-    // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8; half of e2 stays within fp32's exponents
-    const int e2 = top == 0u || odd ? 0 : 135 - max((int)(top >> 7), 1) - ((top & 0x7fu) > 0x60u ? 1 : 0);
-    const int ea = e2 >> 1, eb = e2 - ea;
-    f8 = a.scale_log2 * power_of_two(-ea) * power_of_two(-eb);
-    if (odd) f8 = f16 = __uint_as_float(0x7fc00000u);
-    if (n8 > 0 && (w == 0 || !shared_rows)) {
-      const float lift_a = power_of_two(ea), lift_b = power_of_two(eb);
-      const uint32_t dst = sb + Sh::off_q + (uint32_t)w * Sh::tile16;
+      // the row's largest magnitude, as the bits of a bf16 value: they order like the values
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t hi[4], lo[4], x[8];
+      for (int u = 0; u < U; ++u) {
+        const uint32_t m = __vmaxu2(__vmaxu2(w[u][0] & 0x7fff7fffu, w[u][1] & 0x7fff7fffu), __vmaxu2(w[u][2] & 0x7fff7fffu, w[u][3] & 0x7fff7fffu));
+        top[u] = max(m & 0xffffu, m >> 16);
+      }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint4 v = src ? reinterpret_cast<const uint4 *>(src)[2 * c + e] : make_uint4(0u, 0u, 0u, 0u);
-          x[4 * e] = v.x; x[4 * e + 1] = v.y; x[4 * e + 2] = v.z; x[4 * e + 3] = v.w;
-        }
+      for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o, kLanes));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + u * count, r = x / kLanes, c = x % kLanes;
+        if (x >= qrows * kLanes) break;
+        const bool odd = top[u] >= 0x7f80u;  // NaN or infinity: the row scores NaN
+        // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8; half of e2 stays within fp32's exponents
+        const int e2 = top[u] == 0u || odd ? 0 : 135 - max((int)(top[u] >> 7), 1) - ((top[u] & 0x7fu) > 0x60u ? 1 : 0);
+        const int ea = e2 >> 1, eb = e2 - ea;
+        if (c == 0) row_f[r] = odd ? __uint_as_float(0x7fc00000u) : a.scale_log2 * power_of_two(-ea) * power_of_two(-eb);
+        if (n8 == 0) continue;
+        const float lift_a = power_of_two(ea), lift_b = power_of_two(eb);
+        uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          hi[e] = lo[e] = 0u;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float y0 = __uint_as_float(x[2 * e + k] << 16) * lift_a * lift_b;
-            const float y1 = __uint_as_float(x[2 * e + k] & 0xffff0000u) * lift_a * lift_b;
-            const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1), hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
-            const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
-            hi[e] |= h2 << (16 * k);
-            lo[e] |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (16 * k);
-          }
+          const float y0 = __uint_as_float(w[u][e] << 16) * lift_a * lift_b, y1 = __uint_as_float(w[u][e] & 0xffff0000u) * lift_a * lift_b;
+          const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1), hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
+          const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
+          hi[e >> 1] |= h2 << (16 * (e & 1));
+          lo[e >> 1] |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (16 * (e & 1));
         }
-        sts128(dst + at8<D>(r, c), hi[0], hi[1], hi[2], hi[3]);
-        sts128(dst + Sh::tile8 + at8<D>(r, c), lo[0], lo[1], lo[2], lo[3]);
+        unsigned char *d8 = sm + Sh::off_q + (uint32_t)(r >> 7) * Sh::tile16 + at8<D>(r & 127, c >> 1) + 8 * (c & 1);
+        *reinterpret_cast<uint2 *>(d8) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2 *>(d8 + Sh::tile8) = make_uint2(lo[0], lo[1]);
       }
-    } else if (n8 == 0 && (w == 0 || !shared_rows)) {
-      stage_q16(w, r);
+    }
+  } else if (warp == kCtTmaWarp || warp == kCtTmaVWarp) {  // the first tiles, while q is staged
+    const bool is_v = warp == kCtTmaVWarp;
+    if (n8 > 0) {
+      fetch_pages(0, pg, sl);
+      fetch_scales(0, pg, ks, vs, !is_v);
+      for (int j = 0; j < n8 && j < (is_v ? 1 : kCtStages8); ++j) {
+        turn_pages(j, !is_v);
+        if (is_v) load_v8(j);
+        else load_k8(j);
+      }
+    } else if (lane == 0) {
+      for (int j = 0; j < n16 && j < 2; ++j) load16(j, is_v);
     }
   }
   fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  float f8 = 0.f, f16 = a.scale_log2;  // what a score of lifted q and codes, or of bf16 values, stands for in log2 units
+  if (warp < 8) {
+    f8 = row_f[shared_rows ? t & 127 : t];
+    if (f8 != f8) f16 = f8;
+  }
+  __syncthreads();  // the factors have been read
   pdl_trigger();  // after the TMEM allocation: a waiting dependent block must not hold what this block needs
-  const uint32_t tmem = s_tmem;
   const long long limit = ca.wait_cycles;
+  const uint32_t tmem = (uint32_t)uni((int)s_tmem);
+  const uint32_t lead = elect_lane() ? 1u : 0u;
   float l = 0.f, ref = 0.f;   // a softmax thread's row: sum of weights, reference
   bool fresh = true;          // no key seen yet
   int items = 0;              // tiles this group has taken
@@ -323,117 +474,64 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   if (warp >= kCtTmaWarp) {
   regs_down<64>();
   if (warp == kCtTmaWarp) {
-    // ---------------- TMA: tile j of the prefix into stage j & 3 (K) and j & 1 (V) ----------------
-    // lane: unit (lane & 7) of tile 4 * (j / 4) + (lane >> 3), 16 keys a unit; the next four tiles' (_n) in flight ahead
-    int page = -1, slot = 0, page_n = -1, slot_n = 0;
-    float ks = 0.f, vs = 1.f, ks_n = 0.f, vs_n = 1.f;
-    auto unit_key = [&](int j0) -> long long {
-      const int j = j0 + (lane >> 3);
-      const long long key = (long long)(t0 + j) * kCtKeys + 16 * (lane & 7);
-      return j < n8 && key < L ? key : -1;
-    };
-    auto fetch_pages = [&](int j0, int &pg, int &sl) {
-      const int key = (int)unit_key(j0);
-      pg = -1;
-      if (key >= 0) {
-        const int blk = ct_page_index(ca, key);
-        sl = key - blk * a.P;
-        pg = a.block_table[(long long)b * a.max_blocks + blk];
-      }
-    };
-    auto fetch_scales = [&](int j0, int &pg, float &k, float &v) {
-      if (pg < 0 || pg >= a.num_pages) {
-        if (unit_key(j0) >= 0) bad = 1;
-        pg = -1;
-      }
-      k = 0.f;
-      v = 1.f;
-      if (pg >= 0) {
-        k = a.k_scale[(long long)pg * a.Hkv + g];
-        v = a.v_scale[(long long)pg * a.Hkv + g];
-      }
-    };
-    const int per_box = ca.box / 16;
+    // ---------------- TMA: K ----------------
     bool ok = true;
-    int issued_k = 0, issued_v = 0;
-    fetch_pages(0, page, slot);
-    fetch_scales(0, page, ks, vs);
-    fetch_pages(4, page_n, slot_n);
-    for (int j = 0; j < n8; ++j) {
-      if ((j & 3) == 2) fetch_scales(j + 2, page_n, ks_n, vs_n);
-      if ((j & 3) == 0 && j > 0) {
-        page = page_n; slot = slot_n; ks = ks_n; vs = vs_n;
-        fetch_pages(j + 4, page_n, slot_n);
-      }
-      const int src = 8 * (j & 3) + (lane & 7);
-      const int pg = __shfl_sync(0xffffffffu, page, src), sl = __shfl_sync(0xffffffffu, slot, src);
-      const float k = __shfl_sync(0xffffffffu, ks, src), v = clamp_v_scale(__shfl_sync(0xffffffffu, vs, src));
-      const uint32_t there = __ballot_sync(0xffffffffu, lane < 8 && pg >= 0);
-      const uint32_t mine = __ballot_sync(0xffffffffu, lane < 8 && lane % per_box == 0 && pg >= 0);
-      const uint32_t bytes = (uint32_t)__popc(mine) * (uint32_t)ca.box * D;
-      const int sk = j % kCtStages8, sv = j & 1;
-      if (j >= kCtStages8) ok = pt_wait(bar(C_KEMPTY + sk), (uint32_t)(j / kCtStages8 - 1) & 1u, &s_abort, limit);
+    int issued = min(n8, kCtStages8), issued16 = n8 == 0 ? min(n16, 2) : 0;
+    for (int j = issued; j < n8; ++j) {
+      turn_pages(j, true);
+      ok = pt_wait(bar(C_KEMPTY + j % kCtStages8), (uint32_t)(j / kCtStages8 - 1) & 1u, &s_abort, limit);
       if (!__all_sync(0xffffffffu, ok)) break;
-      // the scales' slot was last read for tile j - 8, whose softmax is past: tile j - 4's scores have run
-      if (lane < 8) s_scale[j % kCtSlots][lane] = make_float4(k, __log2f(v), __fdividef(1.f, v), 0.f);
-      if (lane == 0) s_units[j % kCtSlots] = there;
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(C_SCALES + j % kCtSlots));
-        if (bytes) mbar_expect_tx(bar(C_KFULL + sk), bytes);
-        else mbar_arrive(bar(C_KFULL + sk));
-      }
-      __syncwarp();
-      if ((mine >> lane) & 1u)
-        tma_4d(sb + Sh::off_k + (uint32_t)sk * Sh::tile8 + (uint32_t)(lane * 16 * D), &tm_k, 0, sl, g, pg, bar(C_KFULL + sk));
-      issued_k = j + 1;
-      if (j >= 2) ok = pt_wait(bar(C_VEMPTY + sv), (uint32_t)((j >> 1) - 1) & 1u, &s_abort, limit);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) {
-        if (bytes) mbar_expect_tx(bar(C_VFULL + sv), bytes);
-        else mbar_arrive(bar(C_VFULL + sv));
-      }
-      __syncwarp();
-      if ((mine >> lane) & 1u)
-        tma_4d(sb + Sh::off_v8 + (uint32_t)sv * Sh::tile8 + (uint32_t)(lane * 16 * D), &tm_v, 0, sl, g, pg, bar(C_VFULL + sv));
-      issued_v = j + 1;
+      load_k8(j);
+      issued = j + 1;
     }
     if (bad) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
-    // ---- the new rows' own keys and values ----
-    int issued16 = 0, issued_v16 = 0;
     ok = __all_sync(0xffffffffu, ok);
-    if (lane == 0 && ok && n16 > 0) {
-      if (n8 > 0) ok = pt_wait(bar(C_QFREE), 0, &s_abort, limit);
-      for (int j = 0; ok && j < n16; ++j) {
-        const int sk = j & 1, i = n8 + j, sv = i & 1, row = first + (o0 + j) * kCtKeys;
-        if (j >= 2 && !pt_wait(bar(C_K2EMPTY + sk), (uint32_t)((j >> 1) - 1) & 1u, &s_abort, limit)) break;
-        mbar_expect_tx(bar(C_K2FULL + sk), Sh::tile16);
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-          tma_3d(sb + Sh::off_k + (uint32_t)sk * Sh::tile16 + (uint32_t)x * Sh::half16, &tm_kn, 64 * x, g, row, bar(C_K2FULL + sk));
+    if (lane == 0) {
+      if (n8 > 0 && n16 > 0) ok = ok && pt_wait(bar(C_QFREE), 0, &s_abort, limit);
+      for (int j = issued16; ok && j < n16; ++j) {
+        if (j >= 2 && !pt_wait(bar(C_K2EMPTY + (j & 1)), (uint32_t)((j >> 1) - 1) & 1u, &s_abort, limit)) break;
+        load16(j, false);
         issued16 = j + 1;
-        if (i >= 2 && !pt_wait(bar(C_VHFREE + sv), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit)) break;
-        mbar_expect_tx(bar(C_VTMA + sv), Sh::tile16);
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-          tma_3d(sb + Sh::off_v16 + (uint32_t)sv * Sh::tile16 + (uint32_t)x * Sh::half16, &tm_vn, 64 * x, g, row, bar(C_VTMA + sv));
-        issued_v16 = j + 1;
       }
-    }
-    if (lane == 0) {  // no copy may be in flight when the block leaves
-      for (int j = max(0, issued_k - kCtStages8); j < issued_k; ++j)
+      // no copy may be in flight when the block leaves
+      for (int j = max(0, issued - kCtStages8); j < issued; ++j)
         ct_drain(bar(C_KFULL + j % kCtStages8), (uint32_t)(j / kCtStages8) & 1u);
-      for (int j = max(0, issued_v - 2); j < issued_v; ++j) ct_drain(bar(C_VFULL + (j & 1)), (uint32_t)(j >> 1) & 1u);
       for (int j = max(0, issued16 - 2); j < issued16; ++j) ct_drain(bar(C_K2FULL + (j & 1)), (uint32_t)(j >> 1) & 1u);
+    }
+  } else if (warp == kCtTmaVWarp) {
+    // ---------------- TMA: V ----------------
+    bool ok = true;
+    int issued = min(n8, 1), issued16 = n8 == 0 ? min(n16, 2) : 0;
+    for (int j = issued; j < n8; ++j) {
+      turn_pages(j, false);
+      if (j >= v_stages)
+        ok = pt_wait(bar(C_VEMPTY + (j & (v_stages - 1))), (uint32_t)(j / v_stages - 1) & 1u, &s_abort, limit);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      load_v8(j);
+      issued = j + 1;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (lane == 0) {
+      // The buffers' phases have not been followed so far.  With the prefix's scores done, the product of tile n8 - 3 has run:
+      // from there on a buffer is at the phase before the one that is waited for, and a parity tells them apart
+      if (n8 > 0 && n16 > 0) ok = ok && pt_wait(bar(C_QFREE), 0, &s_abort, limit);
+      for (int j = issued16; ok && j < n16; ++j) {
+        const int i = n8 + j;
+        if (i >= 2 && !pt_wait(bar(C_VHFREE + (i & 1)), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit)) break;
+        load16(j, true);
+        issued16 = j + 1;
+      }
+      for (int j = max(0, issued - v_stages); j < issued; ++j)
+        ct_drain(bar(C_VFULL + (j & (v_stages - 1))), (uint32_t)(j / v_stages) & 1u);
       // bf16 tiles of V: the k-th of a buffer is its k-th arrival
-      for (int j = max(0, issued_v16 - 2); j < issued_v16; ++j) {
+      for (int j = max(0, issued16 - 2); j < issued16; ++j) {
         const int sv = (n8 + j) & 1, first_j = (n8 & 1) == sv ? 0 : 1;
         ct_drain(bar(C_VTMA + sv), (uint32_t)((j - first_j) >> 1) & 1u);
       }
     }
   } else if (warp == kCtScoreWarp) {
     // ---------------- score products ----------------
-    if (lane == 0) {
+    {
       constexpr uint32_t i8 = pt_idesc(0, FMT == ET_KV_E4M3 ? 0 : 1, false, false, 128, kCtKeys);
       constexpr uint32_t i16 = pt_idesc(1, 1, false, false, 128, kCtKeys);
       int k[2] = {0, 0};
@@ -446,62 +544,77 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           if (j == 0 && n8 > 0) ok = pt_wait(bar(C_QFULL), 0, &s_abort, limit);
           ok = ok && pt_wait(bar(C_K2FULL + sk), (uint32_t)(j >> 1) & 1u, &s_abort, limit);
         }
+        ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || !uses(w, i)) continue;
           // S lies where P of the group's last tile was: that product has run
-          if (k[w] > 0 && !pt_wait(bar(C_PVDONE + w), (uint32_t)(k[w] - 1) & 1u, &s_abort, limit)) { ok = false; continue; }
+          if (k[w] > 0) ok = pt_wait(bar(C_PVDONE + w), (uint32_t)(k[w] - 1) & 1u, &s_abort, limit);
+          // the groups run half a turn apart, so that one's products find the tensor cores free
+          else if (w == 1 && k[0] > 0 && !shared_rows) ok = pt_wait(bar(C_PHALF), 0, &s_abort, limit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;
           tc_fence_after();
           const uint32_t q = sb + Sh::off_q + (shared_rows ? 0u : (uint32_t)w * Sh::tile16), d = tmem + kCtColS + 128u * (uint32_t)w;
           if (i < n8) {
+            const uint64_t qd = desc8<D>(q), kd = desc8<D>(sb + Sh::off_k + (uint32_t)sk * Sh::tile8);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)  // the two terms of q one after the other
-              pt_mma_f8(d, desc8<D>(q + (kk / (D / 32)) * Sh::tile8 + (kk % (D / 32)) * 32),
-                        desc8<D>(sb + Sh::off_k + (uint32_t)sk * Sh::tile8 + (kk % (D / 32)) * 32), i8, kk > 0);
+              ct_mma_f8(d, qd + (((kk / (D / 32)) * Sh::tile8 + (kk % (D / 32)) * 32) >> 4), kd + ((kk % (D / 32)) * 32 >> 4), i8, kk > 0, lead);
           } else {
+            const uint64_t qd = sw128_desc(q, 16, 1024), kd = sw128_desc(sb + Sh::off_k + (uint32_t)sk * Sh::tile16, 16, 1024);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma(d, sw128_desc(q + (kk >> 2) * Sh::half16 + (kk & 3) * 32, 16, 1024),
-                     sw128_desc(sb + Sh::off_k + (uint32_t)sk * Sh::tile16 + (kk >> 2) * Sh::half16 + (kk & 3) * 32, 16, 1024),
-                     i16, kk > 0);
+              ct_mma(d, qd + (((kk >> 2) * Sh::half16 + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * Sh::half16 + (kk & 3) * 32) >> 4), i16, kk > 0, lead);
           }
-          tc_commit(bar(C_SFULL + w));
+          ct_commit(bar(C_SFULL + w), lead);
           ++k[w];
         }
         if (!ok) break;
-        if (i < n8 && i + kCtStages8 < n8) tc_commit(bar(C_KEMPTY + sk));
-        if (i >= n8 && j + 2 < n16) tc_commit(bar(C_K2EMPTY + sk));
-        if (i == n8 - 1 && n16 > 0) tc_commit(bar(C_QFREE));
+        {
+          if (i < n8 && i + kCtStages8 < n8) ct_commit(bar(C_KEMPTY + sk), lead);
+          if (i >= n8 && j + 2 < n16) ct_commit(bar(C_K2EMPTY + sk), lead);
+          if (i == n8 - 1 && n16 > 0) ct_commit(bar(C_QFREE), lead);
+        }
       }
       // every product this thread issued has finished before TMEM is freed
-      tc_commit(bar(C_DRAIN));
+      ct_commit(bar(C_DRAIN), lead);
       ct_drain(bar(C_DRAIN), 0);
     }
   } else if (warp == kCtPvWarp) {
     // ---------------- P.V products ----------------
-    if (lane == 0) {
+    {
       constexpr uint32_t i8 = pt_idesc(0, 0, false, true, 128, D), i16 = pt_idesc(1, 1, false, true, 128, D);
       int k[2] = {0, 0};
       bool ok = true;
       for (int i = 0; ok && i < n; ++i) {
         ok = pt_wait(bar(C_VHFULL + (i & 1)), (uint32_t)(i >> 1) & 1u, &s_abort, limit);
+        ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || !uses(w, i)) continue;
-          if (!pt_wait(bar(C_PFULL + w), (uint32_t)k[w] & 1u, &s_abort, limit)) { ok = false; continue; }
-          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kCtKeys / 16; ++kk)
-            tc_mma_ts(tmem + kCtColO + 128u * (uint32_t)w, tmem + kCtColS + 128u * (uint32_t)w + 8u * kk,
-                      sw128_desc(sb + Sh::off_v16 + (uint32_t)(i & 1) * Sh::tile16 + kk * 2048, Sh::half16, 1024),
-                      i < n8 ? i8 : i16, (k[w] > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(bar(C_PVDONE + w));
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && pt_wait(bar((h ? C_PFULL : C_PHALF) + w), (uint32_t)k[w] & 1u, &s_abort, limit);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            {
+              const uint64_t vd = sw128_desc(sb + Sh::off_v16 + (uint32_t)(i & 1) * Sh::tile16, Sh::half16, 1024);
+              const uint32_t o = tmem + kCtColO + 128u * (uint32_t)w, p = tmem + kCtColS + 128u * (uint32_t)w;
+              const uint32_t id = i < n8 ? i8 : i16;
+#pragma unroll
+              for (int kk = 4 * h; kk < 4 * h + 4; ++kk) ct_mma_ts(o, p + 8u * kk, vd + (kk * 2048 >> 4), id, (k[w] > 0 || kk > 0) ? 1u : 0u, lead);
+              if (h) ct_commit(bar(C_PVDONE + w), lead);
+            }
+          }
+          if (!ok) continue;
           ++k[w];
         }
         if (!ok) break;
-        tc_commit(bar(C_VHFREE + (i & 1)));
+        ct_commit(bar(C_VHFREE + (i & 1)), lead);
       }
-      tc_commit(bar(C_DRAIN + 1));
+      ct_commit(bar(C_DRAIN + 1), lead);
       ct_drain(bar(C_DRAIN + 1), 0);
     }
   }
@@ -514,8 +627,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const int gt = t & 127;
     bool ok = true;
     for (int i = 0; i < n8; ++i) {
-      const int sv = i & 1;
-      ok = ok && pt_wait(bar(C_VFULL + sv), (uint32_t)(i >> 1) & 1u, &s_abort, limit);
+      const int sv = i & 1, s8 = i & (v_stages - 1);
+      ok = ok && pt_wait(bar(C_VFULL + s8), (uint32_t)(i / v_stages) & 1u, &s_abort, limit);
+      // the K warp says which units there are
+      if (ok) ok = pt_wait(bar(C_SCALES + i % kCtSlots), (uint32_t)(i / kCtSlots) & 1u, &s_abort, limit);
       if (ok && i >= 2) ok = pt_wait(bar(C_VHFREE + sv), (uint32_t)((i >> 1) - 1) & 1u, &s_abort, limit);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       const uint32_t units = *(volatile uint32_t *)&s_units[i % kCtSlots];
@@ -523,7 +638,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const bool whole = lim >= kCtKeys && units == 0xffu;
       constexpr int C = D / 16, RP = 128 / C;  // 16-code chunks of a row; rows the threads take at once
       const int c = gt % C, r0 = gt / C;
-      const uint32_t from = sb + Sh::off_v8 + (uint32_t)sv * Sh::tile8, to = sb + Sh::off_v16 + (uint32_t)sv * Sh::tile16;
+      const uint32_t from = v8_at(s8), to = sb + Sh::off_v16 + (uint32_t)sv * Sh::tile16;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         constexpr int K = kCtKeys / RP / 2;
@@ -551,7 +666,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar(C_VEMPTY + sv));
+        mbar_arrive(bar(C_VEMPTY + s8));
         mbar_arrive(bar(C_VHFULL + sv));
       }
     }
@@ -559,8 +674,15 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (ok && n8 > 0) {  // q as it is, once the prefix's score products have run
         ok = __all_sync(0xffffffffu, pt_wait(bar(C_QFREE), 0, &s_abort, limit));
         if (ok) {
-          stage_q16(0, gt);
-          if (!shared_rows) stage_q16(1, gt);
+#pragma unroll 4
+          for (int x = gt; x < qrows * kLanes; x += 128) {
+            const int qr = x / kLanes, c = x % kLanes;
+            const uint32_t dst = sb + Sh::off_q + (uint32_t)(qr >> 7) * Sh::tile16 + (uint32_t)(c >> 3) * Sh::half16 + sw128(qr & 127, c & 7);
+            const __nv_bfloat16 *src = q_row(qr);
+            if (src) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + 8 * c) : "memory");
+            else sts128(dst, 0u, 0u, 0u, 0u);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C_QFULL));
@@ -611,6 +733,17 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     auto tile = [&](int i, auto own_, auto masked_) {
       constexpr bool own = decltype(own_)::value, masked = decltype(masked_)::value;
       const int slot = i % kCtSlots;
+      // a unit's factor, offset and inverse V scale, before the scores are there
+      float fu[kCtKeys / 16], cu[kCtKeys / 16], iu[kCtKeys / 16];
+      if (!own) {
+#pragma unroll
+        for (int u = 0; u < kCtKeys / 16; ++u) {
+          float ks, lv;
+          lds_f4(saddr(&s_scale[slot][u]), ks, lv, iu[u]);
+          fu[u] = f8 * ks;
+          cu[u] = lv - ref;
+        }
+      }
       int lim = 0;
       uint32_t units = 0xffu;
       if (masked) {
@@ -621,6 +754,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           lim = tok < 0 ? 0 : L - (t0 + i) * kCtKeys;
         }
       }
+      dead = dead || !pt_wait(bar(C_SFULL + w), (uint32_t)items & 1u, &s_abort, limit);
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) return;
+      tc_fence_after();
       uint32_t raw[kCtKeys / 32][32];
 #pragma unroll
       for (int p = 0; p < kCtKeys / 32; ++p) tmem_ld32(sc + 32u * p, raw[p]);
@@ -628,9 +765,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       float top = -INFINITY;
 #pragma unroll
       for (int u = 0; u < kCtKeys / 16; ++u) {
-        float ks = 1.f, lv = 0.f, iv;
-        if (!own) lds_f4(saddr(&s_scale[slot][u]), ks, lv, iv);
-        const float f = own ? f16 : f8 * ks, c = lv - ref;
+        const float f = own ? f16 : fu[u], c = own ? -ref : cu[u];
         const uint64_t f2 = pair(f, f), c2 = pair(c, c);
         int limu = masked ? lim - 16 * u : 16;
         if (masked && !own && !((units >> u) & 1u)) limu = 0;
@@ -680,9 +815,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         uint32_t pk[16];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float ks, lv, iv = 1.f;
-          if (!own) lds_f4(saddr(&s_scale[slot][2 * p + u]), ks, lv, iv);
-          const uint64_t iv2 = pair(iv, iv);
+          const uint64_t iv2 = own ? 0ull : pair(iu[2 * p + u], iu[2 * p + u]);
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             const float w0 = ex2_fast(__uint_as_float(raw[p][16 * u + e])), w1 = ex2_fast(__uint_as_float(raw[p][16 * u + e + 1]));
@@ -691,6 +824,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           }
         }
         tmem_st16(sc + 16u * p, pk);
+        if (p == 1) {  // the first 64 keys' weights: their product may begin
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C_PHALF + w));
+        }
       }
       float s0, s1;
       unpair(add2(l2[0], l2[1]), s0, s1);
@@ -704,10 +843,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     for (int i = 0; i < n; ++i) {
       if (!uses(w, i)) continue;
       if (i < n8) dead = dead || !pt_wait(bar(C_SCALES + i % kCtSlots), (uint32_t)(i / kCtSlots) & 1u, &s_abort, limit);
-      dead = dead || !pt_wait(bar(C_SFULL + w), (uint32_t)items & 1u, &s_abort, limit);
       dead = __any_sync(0xffffffffu, dead);
       if (dead) break;
-      tc_fence_after();
       if (i < n8) {
         const bool whole = L - (t0 + i) * kCtKeys >= kCtKeys && *(volatile uint32_t *)&s_units[i % kCtSlots] == 0xffu;
         if (whole) tile(i, std::false_type{}, std::false_type{});
@@ -731,6 +868,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   // ---- the rows: one group's, or the two groups' halves of the keys joined ----
   float *xo = reinterpret_cast<float *>(sm + Sh::off_q);                       // [D][128] of group 1
   float2 *xm = reinterpret_cast<float2 *>(sm + Sh::off_v8);                    // [128]
+  // the rows as they go out: behind the other group's, or (fp32 rows of both groups) from the start
+  const uint32_t stage = sb + (parts > 1 && !shared_rows ? Sh::off_q : Sh::off_k);
+  const long long slot0 = ((long long)unit * ca.S + part) * 256;
   const int w = warp >> 2, r = t & 127, Rr = shared_rows ? r : 128 * w + r;
   const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCtColO + 128u * (uint32_t)w;
   if (shared_rows && w == 1) {
@@ -764,16 +904,15 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const int R = R0 + Rr, i = ct_token(ca, R), h = g * a.G + (R - i * a.G);
     const long long row = (long long)(first + i) * a.Hq + h;
     const bool odd = s_odd != 0;
-    const long long slot = ((long long)unit * ca.S + part) * 256 + Rr;
     if (parts == 1) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
       mine *= inv;
       other *= inv;
       if (Rr < real && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
     } else if (Rr < real) {
-      ca.part_ml[slot] = make_float2(M, l);
+      ca.part_ml[slot0 + Rr] = make_float2(M, l);
     }
-#pragma unroll 1
+#pragma unroll 2
     for (int p = 0; p < D / 16; ++p) {
       uint32_t o[16];
       pt_ld16(lanes + 16u * p, o);
@@ -797,16 +936,33 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           }
         }
       }
-      if (Rr < real) {
-        if (parts == 1) {
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + 16 * p);
-          dst[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-          dst[1] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
-        } else {
-          float4 *dst = ca.part_o + slot * (D / 4) + 4 * p;
+      // through shared memory, where rows are written one by one: a row's 16-byte pieces trade places by the row's number
+      if (parts == 1) {
+        const uint32_t dst = stage + (uint32_t)(Rr * D * 2);
+        const int c = 2 * p;
+        sts128(dst + (uint32_t)((c ^ (Rr & 7)) << 4), pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        sts128(dst + (uint32_t)(((c + 1) ^ (Rr & 7)) << 4), pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
+      } else {
+        const uint32_t dst = stage + (uint32_t)(Rr * D * 4);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-        }
+        for (int e = 0; e < 4; ++e)
+          sts128(dst + (uint32_t)(((4 * p + e) ^ (Rr & 7)) << 4), __float_as_uint(x[4 * e]), __float_as_uint(x[4 * e + 1]),
+                 __float_as_uint(x[4 * e + 2]), __float_as_uint(x[4 * e + 3]));
+      }
+    }
+  }
+  __syncthreads();
+  {
+    const int per_row = parts == 1 ? D / 8 : D / 4;  // 16-byte pieces
+#pragma unroll 4
+    for (int x = t; x < real * per_row; x += kCtThreads) {
+      const int rr = x / per_row, c = x - rr * per_row;
+      const uint4 v = *reinterpret_cast<const uint4 *>(sm + (stage - sb) + (uint32_t)(16 * (rr * per_row + (c ^ (rr & 7)))));
+      if (parts == 1) {
+        const int R = R0 + rr, i = ct_token(ca, R), h = g * a.G + (R - i * a.G);
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + ((long long)(first + i) * a.Hq + h) * D + 8 * c) = v;
+      } else {
+        reinterpret_cast<uint4 *>(ca.part_o)[(slot0 + rr) * (D / 4) + c] = v;
       }
     }
   }

@@ -145,3 +145,23 @@ def test_matches_the_formula(prefix, rows, Hq, Hkv, P, d, dtype, fmt):
     x = Batch(prefix, rows, Hq, Hkv, d, P, fmt, dtype, seed=len(prefix) + rows[0])
     x.run()
     x.check()
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3, 7])
+@pytest.mark.parametrize("prefix,rows,Hq,Hkv,P,d", [
+    ([2100], [300], 2, 2, 64, 128),                 # two tiles of rows over many tiles of keys
+    ([1900], [270], 2, 2, 16, 64),
+    ([3000], [17], 2, 1, 32, 128),                  # one tile of rows: the groups take the keys in turn
+    ([2305], [5], 8, 1, 48, 64),
+    ([0], [1500], 1, 1, 64, 128),                   # new rows only, up to six tiles of rows
+    ([700, 0, 1500], [600, 900, 1], 4, 2, 128, 128),
+    ([128 * 9, 128 * 8], [256, 128], 1, 1, 64, 128),  # everything whole tiles
+])
+def test_many_tiles_in_any_number_of_parts(prefix, rows, Hq, Hkv, P, d, splits):
+    x = Batch(prefix, rows, Hq, Hkv, d, P, seed=splits)
+    ws = x.run(splits=splits)
+    x.check()
+    first = x.out.clone(), x.lse.clone()
+    x.out.fill_(7.0)
+    x.run(splits=splits, ws=ws)                     # the workspace is as it was; the same bits again
+    assert torch.equal(first[0], x.out) and torch.equal(first[1], x.lse)
