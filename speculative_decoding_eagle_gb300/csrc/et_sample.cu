@@ -3,16 +3,19 @@
 // which the acceptance walk is lossless for the truncated distribution (EAGLE
 // blog 1.2: lossless in non-greedy decoding).
 //
-// One thread-block cluster per row; every block keeps its slice of the row in
-// shared memory, so that the logits are read from HBM once whatever is asked
-// for.  Two questions are put to the row, both "where does a cumulative count
-// or mass pass a border": in the order of the logits (top-k by count, top-p by
-// mass) and in the order of ids (the draw).
+// One thread-block cluster per row (of one block where there are rows enough);
+// every block keeps its slice of the row in shared memory, so that the logits
+// are read from HBM once whatever is asked for.  Two questions are put to the
+// row, both "where does a cumulative count or mass pass a border": in the
+// order of the logits (top-k by count, top-p by mass) and in the order of ids
+// (the draw).
 //   Order of logits: a histogram over equal steps of the logit finds the step
-// with the border, then histograms over the keys (order-preserving integer
-// images of the logits) inside it, until one key value is left; equal keys are
-// told apart by id.  Counts and masses are integers, so blocks and atomics may
-// come in any order.
+// with the border.  If it and the steps above hold few tokens, as they do for
+// all but flat rows, one block sorts these and answers everything.  Else
+// histograms over the keys (order-preserving integer images of the logits)
+// inside the step follow, until one key value is left; equal keys are told
+// apart by id.  Counts and masses are integers, so blocks and atomics may come
+// in any order.
 //   Order of ids: masses per block, per warp, per 32 tokens.
 // Masses are sums of weights 2^44 exp((z - max) / T) rounded to integers.  The
 // exponential is evaluated in pairs of fp32 numbers (error-free sums and
@@ -25,13 +28,14 @@
 namespace et {
 namespace {
 
-constexpr int kSaThreads = 512;
+constexpr int kSaThreads = 1024;
 constexpr int kSaWarps = kSaThreads / 32;
-constexpr int kSaBins = 1024;
-constexpr int kSaLimbs = 3;          // a mass of 45 bits in three sums of 15 bits
+constexpr int kSaBins = 512;
+constexpr int kSaLimbs = 4;          // a mass of 45 bits in three sums of 15 bits, and a count
 constexpr int kSaMaxCluster = 8;
 constexpr int kSaMaxSlice = 32768;   // tokens per block: 8 * 32768 = the largest vocabulary
 constexpr int kSaFrac = 44;
+constexpr int kSaList = 1024;        // tokens that one block sorts
 
 struct SampleArgs {
   int B, V, slice, cluster;
@@ -43,16 +47,28 @@ struct SampleArgs {
   float *logprob, *truncated;
 };
 
-// what a block's peers read of it
+// where a cumulative weight passes a border
+struct Crossing {
+  int bin;                               // -1: nowhere
+  unsigned int upto;                     // tokens of this bin and those above
+  unsigned long long above;              // weight of the bins above
+};
+// what a block's peers read and write of it
 struct SampleShared {
   float zmax, zmin;                      // of the block's slice (zmin: of what is above -inf)
   unsigned int first;                    // lowest id of the block's largest
   int odd;
   unsigned int key_lo, key_hi;           // of the slice's members of the current bin
-  unsigned long long mass;               // of the slice's kept tokens
-  unsigned int ties;
+  unsigned long long mass;               // of the slice's kept tokens, or of the block's share of the bins
+  unsigned int count;
+  Crossing crossing;
+  unsigned int listed;                   // tokens in the list (block 0)
+  unsigned int kept_tau;
+  int kept_cut;
   unsigned long long warp_mass[kSaWarps];
+  unsigned int warp_count[kSaWarps];
   unsigned int hist[2][kSaLimbs][kSaBins];  // alternating: a pass clears the other one
+  unsigned long long list[kSaList], weight[kSaList];
 };
 
 // order-preserving image of a logit: larger logit, larger key; -0 as +0
@@ -66,6 +82,14 @@ __device__ __forceinline__ unsigned long long cl_ld_u64(uint32_t addr) {
   unsigned long long v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
   return v;
+}
+// all blocks of the row
+__device__ __forceinline__ void row_sync(int C) {
+  if (C > 1) cl_sync();
+  else __syncthreads();
+}
+__device__ __forceinline__ float key_value(unsigned int key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
 #pragma unroll
@@ -100,12 +124,13 @@ struct Weigher {
   }
 };
 
-// the three limbs of a mass into a bin; high limbs are rarely there
+// a token's mass, in three limbs of which the high ones are rarely there, and count into a bin
 __device__ __forceinline__ void add_mass(unsigned int (*h)[kSaBins], int bin, unsigned long long w) {
   const unsigned int l0 = (unsigned int)w & 0x7fffu, l1 = (unsigned int)(w >> 15) & 0x7fffu, l2 = (unsigned int)(w >> 30);
   if (l0) atomicAdd(&h[0][bin], l0);
   if (l1) atomicAdd(&h[1][bin], l1);
   if (l2) atomicAdd(&h[2][bin], l2);
+  atomicAdd(&h[3][bin], 1u);
 }
 
 // what is kept: keys above tau, and of those equal to it ids up to cut
@@ -145,10 +170,10 @@ __device__ int locate(const Row &row, int slice, unsigned long long *s_red, int 
     row.sh->mass = sum;
     *s_id = -1;
   }
-  cl_sync();
+  row_sync(row.C);
   unsigned long long before = 0ull, all = 0ull;
   for (int k = 0; k < row.C; ++k) {
-    const unsigned long long m = cl_ld_u64(cl_map(&row.sh->mass, (uint32_t)k));
+    const unsigned long long m = row.C > 1 ? cl_ld_u64(cl_map(&row.sh->mass, (uint32_t)k)) : row.sh->mass;
     if (k < row.rank) before += m;
     all += m;
   }
@@ -175,98 +200,130 @@ __device__ int locate(const Row &row, int slice, unsigned long long *s_red, int 
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  cl_sync();
+  row_sync(row.C);
   const int id = *s_id;
   __syncthreads();
   return id;
 }
 
-// Where the cumulative weight in the order of the logits passes `target`: the
-// kept set that ends with that token.  MASS: weights are masses of the tokens
-// in `in`, and target a share of their sum; else counts.
+// inclusive sum over the block's threads in order; red holds kSaWarps
+__device__ __forceinline__ unsigned long long block_scan_u64(unsigned long long v, unsigned long long *red, unsigned long long &all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) red[warp] = v;
+  __syncthreads();
+  unsigned long long mine = red[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, mine, o);
+    if (lane >= o) mine += y;
+  }
+  static_assert(kSaWarps == 32, "one warp scans the warps");
+  all = __shfl_sync(0xffffffffu, mine, 31);
+  const unsigned long long before = __shfl_sync(0xffffffffu, mine, (warp + 31) & 31);
+  __syncthreads();
+  return v + (warp ? before : 0ull);
+}
+
+// The cluster's histogram `h`, its bins in order, and where the cumulative weight reaches `target` (share >= 0: that share
+// of the sum, rounded up, one at least).  Block r adds up its share of the bins over the blocks.
 template <bool MASS>
-__device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weigher &weigh, float zm, float step,
-                       unsigned long long count, float share, unsigned long long *s_red, int *s_id) {
+__device__ Crossing cross(const Row &row, unsigned int (*h)[kSaBins], unsigned long long above, float share,
+                          unsigned long long *target, unsigned long long *all_mass, unsigned long long *s_red) {
   SampleShared *sh = row.sh;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  unsigned long long target = count;  // the border lies in the first bin whose cumulative weight reaches it
-  unsigned long long above = 0ull;    // weight of the bins above
+  const int t = threadIdx.x, C = row.C, per = kSaBins / C;
+  row_sync(C);  // every block's histogram is whole
+  unsigned long long w = 0ull;
+  unsigned int count = 0u;
+  if (t < kSaBins) {  // bin t / C of the share, as block t % C has it
+    const int bin = row.rank * per + t / C;
+    const uint32_t k = (uint32_t)(t % C);
+    unsigned int l[kSaLimbs];
+#pragma unroll
+    for (int x = 0; x < kSaLimbs; ++x)
+      l[x] = !MASS && x < 3 ? 0u : C > 1 ? cl_ld_u32(cl_map(&h[x][bin], k)) : h[x][bin];
+    count = l[3];
+    w = MASS ? (unsigned long long)l[0] + ((unsigned long long)l[1] << 15) + ((unsigned long long)l[2] << 30) : count;
+  }
+  // the sum over a bin's C threads comes out of a running sum over all of them
+  unsigned long long all, all_count;
+  const unsigned long long incl = block_scan_u64(w, s_red, all);
+  const unsigned long long incl_count = block_scan_u64(count, s_red, all_count);
+  if (t == 0) {
+    sh->mass = all;
+    sh->count = (unsigned int)all_count;
+    sh->crossing.bin = -1;
+  }
+  row_sync(C);
+  unsigned long long before = above, sum = above;
+  unsigned int before_count = 0u;
+  for (int k = 0; k < C; ++k) {
+    const unsigned long long m = C > 1 ? cl_ld_u64(cl_map(&sh->mass, (uint32_t)k)) : sh->mass;
+    const unsigned int n = C > 1 ? cl_ld_u32(cl_map(&sh->count, (uint32_t)k)) : sh->count;
+    if (k < row.rank) {
+      before += m;
+      before_count += n;
+    }
+    sum += m;
+  }
+  *all_mass = sum;
+  if (share >= 0.f) {
+    *target = (unsigned long long)ceil((double)share * (double)sum);
+    if (*target < 1ull) *target = 1ull;
+  }
+  // the last of a bin's threads knows the weight up to its end; the bin before, up to its beginning
+  unsigned long long begin = __shfl_up_sync(0xffffffffu, incl, C);
+  if ((t & 31) == 31) s_red[t >> 5] = incl;
+  __syncthreads();
+  if ((t & 31) < C) begin = t < 32 ? 0ull : s_red[(t >> 5) - 1];  // the bin before is the previous warp's last
+  if (t < kSaBins && t % C == C - 1) {
+    const unsigned long long from = before + begin, to = before + incl;
+    if (from < *target && *target <= to) {
+      Crossing c;
+      c.bin = row.rank * per + t / C;
+      c.upto = before_count + (unsigned int)incl_count;
+      c.above = from;
+      for (int k = 0; k < C; ++k) {
+        const uint32_t at = cl_map(&sh->crossing, (uint32_t)k);
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at + 8u), "l"(c.above) : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + 4u), "r"(c.upto) : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(c.bin) : "memory");
+      }
+    }
+  }
+  row_sync(C);
+  return sh->crossing;
+}
+
+// steps of the logit below the maximum
+__device__ __forceinline__ int step_of(float z, float zm, float step) { return min(kSaBins - 1, (int)((zm - z) * step)); }
+
+// Where the cumulative weight in the order of the logits passes the border: the kept set that ends with that token.  The
+// first histogram's crossing is `c`.  MASS: weights are masses of the tokens in `in`; else counts.
+template <bool MASS>
+__device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weigher &weigh, float zm, float step, Crossing c,
+                       unsigned long long target, unsigned long long *s_red, int *s_id) {
+  SampleShared *sh = row.sh;
+  const int t = threadIdx.x, lane = t & 31;
   unsigned int lo = 0u, hi = 0xffffffffu;
-  int shift = -1;                     // -1: bins are steps of the logit below the maximum; else (key - lo) >> shift from above
-  bool first = true;
-  for (int round = 0; round < 8; ++round) {  // 1 + at most 4 rounds: a round leaves 2^22 of 2^32 keys, 2^12, 2^2, one
-    unsigned int (*h)[kSaBins] = sh->hist[row.buf];
-    auto bin_of = [&](unsigned int key, float z) -> int {
-      if (shift < 0) return min(kSaBins - 1, (int)((zm - z) * step));
-      return (int)((hi - key) >> shift);
-    };
-    for (int i = t; i < row.n; i += kSaThreads) {
-      const float z = row.z[i];
-      const unsigned int key = order_key(z);
-      if (z == -INFINITY || key < lo || key > hi || !in(key, row.base + i)) continue;
-      if (MASS) add_mass(h, bin_of(key, z), weigh(z));
-      else atomicAdd(&h[0][bin_of(key, z)], 1u);
-    }
-    cl_sync();
-    // every block adds the cluster's histograms up: thread t has bins 2 t and 2 t + 1
-    unsigned long long w[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      w[e] = 0ull;
-      for (int k = 0; k < row.C; ++k) {
-#pragma unroll
-        for (int l = 0; l < (MASS ? kSaLimbs : 1); ++l)
-          w[e] += (unsigned long long)cl_ld_u32(cl_map(&h[l][2 * t + e], (uint32_t)k)) << (15 * l);
-      }
-    }
-    unsigned long long incl = w[0] + w[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) s_red[warp] = incl;
-    if (t == 0) *s_id = -1;
-    // the other histogram is free: its readers have passed this pass's first barrier
-    for (int x = t; x < kSaLimbs * kSaBins; x += kSaThreads) (&sh->hist[row.buf ^ 1][0][0])[x] = 0u;
-    __syncthreads();
-    unsigned long long before = above, all = above;
-    for (int k = 0; k < kSaWarps; ++k) {
-      if (k < warp) before += s_red[k];
-      all += s_red[k];
-    }
-    if (MASS && first) {  // tokens before which less than the share of the mass lies: ceil(share * mass), one at least
-      target = (unsigned long long)ceil((double)share * (double)all);
-      if (target < 1ull) target = 1ull;
-    }
-    first = false;
-    before += incl - w[0] - w[1];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (before < target && target <= before + w[e]) {
-        s_id[0] = 2 * t + e;
-        s_red[kSaWarps] = before;
-      }
-      before += w[e];
-    }
+  int shift = -1;  // -1: bins are steps of the logit below the maximum; else (hi - key) >> shift
+  for (int round = 0; round < 8; ++round) {  // 1 + at most 4 rounds: a round leaves 2^23 of 2^32 keys, 2^14, 2^5, one
+    if (c.bin < 0) return in;  // more was asked for than there is: everything stays
+    auto bin_of = [&](unsigned int key, float z) -> int { return shift < 0 ? step_of(z, zm, step) : (int)((hi - key) >> shift); };
     if (t == 0) {
       sh->key_lo = 0xffffffffu;
       sh->key_hi = 0u;
     }
     __syncthreads();
-    const int bin = *s_id;
-    above = s_red[kSaWarps];
-    if (bin < 0) {  // more was asked for than there is: everything stays
-      cl_sync();
-      row.buf ^= 1;
-      return in;
-    }
-    // the bin's keys
-    unsigned int kl = 0xffffffffu, kh = 0u;
+    unsigned int kl = 0xffffffffu, kh = 0u;  // the bin's keys
     for (int i = t; i < row.n; i += kSaThreads) {
       const float z = row.z[i];
       const unsigned int key = order_key(z);
-      if (z == -INFINITY || key < lo || key > hi || !in(key, row.base + i) || bin_of(key, z) != bin) continue;
+      if (z == -INFINITY || key < lo || key > hi || !in(key, row.base + i) || bin_of(key, z) != c.bin) continue;
       kl = min(kl, key);
       kh = max(kh, key);
     }
@@ -276,29 +333,61 @@ __device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weig
       atomicMin(&sh->key_lo, kl);
       atomicMax(&sh->key_hi, kh);
     }
-    cl_sync();
+    row_sync(row.C);
     lo = 0xffffffffu;
     hi = 0u;
     for (int k = 0; k < row.C; ++k) {
-      lo = min(lo, cl_ld_u32(cl_map(&sh->key_lo, (uint32_t)k)));
-      hi = max(hi, cl_ld_u32(cl_map(&sh->key_hi, (uint32_t)k)));
+      lo = min(lo, row.C > 1 ? cl_ld_u32(cl_map(&sh->key_lo, (uint32_t)k)) : sh->key_lo);
+      hi = max(hi, row.C > 1 ? cl_ld_u32(cl_map(&sh->key_hi, (uint32_t)k)) : sh->key_hi);
     }
-    row.buf ^= 1;
     if (lo >= hi) break;
-    shift = max(0, 22 - __clz(hi - lo));  // at most 1024 bins of 2^shift keys
+    shift = max(0, 23 - __clz(hi - lo));  // at most 512 bins of 2^shift keys
+    // the other histogram has been clear since the last pass; this pass clears the one before
+    row.buf ^= 1;
+    unsigned int (*h)[kSaBins] = sh->hist[row.buf];
+    for (int i = t; i < row.n; i += kSaThreads) {
+      const float z = row.z[i];
+      const unsigned int key = order_key(z);
+      if (z == -INFINITY || key < lo || key > hi || !in(key, row.base + i)) continue;
+      if (MASS) add_mass(h, bin_of(key, z), weigh(z));
+      else atomicAdd(&h[3][bin_of(key, z)], 1u);
+    }
+    for (int x = t; x < kSaLimbs * kSaBins; x += kSaThreads) (&sh->hist[row.buf ^ 1][0][0])[x] = 0u;
+    unsigned long long all;
+    c = cross<MASS>(row, h, c.above, -1.f, &target, &all, s_red);
   }
   // one key value: the first of its tokens, in ascending id, up to the border
   Kept out;
   out.tau = lo;
   out.cut = 0x7fffffff;
-  const unsigned long long each = MASS ? weigh(__uint_as_float((lo & 0x80000000u) ? (lo & 0x7fffffffu) : ~lo)) : 1ull;
-  const unsigned long long nth = each ? (target - above + each - 1) / each : 1ull;  // how many of them
+  const unsigned long long each = MASS ? weigh(key_value(lo)) : 1ull;
+  const unsigned long long nth = each ? (target - c.above + each - 1) / each : 1ull;  // how many of them
   const int id = locate(row, a.slice, s_red, s_id, [&](float z, int i) -> unsigned long long {
     const unsigned int key = order_key(z);
     return key == lo && in(key, i) ? 1ull : 0ull;
   }, nth - 1, nullptr, false, 0.f);
   if (id >= 0) out.cut = id;
   return out;
+}
+
+// v[0 .. n) ascending, n <= kSaThreads: a bitonic network, a value per thread
+__device__ unsigned long long block_sort(unsigned long long v, int n, unsigned long long *buf) {
+  const int t = threadIdx.x;
+  for (int k = 2; k < 2 * n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      unsigned long long o;
+      if (j >= 32) {
+        __syncthreads();
+        buf[t] = v;
+        __syncthreads();
+        o = buf[t ^ j];
+      } else {
+        o = __shfl_xor_sync(0xffffffffu, v, j);
+      }
+      const bool low = ((t & j) == 0) == ((t & k) == 0);  // this thread takes the smaller one
+      v = low == (o < v) ? o : v;
+    }
+  return v;
 }
 
 __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
@@ -308,8 +397,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   __shared__ unsigned long long s_red[kSaWarps + 1];
   __shared__ int s_id;
   __shared__ float s_f[32];
-  __shared__ unsigned int s_u[kSaWarps];
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int t = threadIdx.x, lane = t & 31;
   Row row;
   row.sh = &sh;
   row.z = s_z;
@@ -324,11 +412,16 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
     const float h = (float)x;
     s_table[t] = make_float2(h, (float)(x - (double)h));
   }
-  for (int x = t; x < kSaLimbs * kSaBins; x += kSaThreads) (&sh.hist[0][0][0])[x] = 0u;
+  for (int x = t; x < 2 * kSaLimbs * kSaBins; x += kSaThreads) (&sh.hist[0][0][0])[x] = 0u;
+  if (t == 0) sh.listed = 0u;
   pdl_wait();
   pdl_trigger();
   // ---- the slice into shared memory; its extremes ----
   const float *zr = a.logits + (long long)b * a.row_stride + row.base;
+  float T = a.temperature ? a.temperature[b] : 1.f;
+  const int k = a.top_k ? a.top_k[b] : 0;
+  const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
+  float u = a.uniforms[b];
   float zmax = -INFINITY, zmin = INFINITY;
   int odd = 0;
   auto take = [&](float z) -> float {
@@ -339,6 +432,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   };
   if (a.vec4) {  // the slice is a multiple of 4: only the row's end is ragged
     const int n4 = row.n >> 2;
+#pragma unroll 4
     for (int i = t; i < n4; i += kSaThreads) {
       float4 v = __ldcs(reinterpret_cast<const float4 *>(zr) + i);
       v.x = take(v.x); v.y = take(v.y); v.z = take(v.z); v.w = take(v.w);
@@ -346,39 +440,36 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
     }
     for (int i = 4 * n4 + t; i < row.n; i += kSaThreads) s_z[i] = take(zr[i]);
   } else {
+#pragma unroll 8
     for (int i = t; i < row.n; i += kSaThreads) s_z[i] = take(zr[i]);
   }
   zmax = block_max<kSaThreads>(zmax, s_f);
   zmin = -block_max<kSaThreads>(-zmin, s_f);
   odd = __syncthreads_or(odd);
-  unsigned int first = 0xffffffffu;  // lowest id of the largest logit
-  for (int i = t; i < row.n; i += kSaThreads)
-    if (s_z[i] == zmax) first = min(first, (unsigned int)(row.base + i));
-  first = __reduce_min_sync(0xffffffffu, first);
-  if (lane == 0) s_u[warp] = first;
-  __syncthreads();
   if (t == 0) {
-    for (int k = 0; k < kSaWarps; ++k) first = min(first, s_u[k]);
     sh.zmax = zmax;
     sh.zmin = zmin;
-    sh.first = first;
+    sh.first = 0xffffffffu;
     sh.odd = odd;
   }
-  cl_sync();
+  __syncthreads();
+  // the lowest id of the largest logit, where a block may have it
+  for (int i = t; i < row.n; i += kSaThreads)
+    if (s_z[i] == zmax) {
+      atomicMin(&sh.first, (unsigned int)(row.base + i));
+      break;
+    }
+  row_sync(row.C);
   float zm = -INFINITY, zl = INFINITY;
   unsigned int top = 0xffffffffu;
-  for (int k = 0; k < a.cluster; ++k) {
-    const float m = cl_ld_f32(cl_map(&sh.zmax, (uint32_t)k));
-    const unsigned int f = cl_ld_u32(cl_map(&sh.first, (uint32_t)k));
+  for (int x = 0; x < a.cluster; ++x) {
+    const float m = row.C > 1 ? cl_ld_f32(cl_map(&sh.zmax, (uint32_t)x)) : sh.zmax;
+    const unsigned int f = row.C > 1 ? cl_ld_u32(cl_map(&sh.first, (uint32_t)x)) : sh.first;
     if (m > zm) { zm = m; top = f; }  // blocks hold ascending ids: the first one wins a tie
-    zl = fminf(zl, cl_ld_f32(cl_map(&sh.zmin, (uint32_t)k)));
+    zl = fminf(zl, row.C > 1 ? cl_ld_f32(cl_map(&sh.zmin, (uint32_t)x)) : sh.zmin);
   }
   if (odd && t == 0) flag_status(a.dev_status, ET_DEV_NONFINITE);
 
-  float T = a.temperature ? a.temperature[b] : 1.f;
-  const int k = a.top_k ? a.top_k[b] : 0;
-  const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
-  float u = a.uniforms[b];
   u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
   const bool none = zm == -INFINITY, greedy = !(T > 0.f) || k == 1 || p <= 0.f;
   Kept kept;
@@ -386,6 +477,10 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   kept.cut = -1;  // every key above zero: -inf is above it, and left out where it matters
   int token = -1;
   float logprob = -INFINITY;
+  T = fminf(fmaxf(T, 1e-30f), 1e30f);
+  auto log_share = [&](float z, unsigned long long total) -> float {
+    return (float)(((double)z - (double)zm) / (double)T - log((double)total / (double)(1ll << kSaFrac)));
+  };
   if (none) {
     if (t == 0 && row.rank == 0) flag_status(a.dev_status, ET_DEV_NONFINITE);
     kept.tau = 0xffffffffu;
@@ -395,55 +490,153 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
     kept.tau = order_key(zm);
     kept.cut = token;
   } else {
-    T = fminf(fmaxf(T, 1e-30f), 1e30f);
     const double c = 1.4426950408889634074 / (double)T;
     Weigher weigh;
     weigh.zm = zm;
     weigh.ch = (float)c;
     weigh.cl = (float)(c - (double)weigh.ch);
     weigh.table = s_table;
-    // steps of the logit: the row's own range, but no more than what has mass
-    const float range = fminf(zm - zl, fmaxf(32.f * T, 32.f));
-    const float step = range > 0.f ? (float)(kSaBins - 1) / range : 0.f;
-    if (k > 0 && k < a.V) kept = border<false>(row, a, kept, weigh, zm, step, (unsigned long long)k, 0.f, s_red, &s_id);
-    if (p < 1.f) kept = border<true>(row, a, kept, weigh, zm, step, 0ull, p, s_red, &s_id);
+    // min-p: keys from this one on
+    unsigned int key_min = 0u;
     if (mp > 0.f) {
       // the smallest logit with (z - max) / T >= log(min_p)
       const double depth = (double)T * log((double)mp);
       float zf = (float)((double)zm + depth);
       if ((double)zf - (double)zm < depth) zf = nextafterf(zf, INFINITY);
-      const unsigned int key = order_key(fminf(zf, zm));
-      if (mp > 1.f || zf > zm) {  // the largest token alone
-        kept.tau = order_key(zm);
-        kept.cut = (int)top;
-      } else if (key > kept.tau) {
-        kept.tau = key;
-        kept.cut = 0x7fffffff;
+      key_min = mp > 1.f || zf > zm ? 0xffffffffu : order_key(zf);
+    }
+    const bool by_count = k > 0 && k < a.V, by_mass = p < 1.f;
+    bool done = false;
+    if (by_count || by_mass) {
+      // steps of the logit: the row's own range, but no more than what has mass
+      const float range = fminf(zm - zl, fmaxf(32.f * T, 32.f));
+      const float step = range > 0.f ? (float)(kSaBins - 1) / range : 0.f;
+      unsigned int (*h)[kSaBins] = sh.hist[0];
+      for (int i = t; i < row.n; i += kSaThreads) {
+        const float z = s_z[i];
+        if (z == -INFINITY) continue;
+        if (by_count) atomicAdd(&h[3][step_of(z, zm, step)], 1u);
+        else add_mass(h, step_of(z, zm, step), weigh(z));
+      }
+      unsigned long long target = by_count ? (unsigned long long)k : 0ull, all = 0ull;
+      Crossing x = by_count ? cross<false>(row, h, 0ull, -1.f, &target, &all, s_red) : cross<true>(row, h, 0ull, p, &target, &all, s_red);
+      if (x.bin >= 0 && x.upto <= kSaList) {
+        // ---- few tokens: block 0 sorts them ----
+        for (int i0 = 0; i0 < row.n; i0 += kSaThreads) {
+          const int i = i0 + t;
+          const float z = i < row.n ? s_z[i] : -INFINITY;
+          const bool in = z > -INFINITY && step_of(z, zm, step) <= x.bin;
+          const unsigned int m = __ballot_sync(0xffffffffu, in);
+          if (!m) continue;
+          unsigned int at = 0u;
+          if (lane == 0) {
+            const uint32_t n = cl_map(&sh.listed, 0u);
+            asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(n), "r"((unsigned int)__popc(m)) : "memory");
+          }
+          at = __shfl_sync(0xffffffffu, at, 0) + (unsigned int)__popc(m & ((1u << lane) - 1u));
+          if (in)
+            cl_st_u64(cl_map(&sh.list[0], 0u) + 8u * at, ((unsigned long long)~order_key(z) << 32) | (unsigned int)(row.base + i));
+        }
+        row_sync(row.C);
+        if (row.rank == 0) {
+          const int n = (int)x.upto;
+          unsigned long long mine = t < n ? sh.list[t] : ~0ull;
+          mine = block_sort(mine, n, sh.weight);
+          const unsigned int key = ~(unsigned int)(mine >> 32);
+          bool stays = t < n && !(by_count && t >= k);
+          unsigned long long w = stays ? weigh(key_value(key)) : 0ull, sum;
+          const unsigned long long incl = block_scan_u64(w, s_red, sum);
+          if (by_mass) {
+            if (by_count) {
+              target = (unsigned long long)ceil((double)p * (double)sum);
+              if (target < 1ull) target = 1ull;
+            }
+            stays = stays && incl - w < target;
+          }
+          stays = stays && (key >= key_min || t == 0);
+          const int m = __syncthreads_count(stays);  // the first m: every rule keeps a leading part
+          if (t == m - 1) {
+            sh.kept_tau = key;
+            sh.kept_cut = (int)(unsigned int)mine;
+          }
+          // the draw: the kept tokens in the order of ids
+          __syncthreads();
+          sh.weight[t] = stays ? w : 0ull;
+          unsigned long long by_id = stays ? (mine << 32) | (unsigned int)t : ~0ull;
+          by_id = block_sort(by_id, m, sh.list);
+          __syncthreads();
+          w = t < m ? sh.weight[(unsigned int)by_id] : 0ull;
+          const unsigned long long run = block_scan_u64(w, s_red, sum);
+          const unsigned long long aim = (unsigned long long)((double)u * (double)sum);
+          if (t < m && run - w <= aim && aim < run) {  // one token
+            token = (int)(by_id >> 32);
+            a.token[b] = token;
+            int ignore = 0;
+            if (a.logprob) a.logprob[b] = log_share(sanitize_logit(a.logits[(long long)b * a.row_stride + token], ignore), sum);
+          }
+          __syncthreads();
+        }
+        if (!a.truncated) return;  // nobody reads another block's memory from here on
+        if (row.C > 1) {
+          cl_sync();
+          kept.tau = cl_ld_u32(cl_map(&sh.kept_tau, 0u));
+          kept.cut = cl_ld_s32(cl_map(&sh.kept_cut, 0u));
+        } else {
+          kept.tau = sh.kept_tau;
+          kept.cut = sh.kept_cut;
+        }
+        done = true;
+      } else if (by_count) {
+        kept = border<false>(row, a, kept, weigh, zm, step, x, target, s_red, &s_id);
+        if (by_mass) {
+          row.buf ^= 1;
+          h = sh.hist[row.buf];
+          row_sync(row.C);  // the histogram that is used next has been cleared, or never used
+          for (int i = t; i < kSaLimbs * kSaBins; i += kSaThreads) (&sh.hist[row.buf ^ 1][0][0])[i] = 0u;
+          for (int i = t; i < row.n; i += kSaThreads) {
+            const float z = s_z[i];
+            if (z > -INFINITY && kept(order_key(z), row.base + i)) add_mass(h, step_of(z, zm, step), weigh(z));
+          }
+          x = cross<true>(row, h, 0ull, p, &target, &all, s_red);
+          kept = border<true>(row, a, kept, weigh, zm, step, x, target, s_red, &s_id);
+        }
+      } else {
+        kept = border<true>(row, a, kept, weigh, zm, step, x, target, s_red, &s_id);
       }
     }
-    unsigned long long total = 0ull;
-    token = locate(row, a.slice, s_red, &s_id, [&](float z, int i) -> unsigned long long {
-      return kept(order_key(z), i) ? weigh(z) : 0ull;
-    }, 0ull, &total, true, u);
-    if (t == 0 && row.rank == 0 && a.logprob && token >= 0) {
-      const float z = a.logits[(long long)b * a.row_stride + token];
-      int ignore = 0;
-      const double depth = ((double)sanitize_logit(z, ignore) - (double)zm) / (double)T;
-      logprob = (float)(depth - log((double)total / (double)(1ll << kSaFrac)));
+    if (!done) {
+      if (key_min > order_key(zm)) {  // the largest token alone
+        kept.tau = order_key(zm);
+        kept.cut = (int)top;
+      } else if (key_min > kept.tau) {
+        kept.tau = key_min;
+        kept.cut = 0x7fffffff;
+      }
+      unsigned long long total = 0ull;
+      token = locate(row, a.slice, s_red, &s_id, [&](float z, int i) -> unsigned long long {
+        return kept(order_key(z), i) ? weigh(z) : 0ull;
+      }, 0ull, &total, true, u);
+      if (t == 0 && row.rank == 0) {
+        a.token[b] = token;
+        int ignore = 0;
+        if (a.logprob && token >= 0)
+          a.logprob[b] = log_share(sanitize_logit(a.logits[(long long)b * a.row_stride + token], ignore), total);
+      }
     }
+  }
+  if ((none || greedy) && t == 0 && row.rank == 0) {
+    a.token[b] = token;
+    if (a.logprob) a.logprob[b] = logprob;
   }
   if (a.truncated) {
     float *out = a.truncated + (long long)b * a.out_stride + row.base;
+#pragma unroll 4
     for (int i = t; i < row.n; i += kSaThreads) {
       const float z = s_z[i];
       out[i] = kept(order_key(z), row.base + i) ? z : -INFINITY;
     }
   }
-  if (t == 0 && row.rank == 0) {
-    a.token[b] = token;
-    if (a.logprob) a.logprob[b] = logprob;
-  }
-  cl_sync();  // no block leaves while another reads its memory
+  if (row.C > 1) cl_sync();  // no block leaves while another reads its memory
 }
 
 }  // namespace
@@ -467,8 +660,12 @@ extern "C" et_status et_sample(const et_sample_shape *s, const float *logits, co
   a.vec4 = et_aligned(logits, 16) && s->row_stride % 4 == 0;
   a.logits = logits; a.temperature = temperature; a.top_k = top_k; a.top_p = top_p; a.min_p = min_p;
   a.uniforms = uniforms; a.token = token; a.logprob = logprob; a.truncated = truncated; a.dev_status = dev_status;
-  int C = kSaMaxCluster;
-  while (C > 1 && s->V <= 4096 * (C / 2)) C /= 2;
+  // blocks of a row: as few as hold it, or more while every block of the call has an SM to itself
+  int C = 1, dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 152;
+  cudaGetLastError();
+  while ((s->V + C - 1) / C > kSaMaxSlice) C *= 2;
+  while (C < kSaMaxCluster && 2ll * C * s->B <= sms && s->V > 2048 * C) C *= 2;
   a.cluster = C;
   a.slice = ((s->V + C - 1) / C + 3) & ~3;
   const size_t smem = (size_t)a.slice * sizeof(float);
