@@ -91,11 +91,36 @@ __device__ __forceinline__ void row_sync(int C) {
 __device__ __forceinline__ float key_value(unsigned int key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
+// floor or ceil of f * m, exactly: f in [0, 1), m < 2^62 (fp64 arithmetic takes a sixtieth of fp32's rate)
+__device__ __forceinline__ unsigned long long fraction_of(float f, unsigned long long m, bool up) {
+  const unsigned int bits = __float_as_uint(f);
+  const int e = max((int)(bits >> 23), 1), s = 150 - e;  // f = q 2^-s, s >= 24
+  const unsigned long long q = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);
+  unsigned long long lo = q * m, hi = __umul64hi(q, m);
+  if (s >= 128) return up && q && m ? 1ull : 0ull;       // less than 2^86 / 2^128
+  const unsigned long long rest = s >= 64 ? lo | (hi & ((1ull << (s - 64)) - 1ull)) : lo & ((1ull << s) - 1ull);
+  const unsigned long long whole = s >= 64 ? (hi >> (s - 64)) : (hi << (64 - s)) | (lo >> s);
+  return whole + (up && rest ? 1ull : 0ull);
+}
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+
+// 2^(j / 64) in two fp32 numbers, by repeated products in fp64 (off by 2^-47 at most)
+struct PowerTable {
+  float hi[64], lo[64];
+  constexpr PowerTable() : hi(), lo() {
+    double x = 1.0;
+    for (int j = 0; j < 64; ++j) {
+      hi[j] = (float)x;
+      lo[j] = (float)(x - (double)hi[j]);
+      x *= 1.01088928605170046002;  // 2^(1 / 64)
+    }
+  }
+};
+__constant__ constexpr PowerTable kPowers{};
 
 // 2^44 * exp((z - zm) / T), rounded; ch + cl = log2(e) / T
 struct Weigher {
@@ -148,6 +173,16 @@ struct Row {
   int buf;          // histogram of the next pass
 };
 
+// A mass of every block of the row: their sum, and the sum of the blocks before this one.  Lane k reads block k's, so that
+// the reads of other blocks' memory run at once.
+__device__ __forceinline__ unsigned long long peers_mass(const Row &row, unsigned long long &before) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long m = 0ull;
+  if (lane < row.C) m = row.C > 1 ? cl_ld_u64(cl_map(&row.sh->mass, (uint32_t)lane)) : row.sh->mass;
+  before = warp_sum_u64(lane < row.rank ? m : 0ull);
+  return warp_sum_u64(m);
+}
+
 // Warp w of the block has tokens [w * span, ...) of the slice, in steps of 32.
 __device__ __forceinline__ int warp_span(int slice) { return ((slice + kSaWarps - 1) / kSaWarps + 31) & ~31; }
 
@@ -171,14 +206,10 @@ __device__ int locate(const Row &row, int slice, unsigned long long *s_red, int 
     *s_id = -1;
   }
   row_sync(row.C);
-  unsigned long long before = 0ull, all = 0ull;
-  for (int k = 0; k < row.C; ++k) {
-    const unsigned long long m = row.C > 1 ? cl_ld_u64(cl_map(&row.sh->mass, (uint32_t)k)) : row.sh->mass;
-    if (k < row.rank) before += m;
-    all += m;
-  }
+  unsigned long long before;
+  const unsigned long long all = peers_mass(row, before);
   if (total) *total = all;
-  if (fraction) target = (unsigned long long)((double)uniform * (double)all);
+  if (fraction) target = fraction_of(uniform, all, false);
   // this warp's tokens begin behind `before`
   for (int k = 0; k < warp; ++k) before += row.sh->warp_mass[k];
   if (before <= target && target < before + mine) {  // one warp of the cluster
@@ -206,27 +237,51 @@ __device__ int locate(const Row &row, int slice, unsigned long long *s_red, int 
   return id;
 }
 
-// inclusive sum over the block's threads in order; red holds kSaWarps
-__device__ __forceinline__ unsigned long long block_scan_u64(unsigned long long v, unsigned long long *red, unsigned long long &all) {
+// inclusive sums over the block's threads in order, of a mass and (if asked for) a count; red holds twice kSaWarps
+template <bool COUNT>
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned int n, unsigned long long *red,
+                                                         unsigned long long &all, unsigned int &incl_n, unsigned int &all_n) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned int *red_n = reinterpret_cast<unsigned int *>(red + kSaWarps);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned long long y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
+    const unsigned int yn = COUNT ? __shfl_up_sync(0xffffffffu, n, o) : 0u;
+    if (lane >= o) {
+      v += y;
+      n += yn;
+    }
   }
-  if (lane == 31) red[warp] = v;
+  if (lane == 31) {
+    red[warp] = v;
+    if (COUNT) red_n[warp] = n;
+  }
   __syncthreads();
   unsigned long long mine = red[lane];
+  unsigned int mine_n = COUNT ? red_n[lane] : 0u;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned long long y = __shfl_up_sync(0xffffffffu, mine, o);
-    if (lane >= o) mine += y;
+    const unsigned int yn = COUNT ? __shfl_up_sync(0xffffffffu, mine_n, o) : 0u;
+    if (lane >= o) {
+      mine += y;
+      mine_n += yn;
+    }
   }
   static_assert(kSaWarps == 32, "one warp scans the warps");
   all = __shfl_sync(0xffffffffu, mine, 31);
   const unsigned long long before = __shfl_sync(0xffffffffu, mine, (warp + 31) & 31);
+  if (COUNT) {
+    all_n = __shfl_sync(0xffffffffu, mine_n, 31);
+    const unsigned int before_n = __shfl_sync(0xffffffffu, mine_n, (warp + 31) & 31);
+    incl_n = n + (warp ? before_n : 0u);
+  }
   __syncthreads();
   return v + (warp ? before : 0ull);
+}
+__device__ __forceinline__ unsigned long long block_scan_u64(unsigned long long v, unsigned long long *red, unsigned long long &all) {
+  unsigned int n, all_n;
+  return block_scan<false>(v, 0u, red, all, n, all_n);
 }
 
 // The cluster's histogram `h`, its bins in order, and where the cumulative weight reaches `target` (share >= 0: that share
@@ -250,29 +305,27 @@ __device__ Crossing cross(const Row &row, unsigned int (*h)[kSaBins], unsigned l
     w = MASS ? (unsigned long long)l[0] + ((unsigned long long)l[1] << 15) + ((unsigned long long)l[2] << 30) : count;
   }
   // the sum over a bin's C threads comes out of a running sum over all of them
-  unsigned long long all, all_count;
-  const unsigned long long incl = block_scan_u64(w, s_red, all);
-  const unsigned long long incl_count = block_scan_u64(count, s_red, all_count);
+  unsigned long long all;
+  unsigned int incl_count, all_count;
+  const unsigned long long incl = block_scan<true>(w, count, s_red, all, incl_count, all_count);
   if (t == 0) {
     sh->mass = all;
-    sh->count = (unsigned int)all_count;
+    sh->count = all_count;
     sh->crossing.bin = -1;
   }
   row_sync(C);
-  unsigned long long before = above, sum = above;
+  unsigned long long before;
+  const unsigned long long sum = above + peers_mass(row, before);
+  before += above;
   unsigned int before_count = 0u;
-  for (int k = 0; k < C; ++k) {
-    const unsigned long long m = C > 1 ? cl_ld_u64(cl_map(&sh->mass, (uint32_t)k)) : sh->mass;
-    const unsigned int n = C > 1 ? cl_ld_u32(cl_map(&sh->count, (uint32_t)k)) : sh->count;
-    if (k < row.rank) {
-      before += m;
-      before_count += n;
-    }
-    sum += m;
+  {
+    const int lane = t & 31;
+    if (lane < row.rank) before_count = cl_ld_u32(cl_map(&sh->count, (uint32_t)lane));
+    before_count = __reduce_add_sync(0xffffffffu, before_count);
   }
   *all_mass = sum;
   if (share >= 0.f) {
-    *target = (unsigned long long)ceil((double)share * (double)sum);
+    *target = fraction_of(share, sum, true);
     if (*target < 1ull) *target = 1ull;
   }
   // the last of a bin's threads knows the weight up to its end; the bin before, up to its beginning
@@ -285,7 +338,7 @@ __device__ Crossing cross(const Row &row, unsigned int (*h)[kSaBins], unsigned l
     if (from < *target && *target <= to) {
       Crossing c;
       c.bin = row.rank * per + t / C;
-      c.upto = before_count + (unsigned int)incl_count;
+      c.upto = before_count + incl_count;
       c.above = from;
       for (int k = 0; k < C; ++k) {
         const uint32_t at = cl_map(&sh->crossing, (uint32_t)k);
@@ -336,10 +389,12 @@ __device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weig
     row_sync(row.C);
     lo = 0xffffffffu;
     hi = 0u;
-    for (int k = 0; k < row.C; ++k) {
-      lo = min(lo, row.C > 1 ? cl_ld_u32(cl_map(&sh->key_lo, (uint32_t)k)) : sh->key_lo);
-      hi = max(hi, row.C > 1 ? cl_ld_u32(cl_map(&sh->key_hi, (uint32_t)k)) : sh->key_hi);
+    if (lane < row.C) {
+      lo = row.C > 1 ? cl_ld_u32(cl_map(&sh->key_lo, (uint32_t)lane)) : sh->key_lo;
+      hi = row.C > 1 ? cl_ld_u32(cl_map(&sh->key_hi, (uint32_t)lane)) : sh->key_hi;
     }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
     if (lo >= hi) break;
     shift = max(0, 23 - __clz(hi - lo));  // at most 512 bins of 2^shift keys
     // the other histogram has been clear since the last pass; this pass clears the one before
@@ -373,6 +428,7 @@ __device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weig
 // v[0 .. n) ascending, n <= kSaThreads: a bitonic network, a value per thread
 __device__ unsigned long long block_sort(unsigned long long v, int n, unsigned long long *buf) {
   const int t = threadIdx.x;
+  const bool busy = (t & ~31) < n;  // whole warps; beyond the last value everything is at its place
   for (int k = 2; k < 2 * n; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
       unsigned long long o;
@@ -382,6 +438,7 @@ __device__ unsigned long long block_sort(unsigned long long v, int n, unsigned l
         __syncthreads();
         o = buf[t ^ j];
       } else {
+        if (!busy && k <= 32) continue;
         o = __shfl_xor_sync(0xffffffffu, v, j);
       }
       const bool low = ((t & j) == 0) == ((t & k) == 0);  // this thread takes the smaller one
@@ -394,9 +451,9 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   extern __shared__ __align__(16) float s_z[];
   __shared__ SampleShared sh;
   __shared__ float2 s_table[64];
-  __shared__ unsigned long long s_red[kSaWarps + 1];
+  __shared__ unsigned long long s_red[2 * kSaWarps];
   __shared__ int s_id;
-  __shared__ float s_f[32];
+  __shared__ float s_f[32], s_row[3];
   const int t = threadIdx.x, lane = t & 31;
   Row row;
   row.sh = &sh;
@@ -407,11 +464,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   row.n = max(0, min(a.slice, a.V - row.base));
   row.buf = 0;
   const int b = blockIdx.x / a.cluster;
-  if (t < 64) {
-    const double x = exp2((double)t / 64);
-    const float h = (float)x;
-    s_table[t] = make_float2(h, (float)(x - (double)h));
-  }
+  if (t < 64) s_table[t] = make_float2(kPowers.hi[t], kPowers.lo[t]);
   for (int x = t; x < 2 * kSaLimbs * kSaBins; x += kSaThreads) (&sh.hist[0][0][0])[x] = 0u;
   if (t == 0) sh.listed = 0u;
   pdl_wait();
@@ -462,12 +515,15 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   row_sync(row.C);
   float zm = -INFINITY, zl = INFINITY;
   unsigned int top = 0xffffffffu;
-  for (int x = 0; x < a.cluster; ++x) {
-    const float m = row.C > 1 ? cl_ld_f32(cl_map(&sh.zmax, (uint32_t)x)) : sh.zmax;
-    const unsigned int f = row.C > 1 ? cl_ld_u32(cl_map(&sh.first, (uint32_t)x)) : sh.first;
-    if (m > zm) { zm = m; top = f; }  // blocks hold ascending ids: the first one wins a tie
-    zl = fminf(zl, row.C > 1 ? cl_ld_f32(cl_map(&sh.zmin, (uint32_t)x)) : sh.zmin);
+  if (lane < row.C) {
+    zm = row.C > 1 ? cl_ld_f32(cl_map(&sh.zmax, (uint32_t)lane)) : sh.zmax;
+    zl = row.C > 1 ? cl_ld_f32(cl_map(&sh.zmin, (uint32_t)lane)) : sh.zmin;
+    top = row.C > 1 ? cl_ld_u32(cl_map(&sh.first, (uint32_t)lane)) : sh.first;
   }
+  const float mine_max = zm;
+  zm = warp_max(zm);
+  zl = -warp_max(-zl);
+  top = __reduce_min_sync(0xffffffffu, mine_max == zm ? top : 0xffffffffu);  // the lowest id of the largest
   if (odd && t == 0) flag_status(a.dev_status, ET_DEV_NONFINITE);
 
   u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
@@ -478,6 +534,22 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   int token = -1;
   float logprob = -INFINITY;
   T = fminf(fmaxf(T, 1e-30f), 1e30f);
+  // what takes fp64 arithmetic, by one thread
+  if (t == 0 && !none && !greedy) {
+    const double c = 1.4426950408889634074 / (double)T;
+    s_row[0] = (float)c;
+    s_row[1] = (float)(c - (double)(float)c);
+    unsigned int key_min = 0u;  // min-p: keys from this one on
+    if (mp > 0.f) {
+      // the smallest logit with (z - max) / T >= log(min_p)
+      const double depth = (double)T * log((double)mp);
+      float zf = (float)((double)zm + depth);
+      if ((double)zf - (double)zm < depth) zf = nextafterf(zf, INFINITY);
+      key_min = mp > 1.f || zf > zm ? 0xffffffffu : order_key(zf);
+    }
+    s_row[2] = __uint_as_float(key_min);
+  }
+  __syncthreads();
   auto log_share = [&](float z, unsigned long long total) -> float {
     return (float)(((double)z - (double)zm) / (double)T - log((double)total / (double)(1ll << kSaFrac)));
   };
@@ -490,21 +562,12 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
     kept.tau = order_key(zm);
     kept.cut = token;
   } else {
-    const double c = 1.4426950408889634074 / (double)T;
     Weigher weigh;
     weigh.zm = zm;
-    weigh.ch = (float)c;
-    weigh.cl = (float)(c - (double)weigh.ch);
+    weigh.ch = s_row[0];
+    weigh.cl = s_row[1];
     weigh.table = s_table;
-    // min-p: keys from this one on
-    unsigned int key_min = 0u;
-    if (mp > 0.f) {
-      // the smallest logit with (z - max) / T >= log(min_p)
-      const double depth = (double)T * log((double)mp);
-      float zf = (float)((double)zm + depth);
-      if ((double)zf - (double)zm < depth) zf = nextafterf(zf, INFINITY);
-      key_min = mp > 1.f || zf > zm ? 0xffffffffu : order_key(zf);
-    }
+    const unsigned int key_min = __float_as_uint(s_row[2]);
     const bool by_count = k > 0 && k < a.V, by_mass = p < 1.f;
     bool done = false;
     if (by_count || by_mass) {
@@ -548,7 +611,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
           const unsigned long long incl = block_scan_u64(w, s_red, sum);
           if (by_mass) {
             if (by_count) {
-              target = (unsigned long long)ceil((double)p * (double)sum);
+              target = fraction_of(p, sum, true);
               if (target < 1ull) target = 1ull;
             }
             stays = stays && incl - w < target;
@@ -567,7 +630,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
           __syncthreads();
           w = t < m ? sh.weight[(unsigned int)by_id] : 0ull;
           const unsigned long long run = block_scan_u64(w, s_red, sum);
-          const unsigned long long aim = (unsigned long long)((double)u * (double)sum);
+          const unsigned long long aim = fraction_of(u, sum, false);
           if (t < m && run - w <= aim && aim < run) {  // one token
             token = (int)(by_id >> 32);
             a.token[b] = token;
