@@ -28,14 +28,15 @@
 namespace et {
 namespace {
 
-constexpr int kSaThreads = 1024;
+constexpr int kSaThreads = 512;      // two blocks per SM: one's barriers under the other's arithmetic
 constexpr int kSaWarps = kSaThreads / 32;
 constexpr int kSaBins = 512;
-constexpr int kSaLimbs = 4;          // a mass of 45 bits in three sums of 15 bits, and a count
+constexpr int kSaLimbs = 3;          // a mass of 45 bits in three sums of 15 bits; a count is the first alone
 constexpr int kSaMaxCluster = 8;
 constexpr int kSaMaxSlice = 32768;   // tokens per block: 8 * 32768 = the largest vocabulary
+constexpr int kSaSlice = 20000;      // tokens per block that two blocks of an SM can hold
 constexpr int kSaFrac = 44;
-constexpr int kSaList = 1024;        // tokens that one block sorts
+constexpr int kSaList = 1024;        // tokens that one block sorts, two per thread
 
 struct SampleArgs {
   int B, V, slice, cluster;
@@ -50,7 +51,6 @@ struct SampleArgs {
 // where a cumulative weight passes a border
 struct Crossing {
   int bin;                               // -1: nowhere
-  unsigned int upto;                     // tokens of this bin and those above
   unsigned long long above;              // weight of the bins above
 };
 // what a block's peers read and write of it
@@ -60,13 +60,11 @@ struct SampleShared {
   int odd;
   unsigned int key_lo, key_hi;           // of the slice's members of the current bin
   unsigned long long mass;               // of the slice's kept tokens, or of the block's share of the bins
-  unsigned int count;
   Crossing crossing;
-  unsigned int listed;                   // tokens in the list (block 0)
+  unsigned int listed;                   // tokens for the list, which takes kSaList (block 0)
   unsigned int kept_tau;
   int kept_cut;
   unsigned long long warp_mass[kSaWarps];
-  unsigned int warp_count[kSaWarps];
   unsigned int hist[2][kSaLimbs][kSaBins];  // alternating: a pass clears the other one
   unsigned long long list[kSaList], weight[kSaList];
 };
@@ -133,29 +131,33 @@ struct Weigher {
     const float err = (z - (s - back)) - (zm + back);
     float e = fmaf(s, ch, -p);
     e = fmaf(err, ch, fmaf(s, cl, e));                         // the exponent is p + e
-    const float k = rintf(p * 64.f), r = fmaf(k, -0.015625f, p);
+    // k = round(64 p): the sum's last bits hold it (1.5 2^23)
+    const float kk = fmaf(p, 64.f, 12582912.f);
+    const float r = fmaf(kk - 12582912.f, -0.015625f, p);
     const float yh = r + e, yl = e - (yh - r);
     // u = y ln 2
     const float L1 = 0.693147182464599609375f, L2 = -1.904654299957767e-9f;
     const float uh = yh * L1, ul = fmaf(yl, L1, fmaf(yh, L2, fmaf(yh, L1, -uh)));
     const float q = fmaf(uh * uh, fmaf(uh, fmaf(uh, 0.041666667f, 0.16666667f), 0.5f), ul);  // exp(u) - 1 - uh
-    const int ki = (int)k;
+    const int ki = __float_as_int(kk) - 0x4b400000;
     const float2 t = table[ki & 63];
     const float a = t.x * uh, al = fmaf(t.x, uh, -a);
     const float wh = t.x + a, wl = (a - (wh - t.x)) + (fmaf(t.x, q, al) + fmaf(t.y, uh, t.y));
-    const long long w = ((long long)__float2int_rn(wh * 16777216.f) << (kSaFrac - 24)) + __float2int_rn(wl * 17592186044416.f);
+    // wh, between 1/2 and 2, in units of 2^-24 from its bits; wl, below 2^-15, in units of 2^-37
+    const int d = __float_as_int(wh) - 0x3f800000, ih = 0x1000000 + (d < 0 ? d : 2 * d);
+    const int il = __float_as_int(fmaf(wl, 137438953472.f, 12582912.f)) - 0x4b400000;
+    const long long w = ((long long)ih << (kSaFrac - 24)) + ((long long)il << (kSaFrac - 37));
     const int n = -(ki >> 6);  // 0..46
     return (unsigned long long)(n ? (w + (1ll << (n - 1))) >> n : w);
   }
 };
 
-// a token's mass, in three limbs of which the high ones are rarely there, and count into a bin
+// a token's mass into a bin, in three limbs of which the high ones are rarely there
 __device__ __forceinline__ void add_mass(unsigned int (*h)[kSaBins], int bin, unsigned long long w) {
   const unsigned int l0 = (unsigned int)w & 0x7fffu, l1 = (unsigned int)(w >> 15) & 0x7fffu, l2 = (unsigned int)(w >> 30);
   if (l0) atomicAdd(&h[0][bin], l0);
   if (l1) atomicAdd(&h[1][bin], l1);
   if (l2) atomicAdd(&h[2][bin], l2);
-  atomicAdd(&h[3][bin], 1u);
 }
 
 // what is kept: keys above tau, and of those equal to it ids up to cut
@@ -257,10 +259,10 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
     if (COUNT) red_n[warp] = n;
   }
   __syncthreads();
-  unsigned long long mine = red[lane];
-  unsigned int mine_n = COUNT ? red_n[lane] : 0u;
+  unsigned long long mine = lane < kSaWarps ? red[lane] : 0ull;
+  unsigned int mine_n = COUNT && lane < kSaWarps ? red_n[lane] : 0u;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < kSaWarps; o <<= 1) {
     const unsigned long long y = __shfl_up_sync(0xffffffffu, mine, o);
     const unsigned int yn = COUNT ? __shfl_up_sync(0xffffffffu, mine_n, o) : 0u;
     if (lane >= o) {
@@ -268,11 +270,10 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
       mine_n += yn;
     }
   }
-  static_assert(kSaWarps == 32, "one warp scans the warps");
-  all = __shfl_sync(0xffffffffu, mine, 31);
+  all = __shfl_sync(0xffffffffu, mine, kSaWarps - 1);
   const unsigned long long before = __shfl_sync(0xffffffffu, mine, (warp + 31) & 31);
   if (COUNT) {
-    all_n = __shfl_sync(0xffffffffu, mine_n, 31);
+    all_n = __shfl_sync(0xffffffffu, mine_n, kSaWarps - 1);
     const unsigned int before_n = __shfl_sync(0xffffffffu, mine_n, (warp + 31) & 31);
     incl_n = n + (warp ? before_n : 0u);
   }
@@ -288,43 +289,32 @@ __device__ __forceinline__ unsigned long long block_scan_u64(unsigned long long 
 // of the sum, rounded up, one at least).  Block r adds up its share of the bins over the blocks.
 template <bool MASS>
 __device__ Crossing cross(const Row &row, unsigned int (*h)[kSaBins], unsigned long long above, float share,
-                          unsigned long long *target, unsigned long long *all_mass, unsigned long long *s_red) {
+                          unsigned long long *target, unsigned long long *s_red) {
   SampleShared *sh = row.sh;
   const int t = threadIdx.x, C = row.C, per = kSaBins / C;
   row_sync(C);  // every block's histogram is whole
   unsigned long long w = 0ull;
-  unsigned int count = 0u;
+  static_assert(kSaBins <= kSaThreads, "a thread per bin and block");
   if (t < kSaBins) {  // bin t / C of the share, as block t % C has it
     const int bin = row.rank * per + t / C;
     const uint32_t k = (uint32_t)(t % C);
     unsigned int l[kSaLimbs];
 #pragma unroll
-    for (int x = 0; x < kSaLimbs; ++x)
-      l[x] = !MASS && x < 3 ? 0u : C > 1 ? cl_ld_u32(cl_map(&h[x][bin], k)) : h[x][bin];
-    count = l[3];
-    w = MASS ? (unsigned long long)l[0] + ((unsigned long long)l[1] << 15) + ((unsigned long long)l[2] << 30) : count;
+    for (int x = 0; x < kSaLimbs; ++x) l[x] = !MASS && x ? 0u : C > 1 ? cl_ld_u32(cl_map(&h[x][bin], k)) : h[x][bin];
+    w = (unsigned long long)l[0] + ((unsigned long long)l[1] << 15) + ((unsigned long long)l[2] << 30);
   }
   // the sum over a bin's C threads comes out of a running sum over all of them
   unsigned long long all;
-  unsigned int incl_count, all_count;
-  const unsigned long long incl = block_scan<true>(w, count, s_red, all, incl_count, all_count);
+  const unsigned long long incl = block_scan_u64(w, s_red, all);
   if (t == 0) {
     sh->mass = all;
-    sh->count = all_count;
     sh->crossing.bin = -1;
   }
   row_sync(C);
   unsigned long long before;
-  const unsigned long long sum = above + peers_mass(row, before);
+  const unsigned long long sum = peers_mass(row, before);
   before += above;
-  unsigned int before_count = 0u;
-  {
-    const int lane = t & 31;
-    if (lane < row.rank) before_count = cl_ld_u32(cl_map(&sh->count, (uint32_t)lane));
-    before_count = __reduce_add_sync(0xffffffffu, before_count);
-  }
-  *all_mass = sum;
-  if (share >= 0.f) {
+  if (MASS && share >= 0.f) {
     *target = fraction_of(share, sum, true);
     if (*target < 1ull) *target = 1ull;
   }
@@ -338,12 +328,10 @@ __device__ Crossing cross(const Row &row, unsigned int (*h)[kSaBins], unsigned l
     if (from < *target && *target <= to) {
       Crossing c;
       c.bin = row.rank * per + t / C;
-      c.upto = before_count + incl_count;
       c.above = from;
       for (int k = 0; k < C; ++k) {
         const uint32_t at = cl_map(&sh->crossing, (uint32_t)k);
         asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at + 8u), "l"(c.above) : "memory");
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + 4u), "r"(c.upto) : "memory");
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(c.bin) : "memory");
       }
     }
@@ -405,11 +393,10 @@ __device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weig
       const unsigned int key = order_key(z);
       if (z == -INFINITY || key < lo || key > hi || !in(key, row.base + i)) continue;
       if (MASS) add_mass(h, bin_of(key, z), weigh(z));
-      else atomicAdd(&h[3][bin_of(key, z)], 1u);
+      else atomicAdd(&h[0][bin_of(key, z)], 1u);
     }
     for (int x = t; x < kSaLimbs * kSaBins; x += kSaThreads) (&sh->hist[row.buf ^ 1][0][0])[x] = 0u;
-    unsigned long long all;
-    c = cross<MASS>(row, h, c.above, -1.f, &target, &all, s_red);
+    c = cross<MASS>(row, h, c.above, -1.f, &target, s_red);
   }
   // one key value: the first of its tokens, in ascending id, up to the border
   Kept out;
@@ -425,26 +412,36 @@ __device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weig
   return out;
 }
 
-// v[0 .. n) ascending, n <= kSaThreads: a bitonic network, a value per thread
-__device__ unsigned long long block_sort(unsigned long long v, int n, unsigned long long *buf) {
+// v[e] of thread t, number t + e * kSaThreads of n, ascending: a bitonic network; beyond n everything is ~0
+__device__ void block_sort(unsigned long long (&v)[2], int n, unsigned long long *buf) {
   const int t = threadIdx.x;
-  const bool busy = (t & ~31) < n;  // whole warps; beyond the last value everything is at its place
+  const int count = n > kSaThreads ? 2 : 1;
   for (int k = 2; k < 2 * n; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
-      unsigned long long o;
+      if (j == kSaThreads) {
+        if (v[1] < v[0]) {
+          const unsigned long long x = v[0];
+          v[0] = v[1];
+          v[1] = x;
+        }
+        continue;
+      }
       if (j >= 32) {
         __syncthreads();
-        buf[t] = v;
+        for (int e = 0; e < count; ++e) buf[t + e * kSaThreads] = v[e];
         __syncthreads();
-        o = buf[t ^ j];
-      } else {
-        if (!busy && k <= 32) continue;
-        o = __shfl_xor_sync(0xffffffffu, v, j);
+      } else if (k <= 32 && (t & ~31) >= n) {
+        continue;  // whole warps
       }
-      const bool low = ((t & j) == 0) == ((t & k) == 0);  // this thread takes the smaller one
-      v = low == (o < v) ? o : v;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (e >= count) break;
+        const int i = t + e * kSaThreads;
+        const unsigned long long o = j >= 32 ? buf[i ^ j] : __shfl_xor_sync(0xffffffffu, v[e], j);
+        const bool low = ((i & j) == 0) == ((i & k) == 0);  // this place takes the smaller one
+        v[e] = low == (o < v[e]) ? o : v[e];
+      }
     }
-  return v;
 }
 
 __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
@@ -575,16 +572,19 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
       const float range = fminf(zm - zl, fmaxf(32.f * T, 32.f));
       const float step = range > 0.f ? (float)(kSaBins - 1) / range : 0.f;
       unsigned int (*h)[kSaBins] = sh.hist[0];
+      unsigned long long target = by_count ? (unsigned long long)k : 0ull;
+#pragma unroll 2
       for (int i = t; i < row.n; i += kSaThreads) {
         const float z = s_z[i];
         if (z == -INFINITY) continue;
-        if (by_count) atomicAdd(&h[3][step_of(z, zm, step)], 1u);
-        else add_mass(h, step_of(z, zm, step), weigh(z));
+        const int at = step_of(z, zm, step);
+        if (by_count) atomicAdd(&h[0][at], 1u);
+        else add_mass(h, at, weigh(z));
       }
-      unsigned long long target = by_count ? (unsigned long long)k : 0ull, all = 0ull;
-      Crossing x = by_count ? cross<false>(row, h, 0ull, -1.f, &target, &all, s_red) : cross<true>(row, h, 0ull, p, &target, &all, s_red);
-      if (x.bin >= 0 && x.upto <= kSaList) {
-        // ---- few tokens: block 0 sorts them ----
+      Crossing x = by_count ? cross<false>(row, h, 0ull, -1.f, &target, s_red) : cross<true>(row, h, 0ull, p, &target, s_red);
+      unsigned int listed = ~0u;
+      if (x.bin >= 0) {
+        // ---- the tokens up to the border's step go to block 0, if they are few ----
         for (int i0 = 0; i0 < row.n; i0 += kSaThreads) {
           const int i = i0 + t;
           const float z = i < row.n ? s_z[i] : -INFINITY;
@@ -597,49 +597,74 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
             asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(n), "r"((unsigned int)__popc(m)) : "memory");
           }
           at = __shfl_sync(0xffffffffu, at, 0) + (unsigned int)__popc(m & ((1u << lane) - 1u));
-          if (in)
+          if (in && at < kSaList)
             cl_st_u64(cl_map(&sh.list[0], 0u) + 8u * at, ((unsigned long long)~order_key(z) << 32) | (unsigned int)(row.base + i));
         }
         row_sync(row.C);
+        listed = row.C > 1 ? cl_ld_u32(cl_map(&sh.listed, 0u)) : sh.listed;
+      }
+      if (listed <= kSaList) {
+        // ---- one block sorts them and answers everything ----
         if (row.rank == 0) {
-          const int n = (int)x.upto;
-          unsigned long long mine = t < n ? sh.list[t] : ~0ull;
-          mine = block_sort(mine, n, sh.weight);
-          const unsigned int key = ~(unsigned int)(mine >> 32);
-          bool stays = t < n && !(by_count && t >= k);
-          unsigned long long w = stays ? weigh(key_value(key)) : 0ull, sum;
-          const unsigned long long incl = block_scan_u64(w, s_red, sum);
-          if (by_mass) {
-            if (by_count) {
-              target = fraction_of(p, sum, true);
-              if (target < 1ull) target = 1ull;
-            }
-            stays = stays && incl - w < target;
+          const int n = (int)listed, places = n > kSaThreads ? 2 : 1;
+          unsigned long long mine[2], w[2], incl[2], sum = 0ull;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = t + e * kSaThreads;
+            mine[e] = i < n ? sh.list[i] : ~0ull;
           }
-          stays = stays && (key >= key_min || t == 0);
-          const int m = __syncthreads_count(stays);  // the first m: every rule keeps a leading part
-          if (t == m - 1) {
-            sh.kept_tau = key;
-            sh.kept_cut = (int)(unsigned int)mine;
+          block_sort(mine, n, sh.weight);
+          for (int e = 0; e < places; ++e) {
+            const int i = t + e * kSaThreads;
+            w[e] = i < n && !(by_count && i >= k) ? weigh(key_value(~(unsigned int)(mine[e] >> 32))) : 0ull;
+            unsigned long long all;
+            incl[e] = sum + block_scan_u64(w[e], s_red, all);
+            sum += all;
+          }
+          if (by_mass && by_count) {
+            target = fraction_of(p, sum, true);
+            if (target < 1ull) target = 1ull;
+          }
+          int m = 0;  // how many stay: every rule keeps a leading part
+          for (int e = 0; e < places; ++e) {
+            const int i = t + e * kSaThreads;
+            const unsigned int key = ~(unsigned int)(mine[e] >> 32);
+            m += __syncthreads_count(i < n && !(by_count && i >= k) && (!by_mass || incl[e] - w[e] < target) && (key >= key_min || i == 0));
           }
           // the draw: the kept tokens in the order of ids
-          __syncthreads();
-          sh.weight[t] = stays ? w : 0ull;
-          unsigned long long by_id = stays ? (mine << 32) | (unsigned int)t : ~0ull;
-          by_id = block_sort(by_id, m, sh.list);
-          __syncthreads();
-          w = t < m ? sh.weight[(unsigned int)by_id] : 0ull;
-          const unsigned long long run = block_scan_u64(w, s_red, sum);
-          const unsigned long long aim = fraction_of(u, sum, false);
-          if (t < m && run - w <= aim && aim < run) {  // one token
-            token = (int)(by_id >> 32);
-            a.token[b] = token;
-            int ignore = 0;
-            if (a.logprob) a.logprob[b] = log_share(sanitize_logit(a.logits[(long long)b * a.row_stride + token], ignore), sum);
+          for (int e = 0; e < places; ++e) {
+            const int i = t + e * kSaThreads;
+            if (i == m - 1) {
+              sh.kept_tau = ~(unsigned int)(mine[e] >> 32);
+              sh.kept_cut = (int)(unsigned int)mine[e];
+            }
+            sh.weight[i] = w[e];
+            mine[e] = i < m ? (mine[e] << 32) | (unsigned int)i : ~0ull;
           }
+          block_sort(mine, m, sh.list);
+          __syncthreads();
+          unsigned long long all = 0ull;
+          for (int e = 0; e < places; ++e) {
+            const int i = t + e * kSaThreads;
+            w[e] = i < m ? sh.weight[(unsigned int)mine[e]] : 0ull;
+            unsigned long long part;
+            incl[e] = all + block_scan_u64(w[e], s_red, part);
+            all += part;
+          }
+          const unsigned long long aim = fraction_of(u, all, false);
+          for (int e = 0; e < places; ++e)
+            if (t + e * kSaThreads < m && incl[e] - w[e] <= aim && aim < incl[e]) {  // one token
+              token = (int)(mine[e] >> 32);
+              a.token[b] = token;
+              int ignore = 0;
+              if (a.logprob) a.logprob[b] = log_share(sanitize_logit(a.logits[(long long)b * a.row_stride + token], ignore), all);
+            }
           __syncthreads();
         }
-        if (!a.truncated) return;  // nobody reads another block's memory from here on
+        if (!a.truncated) {
+          if (row.C > 1) cl_sync();  // block 0's memory has been read
+          return;
+        }
         if (row.C > 1) {
           cl_sync();
           kept.tau = cl_ld_u32(cl_map(&sh.kept_tau, 0u));
@@ -660,7 +685,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
             const float z = s_z[i];
             if (z > -INFINITY && kept(order_key(z), row.base + i)) add_mass(h, step_of(z, zm, step), weigh(z));
           }
-          x = cross<true>(row, h, 0ull, p, &target, &all, s_red);
+          x = cross<true>(row, h, 0ull, p, &target, s_red);
           kept = border<true>(row, a, kept, weigh, zm, step, x, target, s_red, &s_id);
         }
       } else {
@@ -723,11 +748,12 @@ extern "C" et_status et_sample(const et_sample_shape *s, const float *logits, co
   a.vec4 = et_aligned(logits, 16) && s->row_stride % 4 == 0;
   a.logits = logits; a.temperature = temperature; a.top_k = top_k; a.top_p = top_p; a.min_p = min_p;
   a.uniforms = uniforms; a.token = token; a.logprob = logprob; a.truncated = truncated; a.dev_status = dev_status;
-  // blocks of a row: as few as hold it, or more while every block of the call has an SM to itself
+  // blocks of a row: slices of at most kSaSlice tokens, so that two blocks fit an SM, or less while every block of the call has
+  // an SM to itself
   int C = 1, dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 152;
   cudaGetLastError();
-  while ((s->V + C - 1) / C > kSaMaxSlice) C *= 2;
+  while (C < kSaMaxCluster && (s->V + C - 1) / C > kSaSlice) C *= 2;
   while (C < kSaMaxCluster && 2ll * C * s->B <= sms && s->V > 2048 * C) C *= 2;
   a.cluster = C;
   a.slice = ((s->V + C - 1) / C + 3) & ~3;
