@@ -784,14 +784,13 @@ def et_tree_attention_paged(shape: PagedAttnShape, cache: PagedCache, block_tabl
 # ---------------------------------------------------------------------------
 # around the step: a prompt's rows, their positions, the drawn token
 # ---------------------------------------------------------------------------
-def _rows(t: torch.Tensor, dtype, shape, device: int, what: str) -> int:
-    """The stride from row to row of a [rows, H, d] tensor whose heads are contiguous."""
-    rows, H, d = shape
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or t.stride(2) != 1 or \
-            (H > 1 and t.stride(1) != d):
-        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} with contiguous heads on CUDA device "
-                         f"{device}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-    return t.stride(0) if rows > 1 else H * d  # one row: its stride may be anything
+def _refuse_rows(device: int, *args) -> None:
+    """Name the [rows, H, d] tensor that the caller's check found wrong: heads contiguous, rows any stride apart."""
+    for t, dtype, shape, what in args:
+        s = t.stride()
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != device or s[2] != 1 or (shape[1] > 1 and s[1] != shape[2]):
+            raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} with contiguous heads on CUDA device "
+                             f"{device}, got {t.dtype} {tuple(t.shape)}, strides {s}, on {t.device}")
 
 
 @dataclasses.dataclass(frozen=True)
@@ -835,10 +834,16 @@ def et_chunk_attention_paged(shape: ChunkAttnShape, cache: PagedCache, block_tab
                              ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
                              stream=None) -> None:
     """Causal attention of each sequence's new rows (packed, ``row_start``) over its paged 8-bit prefix and themselves."""
-    dev = cache.device
+    dev, d = cache.device, cache.d
     _, dt, B, table, starts, rows, new, sums = shape.for_cache(cache)
-    strides = (_rows(q, dt, rows, dev, "q"), _rows(k_new, dt, new, dev, "k_new"), _rows(v_new, dt, new, dev, "v_new"))
-    ref = shape.for_cache(cache, strides)[0]
+    if not (q.dtype is k_new.dtype is v_new.dtype is dt and q.shape == rows and k_new.shape == new and v_new.shape == new
+            and q.get_device() == k_new.get_device() == v_new.get_device() == dev):
+        _refuse_rows(dev, (q, dt, rows, "q"), (k_new, dt, new, "k_new"), (v_new, dt, new, "v_new"))
+    (sq, hq, eq), (sk, hk, ek), (sv, hv, ev) = q.stride(), k_new.stride(), v_new.stride()
+    if not (eq == ek == ev == 1 and (hq == d or rows[1] == 1) and (hk == hv == d or new[1] == 1)):
+        _refuse_rows(dev, (q, dt, rows, "q"), (k_new, dt, new, "k_new"), (v_new, dt, new, "v_new"))
+    # one row: its stride may be anything
+    ref = shape.for_cache(cache, (sq, sk, sv) if shape.rows > 1 else None)[0]
     if not (block_table.dtype is prefix_len.dtype is row_start.dtype is _i32 and out.dtype is dt
             and block_table.shape == table and prefix_len.shape == B and row_start.shape == starts and out.shape == rows
             and block_table.get_device() == prefix_len.get_device() == row_start.get_device() == out.get_device() == dev
@@ -877,24 +882,41 @@ class RotaryShape(_Kept):
     factor: float = 1.0
 
     def with_strides(self, strides):
+        """The C struct with the rows' strides (of q, k, q_out and k_out) filled in, and the tensors' shapes."""
         def make():
-            return ctypes.byref(RotaryShapeC(self.rows, self.Hq, self.Hkv, self.d, self.rot or self.d, self.layout,
-                                             self.dtype, self.factor, *strides))
+            rot = self.rot or self.d
+            c = RotaryShapeC(self.rows, self.Hq, self.Hkv, self.d, rot, self.layout, self.dtype, self.factor, *strides)
+            return (ctypes.byref(c), _TORCH_DTYPE[self.dtype], (self.rows,), (rot // 2,), (self.rows, self.Hq, self.d),
+                    (self.rows, self.Hkv, self.d))
         return _kept(self, strides, make)
 
 
 def et_rotary(shape: RotaryShape, positions: torch.Tensor, freq: torch.Tensor, q: torch.Tensor, q_out: torch.Tensor,
               k: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None) -> None:
     """Turn q and k (``[rows, H, d]``, rows any stride apart) at ``positions``; outputs may be the inputs themselves."""
-    dt, dev = _TORCH_DTYPE[shape.dtype], positions.get_device()
     if (k is None) != (k_out is None) or (k is None) != (shape.Hkv == 0):
         raise ValueError("k and k_out go with Hkv heads")
-    qs, ks = (shape.rows, shape.Hq, shape.d), (shape.rows, shape.Hkv, shape.d)
-    strides = (_rows(q, dt, qs, dev, "q"), 0 if k is None else _rows(k, dt, ks, dev, "k"),
-               _rows(q_out, dt, qs, dev, "q_out"), 0 if k is None else _rows(k_out, dt, ks, dev, "k_out"))
-    _call("et_rotary", dev, stream, shape.with_strides(strides),
-          _arg(positions, _i32, (shape.rows,), dev, "positions"),
-          _arg(freq, torch.float64, ((shape.rot or shape.d) // 2,), dev, "freq"), q.data_ptr(),
+    dev, d = positions.get_device(), shape.d
+    a, b = q.stride(), q_out.stride()
+    c, e = (k.stride(), k_out.stride()) if k is not None else ((0, d, 1), (0, d, 1))
+    if shape.rows > 1:
+        strides = (a[0], c[0], b[0], e[0])
+    else:  # one row: its stride may be anything
+        strides = (shape.Hq * d, shape.Hkv * d, shape.Hq * d, shape.Hkv * d)
+    ref, dt, n, half, qs, ks = shape.with_strides(strides)
+    if not (q.dtype is q_out.dtype is dt and q.shape == qs and q_out.shape == qs and a[-1] == b[-1] == c[-1] == e[-1] == 1
+            and (a[1] == b[1] == d or qs[1] == 1) and (c[1] == e[1] == d or ks[1] == 1)
+            and (k is None or (k.dtype is k_out.dtype is dt and k.shape == ks and k_out.shape == ks
+                               and k.get_device() == k_out.get_device() == dev))
+            and positions.dtype is _i32 and positions.shape == n and freq.dtype is torch.float64 and freq.shape == half
+            and q.get_device() == q_out.get_device() == freq.get_device() == dev
+            and positions.is_contiguous() and freq.is_contiguous()):
+        _arg(positions, _i32, n, dev, "positions")
+        _arg(freq, torch.float64, half, dev, "freq")
+        _refuse_rows(dev, (q, dt, qs, "q"), (q_out, dt, qs, "q_out"),
+                     *(() if k is None else ((k, dt, ks, "k"), (k_out, dt, ks, "k_out"))))
+        raise ValueError("arguments must be tensors on one CUDA device")
+    _call("et_rotary", dev, stream, ref, positions.data_ptr(), freq.data_ptr(), q.data_ptr(),
           None if k is None else k.data_ptr(), q_out.data_ptr(), None if k is None else k_out.data_ptr())
 
 
@@ -907,16 +929,17 @@ def et_sample(logits: torch.Tensor, uniforms: torch.Tensor, token: torch.Tensor,
     dev = logits.get_device()
     for t, what in ((logits, "logits"), (truncated, "truncated")):
         if t is not None and (t.dim() != 2 or t.dtype is not _f32 or t.shape != logits.shape or t.get_device() != dev
-                              or (t.shape[1] > 1 and t.stride(1) != 1)):
+                              or (t.stride(1) != 1 and t.shape[1] > 1)):
             raise ValueError(f"{what} must be an fp32 CUDA [B, V] tensor with unit inner stride")
     B, V = logits.shape
     n = (B,)
-
-    def stride(t):
-        return t.stride(0) if B > 1 else V
-    c = SampleShapeC(B, V, stride(logits), 0 if truncated is None else stride(truncated))
-    _call("et_sample", dev, stream, ctypes.byref(c), logits.data_ptr(), _arg(temperature, _f32, n, dev, "temperature"),
-          _arg(top_k, _i32, n, dev, "top_k"), _arg(top_p, _f32, n, dev, "top_p"), _arg(min_p, _f32, n, dev, "min_p"),
-          _arg(uniforms, _f32, n, dev, "uniforms"), _arg(token, _i32, n, dev, "token"),
-          _arg(logprob, _f32, n, dev, "logprob"), None if truncated is None else truncated.data_ptr(),
+    for t, dt, what in ((uniforms, _f32, "uniforms"), (token, _i32, "token"), (temperature, _f32, "temperature"),
+                        (top_k, _i32, "top_k"), (top_p, _f32, "top_p"), (min_p, _f32, "min_p"), (logprob, _f32, "logprob")):
+        if t is not None and (t.dtype is not dt or t.shape != n or t.get_device() != dev or not t.is_contiguous()):
+            _arg(t, dt, n, dev, what)
+    c = SampleShapeC(B, V, logits.stride(0) if B > 1 else V, 0 if truncated is None else truncated.stride(0) if B > 1 else V)
+    _call("et_sample", dev, stream, ctypes.byref(c), logits.data_ptr(), None if temperature is None else temperature.data_ptr(),
+          None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+          None if min_p is None else min_p.data_ptr(), uniforms.data_ptr(), token.data_ptr(),
+          None if logprob is None else logprob.data_ptr(), None if truncated is None else truncated.data_ptr(),
           None if dev_status is None else _status(dev_status, dev))
