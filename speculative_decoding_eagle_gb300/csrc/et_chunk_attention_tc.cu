@@ -76,7 +76,8 @@ enum {
   C_QFREE = C_PVDONE + 2,             // the prefix's score products have run: q and the K ring are free
   C_QFULL = C_QFREE + 1,              // q in bf16
   C_SCALES = C_QFULL + 1,             // eight slots: a tile's scales are there
-  C_DRAIN = C_SCALES + kCtSlots,      // two
+  C_QRAW = C_SCALES + kCtSlots,       // q has landed as it is
+  C_DRAIN = C_QRAW + 1,               // two
   C_COUNT = C_DRAIN + 2
 };
 static_assert(C_COUNT * 8 <= 512, "barriers");
@@ -144,6 +145,7 @@ struct ChunkTcArgs {
   ChunkArgs c;
   int S;                 // parts of a block's tiles at most
   int tiles;             // tiles of 256 rows per KV head in the grid
+  int q_tma;             // q by TMA: the heads of a group divide a tile's 128 rows
   int box;               // rows per TMA box of a page
   unsigned int *cnt;     // arrival counters (null with S = 1)
   float2 *part_ml;
@@ -163,6 +165,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(kCtThreads, 1)
     k_chunk_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
+               const __grid_constant__ CUtensorMap tm_q,
                const __grid_constant__ ChunkTcArgs ca) {
   using Sh = CtShape<D>;
   const PagedAttnArgs &a = ca.c.a;
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 
   // ---- set-up that touches no global memory ----
   if (t < C_COUNT) {
-    const bool warps = (t >= C_VEMPTY && t < C_VTMA) || (t >= C_VHFULL && t < C_VHFREE) || (t >= C_PFULL && t < C_PVDONE) || t == C_QFULL;
+    const bool warps = (t >= C_VEMPTY && t < C_VTMA) || (t >= C_VHFULL && t < C_VHFREE) || (t >= C_PFULL && t < C_PVDONE) || (t == C_QFULL && !ca.q_tma);
     mbar_init(bar(t), warps ? 4u : 1u);  // the warps of a group, or one
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (t == C_COUNT) {
@@ -187,14 +190,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     s_odd = 0;
     s_seq = -1;
     s_longest = 0;
-  } else if (warp == 3 && lane < 4) {
-    prefetch_tmap(lane == 0 ? &tm_k : lane == 1 ? &tm_v : lane == 2 ? &tm_kn : &tm_vn);
+  } else if (warp == 3 && lane < 5) {
+    prefetch_tmap(lane == 0 ? &tm_k : lane == 1 ? &tm_v : lane == 2 ? &tm_kn : lane == 3 ? &tm_vn : &tm_q);
   }
   __syncthreads();
   pdl_wait();  // the previous kernel in the stream has completed
 
   // ---- which rows: tile `index` of the batch's tiles of 256 rows, in the sequences' order ----
-  const int part = blockIdx.x % ca.S, unit = blockIdx.x / ca.S;
+  const int unit = ca.S == 1 ? blockIdx.x : blockIdx.x / ca.S, part = blockIdx.x - unit * ca.S;
   const int index = unit / a.Hkv, g = unit - index * a.Hkv;
   int bad = 0;
   {
@@ -266,8 +269,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   const bool shared_rows = uni(real <= 128) != 0;                            // both groups have the same rows
   const int tok_first = ct_token(ca, R0), tok_last = ct_token(ca, R0 + real - 1);
   const int Tp = tiles_of(L, kCtKeys), To = tok_last / kCtKeys + 1, T = Tp + To;
-  const int per = max((s_longest + ca.S - 1) / ca.S, 1);
-  const int parts = (T + per - 1) / per;
+  const int per = ca.S == 1 ? T : max((s_longest + ca.S - 1) / ca.S, 1);
+  const int parts = ca.S == 1 ? 1 : (T + per - 1) / per;
   if (part >= parts) return;
   const int t0 = part * per, t1 = min(T, t0 + per);
   const int n8 = uni(max(0, min(t1, Tp) - t0));                         // tiles of the prefix
@@ -377,73 +380,25 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   };
   constexpr int kLanes = D / 8;  // of a row, eight dims each
   const int qrows = shared_rows ? 128 : 256;
-  float *row_f = reinterpret_cast<float *>(sm + Sh::off_v8 + Sh::tile8);  // [256], read before V's second stage is loaded
-  if (warp < kCtTmaWarp) {
-    // The rows come by asynchronous copies to where V's fp16 tiles will be (bf16 rows to their place), each thread then takes what it copied
-    constexpr int count = kCtTmaWarp * 32;
-    auto place16 = [&](int x) -> uint32_t {
-      const int r = x / kLanes, c = x % kLanes;
-      return sb + Sh::off_q + (uint32_t)(r >> 7) * Sh::tile16 + (uint32_t)(c >> 3) * Sh::half16 + sw128(r & 127, c & 7);
-    };
-#pragma unroll 4
-    for (int x = t; x < qrows * kLanes; x += count) {
-      const uint32_t dst = n8 > 0 ? sb + Sh::off_v16 + 16u * (uint32_t)x : place16(x);
-      const __nv_bfloat16 *src = q_row(x / kLanes);
-      if (src) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + 8 * (x % kLanes)) : "memory");
-      else sts128(dst, 0u, 0u, 0u, 0u);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    constexpr int U = 4;
-#pragma unroll 1
-    for (int x0 = t; x0 < qrows * kLanes; x0 += U * count) {
-      uint32_t w[U][4], top[U];
+  const long long limit = ca.wait_cycles;
+  auto load_q = [&](uint32_t dst, uint32_t full) {  // one lane
+    const int token = first + ct_token(ca, R0), tiles = qrows >> 7;
+    mbar_expect_tx(full, (uint32_t)tiles * Sh::tile16);
+    for (int w = 0; w < tiles; ++w)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int x = x0 + u * count < qrows * kLanes ? x0 + u * count : t;  // past the end: its first one again
-        const uint32_t at = n8 > 0 ? sb + Sh::off_v16 + 16u * (uint32_t)x : place16(x);
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3]) : "r"(at) : "memory");
-      }
-      // the row's largest magnitude, as the bits of a bf16 value: they order like the values
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t m = __vmaxu2(__vmaxu2(w[u][0] & 0x7fff7fffu, w[u][1] & 0x7fff7fffu), __vmaxu2(w[u][2] & 0x7fff7fffu, w[u][3] & 0x7fff7fffu));
-        top[u] = max(m & 0xffffu, m >> 16);
-      }
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o, kLanes));
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int x = x0 + u * count, r = x / kLanes, c = x % kLanes;
-        if (x >= qrows * kLanes) break;
-        const bool odd = top[u] >= 0x7f80u;  // NaN or infinity: the row scores NaN
-        // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8; half of e2 stays within fp32's exponents
-        const int e2 = top[u] == 0u || odd ? 0 : 135 - max((int)(top[u] >> 7), 1) - ((top[u] & 0x7fu) > 0x60u ? 1 : 0);
-        const int ea = e2 >> 1, eb = e2 - ea;
-        if (c == 0) row_f[r] = odd ? __uint_as_float(0x7fc00000u) : a.scale_log2 * power_of_two(-ea) * power_of_two(-eb);
-        if (n8 == 0) continue;
-        const float lift_a = power_of_two(ea), lift_b = power_of_two(eb);
-        uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y0 = __uint_as_float(w[u][e] << 16) * lift_a * lift_b, y1 = __uint_as_float(w[u][e] & 0xffff0000u) * lift_a * lift_b;
-          const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1), hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
-          const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
-          hi[e >> 1] |= h2 << (16 * (e & 1));
-          lo[e >> 1] |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (16 * (e & 1));
-        }
-        unsigned char *d8 = sm + Sh::off_q + (uint32_t)(r >> 7) * Sh::tile16 + at8<D>(r & 127, c >> 1) + 8 * (c & 1);
-        *reinterpret_cast<uint2 *>(d8) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2 *>(d8 + Sh::tile8) = make_uint2(lo[0], lo[1]);
-      }
-    }
-  } else if (warp == kCtTmaWarp || warp == kCtTmaVWarp) {  // the first tiles, while q is staged
+      for (int x = 0; x < D / 64; ++x)
+        tma_4d(dst + (uint32_t)w * Sh::tile16 + (uint32_t)x * Sh::half16, &tm_q, 64 * x, 0, g, token + w * (128 / a.G), full);
+  };
+  // q lands as it is, in two halves of 64 dims a tile and in its place for bf16 products, or where V's fp16 tiles will be
+  const uint32_t raw_q = sb + (n8 > 0 ? Sh::off_v16 : Sh::off_q);
+  if (warp == kCtTmaWarp || warp == kCtTmaVWarp) {  // the first tiles
     const bool is_v = warp == kCtTmaVWarp;
+    if (!is_v && ca.q_tma && lane == 0) load_q(raw_q, bar(C_QRAW));
+    __syncwarp();
     if (n8 > 0) {
       fetch_pages(0, pg, sl);
       fetch_scales(0, pg, ks, vs, !is_v);
-      for (int j = 0; j < n8 && j < (is_v ? 1 : kCtStages8); ++j) {
+      for (int j = 0; j < n8 && j < (is_v ? 2 : kCtStages8); ++j) {
         turn_pages(j, !is_v);
         if (is_v) load_v8(j);
         else load_k8(j);
@@ -451,19 +406,78 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     } else if (lane == 0) {
       for (int j = 0; j < n16 && j < 2; ++j) load16(j, is_v);
     }
+  } else if (!ca.q_tma && warp < kCtTmaWarp) {
+#pragma unroll 4
+    for (int x = t; x < qrows * kLanes; x += kCtTmaWarp * 32) {
+      const int r = x / kLanes, c = x % kLanes;
+      const uint32_t dst = raw_q + (uint32_t)(r >> 7) * Sh::tile16 + (uint32_t)(c >> 3) * Sh::half16 + sw128(r & 127, c & 7);
+      const __nv_bfloat16 *src = q_row(r);
+      if (src) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + 8 * c) : "memory");
+      else sts128(dst, 0u, 0u, 0u, 0u);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  if (!ca.q_tma) __syncthreads();
+  float f8 = 0.f, f16 = a.scale_log2;  // what a score of lifted q and codes, or of bf16 values, stands for in log2 units
+  if (warp < 8) {
+    // a softmax thread's row: its largest magnitude, as the bits of a bf16 value (they order like the values)
+    if (ca.q_tma) pt_wait(bar(C_QRAW), 0, &s_abort, limit);
+    const int r = t & 127, w = shared_rows ? 0 : warp >> 2;
+    const uint32_t src = raw_q + (uint32_t)w * Sh::tile16;
+    auto piece = [&](int c, uint32_t (&x)[4]) {  // eight dims
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                   : "r"(src + (uint32_t)(c >> 3) * Sh::half16 + sw128(r, c & 7))
+                   : "memory");
+    };
+    uint32_t top = 0u;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      uint32_t x[4];
+      piece(c, x);
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu), __vmaxu2(x[2] & 0x7fff7fffu, x[3] & 0x7fff7fffu)));
+    }
+    top = max(top & 0xffffu, top >> 16);
+    const bool odd = top >= 0x7f80u;  // NaN or infinity: the row scores NaN
+    // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8; half of e2 stays within fp32's exponents
+    const int e2 = top == 0u || odd ? 0 : 135 - max((int)(top >> 7), 1) - ((top & 0x7fu) > 0x60u ? 1 : 0);
+    const int ea = e2 >> 1, eb = e2 - ea;
+    f8 = a.scale_log2 * power_of_two(-ea) * power_of_two(-eb);
+    if (odd) f8 = f16 = __uint_as_float(0x7fc00000u);
+    if (n8 > 0 && (!shared_rows || warp < 4)) {
+      const float lift_a = power_of_two(ea), lift_b = power_of_two(eb);
+      const uint32_t dst = sb + Sh::off_q + (uint32_t)w * Sh::tile16;
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[4];
+          piece(2 * c + h, x);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            hi[2 * h + e] = lo[2 * h + e] = 0u;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float y0 = __uint_as_float(x[2 * e + k] << 16) * lift_a * lift_b;
+              const float y1 = __uint_as_float(x[2 * e + k] & 0xffff0000u) * lift_a * lift_b;
+              const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1), hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
+              const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
+              hi[2 * h + e] |= h2 << (16 * k);
+              lo[2 * h + e] |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (16 * k);
+            }
+          }
+        }
+        sts128(dst + at8<D>(r, c), hi[0], hi[1], hi[2], hi[3]);
+        sts128(dst + Sh::tile8 + at8<D>(r, c), lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
   }
   fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  float f8 = 0.f, f16 = a.scale_log2;  // what a score of lifted q and codes, or of bf16 values, stands for in log2 units
-  if (warp < 8) {
-    f8 = row_f[shared_rows ? t & 127 : t];
-    if (f8 != f8) f16 = f8;
-  }
-  __syncthreads();  // the factors have been read
   pdl_trigger();  // after the TMEM allocation: a waiting dependent block must not hold what this block needs
-  const long long limit = ca.wait_cycles;
   const uint32_t tmem = (uint32_t)uni((int)s_tmem);
   const uint32_t lead = elect_lane() ? 1u : 0u;
   float l = 0.f, ref = 0.f;   // a softmax thread's row: sum of weights, reference
@@ -487,13 +501,22 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     if (bad) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
     ok = __all_sync(0xffffffffu, ok);
     if (lane == 0) {
-      if (n8 > 0 && n16 > 0) ok = ok && pt_wait(bar(C_QFREE), 0, &s_abort, limit);
+      bool q_again = false;
+      if (n8 > 0 && n16 > 0) {
+        ok = ok && pt_wait(bar(C_QFREE), 0, &s_abort, limit);
+        if (ok && ca.q_tma) {  // q as it is, for the new rows' keys
+          load_q(sb + Sh::off_q, bar(C_QFULL));
+          q_again = true;
+        }
+      }
       for (int j = issued16; ok && j < n16; ++j) {
         if (j >= 2 && !pt_wait(bar(C_K2EMPTY + (j & 1)), (uint32_t)((j >> 1) - 1) & 1u, &s_abort, limit)) break;
         load16(j, false);
         issued16 = j + 1;
       }
       // no copy may be in flight when the block leaves
+      if (ca.q_tma) ct_drain(bar(C_QRAW), 0);
+      if (q_again) ct_drain(bar(C_QFULL), 0);
       for (int j = max(0, issued - kCtStages8); j < issued; ++j)
         ct_drain(bar(C_KFULL + j % kCtStages8), (uint32_t)(j / kCtStages8) & 1u);
       for (int j = max(0, issued16 - 2); j < issued16; ++j) ct_drain(bar(C_K2FULL + (j & 1)), (uint32_t)(j >> 1) & 1u);
@@ -501,7 +524,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   } else if (warp == kCtTmaVWarp) {
     // ---------------- TMA: V ----------------
     bool ok = true;
-    int issued = min(n8, 1), issued16 = n8 == 0 ? min(n16, 2) : 0;
+    int issued = min(n8, 2), issued16 = n8 == 0 ? min(n16, 2) : 0;
     for (int j = issued; j < n8; ++j) {
       turn_pages(j, false);
       if (j >= v_stages)
@@ -535,7 +558,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       constexpr uint32_t i8 = pt_idesc(0, FMT == ET_KV_E4M3 ? 0 : 1, false, false, 128, kCtKeys);
       constexpr uint32_t i16 = pt_idesc(1, 1, false, false, 128, kCtKeys);
       int k[2] = {0, 0};
-      bool ok = true;
+      bool ok = !ca.q_tma || pt_wait(bar(C_QRAW), 0, &s_abort, limit);
+      ok = __all_sync(0xffffffffu, ok);
       for (int i = 0; ok && i < n; ++i) {
         const int j = i - n8, sk = i < n8 ? i % kCtStages8 : j & 1;
         if (i < n8) {
@@ -639,9 +663,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       constexpr int C = D / 16, RP = 128 / C;  // 16-code chunks of a row; rows the threads take at once
       const int c = gt % C, r0 = gt / C;
       const uint32_t from = v8_at(s8), to = sb + Sh::off_v16 + (uint32_t)sv * Sh::tile16;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        constexpr int K = kCtKeys / RP / 2;
+#pragma unroll 1
+      for (int half = 0; half < 4; ++half) {
+        constexpr int K = kCtKeys / RP / 4 > 0 ? kCtKeys / RP / 4 : 1;
         uint4 v[K];
 #pragma unroll
         for (int x = 0; x < K; ++x) {
@@ -671,7 +695,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       }
     }
     if (n16 > 0) {
-      if (ok && n8 > 0) {  // q as it is, once the prefix's score products have run
+      if (ok && n8 > 0 && !ca.q_tma) {  // q as it is, once the prefix's score products have run
         ok = __all_sync(0xffffffffu, pt_wait(bar(C_QFREE), 0, &s_abort, limit));
         if (ok) {
 #pragma unroll 4
@@ -762,7 +786,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
       for (int p = 0; p < kCtKeys / 32; ++p) tmem_ld32(sc + 32u * p, raw[p]);
       tmem_wait_ld();
-      float top = -INFINITY;
+      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains: one would wait for itself
 #pragma unroll
       for (int u = 0; u < kCtKeys / 16; ++u) {
         const float f = own ? f16 : fu[u], c = own ? -ref : cu[u];
@@ -778,11 +802,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             x0 = e < limu ? x0 : -INFINITY;
             x1 = e + 1 < limu ? x1 : -INFINITY;
           }
-          top = fmaxf(top, fmaxf(x0, x1));
+          tops[(e >> 1) & 3] = fmaxf(tops[(e >> 1) & 3], fmaxf(x0, x1));
           x[0] = __float_as_uint(x0);
           x[1] = __float_as_uint(x1);
         }
       }
+      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
       const bool move = top > kPaTop + kPaSlack || (fresh && top > -INFINITY);
       if (__any_sync(0xffffffffu, move)) {
         const float now = move ? top + ref - kPaTop : ref, by = move ? ref - now : 0.f;
@@ -809,7 +834,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         if (move) fresh = false;
       }
-      uint64_t l2[2] = {0ull, 0ull};
+      uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
       for (int p = 0; p < kCtKeys / 32; ++p) {
         uint32_t pk[16];
@@ -819,7 +844,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             const float w0 = ex2_fast(__uint_as_float(raw[p][16 * u + e])), w1 = ex2_fast(__uint_as_float(raw[p][16 * u + e + 1]));
-            l2[(e >> 1) & 1] = own ? add2(pair(w0, w1), l2[(e >> 1) & 1]) : fma2(pair(w0, w1), iv2, l2[(e >> 1) & 1]);
+            l2[(e >> 1) & 3] = own ? add2(pair(w0, w1), l2[(e >> 1) & 3]) : fma2(pair(w0, w1), iv2, l2[(e >> 1) & 3]);
             pk[8 * u + (e >> 1)] = own ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1);
           }
         }
@@ -832,7 +857,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
       }
       float s0, s1;
-      unpair(add2(l2[0], l2[1]), s0, s1);
+      unpair(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])), s0, s1);
       l += s0 + s1;
       tmem_wait_st();
       tc_fence_before();
@@ -912,25 +937,26 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     } else if (Rr < real) {
       ca.part_ml[slot0 + Rr] = make_float2(M, l);
     }
-#pragma unroll 2
-    for (int p = 0; p < D / 16; ++p) {
-      uint32_t o[16];
-      pt_ld16(lanes + 16u * p, o);
+#pragma unroll 1
+    for (int p = 0; p < D / 32; ++p) {
+      uint32_t o[32];
+      tmem_ld32(lanes + 32u * p, o);
       tmem_wait_ld();
-      float x[16];
+      float x[32];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = mine_any ? __uint_as_float(o[e]) * mine : 0.f;
-        if (shared_rows) x[e] = fmaf(xo[(16 * p + e) * 128 + r], other, x[e]);
+      for (int e = 0; e < 32; ++e) x[e] = mine_any ? __uint_as_float(o[e]) * mine : 0.f;
+      if (shared_rows) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = fmaf(xo[(32 * p + e) * 128 + r], other, x[e]);
       }
       if (odd && Rr < real) {
         // values that are not finite, taken out of the tiles that not every row sees whole
         const int from = max(tok_first / kCtKeys, o0) * kCtKeys, to = min(i, (o0 + n16) * kCtKeys - 1);
 #pragma unroll 1
         for (int key = from; key <= to; ++key) {
-          const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.vt) + (long long)(first + key) * ca.c.vs + (long long)g * D + 16 * p;
+          const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.vt) + (long long)(first + key) * ca.c.vs + (long long)g * D + 32 * p;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 32; ++e) {
             const float z = __bfloat162float(v[e]);
             if (!(fabsf(z) <= FLT_MAX)) x[e] += z;
           }
@@ -939,14 +965,15 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       // through shared memory, where rows are written one by one: a row's 16-byte pieces trade places by the row's number
       if (parts == 1) {
         const uint32_t dst = stage + (uint32_t)(Rr * D * 2);
-        const int c = 2 * p;
-        sts128(dst + (uint32_t)((c ^ (Rr & 7)) << 4), pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-        sts128(dst + (uint32_t)(((c + 1) ^ (Rr & 7)) << 4), pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sts128(dst + (uint32_t)(((4 * p + e) ^ (Rr & 7)) << 4), pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
+                 pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
       } else {
         const uint32_t dst = stage + (uint32_t)(Rr * D * 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sts128(dst + (uint32_t)(((4 * p + e) ^ (Rr & 7)) << 4), __float_as_uint(x[4 * e]), __float_as_uint(x[4 * e + 1]),
+        for (int e = 0; e < 8; ++e)
+          sts128(dst + (uint32_t)(((8 * p + e) ^ (Rr & 7)) << 4), __float_as_uint(x[4 * e]), __float_as_uint(x[4 * e + 1]),
                  __float_as_uint(x[4 * e + 2]), __float_as_uint(x[4 * e + 3]));
       }
     }
@@ -1008,12 +1035,23 @@ bool make_new_map(CUtensorMap *m, const void *base, const ChunkArgs &c, int d, l
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q: [rows][Hkv][G][D]; a box is the rows of 128 / G tokens of one KV head, 64 dims
+bool make_q_map(CUtensorMap *m, const ChunkArgs &c, int d) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)c.a.G, (cuuint64_t)c.a.Hkv, (cuuint64_t)c.rows};
+  const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)c.a.G * d * 2, (cuuint64_t)c.qs * 2};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)c.a.G, 1, (cuuint32_t)(128 / c.a.G)};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(c.a.q), dims, strides, boxes, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int FMT>
-et_status launch_tc(const CUtensorMap (&m)[4], const ChunkTcArgs &ca, cudaStream_t st) {
+et_status launch_tc(const CUtensorMap (&m)[5], const ChunkTcArgs &ca, cudaStream_t st) {
   if (et_smem_attr((const void *)k_chunk_tc<D, FMT>, (int)CtShape<D>::bytes) != cudaSuccess) return ET_ERR_CUDA;
   const long long blocks = (long long)ca.tiles * ca.c.a.Hkv * ca.S;
   return et_launch(k_chunk_tc<D, FMT>, dim3((unsigned)blocks), dim3(kCtThreads), CtShape<D>::bytes, st, 0, m[0], m[1], m[2],
-                   m[3], ca);
+                   m[3], m[4], ca);
 }
 
 }  // namespace
@@ -1036,10 +1074,12 @@ et_status chunk_tc_launch(const et_paged_cache *cache, const ChunkArgs &c, const
   while ((2ull << ca.group_shift) < G) ++ca.group_shift;
   ca.group_magic = G == 1 ? 0u : (uint32_t)(((1ull << (32 + ca.group_shift)) + G - 1) / G);
   ca.wait_cycles = et_wait_limit_cycles();
-  CUtensorMap m[4];
+  CUtensorMap m[5];
+  ca.q_tma = G <= 128 && 128 % G == 0;
   if (!make_page_map(&m[0], cache->k_pages, cache, ca.box) || !make_page_map(&m[1], cache->v_pages, cache, ca.box) ||
-      !make_new_map(&m[2], c.a.kt, c, cache->d, c.ks) || !make_new_map(&m[3], c.a.vt, c, cache->d, c.vs))
+      !make_new_map(&m[2], c.a.kt, c, cache->d, c.ks) || !make_new_map(&m[3], c.a.vt, c, cache->d, c.vs) || (ca.q_tma && !make_q_map(&m[4], c, cache->d)))
     return ET_ERR_INVALID_ARG;
+  if (!ca.q_tma) m[4] = m[2];  // not read
   const bool e4m3 = cache->format == ET_KV_E4M3;
   if (cache->d == 64) return e4m3 ? launch_tc<64, ET_KV_E4M3>(m, ca, st) : launch_tc<64, ET_KV_E5M2>(m, ca, st);
   return e4m3 ? launch_tc<128, ET_KV_E4M3>(m, ca, st) : launch_tc<128, ET_KV_E5M2>(m, ca, st);
