@@ -660,32 +660,31 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const uint32_t units = *(volatile uint32_t *)&s_units[i % kCtSlots];
       const int lim = L - (t0 + i) * kCtKeys;  // rows past it hold no key of this sequence
       const bool whole = lim >= kCtKeys && units == 0xffu;
-      constexpr int C = D / 16, RP = 128 / C;  // 16-code chunks of a row; rows the threads take at once
-      const int c = gt % C, r0 = gt / C;
-      const uint32_t from = v8_at(s8), to = sb + Sh::off_v16 + (uint32_t)sv * Sh::tile16;
-#pragma unroll 1
-      for (int half = 0; half < 4; ++half) {
-        constexpr int K = kCtKeys / RP / 4 > 0 ? kCtKeys / RP / 4 : 1;
-        uint4 v[K];
-#pragma unroll
-        for (int x = 0; x < K; ++x) {
-          const int r = r0 + RP * (K * half + x);
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[x].x), "=r"(v[x].y), "=r"(v[x].z), "=r"(v[x].w) : "r"(from + at8<D>(r, c)));
-          if (!whole && (r >= lim || !((units >> (r >> 4)) & 1u))) v[x] = make_uint4(0u, 0u, 0u, 0u);
+      // 16 codes of a row a thread, read as two chunks of eight.  Which one it takes first alternates between the 64-dim
+      // halves, which keeps the stores free of bank conflicts, and between rows, which keeps the reads free of them
+      constexpr int C = D / 16, RP = 128 / C, ROUNDS = kCtKeys / RP;  // 16-code chunks of a row; rows the threads take at once
+      const int c = gt % C, r0 = gt / C, c0 = 2 * (c & 3), s = (c >> 2) ^ (r0 & 1);
+      const uint32_t from = v8_at(s8) + at8<D>(r0, c), to = sb + Sh::off_v16 + (uint32_t)sv * Sh::tile16 + (uint32_t)(c >> 2) * Sh::half16;
+      const uint32_t from0 = from + 8u * (uint32_t)s, from1 = from + 8u - 8u * (uint32_t)s;
+      const uint32_t to0 = to + sw128(r0, c0 + s), to1 = to + sw128(r0, c0 + 1 - s);
+      static_assert(RP % 8 == 0, "a row's place in its group of eight is the thread's own");
+#pragma unroll 2
+      for (int k = 0; k < ROUNDS; ++k) {
+        const uint32_t in = (uint32_t)(k * RP * D), out = (uint32_t)(k * RP * 128);
+        uint4 v;
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(from0 + in));
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.z), "=r"(v.w) : "r"(from1 + in));
+        if (!whole) {
+          const int r = r0 + RP * k;
+          if (r >= lim || !((units >> (r >> 4)) & 1u)) v = make_uint4(0u, 0u, 0u, 0u);
         }
-#pragma unroll
-        for (int x = 0; x < K; ++x) {
-          const int r = r0 + RP * (K * half + x);
-          uint32_t h[8];
-          f8x4_to_f16<FMT>(v[x].x, h[0], h[1]);
-          f8x4_to_f16<FMT>(v[x].y, h[2], h[3]);
-          f8x4_to_f16<FMT>(v[x].z, h[4], h[5]);
-          f8x4_to_f16<FMT>(v[x].w, h[6], h[7]);
-          const uint32_t dst = to + (uint32_t)(c >> 2) * Sh::half16;
-          const int c0 = 2 * (c & 3), s = (c >> 2) ^ (r & 1);  // which of the two 16-byte chunks goes first
-          sts128(dst + sw128(r, c0 + s), s ? h[4] : h[0], s ? h[5] : h[1], s ? h[6] : h[2], s ? h[7] : h[3]);
-          sts128(dst + sw128(r, c0 + 1 - s), s ? h[0] : h[4], s ? h[1] : h[5], s ? h[2] : h[6], s ? h[3] : h[7]);
-        }
+        uint32_t h[8];
+        f8x4_to_f16<FMT>(v.x, h[0], h[1]);
+        f8x4_to_f16<FMT>(v.y, h[2], h[3]);
+        f8x4_to_f16<FMT>(v.z, h[4], h[5]);
+        f8x4_to_f16<FMT>(v.w, h[6], h[7]);
+        sts128(to0 + out, h[0], h[1], h[2], h[3]);
+        sts128(to1 + out, h[4], h[5], h[6], h[7]);
       }
       fence_async_smem();
       __syncwarp();
