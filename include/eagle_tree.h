@@ -238,7 +238,8 @@ typedef struct {
 typedef struct {
     int32_t B, Hq;            /* sequences; query heads, a multiple of the cache's Hkv */
     int32_t rows;             /* rows in each of q, k_new, v_new and out, >= 1 */
-    int32_t max_rows;         /* host upper bound of one sequence's new rows (sizes the grid), 1..rows */
+    int32_t max_rows;         /* host upper bound of one sequence's new rows (sizes the grid), >= 1 (rows at most
+                                 are used) */
     int32_t max_blocks;       /* columns of block_table */
     et_dtype dtype;           /* of q, k/v new and out */
     float scale;              /* score scale, usually 1/sqrt(d) */

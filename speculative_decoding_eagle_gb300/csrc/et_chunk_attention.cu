@@ -54,12 +54,15 @@ __global__ void __launch_bounds__(kCrThreads) k_chunk_rows(const ChunkArgs c) {
   const int tok[2] = {(int)((R0 + ty) / a.G), (int)((R0 + ty + 16) / a.G)};
   const int prefix_tiles = (int)(((long long)L + kCrKeys - 1) / kCrKeys), own_tiles = last_token / kCrKeys + 1;
   int page_bad = 0;
-  for (int j = 0; j < prefix_tiles + own_tiles; ++j) {
+  // a tile's rows, four dims of a row a cell: the next tile's are on their way while this one's scores are found
+  constexpr int CELLS = kCrKeys * (D / 4) / kCrThreads;
+  float4 next_k[CELLS], next_v[CELLS];
+  auto fetch = [&](int j) {
     const bool mine = j >= prefix_tiles;
     const int key0 = (mine ? j - prefix_tiles : j) * kCrKeys;
-    __syncthreads();
-    for (int x = t; x < kCrKeys * (D / 4); x += kCrThreads) {
-      const int r = x / (D / 4), e = x % (D / 4) * 4, key = key0 + r;
+#pragma unroll
+    for (int z = 0; z < CELLS; ++z) {
+      const int x = t + z * kCrThreads, r = x / (D / 4), e = x % (D / 4) * 4, key = key0 + r;
       float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
       if (mine) {
         if (key <= last_token) {
@@ -82,10 +85,23 @@ __global__ void __launch_bounds__(kCrThreads) k_chunk_rows(const ChunkArgs c) {
           kv.x = __uint_as_float(0x7fc00001u);  // marks a key that is not there
         }
       }
-      *reinterpret_cast<float4 *>(K + r * LD + e) = kv;
-      *reinterpret_cast<float4 *>(V + r * D + e) = vv;
+      next_k[z] = kv;
+      next_v[z] = vv;
+    }
+  };
+  fetch(0);
+  for (int j = 0; j < prefix_tiles + own_tiles; ++j) {
+    const bool mine = j >= prefix_tiles;
+    const int key0 = (mine ? j - prefix_tiles : j) * kCrKeys;
+    __syncthreads();
+#pragma unroll
+    for (int z = 0; z < CELLS; ++z) {
+      const int x = t + z * kCrThreads, r = x / (D / 4), e = x % (D / 4) * 4;
+      *reinterpret_cast<float4 *>(K + r * LD + e) = next_k[z];
+      *reinterpret_cast<float4 *>(V + r * D + e) = next_v[z];
     }
     __syncthreads();
+    if (j + 1 < prefix_tiles + own_tiles) fetch(j + 1);
     // ---- scores of rows ty, ty + 16 and keys tx, tx + 16 ----
     float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll 8
@@ -131,6 +147,7 @@ __global__ void __launch_bounds__(kCrThreads) k_chunk_rows(const ChunkArgs c) {
     }
     __syncwarp();  // a row's 32 weights come from its own half warp
     // ---- output: rows ty, ty + 16, dims 4 tx + 64 jj ----
+#pragma unroll 8
     for (int kk = 0; kk < kCrKeys; ++kk) {
       const float p0 = P[ty * 33 + kk], p1 = P[(ty + 16) * 33 + kk];
       const int key = key0 + kk;
@@ -202,7 +219,7 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
   if (!s) return ET_ERR_INVALID_ARG;
   const et_status cs = paged_cache_status(c);
   if (cs != ET_OK) return cs;
-  if (s->B < 1 || s->rows < 1 || s->max_rows < 1 || s->max_rows > s->rows || s->Hq < 1 || s->Hq % c->Hkv ||
+  if (s->B < 1 || s->rows < 1 || s->max_rows < 1 || s->Hq < 1 || s->Hq % c->Hkv ||
       s->max_blocks < 1 || s->max_prefix < 0 || s->num_splits < 0 || !(s->scale > 0.f) || !(s->scale <= FLT_MAX) ||
       (s->dtype != ET_BF16 && s->dtype != ET_F32))
     return ET_ERR_INVALID_ARG;
@@ -211,7 +228,7 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
   for (int i = 0; i < 3; ++i)
     if (strides[i] < sizes[i] * c->d || strides[i] * es % 16 || strides[i] >= (1ll << 38)) return ET_ERR_INVALID_ARG;
   if (s->B > 65535 || s->Hq > 65535 || (long long)s->max_blocks * c->page_size >= (1ll << 31) ||
-      (long long)s->max_rows * (s->Hq / c->Hkv) >= (1ll << 31))
+      (long long)s->rows * (s->Hq / c->Hkv) >= (1ll << 31))
     return ET_ERR_UNSUPPORTED;
   p->tc.S = 1;
   p->tc.tiles = 0;
@@ -223,7 +240,8 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
   const long long units = tiles * c->Hkv;
   if (units >= (1ll << 24)) return ET_ERR_UNSUPPORTED;
   const long long room = (long long)s->max_blocks * c->page_size;
-  const long long T = ((s->max_prefix < room ? s->max_prefix : room) + 127) / 128 + (s->max_rows + 127) / 128;
+  const int most = s->max_rows < s->rows ? s->max_rows : s->rows;
+  const long long T = ((s->max_prefix < room ? s->max_prefix : room) + 127) / 128 + (most + 127) / 128;
   long long S = s->num_splits;
   if (S <= 0) {
     // A block costs about 14 of its tiles before its first and after its last, and a merge through the workspace six more
@@ -283,7 +301,7 @@ extern "C" et_status et_chunk_attention_paged(const et_chunk_attn_shape *shape, 
   ET_RETURN_IF(plan.ws > 0 && (!ws || ws_bytes < plan.ws || !et_aligned(ws, 256)), ET_ERR_WORKSPACE);
   ChunkArgs c = {};
   PagedAttnArgs &a = c.a;
-  a.B = shape->B; a.N = shape->max_rows; a.Hq = shape->Hq; a.Hkv = cache->Hkv; a.G = shape->Hq / cache->Hkv;
+  a.B = shape->B; a.N = shape->max_rows < shape->rows ? shape->max_rows : shape->rows; a.Hq = shape->Hq; a.Hkv = cache->Hkv; a.G = shape->Hq / cache->Hkv;
   a.P = cache->page_size; a.max_blocks = shape->max_blocks; a.max_prefix = shape->max_prefix;
   a.scale_log2 = shape->scale * 1.4426950408889634f;
   a.num_pages = cache->num_pages; a.page_stride = cache->page_stride;

@@ -114,7 +114,7 @@ def chunk_status(lib, cache_=None, table=FAKE, plen=FAKE, start=FAKE, q=FAKE, k=
 
 @pytest.mark.parametrize("over,want", [
     (dict(table=None), 1), (dict(plen=None), 1), (dict(start=None), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1),
-    (dict(out=None), 1), (dict(B=0), 1), (dict(rows=0), 1), (dict(max_rows=0), 1), (dict(max_rows=101), 1), (dict(Hq=0), 1),
+    (dict(out=None), 1), (dict(B=0), 1), (dict(rows=0), 1), (dict(max_rows=0), 1), (dict(max_rows=-5), 1), (dict(Hq=0), 1),
     (dict(Hq=3), 1), (dict(max_blocks=0), 1), (dict(max_prefix=-1), 1), (dict(num_splits=-1), 1), (dict(scale=0.0), 1),
     (dict(scale=-1.0), 1), (dict(scale=math.nan), 1), (dict(scale=math.inf), 1), (dict(dtype=2), 1), (dict(q_stride=511), 1),
     (dict(q_stride=516), 1), (dict(k_stride=128), 1), (dict(v_stride=260), 1), (dict(v_stride=1 << 40), 1), (dict(q=FAKE + 8), 1),
@@ -141,6 +141,7 @@ def test_chunk_attention_plans(lib):
                 lib.et_chunk_attention_paged_workspace_size(ctypes.byref(s), ctypes.byref(c)))
     assert plan(dtype=1) == (1, 0)                                        # fp32: one part
     assert plan(num_splits=1) == (1, 0)
+    assert plan(max_rows=2 ** 31 - 1) == plan(max_rows=100)                # a bound past the rows is the rows
     S, ws = plan(num_splits=3)
     # (tiles of 256 rows: 100 * 2 / 256 of them whole, and one that each sequence ends in) x heads x parts x 256 rows
     assert S == 3 and ws == 16384 * 4 + (0 + 2) * 2 * 3 * 256 * (8 + 128 * 4)
