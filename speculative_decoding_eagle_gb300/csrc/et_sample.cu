@@ -125,12 +125,11 @@ struct Weigher {
   float zm, ch, cl;
   const float2 *table;  // [64] 2^(j / 64) in two fp32 numbers
   __device__ __forceinline__ unsigned long long operator()(float z) const {
-    const float s = z - zm, p = s * ch;
-    if (!(p > -46.f)) return 0ull;
-    const float back = s - z;                                  // z - zm = s + err exactly
+    const float s = z - zm, back = s - z;                      // z - zm = s + err exactly
+    const float p = s * ch;
+    if (!(p > -46.f)) return 0ull;                             // -inf, too
     const float err = (z - (s - back)) - (zm + back);
-    float e = fmaf(s, ch, -p);
-    e = fmaf(err, ch, fmaf(s, cl, e));                         // the exponent is p + e
+    const float e = fmaf(err, ch, fmaf(s, cl, fmaf(s, ch, -p)));  // the exponent of 2 is p + e
     // k = round(64 p): the sum's last bits hold it (1.5 2^23)
     const float kk = fmaf(p, 64.f, 12582912.f);
     const float r = fmaf(kk - 12582912.f, -0.015625f, p);
@@ -189,14 +188,15 @@ __device__ __forceinline__ unsigned long long peers_mass(const Row &row, unsigne
 __device__ __forceinline__ int warp_span(int slice) { return ((slice + kSaWarps - 1) / kSaWarps + 31) & ~31; }
 
 // The id of the token at which the cumulative weight, in ascending id, passes
-// `target` (target < the cluster's total, else -1).  w(key, id, z) weighs.  Every thread
-// of the cluster calls it and gets the id.
+// `target` (target < the cluster's total, else -1).  weigh(z, id) is a token's weight.  Every thread of the cluster
+// calls it and gets the id.
 template <typename W>
 __device__ int locate(const Row &row, int slice, unsigned long long *s_red, int *s_id, W weigh, unsigned long long target,
                       unsigned long long *total, bool fraction, float uniform) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, span = warp_span(slice);
   const int i0 = warp * span, i1 = min(i0 + span, row.n);
   unsigned long long mine = 0ull;
+#pragma unroll 2
   for (int i = i0 + lane; i < i1; i += 32) mine += weigh(row.z[i], row.base + i);
   mine = warp_sum_u64(mine);
   if (lane == 0) row.sh->warp_mass[warp] = mine;
@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   __shared__ float2 s_table[64];
   __shared__ unsigned long long s_red[2 * kSaWarps];
   __shared__ int s_id;
-  __shared__ float s_f[32], s_row[3];
+  __shared__ float s_f[2 * kSaWarps], s_row[3];
+  __shared__ int s_odd[kSaWarps];
   const int t = threadIdx.x, lane = t & 31;
   Row row;
   row.sh = &sh;
@@ -472,6 +473,14 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   const int k = a.top_k ? a.top_k[b] : 0;
   const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
   float u = a.uniforms[b];
+  T = T > 0.f ? fminf(fmaxf(T, 1e-30f), 1e30f) : 0.f;
+  double depth = 0.0;  // of min-p
+  if (t == 0 && T > 0.f) {  // what takes fp64 arithmetic, by one thread and while the logits come
+    const double c = 1.4426950408889634074 / (double)T;
+    s_row[0] = (float)c;
+    s_row[1] = (float)(c - (double)(float)c);
+    if (mp > 0.f) depth = (double)T * log((double)mp);
+  }
   float zmax = -INFINITY, zmin = INFINITY;
   int odd = 0;
   auto take = [&](float z) -> float {
@@ -493,9 +502,19 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
 #pragma unroll 8
     for (int i = t; i < row.n; i += kSaThreads) s_z[i] = take(zr[i]);
   }
-  zmax = block_max<kSaThreads>(zmax, s_f);
-  zmin = -block_max<kSaThreads>(-zmin, s_f);
-  odd = __syncthreads_or(odd);
+  zmax = warp_max(zmax);
+  zmin = -warp_max(-zmin);
+  const float warp_top = zmax;
+  odd = __any_sync(0xffffffffu, odd);
+  if (lane == 0) {
+    s_f[t >> 5] = zmax;
+    s_f[kSaWarps + (t >> 5)] = zmin;
+    s_odd[t >> 5] = odd;
+  }
+  __syncthreads();
+  zmax = warp_max(lane < kSaWarps ? s_f[lane] : -INFINITY);
+  zmin = -warp_max(lane < kSaWarps ? -s_f[kSaWarps + lane] : -INFINITY);
+  odd = __any_sync(0xffffffffu, lane < kSaWarps && s_odd[lane]);
   if (t == 0) {
     sh.zmax = zmax;
     sh.zmin = zmin;
@@ -503,12 +522,19 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
     sh.odd = odd;
   }
   __syncthreads();
-  // the lowest id of the largest logit, where a block may have it
-  for (int i = t; i < row.n; i += kSaThreads)
-    if (s_z[i] == zmax) {
-      atomicMin(&sh.first, (unsigned int)(row.base + i));
-      break;
-    }
+  // the lowest id of the largest logit: a warp that has it looks for it
+  if (warp_top == zmax) {
+    const int stride = a.vec4 ? 4 : 1;  // what a thread has read
+    unsigned int found = 0xffffffffu;
+    for (int i = stride * t; i < row.n; i += stride * kSaThreads)
+      for (int e = 0; e < stride && i + e < row.n; ++e)
+        if (s_z[i + e] == zmax) found = min(found, (unsigned int)(row.base + i + e));
+    if (a.vec4)  // the row's ragged end was read one by one
+      for (int i = (row.n & ~3) + t; i < row.n; i += kSaThreads)
+        if (s_z[i] == zmax) found = min(found, (unsigned int)(row.base + i));
+    found = __reduce_min_sync(0xffffffffu, found);
+    if (lane == 0) atomicMin(&sh.first, found);
+  }
   row_sync(row.C);
   float zm = -INFINITY, zl = INFINITY;
   unsigned int top = 0xffffffffu;
@@ -530,16 +556,10 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   kept.cut = -1;  // every key above zero: -inf is above it, and left out where it matters
   int token = -1;
   float logprob = -INFINITY;
-  T = fminf(fmaxf(T, 1e-30f), 1e30f);
-  // what takes fp64 arithmetic, by one thread
   if (t == 0 && !none && !greedy) {
-    const double c = 1.4426950408889634074 / (double)T;
-    s_row[0] = (float)c;
-    s_row[1] = (float)(c - (double)(float)c);
     unsigned int key_min = 0u;  // min-p: keys from this one on
     if (mp > 0.f) {
       // the smallest logit with (z - max) / T >= log(min_p)
-      const double depth = (double)T * log((double)mp);
       float zf = (float)((double)zm + depth);
       if ((double)zf - (double)zm < depth) zf = nextafterf(zf, INFINITY);
       key_min = mp > 1.f || zf > zm ? 0xffffffffu : order_key(zf);
@@ -573,18 +593,26 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
       const float step = range > 0.f ? (float)(kSaBins - 1) / range : 0.f;
       unsigned int (*h)[kSaBins] = sh.hist[0];
       unsigned long long target = by_count ? (unsigned long long)k : 0ull;
+      Crossing x;
+      if (by_count) {
+#pragma unroll 4
+        for (int i = t; i < row.n; i += kSaThreads) {
+          const float z = s_z[i];
+          if (z > -INFINITY) atomicAdd(&h[0][step_of(z, zm, step)], 1u);
+        }
+        x = cross<false>(row, h, 0ull, -1.f, &target, s_red);
+      } else {
 #pragma unroll 2
-      for (int i = t; i < row.n; i += kSaThreads) {
-        const float z = s_z[i];
-        if (z == -INFINITY) continue;
-        const int at = step_of(z, zm, step);
-        if (by_count) atomicAdd(&h[0][at], 1u);
-        else add_mass(h, at, weigh(z));
+        for (int i = t; i < row.n; i += kSaThreads) {
+          const float z = s_z[i];
+          if (z > -INFINITY) add_mass(h, step_of(z, zm, step), weigh(z));
+        }
+        x = cross<true>(row, h, 0ull, p, &target, s_red);
       }
-      Crossing x = by_count ? cross<false>(row, h, 0ull, -1.f, &target, s_red) : cross<true>(row, h, 0ull, p, &target, s_red);
       unsigned int listed = ~0u;
       if (x.bin >= 0) {
         // ---- the tokens up to the border's step go to block 0, if they are few ----
+#pragma unroll 4
         for (int i0 = 0; i0 < row.n; i0 += kSaThreads) {
           const int i = i0 + t;
           const float z = i < row.n ? s_z[i] : -INFINITY;
