@@ -231,38 +231,52 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
       (long long)s->rows * (s->Hq / c->Hkv) >= (1ll << 31))
     return ET_ERR_UNSUPPORTED;
   p->tc.S = 1;
-  p->tc.tiles = 0;
+  p->tc.tiles = p->tc.whole = 0;
   p->tc.ml_off = p->tc.o_off = p->ws = 0;
   if (s->dtype == ET_F32) return ET_OK;
   // every sequence's rows end in a tile of their own, if they have any
   const long long rows = (long long)s->rows * (s->Hq / c->Hkv);
-  const long long tiles = rows / 256 + (s->B < s->rows ? s->B : s->rows);
+  const long long tiles = (rows + 255ll * (s->B < s->rows ? s->B : s->rows)) / 256;
   const long long units = tiles * c->Hkv;
   if (units >= (1ll << 24)) return ET_ERR_UNSUPPORTED;
   const long long room = (long long)s->max_blocks * c->page_size;
   const int most = s->max_rows < s->rows ? s->max_rows : s->rows;
-  const long long T = ((s->max_prefix < room ? s->max_prefix : room) + 127) / 128 + (most + 127) / 128;
-  long long S = s->num_splits;
+  const long long Tp = ((s->max_prefix < room ? s->max_prefix : room) + 127) / 128, T = Tp + (most + 127) / 128;
+  long long S = s->num_splits, whole = 0;
   if (S <= 0) {
-    // A block costs about 14 of its tiles before its first and after its last, and a merge through the workspace six more
-    // (measured: 25000 cycles and 2000 a tile): parts pay where blocks are few and tiles many.  One block per SM
-    const long long sms = sm_count();
-    double best = 1e30;
-    for (long long k = 1; k <= 64 && k <= T; ++k) {
-      const double cost = (double)((units * k + sms - 1) / sms) * (14 + (double)((T + k - 1) / k) + (k > 1 ? 6 : 0));
-      if (cost < best) {
-        best = cost;
+    // One block per SM.  A block costs about 14 of its tiles before its first and after its last, and a merge through the
+    // workspace six to nine more (64 rows, 32 heads, in 1 / 2 / 3 / 4 parts: 4096 keys 39.5 / 31.2 / 28.9 / 26.8 us, 1024 keys 18.9 /
+    // 20.3 / 21.2 / 20.9): parts pay where blocks are few and tiles many, and where a last round of whole units would leave
+    // SMs idle (512 units of 65 to 80 tiles, the last 56 in two parts: 505 us, whole: 534).  That round has the units with the
+    // fewest keys, little more than the prefix
+    const long long sms = sm_count(), rounds = units / sms, rest = units % sms, least = Tp + 1 < T ? Tp + 1 : T;
+    double best = (double)((units + sms - 1) / sms) * (14 + (double)T);
+    const double plain = best;
+    S = 1;
+    for (long long k = 2; k <= 64 && k <= T; ++k) {
+      const double all = (double)((units * k + sms - 1) / sms) * (14 + (double)((T + k - 1) / k) + 8);
+      if (all < best) {
+        best = all;
         S = k;
+        whole = 0;
+      }
+      if (!rounds || !rest) continue;
+      const double last = plain - (14 + (double)least) + (double)((rest * k + sms - 1) / sms) * (14 + (double)((least + k - 1) / k) + 8);
+      if (last < best && last < 0.95 * plain) {
+        best = last;
+        S = k;
+        whole = rounds * sms;
       }
     }
   }
   if (S > T) S = T;
   if (S > 64) S = 64;
-  if (S < 1 || units > kChunkCounters) S = 1;
+  if (S < 1 || units - whole > kChunkCounters) S = 1;
   p->tc.S = (int)S;
   p->tc.tiles = (int)tiles;
+  p->tc.whole = S > 1 ? (int)whole : 0;
   if (S > 1) {
-    const size_t slots = (size_t)units * S * 256;
+    const size_t slots = (size_t)(units - whole) * S * 256;
     p->tc.ml_off = kChunkCounters * sizeof(unsigned int);
     p->tc.o_off = p->tc.ml_off + slots * sizeof(float2);
     p->ws = p->tc.o_off + slots * c->d * sizeof(float);

@@ -143,8 +143,9 @@ __device__ __forceinline__ void ct_commit(uint32_t bar, uint32_t lead) {
 }
 struct ChunkTcArgs {
   ChunkArgs c;
-  int S;                 // parts of a block's tiles at most
+  int S;                 // parts of a unit's tiles at most (a unit: 256 rows of a KV head)
   int tiles;             // tiles of 256 rows per KV head in the grid
+  int whole;             // the first units, each a block
   int q_tma;             // q by TMA: the heads of a group divide a tile's 128 rows
   int box;               // rows per TMA box of a page
   unsigned int *cnt;     // arrival counters (null with S = 1)
@@ -197,7 +198,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   pdl_wait();  // the previous kernel in the stream has completed
 
   // ---- which rows: tile `index` of the batch's tiles of 256 rows, in the sequences' order ----
-  const int unit = ca.S == 1 ? blockIdx.x : blockIdx.x / ca.S, part = blockIdx.x - unit * ca.S;
+  const int behind = (int)blockIdx.x - ca.whole;  // a block of the units in parts
+  const int cut = behind < 0 ? 0 : behind / ca.S, part = behind < 0 ? 0 : behind - cut * ca.S;
+  const int unit = behind < 0 ? (int)blockIdx.x : ca.whole + cut;
   const int index = unit / a.Hkv, g = unit - index * a.Hkv;
   int bad = 0;
   {
@@ -269,8 +272,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   const bool shared_rows = uni(real <= 128) != 0;                            // both groups have the same rows
   const int tok_first = ct_token(ca, R0), tok_last = ct_token(ca, R0 + real - 1);
   const int Tp = tiles_of(L, kCtKeys), To = tok_last / kCtKeys + 1, T = Tp + To;
-  const int per = ca.S == 1 ? T : max((s_longest + ca.S - 1) / ca.S, 1);
-  const int parts = ca.S == 1 ? 1 : (T + per - 1) / per;
+  int parts = 1, per = T;
+  if (behind >= 0 && ca.S > 1) {  // shorter sequences have fewer parts
+    const int most = max((s_longest + ca.S - 1) / ca.S, 1);
+    per = tiles_of(T, (T + most - 1) / most);
+    parts = tiles_of(T, per);
+  }
   if (part >= parts) return;
   const int t0 = part * per, t1 = min(T, t0 + per);
   const int n8 = uni(max(0, min(t1, Tp) - t0));                         // tiles of the prefix
@@ -894,7 +901,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   float2 *xm = reinterpret_cast<float2 *>(sm + Sh::off_v8);                    // [128]
   // the rows as they go out: behind the other group's, or (fp32 rows of both groups) from the start
   const uint32_t stage = sb + (parts > 1 && !shared_rows ? Sh::off_q : Sh::off_k);
-  const long long slot0 = ((long long)unit * ca.S + part) * 256;
+  const long long slot0 = ((long long)cut * ca.S + part) * 256;
   const int w = warp >> 2, r = t & 127, Rr = shared_rows ? r : 128 * w + r;
   const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCtColO + 128u * (uint32_t)w;
   if (shared_rows && w == 1) {
@@ -999,8 +1006,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCtTmemCols) : "memory");
   if (parts == 1) return;
   // ---- the parts' rows, merged by the last block to arrive ----
-  if (!arrive_last(ca.cnt + unit, (unsigned)parts, &s_last)) return;
-  const long long base = (long long)unit * ca.S * 256;
+  if (!arrive_last(ca.cnt + cut, (unsigned)parts, &s_last)) return;
+  const long long base = (long long)cut * ca.S * 256;
 #pragma unroll 1
   for (int x = t; x < real * (D / 4); x += kCtThreads) {
     const int rr = x / (D / 4), c = x % (D / 4);
@@ -1048,7 +1055,7 @@ bool make_q_map(CUtensorMap *m, const ChunkArgs &c, int d) {
 template <int D, int FMT>
 et_status launch_tc(const CUtensorMap (&m)[5], const ChunkTcArgs &ca, cudaStream_t st) {
   if (et_smem_attr((const void *)k_chunk_tc<D, FMT>, (int)CtShape<D>::bytes) != cudaSuccess) return ET_ERR_CUDA;
-  const long long blocks = (long long)ca.tiles * ca.c.a.Hkv * ca.S;
+  const long long blocks = ca.whole + ((long long)ca.tiles * ca.c.a.Hkv - ca.whole) * ca.S;
   return et_launch(k_chunk_tc<D, FMT>, dim3((unsigned)blocks), dim3(kCtThreads), CtShape<D>::bytes, st, 0, m[0], m[1], m[2],
                    m[3], m[4], ca);
 }
@@ -1061,6 +1068,7 @@ et_status chunk_tc_launch(const et_paged_cache *cache, const ChunkArgs &c, const
   ca.c = c;
   ca.S = p.S;
   ca.tiles = p.tiles;
+  ca.whole = p.whole;
   const int P = cache->page_size;
   ca.box = P % 128 == 0 ? 128 : P % 64 == 0 ? 64 : P % 32 == 0 ? 32 : 16;
   unsigned char *wsb = static_cast<unsigned char *>(ws);

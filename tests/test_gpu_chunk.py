@@ -167,6 +167,28 @@ def test_many_tiles_in_any_number_of_parts(prefix, rows, Hq, Hkv, P, d, splits):
     assert torch.equal(first[0], x.out) and torch.equal(first[1], x.lse)
 
 
+@pytest.mark.parametrize("prefix,rows,Hq,Hkv,P,d", [
+    ([2000], [700], 64, 8, 64, 128),                # 22 units of 256 rows a KV head
+    ([1100, 0, 2300, -1, 40], [260, 600, 130, 9, 1], 64, 16, 32, 64),
+    ([1900] * 5, [33] * 5, 32, 32, 16, 128),         # 33 rows a unit
+])
+def test_whole_rounds_of_blocks_and_a_last_one_in_parts(prefix, rows, Hq, Hkv, P, d):
+    """As many units as SMs go out whole; what is left over is taken in parts."""
+    x = Batch(prefix, rows, Hq, Hkv, d, P, seed=5)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    units = Hkv * ((x.T * (Hq // Hkv) + 255 * len(rows)) // 256)
+    shape = E.ChunkAttnShape(B=len(prefix), rows=x.T, Hq=Hq, max_rows=max(rows), max_blocks=x.table.shape[1])
+    S, need = E.et_chunk_attention_paged_splits(shape, x.cache), E.et_chunk_attention_paged_workspace_size(shape, x.cache)
+    assert units > sms and S > 1
+    assert need == 16384 * 4 + (units % sms) * S * 256 * (8 + 4 * d)
+    ws = x.run()
+    x.check()
+    first = x.out.clone(), x.lse.clone()
+    x.out.fill_(7.0)
+    x.run(ws=ws)
+    assert torch.equal(first[0], x.out) and torch.equal(first[1], x.lse)
+
+
 def test_values_that_are_not_finite_stay_with_the_rows_that_see_them():
     """NaN and infinities in a later row's key or value, in the next sequence's rows and behind the prefix."""
     for dtype in ("bf16", "f32"):
