@@ -231,52 +231,74 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
       (long long)s->rows * (s->Hq / c->Hkv) >= (1ll << 31))
     return ET_ERR_UNSUPPORTED;
   p->tc.S = 1;
+  p->tc.shift = 8;
   p->tc.tiles = p->tc.whole = 0;
   p->tc.ml_off = p->tc.o_off = p->ws = 0;
   if (s->dtype == ET_F32) return ET_OK;
-  // every sequence's rows end in a tile of their own, if they have any
-  const long long rows = (long long)s->rows * (s->Hq / c->Hkv);
-  const long long tiles = (rows + 255ll * (s->B < s->rows ? s->B : s->rows)) / 256;
-  const long long units = tiles * c->Hkv;
-  if (units >= (1ll << 24)) return ET_ERR_UNSUPPORTED;
   const long long room = (long long)s->max_blocks * c->page_size;
   const int most = s->max_rows < s->rows ? s->max_rows : s->rows;
   const long long Tp = ((s->max_prefix < room ? s->max_prefix : room) + 127) / 128, T = Tp + (most + 127) / 128;
+  const long long G = s->Hq / c->Hkv, rows = (long long)s->rows * G, seqs = s->B < s->rows ? s->B : s->rows;
+  // every sequence's rows end in a unit of their own, if they have any
+  auto units_of = [&](int shift) { return ((rows + seqs * ((1 << shift) - 1)) >> shift) * c->Hkv; };
+  if (units_of(7) >= (1ll << 24)) return ET_ERR_UNSUPPORTED;
+  int shift = 8;
   long long S = s->num_splits, whole = 0;
   if (S <= 0) {
-    // One block per SM.  A block costs about 14 of its tiles before its first and after its last, and a merge through the
-    // workspace six to nine more (64 rows, 32 heads, in 1 / 2 / 3 / 4 parts: 4096 keys 39.5 / 31.2 / 28.9 / 26.8 us, 1024 keys 18.9 /
-    // 20.3 / 21.2 / 20.9): parts pay where blocks are few and tiles many, and where a last round of whole units would leave
-    // SMs idle (512 units of 65 to 80 tiles, the last 56 in two parts: 505 us, whole: 534).  That round has the units with the
-    // fewest keys, little more than the prefix
-    const long long sms = sm_count(), rounds = units / sms, rest = units % sms, least = Tp + 1 < T ? Tp + 1 : T;
-    double best = (double)((units + sms - 1) / sms) * (14 + (double)T);
-    const double plain = best;
-    S = 1;
-    for (long long k = 2; k <= 64 && k <= T; ++k) {
-      const double all = (double)((units * k + sms - 1) / sms) * (14 + (double)((T + k - 1) / k) + 8);
-      if (all < best) {
-        best = all;
-        S = k;
-        whole = 0;
+    // One block per SM.  In units of 0.88 us, measured: a tile takes 1.2 where both groups have the same rows (1.0 to 1.4, by
+    // how many SMs are at it) and 1.9 for 256 rows, a block's start and end 14, a merge through the workspace 1, 0.04 a row
+    // and 1 a part.  So parts pay
+    //   where blocks are few and tiles many: 64 rows, 32 heads, in 1 / 2 / 3 / 4 parts: 4096 keys 39.5 / 29.6 / 28.0 / 26.2 us,
+    //   but 1024 keys 18.9 / 18.7 / 19.6 / 19.1;
+    //   where a last round of whole units would leave SMs idle: 512 units of 65 to 80 tiles, the last 56 in two parts 496 us,
+    //   whole 534 (that round has the units with the fewest keys, little more than the prefix).
+    // Units of 128 rows pay where those of 256 leave half of the SMs idle: 512 rows, 32 heads, 4096 keys 49.7 against 72.5 us
+    const long long sms = sm_count(), least = Tp + 1 < T ? Tp + 1 : T;
+    double best = 0.0;
+    for (int u = 8; u >= 7; --u) {
+      if (u == 7 && most * G <= 128) break;  // the same units
+      const long long units = units_of(u), rounds = units / sms, rest = units % sms;
+      const double tile = u == 8 && most * G > 128 ? 1.9 : 1.2;
+      const double merge = 1 + 0.04 * (double)(most * G < (1 << u) ? most * G : 1 << u);
+      auto block = [&](long long tiles, long long parts) {
+        return 14 + tile * (double)((tiles + parts - 1) / parts) + (parts > 1 ? merge + (double)parts : 0.0);
+      };
+      const double plain = (double)((units + sms - 1) / sms) * block(T, 1);
+      double cost = plain;
+      long long parts = 1, first = 0;
+      for (long long k = 2; k <= 64 && k <= T; ++k) {
+        const double all = (double)((units * k + sms - 1) / sms) * block(T, k);
+        if (all < cost && all < 0.95 * plain) {
+          cost = all;
+          parts = k;
+          first = 0;
+        }
+        if (!rounds || !rest) continue;
+        const double last = plain - block(least, 1) + (double)((rest * k + sms - 1) / sms) * block(least, k);
+        if (last < cost && last < 0.95 * plain) {
+          cost = last;
+          parts = k;
+          first = rounds * sms;
+        }
       }
-      if (!rounds || !rest) continue;
-      const double last = plain - (14 + (double)least) + (double)((rest * k + sms - 1) / sms) * (14 + (double)((least + k - 1) / k) + 8);
-      if (last < best && last < 0.95 * plain) {
-        best = last;
-        S = k;
-        whole = rounds * sms;
+      if (u == 8 || cost < 0.95 * best) {
+        best = cost;
+        shift = u;
+        S = parts;
+        whole = first;
       }
     }
   }
+  const long long units = units_of(shift);
   if (S > T) S = T;
   if (S > 64) S = 64;
   if (S < 1 || units - whole > kChunkCounters) S = 1;
   p->tc.S = (int)S;
-  p->tc.tiles = (int)tiles;
+  p->tc.shift = shift;
+  p->tc.tiles = (int)(units / c->Hkv);
   p->tc.whole = S > 1 ? (int)whole : 0;
   if (S > 1) {
-    const size_t slots = (size_t)(units - whole) * S * 256;
+    const size_t slots = (size_t)(units - whole) * S << shift;
     p->tc.ml_off = kChunkCounters * sizeof(unsigned int);
     p->tc.o_off = p->tc.ml_off + slots * sizeof(float2);
     p->ws = p->tc.o_off + slots * c->d * sizeof(float);

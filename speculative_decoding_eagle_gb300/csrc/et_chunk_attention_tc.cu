@@ -143,8 +143,9 @@ __device__ __forceinline__ void ct_commit(uint32_t bar, uint32_t lead) {
 }
 struct ChunkTcArgs {
   ChunkArgs c;
-  int S;                 // parts of a unit's tiles at most (a unit: 256 rows of a KV head)
-  int tiles;             // tiles of 256 rows per KV head in the grid
+  int S;                 // parts of a unit's tiles at most
+  int shift;             // a unit: 1 << shift (token, head) rows of a KV head, 128 or 256
+  int tiles;             // units per KV head in the grid
   int whole;             // the first units, each a block
   int q_tma;             // q by TMA: the heads of a group divide a tile's 128 rows
   int box;               // rows per TMA box of a page
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   __syncthreads();
   pdl_wait();  // the previous kernel in the stream has completed
 
-  // ---- which rows: tile `index` of the batch's tiles of 256 rows, in the sequences' order ----
+  // ---- which rows: unit `index` of a KV head's units, in the sequences' order ----
   const int behind = (int)blockIdx.x - ca.whole;  // a block of the units in parts
   const int cut = behind < 0 ? 0 : behind / ca.S, part = behind < 0 ? 0 : behind - cut * ca.S;
   const int unit = behind < 0 ? (int)blockIdx.x : ca.whole + cut;
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         L = paged_prefix(a, b, ignore);
         if (ignore && blockIdx.x == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
         if (L >= 0 && n > 0) {
-          mine = (int)(((long long)n * a.G + 255) >> 8);
+          mine = (int)(((long long)n * a.G + (1 << ca.shift) - 1) >> ca.shift);
           keys = tiles_of(L, kCtKeys) + tiles_of(n, kCtKeys);
         }
       }
@@ -266,9 +267,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   const int first = s_first, nrows = s_rows, L = s_prefix;
   // the last tiles have the most keys: they go out first
   const long long all_rows = (long long)nrows * a.G;
-  const int row_tiles = (int)((all_rows + 255) >> 8);
-  const int R0 = (row_tiles - 1 - s_tile) << 8;                    // first row of the KV head's (token, head) rows
-  const int real = (int)min(256ll, all_rows - R0);
+  const int row_tiles = (int)((all_rows + (1 << ca.shift) - 1) >> ca.shift);
+  const int R0 = (row_tiles - 1 - s_tile) << ca.shift;             // first row of the KV head's (token, head) rows
+  const int real = (int)min(1ll << ca.shift, all_rows - R0);
   const bool shared_rows = uni(real <= 128) != 0;                            // both groups have the same rows
   const int tok_first = ct_token(ca, R0), tok_last = ct_token(ca, R0 + real - 1);
   const int Tp = tiles_of(L, kCtKeys), To = tok_last / kCtKeys + 1, T = Tp + To;
@@ -901,7 +902,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   float2 *xm = reinterpret_cast<float2 *>(sm + Sh::off_v8);                    // [128]
   // the rows as they go out: behind the other group's, or (fp32 rows of both groups) from the start
   const uint32_t stage = sb + (parts > 1 && !shared_rows ? Sh::off_q : Sh::off_k);
-  const long long slot0 = ((long long)cut * ca.S + part) * 256;
+  const long long slot0 = (((long long)cut * ca.S + part) << ca.shift);
   const int w = warp >> 2, r = t & 127, Rr = shared_rows ? r : 128 * w + r;
   const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCtColO + 128u * (uint32_t)w;
   if (shared_rows && w == 1) {
@@ -1007,26 +1008,50 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   if (parts == 1) return;
   // ---- the parts' rows, merged by the last block to arrive ----
   if (!arrive_last(ca.cnt + cut, (unsigned)parts, &s_last)) return;
-  const long long base = (long long)cut * ca.S * 256;
-#pragma unroll 1
-  for (int x = t; x < real * (D / 4); x += kCtThreads) {
-    const int rr = x / (D / 4), c = x % (D / 4);
+  const long long base = (long long)cut * ca.S << ca.shift;
+  float *share = reinterpret_cast<float *>(sm);  // [parts][256]: what a part's row counts for
+  if (t < real) {
     float M = -3e38f, sum = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(&ca.part_ml[base + k * 256 + rr]).x);
+    for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(&ca.part_ml[base + (k << ca.shift) + t]).x);
     for (int k = 0; k < parts; ++k) {
-      const float2 e = __ldcg(&ca.part_ml[base + k * 256 + rr]);
-      const float4 y = __ldcg(&ca.part_o[(base + k * 256 + rr) * (D / 4) + c]);
+      const float2 e = __ldcg(&ca.part_ml[base + (k << ca.shift) + t]);
       const float f = ex2_fast(e.x - M);
       sum = fmaf(e.y, f, sum);
-      v.x = fmaf(y.x, f, v.x); v.y = fmaf(y.y, f, v.y); v.z = fmaf(y.z, f, v.z); v.w = fmaf(y.w, f, v.w);
+      share[k * 256 + t] = f;
     }
-    const int R = R0 + rr, i = ct_token(ca, R), h = g * a.G + (R - i * a.G);
-    const long long row = (long long)(first + i) * a.Hq + h;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + 4 * c) =
-        make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-    if (c == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+    for (int k = 0; k < parts; ++k) share[k * 256 + t] *= inv;
+    const int R = R0 + t, i = ct_token(ca, R);
+    if (a.lse)
+      a.lse[(long long)(first + i) * a.Hq + g * a.G + (R - i * a.G)] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+  }
+  __syncthreads();
+  // four pieces a thread, two parts at a time: eight loads under way
+  const int pieces = real * (D / 4);
+#pragma unroll 1
+  for (int x0 = t; x0 < pieces; x0 += 4 * kCtThreads) {
+    float4 v[4] = {};
+#pragma unroll 2
+    for (int k = 0; k < parts; ++k) {
+      const float4 *from = ca.part_o + (base + (k << ca.shift)) * (D / 4);
+      float4 y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = __ldcg(&from[min(x0 + e * kCtThreads, pieces - 1)]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = share[k * 256 + min(x0 + e * kCtThreads, pieces - 1) / (D / 4)];
+        v[e].x = fmaf(y[e].x, f, v[e].x); v[e].y = fmaf(y[e].y, f, v[e].y);
+        v[e].z = fmaf(y[e].z, f, v[e].z); v[e].w = fmaf(y[e].w, f, v[e].w);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int x = x0 + e * kCtThreads, rr = x / (D / 4), c = x % (D / 4);
+      if (x >= pieces) break;
+      const int R = R0 + rr, i = ct_token(ca, R), h = g * a.G + (R - i * a.G);
+      *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + ((long long)(first + i) * a.Hq + h) * D + 4 * c) =
+          make_uint2(pack_bf16x2(v[e].x, v[e].y), pack_bf16x2(v[e].z, v[e].w));
+    }
   }
 }
 
@@ -1067,6 +1092,7 @@ et_status chunk_tc_launch(const et_paged_cache *cache, const ChunkArgs &c, const
   ChunkTcArgs ca;
   ca.c = c;
   ca.S = p.S;
+  ca.shift = p.shift;
   ca.tiles = p.tiles;
   ca.whole = p.whole;
   const int P = cache->page_size;

@@ -15,8 +15,9 @@ struct ChunkArgs {
 
 // bf16 (et_chunk_attention_tc.cu): blocks of 256 (token, head) rows of a KV head
 struct ChunkTcPlan {
-  int S;      // parts of a unit's keys at most (a unit: 256 rows of a KV head)
-  int tiles;  // tiles of 256 rows per KV head at most
+  int S;      // parts of a unit's keys at most
+  int shift;  // a unit: 1 << shift rows of a KV head, 128 or 256
+  int tiles;  // units per KV head at most
   int whole;  // units that stay in one part, the ones with the most keys
   size_t ml_off, o_off;
 };

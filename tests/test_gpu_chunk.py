@@ -147,7 +147,7 @@ def test_matches_the_formula(prefix, rows, Hq, Hkv, P, d, dtype, fmt):
     x.check()
 
 
-@pytest.mark.parametrize("splits", [1, 2, 3, 7])
+@pytest.mark.parametrize("splits", [0, 1, 2, 3, 7])
 @pytest.mark.parametrize("prefix,rows,Hq,Hkv,P,d", [
     ([2100], [300], 2, 2, 64, 128),                 # two tiles of rows over many tiles of keys
     ([1900], [270], 2, 2, 16, 64),
@@ -170,7 +170,7 @@ def test_many_tiles_in_any_number_of_parts(prefix, rows, Hq, Hkv, P, d, splits):
 @pytest.mark.parametrize("prefix,rows,Hq,Hkv,P,d", [
     ([2000], [700], 64, 8, 64, 128),                # 22 units of 256 rows a KV head
     ([1100, 0, 2300, -1, 40], [260, 600, 130, 9, 1], 64, 16, 32, 64),
-    ([1900] * 5, [33] * 5, 32, 32, 16, 128),         # 33 rows a unit
+    ([3900] * 5, [33] * 5, 32, 32, 16, 128),         # 33 rows a unit
 ])
 def test_whole_rounds_of_blocks_and_a_last_one_in_parts(prefix, rows, Hq, Hkv, P, d):
     """As many units as SMs go out whole; what is left over is taken in parts."""
