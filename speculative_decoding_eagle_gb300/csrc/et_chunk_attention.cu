@@ -5,8 +5,9 @@
 // k_chunk_rows: one block per 32 (token, head) rows of a KV head; online
 // softmax over tiles of 32 keys in fp32.  Scores: a thread has two rows and
 // two keys of the tile; output: two rows and D / 16 dims.  Bound by shared
-// memory reads and the fp32 units; fp32 inputs are for checks and small
-// models.
+// memory reads and the fp32 units, in small calls by latency (17.3 us: two
+// sequences of up to 40 rows after 128 cached, 4 heads of 64); fp32 inputs are
+// for checks and small models.
 #include "et_chunk_attn.cuh"
 
 namespace et {
@@ -241,7 +242,7 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
   const long long G = s->Hq / c->Hkv, rows = (long long)s->rows * G, seqs = s->B < s->rows ? s->B : s->rows;
   // every sequence's rows end in a unit of their own, if they have any
   auto units_of = [&](int shift) { return ((rows + seqs * ((1 << shift) - 1)) >> shift) * c->Hkv; };
-  if (units_of(7) >= (1ll << 24)) return ET_ERR_UNSUPPORTED;
+  if (units_of(8) >= (1ll << 24)) return ET_ERR_UNSUPPORTED;
   int shift = 8;
   long long S = s->num_splits, whole = 0;
   if (S <= 0) {
@@ -256,7 +257,7 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
     const long long sms = sm_count(), least = Tp + 1 < T ? Tp + 1 : T;
     double best = 0.0;
     for (int u = 8; u >= 7; --u) {
-      if (u == 7 && most * G <= 128) break;  // the same units
+      if (u == 7 && (most * G <= 128 || units_of(7) >= (1ll << 24))) break;  // the same units, or too many
       const long long units = units_of(u), rounds = units / sms, rest = units % sms;
       const double tile = u == 8 && most * G > 128 ? 1.9 : 1.2;
       const double merge = 1 + 0.04 * (double)(most * G < (1 << u) ? most * G : 1 << u);
