@@ -29,11 +29,11 @@
 // Few rows, or a last round of blocks that would not fill the SMs: a unit's
 // tiles are split over several blocks, which leave their rows in the
 // workspace; the last one to arrive merges them.
-// Bounds, measured: 2048 rows after 8192 cached, 64 / 8 heads, 495 us = 1250
-// TFLOP/s (64% of the measured bf16 rate); a tile of 256 x 128 takes about 3200
+// Bounds, measured: 2048 rows after 8192 cached, 64 / 8 heads, 486 us = 1272
+// TFLOP/s (66% of the measured bf16 rate); a tile of 256 x 128 takes about 3150
 // cycles of which the tensor cores work 2048: the rest is the softmax warps'
 // chain (scores out of tensor memory, exponentials, weights back) against the
-// two groups' turns.  16 sequences, mostly one row each, 199 us = 3.1 TB/s of
+// two groups' turns.  16 sequences, mostly one row each, 197 us = 3.1 TB/s of
 // codes: about 2100 cycles a tile where its bytes take 1400.  Beside its
 // tiles a block costs 11000 cycles to the first scores (rows, pages, q and the
 // first keys one after the other) and 9000 behind the last, which is most of a
@@ -151,6 +151,12 @@ __device__ __forceinline__ void ct_commit(uint32_t bar, uint32_t lead) {
       "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(lead)
       : "memory");
+}
+// two values -> two codes, round to nearest even, saturating, NaN kept
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+  return r;
 }
 struct ChunkTcArgs {
   ChunkArgs c;
@@ -458,16 +464,18 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     }
     top = max(top & 0xffffu, top >> 16);
     const bool odd = top >= 0x7f80u;  // NaN or infinity: the row scores NaN
-    // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8; half of e2 stays within fp32's exponents
-    const int e2 = top == 0u || odd ? 0 : 135 - max((int)(top >> 7), 1) - ((top & 0x7fu) > 0x60u ? 1 : 0);
-    const int ea = e2 >> 1, eb = e2 - ea;
-    f8 = a.scale_log2 * power_of_two(-ea) * power_of_two(-eb);
+    // 2^e2 lifts the largest magnitude into (224, 448], 448 = 1.75 * 2^8 (or, of rows below 2^-118, as far as fp32 goes)
+    const int e2 = top == 0u || odd ? 0 : min(126, 135 - max((int)(top >> 7), 1) - ((top & 0x7fu) > 0x60u ? 1 : 0));
+    f8 = a.scale_log2 * power_of_two(-e2);
     if (odd) f8 = f16 = __uint_as_float(0x7fc00000u);
-    if (n8 > 0 && (!shared_rows || warp < 4)) {
-      const float lift_a = power_of_two(ea), lift_b = power_of_two(eb);
+    if (n8 > 0) {
+      // (fp16 holds the lifted bf16 values, and their distance to the first term, as they are down to 2^-14, and with an error of
+      // 2^-25 below; the second term's last bit is 2^-9.)  Groups that share their rows take half of the dims each
+      const float lift = power_of_two(e2);
       const uint32_t dst = sb + Sh::off_q + (uint32_t)w * Sh::tile16;
+      const int c0 = shared_rows && warp >= 4 ? D / 32 : 0, c1 = shared_rows && warp < 4 ? D / 32 : D / 16;
 #pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
+      for (int c = c0; c < c1; ++c) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -475,16 +483,16 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           piece(2 * c + h, x);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            hi[2 * h + e] = lo[2 * h + e] = 0u;
+            uint32_t h2[2], l2[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float y0 = __uint_as_float(x[2 * e + k] << 16) * lift_a * lift_b;
-              const float y1 = __uint_as_float(x[2 * e + k] & 0xffff0000u) * lift_a * lift_b;
-              const uint32_t h2 = f32x2_to_f8x2<ET_KV_E4M3>(y0, y1), hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2);
-              const float2 hv = __half22float2(*reinterpret_cast<const __half2 *>(&hf));
-              hi[2 * h + e] |= h2 << (16 * k);
-              lo[2 * h + e] |= f32x2_to_f8x2<ET_KV_E4M3>(y0 - hv.x, y1 - hv.y) << (16 * k);
+              const __half2 y = __floats2half2_rn(__uint_as_float(x[2 * e + k] << 16) * lift, __uint_as_float(x[2 * e + k] & 0xffff0000u) * lift);
+              h2[k] = f16x2_to_e4m3x2(y);
+              const uint32_t hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2[k]);
+              l2[k] = f16x2_to_e4m3x2(__hsub2(y, *reinterpret_cast<const __half2 *>(&hf)));
             }
+            hi[2 * h + e] = h2[0] | h2[1] << 16;
+            lo[2 * h + e] = l2[0] | l2[1] << 16;
           }
         }
         sts128(dst + at8<D>(r, c), hi[0], hi[1], hi[2], hi[3]);
@@ -909,34 +917,32 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   if (*(volatile int *)&s_abort != 0 && t == 0) flag_status(a.dev_status, ET_DEV_TIMEOUT);
 
   // ---- the rows: one group's, or the two groups' halves of the keys joined ----
-  float *xo = reinterpret_cast<float *>(sm + Sh::off_q);                       // [D][128] of group 1
-  float2 *xm = reinterpret_cast<float2 *>(sm + Sh::off_v8);                    // [128]
+  float *xo = reinterpret_cast<float *>(sm + Sh::off_q);     // [D][128]: of each dim what the group gives that does not join it
+  float2 *xm = reinterpret_cast<float2 *>(sm + Sh::off_v8);  // [2][128]
   // the rows as they go out: behind the other group's, or (fp32 rows of both groups) from the start
   const uint32_t stage = sb + (parts > 1 && !shared_rows ? Sh::off_q : Sh::off_k);
   const long long slot0 = (((long long)cut * ca.S + part) << ca.shift);
   const int w = warp >> 2, r = t & 127, Rr = shared_rows ? r : 128 * w + r;
   const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCtColO + 128u * (uint32_t)w;
-  if (shared_rows && w == 1) {
-    xm[r] = make_float2(fresh ? -3e38f : ref, l);
-    if (items > 0) {
+  if (shared_rows && warp < 8) {  // a group joins half of the dims and gives the other half away
+    xm[128 * w + r] = make_float2(fresh ? -3e38f : ref, l);
+    float *give = xo + (1 - w) * (D / 2) * 128 + r;
 #pragma unroll 1
-      for (int p = 0; p < D / 8; ++p) {
-        uint32_t o[8];
-        pt_ld8(lanes + 8u * p, o);
+    for (int p = 0; p < D / 64; ++p) {
+      uint32_t o[32];
+      if (items > 0) {
+        tmem_ld32(lanes + (uint32_t)((1 - w) * (D / 2) + 32 * p), o);
         tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xo[(8 * p + e) * 128 + r] = __uint_as_float(o[e]);
       }
-    } else {
-      for (int e = 0; e < D; ++e) xo[e * 128 + r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) give[(32 * p + e) * 128] = items > 0 ? __uint_as_float(o[e]) : 0.f;
     }
   }
   __syncthreads();
-  const bool writes = warp < 8 && (w == 0 || !shared_rows);
-  if (writes) {
+  if (warp < 8) {
     float M = fresh ? -3e38f : ref, mine = 1.f, other = 0.f;
     if (shared_rows) {
-      const float2 y = xm[r];
+      const float2 y = xm[128 * (1 - w) + r];
       const float both = fmaxf(M, y.x);
       mine = ex2_fast(M - both);
       other = ex2_fast(y.x - both);
@@ -951,12 +957,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       mine *= inv;
       other *= inv;
-      if (Rr < real && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
-    } else if (Rr < real) {
+      if (Rr < real && a.lse && (w == 0 || !shared_rows)) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+    } else if (Rr < real && (w == 0 || !shared_rows)) {
       ca.part_ml[slot0 + Rr] = make_float2(M, l);
     }
 #pragma unroll 1
-    for (int p = 0; p < D / 32; ++p) {
+    for (int p = shared_rows ? w * (D / 64) : 0; p < (shared_rows ? (w + 1) * (D / 64) : D / 32); ++p) {
       uint32_t o[32];
       tmem_ld32(lanes + 32u * p, o);
       tmem_wait_ld();
