@@ -938,7 +938,8 @@ et_status et_rotary_frequencies(const et_rope_cfg *cfg, double *freq, float *fac
  * Masses are sums of w in 64-bit fixed point (2^-44 of the largest weight, w
  * evaluated to 2^-40), so tokens and kept sets do not depend on the order of
  * any sum and agree with 64-bit floating point but where a border lies within
- * about 2^-36 of the total.  No workspace; one launch, a thread-block cluster
+ * about 2^-36 of the total (V 2^-45 at worst, where a row's weights far below
+ * the largest are all alike).  No workspace; one launch, a thread-block cluster
  * per row.
  */
 et_status et_sample(const et_sample_shape *shape, const float *logits, const float *temperature, const int32_t *top_k,

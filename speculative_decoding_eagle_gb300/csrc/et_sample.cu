@@ -11,7 +11,8 @@
 // (the draw).
 //   Order of logits: a histogram over equal steps of the logit finds the step
 // with the border.  If it and the steps above hold few tokens, as they do for
-// all but flat rows, one block sorts these and answers everything.  Else
+// all but flat rows, one block sorts these and answers everything.  Else, if
+// that step alone holds few, one block sorts it and finds the border.  Else
 // histograms over the keys (order-preserving integer images of the logits)
 // inside the step follow, until one key value is left; equal keys are told
 // apart by id.  Counts and masses are integers, so blocks and atomics may come
@@ -67,7 +68,7 @@ struct SampleShared {
   unsigned int key_lo, key_hi;           // of the slice's members of the current bin
   unsigned long long mass;               // of the slice's kept tokens, or of the block's share of the bins
   Crossing crossing;
-  unsigned int listed;                   // tokens for the list, which takes kSaList (block 0)
+  unsigned int listed[3];                // tokens for each list that may be made (block 0)
   unsigned int kept_tau;
   int kept_cut;
   unsigned long long warp_mass[kSaWarps];
@@ -349,17 +350,101 @@ __device__ Crossing cross(const Row &row, unsigned int (*h)[kSaBins], unsigned l
 // steps of the logit below the maximum
 __device__ __forceinline__ int step_of(float z, float zm, float step) { return min(kSaBins - 1, (int)((zm - z) * step)); }
 
+// v[e] of thread t, number t + e * kSaThreads of n, ascending: a bitonic network; beyond n everything is ~0
+__device__ void block_sort(unsigned long long (&v)[2], int n, unsigned long long *buf) {
+  const int t = threadIdx.x;
+  const int count = n > kSaThreads ? 2 : 1;
+  for (int k = 2; k < 2 * n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      if (j == kSaThreads) {
+        if (v[1] < v[0]) {
+          const unsigned long long x = v[0];
+          v[0] = v[1];
+          v[1] = x;
+        }
+        continue;
+      }
+      if (j >= 32) {
+        __syncthreads();
+        for (int e = 0; e < count; ++e) buf[t + e * kSaThreads] = v[e];
+        __syncthreads();
+      } else if (k <= 32 && (t & ~31) >= n) {
+        continue;  // whole warps
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (e >= count) break;
+        const int i = t + e * kSaThreads;
+        const unsigned long long o = j >= 32 ? buf[i ^ j] : __shfl_xor_sync(0xffffffffu, v[e], j);
+        const bool low = ((i & j) == 0) == ((i & k) == 0);  // this place takes the smaller one
+        v[e] = low == (o < v[e]) ? o : v[e];
+      }
+    }
+}
+
+// The tokens that `in` holds of, from every block of the row into block 0's list, which has room for kSaList of them; how many
+// there are comes back.  `count` is zero before, and not used again.
+template <typename In>
+__device__ unsigned int gather(const Row &row, unsigned int *count, In in) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int i0 = 0; i0 < row.n; i0 += kSaThreads) {
+    const int i = i0 + threadIdx.x;
+    const float z = i < row.n ? row.z[i] : -INFINITY;
+    const bool here = z > -INFINITY && in(z, row.base + i);
+    const unsigned int m = __ballot_sync(0xffffffffu, here);
+    if (!m) continue;
+    unsigned int at = 0u;
+    if (lane == 0)
+      asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(cl_map(count, 0u)), "r"((unsigned int)__popc(m)) : "memory");
+    at = __shfl_sync(0xffffffffu, at, 0) + (unsigned int)__popc(m & ((1u << lane) - 1u));
+    if (here && at < kSaList)
+      cl_st_u64(cl_map(&row.sh->list[0], 0u) + 8u * at, ((unsigned long long)~order_key(z) << 32) | (unsigned int)(row.base + i));
+  }
+  row_sync(row.C);
+  return row.C > 1 ? cl_ld_u32(cl_map(count, 0u)) : *count;
+}
+
 // Where the cumulative weight in the order of the logits passes the border: the kept set that ends with that token.  The
 // first histogram's crossing is `c`.  MASS: weights are masses of the tokens in `in`; else counts.
 template <bool MASS>
 __device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weigher &weigh, float zm, float step, Crossing c,
-                       unsigned long long target, unsigned long long *s_red, int *s_id) {
+                       unsigned long long target, unsigned int *count, unsigned long long *s_red, int *s_id) {
   SampleShared *sh = row.sh;
   const int t = threadIdx.x, lane = t & 31;
+  if (c.bin < 0) return in;  // more was asked for than there is: everything stays
+  // ---- the step's tokens, if they are few: block 0 sorts them ----
+  if (gather(row, count, [&](float z, int id) { return step_of(z, zm, step) == c.bin && in(order_key(z), id); }) <= kSaList) {
+    if (row.rank == 0) {
+      const int n = (int)*count, places = n > kSaThreads ? 2 : 1;
+      unsigned long long mine[2], sum = c.above;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = t + e * kSaThreads;
+        mine[e] = i < n ? sh->list[i] : ~0ull;
+      }
+      block_sort(mine, n, sh->weight);
+      for (int e = 0; e < places; ++e) {
+        const unsigned int key = ~(unsigned int)(mine[e] >> 32);
+        const unsigned long long w = t + e * kSaThreads >= n ? 0ull : MASS ? weigh(key_value(key)) : 1ull;
+        unsigned long long all;
+        const unsigned long long incl = sum + block_scan_u64(w, s_red, all);
+        if (incl - w < target && target <= incl) {  // one token
+          sh->kept_tau = key;
+          sh->kept_cut = (int)(unsigned int)mine[e];
+        }
+        sum += all;
+      }
+    }
+    row_sync(row.C);
+    Kept out;
+    out.tau = row.C > 1 ? cl_ld_u32(cl_map(&sh->kept_tau, 0u)) : sh->kept_tau;
+    out.cut = row.C > 1 ? cl_ld_s32(cl_map(&sh->kept_cut, 0u)) : sh->kept_cut;
+    return out;
+  }
   unsigned int lo = 0u, hi = 0xffffffffu;
   int shift = -1;  // -1: bins are steps of the logit below the maximum; else (hi - key) >> shift
   for (int round = 0; round < 8; ++round) {  // 1 + at most 4 rounds: a round leaves 2^23 of 2^32 keys, 2^14, 2^5, one
-    if (c.bin < 0) return in;  // more was asked for than there is: everything stays
     auto bin_of = [&](unsigned int key, float z) -> int { return shift < 0 ? step_of(z, zm, step) : (int)((hi - key) >> shift); };
     if (t == 0) {
       sh->key_lo = 0xffffffffu;
@@ -418,38 +503,6 @@ __device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weig
   return out;
 }
 
-// v[e] of thread t, number t + e * kSaThreads of n, ascending: a bitonic network; beyond n everything is ~0
-__device__ void block_sort(unsigned long long (&v)[2], int n, unsigned long long *buf) {
-  const int t = threadIdx.x;
-  const int count = n > kSaThreads ? 2 : 1;
-  for (int k = 2; k < 2 * n; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      if (j == kSaThreads) {
-        if (v[1] < v[0]) {
-          const unsigned long long x = v[0];
-          v[0] = v[1];
-          v[1] = x;
-        }
-        continue;
-      }
-      if (j >= 32) {
-        __syncthreads();
-        for (int e = 0; e < count; ++e) buf[t + e * kSaThreads] = v[e];
-        __syncthreads();
-      } else if (k <= 32 && (t & ~31) >= n) {
-        continue;  // whole warps
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (e >= count) break;
-        const int i = t + e * kSaThreads;
-        const unsigned long long o = j >= 32 ? buf[i ^ j] : __shfl_xor_sync(0xffffffffu, v[e], j);
-        const bool low = ((i & j) == 0) == ((i & k) == 0);  // this place takes the smaller one
-        v[e] = low == (o < v[e]) ? o : v[e];
-      }
-    }
-}
-
 __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   extern __shared__ __align__(16) float s_z[];
   __shared__ SampleShared sh;
@@ -470,7 +523,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   const int b = blockIdx.x / a.cluster;
   if (t < 64) s_table[t] = make_float2(kPowers.hi[t], kPowers.lo[t]);
   for (int x = t; x < 2 * kSaLimbs * kSaBins; x += kSaThreads) (&sh.hist[0][0][0])[x] = 0u;
-  if (t == 0) sh.listed = 0u;
+  if (t < 3) sh.listed[t] = 0u;
   pdl_wait();
   pdl_trigger();
   // ---- the slice into shared memory; its extremes ----
@@ -561,6 +614,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
   kept.tau = 0u;
   kept.cut = -1;  // every key above zero: -inf is above it, and left out where it matters
   int token = -1;
+  bool listed_one = false;  // block 0 has answered everything from the list
   float logprob = -INFINITY;
   if (t == 0 && !none && !greedy) {
     unsigned int key_min = 0u;  // min-p: keys from this one on
@@ -592,7 +646,6 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
     weigh.table = s_table;
     const unsigned int key_min = __float_as_uint(s_row[2]);
     const bool by_count = k > 0 && k < a.V, by_mass = p < 1.f;
-    bool done = false;
     if (by_count || by_mass) {
       // steps of the logit: the row's own range, but no more than what has mass
       const float range = fminf(zm - zl, fmaxf(32.f * T, 32.f));
@@ -618,24 +671,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
       unsigned int listed = ~0u;
       if (x.bin >= 0) {
         // ---- the tokens up to the border's step go to block 0, if they are few ----
-#pragma unroll 4
-        for (int i0 = 0; i0 < row.n; i0 += kSaThreads) {
-          const int i = i0 + t;
-          const float z = i < row.n ? s_z[i] : -INFINITY;
-          const bool in = z > -INFINITY && step_of(z, zm, step) <= x.bin;
-          const unsigned int m = __ballot_sync(0xffffffffu, in);
-          if (!m) continue;
-          unsigned int at = 0u;
-          if (lane == 0) {
-            const uint32_t n = cl_map(&sh.listed, 0u);
-            asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(n), "r"((unsigned int)__popc(m)) : "memory");
-          }
-          at = __shfl_sync(0xffffffffu, at, 0) + (unsigned int)__popc(m & ((1u << lane) - 1u));
-          if (in && at < kSaList)
-            cl_st_u64(cl_map(&sh.list[0], 0u) + 8u * at, ((unsigned long long)~order_key(z) << 32) | (unsigned int)(row.base + i));
-        }
-        row_sync(row.C);
-        listed = row.C > 1 ? cl_ld_u32(cl_map(&sh.listed, 0u)) : sh.listed;
+        listed = gather(row, &sh.listed[0], [&](float z, int) { return step_of(z, zm, step) <= x.bin; });
       }
       if (listed <= kSaList) {
         // ---- one block sorts them and answers everything ----
@@ -675,6 +711,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
             sh.weight[i] = w[e];
             mine[e] = i < m ? (mine[e] << 32) | (unsigned int)i : ~0ull;
           }
+          if (a.truncated && row.C > 1) cl_arrive();  // the other blocks know what is kept while this one draws
           block_sort(mine, m, sh.list);
           __syncthreads();
           unsigned long long all = 0ull;
@@ -693,23 +730,26 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
               int ignore = 0;
               if (a.logprob) a.logprob[b] = log_share(sanitize_logit(a.logits[(long long)b * a.row_stride + token], ignore), all);
             }
-          __syncthreads();
-        }
-        if (!a.truncated) {
-          if (row.C > 1) cl_sync();  // block 0's memory has been read
-          return;
-        }
-        if (row.C > 1) {
+          __syncwarp();
+          if (!a.truncated) {
+            if (row.C > 1) cl_sync();  // no block leaves while another reads its memory
+            return;
+          }
+          if (row.C > 1) cl_wait();
+          kept.tau = sh.kept_tau;
+          kept.cut = sh.kept_cut;
+        } else {
+          if (!a.truncated) {  // this block's memory is not read any more, and it has read block 0's
+            cl_arrive();
+            return;
+          }
           cl_sync();
           kept.tau = cl_ld_u32(cl_map(&sh.kept_tau, 0u));
           kept.cut = cl_ld_s32(cl_map(&sh.kept_cut, 0u));
-        } else {
-          kept.tau = sh.kept_tau;
-          kept.cut = sh.kept_cut;
         }
-        done = true;
+        listed_one = true;
       } else if (by_count) {
-        kept = border<false>(row, a, kept, weigh, zm, step, x, target, s_red, &s_id);
+        kept = border<false>(row, a, kept, weigh, zm, step, x, target, &sh.listed[1], s_red, &s_id);
         if (by_mass) {
           row.buf ^= 1;
           h = sh.hist[row.buf];
@@ -720,13 +760,13 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
             if (z > -INFINITY && kept(order_key(z), row.base + i)) add_mass(h, step_of(z, zm, step), weigh(z));
           }
           x = cross<true>(row, h, 0ull, p, &target, s_red);
-          kept = border<true>(row, a, kept, weigh, zm, step, x, target, s_red, &s_id);
+          kept = border<true>(row, a, kept, weigh, zm, step, x, target, &sh.listed[2], s_red, &s_id);
         }
       } else {
-        kept = border<true>(row, a, kept, weigh, zm, step, x, target, s_red, &s_id);
+        kept = border<true>(row, a, kept, weigh, zm, step, x, target, &sh.listed[1], s_red, &s_id);
       }
     }
-    if (!done) {
+    if (!listed_one) {
       if (key_min > order_key(zm)) {  // the largest token alone
         kept.tau = order_key(zm);
         kept.cut = (int)top;
@@ -758,7 +798,11 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
       out[i] = kept(order_key(z), row.base + i) ? z : -INFINITY;
     }
   }
-  if (row.C > 1) cl_sync();  // no block leaves while another reads its memory
+  __syncwarp();
+  if (row.C > 1) {
+    if (listed_one && row.rank > 0) cl_arrive();
+    else cl_sync();
+  }
 }
 
 }  // namespace
