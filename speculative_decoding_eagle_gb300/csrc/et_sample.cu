@@ -27,8 +27,8 @@
 // Measured: nothing comes near the memory's rate.  One row of 32000: 16 us, the
 // latency of a dozen steps that follow on one another (load, extremes,
 // histogram, crossing, list, sort by weight, sort by id, draw), each gone
-// through once.  244 rows of 32000, top-p and truncated logits: 80 us.  128 rows
-// of 100003: 133 us, of which the weights' arithmetic (65 instructions a token)
+// through once.  244 rows of 32000, top-p and truncated logits: 79 us.  128 rows
+// of 100003: 120 us, of which the weights' arithmetic (65 instructions a token)
 // is a third.
 #include "et_common.cuh"
 
