@@ -444,17 +444,16 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   }
   if (!ca.q_tma) __syncthreads();
   float f8 = 0.f, f16 = a.scale_log2;  // what a score of lifted q and codes, or of bf16 values, stands for in log2 units
-  if (warp < 8) {
-    // a softmax thread's row: its largest magnitude, as the bits of a bf16 value (they order like the values)
+  const uint32_t my_q = raw_q + (shared_rows ? 0u : (uint32_t)(warp >> 2) * Sh::tile16);  // a softmax warp's tile
+  auto piece = [&](int c, uint32_t (&x)[4]) {  // eight dims of a softmax thread's row
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(my_q + (uint32_t)(c >> 3) * Sh::half16 + sw128(t & 127, c & 7))
+                 : "memory");
+  };
+  auto row_exponent = [&]() -> int {
+    // the row's largest magnitude, as the bits of a bf16 value (they order like the values)
     if (ca.q_tma) pt_wait(bar(C_QRAW), 0, &s_abort, limit);
-    const int r = t & 127, w = shared_rows ? 0 : warp >> 2;
-    const uint32_t src = raw_q + (uint32_t)w * Sh::tile16;
-    auto piece = [&](int c, uint32_t (&x)[4]) {  // eight dims
-      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                   : "r"(src + (uint32_t)(c >> 3) * Sh::half16 + sw128(r, c & 7))
-                   : "memory");
-    };
     uint32_t top = 0u;
 #pragma unroll 4
     for (int c = 0; c < D / 8; ++c) {
@@ -468,36 +467,38 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const int e2 = top == 0u || odd ? 0 : min(126, 135 - max((int)(top >> 7), 1) - ((top & 0x7fu) > 0x60u ? 1 : 0));
     f8 = a.scale_log2 * power_of_two(-e2);
     if (odd) f8 = f16 = __uint_as_float(0x7fc00000u);
-    if (n8 > 0) {
-      // (fp16 holds the lifted bf16 values, and their distance to the first term, as they are down to 2^-14, and with an error of
-      // 2^-25 below; the second term's last bit is 2^-9.)  Groups that share their rows take half of the dims each
-      const float lift = power_of_two(e2);
-      const uint32_t dst = sb + Sh::off_q + (uint32_t)w * Sh::tile16;
-      const int c0 = shared_rows && warp >= 4 ? D / 32 : 0, c1 = shared_rows && warp < 4 ? D / 32 : D / 16;
+    return e2;
+  };
+  if (warp < 8 && n8 > 0) {
+    // (fp16 holds the lifted bf16 values, and their distance to the first term, as they are down to 2^-14, and with an error of
+    // 2^-25 below; the second term's last bit is 2^-9.)  Groups that share their rows take half of the dims each
+    const float lift = power_of_two(row_exponent());
+    const int r = t & 127;
+    const uint32_t dst = sb + Sh::off_q + (shared_rows ? 0u : (uint32_t)(warp >> 2) * Sh::tile16);
+    const int c0 = shared_rows && warp >= 4 ? D / 32 : 0, c1 = shared_rows && warp < 4 ? D / 32 : D / 16;
 #pragma unroll 1
-      for (int c = c0; c < c1; ++c) {
-        uint32_t hi[4], lo[4];
+    for (int c = c0; c < c1; ++c) {
+      uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[4];
-          piece(2 * c + h, x);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[4];
+        piece(2 * c + h, x);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t h2[2], l2[2];
+        for (int e = 0; e < 2; ++e) {
+          uint32_t h2[2], l2[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const __half2 y = __floats2half2_rn(__uint_as_float(x[2 * e + k] << 16) * lift, __uint_as_float(x[2 * e + k] & 0xffff0000u) * lift);
-              h2[k] = f16x2_to_e4m3x2(y);
-              const uint32_t hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2[k]);
-              l2[k] = f16x2_to_e4m3x2(__hsub2(y, *reinterpret_cast<const __half2 *>(&hf)));
-            }
-            hi[2 * h + e] = h2[0] | h2[1] << 16;
-            lo[2 * h + e] = l2[0] | l2[1] << 16;
+          for (int k = 0; k < 2; ++k) {
+            const __half2 y = __floats2half2_rn(__uint_as_float(x[2 * e + k] << 16) * lift, __uint_as_float(x[2 * e + k] & 0xffff0000u) * lift);
+            h2[k] = f16x2_to_e4m3x2(y);
+            const uint32_t hf = f8x2_to_f16x2<ET_KV_E4M3>((uint16_t)h2[k]);
+            l2[k] = f16x2_to_e4m3x2(__hsub2(y, *reinterpret_cast<const __half2 *>(&hf)));
           }
+          hi[2 * h + e] = h2[0] | h2[1] << 16;
+          lo[2 * h + e] = l2[0] | l2[1] << 16;
         }
-        sts128(dst + at8<D>(r, c), hi[0], hi[1], hi[2], hi[3]);
-        sts128(dst + Sh::tile8 + at8<D>(r, c), lo[0], lo[1], lo[2], lo[3]);
       }
+      sts128(dst + at8<D>(r, c), hi[0], hi[1], hi[2], hi[3]);
+      sts128(dst + Sh::tile8 + at8<D>(r, c), lo[0], lo[1], lo[2], lo[3]);
     }
   }
   fence_async_smem();
@@ -778,6 +779,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const int tok = Rr < real ? ct_token(ca, R0 + Rr) : -1;  // rows that do not exist see nothing
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t sc = lanes + kCtColS + 128u * (uint32_t)w, oc = lanes + kCtColO + 128u * (uint32_t)w;
+    if (n8 == 0) row_exponent();  // under the first product
     bool dead = false;
     // the weights of one tile from its scores; `own`: the new rows' keys
     auto tile = [&](int i, auto own_, auto masked_) {
