@@ -279,13 +279,13 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     }
   }
   auto uni = [](int x) -> int { return __shfl_sync(0xffffffffu, x, 0); };  // the same in every lane, and known to be so
-  const int b = s_seq;
+  const int b = uni(s_seq);
   if (b < 0) return;  // fewer tiles than the grid has places for
-  const int first = s_first, nrows = s_rows, L = s_prefix;
+  const int first = uni(s_first), nrows = uni(s_rows), L = uni(s_prefix);
   // the last tiles have the most keys: they go out first
   const long long all_rows = (long long)nrows * a.G;
   const int row_tiles = (int)((all_rows + (1 << ca.shift) - 1) >> ca.shift);
-  const int R0 = (row_tiles - 1 - s_tile) << ca.shift;             // first row of the KV head's (token, head) rows
+  const int R0 = (row_tiles - 1 - uni(s_tile)) << ca.shift;             // first row of the KV head's (token, head) rows
   const int real = (int)min(1ll << ca.shift, all_rows - R0);
   const bool shared_rows = uni(real <= 128) != 0;                            // both groups have the same rows
   const int tok_first = ct_token(ca, R0), tok_last = ct_token(ca, R0 + real - 1);
@@ -512,9 +512,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   bool fresh = true;          // no key seen yet
   int items = 0;              // tiles this group has taken
 
-  // a softmax thread holds a row's 128 scores: it gets registers of the other warps (512 x 128 = 256 x 64 + 256 x 192)
+  // a softmax thread holds a row's 128 scores: it gets registers of the other warps (512 x 128 = 256 x 48 + 256 x 208; at 64 and 192 it spills)
   if (warp >= kCtTmaWarp) {
-  regs_down<64>();
+  regs_down<48>();
   if (warp == kCtTmaWarp) {
     // ---------------- TMA: K ----------------
     bool ok = true;
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   roles_end();
   regs_up<128>();
   } else if (warp >= 8) {
-    regs_down<64>();
+    regs_down<48>();
     // ---------------- V as the products take it ----------------
     const int gt = t & 127;
     bool ok = true;
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     roles_end();
     regs_up<128>();
   } else {
-    regs_up<192>();
+    regs_up<208>();
     // ---------------- softmax: group w, a row per thread ----------------
     const int w = warp >> 2, r = t & 127, Rr = shared_rows ? r : 128 * w + r;
     const int tok = Rr < real ? ct_token(ca, R0 + Rr) : -1;  // rows that do not exist see nothing
@@ -893,7 +893,20 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (lane == 0) mbar_arrive(bar(C_PFULL + w));
       ++items;
     };
-    for (int i = 0; i < n; ++i) {
+    // A warp without a row that exists (few rows) leaves its lanes of P as they are, which is its own rows' matter, and the
+    // issue slots to the others
+    const bool idle = uni((Rr & ~31) >= real) != 0;
+    for (int i = 0; idle && i < n; ++i) {
+      if (!uses(w, i)) continue;
+      dead = __any_sync(0xffffffffu, !pt_wait(bar(C_SFULL + w), (uint32_t)items & 1u, &s_abort, limit));
+      if (dead) break;
+      if (lane == 0) {
+        mbar_arrive(bar(C_PHALF + w));
+        mbar_arrive(bar(C_PFULL + w));
+      }
+      ++items;
+    }
+    for (int i = idle ? n : 0; i < n; ++i) {
       if (!uses(w, i)) continue;
       if (i < n8) dead = dead || !pt_wait(bar(C_SCALES + i % kCtSlots), (uint32_t)(i / kCtSlots) & 1u, &s_abort, limit);
       dead = __any_sync(0xffffffffu, dead);
