@@ -29,12 +29,12 @@
 // Few rows, or a last round of blocks that would not fill the SMs: a unit's
 // tiles are split over several blocks, which leave their rows in the
 // workspace; the last one to arrive merges them.
-// Bounds, measured: 2048 rows after 8192 cached, 64 / 8 heads, 486 us = 1272
-// TFLOP/s (66% of the measured bf16 rate); a tile of 256 x 128 takes about 3150
+// Bounds, measured: 2048 rows after 8192 cached, 64 / 8 heads, 467 us = 1323
+// TFLOP/s (68% of the measured bf16 rate); a tile of 256 x 128 takes about 3000
 // cycles of which the tensor cores work 2048: the rest is the softmax warps'
 // chain (scores out of tensor memory, exponentials, weights back) against the
-// two groups' turns.  16 sequences, mostly one row each, 197 us = 3.1 TB/s of
-// codes: about 2100 cycles a tile where its bytes take 1400.  Beside its
+// two groups' turns.  16 sequences, mostly one row each, 182 us = 3.4 TB/s of
+// codes: about 1900 cycles a tile where its bytes take 1400.  Beside its
 // tiles a block costs 11000 cycles to the first scores (rows, pages, q and the
 // first keys one after the other) and 9000 behind the last, which is most of a
 // call over a short prefix.

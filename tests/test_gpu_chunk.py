@@ -167,20 +167,21 @@ def test_many_tiles_in_any_number_of_parts(prefix, rows, Hq, Hkv, P, d, splits):
     assert torch.equal(first[0], x.out) and torch.equal(first[1], x.lse)
 
 
-@pytest.mark.parametrize("prefix,rows,Hq,Hkv,P,d", [
-    ([2000], [700], 64, 8, 64, 128),                # 22 units of 256 rows a KV head
-    ([1100, 0, 2300, -1, 40], [260, 600, 130, 9, 1], 64, 16, 32, 64),
-    ([3900] * 5, [33] * 5, 32, 32, 16, 128),         # 33 rows a unit
+@pytest.mark.parametrize("prefix,rows,Hq,Hkv,P,d,unit", [
+    ([2000], [700], 64, 8, 64, 128, 256),           # 22 units of 256 rows a KV head
+    ([1100, 0, 2300, -1, 40], [260, 600, 130, 9, 1], 64, 16, 32, 64, 256),
+    ([3900] * 5, [33] * 5, 32, 32, 16, 128, 256),    # 33 rows a unit
+    ([16384], [385], 64, 8, 64, 64, 128),           # 25 units of 128 rows a KV head
 ])
-def test_whole_rounds_of_blocks_and_a_last_one_in_parts(prefix, rows, Hq, Hkv, P, d):
+def test_whole_rounds_of_blocks_and_a_last_one_in_parts(prefix, rows, Hq, Hkv, P, d, unit):
     """As many units as SMs go out whole; what is left over is taken in parts."""
     x = Batch(prefix, rows, Hq, Hkv, d, P, seed=5)
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    units = Hkv * ((x.T * (Hq // Hkv) + 255 * len(rows)) // 256)
+    units = Hkv * ((x.T * (Hq // Hkv) + (unit - 1) * len(rows)) // unit)
     shape = E.ChunkAttnShape(B=len(prefix), rows=x.T, Hq=Hq, max_rows=max(rows), max_blocks=x.table.shape[1])
     S, need = E.et_chunk_attention_paged_splits(shape, x.cache), E.et_chunk_attention_paged_workspace_size(shape, x.cache)
     assert units > sms and S > 1
-    assert need == 16384 * 4 + (units % sms) * S * 256 * (8 + 4 * d)
+    assert need == 16384 * 4 + (units % sms) * S * unit * (8 + 4 * d)
     ws = x.run()
     x.check()
     first = x.out.clone(), x.lse.clone()
