@@ -284,6 +284,25 @@ def test_scales_far_from_one(scales):
     x.check()
 
 
+def test_queries_of_the_smallest_magnitudes():
+    """Rows down to the last subnormal, and zero: every key counts the same, the sum of weights stays right."""
+    x = Batch([300, 0], [130, 70], 4, 2, 128, 32, seed=9)
+    for i, f in enumerate([0.0, 2.0 ** -133, 2.0 ** -126, 2.0 ** -118, 2.0 ** -117, 2.0 ** -60, 2.0 ** -9, 1.0]):
+        x.q[i::8] = (x.q[i::8].float().sign() * f).to(torch.bfloat16) if f < 2.0 ** -100 else x.q[i::8] * f
+    x.run()
+    x.check()
+
+
+def test_more_sequences_than_are_ordered():
+    """Batches past 32 sequences keep their order; whole units, parts and sequences without rows among them."""
+    for n, splits in ((33, 0), (47, 3), (70, 1), (130, 0)):
+        prefix = [(37 * b) % 290 - (b % 11 == 5) * 300 for b in range(n)]
+        rows = [0 if b % 7 == 3 else 1 + (b * b) % 9 * (40 if b % 13 == 0 else 1) for b in range(n)]
+        x = Batch([max(p, -1) for p in prefix], rows, 4, 2, 64, 16, seed=n)
+        x.run(splits=splits)
+        x.check()
+
+
 def test_scores_far_apart():
     """Scores that rise by thousands from tile to tile: the reference moves each time; and one row's lie far below another's."""
     x = Batch([1024], [130], 1, 1, 128, 64, seed=11)
