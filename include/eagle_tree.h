@@ -269,8 +269,9 @@ typedef enum {
     ET_ROPE_PLAIN = 0,   /* f_i = theta^(-2 i / rot) */
     ET_ROPE_LINEAR = 1,  /* f_i / scale */
     ET_ROPE_BASE = 2,    /* theta replaced by theta * scale^(rot / (rot - 2)) */
-    ET_ROPE_RAMP = 3,    /* by dims: a linear ramp from f_i to f_i / scale between the dims that turn `fast` and `slow`
-                            times over `trained` tokens, and the factor 0.1 ln(scale) + 1 */
+    ET_ROPE_RAMP = 3,    /* by dims: a linear ramp over i from f_i to f_i / scale between the pairs that turn `fast` and
+                            `slow` times over `trained` tokens (rounded outward to whole ones and held within
+                            0 .. rot - 1; the last pair is rot / 2 - 1), and the factor 0.1 ln(scale) + 1 */
     ET_ROPE_BANDS = 4    /* by wavelengths: f_i where it turns `fast` times or more over `trained` tokens, f_i / scale
                             where it turns `slow` times or fewer, in between mixed linearly in the number of turns */
 } et_rope_scaling;

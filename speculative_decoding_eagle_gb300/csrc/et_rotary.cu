@@ -220,11 +220,12 @@ extern "C" et_status et_rotary_frequencies(const et_rope_cfg *c, double *freq, f
   const int n = c->rot / 2;
   const double theta = c->scaling == ET_ROPE_BASE ? c->theta * pow(c->scale, (double)c->rot / (c->rot - 2)) : c->theta;
   *factor = c->scaling == ET_ROPE_RAMP ? (float)(0.1 * log(c->scale) + 1.0) : 1.f;
-  // RAMP: the (whole) dims that turn `fast` and `slow` times over `trained` tokens
+  // RAMP: the pairs that turn `fast` and `slow` times over `trained` tokens, rounded outward.  The slow end may lie past the last
+  // pair, n - 1, when every pair turns more often than `slow` times: the last one keeps its part then
   double lo = 0, hi = 0;
   if (c->scaling == ET_ROPE_RAMP) {
     lo = fmax(0.0, floor(n * log(c->trained / (c->fast * two_pi)) / log(theta)));
-    hi = fmin(n - 1.0, ceil(n * log(c->trained / (c->slow * two_pi)) / log(theta)));
+    hi = fmin(c->rot - 1.0, ceil(n * log(c->trained / (c->slow * two_pi)) / log(theta)));
   }
   for (int i = 0; i < n; ++i) {
     const double f = pow(theta, -(double)i / n);
