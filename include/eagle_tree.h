@@ -868,7 +868,9 @@ int32_t et_tree_attention_paged_splits(const et_paged_attn_shape *shape, const e
  * cache: as in et_tree_attention_paged.  A row_start that descends, lies
  * outside [0, rows] or gives a sequence more than max_rows rows sets
  * ET_DEV_BAD_INDEX; the sequence is skipped, or in the last case cut after
- * max_rows.
+ * max_rows.  Behind a row_start that descends, a sequence whose first row lies
+ * before an earlier sequence's row_start (of those in [0, rows]) is skipped
+ * too, so that no row has two sequences; the others get their rows.
  * Scores, softmax statistics and outputs accumulate in fp32.  bf16 inputs:
  * q meets the cached codes in two 8-bit terms (as there, for any number of
  * rows) and the new keys as it is; a cached key's weight times its V scale is

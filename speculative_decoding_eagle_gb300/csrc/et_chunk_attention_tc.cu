@@ -225,18 +225,21 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     // Sequences of the most keys go out first (ties: lower index), as far as one round of threads ranks them: a block that
     // starts last should not be the longest.  Larger batches keep their order
     int done = 0;  // tiles of the sequences before this round's
+    int wrong = 0;  // a row_start so far was
     for (int b0 = 0; b0 < a.B; b0 += kCtThreads) {
       const int b = b0 + t;
-      int mine = 0, keys = 0, first = 0, n = 0, L = -1;
+      int mine = 0, keys = 0, first = 0, n = 0, L = -1, odd = 0;
       if (b < a.B) {
-        int ignore = 0;
-        chunk_rows(ca.c, b, first, n, ignore);
+        chunk_rows(ca.c, b, first, n, odd);
+        int ignore = odd;
         L = paged_prefix(a, b, ignore);
         if (ignore && blockIdx.x == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
-        if (L >= 0 && n > 0) {
-          mine = (int)(((long long)n * a.G + (1 << ca.shift) - 1) >> ca.shift);
-          keys = tiles_of(L, kCtKeys) + tiles_of(n, kCtKeys);
-        }
+      }
+      wrong |= __syncthreads_or(odd);
+      if (wrong && n > 0 && chunk_overlaps(ca.c, b, first)) n = 0;
+      if (L >= 0 && n > 0) {
+        mine = (int)(((long long)n * a.G + (1 << ca.shift) - 1) >> ca.shift);
+        keys = tiles_of(L, kCtKeys) + tiles_of(n, kCtKeys);
       }
       const int longest_here = __reduce_max_sync(0xffffffffu, keys);
       if (lane == 0) s_len[warp] = longest_here;
