@@ -230,10 +230,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const int b = b0 + t;
       int mine = 0, keys = 0, first = 0, n = 0, L = -1, odd = 0;
       if (b < a.B) {
-        chunk_rows(ca.c, b, first, n, odd);
-        int ignore = odd;
+        int ignore = 0;
         L = paged_prefix(a, b, ignore);
-        if (ignore && blockIdx.x == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
+        chunk_rows(ca.c, b, first, n, odd);
+        if ((ignore | odd) && blockIdx.x == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
       }
       wrong |= __syncthreads_or(odd);
       if (wrong && n > 0 && chunk_overlaps(ca.c, b, first)) n = 0;
