@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+from speculative_decoding_eagle_gb300 import binding as E
 from test_gpu_chunk import Batch
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +83,27 @@ def test_scores_far_apart_in_parts(splits):
     assert bool(((x.lse[:130, 0].double() - lse[:130, 0]).abs() <= slack + 1e-5 * (1 + lse[:130, 0].abs())).all())
     tol = (2.0 ** -8 + 2 * torch.expm1(slack)[:, None]) * (out[:130, 0].abs() + mass[:130, 0])
     assert bool(((x.out[:130, 0].double() - out[:130, 0]).abs() <= tol).all())
+
+
+def test_two_calls_at_once():
+    """Two streams, each with a workspace of its own, give what the calls give alone."""
+    calls = [(Batch([2100, 0], [300, 90], 4, 2, 128, 64, seed=23), 3), (Batch([1500] * 6, [1] * 6, 8, 2, 64, 16, seed=24), 2),
+             (Batch([400], [700], 2, 2, 128, 32, seed=25), 0)]
+    want, spaces = [], []
+    for x, splits in calls:
+        spaces.append(again(x, splits=splits))
+        x.check()
+        want.append((x.out.clone(), x.lse.clone()))
+        x.out.fill_(7.0)
+        x.lse.fill_(7.0)
+    streams = [torch.cuda.Stream() for _ in calls]
+    shapes = [E.ChunkAttnShape(B=len(x.prefix), rows=x.T, Hq=x.Hq, max_rows=max(x.rows), max_blocks=x.table.shape[1],
+                               num_splits=splits) for x, splits in calls]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (x, _), ws, s, shape in zip(calls, spaces, streams, shapes):
+            E.et_chunk_attention_paged(shape, x.cache, x.table, x.plen, x.start, x.q, x.k, x.v, x.out, lse=x.lse, ws=ws,
+                                       dev_status=x.status, stream=s)
+    torch.cuda.synchronize()
+    for (x, _), (out, lse) in zip(calls, want):
+        assert int(x.status.item()) == 0 and torch.equal(out, x.out) and torch.equal(lse, x.lse)
