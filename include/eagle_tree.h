@@ -863,7 +863,8 @@ int32_t et_tree_attention_paged_splits(const et_paged_attn_shape *shape, const e
  *               this function with other shapes may use it before and after,
  *               other functions may not.
  * The new rows are not written to the cache (et_kv_commit_paged with path =
- * NULL does that, after this call has read the prefix).  Scales, codes that
+ * NULL does that, after this call has read the prefix; it takes them
+ * contiguous and padded to [B, N, Hkv, d], not packed).  Scales, codes that
  * are NaN or infinite, prefixes past their bounds and page ids outside the
  * cache: as in et_tree_attention_paged.  A row_start that descends, lies
  * outside [0, rows] or gives a sequence more than max_rows rows sets
@@ -901,9 +902,12 @@ int32_t et_chunk_attention_paged_splits(const et_chunk_attn_shape *shape, const 
  * q_out, k_out  the same shape; each may be its input (same stride), or lie
  *               apart from every input.  k and k_out NULL: q alone.
  * All 16-byte aligned.  The angle is taken modulo a turn in 64-bit fixed
- * point, freq / 2 pi rounded to 2^-64 of a turn: exact to t * 2^-65 turns at any
- * position.  Sine and cosine are fp32, the products fp32, one rounding to
- * the output's type.  No workspace.
+ * point: freq / 2 pi, a product of doubles cut to 2^-64 of a turn, times t; the
+ * second product and the reduction are exact.  So the angle is off by less
+ * than t * (|freq| 2^-54 + 2^-63) of a turn, and t * 2^-54 more where freq is
+ * negative: 2^-23 of a turn at the farthest position of the fastest pair
+ * (freq = 1).  Sine and cosine are fp32, the products fp32, one rounding to the
+ * output's type.  No workspace.
  */
 et_status et_rotary(const et_rotary_shape *shape, const int32_t *positions, const double *freq, const void *q,
                     const void *k, void *q_out, void *k_out, et_stream_t stream);
@@ -939,7 +943,7 @@ et_status et_rotary_frequencies(const et_rope_cfg *cfg, double *freq, float *fac
  *               acceptance lossless for the truncated distribution.  May not
  *               overlap logits.
  * Masses are sums of w in 64-bit fixed point (2^-44 of the largest weight, w
- * evaluated to 2^-40), so tokens and kept sets do not depend on the order of
+ * evaluated to 2^-36.8), so tokens and kept sets do not depend on the order of
  * any sum and agree with 64-bit floating point but where a border lies within
  * about 2^-36 of the total (V 2^-45 at worst, where a row's weights far below
  * the largest are all alike).  No workspace; one launch, a thread-block cluster

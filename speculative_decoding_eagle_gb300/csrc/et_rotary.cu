@@ -5,10 +5,12 @@
 // Bound by memory: each value is read once and written once, in 16-byte
 // accesses (8192 rows of 72 heads of 128, bf16: 49.7 us = 6.07 TB/s).  A block takes a token; it finds the sines and cosines once, for
 // all heads, while its first values are on their way.
-// The angle in turns is t * (freq / 2 pi) modulo 1, which a 64-bit integer
-// product gives exactly: freq / 2 pi as a multiple of 2^-64, times t, wraps by
-// itself, so no position is too far and no fp64 arithmetic is left per token
-// and dim but the one product that makes the integer.
+// The angle in turns is t * (freq / 2 pi) modulo 1: freq / 2 pi, an fp64 product
+// (off by freq 2^-55 of a turn, the constant's rounding included), is cut to a
+// multiple of 2^-64, and that times t in 64-bit integers is exact and wraps by
+// itself.  So an angle is off by t times that product's error and nothing
+// else (2^-24 of a turn at position 2^31 for freq = 1), and no fp64 arithmetic
+// is left per token and dim but the one product that makes the integer.
 #include <cuda_bf16.h>
 
 #include "et_common.cuh"

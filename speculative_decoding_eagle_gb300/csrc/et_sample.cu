@@ -21,15 +21,17 @@
 // Masses are sums of weights 2^44 exp((z - max) / T) rounded to integers.  The
 // exponential is evaluated in pairs of fp32 numbers (error-free sums and
 // products after T. J. Dekker, Numer. Math. 18, 1971; reduction to 2^(k/64) and
-// a Taylor polynomial) to about 2^-40: with plain fp32 exponentials a row of
+// a Taylor polynomial) to 2^-36.8, 2^-39 in the mean square (its fp32 steps
+// against long doubles, 16 million logits): with plain fp32 exponentials a row of
 // 10^5 tokens would give another token than 64-bit arithmetic in one draw of
 // some hundred.
 // Measured: nothing comes near the memory's rate.  One row of 32000: 16 us, the
 // latency of a dozen steps that follow on one another (load, extremes,
 // histogram, crossing, list, sort by weight, sort by id, draw), each gone
 // through once.  244 rows of 32000, top-p and truncated logits: 79 us.  128 rows
-// of 100003: 120 us, of which the weights' arithmetic (65 instructions a token)
-// is a third.
+// of 100003: 110 to 129 us by the draw of rows; two blocks of an SM issue in 37%
+// of the cycles, and most of a warp's waiting is at barriers (8.4 of 20 warps
+// per issue), where the steps follow on one another.
 #include "et_common.cuh"
 
 namespace et {
