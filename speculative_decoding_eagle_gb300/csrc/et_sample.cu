@@ -200,7 +200,7 @@ __device__ __forceinline__ int warp_span(int slice) { return ((slice + kSaWarps 
 // `target` (target < the cluster's total, else -1).  weigh(z, id) is a token's weight.  Every thread of the cluster
 // calls it and gets the id.
 template <typename W>
-__device__ int locate(const Row &row, int slice, unsigned long long *s_red, int *s_id, W weigh, unsigned long long target,
+__device__ int locate(const Row &row, int slice, int *s_id, W weigh, unsigned long long target,
                       unsigned long long *total, bool fraction, float uniform) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, span = warp_span(slice);
   const int i0 = warp * span, i1 = min(i0 + span, row.n);
@@ -497,7 +497,7 @@ __device__ Kept border(Row &row, const SampleArgs &a, const Kept &in, const Weig
   out.cut = 0x7fffffff;
   const unsigned long long each = MASS ? weigh(key_value(lo)) : 1ull;
   const unsigned long long nth = each ? (target - c.above + each - 1) / each : 1ull;  // how many of them
-  const int id = locate(row, a.slice, s_red, s_id, [&](float z, int i) -> unsigned long long {
+  const int id = locate(row, a.slice, s_id, [&](float z, int i) -> unsigned long long {
     const unsigned int key = order_key(z);
     return key == lo && in(key, i) ? 1ull : 0ull;
   }, nth - 1, nullptr, false, 0.f);
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(kSaThreads) k_sample(const SampleArgs a) {
         kept.cut = 0x7fffffff;
       }
       unsigned long long total = 0ull;
-      token = locate(row, a.slice, s_red, &s_id, [&](float z, int i) -> unsigned long long {
+      token = locate(row, a.slice, &s_id, [&](float z, int i) -> unsigned long long {
         return kept(order_key(z), i) ? weigh(z) : 0ull;
       }, 0ull, &total, true, u);
       if (t == 0 && row.rank == 0) {
