@@ -252,11 +252,13 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
     // One block per SM.  In units of 0.88 us, measured: a tile takes 1.2 where both groups have the same rows (1.0 to 1.4, by
     // how many SMs are at it) and 1.9 for 256 rows, a block's start and end 14, a merge through the workspace 1, 0.04 a row
     // and 1 a part.  So parts pay
-    //   where blocks are few and tiles many: 64 rows, 32 heads, in 1 / 2 / 3 / 4 parts: 4096 keys 39.5 / 29.6 / 28.0 / 26.2 us,
-    //   but 1024 keys 18.9 / 18.7 / 19.6 / 19.1;
-    //   where a last round of whole units would leave SMs idle: 512 units of 65 to 80 tiles, the last 56 in two parts 496 us,
-    //   whole 534 (that round has the units with the fewest keys, little more than the prefix).
-    // Units of 128 rows pay where those of 256 leave half of the SMs idle: 512 rows, 32 heads, 4096 keys 49.7 against 72.5 us
+    //   where blocks are few and tiles many: 64 rows, 32 heads, in 1 / 2 / 3 / 4 parts: 4096 keys 39.7 / 29.2 / 26.9 / 25.5 us,
+    //   but 1024 keys 18.3 / 18.4 / 18.9 / 18.6;
+    //   where a last round of whole units would leave SMs idle: 512 units of 65 to 80 tiles, the last 56 in two parts 469 us,
+    //   whole 516 (that round has the units with the fewest keys, little more than the prefix; of more than 32 sequences it may
+    //   have others, and the price is low).
+    // Units of 128 rows pay where those of 256 leave half of the SMs idle: 512 rows, 32 heads, 4096 keys 45.5 us,
+    // against 53.5 in parts and 70.6 whole
     const long long sms = sm_count(), least = Tp + 1 < T ? Tp + 1 : T;
     double best = 0.0;
     for (int u = 8; u >= 7; --u) {

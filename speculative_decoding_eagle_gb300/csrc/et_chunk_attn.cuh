@@ -13,12 +13,12 @@ struct ChunkArgs {
   const int32_t *row_start;
 };
 
-// bf16 (et_chunk_attention_tc.cu): blocks of 256 (token, head) rows of a KV head
+// bf16 (et_chunk_attention_tc.cu): units of 128 or 256 (token, head) rows of a KV head, a block or several each
 struct ChunkTcPlan {
   int S;      // parts of a unit's keys at most
   int shift;  // a unit: 1 << shift rows of a KV head, 128 or 256
   int tiles;  // units per KV head at most
-  int whole;  // units that stay in one part, the ones with the most keys
+  int whole;  // units that stay in one part: of up to 32 sequences those with the most keys, of more the first ones
   size_t ml_off, o_off;
 };
 ET_HIDDEN et_status chunk_tc_launch(const et_paged_cache *cache, const ChunkArgs &c, const ChunkTcPlan &p, void *ws,
