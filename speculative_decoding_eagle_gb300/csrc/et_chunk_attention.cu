@@ -5,7 +5,7 @@
 // k_chunk_rows: one block per 32 (token, head) rows of a KV head; online
 // softmax over tiles of 32 keys in fp32.  Scores: a thread has two rows and
 // two keys of the tile; output: two rows and D / 16 dims.  Bound by shared
-// memory reads and the fp32 units, in small calls by latency (17.3 us: two
+// memory reads and the fp32 units, in small calls by latency (17.5 us: two
 // sequences of up to 40 rows after 128 cached, 4 heads of 64); fp32 inputs are
 // for checks and small models.
 #include "et_chunk_attn.cuh"

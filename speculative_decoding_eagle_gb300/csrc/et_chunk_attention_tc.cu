@@ -29,7 +29,7 @@
 // Few rows, or a last round of blocks that would not fill the SMs: a unit's
 // tiles are split over several blocks, which leave their rows in the
 // workspace; the last one to arrive merges them.
-// Bounds, measured: 2048 rows after 8192 cached, 64 / 8 heads, 469 us = 1318
+// Bounds, measured: 2048 rows after 8192 cached, 64 / 8 heads, 470 us = 1316
 // TFLOP/s (68% of the measured bf16 rate); a tile of 256 x 128 takes about 3000
 // cycles of which the tensor cores work 2048: the rest is the softmax warps'
 // chain (scores out of tensor memory, exponentials, weights back) against the
