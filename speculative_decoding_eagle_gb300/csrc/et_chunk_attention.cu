@@ -34,8 +34,9 @@ __global__ void __launch_bounds__(kCrThreads) k_chunk_rows(const ChunkArgs c) {
   int bad = 0, first, n;
   const int L = paged_prefix(a, b, bad);
   chunk_rows(c, b, first, n, bad);
-  bool behind = false;  // some sequence before starts behind this one's first row (chunk_overlaps): a thread looks at a few
-  for (int k = t; k < b; k += kCrThreads) behind = behind || (c.row_start[k] <= c.rows && c.row_start[k] > first);
+  int behind = 0;  // some sequence before starts behind this one's first row: a thread looks at a few
+#pragma unroll 8
+  for (int k = t; k < b; k += kCrThreads) behind |= chunk_start(c, c.row_start[k]) > first;
   if (__syncthreads_or(behind)) n = 0;
   if (bad && t == 0 && blockIdx.x == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
   const long long R0 = (long long)blockIdx.x * kCrRows;  // row of the KV head: token * G + head of the group

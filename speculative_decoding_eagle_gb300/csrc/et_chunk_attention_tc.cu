@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     // Sequences of the most keys go out first (ties: lower index), as far as one round of threads ranks them: a block that
     // starts last should not be the longest.  Larger batches keep their order
     int done = 0;  // tiles of the sequences before this round's
-    int wrong = 0;  // a row_start so far was
+    int wrong = 0, top = -1;  // a row_start so far was; the largest start so far, once one was
     for (int b0 = 0; b0 < a.B; b0 += kCtThreads) {
       const int b = b0 + t;
       int mine = 0, keys = 0, first = 0, n = 0, L = -1, odd = 0;
@@ -236,8 +236,22 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         chunk_rows(ca.c, b, first, n, odd);
         if ((ignore | odd) && blockIdx.x == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
       }
-      wrong |= __syncthreads_or(odd);
-      if (wrong && n > 0 && chunk_overlaps(ca.c, b, first)) n = 0;
+      if (__syncthreads_or(odd | wrong)) {
+        if (!wrong && b0 > 0) top = ca.c.row_start[b0];  // they ascended up to here
+        wrong = 1;
+        int high = b < a.B ? chunk_start(ca.c, first) : -1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, high, o);
+          if (lane >= o) high = max(high, y);
+        }
+        if (lane == 31) s_red[warp] = high;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) high = max(high, s_red[w]);
+        if (first < max(high, top)) n = 0;
+        for (int w = 0; w < kCtThreads / 32; ++w) top = max(top, s_red[w]);
+        __syncthreads();
+      }
       if (L >= 0 && n > 0) {
         mine = (int)(((long long)n * a.G + (1 << ca.shift) - 1) >> ca.shift);
         keys = tiles_of(L, kCtKeys) + tiles_of(n, kCtKeys);

@@ -42,16 +42,10 @@ __device__ __forceinline__ void chunk_rows(const ChunkArgs &c, int b, int &first
   }
 }
 
-// Does a sequence before b start behind b's first row?  Then row_start descends between them and b's rows may be others', too.
-// Without such sequences no two have a row in common: the units fit the plan's count of them, and their sums fit 32 bits.  (Only
-// asked where some row_start is wrong.)
-__device__ __forceinline__ bool chunk_overlaps(const ChunkArgs &c, int b, int first) {
-  for (int k = 0; k < b; ++k) {
-    const int r = c.row_start[k];
-    if (r > first && r <= c.rows) return true;
-  }
-  return false;
-}
+// A start that counts where row_start is wrong.  A sequence whose first row lies before an earlier one of them is left out: b's
+// rows may be others', too.  Without such sequences no two have a row in common: the units fit the plan's count of them, and
+// their sums fit 32 bits.
+__device__ __forceinline__ int chunk_start(const ChunkArgs &c, int first) { return first >= 0 && first <= c.rows ? first : -1; }
 
 }  // namespace
 }  // namespace et

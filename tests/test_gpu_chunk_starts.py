@@ -59,6 +59,8 @@ def chain(n, width):
     ([0, 8, 8, 3, 8, 30], 1, 10),                      # descends, and a last one that is cut
     (chain(60, 7), 3, 9),                              # past the batches that are ordered
     (chain(700, 1), 0, 2),                             # more sequences than a block has threads
+    (list(range(1100)) + [50, 60, 1099, 1105], 2, 64),  # right for two rounds of threads, then back into their rows
+    ([0, 1500] + list(range(0, 1400, 2)) + [1500, 1510], 0, 1500),  # a first sequence that has everyone's rows but the last's
 ])
 def test_wrong_starts(starts, spare, max_rows, dtype):
     et, dt = DT[dtype]
