@@ -244,7 +244,7 @@ typedef struct {
     et_dtype dtype;           /* of q, k/v new and out */
     float scale;              /* score scale, usually 1/sqrt(d) */
     int32_t max_prefix;       /* host upper bound of prefix_len[b] (sizes the grid) */
-    int32_t num_splits;       /* parts a sequence's keys are split into; 0 = library heuristic (also: 2^18 keys a part at most) */
+    int32_t num_splits;       /* parts a sequence's keys are split into; 0 = library heuristic */
     int64_t q_stride, k_stride, v_stride; /* elements from row to row, >= Hq * d (Hkv * d); multiples of 16 bytes */
 } et_chunk_attn_shape;
 
@@ -876,11 +876,8 @@ int32_t et_tree_attention_paged_splits(const et_paged_attn_shape *shape, const e
  * q meets the cached codes in two 8-bit terms (as there, for any number of
  * rows) and the new keys as it is; a cached key's weight times its V scale is
  * rounded to fp16, a new key's weight to bf16; the sum of weights is not
- * rounded.  The tensor cores' sums lose what lies below their last bit, once
- * every 16 keys, so that an output is low by up to 2^-27 of itself per key of
- * a part: 2^-9 over 2^18 keys, the most a part has with num_splits = 0 and
- * prefixes of up to 2^24.  A q row that holds a NaN or an infinity gives NaN.
- * fp32 inputs: fp32 throughout.
+ * rounded.  A q row that holds a NaN or an infinity gives NaN.  fp32 inputs:
+ * fp32 throughout.
  * bf16 inputs: a bounded wait that expires sets ET_DEV_TIMEOUT and leaves that
  * block's rows undefined.
  */

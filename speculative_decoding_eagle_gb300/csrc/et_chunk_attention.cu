@@ -236,10 +236,6 @@ struct ChunkPlan {
   size_t ws;
 };
 
-// Tiles of 128 keys that a part has at most, as long as 64 parts do (2^24 keys).  The tensor cores cut a sum's last bit off, every
-// 16 keys: over 2048 tiles an output is low by 2^-9 of itself at most.  In one part (V between 1 and 2) 2^20 keys lost 0.5%, 2^22
-// 1.6%, more than the output's rounding
-constexpr int kChunkLong = 2048;
 constexpr int kChunkCounters = 16384;  // in one place of every workspace, so that calls of other shapes can share it
 
 int sm_count() {
@@ -331,16 +327,6 @@ et_status make_plan(const et_chunk_attn_shape *s, const et_paged_cache *c, Chunk
   if (S > T) S = T;
   if (S > 64) S = 64;
   if (S < 1 || units - whole > kChunkCounters) S = 1;
-  p->tc.aim = (int)S;
-  p->tc.cap = 0x7fffffff;
-  if (s->num_splits == 0 && T > kChunkLong && units <= kChunkCounters) {
-    if (whole) p->tc.aim = 1;  // parts for all of them or none: which units are long is not known here
-    whole = 0;
-    S = (T + kChunkLong - 1) / kChunkLong;
-    S = S > 64 ? 64 : S;
-    p->tc.cap = (int)((T + S - 1) / S > kChunkLong ? (T + S - 1) / S : kChunkLong);
-    if (S < p->tc.aim) S = p->tc.aim;
-  }
   p->tc.S = (int)S;
   p->tc.shift = shift;
   p->tc.tiles = (int)(units / c->Hkv);

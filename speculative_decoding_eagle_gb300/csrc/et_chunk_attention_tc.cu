@@ -161,7 +161,6 @@ __device__ __forceinline__ uint32_t f16x2_to_e4m3x2(__half2 x) {
 struct ChunkTcArgs {
   ChunkArgs c;
   int S;                 // parts of a unit's tiles at most
-  int aim, cap;          // parts of the longest unit, unless they would have more than `cap` tiles
   int shift;             // a unit: 1 << shift (token, head) rows of a KV head, 128 or 256
   int tiles;             // units per KV head in the grid
   int whole;             // the first units, each a block
@@ -310,7 +309,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   const int Tp = tiles_of(L, kCtKeys), To = tok_last / kCtKeys + 1, T = Tp + To;
   int parts = 1, per = T;
   if (behind >= 0 && ca.S > 1) {  // shorter sequences have fewer parts
-    const int most = max(min((s_longest + ca.aim - 1) / ca.aim, ca.cap), 1);
+    const int most = max((s_longest + ca.S - 1) / ca.S, 1);
     per = tiles_of(T, (T + most - 1) / most);
     parts = tiles_of(T, per);
   }
@@ -1142,8 +1141,6 @@ et_status chunk_tc_launch(const et_paged_cache *cache, const ChunkArgs &c, const
   ChunkTcArgs ca;
   ca.c = c;
   ca.S = p.S;
-  ca.aim = p.aim;
-  ca.cap = p.cap;
   ca.shift = p.shift;
   ca.tiles = p.tiles;
   ca.whole = p.whole;

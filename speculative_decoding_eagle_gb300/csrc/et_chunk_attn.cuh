@@ -16,8 +16,6 @@ struct ChunkArgs {
 // bf16 (et_chunk_attention_tc.cu): units of 128 or 256 (token, head) rows of a KV head, a block or several each
 struct ChunkTcPlan {
   int S;      // parts of a unit's keys at most
-  int aim;    // parts of the longest unit, unless they would have more than
-  int cap;    // tiles
   int shift;  // a unit: 1 << shift rows of a KV head, 128 or 256
   int tiles;  // units per KV head at most
   int whole;  // units that stay in one part: of up to 32 sequences those with the most keys, of more the first ones

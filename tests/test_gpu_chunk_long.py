@@ -1,11 +1,9 @@
-"""Chunk attention over long prefixes: many keys that are each far too small for the sum, and together are not (fp32), and the
-tensor cores' sums (bf16)."""
+"""fp32 chunk attention over long prefixes: many keys that are each far too small for the sum, and together are not."""
 import math
 
 import pytest
 import torch
 
-from speculative_decoding_eagle_gb300 import binding as E
 from test_gpu_chunk import Batch
 
 pytestmark = pytest.mark.gpu
@@ -48,38 +46,3 @@ def test_many_small_weights_count(first, log2_below, d):
     assert bool(((x.lse[:5].double() - lse[:5]).abs() <= tol + 2.0 ** -22 * lse[:5].abs()).all())
     # without the small keys the output would be 1
     assert bool((out[:5] > 1 + 0.9 * 2.0 ** (18 - log2_below)).all())
-
-
-@pytest.mark.parametrize("rows_bound", [1, 40000])       # few units, or many: the heuristic alone would take one part then
-def test_long_sums_of_the_tensor_cores(rows_bound):
-    """2^22 keys with values between 1 and 2: in one part the sums would lose 1.6%."""
-    L, P, d = 1 << 22, 256, 64
-    cols = L // P
-    g = torch.Generator(device="cuda").manual_seed(31)
-    cache = E.PagedCache.allocate(cols, 1, P, d)
-    for pages, x in ((cache.k_pages, torch.randn(cols, 1, P, d, generator=g, device="cuda")),
-                     (cache.v_pages, 1 + torch.rand(cols, 1, P, d, generator=g, device="cuda"))):
-        pages.view(torch.uint8).copy_(x.to(torch.float8_e4m3fn).view(torch.uint8))
-    cache.k_scale.fill_(1.0)
-    cache.v_scale.fill_(1.0)
-    T = rows_bound
-    q, k, v = (torch.randn(T, 1, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
-    v = v.abs() + 1
-    shape = E.ChunkAttnShape(B=1, rows=T, Hq=1, max_rows=T, max_blocks=cols)
-    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
-    ws = E.new_workspace(E.et_chunk_attention_paged_workspace_size(shape, cache))
-    for n in (L, L // 8, 1000):                           # shorter ones under the same plan
-        out, lse = torch.full((T, 1, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((T, 1), 7.0, device="cuda")
-        st = i32(0)
-        E.et_chunk_attention_paged(shape, cache, torch.arange(cols, device="cuda", dtype=torch.int32)[None], i32(n), i32(0, 1), q, k, v,
-                                   out, lse=lse, ws=ws, dev_status=st)
-        torch.cuda.synchronize()
-        assert int(st.item()) == 0
-        keys = torch.cat([cache.k_pages.float().reshape(L, d)[:n], k[0].float()])
-        z = keys.double() @ q[0, 0].double() / 8
-        p = torch.softmax(z, 0)
-        want = p @ torch.cat([cache.v_pages.float().reshape(L, d)[:n], v[0].float()]).double()
-        # the output's rounding (2^-8), the weights' (2^-11; the new row's counts as little as it weighs), the sums' (2^-9)
-        assert bool(((out[0, 0].double() / want - 1).abs() <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -9).all())
-        assert abs(float(lse[0, 0]) - float(torch.logsumexp(z, 0))) <= 1e-5 * (1 + abs(float(lse[0, 0])))
-        assert bool((out[1:] == 7).all())
