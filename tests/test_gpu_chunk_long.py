@@ -1,9 +1,11 @@
-"""fp32 chunk attention over long prefixes: many keys that are each far too small for the sum, and together are not."""
+"""Chunk attention over long prefixes: many keys that are each far too small for the sum, and together are not (fp32), and the
+tensor cores' sums in parts (bf16)."""
 import math
 
 import pytest
 import torch
 
+from speculative_decoding_eagle_gb300 import binding as E
 from test_gpu_chunk import Batch
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +48,37 @@ def test_many_small_weights_count(first, log2_below, d):
     assert bool(((x.lse[:5].double() - lse[:5]).abs() <= tol + 2.0 ** -22 * lse[:5].abs()).all())
     # without the small keys the output would be 1
     assert bool((out[:5] > 1 + 0.9 * 2.0 ** (18 - log2_below)).all())
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_long_sums_of_the_tensor_cores_in_parts(rows):
+    """2^22 keys with values between 1 and 2 (in one part the sums would lose 1.6%): parts of 2^18 keys keep them."""
+    L, P, d = 1 << 22, 256, 64
+    cols = L // P
+    g = torch.Generator(device="cuda").manual_seed(31)
+    cache = E.PagedCache.allocate(cols, 1, P, d)
+    for pages, x in ((cache.k_pages, torch.randn(cols, 1, P, d, generator=g, device="cuda")),
+                     (cache.v_pages, 1 + torch.rand(cols, 1, P, d, generator=g, device="cuda"))):
+        pages.view(torch.uint8).copy_(x.to(torch.float8_e4m3fn).view(torch.uint8))
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(1.0)
+    q, k, v = (torch.randn(rows, 1, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    v = v.abs() + 1
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out, lse = torch.full((rows, 1, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((rows, 1), 7.0, device="cuda")
+    st = i32(0)
+    shape = E.ChunkAttnShape(B=1, rows=rows, Hq=1, max_rows=rows, max_blocks=cols, num_splits=17)
+    ws = E.new_workspace(E.et_chunk_attention_paged_workspace_size(shape, cache))
+    E.et_chunk_attention_paged(shape, cache, torch.arange(cols, device="cuda", dtype=torch.int32)[None], i32(L), i32(0, rows), q, k, v,
+                               out, lse=lse, ws=ws, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for r in {0, rows // 2, rows - 1}:
+        keys = torch.cat([cache.k_pages.float().reshape(L, d), k[:r + 1, 0].float()])
+        z = keys.double() @ q[r, 0].double() / 8
+        p = torch.softmax(z, 0)
+        want = p @ torch.cat([cache.v_pages.float().reshape(L, d), v[:r + 1, 0].float()]).double()
+        # the output's rounding (2^-8), the weights' (2^-11; the new rows' few count as little as they weigh), and the sums':
+        # 2^-27 a key of a part, 2^18 of them
+        assert bool(((out[r, 0].double() / want - 1).abs() <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -9).all())
+        assert abs(float(lse[r, 0]) - float(torch.logsumexp(z, 0))) <= 1e-5 * (1 + abs(float(lse[r, 0])))
