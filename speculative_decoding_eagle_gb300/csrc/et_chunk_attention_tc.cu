@@ -235,7 +235,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         chunk_rows(ca.c, b, first, n, odd);
         if ((ignore | odd) && blockIdx.x == 0) flag_status(a.dev_status, ET_DEV_BAD_INDEX);
       }
-      if (__syncthreads_or(odd | wrong)) {
+      // Some start is wrong: a sequence whose first row lies before an earlier one is left out (chunk_start).  Up to kCtOrdered
+      // sequences lie in one warp
+      if (a.B <= kCtOrdered ? __any_sync(0xffffffffu, odd) : __syncthreads_or(odd | wrong)) {
         if (!wrong && b0 > 0) top = ca.c.row_start[b0];  // they ascended up to here
         wrong = 1;
         int high = b < a.B ? chunk_start(ca.c, first) : -1;
@@ -244,12 +246,15 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           const int y = __shfl_up_sync(0xffffffffu, high, o);
           if (lane >= o) high = max(high, y);
         }
-        if (lane == 31) s_red[warp] = high;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) high = max(high, s_red[w]);
-        if (first < max(high, top)) n = 0;
-        for (int w = 0; w < kCtThreads / 32; ++w) top = max(top, s_red[w]);
-        __syncthreads();
+        if (a.B > kCtOrdered) {
+          if (lane == 31) s_red[warp] = high;
+          __syncthreads();
+          for (int w = 0; w < warp; ++w) high = max(high, s_red[w]);
+          high = max(high, top);
+          for (int w = 0; w < kCtThreads / 32; ++w) top = max(top, s_red[w]);
+          __syncthreads();
+        }
+        if (first < high) n = 0;
       }
       if (L >= 0 && n > 0) {
         mine = (int)(((long long)n * a.G + (1 << ca.shift) - 1) >> ca.shift);
